@@ -69,6 +69,16 @@ enum moe_router_mode {
     MOE_MODE_SOFTMAX = 1  /* softmax over all experts, top-k of logits, gates not renormalised */
 };
 
+enum moe_type { /* element type of a buffer that may have either */
+    MOE_TYPE_BF16 = 0,
+    MOE_TYPE_F32 = 1
+};
+
+enum moe_group_rule {    /* score of a group of experts */
+    MOE_GROUP_MAX = 0,  /* its largest selection value */
+    MOE_GROUP_TOP2 = 1  /* the sum of its two largest (its only one, in groups of one) */
+};
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* moe_status_string(int status);
 
@@ -537,6 +547,133 @@ int moe_permute_bwd(const moe_bf16* dX_perm, const int32_t* slot_to_row,
                     const moe_bf16* dx_shared, const float* dlogits, const float* W_r,
                     const float* dx_router, int64_t T, int d, int E, int k, moe_bf16* dx,
                     moe_stream_t stream);
+
+/*
+ * moe_rms_norm - the residual stream's addition and the root-mean-square norm in front of the
+ * layer, with the operand codes of the FP8 experts.
+ * Definition, per token: z = residual + x, rounded once to the residual stream's type;
+ * rstd = 1 / sqrt(mean_j(z_j^2) + eps), from the stored z; y_j = z_j rstd w_j in fp32, stored
+ * as bf16. Codes: sy = fp32(amax_j |y_j| / 448) (1 for a zero row), yq = E4M3(y / sy), round
+ * to nearest even, saturating at +-448, both from the fp32 y: one rounding fewer than
+ * quantising the bf16 y (moe_quantize_rows_fp8) has. Sums are fp32, in a fixed order.
+ * In : x [T,d] bf16; residual [T,d] of res_type (MOE_TYPE_BF16 or MOE_TYPE_F32), or NULL: then
+ *      z is x itself; w [d] fp32; eps >= 0.
+ * Out: z [T,d] of res_type (both or neither of residual and z; z may be the residual's own
+ *      buffer); y [T,d] bf16 (may be x's own buffer); yq [T,d] E4M3 codes with sy [T] fp32
+ *      (both or neither); rstd [T] fp32 or NULL (moe_rms_norm_bwd needs it). y may be NULL
+ *      where the codes are asked for.
+ * d % 8 == 0, d <= 32768 (not a multiple of 128 as elsewhere); x, residual, w, z, y 16-byte
+ * aligned, yq 8-byte aligned.
+ */
+int moe_rms_norm(const moe_bf16* x, const void* residual, int res_type, const float* w,
+                 float eps, int64_t T, int d, void* z, moe_bf16* y, uint8_t* yq, float* sy,
+                 float* rstd, moe_stream_t stream);
+
+/*
+ * moe_rms_norm_bwd - backward of moe_rms_norm (the codes pass their gradient to y unchanged).
+ * Definition, with xhat = z rstd and g = dy w: dz = rstd (g - xhat mean_j(g_j xhat_j)) + dres,
+ * the gradient of both the residual and x; dw_j = sum_t dy[t,j] xhat[t,j] (fp32, each CTA's
+ * tokens in order, then the CTAs in order).
+ * In : dy [T,d] bf16 (gradient of y); dres [T,d] of res_type or NULL (gradient that reaches z
+ *      past the norm); z [T,d] of res_type (x itself where the forward had no residual) and
+ *      rstd [T] from moe_rms_norm; w [d] fp32.
+ * Out: dz [T,d] of res_type (may be dres's own buffer); dx [T,d] bf16 or NULL: the same
+ *      gradient as bf16, for x beside an fp32 residual; dw [d] fp32.
+ * Sizes and alignment as moe_rms_norm. Scratch: ws (moe_workspace_bytes).
+ */
+int moe_rms_norm_bwd(const moe_bf16* dy, const void* dres, const void* z, int res_type,
+                     const float* rstd, const float* w, int64_t T, int d, void* dz, moe_bf16* dx,
+                     float* dw, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_router_logits - the router's logits alone, l = x W_r^T in fp32 as in moe_route, for a
+ * choice made by moe_select_experts; with the logits' logsumexp and the z-loss when asked.
+ * In : x [T,d] bf16; W_r [E,d] fp32.
+ * Out: logits [T,E] fp32; lse [T] fp32 or NULL; z_loss [1] fp32 or NULL: z_coef *
+ *      mean_t(lse_t^2).
+ */
+int moe_router_logits(const moe_bf16* x, const float* W_r, int64_t T, int d, int E, float z_coef,
+                      float* logits, float* lse, float* z_loss, void* ws, size_t ws_bytes,
+                      moe_stream_t stream);
+
+/*
+ * moe_router_dw - the router weight's gradient dW_r = dlogits^T x from a logit gradient that
+ * is known already (moe_select_experts_bwd), as moe_route_bwd forms it.
+ * In : dlogits [T,E] fp32; x [T,d] bf16.  Out: dW_r [E,d] fp32.
+ */
+int moe_router_dw(const float* dlogits, const moe_bf16* x, int64_t T, int d, int E, float* dW_r,
+                  void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_select_experts - choice of experts from router logits, with groups of experts.
+ * Definition, per token: s = 1/(1+exp(-l)) (MOE_MODE_SIGMOID) or softmax(l) over all experts
+ * (MOE_MODE_SOFTMAX); the selection value is s + b, or l itself where b is NULL (scores have
+ * the logits' order). The experts form n_group groups of E / n_group consecutive ones. A
+ * group's score is its largest selection value (MOE_GROUP_MAX) or the sum of its two largest
+ * s (+ b) (MOE_GROUP_TOP2). The topk_group best groups stay, and of their experts the k of the
+ * largest selection value are chosen; equal values: the lower index first. topk_score = s of
+ * the chosen expert; topk_gate = scale * s, with renorm scale * s / sum of the chosen s (0
+ * where that sum is 0 in 64 bits).
+ * The choice is the one the values have in 64 bits, whatever the kernel's own rounding.
+ * In : logits [T,E] fp32 (moe_route or moe_router_logits); b [E] fp32 or NULL. A logit of -inf
+ *      has score 0; a bias of -inf keeps an expert out while there are others. Values that are
+ *      NaN come last; every choice is of k distinct experts of [0,E) even so. In softmax mode a
+ *      NaN or +inf logit makes the token's scores NaN; a token whose logits are all -inf has
+ *      scores of 0 and lse -inf.
+ * Out: topk_idx [T,k] int32, slots in descending selection value; topk_gate, topk_score [T,k]
+ *      fp32; lse [T] fp32 (softmax mode; may be NULL).
+ * 1 <= topk_group <= n_group <= 32, E % n_group == 0, k <= topk_group * E / n_group.
+ */
+int moe_select_experts(const float* logits, const float* b, int64_t T, int E, int k, int mode,
+                       int n_group, int topk_group, int group_rule, int renorm, float scale,
+                       int32_t* topk_idx, float* topk_gate, float* topk_score, float* lse,
+                       moe_stream_t stream);
+
+/*
+ * moe_select_experts_bwd - the logit gradient of moe_select_experts. No gradient reaches the
+ * bias or the choice.
+ * Definition, per token, with s = topk_score and S their sum: ds_i = scale dg_i, with renorm
+ * ds_i = scale / S (dg_i - sum_j (s_j / S) dg_j) (0 where S is 0, as it is once every chosen
+ * score has left fp32's range: logits below about -103). MOE_MODE_SIGMOID: dlogits at
+ * the chosen experts is ds_i s_i (1 - s_i), 0 elsewhere. MOE_MODE_SOFTMAX: dlogits_e = p_e
+ * (ds_e - sum_i s_i ds_i) with p = exp(l - lse) and ds_e = 0 off the chosen experts (with
+ * renorm that sum is 0 and only the chosen experts have a gradient), plus the z-loss's
+ * (2 z_coef / T) lse p_e. dlogits_extra (the balancing losses') is added.
+ * In : dg [T,k] fp32 (gradient of topk_gate); topk_idx, topk_score [T,k]; logits [T,E] and lse
+ *      [T] (softmax mode without renorm or with a z_coef; else may be NULL); dlogits_extra
+ *      [T,E] fp32 or NULL. An index outside [0,E) records MOE_ERR_BAD_INDEX and its slot is
+ *      dropped; an expert named twice gets both slots' gradients.
+ * Out: dlogits [T,E] fp32 (for moe_router_dw, moe_router_dx and moe_permute_bwd; may be
+ *      dlogits_extra's own buffer).
+ */
+int moe_select_experts_bwd(const float* dg, const int32_t* topk_idx, const float* topk_score,
+                           const float* logits, const float* lse, const float* dlogits_extra,
+                           int64_t T, int E, int k, int mode, int renorm, float scale,
+                           float z_coef, float* dlogits, moe_stream_t stream);
+
+/*
+ * moe_grad_norm - global norm over a step's gradients, and the factor that clips them.
+ * Definition: norm[0] = sqrt(sum over the tensors of their squares); norm[1] = max_norm /
+ * norm[0] where norm[0] is finite and above max_norm, else 1. Squares are summed in fp32 over
+ * at most 32 elements and in 64 bits from there on, in a fixed order; groups whose squares
+ * leave fp32's range are summed in 64 bits throughout.
+ * In : grads, numel, types: HOST arrays of `count` device pointers, element counts (0 is
+ *      allowed, the pointer is then not read) and MOE_TYPE_BF16 or MOE_TYPE_F32. Any count,
+ *      any element alignment. They are read before the call returns.
+ * Out: norm [2] fp32 (device). Scratch: ws (any moe_workspace_bytes() covers it).
+ */
+int moe_grad_norm(const void* const* grads, const int64_t* numel, const int* types, int count,
+                  float max_norm, float* norm, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_clip_grads - moe_grad_norm, then out[i] = norm[1] * grads[i] (fp32 product, one rounding
+ * to the tensor's type). out[i] may be grads[i] itself (which is left untouched when norm[1]
+ * is 1) and overlaps no other tensor. A norm that is not finite leaves the gradients as they
+ * are (out is a copy): the caller sees it in norm[0] and drops the step.
+ */
+int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* numel,
+                   const int* types, int count, float max_norm, float* norm, void* ws,
+                   size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -54,6 +54,14 @@ PROTOTYPES = {
     "moe_aux_loss_bwd": (_I, [_P, _P, _I64, _I, _I, _I64, _F, _F, _P, _P]),
     "moe_permute_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P]),
     "moe_router_dx": (_I, [_P, _P, _I64, _I, _I, _P, _P, _SZ, _P]),
+    "moe_rms_norm": (_I, [_P, _P, _I, _P, _F, _I64, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_rms_norm_bwd": (_I, [_P, _P, _P, _I, _P, _P, _I64, _I, _P, _P, _P, _P, _SZ, _P]),
+    "moe_router_logits": (_I, [_P, _P, _I64, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]),
+    "moe_router_dw": (_I, [_P, _P, _I64, _I, _I, _P, _P, _SZ, _P]),
+    "moe_select_experts": (_I, [_P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
+    "moe_select_experts_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _F, _F, _P, _P]),
+    "moe_grad_norm": (_I, [_P, _P, _P, _I, _F, _P, _P, _SZ, _P]),
+    "moe_clip_grads": (_I, [_P, _P, _P, _P, _I, _F, _P, _P, _SZ, _P]),
 }
 
 _lib = None

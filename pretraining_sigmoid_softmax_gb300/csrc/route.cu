@@ -421,6 +421,24 @@ __global__ void __launch_bounds__(256) route_bwd_dwr_kernel(
     }
 }
 
+// The three bf16 pieces of a logit gradient [T, E] for the tensor-core dW_r: piece p at
+// dl3 + p * pstride as a [T, np] matrix (zero past E), as route_bwd_dlogits_kernel writes them.
+__global__ void __launch_bounds__(256) split3_cols_kernel(const float* __restrict__ dlogits,
+                                                          int64_t T, int E, int np, int64_t pstride,
+                                                          __nv_bfloat16* __restrict__ dl3) {
+    const int64_t n = T * np;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = i / np;
+        const int e = (int)(i % np);
+        __nv_bfloat16 p0, p1, p2;
+        split3_bf16(e < E ? dlogits[t * E + e] : 0.f, p0, p1, p2);
+        dl3[i] = p0;
+        dl3[pstride + i] = p1;
+        dl3[2 * pstride + i] = p2;
+    }
+}
+
 __global__ void route_bwd_reduce_kernel(const float* __restrict__ part, int64_t nsplit,
                                         int64_t n, float* __restrict__ dW_r) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -666,6 +684,76 @@ extern "C" int moe_route_bwd(const float* dg, const moe_bf16* x, const int32_t* 
         dim3 grid(d / kBwTJ, (unsigned)cdiv(E, kBwTE), (unsigned)nsplit);
         route_bwd_dwr_kernel<<<grid, 256, 0, st>>>(
             dlogits, reinterpret_cast<const __nv_bfloat16*>(x), T, d, E, part);
+        if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
+    }
+    const int64_t n = (int64_t)E * d;
+    route_bwd_reduce_kernel<<<(unsigned)cdiv(n, 256), 256, 0, st>>>(part, nsplit, n, dW_r);
+    return launch_status();
+}
+
+// The logits come from the router forward with a choice of no experts (k = 0): its softmax
+// form also gives the logsumexp and the z-loss's partial sums.
+extern "C" int moe_router_logits(const moe_bf16* x, const float* W_r, int64_t T, int d, int E,
+                                 float z_coef, float* logits, float* lse, float* z_loss, void* ws,
+                                 size_t ws_bytes, moe_stream_t stream) {
+    if (!x || !W_r || !logits) return MOE_ERR_INVALID_ARG;
+    if (T <= 0 || d <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts || d % 128 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(W_r)) return MOE_ERR_INVALID_ARG;
+    if (!ws) return MOE_ERR_WORKSPACE;
+    WsCarver wc(ws, ws_bytes);
+    const int epad = route_tc_epad(E);
+    int64_t nzp = route_blocks(T);
+    if (4 * route_tc_tiles(T) > nzp) nzp = 4 * route_tc_tiles(T);
+    double* zp = wc.take<double>(nzp);
+    __nv_bfloat16* w3 = epad ? wc.take<__nv_bfloat16>((size_t)3 * epad * d) : nullptr;
+    float* own_lse = wc.take<float>(T);
+    if (!wc.ok()) return MOE_ERR_WORKSPACE;
+    if (!device_supported()) return MOE_ERR_UNSUPPORTED;
+    if (!lse) lse = own_lse;
+    cudaStream_t st = (cudaStream_t)stream;
+    int64_t nb = 0;
+    int rc;
+    if (epad)
+        rc = launch_route_logits_tc(reinterpret_cast<const __nv_bfloat16*>(x), W_r, nullptr, T, d,
+                                    E, 0, MOE_MODE_SOFTMAX, logits, nullptr, nullptr, nullptr, lse,
+                                    zp, &nb, w3, st);
+    else
+        rc = launch_route_fwd<256, 64, 8, 8>(x, W_r, nullptr, T, d, E, 0, MOE_MODE_SOFTMAX, logits,
+                                             nullptr, nullptr, nullptr, lse, zp, &nb, st);
+    if (rc != MOE_OK || !z_loss) return rc;
+    z_finalize_kernel<<<1, 256, 0, st>>>(zp, nb, T, z_coef, z_loss);
+    return launch_status();
+}
+
+extern "C" int moe_router_dw(const float* dlogits, const moe_bf16* x, int64_t T, int d, int E,
+                             float* dW_r, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    if (!dlogits || !x || !dW_r) return MOE_ERR_INVALID_ARG;
+    if (T <= 0 || d <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts || d % 128 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(dW_r)) return MOE_ERR_INVALID_ARG;
+    if (!ws) return MOE_ERR_WORKSPACE;
+    WsCarver wc(ws, ws_bytes);
+    const int np = route_tc_np(E);
+    int64_t nsplit = route_bwd_splits(T);
+    if (np && route_tc_splits_max(T) > nsplit) nsplit = route_tc_splits_max(T);
+    float* part = wc.take<float>((size_t)nsplit * E * d);
+    const int64_t pstride = (T * np + 127) / 128 * 128;
+    __nv_bfloat16* dl3 = np ? wc.take<__nv_bfloat16>((size_t)3 * pstride) : nullptr;
+    if (!wc.ok()) return MOE_ERR_WORKSPACE;
+    if (!device_supported()) return MOE_ERR_UNSUPPORTED;
+    cudaStream_t st = (cudaStream_t)stream;
+    const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(x);
+    if (np) {
+        int64_t blocks = cdiv(T * np, 256);
+        if (blocks > (int64_t)sm_count() * 16) blocks = (int64_t)sm_count() * 16;
+        split3_cols_kernel<<<(unsigned)blocks, 256, 0, st>>>(dlogits, T, E, np, pstride, dl3);
+        if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
+        const int rc = launch_route_dwr_tc(xb, dl3, pstride, T, d, E, part, &nsplit, st);
+        if (rc != MOE_OK) return rc;
+    } else {
+        dim3 grid(d / kBwTJ, (unsigned)cdiv(E, kBwTE), (unsigned)nsplit);
+        route_bwd_dwr_kernel<<<grid, 256, 0, st>>>(dlogits, xb, T, d, E, part);
         if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
     }
     const int64_t n = (int64_t)E * d;

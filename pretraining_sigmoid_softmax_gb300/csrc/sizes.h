@@ -10,6 +10,10 @@ constexpr int kRouteTokensPerCta = 64;     // router forward: tokens per CTA
 constexpr int kHistTokensPerCta = 256;     // permute: tokens per histogram chunk
 constexpr int kRouteBwdTokensPerSplit = 2048;  // router backward: tokens per dW_r split
 constexpr int kMaxExperts = 256;
+constexpr int kNormMaxD = 32768;           // norm: widest row
+constexpr int kNormBwdParts = 608;         // norm backward: CTAs, a dw partial row each
+constexpr int kClipParts = 1216;           // gradient norm: CTAs, a partial sum each
+constexpr int kMaxGroups = 32;             // choice of experts: groups
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -67,6 +71,18 @@ inline size_t ws_router_dx(int64_t T, int d, int E) {
     return round256(2 * 2 * pstride) + round256((size_t)3 * np * d * 2);
 }
 
+// Norm backward: one partial row of dw per CTA.
+inline int64_t norm_bwd_parts(int64_t T) { return T < kNormBwdParts ? T : kNormBwdParts; }
+inline size_t ws_norm_bwd(int64_t T, int d) {
+    return round256(sizeof(float) * (size_t)norm_bwd_parts(T) * d);
+}
+// Gradient norm: a partial sum of squares per CTA.
+inline size_t ws_clip() { return round256(sizeof(double) * kClipParts); }
+// Router logits alone: what the router forward takes, and a logsumexp per token.
+inline size_t ws_router_logits(int64_t T, int d, int E) {
+    return ws_route(T, d, E) + round256(sizeof(float) * T) + 256;
+}
+
 inline size_t ws_total(int64_t T, int d, int E, int k) {
     (void)k;
     size_t m = ws_route(T, d, E);
@@ -75,6 +91,9 @@ inline size_t ws_total(int64_t T, int d, int E, int k) {
     if (ws_expert(E) > m) m = ws_expert(E);
     if (ws_aux(T, E) > m) m = ws_aux(T, E);
     if (ws_router_dx(T, d, E) > m) m = ws_router_dx(T, d, E);
+    if (ws_norm_bwd(T, d) > m) m = ws_norm_bwd(T, d);
+    if (ws_clip() > m) m = ws_clip();
+    if (ws_router_logits(T, d, E) > m) m = ws_router_logits(T, d, E);
     return m + 256;
 }
 

@@ -329,3 +329,210 @@ def moe_router_dx(dlogits, W_r, dx_r, ws, stream=None):
     _contig(dlogits, W_r, dx_r, ws)
     _check(_lib.load().moe_router_dx(_p(dlogits), _p(W_r), T, d, E, _p(dx_r), _p(ws), ws.numel(),
                                      _stream(stream)), "moe_router_dx")
+
+
+# ------------------------------------------------- around the layer: norm, groups, clipping
+# These entry points check their tensors here (device, type, shape), since a row count or a
+# type read from the wrong tensor would send a kernel past a buffer's end.
+
+TYPE_BF16 = 0
+TYPE_F32 = 1
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+
+
+def _need(name, t, dtype, shape, optional=False):
+    """`t` has this type and shape, is contiguous and lies on the current CUDA device."""
+    if t is None:
+        if optional:
+            return
+        raise MoEError(f"{name} is missing")
+    if t.dtype is not dtype:
+        raise MoEError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise MoEError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise MoEError("tensors passed to the MoE library must be contiguous")
+    _on_device(name, t)
+
+
+def _on_device(name, t):
+    if not t.is_cuda:
+        raise MoEError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise MoEError(f"{name} is on {t.device}, but the current device is "
+                       f"cuda:{torch.cuda.current_device()}")
+
+
+def _need_ws(ws):
+    if ws is None:
+        raise MoEError("ws is missing")
+    _need("ws", ws, torch.uint8, ws.shape)
+
+
+def _rows(name, t):
+    """The shape of a 2-D tensor; both sizes at least 1."""
+    if t is None or t.dim() != 2 or 0 in t.shape:
+        raise MoEError(f"{name} must be a 2-D tensor with at least one row and column"
+                       + ("" if t is None else f", got shape {tuple(t.shape)}"))
+    return t.shape
+
+
+def _res_type(name, t):
+    if t.dtype not in _TYPES:
+        raise MoEError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def moe_rms_norm(x, residual, w, eps, z, y, yq=None, sy=None, rstd=None, stream=None):
+    """z = residual + x, y = z / rms(z) * w; yq (uint8) and sy: E4M3 codes and scales of y's rows.
+    residual and z None: y = x / rms(x) * w. z may be the residual's buffer, y may be x's."""
+    T, d = shape = _rows("x", x)
+    _need("x", x, torch.bfloat16, shape)
+    _need("w", w, torch.float32, (d,))
+    rt = TYPE_BF16
+    if residual is not None:
+        rt = _res_type("residual", residual)
+        _need("residual", residual, residual.dtype, shape)
+        _need("z", z, residual.dtype, shape)
+    elif z is not None:
+        raise MoEError("z is the sum of x and the residual: without a residual it is x itself")
+    _need("y", y, torch.bfloat16, shape, optional=True)
+    _need("yq", yq, torch.uint8, shape, optional=True)
+    _need("sy", sy, torch.float32, (T,), optional=True)
+    _need("rstd", rstd, torch.float32, (T,), optional=True)
+    _check(_lib.load().moe_rms_norm(_p(x), _p(residual), rt, _p(w), float(eps), T, d, _p(z), _p(y),
+                                    _p(yq), _p(sy), _p(rstd), _stream(stream)), "moe_rms_norm")
+
+
+def moe_rms_norm_bwd(dy, dres, z, rstd, w, dz, dx, dw, ws, stream=None):
+    """dz (of z's type) is the gradient of the residual and of x, dx the same as bf16 or None;
+    dres: the gradient that reaches z past the norm, or None. dz may be dres's buffer."""
+    T, d = shape = _rows("dy", dy)
+    _need("dy", dy, torch.bfloat16, shape)
+    if z is None:
+        raise MoEError("z is missing")
+    rt = _res_type("z", z)
+    _need("z", z, z.dtype, shape)
+    _need("dres", dres, z.dtype, shape, optional=True)
+    _need("rstd", rstd, torch.float32, (T,))
+    _need("w", w, torch.float32, (d,))
+    _need("dz", dz, z.dtype, shape)
+    _need("dx", dx, torch.bfloat16, shape, optional=True)
+    _need("dw", dw, torch.float32, (d,))
+    _need_ws(ws)
+    _check(_lib.load().moe_rms_norm_bwd(_p(dy), _p(dres), _p(z), rt, _p(rstd), _p(w), T, d, _p(dz),
+                                        _p(dx), _p(dw), _p(ws), ws.numel(), _stream(stream)),
+           "moe_rms_norm_bwd")
+
+
+def moe_router_logits(x, W_r, logits, ws, lse=None, z_loss=None, z_coef=0.0, stream=None):
+    """The router's logits alone (and their logsumexp and z-loss), for moe_select_experts."""
+    T, d = shape = _rows("x", x)
+    E = _rows("W_r", W_r)[0]
+    _need("x", x, torch.bfloat16, shape)
+    _need("W_r", W_r, torch.float32, (E, d))
+    _need("logits", logits, torch.float32, (T, E))
+    _need("lse", lse, torch.float32, (T,), optional=True)
+    _need("z_loss", z_loss, torch.float32, (1,), optional=True)
+    _need_ws(ws)
+    _check(_lib.load().moe_router_logits(_p(x), _p(W_r), T, d, E, float(z_coef), _p(logits),
+                                         _p(lse), _p(z_loss), _p(ws), ws.numel(),
+                                         _stream(stream)), "moe_router_logits")
+
+
+def moe_router_dw(dlogits, x, dW_r, ws, stream=None):
+    """The router weight's gradient dlogits^T x from a logit gradient that is known already."""
+    T, E = _rows("dlogits", dlogits)
+    d = _rows("x", x)[1]
+    _need("dlogits", dlogits, torch.float32, (T, E))
+    _need("x", x, torch.bfloat16, (T, d))
+    _need("dW_r", dW_r, torch.float32, (E, d))
+    _need_ws(ws)
+    _check(_lib.load().moe_router_dw(_p(dlogits), _p(x), T, d, E, _p(dW_r), _p(ws), ws.numel(),
+                                     _stream(stream)), "moe_router_dw")
+
+
+def moe_select_experts(logits, b, k, mode, n_group, topk_group, group_rule, renorm, scale,
+                       topk_idx, topk_gate, topk_score, lse=None, stream=None):
+    """The k experts of every token from its logits, within the topk_group best of n_group groups;
+    b: selection bias [E] or None; lse (softmax mode): the logits' logsumexp, or None."""
+    T, E = shape = _rows("logits", logits)
+    _need("logits", logits, torch.float32, shape)
+    _need("b", b, torch.float32, (E,), optional=True)
+    _need("topk_idx", topk_idx, torch.int32, (T, k))
+    _need("topk_gate", topk_gate, torch.float32, (T, k))
+    _need("topk_score", topk_score, torch.float32, (T, k))
+    _need("lse", lse, torch.float32, (T,), optional=True)
+    _check(_lib.load().moe_select_experts(_p(logits), _p(b), T, E, k, mode, n_group, topk_group,
+                                          group_rule, int(bool(renorm)), float(scale),
+                                          _p(topk_idx), _p(topk_gate), _p(topk_score), _p(lse),
+                                          _stream(stream)), "moe_select_experts")
+
+
+def moe_select_experts_bwd(dg, topk_idx, topk_score, logits, lse, mode, renorm, scale, dlogits,
+                           z_coef=0.0, dlogits_extra=None, stream=None):
+    """The logit gradient of moe_select_experts. logits and lse: softmax mode without renormalised
+    gates, or with a z_coef."""
+    T, E = shape = _rows("dlogits", dlogits)
+    k = _rows("topk_idx", topk_idx)[1]
+    _need("dlogits", dlogits, torch.float32, shape)
+    _need("dg", dg, torch.float32, (T, k))
+    _need("topk_idx", topk_idx, torch.int32, (T, k))
+    _need("topk_score", topk_score, torch.float32, (T, k))
+    _need("logits", logits, torch.float32, shape, optional=True)
+    _need("lse", lse, torch.float32, (T,), optional=True)
+    _need("dlogits_extra", dlogits_extra, torch.float32, shape, optional=True)
+    _check(_lib.load().moe_select_experts_bwd(_p(dg), _p(topk_idx), _p(topk_score), _p(logits),
+                                              _p(lse), _p(dlogits_extra), T, E, k, mode,
+                                              int(bool(renorm)), float(scale), float(z_coef),
+                                              _p(dlogits), _stream(stream)),
+           "moe_select_experts_bwd")
+
+
+def _grad_list(name, ts):
+    """Host arrays of a list of gradients: pointers, element counts, types."""
+    n = len(ts)
+    ptr, numel, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int * n)()
+    dev = torch.cuda.current_device() if ts and ts[0].is_cuda else None
+    for i, t in enumerate(ts):
+        rt = _TYPES.get(t.dtype)
+        if rt is None:
+            raise MoEError(f"{name}[{i}] must be bf16 or fp32, got {t.dtype}")
+        if not t.is_contiguous():
+            raise MoEError("tensors passed to the MoE library must be contiguous")
+        if not t.is_cuda or t.device.index != dev:
+            _on_device(f"{name}[{i}]", t)
+        ptr[i], numel[i], types[i] = t.data_ptr(), t.numel(), rt
+    return ptr, numel, types
+
+
+def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
+    """norm[0] = the global 2-norm of a list of bf16 or fp32 gradients, norm[1] = the factor that
+    clips it to max_norm."""
+    ptr, numel, types = _grad_list("grads", grads)
+    _need("norm", norm, torch.float32, (2,))
+    _need_ws(ws)
+    _check(_lib.load().moe_grad_norm(ptr, numel, types, len(grads), float(max_norm), _p(norm),
+                                     _p(ws), ws.numel(), _stream(stream)), "moe_grad_norm")
+
+
+def moe_clip_grads(grads, max_norm, out, norm, ws, stream=None):
+    """moe_grad_norm, and out[i] = norm[1] * grads[i]; out None clips in place."""
+    ptr, numel, types = _grad_list("grads", grads)
+    optr = ptr
+    if out is not None:
+        if len(out) != len(grads):
+            raise MoEError(f"{len(grads)} gradients, but {len(out)} outputs")
+        for i, (t, o) in enumerate(zip(grads, out)):
+            if o.shape != t.shape or o.dtype is not t.dtype:
+                raise MoEError(f"out[{i}] must be like grads[{i}], {tuple(t.shape)} {t.dtype}, "
+                               f"got {tuple(o.shape)} {o.dtype}")
+        optr = _grad_list("out", out)[0]
+    _need("norm", norm, torch.float32, (2,))
+    _need_ws(ws)
+    _check(_lib.load().moe_clip_grads(ptr, optr, numel, types, len(grads), float(max_norm),
+                                      _p(norm), _p(ws), ws.numel(), _stream(stream)),
+           "moe_clip_grads")

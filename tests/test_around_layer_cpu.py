@@ -1,0 +1,172 @@
+"""The argument checks of the operators around the layer (norm, router logits, choice of
+experts, gradient clipping): what they refuse, they refuse on the host, before any device work,
+so the checks hold without a GPU."""
+import ctypes
+import os
+import shutil
+
+import pytest
+import torch
+
+from pretraining_sigmoid_softmax_gb300 import _lib, build, ops
+
+needs_nvcc = pytest.mark.skipif(shutil.which("nvcc") is None and not os.path.exists("/usr/local/cuda/bin/nvcc"),
+                                reason="nvcc not installed")
+P = 4096       # a stand-in device address (never dereferenced on the host), 16-byte aligned
+BAD = P + 2    # not 16-byte aligned
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build_library()
+    return _lib.load()
+
+
+@needs_nvcc
+def test_norm_refusals(lib):
+    def fwd(x=P, res=P, rt=0, w=P, eps=1e-6, T=4, d=256, z=P, y=P, yq=None, sy=None, rstd=P):
+        return lib.moe_rms_norm(x, res, rt, w, eps, T, d, z, y, yq, sy, rstd, None)
+    assert fwd(x=None) == fwd(w=None) == INVALID
+    assert fwd(y=None) == INVALID                                # neither y nor codes
+    assert fwd(res=None) == fwd(z=None) == INVALID               # residual and z come together
+    assert fwd(yq=P) == fwd(sy=P) == INVALID                     # codes and scales come together
+    assert fwd(T=0) == fwd(d=0) == fwd(T=-1) == INVALID
+    assert fwd(eps=-1.0) == fwd(eps=float("nan")) == INVALID
+    assert fwd(rt=2) == INVALID
+    assert fwd(d=260) == fwd(d=32776) == fwd(T=1 << 31) == UNSUPPORTED
+    assert fwd(x=BAD) == fwd(res=BAD) == fwd(w=BAD) == fwd(z=BAD) == fwd(y=BAD) == INVALID
+    assert fwd(yq=P + 4, sy=P) == INVALID
+
+    def bwd(dy=P, dres=P, z=P, rt=0, rstd=P, w=P, T=4, d=256, dz=P, dx=None, dw=P, ws=P,
+            wb=1 << 20):
+        return lib.moe_rms_norm_bwd(dy, dres, z, rt, rstd, w, T, d, dz, dx, dw, ws, wb, None)
+    assert {bwd(dy=None), bwd(z=None), bwd(rstd=None), bwd(w=None), bwd(dz=None),
+            bwd(dw=None)} == {INVALID}
+    assert bwd(T=0) == bwd(d=0) == bwd(rt=-1) == INVALID
+    assert bwd(d=12) == bwd(d=32776) == UNSUPPORTED
+    assert {bwd(dy=BAD), bwd(dres=BAD), bwd(z=BAD), bwd(w=BAD), bwd(dz=BAD), bwd(dx=BAD)} == {INVALID}
+    assert bwd(ws=None) == bwd(ws=BAD) == bwd(wb=4 * 256 * 4 - 1) == WORKSPACE
+
+
+@needs_nvcc
+def test_router_logits_and_weight_gradient_refusals(lib):
+    def logits(x=P, W=P, T=16, d=256, E=8, out=P, ws=P, wb=1 << 20):
+        return lib.moe_router_logits(x, W, T, d, E, 0.0, out, None, None, ws, wb, None)
+    assert logits(x=None) == logits(W=None) == logits(out=None) == INVALID
+    assert logits(T=0) == logits(d=0) == logits(E=0) == INVALID
+    assert logits(E=257) == logits(d=200) == UNSUPPORTED
+    assert logits(x=BAD) == logits(W=BAD) == INVALID
+    assert logits(ws=None) == logits(wb=64) == WORKSPACE
+
+    def dw(dl=P, x=P, T=16, d=256, E=8, out=P, ws=P, wb=1 << 20):
+        return lib.moe_router_dw(dl, x, T, d, E, out, ws, wb, None)
+    assert dw(dl=None) == dw(x=None) == dw(out=None) == INVALID
+    assert dw(T=0) == dw(d=0) == dw(E=0) == INVALID
+    assert dw(E=257) == dw(d=200) == UNSUPPORTED
+    assert dw(x=BAD) == dw(out=BAD) == INVALID
+    assert dw(ws=None) == dw(wb=64) == WORKSPACE
+
+
+@needs_nvcc
+def test_choice_refusals(lib):
+    def sel(l=P, b=None, T=4, E=64, k=8, mode=0, G=8, tg=4, rule=1, idx=P, gate=P, score=P):
+        return lib.moe_select_experts(l, b, T, E, k, mode, G, tg, rule, 1, 1.0, idx, gate, score,
+                                      None, None)
+    assert sel(l=None) == sel(idx=None) == sel(gate=None) == sel(score=None) == INVALID
+    assert sel(T=0) == sel(E=0) == sel(k=0) == sel(G=0) == sel(tg=0) == INVALID
+    assert sel(mode=2) == sel(rule=2) == INVALID
+    assert sel(tg=9) == INVALID                        # more groups kept than there are
+    assert sel(E=60, G=8) == INVALID                   # groups of unequal size
+    assert sel(k=9, G=8, tg=1) == INVALID              # fewer experts left than chosen
+    assert sel(E=264, G=8) == UNSUPPORTED              # too many experts
+    assert sel(E=4, k=5, G=1, tg=1) == UNSUPPORTED     # more chosen than there are
+    assert sel(E=256, k=33, G=1, tg=1) == UNSUPPORTED
+    assert sel(E=64, k=8, G=64, tg=32) == UNSUPPORTED  # too many groups
+
+    def bwd(dg=P, idx=P, score=P, l=P, lse=P, T=4, E=64, k=8, mode=0, renorm=1, z=0.0, out=P):
+        return lib.moe_select_experts_bwd(dg, idx, score, l, lse, None, T, E, k, mode, renorm, 1.0,
+                                          z, out, None)
+    assert bwd(dg=None) == bwd(idx=None) == bwd(score=None) == bwd(out=None) == INVALID
+    assert bwd(T=0) == bwd(E=0) == bwd(k=0) == bwd(mode=5) == INVALID
+    assert bwd(z=1e-3) == INVALID                                   # a z-loss needs softmax scores
+    assert bwd(mode=1, renorm=0, l=None) == bwd(mode=1, renorm=0, lse=None) == INVALID
+    assert bwd(mode=1, z=1e-3, lse=None) == INVALID
+    assert bwd(E=257) == bwd(E=4, k=5) == bwd(k=33) == UNSUPPORTED
+
+
+def _arrays(ptrs, numel, types):
+    n = len(ptrs)
+    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types))
+
+
+@needs_nvcc
+def test_clip_refusals(lib):
+    def clip(grads=(P,), out=None, numel=(64,), types=(1,), count=None, max_norm=1.0, norm=P, ws=P,
+             wb=1 << 20):
+        g, n, t = _arrays(grads, numel, types)
+        o = g if out is None else _arrays(out, numel, types)[0]
+        c = len(grads) if count is None else count
+        return lib.moe_clip_grads(g, o, n, t, c, max_norm, norm, ws, wb, None)
+    assert clip(count=0) == clip(count=-1) == INVALID
+    assert clip(norm=None) == clip(max_norm=-1.0) == clip(max_norm=float("nan")) == INVALID
+    assert clip(types=(2,)) == clip(numel=(-1,)) == INVALID
+    assert clip(grads=(None,)) == INVALID
+    assert clip(grads=(P + 2,)) == INVALID                          # fp32 off its own alignment
+    assert clip(grads=(P + 1,), types=(0,)) == INVALID
+    assert clip(grads=(P,), out=(None,)) == INVALID
+    assert clip(ws=None) == clip(ws=BAD) == clip(wb=128) == WORKSPACE
+    two = dict(numel=(64, 64), types=(1, 1))
+    assert clip(grads=(P, P), **two) == INVALID                     # the same tensor twice, in place
+    assert clip(grads=(P, P + 128), **two) == INVALID               # tensors that overlap
+    far = 1 << 20
+    assert clip(grads=(P, far), out=(2 * far, 2 * far), **two) == INVALID      # one output twice
+    assert clip(grads=(P, far), out=(far, 2 * far), **two) == INVALID          # another's gradient
+    assert clip(grads=(P, far), out=(P + 64, 2 * far), **two) == INVALID       # shifted in place
+    assert lib.moe_clip_grads(*_arrays((P,), (4,), (1,))[:1], None, *_arrays((P,), (4,), (1,))[1:],
+                              1, 1.0, P, P, 1 << 20, None) == INVALID
+    # what only reads may name a tensor twice: the refusal then comes from the missing device
+    g, n, t = _arrays((P, P), (64, 64), (1, 1))
+    assert lib.moe_grad_norm(g, n, t, 2, 1.0, P, P, 128, None) == WORKSPACE
+
+
+@needs_nvcc
+def test_workspace_covers_the_operators(lib):
+    for T, d in [(1, 8), (5, 1000), (65536, 4096), (700, 32768)]:
+        assert lib.moe_workspace_bytes(T, d, 1, 1) >= min(T, 608) * d * 4
+
+
+def test_binding_refuses_wrong_tensors():
+    """Types, shapes, layouts and devices are checked before the library is called."""
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    x, w = torch.zeros(4, 16, dtype=bf), torch.ones(16)
+    y = torch.empty_like(x)
+    bad = [
+        (lambda: ops.moe_rms_norm(x, None, w, 1e-6, None, y), "CUDA tensor"),
+        (lambda: ops.moe_rms_norm(x.float(), None, w, 1e-6, None, y), "x must be torch.bfloat16"),
+        (lambda: ops.moe_rms_norm(x.t(), None, w, 1e-6, None, y), "contiguous"),
+        (lambda: ops.moe_rms_norm(x[0], None, w, 1e-6, None, y), "2-D"),
+        (lambda: ops.moe_rms_norm(x[:0], None, w, 1e-6, None, y), "at least one row"),
+    ]
+    for call, says in bad:
+        with pytest.raises(ops.MoEError, match=says):
+            call()
+    with pytest.raises(ops.MoEError, match="CUDA tensor"):
+        ops.moe_select_experts(torch.zeros(4, 8), None, 2, ops.MODE_SIGMOID, 1, 1, ops.GROUP_MAX,
+                               True, 1.0, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2),
+                               torch.zeros(4, 2))
+    with pytest.raises(ops.MoEError, match="CUDA tensor"):
+        ops.moe_select_experts_bwd(torch.zeros(4, 2), torch.zeros(4, 2, dtype=torch.int32),
+                                   torch.zeros(4, 2), None, None, ops.MODE_SIGMOID, True, 1.0,
+                                   torch.zeros(4, 8))
+    ws, norm = torch.zeros(16384, dtype=u8), torch.zeros(2)
+    with pytest.raises(ops.MoEError, match="CUDA tensor"):
+        ops.moe_clip_grads([torch.zeros(4)], 1.0, None, norm, ws)
+    with pytest.raises(ops.MoEError, match="bf16 or fp32"):
+        ops.moe_grad_norm([torch.zeros(4, dtype=torch.float64)], 1.0, norm, ws)
+    with pytest.raises(ops.MoEError, match="CUDA tensor"):
+        ops.moe_router_logits(x, torch.zeros(2, 16), torch.zeros(4, 2), ws)
+    with pytest.raises(ops.MoEError, match="CUDA tensor"):
+        ops.moe_router_dw(torch.zeros(4, 2), x, torch.zeros(2, 16), ws)
+    with pytest.raises(ops.MoEError, match="CUDA tensor"):
+        ops.moe_rms_norm_bwd(x, None, x, torch.zeros(4), w, y, None, torch.zeros(16), ws)
