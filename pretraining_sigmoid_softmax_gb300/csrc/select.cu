@@ -12,6 +12,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "sizes.h"
 
@@ -40,14 +42,31 @@ __device__ __forceinline__ float stable_sigmoid(float l) {
     return (l >= 0.f ? 1.f : e) / (1.f + e);  // a NaN takes the second form and stays one
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Over the L consecutive lanes that share a token (L a power of two), by a butterfly.
+template <int L>
+__device__ __forceinline__ float seg_max(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+template <int L, typename F>
+__device__ __forceinline__ F seg_sum(F v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ int seg_max(int v) {
+    if constexpr (L == 32) return __reduce_max_sync(kFull, v);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ int seg_min(int v) {
+    if constexpr (L == 32) return __reduce_min_sync(kFull, v);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kFull, v, o));
     return v;
 }
 
@@ -56,7 +75,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ void row_softmax(const float* row, int E, int lane, float& mx, float& sum) {
     mx = -INFINITY;
     for (int e = lane; e < E; e += 32) mx = fmaxf(mx, row[e]);
-    mx = warp_max(mx);
+    mx = seg_max<32>(mx);
     sum = 0.f;
     bool bad = false;
     for (int e = lane; e < E; e += 32) {
@@ -64,25 +83,22 @@ __device__ __forceinline__ void row_softmax(const float* row, int E, int lane, f
         bad |= l != l;
         if (mx != -INFINITY) sum += expf(l - mx);
     }
-    sum = warp_sum(sum);
+    sum = seg_sum<32>(sum);
     if (__any_sync(kFull, bad)) sum = NAN;
-}
-
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
 }
 
 // Below this sum of the chosen scores one of them may have left fp32's normal range without its
 // gate doing so: the gates are then formed in 64 bits.
 constexpr float kSmallSum = 9.5367432e-7f;  // 2^-20
 
-// Scores and gates of the chosen experts (lane i < k holds slot i's expert), stored with the
-// indices. A token whose chosen scores are all zero (in 64 bits) has gates of zero.
-__device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int lane, int my_e,
+// Scores and gates of the chosen experts, stored with the indices: lane `sub` < k of the L lanes
+// of a token holds slot `sub`'s expert. `live` masks tokens that are not there, or whose choice
+// is made elsewhere. A token whose chosen scores are all zero (in 64 bits) has gates of zero.
+// Executed by the whole warp.
+template <int L>
+__device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int sub, bool live, int my_e,
                                        float mx, float sum) {
-    const bool on = lane < P.k, sigmoid = P.mode == MOE_MODE_SIGMOID;
+    const bool on = live && sub < P.k, sigmoid = P.mode == MOE_MODE_SIGMOID;
     float l = 0.f, s = 0.f;
     if (on) {
         l = P.logits[t * P.E + my_e];
@@ -90,22 +106,23 @@ __device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int lan
     }
     float g = s;
     if (P.renorm) {
-        const float S = warp_sum(s);
-        if (S < kSmallSum) {
+        const float S = seg_sum<L>(s);
+        g = s / S;
+        const bool small = S < kSmallSum;
+        if (__any_sync(kFull, live && small)) {  // the whole warp: the sum below is collective
             double sd = 0.0;
-            if (on) sd = sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : sum == 0.f ? 0.0 : exp((double)l - (double)mx);
-            const double Sd = warp_sum(sd);
-            g = Sd == 0.0 ? 0.f : (float)(sd / Sd);
-        } else {
-            g = s / S;
+            if (on && small)
+                sd = sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : sum == 0.f ? 0.0 : exp((double)l - (double)mx);
+            const double Sd = seg_sum<L>(sd);
+            if (small) g = Sd == 0.0 ? 0.f : (float)(sd / Sd);
         }
     }
     if (on) {
-        P.idx[t * P.k + lane] = my_e;
-        P.gate[t * P.k + lane] = P.scale * g;
-        P.score[t * P.k + lane] = s;
+        P.idx[t * P.k + sub] = my_e;
+        P.gate[t * P.k + sub] = P.scale * g;
+        P.score[t * P.k + sub] = s;
     }
-    if (P.mode == MOE_MODE_SOFTMAX && P.lse && lane == 0) P.lse[t] = mx + logf(sum);
+    if (live && sub == 0 && !sigmoid && P.lse) P.lse[t] = mx + logf(sum);
 }
 
 // Total order of the choice: larger value, then lower index. An index of INT_MAX marks "none".
@@ -151,7 +168,9 @@ __device__ int select_exact(const SelectParams& P, int64_t t, int lane, float mx
     const int E = P.E;
     double s[VJ], by[VJ];  // score + bias (a group's sum), and what orders the experts
     double total = 1.0;
-    if (P.mode == MOE_MODE_SOFTMAX) {
+    // the scores themselves are needed for values with a bias and for sums over a group
+    const bool scores = P.b || (P.n_group > 1 && P.rule == MOE_GROUP_TOP2);
+    if (P.mode == MOE_MODE_SOFTMAX && scores) {
         total = 0.0;
 #pragma unroll
         for (int j = 0; j < VJ; ++j) {
@@ -173,9 +192,11 @@ __device__ int select_exact(const SelectParams& P, int64_t t, int lane, float mx
         by[j] = -INFINITY;
         if (e >= E) continue;
         const double l = row[e];
-        s[j] = P.mode == MOE_MODE_SOFTMAX ? s[j] / total : 1.0 / (1.0 + exp(-l));
-        if (P.b) s[j] += (double)P.b[e];
-        s[j] = no_nan(s[j]);
+        if (scores) {
+            s[j] = P.mode == MOE_MODE_SOFTMAX ? s[j] / total : 1.0 / (1.0 + exp(-l));
+            if (P.b) s[j] += (double)P.b[e];
+            s[j] = no_nan(s[j]);
+        }
         by[j] = P.b ? s[j] : no_nan(l);  // without a bias the scores have the logits' order
     }
     uint32_t open = 0;  // bit j: expert lane + 32 j can be chosen
@@ -232,15 +253,307 @@ __device__ int select_exact(const SelectParams& P, int64_t t, int lane, float mx
     return my_e;
 }
 
-// One warp per token.
-__global__ void __launch_bounds__(kSelWarps * 32) select_exact_kernel(const SelectParams P) {
-    const int lane = threadIdx.x % 32;
-    const int64_t t = (int64_t)blockIdx.x * kSelWarps + threadIdx.x / 32;
-    if (t >= P.T) return;  // whole warp
+// One token by a whole warp, in 64 bits, with its outputs.
+__device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int lane) {
     float mx = 0.f, sum = 1.f;
     if (P.mode == MOE_MODE_SOFTMAX) row_softmax(P.logits + t * P.E, P.E, lane, mx, sum);
     const int my_e = select_exact(P, t, lane, mx);
-    finish(P, t, lane, my_e, mx, sum);
+    finish<32>(P, t, lane, true, my_e, mx, sum);
+}
+
+// Every token in 64 bits, one warp each: groupings that the lanes of select_kernel do not hold.
+__global__ void __launch_bounds__(kSelWarps * 32) select_exact_kernel(const SelectParams P) {
+    const int64_t t = (int64_t)blockIdx.x * kSelWarps + threadIdx.x / 32;
+    if (t < P.T) select_token(P, t, threadIdx.x % 32);  // whole warps
+}
+
+// ------------------------------------------------------------------- the choice from 32 bits
+// L lanes per token (32 / L tokens per warp), each holding up to V consecutive experts of one
+// group; lpg lanes (a power of two) hold a group, vr experts each. Every expert becomes one
+// integer key, its selection value above its index in the low 8 bits: a lane sorts its keys with
+// minima and maxima alone, groups are compared by their lanes' first keys, and each of the k
+// rounds takes the largest of the lanes' first keys, which names its expert itself.
+//
+// The keys are rounded values. Where two of them that the choice has to tell apart lie within
+// the rounding's bound, the token is chosen again: the experts that may be among the k are
+// evaluated in 64 bits (select_close), or all of them (select_token) where a group's choice is
+// in doubt. About one token in 500 takes that way on Gaussian logits.
+//
+// With a bias the value is s + b in fixed point, 2^-shift units, s by the fast exponential and
+// reciprocal; without one it is the logit, whose upper 24 bits order it.
+struct SelectLayout {
+    int lpg, vr;
+    int vec;  // a lane's experts are aligned 16-byte vectors (or none)
+};
+
+constexpr float kKeyLimit = 2147483392.f;
+constexpr float kU = 5.9604645e-8f;  // 2^-24
+// Bounds of the fast scores' errors. Sigmoid: 1 / (1 + e^-l): the quotient is within 2 ulp (4 u
+// relative), the sum within u, and the exponential's relative error (1.5 |l| u + 4 u) enters
+// times s (1 - s): below 6.4 u in all. Softmax: e^(l - max) / sum: (1.5 |l - max| + 4) u, at
+// most 20 u for the sum, its reciprocal and the product; p |l - max| <= 0.37: 25 u p + 0.6 u.
+constexpr float kSigmoidErr = 6.4f * kU;
+constexpr float kSoftmaxErr = 25.f * kU;
+
+__device__ __forceinline__ int logit_key(float l) {
+    const int b = __float_as_int((l == l ? l : -INFINITY) + 0.0f);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+// NaN goes to the lower limit.
+__device__ __forceinline__ int value_key(float v, float unit) {
+    return __float2int_rn(fminf(fmaxf(v * unit, -kKeyLimit), kKeyLimit));
+}
+
+template <int V>
+__device__ __forceinline__ void sort_desc(int (&k)[V]) {
+    auto ce = [&](int a, int b) {
+        const int hi = max(k[a], k[b]);
+        k[b] = min(k[a], k[b]);
+        k[a] = hi;
+    };
+    if constexpr (V == 2) ce(0, 1);
+    if constexpr (V == 4) { ce(0, 1); ce(2, 3); ce(0, 2); ce(1, 3); ce(1, 2); }
+    if constexpr (V == 8) {
+        ce(0, 1); ce(2, 3); ce(4, 5); ce(6, 7);
+        ce(0, 2); ce(1, 3); ce(4, 6); ce(5, 7);
+        ce(1, 2); ce(5, 6);
+        ce(0, 4); ce(1, 5); ce(2, 6); ce(3, 7);
+        ce(2, 4); ce(3, 5);
+        ce(1, 2); ce(3, 4); ce(5, 6);
+    }
+}
+
+// Units of the fixed-point keys for biases of up to `maxb`: |s + b| < 2^(31 - shift).
+__device__ __forceinline__ int key_shift(float maxb) {
+    return maxb < 1.f ? 30 : maxb < 3.f ? 29 : maxb < 7.f ? 28 : 27;
+}
+
+// Score of one expert from its logit, fast (within the bounds above).
+__device__ __forceinline__ float fast_score(bool sigmoid, float l, float mx, float inv) {
+    return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __expf(l - mx) * inv;
+}
+
+// One token's choice where its groups are settled (`open`: bit g, group g stays) and the experts
+// that may be chosen are those whose key is at least `least`: they are gathered, one per lane,
+// evaluated in 64 bits and ranked. More than 32 of them: the token is left to select_token
+// (returns false). The keys are formed exactly as select_kernel forms them. Sigmoid scores, or
+// logits.
+template <bool LOGIT>
+__device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, uint32_t open,
+                                          int least, float unit, int* scratch) {
+    const float* row = P.logits + t * P.E;
+    const int per = P.E / P.n_group;
+    int n = 0;
+    for (int e0 = 0; e0 < P.E; e0 += 32) {
+        const int e = e0 + lane;
+        bool in = false;
+        if (e < P.E && ((open >> (e / per)) & 1u)) {
+            const float l = row[e];
+            const int key = LOGIT ? logit_key(l) : value_key(fast_score(true, l, 0.f, 1.f) + P.b[e], unit);
+            in = ((key & ~255) | e) >= least;
+        }
+        const uint32_t m = __ballot_sync(kFull, in);
+        const int at = n + __popc(m & ((1u << lane) - 1u));
+        if (in && at < 32) scratch[at] = e;
+        n += __popc(m);
+    }
+    if (n > 32) return false;
+    __syncwarp();
+    int e = INT_MAX;
+    double v = 0.0;
+    if (lane < n) {
+        e = scratch[lane];
+        const double l = row[e];
+        v = no_nan(LOGIT ? l : 1.0 / (1.0 + exp(-l)) + (double)P.b[e]);
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double ov = __shfl_sync(kFull, v, i);
+        const int oe = __shfl_sync(kFull, e, i);
+        rank += before(ov, oe, v, e) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < n && rank < P.k) scratch[rank] = e;
+    __syncwarp();
+    const int my_e = lane < P.k ? scratch[lane] : 0;
+    __syncwarp();
+    float mx = 0.f, sum = 1.f;
+    if (P.mode == MOE_MODE_SOFTMAX) row_softmax(row, P.E, lane, mx, sum);
+    finish<32>(P, t, lane, true, my_e, mx, sum);
+    return true;
+}
+
+template <int V, int L, bool LOGIT>
+__global__ void __launch_bounds__(kSelWarps * 32) select_kernel(const SelectParams P, const SelectLayout Y) {
+    constexpr int NT = 32 / L;
+    __shared__ int scratch[kSelWarps][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
+    const int per = P.E / P.n_group, G = P.n_group;
+    const bool sigmoid = P.mode == MOE_MODE_SIGMOID;
+    const bool top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
+    const int g = sub / Y.lpg, r = sub % Y.lpg;
+    const int first = g * per + r * Y.vr;
+    int count = g < G ? min(Y.vr, per - r * Y.vr) : 0;
+    if (count < 0) count = 0;
+
+    float bias[V];
+    float unit = 1.f, vmax = 1.f;
+    if constexpr (!LOGIT) {
+        float mb = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            bias[j] = j < count ? P.b[first + j] : 0.f;
+            if (isfinite(bias[j])) mb = fmaxf(mb, fabsf(bias[j]));
+        }
+        mb = seg_max<L>(mb);
+        const int shift = key_shift(mb);
+        unit = (float)(1u << shift);
+        vmax = (float)(1u << (31 - shift));
+    }
+
+    const int64_t stride = (int64_t)gridDim.x * kSelWarps * NT;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kSelWarps + warp) * NT; t0 < P.T; t0 += stride) {
+        const int64_t t = t0 + lane / L;
+        const bool live = t < P.T;
+        float l[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] = 0.f;
+        if (live) {
+            const float* src = P.logits + t * P.E + first;
+            if (V >= 4 && Y.vec) {
+                if (count == V) {
+#pragma unroll
+                    for (int j = 0; j + 3 < V; j += 4) {
+                        const float4 a = *reinterpret_cast<const float4*>(src + j);
+                        l[j] = a.x, l[(j + 1) % V] = a.y, l[(j + 2) % V] = a.z, l[(j + 3) % V] = a.w;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (j < count) l[j] = src[j];
+            }
+        }
+        bool odd = false;  // not a row for this kernel's arithmetic
+        float mx = 0.f, sum = 1.f, inv = 1.f;
+        if (!sigmoid) {
+            mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < count) mx = fmaxf(mx, l[j]);
+            mx = seg_max<L>(mx);
+            sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < count) sum += __expf(l[j] - mx);
+            sum = seg_sum<L>(sum);
+            odd = !(sum < 1e30f) || mx == -INFINITY;  // NaN or infinite logits
+            inv = __fdividef(1.0f, sum);
+        }
+        int key[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int k = LOGIT ? logit_key(l[j]) : value_key(fast_score(sigmoid, l[j], mx, inv) + bias[j], unit);
+            key[j] = j < count ? (k & ~255) | (first + j) : INT_MIN;
+        }
+        // how far apart two keys have to be to settle their order: twice the value's error (the
+        // score's, the sum's rounding and the fixed point's), and the index bits
+        int tol = 0;
+        if constexpr (!LOGIT) {
+            const float es = sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
+            tol = 260 + (int)ceilf(2.f * (es + kU * vmax) * unit);
+        }
+        uint32_t open = 1u;
+        int gs = 0;
+        float fa = -INFINITY, fb = -INFINITY;
+        if (LOGIT && top2 && G > 1) {  // a lane's two largest logits
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float x = j < count && l[j] == l[j] ? l[j] : -INFINITY;
+                fb = fmaxf(fb, fminf(fa, x));
+                fa = fmaxf(fa, x);
+                odd |= j < count && l[j] != l[j];  // a NaN's score counts as -inf in the sum
+            }
+        }
+        sort_desc<V>(key);
+        if (G > 1) {
+            int a = key[0], b = V > 1 ? key[1 % V] : INT_MIN;
+            for (int o = 1; o < Y.lpg; o <<= 1) {
+                if (LOGIT && top2) {
+                    const float oa = __shfl_xor_sync(kFull, fa, o), ob = __shfl_xor_sync(kFull, fb, o);
+                    fb = fmaxf(fmaxf(fb, ob), fminf(fa, oa));
+                    fa = fmaxf(fa, oa);
+                } else {
+                    const int oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+                    b = max(max(b, ob), min(a, oa));
+                    a = max(a, oa);
+                }
+            }
+            if (!top2) gs = a;
+            else if (!LOGIT) gs = (a >> 1) + (b >> 1);
+            else gs = __float_as_int(fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv));
+            // a sum with a value beyond the keys' range, or a second value that does not count
+            if (!LOGIT && top2 && g < G) odd |= b <= -(int)kKeyLimit + 512 || a >= (int)kKeyLimit - 512;
+            int rank = 0;
+            for (int h = 0; h < G; ++h) {
+                const int x = __shfl_sync(kFull, gs, h * Y.lpg, L);
+                rank += x > gs || (x == gs && h < g);
+            }
+            const bool kept = g < G && rank < P.topk_group;
+            if (P.topk_group < G) {
+                const int lo = seg_min<L>(kept ? gs : INT_MAX);
+                const int hi = seg_max<L>(!kept && g < G ? gs : INT_MIN);
+                if (LOGIT && top2) {  // sums of scores: softmax terms are within 160 u of themselves
+                    const float x = __int_as_float(lo), y = __int_as_float(hi);  // down to e^-87
+                    odd |= !(x - y > 2.f * (sigmoid ? 2.f * kSigmoidErr + kU * x : 161.f * kU * x)) || x < 1e-30f;
+                } else if (LOGIT) {
+                    odd |= (lo >> 8) == (hi >> 8);
+                } else {
+                    odd |= (uint32_t)lo - (uint32_t)hi <= (uint32_t)tol;
+                }
+            }
+            const uint32_t bits = __ballot_sync(kFull, kept && r == 0);
+            open = 0u;
+            for (int h = 0; h < G; ++h) open |= ((bits >> (lane / L * L + h * Y.lpg)) & 1u) << h;
+            if (!kept) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) key[j] = INT_MIN;
+            }
+        }
+        int my_key = 0, prev = 0;
+        bool close = false;
+        for (int i = 0; i <= P.k; ++i) {
+            const int w = seg_max<L>(key[0]);
+            if (i > 0) close |= LOGIT ? (w >> 8) == (prev >> 8) : (uint32_t)prev - (uint32_t)w <= (uint32_t)tol;
+            if (i == 0 && !LOGIT) odd |= w >= (int)kKeyLimit - 512;
+            if (i == P.k) break;
+            prev = w;
+            if (sub == i) my_key = w;
+            if (key[0] == w) {
+#pragma unroll
+                for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
+                key[V - 1] = INT_MIN;
+            }
+        }
+        // prev is the k-th key: what is not below it by more than the bound may be chosen
+        const uint32_t flagged = __ballot_sync(kFull, live && (odd || close));
+        const uint32_t oddball = __ballot_sync(kFull, live && odd);
+        const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
+        finish<L>(P, t, sub, live && !(flagged & mask), my_key & 255, mx, sum);
+        if (flagged) {
+            for (int q = 0; q < NT; ++q) {  // the warp together, one token at a time
+                const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (q * L);
+                if (!(flagged & m)) continue;
+                const int least = __shfl_sync(kFull, prev, q * L);
+                const uint32_t o = __shfl_sync(kFull, open, q * L);
+                const int by = LOGIT ? 255 : __shfl_sync(kFull, tol, q * L);
+                const bool all = (oddball & m) || (!LOGIT && !sigmoid);
+                const int from = LOGIT ? least & ~255 : least < INT_MIN + by ? INT_MIN : least - by;
+                if (all || !select_close<LOGIT>(P, t0 + q, lane, o, from, unit, scratch[warp]))
+                    select_token(P, t0 + q, lane);
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------- backward
@@ -283,13 +596,13 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
     }
     float ds = P.scale * dg;
     if (P.renorm) {
-        const float S = warp_sum(s);
-        const float m = warp_sum(s / S * dg);
+        const float S = seg_sum<32>(s);
+        const float m = seg_sum<32>(s / S * dg);
         ds = S == 0.f ? 0.f : P.scale / S * (dg - m);
     }
     const bool dense = softmax && (!P.renorm || P.z_scale != 0.f);
     float c = 0.f, l_se = 0.f;
-    if (softmax && !P.renorm) c = warp_sum(s * ds);
+    if (softmax && !P.renorm) c = seg_sum<32>(s * ds);
     if (dense) l_se = P.lse[t];
     const float v = dense ? ds : softmax ? ds * s : ds * s * (1.f - s);
     for (int e0 = 0; e0 < E; e0 += 32) {  // warp-uniform trip count
@@ -314,6 +627,44 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
     }
 }
 
+template <int L>
+int launch_lanes(const SelectParams& P, const SelectLayout& Y, cudaStream_t st) {
+    constexpr int NT = 32 / L;
+    int64_t blocks = cdiv(P.T, (int64_t)kSelWarps * NT);
+    const int64_t cap = (int64_t)sm_count() * 4;
+    if (blocks > cap) blocks = cap;
+    auto go = [&](auto kern) { kern<<<(unsigned)blocks, kSelWarps * 32, 0, st>>>(P, Y); };
+    auto pick = [&](auto logit) {
+        constexpr bool LOGIT = decltype(logit)::value;
+        if (Y.vr <= 1) go(select_kernel<1, L, LOGIT>);
+        else if (Y.vr <= 2) go(select_kernel<2, L, LOGIT>);
+        else if (Y.vr <= 4) go(select_kernel<4, L, LOGIT>);
+        else go(select_kernel<8, L, LOGIT>);
+    };
+    if (P.b) pick(std::false_type());
+    else pick(std::true_type());
+    return launch_status();
+}
+
+// The lanes of a token: the fewest per group (a power of two) that hold its experts at 8 each, and
+// at least one per slot. Groupings that need more than 32 lanes (their number no power of two
+// and their experts too many) are chosen in 64 bits throughout.
+int launch_select(const SelectParams& P, cudaStream_t st) {
+    const int per = P.E / P.n_group;
+    SelectLayout Y{1, 0, 0};
+    while (Y.lpg * 8 < per) Y.lpg *= 2;
+    int L = 8;
+    while (L < P.n_group * Y.lpg || L < P.k) L *= 2;
+    if (L > 32) {
+        select_exact_kernel<<<(unsigned)cdiv(P.T, kSelWarps), kSelWarps * 32, 0, st>>>(P);
+        return launch_status();
+    }
+    while (P.n_group * Y.lpg * 2 <= L && Y.lpg < per) Y.lpg *= 2;  // no lanes left over
+    Y.vr = (int)cdiv(per, Y.lpg);
+    Y.vec = (Y.vr == 8 || Y.vr == 4) && per % Y.vr == 0 && aligned16(P.logits);
+    return L == 8 ? launch_lanes<8>(P, Y, st) : L == 16 ? launch_lanes<16>(P, Y, st) : launch_lanes<32>(P, Y, st);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -334,8 +685,7 @@ extern "C" int moe_select_experts(const float* logits, const float* b, int64_t T
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     const SelectParams P{logits, b, T, E, k, mode, n_group, topk_group, group_rule, renorm ? 1 : 0,
                          scale, topk_idx, topk_gate, topk_score, lse};
-    select_exact_kernel<<<(unsigned)cdiv(T, kSelWarps), kSelWarps * 32, 0, (cudaStream_t)stream>>>(P);
-    return launch_status();
+    return launch_select(P, (cudaStream_t)stream);
 }
 
 extern "C" int moe_select_experts_bwd(const float* dg, const int32_t* topk_idx,
