@@ -343,11 +343,30 @@ GROUP_TOP2 = 1
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 
 
-def _need(name, t, dtype, shape, optional=False):
-    """`t` has this type and shape, is contiguous and lies on the current CUDA device."""
+_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, dev):
+    """The raw stream of a call: the one given, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _device(t):
+    """The current device's index where `t` is a CUDA tensor, else -2: no tensor's device, so that
+    the first check of one says what is wrong."""
+    return torch.cuda.current_device() if t is not None and t.get_device() >= 0 else -2
+
+
+def _ptr(name, t, dtype, shape, dev):
+    """The address of a tensor of this type and shape, contiguous and on the current device."""
+    if (t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev):
+        return t.data_ptr()
     if t is None:
-        if optional:
-            return
         raise MoEError(f"{name} is missing")
     if t.dtype is not dtype:
         raise MoEError(f"{name} must be {dtype}, got {t.dtype}")
@@ -355,21 +374,20 @@ def _need(name, t, dtype, shape, optional=False):
         raise MoEError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise MoEError("tensors passed to the MoE library must be contiguous")
-    _on_device(name, t)
-
-
-def _on_device(name, t):
     if not t.is_cuda:
         raise MoEError(f"{name} must be a CUDA tensor, got one on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise MoEError(f"{name} is on {t.device}, but the current device is "
-                       f"cuda:{torch.cuda.current_device()}")
+    raise MoEError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
 
 
-def _need_ws(ws):
+def _opt(name, t, dtype, shape, dev):
+    return None if t is None else _ptr(name, t, dtype, shape, dev)
+
+
+def _ws(ws, dev):
+    """Address and size of a workspace."""
     if ws is None:
         raise MoEError("ws is missing")
-    _need("ws", ws, torch.uint8, ws.shape)
+    return _ptr("ws", ws, torch.uint8, ws.shape, dev), ws.numel()
 
 
 def _rows(name, t):
@@ -381,78 +399,77 @@ def _rows(name, t):
 
 
 def _res_type(name, t):
-    if t.dtype not in _TYPES:
-        raise MoEError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    return _TYPES[t.dtype]
+    rt = None if t is None else _TYPES.get(t.dtype)
+    if rt is None:
+        raise MoEError(f"{name} must be bf16 or fp32" + ("" if t is None else f", got {t.dtype}"))
+    return rt
 
 
 def moe_rms_norm(x, residual, w, eps, z, y, yq=None, sy=None, rstd=None, stream=None):
     """z = residual + x, y = z / rms(z) * w; yq (uint8) and sy: E4M3 codes and scales of y's rows.
     residual and z None: y = x / rms(x) * w. z may be the residual's buffer, y may be x's."""
     T, d = shape = _rows("x", x)
-    _need("x", x, torch.bfloat16, shape)
-    _need("w", w, torch.float32, (d,))
-    rt = TYPE_BF16
+    bf16, f32 = torch.bfloat16, torch.float32
+    dev = _device(x)
+    xp = _ptr("x", x, bf16, shape, dev)
+    rt, zp, rp = TYPE_BF16, None, None
     if residual is not None:
         rt = _res_type("residual", residual)
-        _need("residual", residual, residual.dtype, shape)
-        _need("z", z, residual.dtype, shape)
+        rp = _ptr("residual", residual, residual.dtype, shape, dev)
+        zp = _ptr("z", z, residual.dtype, shape, dev)
     elif z is not None:
         raise MoEError("z is the sum of x and the residual: without a residual it is x itself")
-    _need("y", y, torch.bfloat16, shape, optional=True)
-    _need("yq", yq, torch.uint8, shape, optional=True)
-    _need("sy", sy, torch.float32, (T,), optional=True)
-    _need("rstd", rstd, torch.float32, (T,), optional=True)
-    _check(_lib.load().moe_rms_norm(_p(x), _p(residual), rt, _p(w), float(eps), T, d, _p(z), _p(y),
-                                    _p(yq), _p(sy), _p(rstd), _stream(stream)), "moe_rms_norm")
+    _check(_lib.load().moe_rms_norm(xp, rp, rt,
+                                    _ptr("w", w, f32, (d,), dev), eps, T, d, zp,
+                                    _opt("y", y, bf16, shape, dev),
+                                    _opt("yq", yq, torch.uint8, shape, dev),
+                                    _opt("sy", sy, f32, (T,), dev),
+                                    _opt("rstd", rstd, f32, (T,), dev), _stream_of(stream, dev)),
+           "moe_rms_norm")
 
 
 def moe_rms_norm_bwd(dy, dres, z, rstd, w, dz, dx, dw, ws, stream=None):
     """dz (of z's type) is the gradient of the residual and of x, dx the same as bf16 or None;
     dres: the gradient that reaches z past the norm, or None. dz may be dres's buffer."""
     T, d = shape = _rows("dy", dy)
-    _need("dy", dy, torch.bfloat16, shape)
-    if z is None:
-        raise MoEError("z is missing")
-    rt = _res_type("z", z)
-    _need("z", z, z.dtype, shape)
-    _need("dres", dres, z.dtype, shape, optional=True)
-    _need("rstd", rstd, torch.float32, (T,))
-    _need("w", w, torch.float32, (d,))
-    _need("dz", dz, z.dtype, shape)
-    _need("dx", dx, torch.bfloat16, shape, optional=True)
-    _need("dw", dw, torch.float32, (d,))
-    _need_ws(ws)
-    _check(_lib.load().moe_rms_norm_bwd(_p(dy), _p(dres), _p(z), rt, _p(rstd), _p(w), T, d, _p(dz),
-                                        _p(dx), _p(dw), _p(ws), ws.numel(), _stream(stream)),
-           "moe_rms_norm_bwd")
+    dev = _device(dy)
+    rt, zt, bf16, f32 = _res_type("z", z), z.dtype, torch.bfloat16, torch.float32
+    wp, wn = _ws(ws, dev)
+    _check(_lib.load().moe_rms_norm_bwd(_ptr("dy", dy, bf16, shape, dev),
+                                        _opt("dres", dres, zt, shape, dev),
+                                        _ptr("z", z, zt, shape, dev), rt,
+                                        _ptr("rstd", rstd, f32, (T,), dev),
+                                        _ptr("w", w, f32, (d,), dev), T, d,
+                                        _ptr("dz", dz, zt, shape, dev),
+                                        _opt("dx", dx, bf16, shape, dev),
+                                        _ptr("dw", dw, f32, (d,), dev), wp, wn,
+                                        _stream_of(stream, dev)), "moe_rms_norm_bwd")
 
 
 def moe_router_logits(x, W_r, logits, ws, lse=None, z_loss=None, z_coef=0.0, stream=None):
     """The router's logits alone (and their logsumexp and z-loss), for moe_select_experts."""
     T, d = shape = _rows("x", x)
     E = _rows("W_r", W_r)[0]
-    _need("x", x, torch.bfloat16, shape)
-    _need("W_r", W_r, torch.float32, (E, d))
-    _need("logits", logits, torch.float32, (T, E))
-    _need("lse", lse, torch.float32, (T,), optional=True)
-    _need("z_loss", z_loss, torch.float32, (1,), optional=True)
-    _need_ws(ws)
-    _check(_lib.load().moe_router_logits(_p(x), _p(W_r), T, d, E, float(z_coef), _p(logits),
-                                         _p(lse), _p(z_loss), _p(ws), ws.numel(),
-                                         _stream(stream)), "moe_router_logits")
+    dev, f32 = _device(x), torch.float32
+    wp, wn = _ws(ws, dev)
+    _check(_lib.load().moe_router_logits(_ptr("x", x, torch.bfloat16, shape, dev),
+                                         _ptr("W_r", W_r, f32, (E, d), dev), T, d, E, z_coef,
+                                         _ptr("logits", logits, f32, (T, E), dev),
+                                         _opt("lse", lse, f32, (T,), dev),
+                                         _opt("z_loss", z_loss, f32, (1,), dev), wp, wn,
+                                         _stream_of(stream, dev)), "moe_router_logits")
 
 
 def moe_router_dw(dlogits, x, dW_r, ws, stream=None):
     """The router weight's gradient dlogits^T x from a logit gradient that is known already."""
     T, E = _rows("dlogits", dlogits)
     d = _rows("x", x)[1]
-    _need("dlogits", dlogits, torch.float32, (T, E))
-    _need("x", x, torch.bfloat16, (T, d))
-    _need("dW_r", dW_r, torch.float32, (E, d))
-    _need_ws(ws)
-    _check(_lib.load().moe_router_dw(_p(dlogits), _p(x), T, d, E, _p(dW_r), _p(ws), ws.numel(),
-                                     _stream(stream)), "moe_router_dw")
+    dev, f32 = _device(dlogits), torch.float32
+    wp, wn = _ws(ws, dev)
+    _check(_lib.load().moe_router_dw(_ptr("dlogits", dlogits, f32, (T, E), dev),
+                                     _ptr("x", x, torch.bfloat16, (T, d), dev), T, d, E,
+                                     _ptr("dW_r", dW_r, f32, (E, d), dev), wp, wn,
+                                     _stream_of(stream, dev)), "moe_router_dw")
 
 
 def moe_select_experts(logits, b, k, mode, n_group, topk_group, group_rule, renorm, scale,
@@ -460,16 +477,15 @@ def moe_select_experts(logits, b, k, mode, n_group, topk_group, group_rule, reno
     """The k experts of every token from its logits, within the topk_group best of n_group groups;
     b: selection bias [E] or None; lse (softmax mode): the logits' logsumexp, or None."""
     T, E = shape = _rows("logits", logits)
-    _need("logits", logits, torch.float32, shape)
-    _need("b", b, torch.float32, (E,), optional=True)
-    _need("topk_idx", topk_idx, torch.int32, (T, k))
-    _need("topk_gate", topk_gate, torch.float32, (T, k))
-    _need("topk_score", topk_score, torch.float32, (T, k))
-    _need("lse", lse, torch.float32, (T,), optional=True)
-    _check(_lib.load().moe_select_experts(_p(logits), _p(b), T, E, k, mode, n_group, topk_group,
-                                          group_rule, int(bool(renorm)), float(scale),
-                                          _p(topk_idx), _p(topk_gate), _p(topk_score), _p(lse),
-                                          _stream(stream)), "moe_select_experts")
+    dev, f32, out = _device(logits), torch.float32, (T, k)
+    _check(_lib.load().moe_select_experts(_ptr("logits", logits, f32, shape, dev),
+                                          _opt("b", b, f32, (E,), dev), T, E, k, mode, n_group,
+                                          topk_group, group_rule, 1 if renorm else 0, scale,
+                                          _ptr("topk_idx", topk_idx, torch.int32, out, dev),
+                                          _ptr("topk_gate", topk_gate, f32, out, dev),
+                                          _ptr("topk_score", topk_score, f32, out, dev),
+                                          _opt("lse", lse, f32, (T,), dev),
+                                          _stream_of(stream, dev)), "moe_select_experts")
 
 
 def moe_select_experts_bwd(dg, topk_idx, topk_score, logits, lse, mode, renorm, scale, dlogits,
@@ -478,61 +494,52 @@ def moe_select_experts_bwd(dg, topk_idx, topk_score, logits, lse, mode, renorm, 
     gates, or with a z_coef."""
     T, E = shape = _rows("dlogits", dlogits)
     k = _rows("topk_idx", topk_idx)[1]
-    _need("dlogits", dlogits, torch.float32, shape)
-    _need("dg", dg, torch.float32, (T, k))
-    _need("topk_idx", topk_idx, torch.int32, (T, k))
-    _need("topk_score", topk_score, torch.float32, (T, k))
-    _need("logits", logits, torch.float32, shape, optional=True)
-    _need("lse", lse, torch.float32, (T,), optional=True)
-    _need("dlogits_extra", dlogits_extra, torch.float32, shape, optional=True)
-    _check(_lib.load().moe_select_experts_bwd(_p(dg), _p(topk_idx), _p(topk_score), _p(logits),
-                                              _p(lse), _p(dlogits_extra), T, E, k, mode,
-                                              int(bool(renorm)), float(scale), float(z_coef),
-                                              _p(dlogits), _stream(stream)),
-           "moe_select_experts_bwd")
+    dev, f32, out = _device(dlogits), torch.float32, (T, k)
+    _check(_lib.load().moe_select_experts_bwd(_ptr("dg", dg, f32, out, dev),
+                                              _ptr("topk_idx", topk_idx, torch.int32, out, dev),
+                                              _ptr("topk_score", topk_score, f32, out, dev),
+                                              _opt("logits", logits, f32, shape, dev),
+                                              _opt("lse", lse, f32, (T,), dev),
+                                              _opt("dlogits_extra", dlogits_extra, f32, shape, dev),
+                                              T, E, k, mode, 1 if renorm else 0, scale, z_coef,
+                                              _ptr("dlogits", dlogits, f32, shape, dev),
+                                              _stream_of(stream, dev)), "moe_select_experts_bwd")
 
 
-def _grad_list(name, ts):
+def _grad_list(name, ts, dev):
     """Host arrays of a list of gradients: pointers, element counts, types."""
     n = len(ts)
-    ptr, numel, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int * n)()
-    dev = torch.cuda.current_device() if ts and ts[0].is_cuda else None
+    ptr, numel, types = [0] * n, [0] * n, [0] * n
     for i, t in enumerate(ts):
         rt = _TYPES.get(t.dtype)
         if rt is None:
             raise MoEError(f"{name}[{i}] must be bf16 or fp32, got {t.dtype}")
-        if not t.is_contiguous():
-            raise MoEError("tensors passed to the MoE library must be contiguous")
-        if not t.is_cuda or t.device.index != dev:
-            _on_device(f"{name}[{i}]", t)
-        ptr[i], numel[i], types[i] = t.data_ptr(), t.numel(), rt
-    return ptr, numel, types
+        ptr[i], numel[i], types[i] = _ptr(f"{name}[{i}]", t, t.dtype, t.shape, dev), t.numel(), rt
+    return (ctypes.c_void_p * n)(*ptr), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types)
 
 
 def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
     """norm[0] = the global 2-norm of a list of bf16 or fp32 gradients, norm[1] = the factor that
     clips it to max_norm."""
-    ptr, numel, types = _grad_list("grads", grads)
-    _need("norm", norm, torch.float32, (2,))
-    _need_ws(ws)
-    _check(_lib.load().moe_grad_norm(ptr, numel, types, len(grads), float(max_norm), _p(norm),
-                                     _p(ws), ws.numel(), _stream(stream)), "moe_grad_norm")
+    dev = _device(norm)
+    ptr, numel, types = _grad_list("grads", grads, dev)
+    wp, wn = _ws(ws, dev)
+    _check(_lib.load().moe_grad_norm(ptr, numel, types, len(grads), max_norm,
+                                     _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
+                                     _stream_of(stream, dev)), "moe_grad_norm")
 
 
 def moe_clip_grads(grads, max_norm, out, norm, ws, stream=None):
     """moe_grad_norm, and out[i] = norm[1] * grads[i]; out None clips in place."""
-    ptr, numel, types = _grad_list("grads", grads)
+    dev = _device(norm)
+    ptr, numel, types = _grad_list("grads", grads, dev)
     optr = ptr
     if out is not None:
         if len(out) != len(grads):
             raise MoEError(f"{len(grads)} gradients, but {len(out)} outputs")
-        for i, (t, o) in enumerate(zip(grads, out)):
-            if o.shape != t.shape or o.dtype is not t.dtype:
-                raise MoEError(f"out[{i}] must be like grads[{i}], {tuple(t.shape)} {t.dtype}, "
-                               f"got {tuple(o.shape)} {o.dtype}")
-        optr = _grad_list("out", out)[0]
-    _need("norm", norm, torch.float32, (2,))
-    _need_ws(ws)
-    _check(_lib.load().moe_clip_grads(ptr, optr, numel, types, len(grads), float(max_norm),
-                                      _p(norm), _p(ws), ws.numel(), _stream(stream)),
-           "moe_clip_grads")
+        optr = (ctypes.c_void_p * len(out))(*[_ptr(f"out[{i}]", o, t.dtype, t.shape, dev)
+                                              for i, (t, o) in enumerate(zip(grads, out))])
+    wp, wn = _ws(ws, dev)
+    _check(_lib.load().moe_clip_grads(ptr, optr, numel, types, len(grads), max_norm,
+                                      _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
+                                      _stream_of(stream, dev)), "moe_clip_grads")
