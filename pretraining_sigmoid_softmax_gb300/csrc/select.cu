@@ -561,7 +561,10 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_kernel(const SelectPara
 // scale dg_i. Sigmoid: dl = ds_i s_i (1 - s_i) on the chosen experts. Softmax: dl_e = p_e
 // (ds_e - sum_i s_i ds_i), ds_e zero off the chosen experts; with renormalised gates that sum
 // is zero, so only the chosen experts have a gradient. z-loss: + (2 z_coef / T) lse p_e.
-// One warp per token, lane i < k holding slot i.
+//
+// Bound by writing dlogits. L lanes hold a token's slots (L >= k), so a warp forms the gradients of
+// 32 / L tokens at once; it scatters them into zeroed rows in shared memory and stores the rows
+// whole, since the tokens' rows are one piece of memory.
 struct SelectBwdParams {
     const float* dg;
     const int32_t* idx;
@@ -576,55 +579,87 @@ struct SelectBwdParams {
     int* status;
 };
 
+template <int L>
 __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const SelectBwdParams P) {
-    const int lane = threadIdx.x % 32;
-    const int64_t t = (int64_t)blockIdx.x * kSelWarps + threadIdx.x / 32;
-    if (t >= P.T) return;  // whole warp
+    constexpr int NT = 32 / L;
+    extern __shared__ __align__(16) float rows[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, k = P.k;
+    // one warp's rows; a multiple of 16 bytes
+    float* row = rows + (size_t)warp * ((NT * E + 3) / 4 * 4);
+    const int64_t t0 = ((int64_t)blockIdx.x * kSelWarps + warp) * NT;
+    if (t0 >= P.T) return;  // whole warp
+    const int64_t t = t0 + lane / L;
+    const int n = (int)min((int64_t)NT, P.T - t0) * E;  // elements of the warp's tokens
     const bool softmax = P.mode == MOE_MODE_SOFTMAX;
-    int my_e = -1;
+    const bool dense = softmax && (!P.renorm || P.z_scale != 0.f);
+    for (int i = 4 * lane; i < n; i += 128)
+        *reinterpret_cast<float4*>(row + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    int e = -1;
     float s = 0.f, dg = 0.f;
-    if (lane < k) {
-        my_e = P.idx[t * k + lane];
-        if (my_e < 0 || my_e >= E) {  // the slot is dropped
+    if (t < P.T && sub < k) {
+        e = P.idx[t * k + sub];
+        if (e < 0 || e >= E) {  // the slot is dropped
             record_error(P.status, MOE_ERR_BAD_INDEX, kSiteSelectBwd);
-            my_e = -1;
+            e = -1;
         } else {
-            s = P.score[t * k + lane];
-            dg = P.dg[t * k + lane];
+            s = P.score[t * k + sub];
+            dg = P.dg[t * k + sub];
         }
     }
     float ds = P.scale * dg;
     if (P.renorm) {
-        const float S = seg_sum<32>(s);
-        const float m = seg_sum<32>(s / S * dg);
+        const float S = seg_sum<L>(s);
+        const float m = seg_sum<L>(s / S * dg);
         ds = S == 0.f ? 0.f : P.scale / S * (dg - m);
     }
-    const bool dense = softmax && (!P.renorm || P.z_scale != 0.f);
-    float c = 0.f, l_se = 0.f;
-    if (softmax && !P.renorm) c = seg_sum<32>(s * ds);
-    if (dense) l_se = P.lse[t];
-    const float v = dense ? ds : softmax ? ds * s : ds * s * (1.f - s);
-    for (int e0 = 0; e0 < E; e0 += 32) {  // warp-uniform trip count
-        const int e = e0 + lane;
-        float up = 0.f;
-        for (int i = 0; i < k; ++i) {  // an expert named twice gets both slots' terms
-            const int ei = __shfl_sync(kFull, my_e, i);
-            const float vi = __shfl_sync(kFull, v, i);
-            if (ei == e) up += vi;
+    float c = 0.f;
+    if (softmax && !P.renorm) c = seg_sum<L>(s * ds);
+    float v = dense ? ds : softmax ? ds * s : ds * s * (1.f - s);
+    // an expert named twice in a token gets its slots' terms summed in slot order, by the first
+    const uint32_t same = __match_any_sync(kFull, e < 0 ? -1 - lane : lane / L * E + e);
+    if (__any_sync(kFull, (same & (same - 1)) != 0)) {
+        float sum = 0.f;
+        for (int i = 0; i < 32; ++i) {
+            const float o = __shfl_sync(kFull, v, i);
+            if ((same >> i) & 1u) sum += o;
         }
-        if (e >= E) continue;
-        if (dense) {
-            if (l_se == -INFINITY) {  // no expert has a score
-                up = 0.f;
-            } else {
-                const float p = expf(P.logits[t * E + e] - l_se);
-                up = p * (up - c) + P.z_scale * l_se * p;
+        v = sum;
+        if ((same & ((1u << lane) - 1u)) != 0) e = -1;
+    }
+    __syncwarp();
+    if (e >= 0) row[lane / L * E + e] = v;
+    __syncwarp();
+    float* out = P.dlogits + t0 * E;
+    const float* extra = P.extra ? P.extra + t0 * E : nullptr;
+    if (dense) {
+        const float* l = P.logits + t0 * E;
+        for (int q = 0; q * E < n; ++q) {
+            const float l_se = P.lse[t0 + q];
+            const float cq = __shfl_sync(kFull, c, q * L);
+            const float zl = P.z_scale * l_se;
+            for (int i = q * E + lane; i < (q + 1) * E; i += 32) {
+                float g = 0.f;
+                if (l_se != -INFINITY) {  // else no expert has a score
+                    const float p = expf(l[i] - l_se);
+                    g = p * (row[i] - cq) + zl * p;
+                }
+                out[i] = extra ? g + extra[i] : g;
             }
         }
-        if (P.extra) up += P.extra[t * E + e];
-        P.dlogits[t * E + e] = up;
+        return;
     }
+    const bool vec = ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(extra)) & 15u) == 0;
+    const int nv = vec ? n / 4 * 4 : 0;
+    for (int i = 4 * lane; i < nv; i += 128) {
+        float4 g = *reinterpret_cast<const float4*>(row + i);
+        if (extra) {
+            const float4 x = *reinterpret_cast<const float4*>(extra + i);
+            g.x += x.x, g.y += x.y, g.z += x.z, g.w += x.w;
+        }
+        *reinterpret_cast<float4*>(out + i) = g;
+    }
+    for (int i = nv + lane; i < n; i += 32) out[i] = extra ? row[i] + extra[i] : row[i];
 }
 
 template <int L>
@@ -663,6 +698,14 @@ int launch_select(const SelectParams& P, cudaStream_t st) {
     Y.vr = (int)cdiv(per, Y.lpg);
     Y.vec = (Y.vr == 8 || Y.vr == 4) && per % Y.vr == 0 && aligned16(P.logits);
     return L == 8 ? launch_lanes<8>(P, Y, st) : L == 16 ? launch_lanes<16>(P, Y, st) : launch_lanes<32>(P, Y, st);
+}
+
+template <int L>
+int launch_bwd_lanes(const SelectBwdParams& P, cudaStream_t st) {
+    constexpr int NT = 32 / L;
+    const size_t smem = sizeof(float) * kSelWarps * ((NT * P.E + 3) / 4 * 4);  // 32 KB at most
+    select_bwd_kernel<L><<<(unsigned)cdiv(P.T, (int64_t)kSelWarps * NT), kSelWarps * 32, smem, st>>>(P);
+    return launch_status();
 }
 
 }  // namespace
@@ -706,6 +749,6 @@ extern "C" int moe_select_experts_bwd(const float* dg, const int32_t* topk_idx,
     if (!status) return MOE_ERR_LAUNCH;
     const SelectBwdParams P{dg, topk_idx, topk_score, logits, lse, dlogits_extra, T, E, k, mode,
                             renorm ? 1 : 0, scale, 2.0f * z_coef / (float)T, dlogits, status};
-    select_bwd_kernel<<<(unsigned)cdiv(T, kSelWarps), kSelWarps * 32, 0, (cudaStream_t)stream>>>(P);
-    return launch_status();
+    cudaStream_t st = (cudaStream_t)stream;
+    return k <= 8 ? launch_bwd_lanes<8>(P, st) : k <= 16 ? launch_bwd_lanes<16>(P, st) : launch_bwd_lanes<32>(P, st);
 }
