@@ -12,8 +12,6 @@
 #include <limits.h>
 #include <math.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "sizes.h"
 
@@ -57,17 +55,23 @@ __device__ __forceinline__ F seg_sum(F v) {
 }
 template <int L>
 __device__ __forceinline__ int seg_max(int v) {
-    if constexpr (L == 32) return __reduce_max_sync(kFull, v);
+    if constexpr (L == 32) {
+        return __reduce_max_sync(kFull, v);
+    } else {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
-    return v;
+        for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+        return v;
+    }
 }
 template <int L>
 __device__ __forceinline__ int seg_min(int v) {
-    if constexpr (L == 32) return __reduce_min_sync(kFull, v);
+    if constexpr (L == 32) {
+        return __reduce_min_sync(kFull, v);
+    } else {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kFull, v, o));
-    return v;
+        for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kFull, v, o));
+        return v;
+    }
 }
 
 // Softmax statistics of a row: its largest logit (NaN set aside) and the sum of e^(l - max). A
@@ -92,18 +96,15 @@ __device__ __forceinline__ void row_softmax(const float* row, int E, int lane, f
 constexpr float kSmallSum = 9.5367432e-7f;  // 2^-20
 
 // Scores and gates of the chosen experts, stored with the indices: lane `sub` < k of the L lanes
-// of a token holds slot `sub`'s expert. `live` masks tokens that are not there, or whose choice
+// of a token holds slot `sub`'s expert and that expert's logit. `live` masks tokens that are not there, or whose choice
 // is made elsewhere. A token whose chosen scores are all zero (in 64 bits) has gates of zero.
 // Executed by the whole warp.
 template <int L>
 __device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int sub, bool live, int my_e,
-                                       float mx, float sum) {
+                                       float l, float mx, float sum) {
     const bool on = live && sub < P.k, sigmoid = P.mode == MOE_MODE_SIGMOID;
-    float l = 0.f, s = 0.f;
-    if (on) {
-        l = P.logits[t * P.E + my_e];
-        s = sigmoid ? stable_sigmoid(l) : sum == 0.f ? 0.f : expf(l - mx) / sum;
-    }
+    float s = 0.f;
+    if (on) s = sigmoid ? stable_sigmoid(l) : sum == 0.f ? 0.f : expf(l - mx) / sum;
     float g = s;
     if (P.renorm) {
         const float S = seg_sum<L>(s);
@@ -258,226 +259,406 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
     float mx = 0.f, sum = 1.f;
     if (P.mode == MOE_MODE_SOFTMAX) row_softmax(P.logits + t * P.E, P.E, lane, mx, sum);
     const int my_e = select_exact(P, t, lane, mx);
-    finish<32>(P, t, lane, true, my_e, mx, sum);
-}
-
-// Every token in 64 bits, one warp each: groupings that the lanes of select_kernel do not hold.
-__global__ void __launch_bounds__(kSelWarps * 32) select_exact_kernel(const SelectParams P) {
-    const int64_t t = (int64_t)blockIdx.x * kSelWarps + threadIdx.x / 32;
-    if (t < P.T) select_token(P, t, threadIdx.x % 32);  // whole warps
+    finish<32>(P, t, lane, true, my_e, lane < P.k ? P.logits[t * P.E + my_e] : 0.f, mx, sum);
 }
 
 // ------------------------------------------------------------------- the choice from 32 bits
-// L lanes per token (32 / L tokens per warp), each holding up to V consecutive experts of one
-// group; lpg lanes (a power of two) hold a group, vr experts each. Every expert becomes one
-// integer key, its selection value above its index in the low 8 bits: a lane sorts its keys with
-// minima and maxima alone, groups are compared by their lanes' first keys, and each of the k
-// rounds takes the largest of the lanes' first keys, which names its expert itself.
+// L lanes per token (32 / L tokens per warp), each holding up to 8 NB consecutive experts of one
+// group; lpg lanes (a power of two) hold a group, vr experts each. A warp copies its next tokens'
+// logits to shared memory while it works on the present ones. Every expert becomes one integer
+// key, its selection value above its place in the lane (the low bits): a lane keeps its eight
+// best keys, sorted by minima and maxima alone, groups are compared by their lanes' first keys,
+// and each of the k rounds takes the largest of the lanes' first keys.
 //
 // The keys are rounded values. Where two of them that the choice has to tell apart lie within
-// the rounding's bound, the token is chosen again: the experts that may be among the k are
-// evaluated in 64 bits (select_close), or all of them (select_token) where a group's choice is
-// in doubt. About one token in 500 takes that way on Gaussian logits.
+// the rounding's bound, the token is chosen again by select_close: groups and experts near the
+// border are evaluated in 64 bits and ranked. Rows that are not for this arithmetic (NaN,
+// infinities, more than 32 experts near the border) are chosen in 64 bits throughout.
 //
-// With a bias the value is s + b in fixed point, 2^-shift units, s by the fast exponential and
-// reciprocal; without one it is the logit, whose upper 24 bits order it.
+// With a bias the value is s + (b - base), clamped at 0 from below, base the smallest bias within
+// 16 of the largest, s by the fast exponential and reciprocal; a non-negative float orders as its
+// bits do. Without a bias it is the logit, as an order-preserving integer.
 struct SelectLayout {
     int lpg, vr;
-    int vec;  // a lane's experts are aligned 16-byte vectors (or none)
+    int vec;   // rows are 16-byte aligned, and a lane's experts whole 16-byte vectors
+    int pitch; // floats per row in shared memory
 };
 
-constexpr float kKeyLimit = 2147483392.f;
 constexpr float kU = 5.9604645e-8f;  // 2^-24
-// Bounds of the fast scores' errors. Sigmoid: 1 / (1 + e^-l): the quotient is within 2 ulp (4 u
+// Bounds of the fast scores' errors. Sigmoid: 1 / (1 + e^-l): the reciprocal is within 1 ulp (2 u
 // relative), the sum within u, and the exponential's relative error (1.5 |l| u + 4 u) enters
-// times s (1 - s): below 6.4 u in all. Softmax: e^(l - max) / sum: (1.5 |l - max| + 4) u, at
-// most 20 u for the sum, its reciprocal and the product; p |l - max| <= 0.37: 25 u p + 0.6 u.
+// times s (1 - s): below 5 u in all; 6.4 u leaves room. Softmax: e^(l - max) / sum:
+// (1.5 |l - max| + 4) u, at most 20 u for the sum, its reciprocal and the product; p |l - max| <=
+// 0.37: 25 u p + 0.6 u.
 constexpr float kSigmoidErr = 6.4f * kU;
 constexpr float kSoftmaxErr = 25.f * kU;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// Score of one expert from its logit (within the bounds above); inv = 1 / sum for softmax.
+__device__ __forceinline__ float fast_score(bool sigmoid, float l, float mx, float inv) {
+    return sigmoid ? fast_rcp(1.0f + fast_exp2(-kLog2e * l)) : fast_exp2(kLog2e * (l - mx)) * inv;
+}
 
 __device__ __forceinline__ int logit_key(float l) {
     const int b = __float_as_int((l == l ? l : -INFINITY) + 0.0f);
     return b ^ ((b >> 31) & 0x7fffffff);
 }
-// NaN goes to the lower limit.
-__device__ __forceinline__ int value_key(float v, float unit) {
-    return __float2int_rn(fminf(fmaxf(v * unit, -kKeyLimit), kKeyLimit));
+
+// How far below v another value has to lie to come after it for certain, where both are rounded
+// sums s + (b - base): twice the score's error and both sums' roundings (u each, twice), and what
+// dropping `bits` low bits takes off a key (2^bits ulp, of at most 2 u v each).
+__device__ __forceinline__ float value_gap(float v, float es, int bits) {
+    return 2.f * es + (4.2f + (float)(2 << bits)) * kU * v;
+}
+__device__ __forceinline__ float score_err(bool sigmoid, float inv) {
+    return sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
 }
 
-template <int V>
-__device__ __forceinline__ void sort_desc(int (&k)[V]) {
-    auto ce = [&](int a, int b) {
-        const int hi = max(k[a], k[b]);
-        k[b] = min(k[a], k[b]);
-        k[a] = hi;
-    };
-    if constexpr (V == 2) ce(0, 1);
-    if constexpr (V == 4) { ce(0, 1); ce(2, 3); ce(0, 2); ce(1, 3); ce(1, 2); }
-    if constexpr (V == 8) {
-        ce(0, 1); ce(2, 3); ce(4, 5); ce(6, 7);
-        ce(0, 2); ce(1, 3); ce(4, 6); ce(5, 7);
-        ce(1, 2); ce(5, 6);
-        ce(0, 4); ce(1, 5); ce(2, 6); ce(3, 7);
-        ce(2, 4); ce(3, 5);
-        ce(1, 2); ce(3, 4); ce(5, 6);
-    }
+// The smallest bias within 16 of the largest finite one (0 where none is finite). By one warp.
+__device__ __forceinline__ float bias_base(const float* b, int E, int lane) {
+    float hi = -INFINITY;
+    for (int e = lane; e < E; e += 32)
+        if (isfinite(b[e])) hi = fmaxf(hi, b[e]);
+    hi = seg_max<32>(hi);
+    float lo = INFINITY;
+    for (int e = lane; e < E; e += 32)
+        if (b[e] >= hi - 16.f && b[e] <= hi) lo = fminf(lo, b[e]);
+    lo = -seg_max<32>(-lo);
+    return isfinite(lo) ? lo : 0.f;
 }
 
-// Units of the fixed-point keys for biases of up to `maxb`: |s + b| < 2^(31 - shift).
-__device__ __forceinline__ int key_shift(float maxb) {
-    return maxb < 1.f ? 30 : maxb < 3.f ? 29 : maxb < 7.f ? 28 : 27;
-}
-
-// Score of one expert from its logit, fast (within the bounds above).
-__device__ __forceinline__ float fast_score(bool sigmoid, float l, float mx, float inv) {
-    return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __expf(l - mx) * inv;
-}
-
-// One token's choice where its groups are settled (`open`: bit g, group g stays) and the experts
-// that may be chosen are those whose key is at least `least`: they are gathered, one per lane,
-// evaluated in 64 bits and ranked. More than 32 of them: the token is left to select_token
-// (returns false). The keys are formed exactly as select_kernel forms them. Sigmoid scores, or
-// logits.
+// One token whose keys left its choice open, by a whole warp. Groups: lane g finds group g's
+// largest values, evaluates in 64 bits those that may be its two largest, and the groups are
+// ranked. Experts: without a bias the logits' own order; else those that may be among the k
+// largest of the open groups are gathered, one per lane, evaluated in 64 bits and ranked. False
+// where that does not settle it (more than three candidates for a group's two, or more than 32
+// for the k; NaN, or softmax over infinities): the token is then left to select_token.
 template <bool LOGIT>
-__device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, uint32_t open,
-                                          int least, float unit, int* scratch) {
+__device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, float base,
+                                          int* scratch) {
+    constexpr int VJ = kMaxExperts / 32;
     const float* row = P.logits + t * P.E;
-    const int per = P.E / P.n_group;
-    int n = 0;
-    for (int e0 = 0; e0 < P.E; e0 += 32) {
-        const int e = e0 + lane;
-        bool in = false;
-        if (e < P.E && ((open >> (e / per)) & 1u)) {
-            const float l = row[e];
-            const int key = LOGIT ? logit_key(l) : value_key(fast_score(true, l, 0.f, 1.f) + P.b[e], unit);
-            in = ((key & ~255) | e) >= least;
+    const int E = P.E, G = P.n_group, per = E / G, k = P.k;
+    const bool sigmoid = P.mode == MOE_MODE_SIGMOID, top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
+    float mx = 0.f, sum = 1.f, inv = 1.f;
+    double total = 1.0;
+    if (!sigmoid) {
+        row_softmax(row, E, lane, mx, sum);
+        inv = fast_rcp(sum);
+        if (!LOGIT) {
+            total = 0.0;
+            for (int e = lane; e < E; e += 32) total += exp((double)row[e] - (double)mx);
+            total = seg_sum<32>(total);
         }
-        const uint32_t m = __ballot_sync(kFull, in);
-        const int at = n + __popc(m & ((1u << lane) - 1u));
-        if (in && at < 32) scratch[at] = e;
-        n += __popc(m);
     }
-    if (n > 32) return false;
-    __syncwarp();
-    int e = INT_MAX;
-    double v = 0.0;
-    if (lane < n) {
-        e = scratch[lane];
+    bool bad = !(sum < 1e30f) || mx == -INFINITY;
+    for (int e = lane; e < E; e += 32) bad |= row[e] != row[e];
+    if (__any_sync(kFull, bad)) return false;
+    const float es = score_err(sigmoid, inv);
+    auto value = [&](int e) { return fmaxf(fast_score(sigmoid, row[e], mx, inv) + (P.b[e] - base), 0.f); };
+    auto score64 = [&](int e) {
         const double l = row[e];
-        v = no_nan(LOGIT ? l : 1.0 / (1.0 + exp(-l)) + (double)P.b[e]);
+        return sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)mx) / total;
+    };
+    auto value64 = [&](int e) { return no_nan(score64(e) + (double)P.b[e]); };
+
+    uint32_t open = 1u;
+    if (G > 1) {
+        double gs = -INFINITY;
+        bool unsettled = false;
+        if (lane < G) {
+            float a = -INFINITY, b = -INFINITY, c = -INFINITY, d = -INFINITY;  // the four largest
+            int ia = -1, ib = -1, ic = -1;
+            for (int e = lane * per; e < (lane + 1) * per; ++e) {
+                const float v = LOGIT ? (row[e] == row[e] ? row[e] : -INFINITY) : value(e);
+                if (v > a || ia < 0) {
+                    d = c, c = b, b = a, a = v;
+                    ic = ib, ib = ia, ia = e;
+                } else if (v > b || ib < 0) {
+                    d = c, c = b, b = v;
+                    ic = ib, ib = e;
+                } else if (v > c || ic < 0) {
+                    d = c, c = v;
+                    ic = e;
+                } else {
+                    d = fmaxf(d, v);
+                }
+            }
+            if (LOGIT) {
+                gs = top2 ? score64(ia) + score64(ib) : (double)a;
+            } else {
+                // the two largest (or the largest) are among the first three unless the fourth
+                // may reach them
+                const float least = top2 ? b : a;
+                unsettled = per > 3 && !(least - d > value_gap(least, es, 0));
+                double x = value64(ia);
+                double y = per > 1 ? value64(ib) : -INFINITY, z = per > 2 ? value64(ic) : -INFINITY;
+                if (y > x) { const double q = x; x = y; y = q; }
+                y = fmax(y, fmin(x, z));
+                x = fmax(x, z);
+                gs = top2 ? no_nan(x + y) : x;
+            }
+        }
+        if (__any_sync(kFull, unsettled)) return false;
+        int rank = 0;
+        for (int h = 0; h < G; ++h) {
+            const double o = __shfl_sync(kFull, gs, h);
+            rank += before(o, h, gs, lane) ? 1 : 0;
+        }
+        open = __ballot_sync(kFull, lane < G && rank < P.topk_group);
     }
-    int rank = 0;
-    for (int i = 0; i < n; ++i) {
-        const double ov = __shfl_sync(kFull, v, i);
-        const int oe = __shfl_sync(kFull, e, i);
-        rank += before(ov, oe, v, e) ? 1 : 0;
+
+    int key[VJ];  // closed groups and places past the last expert: INT_MIN, below every value
+#pragma unroll
+    for (int j = 0; j < VJ; ++j) {
+        const int e = lane + 32 * j;
+        key[j] = INT_MIN;
+        if (e < E && ((open >> (e / per)) & 1u))
+            key[j] = LOGIT ? logit_key(row[e]) : __float_as_int(value(e));
     }
-    __syncwarp();
-    if (lane < n && rank < P.k) scratch[rank] = e;
-    __syncwarp();
-    const int my_e = lane < P.k ? scratch[lane] : 0;
-    __syncwarp();
-    float mx = 0.f, sum = 1.f;
-    if (P.mode == MOE_MODE_SOFTMAX) row_softmax(row, P.E, lane, mx, sum);
-    finish<32>(P, t, lane, true, my_e, mx, sum);
+    uint32_t taken = 0;
+    int my_e = 0, kth = INT_MIN;
+    for (int i = 0; i < k; ++i) {  // the largest key left, of the lowest index
+        int best = INT_MIN, e = INT_MAX;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j)
+            if (!((taken >> j) & 1u) && key[j] > best) {
+                best = key[j];
+                e = lane + 32 * j;
+            }
+        kth = __reduce_max_sync(kFull, best);
+        const int w = __reduce_min_sync(kFull, best == kth ? e : INT_MAX);
+        if ((w & 31) == lane) taken |= 1u << (w >> 5);
+        if (lane == i) my_e = w;
+    }
+    if (!LOGIT) {
+        const float v = __int_as_float(kth), gap = value_gap(v, es, 0);
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) {
+            const bool in = key[j] != INT_MIN && !(v - __int_as_float(key[j]) > gap);
+            const uint32_t m = __ballot_sync(kFull, in);
+            const int at = n + __popc(m & ((1u << lane) - 1u));
+            if (in && at < 32) scratch[at] = lane + 32 * j;
+            n += __popc(m);
+        }
+        if (n > 32) return false;
+        __syncwarp();
+        int e = INT_MAX;
+        double x = 0.0;
+        if (lane < n) {
+            e = scratch[lane];
+            x = value64(e);
+        }
+        int rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const double ox = __shfl_sync(kFull, x, i);
+            const int oe = __shfl_sync(kFull, e, i);
+            rank += before(ox, oe, x, e) ? 1 : 0;
+        }
+        __syncwarp();
+        if (lane < n && rank < k) scratch[rank] = e;
+        __syncwarp();
+        my_e = lane < k ? scratch[lane] : 0;
+        __syncwarp();
+    }
+    finish<32>(P, t, lane, true, my_e, lane < k ? row[my_e] : 0.f, mx, sum);
     return true;
 }
 
-template <int V, int L, bool LOGIT>
-__global__ void __launch_bounds__(kSelWarps * 32) select_kernel(const SelectParams P, const SelectLayout Y) {
+// Sorting network for eight keys, largest first, and the eight largest of two sorted eights.
+__device__ __forceinline__ void swap_desc(int& a, int& b) {
+    const int hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+__device__ __forceinline__ void sort8(int (&k)[8]) {
+#define MOE_CE(i, j) swap_desc(k[i], k[j])
+    MOE_CE(0, 1); MOE_CE(2, 3); MOE_CE(4, 5); MOE_CE(6, 7);
+    MOE_CE(0, 2); MOE_CE(1, 3); MOE_CE(4, 6); MOE_CE(5, 7);
+    MOE_CE(1, 2); MOE_CE(5, 6);
+    MOE_CE(0, 4); MOE_CE(1, 5); MOE_CE(2, 6); MOE_CE(3, 7);
+    MOE_CE(2, 4); MOE_CE(3, 5);
+    MOE_CE(1, 2); MOE_CE(3, 4); MOE_CE(5, 6);
+}
+__device__ __forceinline__ void merge8(int (&k)[8], const int (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = max(k[i], o[7 - i]);  // the eight largest, bitonic
+    MOE_CE(0, 4); MOE_CE(1, 5); MOE_CE(2, 6); MOE_CE(3, 7);
+    MOE_CE(0, 2); MOE_CE(1, 3); MOE_CE(4, 6); MOE_CE(5, 7);
+    MOE_CE(0, 1); MOE_CE(2, 3); MOE_CE(4, 5); MOE_CE(6, 7);
+#undef MOE_CE
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <int L, int NB, bool LOGIT>
+__global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectParams P, const SelectLayout Y) {
     constexpr int NT = 32 / L;
+    constexpr int BITS = NB == 1 ? 3 : NB == 2 ? 4 : 5;  // of a place in the lane
+    constexpr int PLACE = (1 << BITS) - 1;
+    extern __shared__ __align__(16) float smem[];  // biases, then two buffers of rows per warp
     __shared__ int scratch[kSelWarps][32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
-    const int per = P.E / P.n_group, G = P.n_group;
+    const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID;
     const bool top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
     const int g = sub / Y.lpg, r = sub % Y.lpg;
-    const int first = g * per + r * Y.vr;
-    int count = g < G ? min(Y.vr, per - r * Y.vr) : 0;
-    if (count < 0) count = 0;
+    const int count = g < G ? max(0, min(Y.vr, per - r * Y.vr)) : 0;
+    const int first = count > 0 ? g * per + r * Y.vr : 0;  // idle lanes read the row's start
+    float* const bias = smem;  // b - base
+    float* const rows = smem + (LOGIT ? 0 : Y.pitch) + warp * 2 * NT * Y.pitch;
 
-    float bias[V];
-    float unit = 1.f, vmax = 1.f;
-    if constexpr (!LOGIT) {
-        float mb = 0.f;
+    // this warp's tokens: a run of its own, NT at a time
+    const int64_t groups = (P.T + NT - 1) / NT, warps = (int64_t)gridDim.x * kSelWarps;
+    const int64_t w = (int64_t)blockIdx.x * kSelWarps + warp;
+    const int64_t q0 = w * groups / warps, q1 = (w + 1) * groups / warps;
+    auto fetch = [&](int64_t q, int buf) {
+        if (q < q1) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            bias[j] = j < count ? P.b[first + j] : 0.f;
-            if (isfinite(bias[j])) mb = fmaxf(mb, fabsf(bias[j]));
-        }
-        mb = seg_max<L>(mb);
-        const int shift = key_shift(mb);
-        unit = (float)(1u << shift);
-        vmax = (float)(1u << (31 - shift));
-    }
-
-    const int64_t stride = (int64_t)gridDim.x * kSelWarps * NT;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kSelWarps + warp) * NT; t0 < P.T; t0 += stride) {
-        const int64_t t = t0 + lane / L;
-        const bool live = t < P.T;
-        float l[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) l[j] = 0.f;
-        if (live) {
-            const float* src = P.logits + t * P.E + first;
-            if (V >= 4 && Y.vec) {
-                if (count == V) {
-#pragma unroll
-                    for (int j = 0; j + 3 < V; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4*>(src + j);
-                        l[j] = a.x, l[(j + 1) % V] = a.y, l[(j + 2) % V] = a.z, l[(j + 3) % V] = a.w;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (j < count) l[j] = src[j];
+            for (int i = 0; i < NT; ++i) {
+                const int64_t t = q * NT + i;
+                if (t >= P.T) continue;
+                const float* src = P.logits + t * E;
+                float* dst = rows + (buf * NT + i) * Y.pitch;
+                if (Y.vec)
+                    for (int c = 4 * lane; c < E; c += 128) cp_async<16>(dst + c, src + c);
+                else
+                    for (int c = lane; c < E; c += 32) cp_async<4>(dst + c, src + c);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(q0, 0);
+    float base = 0.f;
+    if constexpr (!LOGIT) {
+        base = bias_base(P.b, E, lane);
+        for (int e = threadIdx.x; e < E; e += kSelWarps * 32) bias[e] = P.b[e] - base;
+        __syncthreads();
+    }
+    // lanes of equal banks start at different vectors of their own (the order is free)
+    const int nvec = Y.vr / 4;
+    const int turn = Y.vec ? (sub * Y.vr / 32) % nvec : 0;
+    const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
+
+    for (int64_t q = q0; q < q1; ++q) {
+        const int buf = (int)(q - q0) & 1;
+        fetch(q + 1, buf ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const int64_t t = q * NT + lane / L;
+        const bool live = t < P.T;
+        const float* row = rows + (buf * NT + lane / L) * Y.pitch + first;
+        // four of the lane's logits, from place `at` on (a multiple of 4), as far as there are
+        auto load4 = [&](int c, int& at, float (&v)[4]) {
+            at = 4 * c;
+            if (Y.vec) {
+                int o = c + turn;
+                if (o >= nvec) o -= nvec;
+                at = 4 * o;
+                const float4 u = *reinterpret_cast<const float4*>(row + at);
+                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = at + j < count ? row[at + j] : 0.f;
+            }
+        };
+        const int nload = (Y.vr + 3) / 4;
         bool odd = false;  // not a row for this kernel's arithmetic
         float mx = 0.f, sum = 1.f, inv = 1.f;
         if (!sigmoid) {
             mx = -INFINITY;
+            for (int c = 0; c < nload; ++c) {
+                int at;
+                float v[4];
+                load4(c, at, v);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j < count) mx = fmaxf(mx, l[j]);
+                for (int j = 0; j < 4; ++j)
+                    if (at + j < count) mx = fmaxf(mx, v[j]);
+            }
             mx = seg_max<L>(mx);
             sum = 0.f;
+            for (int c = 0; c < nload; ++c) {
+                int at;
+                float v[4];
+                load4(c, at, v);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j < count) sum += __expf(l[j] - mx);
+                for (int j = 0; j < 4; ++j)
+                    if (at + j < count) sum += fast_exp2(kLog2e * (v[j] - mx));
+            }
             sum = seg_sum<L>(sum);
             odd = !(sum < 1e30f) || mx == -INFINITY;  // NaN or infinite logits
-            inv = __fdividef(1.0f, sum);
+            inv = fast_rcp(sum);
         }
-        int key[V];
+        const float es = score_err(sigmoid, inv);
+        int key[8];
+        float fa = -INFINITY, fb = -INFINITY;  // a lane's two largest logits
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int k = LOGIT ? logit_key(l[j]) : value_key(fast_score(sigmoid, l[j], mx, inv) + bias[j], unit);
-            key[j] = j < count ? (k & ~255) | (first + j) : INT_MIN;
-        }
-        // how far apart two keys have to be to settle their order: twice the value's error (the
-        // score's, the sum's rounding and the fixed point's), and the index bits
-        int tol = 0;
-        if constexpr (!LOGIT) {
-            const float es = sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
-            tol = 260 + (int)ceilf(2.f * (es + kU * vmax) * unit);
-        }
-        uint32_t open = 1u;
-        int gs = 0;
-        float fa = -INFINITY, fb = -INFINITY;
-        if (LOGIT && top2 && G > 1) {  // a lane's two largest logits
+        for (int blk = 0; blk < NB; ++blk) {
+            if (blk > 0 && 8 * blk >= Y.vr) break;
+            int kb[8];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float x = j < count && l[j] == l[j] ? l[j] : -INFINITY;
-                fb = fmaxf(fb, fminf(fa, x));
-                fa = fmaxf(fa, x);
-                odd |= j < count && l[j] != l[j];  // a NaN's score counts as -inf in the sum
+            for (int h = 0; h < 2; ++h) {
+                int at;
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kb[4 * h + j] = INT_MIN;
+                if (8 * blk + 4 * h >= Y.vr) continue;
+                load4(2 * blk + h, at, v);
+                float bv[4] = {0.f, 0.f, 0.f, 0.f};
+                if (!LOGIT) {
+                    if (Y.vec) {
+                        const float4 u = *reinterpret_cast<const float4*>(bias + first + at);
+                        bv[0] = u.x, bv[1] = u.y, bv[2] = u.z, bv[3] = u.w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (at + j < count) bv[j] = bias[first + at + j];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    int x;
+                    if (LOGIT) {
+                        x = logit_key(v[j]);
+                        if (top2 && G > 1 && at + j < count) {
+                            odd |= v[j] != v[j];  // a NaN's score counts as -inf in the sum
+                            fb = fmaxf(fb, fminf(fa, v[j]));
+                            fa = fmaxf(fa, v[j]);
+                        }
+                    } else {
+                        x = __float_as_int(fmaxf(fast_score(sigmoid, v[j], mx, inv) + bv[j], 0.f));
+                    }
+                    if (at + j < count) kb[4 * h + j] = (x & ~PLACE) | (at + j);
+                }
+            }
+            sort8(kb);
+            if (blk == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) key[j] = kb[j];
+            } else {
+                merge8(key, kb);
             }
         }
-        sort_desc<V>(key);
         if (G > 1) {
-            int a = key[0], b = V > 1 ? key[1 % V] : INT_MIN;
+            int a = key[0], b = key[1];
             for (int o = 1; o < Y.lpg; o <<= 1) {
                 if (LOGIT && top2) {
                     const float oa = __shfl_xor_sync(kFull, fa, o), ob = __shfl_xor_sync(kFull, fb, o);
@@ -489,11 +670,12 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_kernel(const SelectPara
                     a = max(a, oa);
                 }
             }
-            if (!top2) gs = a;
-            else if (!LOGIT) gs = (a >> 1) + (b >> 1);
-            else gs = __float_as_int(fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv));
-            // a sum with a value beyond the keys' range, or a second value that does not count
-            if (!LOGIT && top2 && g < G) odd |= b <= -(int)kKeyLimit + 512 || a >= (int)kKeyLimit - 512;
+            // a sum that counts a value clamped at 0
+            if (!LOGIT && top2 && g < G) odd |= b <= PLACE;
+            int gs = a;  // a score's order as an integer
+            if (top2)
+                gs = __float_as_int(LOGIT ? fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv)
+                                          : __int_as_float(a) + __int_as_float(b));
             int rank = 0;
             for (int h = 0; h < G; ++h) {
                 const int x = __shfl_sync(kFull, gs, h * Y.lpg, L);
@@ -503,56 +685,62 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_kernel(const SelectPara
             if (P.topk_group < G) {
                 const int lo = seg_min<L>(kept ? gs : INT_MAX);
                 const int hi = seg_max<L>(!kept && g < G ? gs : INT_MIN);
-                if (LOGIT && top2) {  // sums of scores: softmax terms are within 160 u of themselves
-                    const float x = __int_as_float(lo), y = __int_as_float(hi);  // down to e^-87
-                    odd |= !(x - y > 2.f * (sigmoid ? 2.f * kSigmoidErr + kU * x : 161.f * kU * x)) || x < 1e-30f;
-                } else if (LOGIT) {
-                    odd |= (lo >> 8) == (hi >> 8);
-                } else {
-                    odd |= (uint32_t)lo - (uint32_t)hi <= (uint32_t)tol;
-                }
+                const float x = __int_as_float(lo), y = __int_as_float(hi);
+                bool sure;
+                if (!LOGIT)  // a NaN (of an infinite value) is never sure
+                    sure = x - y > (top2 ? 2.f * es : 0.f) + value_gap(x, es, BITS);
+                else if (!top2)
+                    sure = (lo >> BITS) != (hi >> BITS);
+                else  // sums of scores: softmax terms are within 160 u of themselves down to e^-87
+                    sure = x - y > 2.f * (sigmoid ? 2.f * kSigmoidErr + kU * x : 161.f * kU * x) && x > 1e-30f;
+                odd |= !sure;
             }
-            const uint32_t bits = __ballot_sync(kFull, kept && r == 0);
-            open = 0u;
-            for (int h = 0; h < G; ++h) open |= ((bits >> (lane / L * L + h * Y.lpg)) & 1u) << h;
             if (!kept) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) key[j] = INT_MIN;
+                for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
             }
         }
-        int my_key = 0, prev = 0;
-        bool close = false;
-        for (int i = 0; i <= P.k; ++i) {
-            const int w = seg_max<L>(key[0]);
-            if (i > 0) close |= LOGIT ? (w >> 8) == (prev >> 8) : (uint32_t)prev - (uint32_t)w <= (uint32_t)tol;
-            if (i == 0 && !LOGIT) odd |= w >= (int)kKeyLimit - 512;
-            if (i == P.k) break;
-            prev = w;
-            if (sub == i) my_key = w;
-            if (key[0] == w) {
+        int my_key = INT_MIN, pops = 0, last = INT_MIN;
+        uint32_t my_from = 0;
+        for (int i = 0; i <= k; ++i) {
+            const int top = seg_max<L>(key[0]);
+            last = top;
+            if (i == k) break;
+            const bool mine = key[0] == top;
+            const uint32_t m = __ballot_sync(kFull, mine) & mask;
+            if (sub == i) {
+                my_key = top;
+                my_from = m;
+            }
+            if (mine && (m & ((1u << lane) - 1u)) == 0) {  // the first of equal ones
+                ++pops;
 #pragma unroll
-                for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
-                key[V - 1] = INT_MIN;
+                for (int j = 0; j < 7; ++j) key[j] = key[j + 1];
+                key[7] = INT_MIN;
             }
         }
-        // prev is the k-th key: what is not below it by more than the bound may be chosen
-        const uint32_t flagged = __ballot_sync(kFull, live && (odd || close));
-        const uint32_t oddball = __ballot_sync(kFull, live && odd);
-        const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
-        finish<L>(P, t, sub, live && !(flagged & mask), my_key & 255, mx, sum);
+        const int from = my_from ? __ffs(my_from) - 1 : lane;
+        const int my_e = __shfl_sync(kFull, first, from) + (my_key & PLACE);
+        // each slot's key against the next one's (the last slot's against the best one left)
+        int next = __shfl_down_sync(kFull, my_key, 1);
+        if (sub == k - 1) next = last;
+        if (sub < k && next != INT_MIN) {
+            const float x = __int_as_float(my_key), y = __int_as_float(next);
+            odd |= !(LOGIT ? (my_key >> BITS) != (next >> BITS) : x - y > value_gap(x, es, BITS));
+        }
+        if (NB > 1 && pops == 8 && count > 8) odd = true;  // its ninth key is not known
+        const uint32_t flagged = __ballot_sync(kFull, live && odd);
+        finish<L>(P, t, sub, live && !(flagged & mask), my_e, rows[(buf * NT + lane / L) * Y.pitch + my_e],
+                  mx, sum);
         if (flagged) {
-            for (int q = 0; q < NT; ++q) {  // the warp together, one token at a time
-                const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (q * L);
+            for (int i = 0; i < NT; ++i) {  // the warp together, one token at a time
+                const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (i * L);
                 if (!(flagged & m)) continue;
-                const int least = __shfl_sync(kFull, prev, q * L);
-                const uint32_t o = __shfl_sync(kFull, open, q * L);
-                const int by = LOGIT ? 255 : __shfl_sync(kFull, tol, q * L);
-                const bool all = (oddball & m) || (!LOGIT && !sigmoid);
-                const int from = LOGIT ? least & ~255 : least < INT_MIN + by ? INT_MIN : least - by;
-                if (all || !select_close<LOGIT>(P, t0 + q, lane, o, from, unit, scratch[warp]))
-                    select_token(P, t0 + q, lane);
+                if (!select_close<LOGIT>(P, q * NT + i, lane, base, scratch[warp]))
+                    select_token(P, q * NT + i, lane);
             }
         }
+        __syncwarp();  // the buffer's readers are done before the next copies into it
     }
 }
 
@@ -662,42 +850,40 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
     for (int i = nv + lane; i < n; i += 32) out[i] = extra ? row[i] + extra[i] : row[i];
 }
 
-template <int L>
+template <int L, int NB>
 int launch_lanes(const SelectParams& P, const SelectLayout& Y, cudaStream_t st) {
     constexpr int NT = 32 / L;
+    const size_t smem = sizeof(float) * Y.pitch * ((P.b ? 1 : 0) + kSelWarps * 2 * NT);
     int64_t blocks = cdiv(P.T, (int64_t)kSelWarps * NT);
-    const int64_t cap = (int64_t)sm_count() * 4;
+    const int64_t cap = (int64_t)sm_count() * 2;  // resident CTAs
     if (blocks > cap) blocks = cap;
-    auto go = [&](auto kern) { kern<<<(unsigned)blocks, kSelWarps * 32, 0, st>>>(P, Y); };
-    auto pick = [&](auto logit) {
-        constexpr bool LOGIT = decltype(logit)::value;
-        if (Y.vr <= 1) go(select_kernel<1, L, LOGIT>);
-        else if (Y.vr <= 2) go(select_kernel<2, L, LOGIT>);
-        else if (Y.vr <= 4) go(select_kernel<4, L, LOGIT>);
-        else go(select_kernel<8, L, LOGIT>);
-    };
-    if (P.b) pick(std::false_type());
-    else pick(std::true_type());
+    auto kern = P.b ? select_kernel<L, NB, false> : select_kernel<L, NB, true>;
+    if (smem > 40 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MOE_ERR_LAUNCH;
+    kern<<<(unsigned)blocks, kSelWarps * 32, smem, st>>>(P, Y);
     return launch_status();
 }
 
-// The lanes of a token: the fewest per group (a power of two) that hold its experts at 8 each, and
-// at least one per slot. Groupings that need more than 32 lanes (their number no power of two
-// and their experts too many) are chosen in 64 bits throughout.
+// The lanes of a token: the fewest (8, 16 or 32) that hold its slots and its groups, each group in
+// the largest power of two of lanes that fits, at up to 32, 16 or 16 experts a lane. 32 lanes hold
+// every grouping: n_group lpg > 16 then, so a lane has at most 256 / 17 < 16 experts.
 int launch_select(const SelectParams& P, cudaStream_t st) {
     const int per = P.E / P.n_group;
-    SelectLayout Y{1, 0, 0};
-    while (Y.lpg * 8 < per) Y.lpg *= 2;
+    SelectLayout Y{};
     int L = 8;
-    while (L < P.n_group * Y.lpg || L < P.k) L *= 2;
-    if (L > 32) {
-        select_exact_kernel<<<(unsigned)cdiv(P.T, kSelWarps), kSelWarps * 32, 0, st>>>(P);
-        return launch_status();
+    for (;; L *= 2) {
+        if (L < 32 && (L < P.k || L < P.n_group)) continue;
+        for (Y.lpg = 1; P.n_group * Y.lpg * 2 <= L;) Y.lpg *= 2;
+        Y.vr = (int)cdiv(per, Y.lpg);
+        if (L == 32 || Y.vr <= (L == 8 ? 32 : 16)) break;
     }
-    while (P.n_group * Y.lpg * 2 <= L && Y.lpg < per) Y.lpg *= 2;  // no lanes left over
-    Y.vr = (int)cdiv(per, Y.lpg);
-    Y.vec = (Y.vr == 8 || Y.vr == 4) && per % Y.vr == 0 && aligned16(P.logits);
-    return L == 8 ? launch_lanes<8>(P, Y, st) : L == 16 ? launch_lanes<16>(P, Y, st) : launch_lanes<32>(P, Y, st);
+    Y.vec = P.E % 4 == 0 && Y.vr % 4 == 0 && per % Y.vr == 0 && aligned16(P.logits);
+    Y.pitch = (P.E + 3) / 4 * 4 + (Y.vec ? 0 : 1);
+    const int nb = Y.vr <= 8 ? 1 : Y.vr <= 16 ? 2 : 4;
+    if (L == 8) return nb == 1 ? launch_lanes<8, 1>(P, Y, st) : nb == 2 ? launch_lanes<8, 2>(P, Y, st) : launch_lanes<8, 4>(P, Y, st);
+    if (L == 16) return nb == 1 ? launch_lanes<16, 1>(P, Y, st) : launch_lanes<16, 2>(P, Y, st);
+    return nb == 1 ? launch_lanes<32, 1>(P, Y, st) : launch_lanes<32, 2>(P, Y, st);
 }
 
 template <int L>
