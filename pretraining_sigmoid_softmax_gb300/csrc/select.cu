@@ -34,10 +34,29 @@ struct SelectParams {
     float* lse;
 };
 
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x / y for y within [2^-20, 2^20] by one correction of the quotient with its exact remainder
+// (Markstein): within one unit in the last place, without a division's slow path.
+__device__ __forceinline__ float quotient(float x, float y) {
+    const float r = fast_rcp(y);
+    const float q = x * r;
+    return fmaf(fmaf(-q, y, x), r, q);
+}
+
 // s = 1 / (1 + e^-l) without overflow on either side.
 __device__ __forceinline__ float stable_sigmoid(float l) {
     const float e = expf(-fabsf(l));
-    return (l >= 0.f ? 1.f : e) / (1.f + e);  // a NaN takes the second form and stays one
+    return quotient(l >= 0.f ? 1.f : e, 1.f + e);  // a NaN takes the second form and stays one
 }
 
 // Over the L consecutive lanes that share a token (L a power of two), by a butterfly.
@@ -108,7 +127,7 @@ __device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int sub
     float g = s;
     if (P.renorm) {
         const float S = seg_sum<L>(s);
-        g = s / S;
+        g = quotient(s, S);
         const bool small = S < kSmallSum;
         if (__any_sync(kFull, live && small)) {  // the whole warp: the sum below is collective
             double sd = 0.0;
@@ -280,8 +299,7 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
 // bits do. Without a bias it is the logit, as an order-preserving integer.
 struct SelectLayout {
     int lpg, vr;
-    int vec;   // rows are 16-byte aligned, and a lane's experts whole 16-byte vectors
-    int pitch; // floats per row in shared memory
+    int vec;  // rows are 16-byte aligned, and a lane's experts whole 16-byte vectors
 };
 
 constexpr float kU = 5.9604645e-8f;  // 2^-24
@@ -293,16 +311,6 @@ constexpr float kU = 5.9604645e-8f;  // 2^-24
 constexpr float kSigmoidErr = 6.4f * kU;
 constexpr float kSoftmaxErr = 25.f * kU;
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float fast_rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 constexpr float kLog2e = 1.44269504f;
 
 // Score of one expert from its logit (within the bounds above); inv = 1 / sum for softmax.
@@ -317,9 +325,10 @@ __device__ __forceinline__ int logit_key(float l) {
 
 // How far below v another value has to lie to come after it for certain, where both are rounded
 // sums s + (b - base): twice the score's error and both sums' roundings (u each, twice), and what
-// dropping `bits` low bits takes off a key (2^bits ulp, of at most 2 u v each).
-__device__ __forceinline__ float value_gap(float v, float es, int bits) {
-    return 2.f * es + (4.2f + (float)(2 << bits)) * kU * v;
+// dropping low bits takes off a key (`dropped` ulp: v's exponent gives an ulp's size).
+__device__ __forceinline__ float value_gap(float v, float es, float dropped) {
+    const float ulp = __int_as_float(__float_as_int(v) & 0x7f800000) * 1.1920929e-7f;
+    return 2.f * es + 4.2f * kU * v + dropped * ulp;
 }
 __device__ __forceinline__ float score_err(bool sigmoid, float inv) {
     return sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
@@ -338,7 +347,8 @@ __device__ __forceinline__ float bias_base(const float* b, int E, int lane) {
     return isfinite(lo) ? lo : 0.f;
 }
 
-// One token whose keys left its choice open, by a whole warp. Groups: lane g finds group g's
+// One token whose keys left its choice open, by a whole warp, from its logits in shared memory.
+// Groups (unless they are settled: bit g of `open`, group g stays): lane g finds group g's
 // largest values, evaluates in 64 bits those that may be its two largest, and the groups are
 // ranked. Experts: without a bias the logits' own order; else those that may be among the k
 // largest of the open groups are gathered, one per lane, evaluated in 64 bits and ranked. False
@@ -346,9 +356,8 @@ __device__ __forceinline__ float bias_base(const float* b, int E, int lane) {
 // for the k; NaN, or softmax over infinities): the token is then left to select_token.
 template <bool LOGIT>
 __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, float base,
-                                          int* scratch) {
+                                          const float* row, bool settled, uint32_t open, int* scratch) {
     constexpr int VJ = kMaxExperts / 32;
-    const float* row = P.logits + t * P.E;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID, top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
     float mx = 0.f, sum = 1.f, inv = 1.f;
@@ -373,8 +382,7 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
     };
     auto value64 = [&](int e) { return no_nan(score64(e) + (double)P.b[e]); };
 
-    uint32_t open = 1u;
-    if (G > 1) {
+    if (!settled) {
         double gs = -INFINITY;
         bool unsettled = false;
         if (lane < G) {
@@ -401,7 +409,7 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
                 // the two largest (or the largest) are among the first three unless the fourth
                 // may reach them
                 const float least = top2 ? b : a;
-                unsettled = per > 3 && !(least - d > value_gap(least, es, 0));
+                unsettled = per > 3 && !(least - d > value_gap(least, es, 0.f));
                 double x = value64(ia);
                 double y = per > 1 ? value64(ib) : -INFINITY, z = per > 2 ? value64(ic) : -INFINITY;
                 if (y > x) { const double q = x; x = y; y = q; }
@@ -443,7 +451,7 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
         if (lane == i) my_e = w;
     }
     if (!LOGIT) {
-        const float v = __int_as_float(kth), gap = value_gap(v, es, 0);
+        const float v = __int_as_float(kth), gap = value_gap(v, es, 0.f);
         int n = 0;
 #pragma unroll
         for (int j = 0; j < VJ; ++j) {
@@ -516,6 +524,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     constexpr int PLACE = (1 << BITS) - 1;
     extern __shared__ __align__(16) float smem[];  // biases, then two buffers of rows per warp
     __shared__ int scratch[kSelWarps][32];
+    __shared__ int2 slots[kSelWarps][32];  // a slot's key and expert
+    __shared__ int taken;                  // steps of the CTA's run that its warps have taken
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID;
@@ -523,49 +533,56 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     const int g = sub / Y.lpg, r = sub % Y.lpg;
     const int count = g < G ? max(0, min(Y.vr, per - r * Y.vr)) : 0;
     const int first = count > 0 ? g * per + r * Y.vr : 0;  // idle lanes read the row's start
+    const int pitch = (E + 3) / 4 * 4;
     float* const bias = smem;  // b - base
-    float* const rows = smem + (LOGIT ? 0 : Y.pitch) + warp * 2 * NT * Y.pitch;
+    float* const rows = smem + (LOGIT ? 0 : pitch) + warp * 2 * NT * pitch;
 
-    // this warp's tokens: a run of its own, NT at a time
-    const int64_t groups = (P.T + NT - 1) / NT, warps = (int64_t)gridDim.x * kSelWarps;
-    const int64_t w = (int64_t)blockIdx.x * kSelWarps + warp;
-    const int64_t q0 = w * groups / warps, q1 = (w + 1) * groups / warps;
-    auto fetch = [&](int64_t q, int buf) {
-        if (q < q1) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int64_t t = q * NT + i;
-                if (t >= P.T) continue;
-                const float* src = P.logits + t * E;
-                float* dst = rows + (buf * NT + i) * Y.pitch;
-                if (Y.vec)
-                    for (int c = 4 * lane; c < E; c += 128) cp_async<16>(dst + c, src + c);
-                else
-                    for (int c = lane; c < E; c += 32) cp_async<4>(dst + c, src + c);
-            }
+    // The CTA's tokens are a run of steps of NT tokens, which its warps take one by one (a token
+    // chosen again delays its warp alone).
+    const int64_t steps = (P.T + NT - 1) / NT;
+    const int64_t s0 = blockIdx.x * steps / gridDim.x;
+    const int n = (int)((blockIdx.x + 1) * steps / gridDim.x - s0);
+    auto fetch = [&](int i, int buf) {
+        if (i < n) {
+            const int64_t t = (s0 + i) * NT;
+            const int m = (int)min((int64_t)NT, P.T - t) * E;  // the step's rows are one piece
+            const float* src = P.logits + t * E;
+            float* dst = rows + buf * NT * pitch;
+            if (Y.vec)
+                for (int c = 4 * lane; c < m; c += 128) cp_async<16>(dst + c, src + c);
+            else
+                for (int c = lane; c < m; c += 32) cp_async<4>(dst + c, src + c);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(q0, 0);
+    auto take = [&]() {
+        int i = 0;
+        if (lane == 0) i = atomicAdd(&taken, 1);
+        return __shfl_sync(kFull, i, 0);
+    };
+    int step = warp;  // the first ones without asking
+    fetch(step, 0);
+    if (threadIdx.x == 0) taken = kSelWarps;
     float base = 0.f;
     if constexpr (!LOGIT) {
         base = bias_base(P.b, E, lane);
         for (int e = threadIdx.x; e < E; e += kSelWarps * 32) bias[e] = P.b[e] - base;
-        __syncthreads();
     }
+    __syncthreads();
     // lanes of equal banks start at different vectors of their own (the order is free)
     const int nvec = Y.vr / 4;
     const int turn = Y.vec ? (sub * Y.vr / 32) % nvec : 0;
     const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
 
-    for (int64_t q = q0; q < q1; ++q) {
-        const int buf = (int)(q - q0) & 1;
-        fetch(q + 1, buf ^ 1);
+    for (int buf = 0; step < n; buf ^= 1) {
+        const int ahead = take();
+        fetch(ahead, buf ^ 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-        const int64_t t = q * NT + lane / L;
+        const int64_t t0 = (s0 + step) * NT, t = t0 + lane / L;
         const bool live = t < P.T;
-        const float* row = rows + (buf * NT + lane / L) * Y.pitch + first;
+        const float* const held = rows + buf * NT * pitch;  // the step's rows
+        const float* row = held + lane / L * E + first;
         // four of the lane's logits, from place `at` on (a multiple of 4), as far as there are
         auto load4 = [&](int c, int& at, float (&v)[4]) {
             at = 4 * c;
@@ -657,6 +674,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 merge8(key, kb);
             }
         }
+        bool groups = false;  // unsettled
+        uint32_t open = 1u;
         if (G > 1) {
             int a = key[0], b = key[1];
             for (int o = 1; o < Y.lpg; o <<= 1) {
@@ -671,11 +690,11 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 }
             }
             // a sum that counts a value clamped at 0
-            if (!LOGIT && top2 && g < G) odd |= b <= PLACE;
-            int gs = a;  // a score's order as an integer
+            if (!LOGIT && top2 && g < G) groups |= b <= PLACE;
+            int gs = a & ~PLACE;  // a score's order as an integer
             if (top2)
                 gs = __float_as_int(LOGIT ? fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv)
-                                          : __int_as_float(a) + __int_as_float(b));
+                                          : __int_as_float(a & ~PLACE) + __int_as_float(b & ~PLACE));
             int rank = 0;
             for (int h = 0; h < G; ++h) {
                 const int x = __shfl_sync(kFull, gs, h * Y.lpg, L);
@@ -687,59 +706,79 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 const int hi = seg_max<L>(!kept && g < G ? gs : INT_MIN);
                 const float x = __int_as_float(lo), y = __int_as_float(hi);
                 bool sure;
-                if (!LOGIT)  // a NaN (of an infinite value) is never sure
-                    sure = x - y > (top2 ? 2.f * es : 0.f) + value_gap(x, es, BITS);
+                if (!LOGIT)  // (an infinite sum is never sure; a sum's two keys drop at most 1.5 of its ulps)
+                    sure = x - y > (top2 ? 2.f * es + value_gap(x, es, 1.5f * (PLACE + 2)) : value_gap(x, es, (float)PLACE));
                 else if (!top2)
-                    sure = (lo >> BITS) != (hi >> BITS);
+                    sure = lo != hi;
                 else  // sums of scores: softmax terms are within 160 u of themselves down to e^-87
                     sure = x - y > 2.f * (sigmoid ? 2.f * kSigmoidErr + kU * x : 161.f * kU * x) && x > 1e-30f;
-                odd |= !sure;
+                groups |= !sure;
             }
+            open = 0u;
+            const uint32_t heads = __ballot_sync(kFull, kept && r == 0) >> (lane / L * L);
+            for (int h = 0; h < G; ++h) open |= ((heads >> (h * Y.lpg)) & 1u) << h;
             if (!kept) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
             }
         }
-        int my_key = INT_MIN, pops = 0, last = INT_MIN;
-        uint32_t my_from = 0;
-        for (int i = 0; i <= k; ++i) {
-            const int top = seg_max<L>(key[0]);
-            last = top;
-            if (i == k) break;
-            const bool mine = key[0] == top;
-            const uint32_t m = __ballot_sync(kFull, mine) & mask;
-            if (sub == i) {
-                my_key = top;
-                my_from = m;
-            }
-            if (mine && (m & ((1u << lane) - 1u)) == 0) {  // the first of equal ones
-                ++pops;
+        // the rounds: the lane that holds the largest key writes the slot and moves its list up
+        int pops = 0, last = INT_MIN;
+        int2* const slot = &slots[warp][lane / L * L];
+        if (L == 8) {  // at most eight slots: after round i, 8 - i keys of a lane can matter
 #pragma unroll
-                for (int j = 0; j < 7; ++j) key[j] = key[j + 1];
-                key[7] = INT_MIN;
+            for (int i = 0; i <= 8; ++i) {
+                last = seg_max<L>(key[0]);
+                if (i == k) break;
+                if (key[0] == last) {
+                    slot[i & 7] = make_int2(last, first + (last & PLACE));
+                    ++pops;
+#pragma unroll
+                    for (int j = 0; j < 7; ++j)
+                        if (j <= 7 - i) key[j] = key[j + 1];
+                    key[7] = INT_MIN;
+                }
+            }
+        } else {
+            for (int i = 0; i <= k; ++i) {
+                last = seg_max<L>(key[0]);
+                if (i == k) break;
+                if (key[0] == last) {
+                    slot[i] = make_int2(last, first + (last & PLACE));
+                    ++pops;
+#pragma unroll
+                    for (int j = 0; j < 7; ++j) key[j] = key[j + 1];
+                    key[7] = INT_MIN;
+                }
             }
         }
-        const int from = my_from ? __ffs(my_from) - 1 : lane;
-        const int my_e = __shfl_sync(kFull, first, from) + (my_key & PLACE);
+        __syncwarp();
+        const int2 mine = slot[sub < k ? sub : 0];
+        const int my_e = mine.y;
         // each slot's key against the next one's (the last slot's against the best one left)
-        int next = __shfl_down_sync(kFull, my_key, 1);
+        int next = __shfl_down_sync(kFull, mine.x, 1);
         if (sub == k - 1) next = last;
+        bool close = false;
         if (sub < k && next != INT_MIN) {
-            const float x = __int_as_float(my_key), y = __int_as_float(next);
-            odd |= !(LOGIT ? (my_key >> BITS) != (next >> BITS) : x - y > value_gap(x, es, BITS));
+            const float x = __int_as_float(mine.x & ~PLACE), y = __int_as_float(next & ~PLACE);
+            close = !(LOGIT ? (mine.x >> BITS) != (next >> BITS) : x - y > value_gap(x, es, (float)PLACE));
         }
-        if (NB > 1 && pops == 8 && count > 8) odd = true;  // its ninth key is not known
-        const uint32_t flagged = __ballot_sync(kFull, live && odd);
-        finish<L>(P, t, sub, live && !(flagged & mask), my_e, rows[(buf * NT + lane / L) * Y.pitch + my_e],
-                  mx, sum);
-        if (flagged) {
+        close |= seg_sum<L>(pops) != k;           // equal keys, taken in one round
+        close |= NB > 1 && pops >= 8 && count > 8;  // the lane's ninth key is not known
+        const uint32_t again = __ballot_sync(kFull, live && (odd || groups || close));
+        finish<L>(P, t, sub, live && !(again & mask), my_e, held[lane / L * E + my_e], mx, sum);
+        if (again) {
+            const uint32_t strange = __ballot_sync(kFull, live && odd), unsettled = __ballot_sync(kFull, live && groups);
             for (int i = 0; i < NT; ++i) {  // the warp together, one token at a time
                 const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (i * L);
-                if (!(flagged & m)) continue;
-                if (!select_close<LOGIT>(P, q * NT + i, lane, base, scratch[warp]))
-                    select_token(P, q * NT + i, lane);
+                if (!(again & m)) continue;
+                const uint32_t o = __shfl_sync(kFull, open, i * L);
+                if ((strange & m) ||
+                    !select_close<LOGIT>(P, t0 + i, lane, base, held + i * E, !(unsettled & m), o, scratch[warp]))
+                    select_token(P, t0 + i, lane);
             }
         }
+        step = ahead;
         __syncwarp();  // the buffer's readers are done before the next copies into it
     }
 }
@@ -853,8 +892,8 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
 template <int L, int NB>
 int launch_lanes(const SelectParams& P, const SelectLayout& Y, cudaStream_t st) {
     constexpr int NT = 32 / L;
-    const size_t smem = sizeof(float) * Y.pitch * ((P.b ? 1 : 0) + kSelWarps * 2 * NT);
-    int64_t blocks = cdiv(P.T, (int64_t)kSelWarps * NT);
+    const size_t smem = sizeof(float) * ((P.E + 3) / 4 * 4) * ((P.b ? 1 : 0) + kSelWarps * 2 * NT);
+    int64_t blocks = cdiv(P.T, (int64_t)NT);      // one step each, until the GPU is full
     const int64_t cap = (int64_t)sm_count() * 2;  // resident CTAs
     if (blocks > cap) blocks = cap;
     auto kern = P.b ? select_kernel<L, NB, false> : select_kernel<L, NB, true>;
@@ -879,7 +918,6 @@ int launch_select(const SelectParams& P, cudaStream_t st) {
         if (L == 32 || Y.vr <= (L == 8 ? 32 : 16)) break;
     }
     Y.vec = P.E % 4 == 0 && Y.vr % 4 == 0 && per % Y.vr == 0 && aligned16(P.logits);
-    Y.pitch = (P.E + 3) / 4 * 4 + (Y.vec ? 0 : 1);
     const int nb = Y.vr <= 8 ? 1 : Y.vr <= 16 ? 2 : 4;
     if (L == 8) return nb == 1 ? launch_lanes<8, 1>(P, Y, st) : nb == 2 ? launch_lanes<8, 2>(P, Y, st) : launch_lanes<8, 4>(P, Y, st);
     if (L == 16) return nb == 1 ? launch_lanes<16, 1>(P, Y, st) : launch_lanes<16, 2>(P, Y, st);
