@@ -4,7 +4,9 @@ Forward (route -> permute -> routed experts -> shared expert -> combine) and bac
 (combine backward -> routed experts backward -> shared expert backward -> router backward
 -> input gradient), then the aux-loss-free bias update. Every step runs in the library's
 CUDA kernels; this module only owns the device buffers (allocated once per shape) and the
-call order.
+call order. Around the layer: the residual addition with the RMS norm in front of it
+(``RMSNorm``, or ``MoELayer(norm_eps=...)``) and the clipping of a step's gradients
+(``clip_grad_norm_``).
 """
 from __future__ import annotations
 
@@ -30,6 +32,23 @@ class MoEShape:
     seq_len: int = 0
     fp8: bool = False        # expert forward GEMMs on E4M3 operands
     fp8_dgrad: bool = False  # and the expert backward's data-gradient GEMMs too
+    # choice of experts within the topk_group best of n_group groups (a group's score: group_rule);
+    # gates renormalised (None: as the mode has them, sigmoid yes, softmax no) and scaled
+    n_group: int = 1
+    topk_group: int = 1
+    group_rule: int = ops.GROUP_TOP2
+    renorm: bool | None = None
+    gate_scale: float = 1.0
+
+    @property
+    def renormalised(self) -> bool:
+        return self.mode == ops.MODE_SIGMOID if self.renorm is None else self.renorm
+
+    @property
+    def selects(self) -> bool:
+        """The choice is moe_select_experts' (groups, or gates other than the mode's own)."""
+        return (self.n_group > 1 or self.gate_scale != 1.0
+                or self.renormalised != (self.mode == ops.MODE_SIGMOID))
 
     @property
     def has_aux(self) -> bool:
@@ -158,7 +177,7 @@ class MoEPlan:
             # its pace and the term costs more there than it saves (small fine-grained
             # layer, d_ff 256: 0.675 -> 0.681 ms per step), so short experts keep the term
             # in the token sum.
-            self.router_rows = (s.mode == ops.MODE_SIGMOID and not s.has_aux
+            self.router_rows = (s.mode == ops.MODE_SIGMOID and not s.has_aux and not s.selects
                                 and s.f >= self.ROUTER_ROWS_MIN_FF)
             self.dl_rows = torch.zeros((R,), dtype=f32, device=dev) if self.router_rows else None
             self.dx_r = _empty((T, d), f32, dev) if self.router_dx_tc else None
@@ -193,6 +212,7 @@ class MoEPlan:
         s = self.s
         n = 1 + (1 if s.E <= 128 else 0)                   # route (W_r pieces + tensor-core
         n += 1 if s.mode == ops.MODE_SOFTMAX else 0         # logits) (+ z-loss reduction)
+        n += 1 if s.selects else 0                          # choice within groups
         if s.has_aux:
             n += 2 + (1 if backward else 0)                 # balancing losses (+ gradient)
         n += 4                                              # permute (the padding rows and
@@ -211,6 +231,7 @@ class MoEPlan:
             else:
                 n += 5 + (4 if s.f_shared else 0)           # expert backward (+ expert order)
             n += 3                                          # router backward
+            n += 1 if s.selects and s.E <= 128 else 0       # the logit gradient's pieces
             if (s.mode == ops.MODE_SOFTMAX or s.has_aux) and s.E <= 128:
                 n += 3                                      # router dx: two splits + GEMM
             n += 1                                          # input gradient
@@ -219,21 +240,30 @@ class MoEPlan:
         return n
 
     # ------------------------------------------------------------------ forward
-    def forward(self, x, W_r, b, W_g, W_u, W_d, Ws_g=None, Ws_u=None, Ws_d=None, stream=None):
+    def forward(self, x, W_r, b, W_g, W_u, W_d, Ws_g=None, Ws_u=None, Ws_d=None, stream=None,
+                codes=False):
+        """codes: x's E4M3 codes and scales are in x8 and sx already (moe_rms_norm wrote them)."""
         s = self.s
         self.x = x
         self.W = (W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d)
         softmax = s.mode == ops.MODE_SOFTMAX
         main = stream if stream is not None else torch.cuda.current_stream()
-        if s.fp8:  # before the fork: the routed rows and the shared expert both use them
-            ops.moe_quantize_rows_fp8(x, None, self.x8, self.sx, stream)
+        if s.fp8 and not codes:  # before the fork: the routed rows and the shared expert both
+            ops.moe_quantize_rows_fp8(x, None, self.x8, self.sx, stream)  # use them
         if s.f_shared and self.overlap:  # fork: the shared expert on the side stream
             self.side.wait_stream(main)
             self._shared_forward(x, Ws_g, Ws_u, Ws_d, self.side)
-        ops.moe_route(x, W_r, None if softmax else b, s.k, s.mode, s.z_coef, self.logits,
-                      self.topk_idx, self.topk_gate, self.topk_score,
-                      self.lse if softmax else None, self.z_loss if softmax else None, self.ws,
-                      stream)
+        if s.selects:
+            ops.moe_router_logits(x, W_r, self.logits, self.ws, self.lse if softmax else None,
+                                  self.z_loss if softmax else None, s.z_coef, stream)
+            ops.moe_select_experts(self.logits, None if softmax else b, s.k, s.mode, s.n_group,
+                                   s.topk_group, s.group_rule, s.renormalised, s.gate_scale,
+                                   self.topk_idx, self.topk_gate, self.topk_score, None, stream)
+        else:
+            ops.moe_route(x, W_r, None if softmax else b, s.k, s.mode, s.z_coef, self.logits,
+                          self.topk_idx, self.topk_gate, self.topk_score,
+                          self.lse if softmax else None, self.z_loss if softmax else None, self.ws,
+                          stream)
         if s.has_aux:
             ops.moe_aux_loss(self.logits, self.topk_idx, s.mode, s.seq_len, s.aux_switch,
                              s.aux_seq, self.aux_loss, self.aux_f, self.ws, stream)
@@ -359,6 +389,14 @@ class MoEPlan:
         s = self.s
         softmax = s.mode == ops.MODE_SOFTMAX
         rows = self.router_rows
+        if s.selects:
+            ops.moe_select_experts_bwd(self.dg, self.topk_idx, self.topk_score,
+                                       self.logits if softmax else None,
+                                       self.lse if softmax else None, s.mode, s.renormalised,
+                                       s.gate_scale, self.dlogits, s.z_coef if softmax else 0.0,
+                                       extra, stream)
+            ops.moe_router_dw(self.dlogits, x, self.dW_r, self.ws, stream)
+            return
         ops.moe_route_bwd(self.dg, x, self.topk_idx, self.topk_gate, self.topk_score,
                           self.logits if softmax else None, self.lse if softmax else None, s.E,
                           s.mode, s.z_coef, self.dlogits, self.dW_r, self.ws, stream,
@@ -412,6 +450,18 @@ class MoEPlan:
             step()
         return graph
 
+    def clip_grads(self, max_norm, out=None, norm=None, stream=None):
+        """The global norm of the weight gradients and the factor that clips them (returned, [2]
+        fp32), and the clipped gradients: in place, or into ``out`` (a dict with the names of
+        ``grads()``, dx not among them), so that an optimiser's own buffers take them."""
+        g = {n: t for n, t in self.grads().items() if n != "dx"}
+        if out is not None and set(out) != set(g):
+            raise ValueError(f"out must hold {sorted(g)}, got {sorted(out)}")
+        norm = torch.empty(2, dtype=torch.float32, device=self.dW_r.device) if norm is None else norm
+        ops.moe_clip_grads(list(g.values()), max_norm, None if out is None else [out[n] for n in g],
+                           norm, self.ws, stream)
+        return norm
+
     def grads(self) -> dict:
         g = {"dx": self.dx, "dW_r": self.dW_r, "dW_g": self.dW_g, "dW_u": self.dW_u,
              "dW_d": self.dW_d}
@@ -428,11 +478,11 @@ class _MoEFunction(torch.autograd.Function):
     forwards and the backward refuses a stale one."""
 
     @staticmethod
-    def forward(ctx, x, W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, plan):
+    def forward(ctx, x, W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, plan, codes=False):
         ctx.plan = plan
         plan.generation += 1
         ctx.generation = plan.generation
-        out = plan.forward(x.contiguous(), W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d)
+        out = plan.forward(x.contiguous(), W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, codes=codes)
         return out.clone()
 
     @staticmethod
@@ -448,7 +498,83 @@ class _MoEFunction(torch.autograd.Function):
         return (g["dx"].clone(), g["dW_r"].clone(), None, g["dW_g"].clone(), g["dW_u"].clone(),
                 g["dW_d"].clone(), g["dWs_g"].clone() if shared else None,
                 g["dWs_u"].clone() if shared else None, g["dWs_d"].clone() if shared else None,
-                None)
+                None, None)
+
+
+class _RMSNormFunction(torch.autograd.Function):
+    """y = rms_norm(z) w with z = residual + x; returns (y, z), or y alone without a residual."""
+
+    @staticmethod
+    def forward(ctx, x, residual, w, eps, yq, sy):
+        x = x.contiguous()
+        y = torch.empty_like(x)
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        z = None
+        if residual is not None:
+            residual = residual.contiguous()
+            z = torch.empty_like(residual)
+        ops.moe_rms_norm(x, residual, w, eps, z, y, yq, sy, rstd)
+        ctx.save_for_backward(x if z is None else z, rstd, w)
+        ctx.summed = z is not None
+        ctx.set_materialize_grads(False)
+        return y if z is None else (y, z)
+
+    @staticmethod
+    def backward(ctx, dy, dres=None):
+        z, rstd, w = ctx.saved_tensors
+        if dy is None:  # only z was used: its gradient is the residual's and x's
+            if dres is None:
+                return None, None, None, None, None, None
+            return dres.to(torch.bfloat16), dres, None, None, None, None
+        T, d = z.shape
+        dy = dy.to(torch.bfloat16).contiguous()
+        dres = None if dres is None else dres.to(z.dtype).contiguous()
+        dz, dw = torch.empty_like(z), torch.empty_like(w)
+        dx = torch.empty_like(dy) if z.dtype is not torch.bfloat16 else None
+        ws = torch.empty(ops.moe_workspace_bytes(T, d, 1, 1), dtype=torch.uint8, device=z.device)
+        ops.moe_rms_norm_bwd(dy, dres, z, rstd, w, dz, dx, dw, ws)
+        return dz if dx is None else dx, dz if ctx.summed else None, dw, None, None, None
+
+
+class RMSNorm(torch.nn.Module):
+    """Residual addition and root-mean-square norm: ``forward(x, residual)`` takes x [T, d] bf16 and
+    the residual stream [T, d] (bf16 or fp32, or None) and returns (y, z): z = residual + x in
+    the stream's type, the next block's residual (x itself without one), and
+    y = z / rms(z) * w in bf16. Gradients flow to x, the residual and w (fp32)."""
+
+    def __init__(self, d, eps=1e-6, device="cuda"):
+        super().__init__()
+        self.d, self.eps = d, eps
+        self.w = torch.nn.Parameter(torch.ones(d, device=device))
+
+    def forward(self, x, residual=None, yq=None, sy=None):
+        """yq, sy: buffers that take y's E4M3 codes and scales too (moe_rms_norm)."""
+        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
+            raise ValueError(f"x must be [T, {self.d}] bf16, got {tuple(x.shape)} {x.dtype}")
+        if residual is None:
+            return _RMSNormFunction.apply(x, None, self.w, self.eps, yq, sy), x
+        if residual.shape != x.shape or residual.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"residual must be [T, {self.d}] bf16 or fp32 as x has it, got "
+                             f"{tuple(residual.shape)} {residual.dtype}")
+        return _RMSNormFunction.apply(x, residual, self.w, self.eps, yq, sy)
+
+
+@torch.no_grad()
+def clip_grad_norm_(parameters, max_norm):
+    """Clips the gradients of ``parameters`` (bf16 or fp32, on one device; those without one are
+    passed over) to a global 2-norm of at most ``max_norm``, in place, and returns that norm as
+    it was ([] fp32 device tensor, no synchronisation). A norm that is not finite leaves the
+    gradients as they are."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in dict.fromkeys(parameters) if p.grad is not None]  # each once
+    if not grads:
+        return torch.zeros(())
+    dev = grads[0].device
+    norm = torch.empty(2, dtype=torch.float32, device=dev)
+    ws = torch.empty(ops.moe_workspace_bytes(1, 128, 1, 1), dtype=torch.uint8, device=dev)
+    ops.moe_clip_grads(grads, max_norm, None, norm, ws)
+    return norm[0]
 
 
 class MoELayer(torch.nn.Module):
@@ -462,12 +588,28 @@ class MoELayer(torch.nn.Module):
     ``update_bias()``, called after backward with that step's expert counts.
 
     One plan (set of device buffers) is kept per token count; each backward must run before
-    the next forward with the same token count."""
+    the next forward with the same token count.
+
+    ``norm_eps`` puts the RMS norm in front of the layer (``norm``, an ``RMSNorm``):
+    ``forward(x, residual)`` then adds x to the residual stream, runs the layer on the norm of
+    the sum and returns (out, stream). With FP8 experts the norm writes their input's codes in
+    the same pass. ``n_group`` > 1 limits each token's experts to the ``topk_group`` best groups
+    (``group_rule`` "max" or "top2": a group's score is its largest selection value or the sum
+    of its two largest); ``renorm`` and ``gate_scale`` set how gates follow from scores."""
 
     def __init__(self, d, E, k, f, f_shared=0, mode="sigmoid", z_coef=0.0, gamma=1e-3,
                  device="cuda", bias_rule="sign", aux_switch=0.0, aux_seq=0.0, seq_len=0,
-                 precision="bf16"):
+                 precision="bf16", norm_eps=None, n_group=1, topk_group=1, group_rule="top2",
+                 renorm=None, gate_scale=1.0):
         super().__init__()
+        if group_rule not in ("max", "top2"):
+            raise ValueError("group_rule is max or top2")
+        if not 0.0 < gate_scale < float("inf"):
+            raise ValueError("gate_scale is positive (the experts' backward counts on gates >= 0)")
+        if n_group < 1 or E % n_group or not 1 <= topk_group <= n_group \
+                or k > topk_group * (E // n_group):
+            raise ValueError(f"{E} experts in {n_group} groups, {topk_group} of them kept, cannot "
+                             f"give {k} experts")
         if mode not in ("sigmoid", "softmax") or bias_rule not in ("sign", "proportional") \
                 or precision not in ("bf16", "fp8", "fp8_dgrad"):
             raise ValueError("mode is sigmoid or softmax, bias_rule sign or proportional, "
@@ -478,6 +620,10 @@ class MoELayer(torch.nn.Module):
         self.aux_switch, self.aux_seq, self.seq_len = aux_switch, aux_seq, seq_len
         self.fp8 = precision in ("fp8", "fp8_dgrad")
         self.fp8_dgrad = precision == "fp8_dgrad"
+        self.n_group, self.topk_group = n_group, topk_group
+        self.group_rule = ops.GROUP_MAX if group_rule == "max" else ops.GROUP_TOP2
+        self.renorm, self.gate_scale = renorm, gate_scale
+        self.norm = None if norm_eps is None else RMSNorm(d, norm_eps, device)
         bf = dict(dtype=torch.bfloat16, device=device)
         self.W_r = torch.nn.Parameter(torch.randn(E, d, device=device) * d ** -0.5)
         self.register_buffer("b", torch.zeros(E, device=device))
@@ -497,19 +643,31 @@ class MoELayer(torch.nn.Module):
         if T not in self._plans:
             shape = MoEShape(T, self.d, self.E, self.k, self.f, self.f_shared, self.mode,
                              self.z_coef, self.aux_switch, self.aux_seq, self.seq_len or T,
-                             self.fp8, self.fp8_dgrad)
+                             self.fp8, self.fp8_dgrad, self.n_group, self.topk_group,
+                             self.group_rule, self.renorm, self.gate_scale)
             plan = MoEPlan(shape, self.W_g.device)
             plan.generation = 0
             self._plans[T] = plan
         return self._plans[T]
 
-    def forward(self, x):
+    def forward(self, x, residual=None):
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
             raise ValueError(f"x must be [T, {self.d}] bf16, got {tuple(x.shape)} {x.dtype}")
+        if residual is not None and self.norm is None:
+            raise ValueError("a residual is taken by a layer with a norm (norm_eps)")
         plan = self._plan(x.shape[0])
         self._last_plan = plan
-        return _MoEFunction.apply(x, self.W_r, self.b, self.W_g, self.W_u, self.W_d, self.Ws_g,
-                                  self.Ws_u, self.Ws_d, plan)
+        z = None
+        if self.norm is not None:
+            x, z = self.norm(x, residual, plan.x8 if self.fp8 else None,
+                             plan.sx if self.fp8 else None)
+        out = _MoEFunction.apply(x, self.W_r, self.b, self.W_g, self.W_u, self.W_d, self.Ws_g,
+                                 self.Ws_u, self.Ws_d, plan, self.fp8 and z is not None)
+        return out if z is None else (out, z)
+
+    def clip_grads_(self, max_norm):
+        """Clips this layer's parameter gradients in place (``clip_grad_norm_``); returns the norm."""
+        return clip_grad_norm_(self.parameters(), max_norm)
 
     @torch.no_grad()
     def update_bias(self):

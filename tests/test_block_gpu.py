@@ -1,0 +1,258 @@
+"""The operators around the layer as a training step uses them: residual addition and RMS norm,
+experts chosen within groups, the layer, its backward through the norm, and clipping, against a
+64-bit autograd graph of the same formulas on the GPU's choice of experts.
+
+Bounds. Every tensor that a step stores in bf16 is off by at most half a step, 2^-8 of each
+value (2^-9 on average over a binade), so by at most 2^-8 of its norm; errors of independent
+roundings do not add up coherently in a product, and the map from one stored tensor to the next
+(a product with a Gaussian matrix, SwiGLU, a sum) keeps relative norms of errors to within a
+small factor. Forward, seven tensors are stored between the inputs and out (z, y, a, u, h, the
+experts' rows, out); a gradient has up to five more (the rows of dY, dA, dU, dX, dx). Twelve
+times 2^-8 bounds the relative norm of every difference: 4.7e-2. FP8 operands have 2^-4 of each
+value instead, twice in a row (the input and h): 2 * 2^-4 on top."""
+import numpy as np
+import pytest
+import torch
+
+from pretraining_sigmoid_softmax_gb300 import ops
+from pretraining_sigmoid_softmax_gb300.layer import MoELayer, MoEPlan, MoEShape, RMSNorm, clip_grad_norm_
+
+from gpu_common import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+REL = 12 * 2.0 ** -8
+REL_FP8 = REL + 2 * 2.0 ** -4
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    require_gpu()
+
+
+def _off(got, want):
+    want = want.double()
+    return float((got.double() - want).norm() / want.norm().clamp_min(1e-300))
+
+
+def _reference(layer, x, residual, idx, dout, dz):
+    """out, the stream and all gradients in 64 bits, with the experts `idx` of each token."""
+    p = {n: t.detach().double().requires_grad_(True) for n, t in layer.named_parameters()}
+    x, r = x.double().requires_grad_(True), residual.double().requires_grad_(True)
+    z = x + r
+    y = z * torch.rsqrt((z * z).mean(1, keepdim=True) + layer.norm.eps) * p["norm.w"]
+    l = y @ p["W_r"].t()
+    s = torch.sigmoid(l) if layer.mode == ops.MODE_SIGMOID else torch.softmax(l, 1)
+    g = s.gather(1, idx)
+    renorm = layer.mode == ops.MODE_SIGMOID if layer.renorm is None else layer.renorm
+    if renorm:
+        g = g / g.sum(1, keepdim=True)
+    g = layer.gate_scale * g
+    out = torch.zeros_like(y)
+    for e in range(layer.E):
+        t, i = (idx == e).nonzero(as_tuple=True)
+        if len(t):
+            h = torch.nn.functional.silu(y[t] @ p["W_g"][e].t()) * (y[t] @ p["W_u"][e].t())
+            out = out.index_add(0, t, g[t, i][:, None] * (h @ p["W_d"][e].t()))
+    if layer.f_shared:
+        out = out + (torch.nn.functional.silu(y @ p["Ws_g"].t()) * (y @ p["Ws_u"].t())) @ p["Ws_d"].t()
+    loss = (out * dout.double()).sum() + (z * dz.double()).sum()
+    if layer.mode == ops.MODE_SOFTMAX and layer.z_coef:
+        loss = loss + layer.z_coef * (torch.logsumexp(l, 1) ** 2).mean()
+    loss.backward()
+    return out, z, x.grad, r.grad, {n: t.grad for n, t in p.items()}
+
+
+CASES = {
+    "sigmoid in groups": dict(T=300, d=256, E=16, k=4, f=128, f_shared=128, mode="sigmoid", n_group=4,
+                              topk_group=2, gate_scale=2.5),
+    "softmax renormalised": dict(T=257, d=384, E=24, k=3, f=256, mode="softmax", n_group=3, topk_group=2,
+                                 group_rule="max", renorm=True),
+    "softmax with z-loss": dict(T=200, d=256, E=32, k=4, f=128, mode="softmax", z_coef=1e-2, n_group=8,
+                                topk_group=4),
+    "many experts": dict(T=150, d=256, E=160, k=6, f=128, mode="sigmoid", n_group=8, topk_group=4,
+                         renorm=False),
+    "no groups, long experts": dict(T=128, d=256, E=8, k=2, f=768, mode="sigmoid"),
+    "fp8": dict(T=256, d=256, E=16, k=4, f=256, f_shared=128, mode="sigmoid", n_group=4, topk_group=2,
+                precision="fp8"),
+    "fp8 data gradients": dict(T=256, d=256, E=16, k=4, f=256, mode="sigmoid", n_group=4, topk_group=2,
+                               precision="fp8_dgrad"),
+}
+
+
+@pytest.mark.parametrize("rdtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("name", CASES)
+def test_block_matches_64_bits(name, rdtype):
+    c = dict(CASES[name])
+    T, d = c.pop("T"), c["d"]
+    torch.manual_seed(len(name))
+    layer = MoELayer(norm_eps=1e-5, **c)
+    with torch.no_grad():
+        layer.norm.w.add_(0.1 * torch.randn(d, device="cuda"))
+        if layer.mode == ops.MODE_SIGMOID:
+            layer.b.copy_(0.1 * torch.rand(layer.E, device="cuda"))
+    x = torch.randn(T, d, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    res = torch.randn(T, d, device="cuda").to(rdtype).requires_grad_(True)
+    dout = torch.randn(T, d, device="cuda").to(torch.bfloat16)
+    dz = torch.randn(T, d, device="cuda").to(rdtype)
+    ops.moe_clear_device_status()
+    out, z = layer(x, res)
+    torch.autograd.backward([out, z], [dout, dz])
+    torch.cuda.synchronize()
+    assert ops.moe_device_status()[0] == 0
+    plan = layer._last_plan
+    assert plan.s.selects == (name != "no groups, long experts")
+    idx = plan.topk_idx.long()
+    per = layer.E // layer.n_group
+    assert (torch.stack([(idx // per == g).any(1) for g in range(layer.n_group)]).sum(0)
+            <= layer.topk_group).all()
+    want_out, want_z, want_dx, want_dr, grads = _reference(layer, x.detach(), res.detach(), idx, dout, dz)
+    rel = REL_FP8 if layer.fp8 else REL
+    assert out.dtype == torch.bfloat16 and z.dtype == rdtype
+    assert torch.equal(z, (x.detach().float() + res.detach().float()).to(rdtype))
+    assert _off(out, want_out) <= rel
+    assert x.grad.dtype == torch.bfloat16 and res.grad.dtype == rdtype
+    assert _off(x.grad, want_dx) <= rel and _off(res.grad, want_dr) <= rel
+    for n, p in layer.named_parameters():
+        assert p.grad.dtype == p.dtype
+        assert _off(p.grad, grads[n]) <= rel, n
+    # the step's end: clip what the backward left
+    before = {n: p.grad.clone() for n, p in layer.named_parameters()}
+    total = float(torch.sqrt(sum((g.double() ** 2).sum() for g in before.values())))
+    norm = layer.clip_grads_(0.5)
+    assert abs(float(norm) - total) <= 1e-5 * total and total > 0.5
+    for n, p in layer.named_parameters():
+        assert _off(p.grad, before[n].double() * (0.5 / total)) <= 2.0 ** -8
+    assert float(clip_grad_norm_(layer.parameters(), 1.0)) == pytest.approx(0.5, rel=2.0 ** -8)
+
+
+def test_fp8_block_takes_the_norm_codes():
+    """The FP8 layer reads the codes that the norm wrote: the experts' inputs are those codes."""
+    torch.manual_seed(0)
+    layer = MoELayer(256, 8, 2, 128, precision="fp8", norm_eps=1e-6)
+    x = torch.randn(200, 256, device="cuda").to(torch.bfloat16)
+    layer(x)
+    plan = layer._last_plan
+    yq, sy = torch.empty_like(plan.x8), torch.empty_like(plan.sx)
+    y, z = layer.norm(x, None, yq, sy)
+    torch.cuda.synchronize()
+    assert z is x and torch.equal(plan.x8, yq) and torch.equal(plan.sx, sy)
+    rows = plan.slot_to_row.reshape(-1).long()
+    assert torch.equal(plan.X8[rows], yq.repeat_interleave(2, 0))
+    dq = yq.view(torch.float8_e4m3fn).float() * sy[:, None]
+    # a code is off by half a step of E4M3, 2^-4 of the value or 2^-10 of the scale, and y itself by
+    # half a step of bf16
+    half = torch.maximum(2.0 ** -4 * y.float().abs(), 2.0 ** -10 * sy[:, None])
+    assert ((dq - y.float()).abs() <= half * (1 + 2.0 ** -7) + 2.0 ** -8 * 1.07 * y.float().abs()).all()
+
+
+def test_two_blocks_share_a_residual_stream():
+    """Two layers in a row on one fp32 stream: gradients meet in it. The stream's own gradient is
+    checked against 64-bit autograd of the same two blocks."""
+    torch.manual_seed(3)
+    T, d = 130, 256
+    layers = [MoELayer(d, 16, 4, 128, norm_eps=1e-6, n_group=4, topk_group=2) for _ in range(2)]
+    x = torch.randn(T, d, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    r = torch.randn(T, d, device="cuda").requires_grad_(True)
+    y1, z1 = layers[0](x, r)
+    y2, z2 = layers[1](y1, z1)
+    dout = torch.randn(T, d, device="cuda").to(torch.bfloat16)
+    dz = torch.randn(T, d, device="cuda")
+    torch.autograd.backward([y2, z2], [dout, dz])
+    torch.cuda.synchronize()
+    idx = [l._last_plan.topk_idx.long() for l in layers]
+    _, _, gx2, gr2, _ = _reference(layers[1], y1.detach(), z1.detach(), idx[1], dout, dz)
+    _, _, gx1, gr1, _ = _reference(layers[0], x.detach(), r.detach(), idx[0], gx2, gr2)
+    assert _off(x.grad, gx1) <= 2 * REL and _off(r.grad, gr1) <= 2 * REL
+
+
+def test_norm_module_alone():
+    torch.manual_seed(4)
+    norm = RMSNorm(512, eps=1e-5)
+    x = torch.randn(33, 512, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    y, z = norm(x)
+    assert z is x
+    dy = torch.randn_like(y)
+    y.backward(dy)
+    x64, w64 = x.detach().double().requires_grad_(True), norm.w.detach().double().requires_grad_(True)
+    y64 = x64 * torch.rsqrt((x64 ** 2).mean(1, keepdim=True) + 1e-5) * w64
+    y64.backward(dy.double())
+    assert _off(y, y64) <= 2.0 ** -8 and _off(x.grad, x64.grad) <= 2.0 ** -8
+    assert _off(norm.w.grad, w64.grad) <= 1e-5
+    # a stream that is used alone: its gradient is x's and the residual's
+    r = torch.randn(33, 512, device="cuda", requires_grad=True)
+    x.grad = None
+    _, z = norm(x, r)
+    g = torch.randn_like(z)
+    z.backward(g)
+    assert torch.equal(r.grad, g) and torch.equal(x.grad, g.to(torch.bfloat16))
+    with pytest.raises(ValueError):
+        norm(x.float())
+    with pytest.raises(ValueError):
+        norm(x, r[:5])
+
+
+def test_layer_refuses_what_it_cannot_do():
+    for kw in (dict(n_group=3), dict(n_group=4, topk_group=5), dict(n_group=4, topk_group=1, k=5),
+               dict(group_rule="sum"), dict(gate_scale=0.0), dict(gate_scale=-1.0)):
+        a = dict(d=128, E=16, k=4, f=128)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            MoELayer(**a)
+    layer = MoELayer(128, 8, 2, 128)
+    x = torch.zeros(8, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="norm_eps"):
+        layer(x, x)
+
+
+@pytest.mark.parametrize("E,mode", [(16, ops.MODE_SIGMOID), (16, ops.MODE_SOFTMAX), (160, ops.MODE_SIGMOID)])
+def test_plan_step_in_a_graph_and_launch_count(E, mode):
+    """A captured step with grouped routing repeats the eager one bit for bit, and runs as many
+    kernels as the plan says."""
+    from torch.autograd import DeviceType
+    from torch.profiler import ProfilerActivity, profile
+    torch.manual_seed(E)
+    T, d, f, k = 260, 256, 128, 4
+    plan = MoEPlan(MoEShape(T, d, E, k, f, mode=mode, seq_len=T, n_group=4, topk_group=2, gate_scale=1.5))
+    dev = dict(device="cuda")
+    W = dict(W_r=torch.randn(E, d, **dev) / 16, W_g=torch.randn(E, f, d, **dev).to(torch.bfloat16) / 16,
+             W_u=torch.randn(E, f, d, **dev).to(torch.bfloat16) / 16,
+             W_d=torch.randn(E, d, f, **dev).to(torch.bfloat16) / 16)
+    b = torch.rand(E, **dev) * 0.1
+    x, dY = (torch.randn(T, d, **dev).to(torch.bfloat16) for _ in range(2))
+    graph = plan.capture_step(x, W, dY, b)
+    for _ in range(2):
+        x.copy_(torch.randn(T, d, **dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [plan.out.clone(), plan.topk_idx.clone(), *(t.clone() for t in plan.grads().values())]
+
+        def step():
+            plan.forward(x, W["W_r"], b, W["W_g"], W["W_u"], W["W_d"])
+            plan.backward(dY)
+        step()
+        torch.cuda.synchronize()
+        for a, t in zip(got, [plan.out, plan.topk_idx, *plan.grads().values()]):
+            assert torch.equal(a, t)
+    kernels = []
+    for _ in range(2):
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            step()
+            torch.cuda.synchronize()
+        kernels = [e.name for e in prof.events() if e.device_type == DeviceType.CUDA]
+        if kernels:
+            break
+    if kernels:
+        assert len([n for n in kernels if "moe::" in n]) == plan.launches_per_step()
+    # the plan's gradients clipped into buffers of an optimiser's own
+    g = {n: t.clone() for n, t in plan.grads().items() if n != "dx"}
+    out = {n: torch.full_like(t, float("nan")) for n, t in g.items()}
+    norm = plan.clip_grads(1e-3, out)
+    torch.cuda.synchronize()
+    total = float(torch.sqrt(sum((t.double() ** 2).sum() for t in g.values())))
+    assert abs(float(norm[0]) - total) <= 1e-5 * total
+    for n, t in g.items():
+        assert torch.equal(plan.grads()[n], t)  # untouched
+        assert _off(out[n], t.double() * (1e-3 / total)) <= 2.0 ** -8
+    with pytest.raises(ValueError):
+        plan.clip_grads(1.0, {"dW_r": out["dW_r"]})
