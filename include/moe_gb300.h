@@ -563,7 +563,7 @@ int moe_permute_bwd(const moe_bf16* dX_perm, const int32_t* slot_to_row,
  *      (both or neither); rstd [T] fp32 or NULL (moe_rms_norm_bwd needs it). y may be NULL
  *      where the codes are asked for.
  * d % 8 == 0, d <= 32768 (not a multiple of 128 as elsewhere); x, residual, w, z, y 16-byte
- * aligned, yq 8-byte aligned.
+ * aligned (an fp32 residual and z 32-byte aligned), yq 8-byte aligned.
  */
 int moe_rms_norm(const moe_bf16* x, const void* residual, int res_type, const float* w,
                  float eps, int64_t T, int d, void* z, moe_bf16* y, uint8_t* yq, float* sy,
@@ -579,7 +579,8 @@ int moe_rms_norm(const moe_bf16* x, const void* residual, int res_type, const fl
  *      rstd [T] from moe_rms_norm; w [d] fp32.
  * Out: dz [T,d] of res_type (may be dres's own buffer); dx [T,d] bf16 or NULL: the same
  *      gradient as bf16, for x beside an fp32 residual; dw [d] fp32.
- * Sizes and alignment as moe_rms_norm. Scratch: ws (moe_workspace_bytes).
+ * Sizes and alignment as moe_rms_norm (fp32 z, dres and dz 32-byte aligned). Scratch: ws
+ * (moe_workspace_bytes).
  */
 int moe_rms_norm_bwd(const moe_bf16* dy, const void* dres, const void* z, int res_type,
                      const float* rstd, const float* w, int64_t T, int d, void* dz, moe_bf16* dx,

@@ -42,7 +42,22 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// fp32 streams in one 32-byte access each: two 16-byte ones would touch every sector twice.
+__device__ __forceinline__ void load8_stream(const float* p, float (&v)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                   "=f"(v[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void load8_stream(const __nv_bfloat16* p, float (&v)[8]) { load8(p, v); }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// The library's own sums (shared or global memory, 16-byte aligned).
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
@@ -73,14 +88,14 @@ __device__ __forceinline__ void row_reduce(float& s, float& m, float2* red, int 
     }
 }
 
-__device__ __forceinline__ float row_reduce(float s, float* red, int nwarps) {
+__device__ __forceinline__ float row_reduce(float s, float2* red, int nwarps) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (nwarps == 1) return s;
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32].x = s;
     __syncthreads();
-    s = red[0];
-    for (int i = 1; i < nwarps; ++i) s += red[i];
+    s = red[0].x;
+    for (int i = 1; i < nwarps; ++i) s += red[i].x;
     return s;
 }
 
@@ -104,7 +119,7 @@ __device__ __forceinline__ uint2 codes8_of(const float (&q)[8]) {
 // y = (z w) rstd, so the largest |y| is rstd times the largest |z w|, which is known together with
 // the sum of squares: one reduction, one barrier. In the quotient of the codes rstd cancels:
 // y / sy = z w (448 / max |z w|), a product with one factor per row.
-template <typename R, int VPT>
+template <typename R, int VPT, bool CODES>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(
     const __nv_bfloat16* x, const R* res, const float* __restrict__ w, float eps, int64_t T, int d,
     R* z_out, __nv_bfloat16* y, uint8_t* __restrict__ yq, float* __restrict__ sy,
@@ -124,7 +139,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(
         load8(w + 8 * c, wv);
         if (res) {
             float r[8];
-            load8(res + t * d + 8 * c, r);
+            load8_stream(res + t * d + 8 * c, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[i][j] = stored(z[i][j] + r[j], res);
             store8(z_out + t * d + 8 * c, z[i]);
@@ -133,13 +148,16 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(
         for (int j = 0; j < 8; ++j) {
             ss = fmaf(z[i][j], z[i][j], ss);
             z[i][j] *= wv[j];
-            top = fmaxf(top, fabsf(z[i][j]));
+            if (CODES) top = fmaxf(top, fabsf(z[i][j]));
         }
     }
-    row_reduce(ss, top, red, nwarps);
+    if (CODES)
+        row_reduce(ss, top, red, nwarps);
+    else
+        ss = row_reduce(ss, red, nwarps);
     const float rstd = 1.0f / sqrtf(ss / (float)d + eps);
     if (rstd_out && threadIdx.x == 0) rstd_out[t] = rstd;
-    if (yq) {
+    if (CODES) {
         // rows of values near zero take a power of two out first: 448 / top stays finite
         const float up = top < 1e-30f ? 1.2676506e30f : 1.f;  // 2^100
         const float f = top > 0.f ? __fdiv_rn(448.f, top * up) : 0.f;
@@ -177,47 +195,46 @@ __device__ __forceinline__ void cp_wait() {
 
 // One row per CTA and step; CTA b takes the rows b, b + gridDim.x, ... Each thread copies its own
 // vectors of the next rows to shared memory (STAGES - 1 rows ahead, no barrier: it reads
-// only what it copied itself), so loads stay in flight across the row's reduction. It keeps the
+// only what its own warp copied), so loads stay in flight across the row's reduction. It keeps the
 // partial sums of dw for its own columns over all rows, so dw costs no traffic per row: the CTA's
 // sums are written once, and norm_dw_kernel adds them in the CTAs' order.
 template <typename R, int VPT, int STAGES>
-__global__ void __launch_bounds__(VPT == 1 ? 256 : 512) norm_bwd_kernel(
+__global__ void __launch_bounds__(512) norm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const R* dres, const R* __restrict__ z,
     const float* __restrict__ rstd, const float* __restrict__ w, int64_t T, int d, R* dz,
     __nv_bfloat16* __restrict__ dx, float* __restrict__ part) {
     constexpr int RW = sizeof(R) / 2;  // 16-byte words of a vector of R
     constexpr int SLOTS = VPT * (1 + 2 * RW);
-    extern __shared__ __align__(16) uint4 ring[];  // [stage][slot][thread]
-    __shared__ float red[2][32];
-    const int nvec = d / 8, nwarps = blockDim.x / 32, nt = blockDim.x;
-    auto slot = [&](int stage, int k) { return ring + ((stage * SLOTS + k) * nt + threadIdx.x); };
+    extern __shared__ __align__(16) uint4 ring[];  // [stage][vector of a thread][dy | z | dres][thread]
+    __shared__ float2 red[2][32];
+    const int nvec = d / 8, nwarps = blockDim.x / 32, nt = blockDim.x, lane = threadIdx.x % 32;
+    auto area = [&](int stage, int i, int which) {  // of dy, z, dres: one, RW and RW words per thread
+        return ring + (stage * SLOTS + i * (1 + 2 * RW) + (which == 0 ? 0 : which == 1 ? 1 : 1 + RW)) * nt;
+    };
     auto fetch = [&](int64_t t, int stage) {
         if (t < T) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = threadIdx.x + i * nt;
-                if (c >= nvec) continue;
-                const int64_t at = t * d + 8 * c;
-                const int k = i * (1 + 2 * RW);
-                cp16(slot(stage, k), dy + at);
+                const int c0 = threadIdx.x - lane + i * nt;  // the warp's first vector
+                if (c0 + lane < nvec) cp16(area(stage, i, 0) + threadIdx.x, dy + t * d + 8 * (c0 + lane));
 #pragma unroll
                 for (int q = 0; q < RW; ++q) {
-                    cp16(slot(stage, k + 1 + q), reinterpret_cast<const uint4*>(z + at) + q);
-                    if (dres) cp16(slot(stage, k + 1 + RW + q), reinterpret_cast<const uint4*>(dres + at) + q);
+                    const int word = lane + 32 * q;  // of the warp's vectors: whole lines per copy
+                    if (c0 + word / RW >= nvec) continue;
+                    const int to = (threadIdx.x - lane) * RW + word;
+                    cp16(area(stage, i, 1) + to, reinterpret_cast<const uint4*>(z + t * d + 8 * c0) + word);
+                    if (dres)
+                        cp16(area(stage, i, 2) + to, reinterpret_cast<const uint4*>(dres + t * d + 8 * c0) + word);
                 }
             }
         }
         cp_commit();
     };
-    auto value8 = [&](int stage, int k, auto* type, float (&v)[8]) {
-        using S = std::remove_pointer_t<decltype(type)>;
-        if constexpr (sizeof(S) == 2) {
-            load8(reinterpret_cast<const S*>(slot(stage, k)), v);
+    auto value8 = [&](const uint4* a, float (&v)[8]) {  // the thread's vector of R
+        if constexpr (RW == 1) {
+            load8(reinterpret_cast<const __nv_bfloat16*>(a + threadIdx.x), v);
         } else {
-            const float4 a = *reinterpret_cast<const float4*>(slot(stage, k));
-            const float4 b = *reinterpret_cast<const float4*>(slot(stage, k + 1));
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            load8(reinterpret_cast<const float*>(a + 2 * threadIdx.x), v);
         }
     };
     float acc[VPT][8], wv[VPT][8];
@@ -234,8 +251,10 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : 512) norm_bwd_kernel(
     float rs = blockIdx.x < T ? rstd[blockIdx.x] : 0.f;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x, side ^= 1) {
         const int ahead = stage == 0 ? STAGES - 1 : stage - 1;
+        __syncwarp();  // the warp is done with that stage's row
         fetch(t + (int64_t)(STAGES - 1) * gridDim.x, ahead);
         cp_wait<STAGES - 1>();
+        __syncwarp();  // a thread's vectors of R are copied by its warp
         const float rs_next = t + gridDim.x < T ? rstd[t + gridDim.x] : 0.f;
         float g[VPT][8], h[VPT][8];  // dy w and xhat
         float dot = 0.f;
@@ -243,8 +262,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : 512) norm_bwd_kernel(
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * nt;
             if (c >= nvec) continue;
-            value8(stage, i * (1 + 2 * RW), (__nv_bfloat16*)nullptr, g[i]);
-            value8(stage, i * (1 + 2 * RW) + 1, (R*)nullptr, h[i]);
+            load8(reinterpret_cast<const __nv_bfloat16*>(area(stage, i, 0) + threadIdx.x), g[i]);
+            value8(area(stage, i, 1), h[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 h[i][j] *= rs;
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : 512) norm_bwd_kernel(
             if (c >= nvec) continue;
             float o[8];
             if (dres) {
-                value8(stage, i * (1 + 2 * RW) + 1 + RW, (R*)nullptr, o);
+                value8(area(stage, i, 2), o);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = 0.f;
@@ -277,7 +296,124 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : 512) norm_bwd_kernel(
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = threadIdx.x + i * nt;
-        if (c < nvec) store8(part + (int64_t)blockIdx.x * d + 8 * c, acc[i]);
+        if (c < nvec) put8(part + (int64_t)blockIdx.x * d + 8 * c, acc[i]);
+    }
+}
+
+// Rows of up to 1024 columns: a warp each, so that a row needs no barrier. The warp copies its own
+// next rows ahead and reads a row from shared memory twice, for the dot product and for the
+// gradient, instead of holding 64 values a thread across the reduction. The CTA's warps add their
+// sums of dw in their order at the end.
+constexpr int kRowWarps = 4;
+
+template <typename R, int VPT, int STAGES>
+__global__ void __launch_bounds__(32 * kRowWarps) norm_bwd_rows_kernel(
+    const __nv_bfloat16* __restrict__ dy, const R* dres, const R* __restrict__ z,
+    const float* __restrict__ rstd, const float* __restrict__ w, int64_t T, int d, R* dz,
+    __nv_bfloat16* __restrict__ dx, float* __restrict__ part) {
+    constexpr int RW = sizeof(R) / 2;  // 16-byte words of a vector of R
+    constexpr int VW = 1 + 2 * RW;     // of a vector of all three tensors
+    extern __shared__ __align__(16) uint4 ring[];  // [warp][stage][vector][dy | z | dres]; then sums of dw
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int nvec = d / 8;
+    auto area = [&](int stage, int i, int which) {
+        return ring + (((warp * STAGES + stage) * VPT + i) * VW + (which == 0 ? 0 : which == 1 ? 1 : 1 + RW)) * 32;
+    };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < T) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (lane + 32 * i < nvec) cp16(area(stage, i, 0) + lane, dy + t * d + 8 * (lane + 32 * i));
+#pragma unroll
+                for (int q = 0; q < RW; ++q) {
+                    const int word = lane + 32 * q;  // whole lines per copy
+                    if (32 * i + word / RW >= nvec) continue;
+                    const int64_t at = t * d + 256 * i;
+                    cp16(area(stage, i, 1) + word, reinterpret_cast<const uint4*>(z + at) + word);
+                    if (dres) cp16(area(stage, i, 2) + word, reinterpret_cast<const uint4*>(dres + at) + word);
+                }
+            }
+        }
+        cp_commit();
+    };
+    auto value8 = [&](const uint4* a, float (&v)[8]) {  // the lane's vector of R
+        if constexpr (RW == 1) {
+            load8(reinterpret_cast<const __nv_bfloat16*>(a + lane), v);
+        } else {
+            load8(reinterpret_cast<const float*>(a + 2 * lane), v);
+        }
+    };
+    const int64_t first = (int64_t)blockIdx.x * kRowWarps + warp, stride = (int64_t)gridDim.x * kRowWarps;
+#pragma unroll
+    for (int q = 0; q < STAGES - 1; ++q) fetch(first + q * stride, q);
+    float acc[VPT][8], wv[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + 32 * i;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = wv[i][j] = 0.f;
+        if (c < nvec) load8(w + 8 * c, wv[i]);
+    }
+    const float inv_d = 1.0f / (float)d;
+    int stage = 0;
+    float rs = first < T ? rstd[first] : 0.f;
+    for (int64_t t = first; t < T; t += stride) {
+        const int ahead = stage == 0 ? STAGES - 1 : stage - 1;
+        __syncwarp();  // every lane is done with that stage's row
+        fetch(t + (STAGES - 1) * stride, ahead);
+        cp_wait<STAGES - 1>();
+        __syncwarp();
+        const float rs_next = t + stride < T ? rstd[t + stride] : 0.f;
+        float dot = 0.f;  // of dy w and z: rstd comes after the sum
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (lane + 32 * i >= nvec) continue;
+            float g[8], h[8];
+            load8(reinterpret_cast<const __nv_bfloat16*>(area(stage, i, 0) + lane), g);
+            value8(area(stage, i, 1), h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = g[j] * h[j];
+                acc[i][j] = fmaf(p, rs, acc[i][j]);
+                dot = fmaf(p, wv[i][j], dot);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        const float c1 = -(dot * rs) * inv_d * rs;  // dz = rs (dy w + c1 z) + dres
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + 32 * i;
+            if (c >= nvec) continue;
+            float g[8], h[8], o[8];
+            load8(reinterpret_cast<const __nv_bfloat16*>(area(stage, i, 0) + lane), g);
+            value8(area(stage, i, 1), h);
+            if (dres) {
+                value8(area(stage, i, 2), o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = fmaf(fmaf(c1, h[j], g[j] * wv[i][j]), rs, o[j]);
+            store8(dz + t * d + 8 * c, o);
+            if (dx) store8(dx + t * d + 8 * c, o);
+        }
+        rs = rs_next;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+    __syncthreads();  // the rings are done with
+    float* const sums = reinterpret_cast<float*>(ring);  // [warp][d]
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        if (lane + 32 * i < nvec) put8(sums + warp * d + 8 * (lane + 32 * i), acc[i]);
+    __syncthreads();
+    for (int j = threadIdx.x; j < d; j += 32 * kRowWarps) {
+        float a = sums[j];
+#pragma unroll
+        for (int q = 1; q < kRowWarps; ++q) a += sums[q * d + j];
+        part[(int64_t)blockIdx.x * d + j] = a;
     }
 }
 
@@ -287,7 +423,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
     const __nv_bfloat16* __restrict__ dy, const R* dres, const R* __restrict__ z,
     const float* __restrict__ rstd, const float* __restrict__ w, int64_t T, int d, R* dz,
     __nv_bfloat16* __restrict__ dx, float* __restrict__ part) {
-    __shared__ float red[2][32];
+    __shared__ float2 red[2][32];
     const int nvec = d / 8, nwarps = blockDim.x / 32;
     float* sums = part + (int64_t)blockIdx.x * d;  // the CTA's own row, in global memory
     int side = 0;
@@ -301,7 +437,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
             if (c >= nvec) continue;
             float g[8], h[8], wv[8], a[8];
             load8(dy + t * d + 8 * c, g);
-            load8(z + t * d + 8 * c, h);
+            load8_stream(z + t * d + 8 * c, h);
             load8(w + 8 * c, wv);
             if (begun) load8(sums + 8 * c, a);
 #pragma unroll
@@ -310,7 +446,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
                 a[j] = fmaf(g[j], h[j], begun ? a[j] : 0.f);
                 dot = fmaf(g[j] * wv[j], h[j], dot);
             }
-            store8(sums + 8 * c, a);
+            put8(sums + 8 * c, a);
         }
         dot = row_reduce(dot, red[side], nwarps) / (float)d;
 #pragma unroll
@@ -319,10 +455,10 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
             if (c >= nvec) continue;
             float g[8], h[8], wv[8], o[8];
             load8(dy + t * d + 8 * c, g);
-            load8(z + t * d + 8 * c, h);
+            load8_stream(z + t * d + 8 * c, h);
             load8(w + 8 * c, wv);
             if (dres) {
-                load8(dres + t * d + 8 * c, o);
+                load8_stream(dres + t * d + 8 * c, o);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = 0.f;
@@ -335,39 +471,58 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
     }
 }
 
-// dw[j] = sum of part[r][j] over r < rows: blocks of 32 columns (eight 16-byte vectors) x 32 row
-// strands, each strand summed in order, then the strands in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int rows,
-                                                      int d, float* __restrict__ dw) {
-    __shared__ float s[32][33];
+// dw[j] = sum of part[r][j] over r < rows: blocks of 32 columns (eight 16-byte vectors) x 128 row
+// strands, each strand summed in order, then the strands by a tree. The few rows of a strand
+// are loaded together: the launch is all latency.
+constexpr int kDwStrands = 128;
+
+__global__ void __launch_bounds__(8 * kDwStrands) norm_dw_kernel(const float* __restrict__ part, int rows,
+                                                                 int d, float* __restrict__ dw) {
+    constexpr int N = (kNormBwdParts + kDwStrands - 1) / kDwStrands;
+    __shared__ float s[kDwStrands][33];
     const int tx = threadIdx.x % 8, ty = threadIdx.x / 8;
     const int j = blockIdx.x * 32 + 4 * tx;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < d) {  // d is a multiple of 8
-#pragma unroll 4
-        for (int r = ty; r < rows; r += 32) {
-            const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)r * d + j);
-            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-        }
+    float4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = ty + i * kDwStrands;
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && j < d)  // d is a multiple of 8
+            v[i] = *reinterpret_cast<const float4*>(part + (int64_t)r * d + j);
     }
+    float4 a = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) a.x += v[i].x, a.y += v[i].y, a.z += v[i].z, a.w += v[i].w;
     s[ty][4 * tx] = a.x, s[ty][4 * tx + 1] = a.y, s[ty][4 * tx + 2] = a.z, s[ty][4 * tx + 3] = a.w;
     __syncthreads();
-    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < d) {
-        float t = 0.f;
+    // a warp per column: four strands a lane, then the lanes by a butterfly
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float t = 0.f;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) t += s[q][threadIdx.x];
-        dw[blockIdx.x * 32 + threadIdx.x] = t;
-    }
+    for (int q = 0; q < kDwStrands / 32; ++q) t += s[lane + 32 * q][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = t;
 }
+static_assert(8 * kDwStrands == 32 * 32, "a warp per column");
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 struct NormShape {
     int threads, vpt;
 };
 
-// Threads of one row, and vectors of eight values per thread.
-NormShape norm_shape(int d) {
+// Threads of one row and vectors of eight values per thread (1, 2 or 4). Many rows: four vectors
+// each, so that few threads share the reduction's and the row's fixed work (8191 x 1024: 13.6 us
+// at a warp a row, 14.1 at 128 threads). Few rows, where a row's latency counts: as many threads
+// as there are vectors (one row of 4096 with codes: 2.4 us, 2.6 at two vectors each).
+NormShape norm_shape(int64_t T, int d) {
     const int nvec = d / 8;
-    const int vpt = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+    int vpt = 1;
+    if (T >= 2 * (int64_t)sm_count())
+        while (vpt < 4 && 32 * vpt < nvec) vpt *= 2;
+    else
+        while (vpt < 4 && 1024 * vpt < nvec) vpt *= 2;
     return {(int)cdiv(cdiv(nvec, vpt), 32) * 32, vpt};
 }
 
@@ -375,8 +530,8 @@ template <typename R>
 int launch_norm_fwd(const moe_bf16* x, const void* res, const float* w, float eps, int64_t T, int d,
                     void* z_out, moe_bf16* y, uint8_t* yq, float* sy, float* rstd,
                     cudaStream_t st) {
-    const NormShape s = norm_shape(d);
-    const int rows = s.threads == 32 ? 8 : 1;
+    const NormShape s = norm_shape(T, d);
+    const int rows = s.threads == 32 ? 4 : 1;
     const dim3 block(s.threads, rows);
     const unsigned grid = (unsigned)cdiv(T, rows);
     auto go = [&](auto kern) {
@@ -385,13 +540,32 @@ int launch_norm_fwd(const moe_bf16* x, const void* res, const float* w, float ep
                                      static_cast<R*>(z_out), reinterpret_cast<__nv_bfloat16*>(y),
                                      yq, sy, rstd);
     };
-    if (s.vpt == 1) go(norm_fwd_kernel<R, 1>);
-    else if (s.vpt == 2) go(norm_fwd_kernel<R, 2>);
-    else go(norm_fwd_kernel<R, 4>);
+    if (s.vpt == 1) yq ? go(norm_fwd_kernel<R, 1, true>) : go(norm_fwd_kernel<R, 1, false>);
+    else if (s.vpt == 2) yq ? go(norm_fwd_kernel<R, 2, true>) : go(norm_fwd_kernel<R, 2, false>);
+    else yq ? go(norm_fwd_kernel<R, 4, true>) : go(norm_fwd_kernel<R, 4, false>);
     return launch_status();
 }
 
 constexpr size_t kRingBytes = 104 * 1024;  // the deepest ring that leaves room for two CTAs per SM
+
+template <typename R, int VPT>
+int launch_bwd_rows(const __nv_bfloat16* dy, const R* dres, const R* z, const float* rstd, const float* w,
+                    int64_t T, int d, R* dz, __nv_bfloat16* dx, float* part, int* rows, cudaStream_t st) {
+    constexpr int STAGES = 3;
+    size_t smem = (size_t)kRowWarps * STAGES * VPT * (1 + sizeof(R)) * 32 * 16;
+    const size_t sums = (size_t)kRowWarps * d * sizeof(float);
+    if (sums > smem) smem = sums;
+    auto kern = norm_bwd_rows_kernel<R, VPT, STAGES>;
+    if (smem > 40 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MOE_ERR_LAUNCH;
+    int64_t ctas = (size_t)(224 * 1024) / (smem + 1024);  // per SM
+    if (ctas > 4) ctas = 4;
+    *rows = (int)norm_bwd_parts(cdiv(T, kRowWarps));
+    if (*rows > ctas * sm_count()) *rows = (int)(ctas * sm_count());
+    kern<<<*rows, 32 * kRowWarps, smem, st>>>(dy, dres, z, rstd, w, T, d, dz, dx, part);
+    return launch_status();
+}
 
 template <typename R, int VPT, int STAGES>
 int launch_bwd(const __nv_bfloat16* dy, const R* dres, const R* z, const float* rstd, const float* w,
@@ -419,29 +593,29 @@ int launch_norm_bwd(const moe_bf16* dy_, const void* dres_, const void* z_, cons
     auto* dx = reinterpret_cast<__nv_bfloat16*>(dx_);
     auto *dres = static_cast<const R*>(dres_), *z = static_cast<const R*>(z_);
     auto* dz = static_cast<R*>(dz_);
-    const NormShape s = norm_shape(d);
-    const size_t row = (size_t)s.vpt * (1 + sizeof(R)) * 16 * s.threads;  // ring bytes of one row
+    const int nvec = d / 8;
     int rc, rows = 0;
-    if (s.vpt == 4) {
-        rows = (int)norm_bwd_parts(T);
-        norm_bwd_wide_kernel<R, 4><<<rows, s.threads, 0, st>>>(dy, dres, z, rstd, w, T, d, dz, dx, part);
-        rc = launch_status();
-    } else {
-        auto go = [&](auto vpt, auto stages) {
-            return launch_bwd<R, decltype(vpt)::value, decltype(stages)::value>(
-                dy, dres, z, rstd, w, T, d, s.threads, dz, dx, part, &rows, st);
+    using std::integral_constant;
+    if (nvec <= 128) {
+        rc = nvec <= 32   ? launch_bwd_rows<R, 1>(dy, dres, z, rstd, w, T, d, dz, dx, part, &rows, st)
+             : nvec <= 64 ? launch_bwd_rows<R, 2>(dy, dres, z, rstd, w, T, d, dz, dx, part, &rows, st)
+                          : launch_bwd_rows<R, 4>(dy, dres, z, rstd, w, T, d, dz, dx, part, &rows, st);
+    } else if (nvec <= 1024) {
+        const int threads = (int)cdiv(cdiv(nvec, 2), 32) * 32;
+        const bool deep = 4 * 2 * (1 + sizeof(R)) * 16 * threads <= kRingBytes;
+        auto go = [&](auto stages) {
+            return launch_bwd<R, 2, decltype(stages)::value>(dy, dres, z, rstd, w, T, d, threads, dz, dx,
+                                                             part, &rows, st);
         };
-        const bool deep = 4 * row <= kRingBytes;
-        using std::integral_constant;
-        if (s.vpt == 1)
-            rc = deep ? go(integral_constant<int, 1>(), integral_constant<int, 4>())
-                      : go(integral_constant<int, 1>(), integral_constant<int, 2>());
-        else
-            rc = deep ? go(integral_constant<int, 2>(), integral_constant<int, 4>())
-                      : go(integral_constant<int, 2>(), integral_constant<int, 2>());
+        rc = deep ? go(integral_constant<int, 4>()) : go(integral_constant<int, 2>());
+    } else {
+        rows = (int)norm_bwd_parts(T);
+        norm_bwd_wide_kernel<R, 4><<<rows, (unsigned)cdiv(cdiv(nvec, 4), 32) * 32, 0, st>>>(
+            dy, dres, z, rstd, w, T, d, dz, dx, part);
+        rc = launch_status();
     }
     if (rc != MOE_OK) return rc;
-    norm_dw_kernel<<<(unsigned)cdiv(d, 32), 256, 0, st>>>(part, rows, d, dw);
+    norm_dw_kernel<<<(unsigned)cdiv(d, 32), 8 * kDwStrands, 0, st>>>(part, rows, d, dw);
     return launch_status();
 }
 
@@ -462,6 +636,7 @@ extern "C" int moe_rms_norm(const moe_bf16* x, const void* residual, int res_typ
     for (const void* p : {(const void*)x, residual, (const void*)w, (const void*)z, (const void*)y})
         if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
     if (yq && (reinterpret_cast<uintptr_t>(yq) & 7u)) return MOE_ERR_INVALID_ARG;
+    if (res_type == MOE_TYPE_F32 && (!aligned32(residual) || !aligned32(z))) return MOE_ERR_INVALID_ARG;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
     return res_type == MOE_TYPE_F32
@@ -479,6 +654,7 @@ extern "C" int moe_rms_norm_bwd(const moe_bf16* dy, const void* dres, const void
     if (d % 8 != 0 || d > kNormMaxD || T > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     for (const void* p : {(const void*)dy, dres, z, (const void*)w, (const void*)dz, (const void*)dx})
         if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (res_type == MOE_TYPE_F32 && (!aligned32(dres) || !aligned32(z) || !aligned32(dz))) return MOE_ERR_INVALID_ARG;
     if (!ws || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     WsCarver wc(ws, ws_bytes);
     float* part = wc.take<float>((size_t)norm_bwd_parts(T) * d);
