@@ -34,6 +34,25 @@ inline int launch_status() {
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
+// Launches a kernel that may start while the stream's previous one still runs (programmatic
+// dependent launch): it must call grid_dependency_wait() before it touches what that one writes
+// or reads. The two share the launch's latency, about 1 us per pair of short kernels.
+template <typename... P, typename... A>
+inline int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                            A&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<A&&>(args)...) == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Scratch carving: consecutive 256-byte aligned regions of the caller's workspace.
@@ -51,6 +70,17 @@ struct WsCarver {
 };
 
 // ----------------------------------------------------------------- device-side helpers
+
+// Waits until the kernels this one was launched behind (launch_dependent) have completed, their
+// writes visible.
+__device__ __forceinline__ void grid_dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets a kernel launched behind this one be set up already. The last CTA's call (or end) counts,
+// so every CTA of this grid has its place by then.
+__device__ __forceinline__ void grid_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 __device__ __forceinline__ void record_error(int* status, int code, int site) {
     if (atomicCAS(status, 0, code) == 0) status[1] = site;

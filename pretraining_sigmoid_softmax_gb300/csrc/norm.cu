@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
+    grid_launch_dependents();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = threadIdx.x + i * nt;
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) norm_bwd_rows_kernel(
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
+    grid_launch_dependents();
     __syncthreads();  // the rings are done with
     float* const sums = reinterpret_cast<float*>(ring);  // [warp][d]
 #pragma unroll
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(8 * kDwStrands) norm_dw_kernel(const float* __
     const int tx = threadIdx.x % 8, ty = threadIdx.x / 8;
     const int j = blockIdx.x * 32 + 4 * tx;
     float4 v[N];
+    grid_dependency_wait();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int r = ty + i * kDwStrands;
@@ -615,8 +618,8 @@ int launch_norm_bwd(const moe_bf16* dy_, const void* dres_, const void* z_, cons
         rc = launch_status();
     }
     if (rc != MOE_OK) return rc;
-    norm_dw_kernel<<<(unsigned)cdiv(d, 32), 8 * kDwStrands, 0, st>>>(part, rows, d, dw);
-    return launch_status();
+    return launch_dependent(norm_dw_kernel, dim3((unsigned)cdiv(d, 32)), dim3(8 * kDwStrands), 0, st,
+                            (const float*)part, rows, d, dw);
 }
 
 }  // namespace

@@ -507,22 +507,33 @@ def moe_select_experts_bwd(dg, topk_idx, topk_score, logits, lse, mode, renorm, 
 
 
 def _grad_list(name, ts, dev):
-    """Host arrays of a list of gradients: pointers, element counts, types."""
-    n = len(ts)
-    ptr, numel, types = [0] * n, [0] * n, [0] * n
-    for i, t in enumerate(ts):
+    """Pointers, element counts and types of a list of gradients."""
+    ptr, numel, types = [], [], []
+    for t in ts:
         rt = _TYPES.get(t.dtype)
-        if rt is None:
-            raise MoEError(f"{name}[{i}] must be bf16 or fp32, got {t.dtype}")
-        ptr[i], numel[i], types[i] = _ptr(f"{name}[{i}]", t, t.dtype, t.shape, dev), t.numel(), rt
-    return (ctypes.c_void_p * n)(*ptr), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types)
+        if rt is None or t.get_device() != dev or not t.is_contiguous():
+            at = f"{name}[{len(ptr)}]"
+            if rt is None:
+                raise MoEError(f"{at} must be bf16 or fp32, got {t.dtype}")
+            _ptr(at, t, t.dtype, t.shape, dev)  # says what is wrong
+        ptr.append(t.data_ptr())
+        numel.append(t.numel())
+        types.append(rt)
+    return ptr, numel, types
+
+
+def _clip_args(grads, dev):
+    """_grad_list as host arrays for the library, and the lists."""
+    ptr, numel, types = lists = _grad_list("grads", grads, dev)
+    n = len(ptr)
+    return (ctypes.c_void_p * n)(*ptr), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), lists
 
 
 def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
     """norm[0] = the global 2-norm of a list of bf16 or fp32 gradients, norm[1] = the factor that
     clips it to max_norm."""
     dev = _device(norm)
-    ptr, numel, types = _grad_list("grads", grads, dev)
+    ptr, numel, types, _ = _clip_args(grads, dev)
     wp, wn = _ws(ws, dev)
     _check(_lib.load().moe_grad_norm(ptr, numel, types, len(grads), max_norm,
                                      _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
@@ -532,13 +543,15 @@ def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
 def moe_clip_grads(grads, max_norm, out, norm, ws, stream=None):
     """moe_grad_norm, and out[i] = norm[1] * grads[i]; out None clips in place."""
     dev = _device(norm)
-    ptr, numel, types = _grad_list("grads", grads, dev)
+    ptr, numel, types, lists = _clip_args(grads, dev)
     optr = ptr
     if out is not None:
         if len(out) != len(grads):
             raise MoEError(f"{len(grads)} gradients, but {len(out)} outputs")
-        optr = (ctypes.c_void_p * len(out))(*[_ptr(f"out[{i}]", o, t.dtype, t.shape, dev)
-                                              for i, (t, o) in enumerate(zip(grads, out))])
+        o = _grad_list("out", out, dev)
+        if o[1:] != lists[1:]:
+            raise MoEError("every output must have its gradient's type and number of elements")
+        optr = (ctypes.c_void_p * len(out))(*o[0])
     wp, wn = _ws(ws, dev)
     _check(_lib.load().moe_clip_grads(ptr, optr, numel, types, len(grads), max_norm,
                                       _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
