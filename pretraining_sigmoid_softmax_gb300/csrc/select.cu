@@ -806,87 +806,127 @@ struct SelectBwdParams {
     int* status;
 };
 
-template <int L>
+template <int L, bool DENSE>
 __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const SelectBwdParams P) {
     constexpr int NT = 32 / L;
     extern __shared__ __align__(16) float rows[];
+    __shared__ float token_c[kSelWarps][NT], token_lse[kSelWarps][NT];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, k = P.k;
     // one warp's rows; a multiple of 16 bytes
     float* row = rows + (size_t)warp * ((NT * E + 3) / 4 * 4);
-    const int64_t t0 = ((int64_t)blockIdx.x * kSelWarps + warp) * NT;
-    if (t0 >= P.T) return;  // whole warp
-    const int64_t t = t0 + lane / L;
-    const int n = (int)min((int64_t)NT, P.T - t0) * E;  // elements of the warp's tokens
     const bool softmax = P.mode == MOE_MODE_SOFTMAX;
-    const bool dense = softmax && (!P.renorm || P.z_scale != 0.f);
-    for (int i = 4 * lane; i < n; i += 128)
-        *reinterpret_cast<float4*>(row + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t stride = (int64_t)gridDim.x * kSelWarps * NT;
     int e = -1;
-    float s = 0.f, dg = 0.f;
-    if (t < P.T && sub < k) {
-        e = P.idx[t * k + sub];
-        if (e < 0 || e >= E) {  // the slot is dropped
-            record_error(P.status, MOE_ERR_BAD_INDEX, kSiteSelectBwd);
-            e = -1;
-        } else {
+    float s = 0.f, dg = 0.f, lse = 0.f;
+    auto load = [&](int64_t t0) {  // a token's slots, ahead of their use
+        const int64_t t = t0 + lane / L;
+        e = -1;
+        s = dg = 0.f;
+        if (t < P.T && sub < k) {
+            e = P.idx[t * k + sub];
             s = P.score[t * k + sub];
             dg = P.dg[t * k + sub];
         }
-    }
-    float ds = P.scale * dg;
-    if (P.renorm) {
-        const float S = seg_sum<L>(s);
-        const float m = seg_sum<L>(s / S * dg);
-        ds = S == 0.f ? 0.f : P.scale / S * (dg - m);
-    }
-    float c = 0.f;
-    if (softmax && !P.renorm) c = seg_sum<L>(s * ds);
-    float v = dense ? ds : softmax ? ds * s : ds * s * (1.f - s);
-    // an expert named twice in a token gets its slots' terms summed in slot order, by the first
-    const uint32_t same = __match_any_sync(kFull, e < 0 ? -1 - lane : lane / L * E + e);
-    if (__any_sync(kFull, (same & (same - 1)) != 0)) {
-        float sum = 0.f;
-        for (int i = 0; i < 32; ++i) {
-            const float o = __shfl_sync(kFull, v, i);
-            if ((same >> i) & 1u) sum += o;
+        if (DENSE && t < P.T && sub == 0) lse = P.lse[t];
+    };
+    int64_t t0 = ((int64_t)blockIdx.x * kSelWarps + warp) * NT;
+    load(t0);
+    for (; t0 < P.T; t0 += stride) {
+        const int n = (int)min((int64_t)NT, P.T - t0) * E;  // elements of the warp's tokens
+        for (int i = 4 * lane; i < n; i += 128)
+            *reinterpret_cast<float4*>(row + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t0 + lane / L < P.T && sub < k && (e < 0 || e >= E)) {  // the slot is dropped
+            record_error(P.status, MOE_ERR_BAD_INDEX, kSiteSelectBwd);
+            e = -1;
+            s = dg = 0.f;
         }
-        v = sum;
-        if ((same & ((1u << lane) - 1u)) != 0) e = -1;
-    }
-    __syncwarp();
-    if (e >= 0) row[lane / L * E + e] = v;
-    __syncwarp();
-    float* out = P.dlogits + t0 * E;
-    const float* extra = P.extra ? P.extra + t0 * E : nullptr;
-    if (dense) {
-        const float* l = P.logits + t0 * E;
-        for (int q = 0; q * E < n; ++q) {
-            const float l_se = P.lse[t0 + q];
-            const float cq = __shfl_sync(kFull, c, q * L);
-            const float zl = P.z_scale * l_se;
-            for (int i = q * E + lane; i < (q + 1) * E; i += 32) {
-                float g = 0.f;
-                if (l_se != -INFINITY) {  // else no expert has a score
-                    const float p = expf(l[i] - l_se);
-                    g = p * (row[i] - cq) + zl * p;
-                }
-                out[i] = extra ? g + extra[i] : g;
+        float ds = P.scale * dg;
+        if (P.renorm) {
+            const float S = seg_sum<L>(s);
+            const float m = seg_sum<L>(s / S * dg);
+            ds = S == 0.f ? 0.f : P.scale / S * (dg - m);
+        }
+        if (DENSE) {
+            const float c = P.renorm ? 0.f : seg_sum<L>(s * ds);
+            if (sub == 0) {
+                token_c[warp][lane / L] = c;
+                token_lse[warp][lane / L] = lse;
             }
         }
-        return;
-    }
-    const bool vec = ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(extra)) & 15u) == 0;
-    const int nv = vec ? n / 4 * 4 : 0;
-    for (int i = 4 * lane; i < nv; i += 128) {
-        float4 g = *reinterpret_cast<const float4*>(row + i);
-        if (extra) {
-            const float4 x = *reinterpret_cast<const float4*>(extra + i);
-            g.x += x.x, g.y += x.y, g.z += x.z, g.w += x.w;
+        float v = DENSE ? ds : softmax ? ds * s : ds * s * (1.f - s);
+        // an expert named twice in a token gets its slots' terms summed in slot order, by the first
+        const uint32_t same = __match_any_sync(kFull, e < 0 ? -1 - lane : lane / L * E + e);
+        if (__any_sync(kFull, (same & (same - 1)) != 0)) {
+            float sum = 0.f;
+            for (int i = 0; i < 32; ++i) {
+                const float o = __shfl_sync(kFull, v, i);
+                if ((same >> i) & 1u) sum += o;
+            }
+            v = sum;
+            if ((same & ((1u << lane) - 1u)) != 0) e = -1;
         }
-        *reinterpret_cast<float4*>(out + i) = g;
+        __syncwarp();
+        if (e >= 0) row[lane / L * E + e] = v;
+        load(t0 + stride);
+        __syncwarp();
+        float* out = P.dlogits + t0 * E;
+        const float* extra = P.extra ? P.extra + t0 * E : nullptr;
+        const float* l = DENSE ? P.logits + t0 * E : nullptr;
+        auto token_of = [&](int i) {
+            int q = 0;
+#pragma unroll
+            for (int h = 1; h < NT; ++h) q += i >= h * E;
+            return q;
+        };
+        // the gradient of a logit x in a token with (lse, sum of s ds) = (lq, cq)
+        auto grad = [&](float x, float up, float lq, float cq) {
+            if (!DENSE) return up;
+            if (lq == -INFINITY) return 0.f;  // no expert has a score
+            const float p = fast_exp2(kLog2e * (x - lq));
+            return p * (up - cq) + P.z_scale * lq * p;
+        };
+        auto grad_at = [&](int i, float x) {
+            const int q = DENSE ? token_of(i) : 0;
+            return grad(x, row[i], DENSE ? token_lse[warp][q] : 0.f, DENSE ? token_c[warp][q] : 0.f);
+        };
+        const bool vec = ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(extra) |
+                           reinterpret_cast<uintptr_t>(l)) & 15u) == 0;
+        const int nv = vec ? n / 4 * 4 : 0;
+        for (int i0 = 4 * lane; i0 < nv; i0 += 512) {  // four vectors' loads in flight
+            float4 x[4], y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + 128 * u >= nv) continue;
+                if (DENSE) x[u] = *reinterpret_cast<const float4*>(l + i0 + 128 * u);
+                if (extra) y[u] = *reinterpret_cast<const float4*>(extra + i0 + 128 * u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 128 * u;
+                if (i >= nv) continue;
+                float4 g;
+                if (DENSE && E % 4 != 0) {  // a vector may lie in two tokens
+                    g = make_float4(grad_at(i, x[u].x), grad_at(i + 1, x[u].y), grad_at(i + 2, x[u].z),
+                                    grad_at(i + 3, x[u].w));
+                } else {
+                    const int q = DENSE ? token_of(i) : 0;
+                    const float lq = DENSE ? token_lse[warp][q] : 0.f, cq = DENSE ? token_c[warp][q] : 0.f;
+                    const float4 up = *reinterpret_cast<const float4*>(row + i);
+                    g = make_float4(grad(x[u].x, up.x, lq, cq), grad(x[u].y, up.y, lq, cq),
+                                    grad(x[u].z, up.z, lq, cq), grad(x[u].w, up.w, lq, cq));
+                }
+                g.x += y[u].x, g.y += y[u].y, g.z += y[u].z, g.w += y[u].w;
+                *reinterpret_cast<float4*>(out + i) = g;
+            }
+        }
+        for (int i = nv + lane; i < n; i += 32) {
+            const float g = grad_at(i, DENSE ? l[i] : 0.f);
+            out[i] = extra ? g + extra[i] : g;
+        }
+        __syncwarp();  // the rows' readers are done
     }
-    for (int i = nv + lane; i < n; i += 32) out[i] = extra ? row[i] + extra[i] : row[i];
 }
 
 template <int L, int NB>
@@ -925,10 +965,14 @@ int launch_select(const SelectParams& P, cudaStream_t st) {
 }
 
 template <int L>
-int launch_bwd_lanes(const SelectBwdParams& P, cudaStream_t st) {
+int launch_bwd_lanes(const SelectBwdParams& P, bool dense, cudaStream_t st) {
     constexpr int NT = 32 / L;
     const size_t smem = sizeof(float) * kSelWarps * ((NT * P.E + 3) / 4 * 4);  // 32 KB at most
-    select_bwd_kernel<L><<<(unsigned)cdiv(P.T, (int64_t)kSelWarps * NT), kSelWarps * 32, smem, st>>>(P);
+    int64_t blocks = cdiv(P.T, (int64_t)kSelWarps * NT);
+    const int64_t cap = (int64_t)sm_count() * 6;  // resident CTAs
+    if (blocks > cap) blocks = cap;
+    auto kern = dense ? select_bwd_kernel<L, true> : select_bwd_kernel<L, false>;
+    kern<<<(unsigned)blocks, kSelWarps * 32, smem, st>>>(P);
     return launch_status();
 }
 
@@ -974,5 +1018,7 @@ extern "C" int moe_select_experts_bwd(const float* dg, const int32_t* topk_idx,
     const SelectBwdParams P{dg, topk_idx, topk_score, logits, lse, dlogits_extra, T, E, k, mode,
                             renorm ? 1 : 0, scale, 2.0f * z_coef / (float)T, dlogits, status};
     cudaStream_t st = (cudaStream_t)stream;
-    return k <= 8 ? launch_bwd_lanes<8>(P, st) : k <= 16 ? launch_bwd_lanes<16>(P, st) : launch_bwd_lanes<32>(P, st);
+    return k <= 8    ? launch_bwd_lanes<8>(P, dense, st)
+           : k <= 16 ? launch_bwd_lanes<16>(P, dense, st)
+                     : launch_bwd_lanes<32>(P, dense, st);
 }
