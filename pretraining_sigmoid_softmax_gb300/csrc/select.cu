@@ -285,18 +285,20 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
 // L lanes per token (32 / L tokens per warp), each holding up to 8 NB consecutive experts of one
 // group; lpg lanes (a power of two) hold a group, vr experts each. A warp copies its next tokens'
 // logits to shared memory while it works on the present ones. Every expert becomes one integer
-// key, its selection value above its place in the lane (the low bits): a lane keeps its eight
-// best keys, sorted by minima and maxima alone, groups are compared by their lanes' first keys,
-// and each of the k rounds takes the largest of the lanes' first keys.
+// key: its selection value as a 23-bit fixed-point number above its index. A lane sorts its keys
+// by minima and maxima alone and keeps the eight largest, groups are compared by their lanes'
+// first keys, and the k largest of the lanes' sorted keys come from a merge across eight lanes
+// that halves what a lane holds at each step (or, for more lanes, from k rounds that take the
+// largest of the lanes' first keys).
 //
 // The keys are rounded values. Where two of them that the choice has to tell apart lie within
 // the rounding's bound, the token is chosen again by select_close: groups and experts near the
 // border are evaluated in 64 bits and ranked. Rows that are not for this arithmetic (NaN,
 // infinities, more than 32 experts near the border) are chosen in 64 bits throughout.
 //
-// With a bias the value is s + (b - base), clamped at 0 from below, base the smallest bias within
-// 16 of the largest, s by the fast exponential and reciprocal; a non-negative float orders as its
-// bits do. Without a bias it is the logit, as an order-preserving integer.
+// With a bias the value is s + (b - base), base the smallest bias within 16 of the largest, s by
+// the fast exponential and reciprocal, scaled so that it lies below 1 and clamped at 0. Without
+// one it is the logit, from 16 below the row's largest up.
 struct SelectLayout {
     int lpg, vr;
     int vec;  // rows are 16-byte aligned, and a lane's experts whole 16-byte vectors
@@ -310,41 +312,58 @@ constexpr float kU = 5.9604645e-8f;  // 2^-24
 // 0.37: 25 u p + 0.6 u.
 constexpr float kSigmoidErr = 6.4f * kU;
 constexpr float kSoftmaxErr = 25.f * kU;
-
 constexpr float kLog2e = 1.44269504f;
 
 // Score of one expert from its logit (within the bounds above); inv = 1 / sum for softmax.
 __device__ __forceinline__ float fast_score(bool sigmoid, float l, float mx, float inv) {
     return sigmoid ? fast_rcp(1.0f + fast_exp2(-kLog2e * l)) : fast_exp2(kLog2e * (l - mx)) * inv;
 }
+__device__ __forceinline__ float score_err(bool sigmoid, float inv) {
+    return sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
+}
+// How far below v another value has to lie to come after it for certain, where both are rounded
+// sums s + (b - base): twice the score's error and both sums' roundings (u each, twice).
+__device__ __forceinline__ float value_gap(float v, float es) { return 2.f * es + 4.2f * kU * v; }
 
 __device__ __forceinline__ int logit_key(float l) {
     const int b = __float_as_int((l == l ? l : -INFINITY) + 0.0f);
     return b ^ ((b >> 31) & 0x7fffffff);
 }
 
-// How far below v another value has to lie to come after it for certain, where both are rounded
-// sums s + (b - base): twice the score's error and both sums' roundings (u each, twice), and what
-// dropping low bits takes off a key (`dropped` ulp: v's exponent gives an ulp's size).
-__device__ __forceinline__ float value_gap(float v, float es, float dropped) {
-    const float ulp = __int_as_float(__float_as_int(v) & 0x7f800000) * 1.1920929e-7f;
-    return 2.f * es + 4.2f * kU * v + dropped * ulp;
+// The key of a value v = a x + b clamped to [0, 1) (a NaN to 0): v + 1 has v's 23 fixed-point
+// bits as its mantissa (rounded to half a unit); times 512 they are the key's upper bits, the
+// sign turned so that signed integers order the keys. `id` = expert + INT_MIN.
+constexpr int kKeyBits = 9;
+constexpr float kUnits = 8388608.f;  // per 1
+__device__ __forceinline__ int fixed_key(float x, float a, float b, int id) {
+    float v;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(x), "f"(a), "f"(b));
+    return __float_as_int(v + 1.0f) * (1 << kKeyBits) + id;
 }
-__device__ __forceinline__ float score_err(bool sigmoid, float inv) {
-    return sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
-}
+__device__ __forceinline__ int units_of(int key) { return (int)((uint32_t)(key ^ INT_MIN) >> kKeyBits); }
+constexpr float kLogitRange = 16.f;
+constexpr float kBelowOne = 0.9990234f;  // 1 - 2^-10
 
-// The smallest bias within 16 of the largest finite one (0 where none is finite). By one warp.
-__device__ __forceinline__ float bias_base(const float* b, int E, int lane) {
+// The biases' base, the smallest within 16 of the largest finite one (0 where none is finite), and
+// 1 + the largest's distance from it; from a warp's b[j] = bias of expert lane + 32 j (NaN past
+// the last). An infinite bias gives an infinite range.
+__device__ __forceinline__ float bias_base(const float (&b)[kMaxExperts / 32], float& range) {
     float hi = -INFINITY;
-    for (int e = lane; e < E; e += 32)
-        if (isfinite(b[e])) hi = fmaxf(hi, b[e]);
+    bool inf = false;
+#pragma unroll
+    for (int j = 0; j < kMaxExperts / 32; ++j) {
+        if (isfinite(b[j])) hi = fmaxf(hi, b[j]);
+        inf |= b[j] == INFINITY;
+    }
     hi = seg_max<32>(hi);
     float lo = INFINITY;
-    for (int e = lane; e < E; e += 32)
-        if (b[e] >= hi - 16.f && b[e] <= hi) lo = fminf(lo, b[e]);
+#pragma unroll
+    for (int j = 0; j < kMaxExperts / 32; ++j)
+        if (b[j] >= hi - 16.f && b[j] <= hi) lo = fminf(lo, b[j]);
     lo = -seg_max<32>(-lo);
-    return isfinite(lo) ? lo : 0.f;
+    if (!isfinite(lo)) lo = hi = 0.f;
+    range = __any_sync(kFull, inf) ? INFINITY : 1.f + (hi - lo);
+    return lo;
 }
 
 // One token whose keys left its choice open, by a whole warp, from its logits in shared memory.
@@ -353,32 +372,43 @@ __device__ __forceinline__ float bias_base(const float* b, int E, int lane) {
 // ranked. Experts: without a bias the logits' own order; else those that may be among the k
 // largest of the open groups are gathered, one per lane, evaluated in 64 bits and ranked. False
 // where that does not settle it (more than three candidates for a group's two, or more than 32
-// for the k; NaN, or softmax over infinities): the token is then left to select_token.
+// for the k): the token is then left to select_token. `kth`: a value that the k-th largest of the
+// open groups reaches, where the groups are settled.
 template <bool LOGIT>
 __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, float base,
-                                          const float* row, bool settled, uint32_t open, int* scratch) {
+                                          const float* row, bool settled, uint32_t open, float kth,
+                                          int* scratch) {
     constexpr int VJ = kMaxExperts / 32;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID, top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
+    float l[VJ];  // of the experts lane, lane + 32, ...
+#pragma unroll
+    for (int j = 0; j < VJ; ++j) l[j] = lane + 32 * j < E ? row[lane + 32 * j] : -INFINITY;
     float mx = 0.f, sum = 1.f, inv = 1.f;
     double total = 1.0;
     if (!sigmoid) {
-        row_softmax(row, E, lane, mx, sum);
+        mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) mx = fmaxf(mx, l[j]);
+        mx = seg_max<32>(mx);
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) sum += fast_exp2(kLog2e * (l[j] - mx));
+        sum = seg_sum<32>(sum);
         inv = fast_rcp(sum);
         if (!LOGIT) {
             total = 0.0;
-            for (int e = lane; e < E; e += 32) total += exp((double)row[e] - (double)mx);
+            for (int j = 0; j < VJ; ++j)
+                if (lane + 32 * j < E) total += exp((double)l[j] - (double)mx);
             total = seg_sum<32>(total);
         }
     }
-    bool bad = !(sum < 1e30f) || mx == -INFINITY;
-    for (int e = lane; e < E; e += 32) bad |= row[e] != row[e];
-    if (__any_sync(kFull, bad)) return false;
     const float es = score_err(sigmoid, inv);
-    auto value = [&](int e) { return fmaxf(fast_score(sigmoid, row[e], mx, inv) + (P.b[e] - base), 0.f); };
+    auto value_of = [&](float x, int e) { return fmaxf(fast_score(sigmoid, x, mx, inv) + (P.b[e] - base), 0.f); };
+    auto value = [&](int e) { return value_of(row[e], e); };
     auto score64 = [&](int e) {
-        const double l = row[e];
-        return sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)mx) / total;
+        const double x = row[e];
+        return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx) / total;
     };
     auto value64 = [&](int e) { return no_nan(score64(e) + (double)P.b[e]); };
 
@@ -409,7 +439,7 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
                 // the two largest (or the largest) are among the first three unless the fourth
                 // may reach them
                 const float least = top2 ? b : a;
-                unsettled = per > 3 && !(least - d > value_gap(least, es, 0.f));
+                unsettled = per > 3 && !(least - d > value_gap(least, es));
                 double x = value64(ia);
                 double y = per > 1 ? value64(ib) : -INFINITY, z = per > 2 ? value64(ic) : -INFINITY;
                 if (y > x) { const double q = x; x = y; y = q; }
@@ -432,30 +462,33 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
     for (int j = 0; j < VJ; ++j) {
         const int e = lane + 32 * j;
         key[j] = INT_MIN;
-        if (e < E && ((open >> (e / per)) & 1u))
-            key[j] = LOGIT ? logit_key(row[e]) : __float_as_int(value(e));
+        if (e < E && ((open >> (e / per)) & 1u)) key[j] = LOGIT ? logit_key(l[j]) : __float_as_int(value_of(l[j], e));
     }
-    uint32_t taken = 0;
-    int my_e = 0, kth = INT_MIN;
-    for (int i = 0; i < k; ++i) {  // the largest key left, of the lowest index
-        int best = INT_MIN, e = INT_MAX;
+    int my_e = 0;
+    if (LOGIT || !settled) {  // (where the groups were settled, kth is known)
+        uint32_t taken = 0;
+        int top = INT_MIN;
+        for (int i = 0; i < k; ++i) {  // the largest key left, of the lowest index
+            int best = INT_MIN, e = INT_MAX;
 #pragma unroll
-        for (int j = 0; j < VJ; ++j)
-            if (!((taken >> j) & 1u) && key[j] > best) {
-                best = key[j];
-                e = lane + 32 * j;
-            }
-        kth = __reduce_max_sync(kFull, best);
-        const int w = __reduce_min_sync(kFull, best == kth ? e : INT_MAX);
-        if ((w & 31) == lane) taken |= 1u << (w >> 5);
-        if (lane == i) my_e = w;
+            for (int j = 0; j < VJ; ++j)
+                if (!((taken >> j) & 1u) && key[j] > best) {
+                    best = key[j];
+                    e = lane + 32 * j;
+                }
+            top = __reduce_max_sync(kFull, best);
+            const int w = __reduce_min_sync(kFull, best == top ? e : INT_MAX);
+            if ((w & 31) == lane) taken |= 1u << (w >> 5);
+            if (lane == i) my_e = w;
+        }
+        kth = __int_as_float(top);
     }
     if (!LOGIT) {
-        const float v = __int_as_float(kth), gap = value_gap(v, es, 0.f);
+        const float gap = value_gap(kth, es);
         int n = 0;
 #pragma unroll
         for (int j = 0; j < VJ; ++j) {
-            const bool in = key[j] != INT_MIN && !(v - __int_as_float(key[j]) > gap);
+            const bool in = key[j] != INT_MIN && !(kth - __int_as_float(key[j]) > gap);
             const uint32_t m = __ballot_sync(kFull, in);
             const int at = n + __popc(m & ((1u << lane) - 1u));
             if (in && at < 32) scratch[at] = lane + 32 * j;
@@ -509,6 +542,62 @@ __device__ __forceinline__ void merge8(int (&k)[8], const int (&o)[8]) {
 #undef MOE_CE
 }
 
+// The eight largest of eight lanes' sorted eights, one per lane: lane `sub` returns the
+// kSlotOfLane[sub]-th largest, and `left` the largest of the rest (each lane's part of it: the
+// caller takes the maximum over the lanes). Bitonic merges of pairs, fours and eights of lanes: the
+// larger of a_i and b_(7-i) over i are the eight largest of two sorted eights, and each lane of
+// a merge takes its share of them, 4, 2 and 1, so that a step moves only those.
+//   After the pairs' step lanes 0, 1 hold a pair's eight in order, four each; after the fours'
+//   step lanes 0, 3, 1, 2 a four's, two each; after the last lanes 0, 6, 3, 5, 1, 7, 2, 4.
+constexpr uint32_t kSlotOfLane = 0x51372640u, kLaneOfSlot = 0x42715360u;  // four bits each
+__device__ __forceinline__ int merge_lanes8(const int (&k)[8], int sub, int& left) {
+    const bool odd = sub & 1, two = sub & 2;
+    int r[4];
+    left = INT_MIN;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int o = __shfl_xor_sync(kFull, k[7 - j], 1);
+        r[j] = max(k[j], o);
+        left = max(left, min(k[j], o));
+    }
+    int n[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // the odd lane holds positions 7 .. 4
+        const int x = odd ? r[3 - j] : r[j], o = __shfl_xor_sync(kFull, x, 1);
+        n[j] = odd ? min(x, o) : max(x, o);
+    }
+    swap_desc(n[0], n[2]);
+    swap_desc(n[1], n[3]);
+    swap_desc(n[0], n[1]);
+    swap_desc(n[2], n[3]);
+    int p, q;
+    {
+        const int o3 = __shfl_xor_sync(kFull, n[3], 3), o2 = __shfl_xor_sync(kFull, n[2], 3);
+        p = max(n[0], o3);
+        q = max(n[1], o2);
+        left = max(left, max(min(n[0], o3), min(n[1], o2)));
+        const bool low = odd != two;  // lanes 1 and 2 hold positions 4 .. 7
+        const int po = __shfl_xor_sync(kFull, p, 1), qo = __shfl_xor_sync(kFull, q, 1);
+        p = low ? min(p, po) : max(p, po);
+        q = low ? min(q, qo) : max(q, qo);
+        const int px = __shfl_xor_sync(kFull, q, 3), qx = __shfl_xor_sync(kFull, p, 3);
+        p = two ? min(p, px) : max(p, px);
+        q = two ? min(q, qx) : max(q, qx);
+        swap_desc(p, q);
+    }
+    const int o = __shfl_xor_sync(kFull, q, 6);
+    int m = max(p, o);
+    left = max(left, min(p, o));
+    // positions: lane 0 0, 6 1, 3 2, 5 3, 1 4, 7 5, 2 6, 4 7
+    const int slot = (int)(kSlotOfLane >> (4 * sub)) & 7;
+    const int o4 = __shfl_xor_sync(kFull, m, 1);
+    m = slot & 4 ? min(m, o4) : max(m, o4);
+    const int o2 = __shfl_xor_sync(kFull, m, 3);
+    m = slot & 2 ? min(m, o2) : max(m, o2);
+    const int o1 = __shfl_xor_sync(kFull, m, 6);
+    return slot & 1 ? min(m, o1) : max(m, o1);
+}
+
 template <int BYTES>
 __device__ __forceinline__ void cp_async(void* dst, const void* src) {
     if constexpr (BYTES == 16)
@@ -520,12 +609,9 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src) {
 template <int L, int NB, bool LOGIT>
 __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectParams P, const SelectLayout Y) {
     constexpr int NT = 32 / L;
-    constexpr int BITS = NB == 1 ? 3 : NB == 2 ? 4 : 5;  // of a place in the lane
-    constexpr int PLACE = (1 << BITS) - 1;
     extern __shared__ __align__(16) float smem[];  // biases, then two buffers of rows per warp
     __shared__ int scratch[kSelWarps][32];
-    __shared__ int2 slots[kSelWarps][32];  // a slot's key and expert
-    __shared__ int taken;                  // steps of the CTA's run that its warps have taken
+    __shared__ int taken;  // steps of the CTA's run that its warps have taken
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID;
@@ -534,7 +620,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     const int count = g < G ? max(0, min(Y.vr, per - r * Y.vr)) : 0;
     const int first = count > 0 ? g * per + r * Y.vr : 0;  // idle lanes read the row's start
     const int pitch = (E + 3) / 4 * 4;
-    float* const bias = smem;  // b - base
+    float* const bias = smem;  // (b - base) times the values' scale
     float* const rows = smem + (LOGIT ? 0 : pitch) + warp * 2 * NT * pitch;
 
     // The CTA's tokens are a run of steps of NT tokens, which its warps take one by one (a token
@@ -563,16 +649,26 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     int step = warp;  // the first ones without asking
     fetch(step, 0);
     if (threadIdx.x == 0) taken = kSelWarps;
-    float base = 0.f;
+    float base = 0.f, scale = 1.f, range = 1.f;
+    bool infinite = false;
     if constexpr (!LOGIT) {
-        base = bias_base(P.b, E, lane);
-        for (int e = threadIdx.x; e < E; e += kSelWarps * 32) bias[e] = P.b[e] - base;
+        float b[kMaxExperts / 32];
+#pragma unroll
+        for (int j = 0; j < kMaxExperts / 32; ++j) b[j] = lane + 32 * j < E ? P.b[lane + 32 * j] : NAN;
+        base = bias_base(b, range);
+        infinite = range == INFINITY;
+        scale = kBelowOne * fast_rcp(range);
+#pragma unroll
+        for (int j = 0; j < kMaxExperts / 32; ++j)  // one warp's share each
+            if (j == warp && lane + 32 * j < E) bias[lane + 32 * j] = (b[j] - base) * scale;
     }
     __syncthreads();
     // lanes of equal banks start at different vectors of their own (the order is free)
     const int nvec = Y.vr / 4;
     const int turn = Y.vec ? (sub * Y.vr / 32) % nvec : 0;
     const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
+    const int my_slot = L == 8 ? (int)(kSlotOfLane >> (4 * sub)) & 7 : sub;
+    const int next_lane = L == 8 ? (int)(kLaneOfSlot >> (4 * ((my_slot + 1) & 7))) & 7 : sub + 1;
 
     for (int buf = 0; step < n; buf ^= 1) {
         const int ahead = take();
@@ -581,8 +677,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
         __syncwarp();
         const int64_t t0 = (s0 + step) * NT, t = t0 + lane / L;
         const bool live = t < P.T;
-        const float* const held = rows + buf * NT * pitch;  // the step's rows
-        const float* row = held + lane / L * E + first;
+        const float* const held = rows + buf * NT * pitch + lane / L * E;  // the token's row
         // four of the lane's logits, from place `at` on (a multiple of 4), as far as there are
         auto load4 = [&](int c, int& at, float (&v)[4]) {
             at = 4 * c;
@@ -590,43 +685,48 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 int o = c + turn;
                 if (o >= nvec) o -= nvec;
                 at = 4 * o;
-                const float4 u = *reinterpret_cast<const float4*>(row + at);
+                const float4 u = *reinterpret_cast<const float4*>(held + first + at);
                 v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = at + j < count ? row[at + j] : 0.f;
+                for (int j = 0; j < 4; ++j) v[j] = at + j < count ? held[first + at + j] : -INFINITY;
             }
         };
         const int nload = (Y.vr + 3) / 4;
         bool odd = false;  // not a row for this kernel's arithmetic
         float mx = 0.f, sum = 1.f, inv = 1.f;
-        if (!sigmoid) {
+        if (LOGIT || !sigmoid) {
             mx = -INFINITY;
             for (int c = 0; c < nload; ++c) {
                 int at;
                 float v[4];
                 load4(c, at, v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (at + j < count) mx = fmaxf(mx, v[j]);
+                mx = fmaxf(fmaxf(mx, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
             }
             mx = seg_max<L>(mx);
+            if (LOGIT) odd = !(fabsf(mx) < 1e5f);  // the keys' offset would round by more than their margin
+        }
+        if (!sigmoid) {
             sum = 0.f;
             for (int c = 0; c < nload; ++c) {
                 int at;
                 float v[4];
                 load4(c, at, v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (at + j < count) sum += fast_exp2(kLog2e * (v[j] - mx));
+                sum += (fast_exp2(kLog2e * (v[0] - mx)) + fast_exp2(kLog2e * (v[1] - mx))) +
+                       (fast_exp2(kLog2e * (v[2] - mx)) + fast_exp2(kLog2e * (v[3] - mx)));
             }
-            sum = seg_sum<L>(sum);
-            odd = !(sum < 1e30f) || mx == -INFINITY;  // NaN or infinite logits
+            sum = seg_sum<L>(count > 0 ? sum : 0.f);
+            odd |= !(sum < 1e30f) || mx == -INFINITY;  // NaN or infinite logits
             inv = fast_rcp(sum);
         }
         const float es = score_err(sigmoid, inv);
+        // a value in the keys: kv x + kc (LOGIT: of the logit; else of the score, plus its bias)
+        const float kv = LOGIT ? kBelowOne / kLogitRange : sigmoid ? scale : scale * inv;
+        const float kc = LOGIT ? (kLogitRange - mx) * kv : 0.f;
+        // units that settle an order: twice the score's error and the three roundings of b - base,
+        // its scaling and the sum (u each), and both values' rounding to half a unit
+        const int tol = LOGIT ? 3 : 3 + (int)((2.f * es + 6.2f * kU * range) * scale * kUnits);
         int key[8];
-        float fa = -INFINITY, fb = -INFINITY;  // a lane's two largest logits
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
             if (blk > 0 && 8 * blk >= Y.vr) break;
@@ -639,6 +739,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 for (int j = 0; j < 4; ++j) kb[4 * h + j] = INT_MIN;
                 if (8 * blk + 4 * h >= Y.vr) continue;
                 load4(2 * blk + h, at, v);
+                const int id = INT_MIN + first + at;
                 float bv[4] = {0.f, 0.f, 0.f, 0.f};
                 if (!LOGIT) {
                     if (Y.vec) {
@@ -653,17 +754,14 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     int x;
-                    if (LOGIT) {
-                        x = logit_key(v[j]);
-                        if (top2 && G > 1 && at + j < count) {
-                            odd |= v[j] != v[j];  // a NaN's score counts as -inf in the sum
-                            fb = fmaxf(fb, fminf(fa, v[j]));
-                            fa = fmaxf(fa, v[j]);
-                        }
-                    } else {
-                        x = __float_as_int(fmaxf(fast_score(sigmoid, v[j], mx, inv) + bv[j], 0.f));
-                    }
-                    if (at + j < count) kb[4 * h + j] = (x & ~PLACE) | (at + j);
+                    if (LOGIT)
+                        x = fixed_key(v[j], kv, kc, id + j);
+                    else if (sigmoid)
+                        x = fixed_key(fast_rcp(1.0f + fast_exp2(-kLog2e * v[j])), kv, bv[j], id + j);
+                    else
+                        x = fixed_key(fast_exp2(kLog2e * (v[j] - mx)), kv, bv[j], id + j);
+                    if (LOGIT && top2 && G > 1) odd |= v[j] != v[j];  // a NaN's score is -inf in the sum
+                    kb[4 * h + j] = Y.vec || at + j < count ? x : INT_MIN;
                 }
             }
             sort8(kb);
@@ -674,27 +772,42 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 merge8(key, kb);
             }
         }
+        if (count == 0) {  // idle lanes
+#pragma unroll
+            for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
+        }
         bool groups = false;  // unsettled
         uint32_t open = 1u;
         if (G > 1) {
+            // a group's score in units; sums of scores without a bias as floats
             int a = key[0], b = key[1];
+            float fa = -INFINITY, fb = -INFINITY;
+            bool rough = false;
+            if (LOGIT && top2) {  // from the logits themselves
+                if (count > 0) fa = held[a & 255];
+                if (count > 1) fb = held[b & 255];
+                if (fb > fa) {
+                    const float x = fa;
+                    fa = fb;
+                    fb = x;
+                }
+                // the third may be the second's equal but for rounding; clamped ones are unordered
+                rough = count > 2 && units_of(b) - units_of(key[2]) <= 3;
+            }
             for (int o = 1; o < Y.lpg; o <<= 1) {
+                const int oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+                b = max(max(b, ob), min(a, oa));
+                a = max(a, oa);
                 if (LOGIT && top2) {
-                    const float oa = __shfl_xor_sync(kFull, fa, o), ob = __shfl_xor_sync(kFull, fb, o);
-                    fb = fmaxf(fmaxf(fb, ob), fminf(fa, oa));
-                    fa = fmaxf(fa, oa);
-                } else {
-                    const int oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
-                    b = max(max(b, ob), min(a, oa));
-                    a = max(a, oa);
+                    const float xa = __shfl_xor_sync(kFull, fa, o), xb = __shfl_xor_sync(kFull, fb, o);
+                    fb = fmaxf(fmaxf(fb, xb), fminf(fa, xa));
+                    fa = fmaxf(fa, xa);
                 }
             }
-            // a sum that counts a value clamped at 0
-            if (!LOGIT && top2 && g < G) groups |= b <= PLACE;
-            int gs = a & ~PLACE;  // a score's order as an integer
-            if (top2)
-                gs = __float_as_int(LOGIT ? fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv)
-                                          : __int_as_float(a & ~PLACE) + __int_as_float(b & ~PLACE));
+            int gs = top2 ? units_of(a) + units_of(b) : units_of(a);
+            if (LOGIT && top2)
+                gs = __float_as_int(fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv));
+            if (top2 && g < G) groups |= units_of(b) == 0;  // a sum that counts a value clamped at 0
             int rank = 0;
             for (int h = 0; h < G; ++h) {
                 const int x = __shfl_sync(kFull, gs, h * Y.lpg, L);
@@ -704,15 +817,17 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
             if (P.topk_group < G) {
                 const int lo = seg_min<L>(kept ? gs : INT_MAX);
                 const int hi = seg_max<L>(!kept && g < G ? gs : INT_MIN);
-                const float x = __int_as_float(lo), y = __int_as_float(hi);
-                bool sure;
-                if (!LOGIT)  // (an infinite sum is never sure; a sum's two keys drop at most 1.5 of its ulps)
-                    sure = x - y > (top2 ? 2.f * es + value_gap(x, es, 1.5f * (PLACE + 2)) : value_gap(x, es, (float)PLACE));
-                else if (!top2)
-                    sure = lo != hi;
-                else  // sums of scores: softmax terms are within 160 u of themselves down to e^-87
-                    sure = x - y > 2.f * (sigmoid ? 2.f * kSigmoidErr + kU * x : 161.f * kU * x) && x > 1e-30f;
-                groups |= !sure;
+                if (LOGIT && top2) {
+                    // softmax terms are within 160 u of themselves down to e^-87; logits that the
+                    // keys do not tell apart are within 6e-6
+                    const float x = __int_as_float(lo), y = __int_as_float(hi);
+                    const bool vague = (__ballot_sync(kFull, rough && g < G) & mask) != 0;
+                    const float gap = sigmoid ? 2.f * (2.f * kSigmoidErr + kU * x) + (vague ? 26.f * kU : 0.f)
+                                              : (322.f + (vague ? 101.f : 0.f)) * kU * x;
+                    groups |= !(x - y > gap && x > 1e-30f);
+                } else {
+                    groups |= lo - hi <= (top2 ? 2 * tol : tol);
+                }
             }
             open = 0u;
             const uint32_t heads = __ballot_sync(kFull, kept && r == 0) >> (lane / L * L);
@@ -722,59 +837,49 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
             }
         }
-        // the rounds: the lane that holds the largest key writes the slot and moves its list up
-        int pops = 0, last = INT_MIN;
-        int2* const slot = &slots[warp][lane / L * L];
-        if (L == 8) {  // at most eight slots: after round i, 8 - i keys of a lane can matter
-#pragma unroll
-            for (int i = 0; i <= 8; ++i) {
+        const int eighth = key[7];  // of a lane that still counts
+        // slot my_slot's key, and the largest one that is in no slot
+        int mine, last;
+        if (L == 8) {
+            mine = merge_lanes8(key, sub, last);
+            last = seg_max<L>(last);  // the ninth: what follows slot 7
+        } else {  // rounds: the lane that holds the largest key moves its list up
+            mine = INT_MIN;
+            for (int i = 0;; ++i) {
                 last = seg_max<L>(key[0]);
                 if (i == k) break;
+                if (sub == i) mine = last;
                 if (key[0] == last) {
-                    slot[i & 7] = make_int2(last, first + (last & PLACE));
-                    ++pops;
-#pragma unroll
-                    for (int j = 0; j < 7; ++j)
-                        if (j <= 7 - i) key[j] = key[j + 1];
-                    key[7] = INT_MIN;
-                }
-            }
-        } else {
-            for (int i = 0; i <= k; ++i) {
-                last = seg_max<L>(key[0]);
-                if (i == k) break;
-                if (key[0] == last) {
-                    slot[i] = make_int2(last, first + (last & PLACE));
-                    ++pops;
 #pragma unroll
                     for (int j = 0; j < 7; ++j) key[j] = key[j + 1];
                     key[7] = INT_MIN;
                 }
             }
         }
-        __syncwarp();
-        const int2 mine = slot[sub < k ? sub : 0];
-        const int my_e = mine.y;
+        const int my_e = min(mine & 255, E - 1);  // (of a key that is none: not used)
+        const bool slot_on = my_slot < k;
         // each slot's key against the next one's (the last slot's against the best one left)
-        int next = __shfl_down_sync(kFull, mine.x, 1);
-        if (sub == k - 1) next = last;
-        bool close = false;
-        if (sub < k && next != INT_MIN) {
-            const float x = __int_as_float(mine.x & ~PLACE), y = __int_as_float(next & ~PLACE);
-            close = !(LOGIT ? (mine.x >> BITS) != (next >> BITS) : x - y > value_gap(x, es, (float)PLACE));
-        }
-        close |= seg_sum<L>(pops) != k;           // equal keys, taken in one round
-        close |= NB > 1 && pops >= 8 && count > 8;  // the lane's ninth key is not known
-        const uint32_t again = __ballot_sync(kFull, live && (odd || groups || close));
-        finish<L>(P, t, sub, live && !(again & mask), my_e, held[lane / L * E + my_e], mx, sum);
+        int next = __shfl_sync(kFull, mine, lane / L * L + (next_lane < L ? next_lane : 0));
+        if (my_slot == L - 1 || (L > 8 && my_slot == k - 1)) next = last;
+        bool close = slot_on && units_of(mine) - units_of(next) <= tol;
+        // a lane whose eight are all chosen may hold the ninth of them
+        const int kth = __shfl_sync(kFull, mine, lane / L * L + (L == 8 ? (int)(kLaneOfSlot >> (4 * (k - 1))) & 7 : k - 1));
+        close |= NB > 1 && count > 8 && eighth >= kth;
+        const uint32_t again = __ballot_sync(kFull, live && (odd || groups || close || infinite));
+        finish<L>(P, t, my_slot, live && !(again & mask), my_e, held[my_e], mx, sum);
         if (again) {
-            const uint32_t strange = __ballot_sync(kFull, live && odd), unsettled = __ballot_sync(kFull, live && groups);
+            const uint32_t strange = __ballot_sync(kFull, live && (odd || infinite));
+            const uint32_t unsettled = __ballot_sync(kFull, live && groups);
             for (int i = 0; i < NT; ++i) {  // the warp together, one token at a time
                 const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (i * L);
                 if (!(again & m)) continue;
                 const uint32_t o = __shfl_sync(kFull, open, i * L);
+                const int ku = units_of(__shfl_sync(kFull, kth, i * L));
+                // the k-th key's value, less what its roundings may have added
+                const float least = (float)(ku - 4) / (scale * kUnits);
                 if ((strange & m) ||
-                    !select_close<LOGIT>(P, t0 + i, lane, base, held + i * E, !(unsettled & m), o, scratch[warp]))
+                    !select_close<LOGIT>(P, t0 + i, lane, base, rows + buf * NT * pitch + i * E, !(unsettled & m),
+                                         o, least, scratch[warp]))
                     select_token(P, t0 + i, lane);
             }
         }
