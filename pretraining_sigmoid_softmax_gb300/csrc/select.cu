@@ -301,7 +301,6 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
 // one it is the logit, from 16 below the row's largest up.
 struct SelectLayout {
     int lpg, vr;
-    int vec;  // rows are 16-byte aligned, and a lane's experts whole 16-byte vectors
 };
 
 constexpr float kU = 5.9604645e-8f;  // 2^-24
@@ -606,7 +605,8 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-template <int L, int NB, bool LOGIT>
+// VEC: rows are 16-byte aligned, and a lane's experts whole 16-byte vectors.
+template <int L, int NB, bool LOGIT, bool VEC>
 __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectParams P, const SelectLayout Y) {
     constexpr int NT = 32 / L;
     extern __shared__ __align__(16) float smem[];  // biases, then two buffers of rows per warp
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID;
-    const bool top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
+    const bool top2 = P.rule == MOE_GROUP_TOP2 && per > 1, sums = top2 && G > 1;
     const int g = sub / Y.lpg, r = sub % Y.lpg;
     const int count = g < G ? max(0, min(Y.vr, per - r * Y.vr)) : 0;
     const int first = count > 0 ? g * per + r * Y.vr : 0;  // idle lanes read the row's start
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
             const int m = (int)min((int64_t)NT, P.T - t) * E;  // the step's rows are one piece
             const float* src = P.logits + t * E;
             float* dst = rows + buf * NT * pitch;
-            if (Y.vec)
+            if (VEC)
                 for (int c = 4 * lane; c < m; c += 128) cp_async<16>(dst + c, src + c);
             else
                 for (int c = lane; c < m; c += 32) cp_async<4>(dst + c, src + c);
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     __syncthreads();
     // lanes of equal banks start at different vectors of their own (the order is free)
     const int nvec = Y.vr / 4;
-    const int turn = Y.vec ? (sub * Y.vr / 32) % nvec : 0;
+    const int turn = VEC ? (sub * Y.vr / 32) % nvec : 0;
     const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
     const int my_slot = L == 8 ? (int)(kSlotOfLane >> (4 * sub)) & 7 : sub;
     const int next_lane = L == 8 ? (int)(kLaneOfSlot >> (4 * ((my_slot + 1) & 7))) & 7 : sub + 1;
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
         // four of the lane's logits, from place `at` on (a multiple of 4), as far as there are
         auto load4 = [&](int c, int& at, float (&v)[4]) {
             at = 4 * c;
-            if (Y.vec) {
+            if (VEC) {
                 int o = c + turn;
                 if (o >= nvec) o -= nvec;
                 at = 4 * o;
@@ -740,9 +740,9 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 if (8 * blk + 4 * h >= Y.vr) continue;
                 load4(2 * blk + h, at, v);
                 const int id = INT_MIN + first + at;
-                float bv[4] = {0.f, 0.f, 0.f, 0.f};
+                float bv[4] = {kc, kc, kc, kc};
                 if (!LOGIT) {
-                    if (Y.vec) {
+                    if (VEC) {
                         const float4 u = *reinterpret_cast<const float4*>(bias + first + at);
                         bv[0] = u.x, bv[1] = u.y, bv[2] = u.z, bv[3] = u.w;
                     } else {
@@ -750,19 +750,19 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                         for (int j = 0; j < 4; ++j)
                             if (at + j < count) bv[j] = bias[first + at + j];
                     }
+                    if (sigmoid) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = fast_rcp(1.0f + fast_exp2(-kLog2e * v[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = fast_exp2(kLog2e * (v[j] - mx));
+                    }
+                } else if (sums) {  // a NaN's score is -inf in the sum
+                    odd |= v[0] != v[0] || v[1] != v[1] || v[2] != v[2] || v[3] != v[3];
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    int x;
-                    if (LOGIT)
-                        x = fixed_key(v[j], kv, kc, id + j);
-                    else if (sigmoid)
-                        x = fixed_key(fast_rcp(1.0f + fast_exp2(-kLog2e * v[j])), kv, bv[j], id + j);
-                    else
-                        x = fixed_key(fast_exp2(kLog2e * (v[j] - mx)), kv, bv[j], id + j);
-                    if (LOGIT && top2 && G > 1) odd |= v[j] != v[j];  // a NaN's score is -inf in the sum
-                    kb[4 * h + j] = Y.vec || at + j < count ? x : INT_MIN;
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (VEC || at + j < count) kb[4 * h + j] = fixed_key(v[j], kv, bv[j], id + j);
             }
             sort8(kb);
             if (blk == 0) {
@@ -1035,13 +1035,14 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
 }
 
 template <int L, int NB>
-int launch_lanes(const SelectParams& P, const SelectLayout& Y, cudaStream_t st) {
-    constexpr int NT = 32 / L;
+int launch_lanes(const SelectParams& P, const SelectLayout& Y, bool vec, cudaStream_t st) {
+    constexpr int NT = 32 / L, NBMAX = L == 8 ? 4 : 2;  // (rows of any alignment share one kernel)
     const size_t smem = sizeof(float) * ((P.E + 3) / 4 * 4) * ((P.b ? 1 : 0) + kSelWarps * 2 * NT);
     int64_t blocks = cdiv(P.T, (int64_t)NT);      // one step each, until the GPU is full
     const int64_t cap = (int64_t)sm_count() * 2;  // resident CTAs
     if (blocks > cap) blocks = cap;
-    auto kern = P.b ? select_kernel<L, NB, false> : select_kernel<L, NB, true>;
+    auto kern = vec ? (P.b ? select_kernel<L, NB, false, true> : select_kernel<L, NB, true, true>)
+                    : (P.b ? select_kernel<L, NBMAX, false, false> : select_kernel<L, NBMAX, true, false>);
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MOE_ERR_LAUNCH;
@@ -1062,11 +1063,14 @@ int launch_select(const SelectParams& P, cudaStream_t st) {
         Y.vr = (int)cdiv(per, Y.lpg);
         if (L == 32 || Y.vr <= (L == 8 ? 32 : 16)) break;
     }
-    Y.vec = P.E % 4 == 0 && Y.vr % 4 == 0 && per % Y.vr == 0 && aligned16(P.logits);
+    const bool vec = P.E % 4 == 0 && Y.vr % 4 == 0 && per % Y.vr == 0 && aligned16(P.logits);
     const int nb = Y.vr <= 8 ? 1 : Y.vr <= 16 ? 2 : 4;
-    if (L == 8) return nb == 1 ? launch_lanes<8, 1>(P, Y, st) : nb == 2 ? launch_lanes<8, 2>(P, Y, st) : launch_lanes<8, 4>(P, Y, st);
-    if (L == 16) return nb == 1 ? launch_lanes<16, 1>(P, Y, st) : launch_lanes<16, 2>(P, Y, st);
-    return nb == 1 ? launch_lanes<32, 1>(P, Y, st) : launch_lanes<32, 2>(P, Y, st);
+    if (L == 8)
+        return nb == 1   ? launch_lanes<8, 1>(P, Y, vec, st)
+               : nb == 2 ? launch_lanes<8, 2>(P, Y, vec, st)
+                         : launch_lanes<8, 4>(P, Y, vec, st);
+    if (L == 16) return nb == 1 ? launch_lanes<16, 1>(P, Y, vec, st) : launch_lanes<16, 2>(P, Y, vec, st);
+    return nb == 1 ? launch_lanes<32, 1>(P, Y, vec, st) : launch_lanes<32, 2>(P, Y, vec, st);
 }
 
 template <int L>
