@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
             for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
         }
         bool groups = false;  // unsettled
-        uint32_t open = 1u;
+        uint32_t heads = 0u;  // lanes that begin a group that stays
         if (G > 1) {
             // a group's score in units; sums of scores without a bias as floats
             int a = key[0], b = key[1];
@@ -829,9 +829,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                     groups |= lo - hi <= (top2 ? 2 * tol : tol);
                 }
             }
-            open = 0u;
-            const uint32_t heads = __ballot_sync(kFull, kept && r == 0) >> (lane / L * L);
-            for (int h = 0; h < G; ++h) open |= ((heads >> (h * Y.lpg)) & 1u) << h;
+            heads = __ballot_sync(kFull, kept && r == 0);
             if (!kept) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
@@ -873,7 +871,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
             for (int i = 0; i < NT; ++i) {  // the warp together, one token at a time
                 const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (i * L);
                 if (!(again & m)) continue;
-                const uint32_t o = __shfl_sync(kFull, open, i * L);
+                uint32_t o = G > 1 ? 0u : 1u;
+                for (int h = 0; h < G; ++h) o |= ((heads >> (i * L + h * Y.lpg)) & 1u) << h;
                 const int ku = units_of(__shfl_sync(kFull, kth, i * L));
                 // the k-th key's value, less what its roundings may have added
                 const float least = (float)(ku - 4) / (scale * kUnits);
