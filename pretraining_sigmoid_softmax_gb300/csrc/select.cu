@@ -1055,7 +1055,9 @@ int launch_lanes(const SelectParams& P, const SelectLayout& Y, bool vec, cudaStr
 int launch_select(const SelectParams& P, cudaStream_t st) {
     const int per = P.E / P.n_group;
     SelectLayout Y{};
-    int L = 8;
+    // few tokens: a warp each, up to one for every resident warp (one token of 256 experts: 3.9 us,
+    // 4.6 with eight lanes)
+    int L = P.T <= (int64_t)sm_count() * 2 * kSelWarps ? 32 : 8;
     for (;; L *= 2) {
         if (L < 32 && (L < P.k || L < P.n_group)) continue;
         for (Y.lpg = 1; P.n_group * Y.lpg * 2 <= L;) Y.lpg *= 2;

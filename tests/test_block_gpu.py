@@ -205,14 +205,15 @@ def test_layer_refuses_what_it_cannot_do():
         layer(x, x)
 
 
-@pytest.mark.parametrize("E,mode", [(16, ops.MODE_SIGMOID), (16, ops.MODE_SOFTMAX), (160, ops.MODE_SIGMOID)])
-def test_plan_step_in_a_graph_and_launch_count(E, mode):
+@pytest.mark.parametrize("E,mode,T", [(16, ops.MODE_SIGMOID, 260), (16, ops.MODE_SOFTMAX, 260),
+                                      (160, ops.MODE_SIGMOID, 260), (32, ops.MODE_SIGMOID, 3000)])
+def test_plan_step_in_a_graph_and_launch_count(E, mode, T):
     """A captured step with grouped routing repeats the eager one bit for bit, and runs as many
     kernels as the plan says."""
     from torch.autograd import DeviceType
     from torch.profiler import ProfilerActivity, profile
     torch.manual_seed(E)
-    T, d, f, k = 260, 256, 128, 4
+    d, f, k = 256, 128, 4
     plan = MoEPlan(MoEShape(T, d, E, k, f, mode=mode, seq_len=T, n_group=4, topk_group=2, gate_scale=1.5))
     dev = dict(device="cuda")
     W = dict(W_r=torch.randn(E, d, **dev) / 16, W_g=torch.randn(E, f, d, **dev).to(torch.bfloat16) / 16,

@@ -178,6 +178,30 @@ def test_choice_with_masked_and_extreme_logits(mode, bias):
             assert ((i >= 0) & (i < E)).all() and all(len(set(r)) == k for r in i.tolist())
 
 
+@pytest.mark.parametrize("mode", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,G,tg", [(64, 8, 8, 4), (256, 8, 8, 4), (100, 5, 10, 4), (160, 12, 16, 5),
+                                      (256, 16, 2, 1), (72, 3, 3, 2), (255, 32, 5, 3), (24, 4, 1, 1)])
+def test_choice_of_many_tokens(E, k, G, tg, mode):
+    """More tokens than are chosen a warp each: ordinary rows, ties and near ties, masks, infinities
+    and NaN among them, with biases and without."""
+    T = 2600
+    g = torch.Generator().manual_seed(E + k + G)
+    l = torch.randn(T, E, generator=g)
+    base = torch.randint(0, 4, (T // 4, E), generator=g).float() * 0.25 - 0.5
+    l[:T // 4] = torch.nextafter(base, base + (torch.randint(0, 3, base.shape, generator=g) - 1).float())
+    l[5::50] = 0.0
+    l[6::50, ::3] = -float("inf")
+    l[7::50] = -float("inf")
+    l[8::50] *= 100
+    l[9::400, 1] = float("nan")
+    l[10::400, 2] = float("inf")
+    l[11::50] = torch.finfo(torch.float32).min
+    b = (torch.rand(E, generator=g) * 0.2 - 0.1).cuda()
+    for bias in (None, b, torch.zeros_like(b)):
+        for rule in ("max", "top2"):
+            _check(l.cuda(), bias, k, mode, G, tg, rule)
+
+
 def test_choice_with_large_biases():
     g = torch.Generator().manual_seed(12)
     l = torch.randn(500, 64, generator=g).cuda()
