@@ -137,7 +137,7 @@ __device__ __forceinline__ void walk(const S* g, int64_t n, int64_t c, F1&& f1, 
     for (int64_t i = full + threadIdx.x; i < hi; i += kClipThreads) f1(head + i);
 }
 
-// The tensor of chunk `c`: the last one whose first chunk is not past it.
+// The tensor of chunk `c`: the last one whose first chunk is not past it (the first one at least).
 template <int N>
 __device__ __forceinline__ int tensor_of(const ClipTable<N>& tab, int c) {
     int lo = 0, hi = tab.count - 1;
@@ -156,8 +156,10 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(
     __shared__ double red[kClipThreads / 32];
     double acc = 0.0;
     grid_launch_dependents();
+    int e = tensor_of(tab, blockIdx.x);
     for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-        const ClipEntry& E = tab.t[tensor_of(tab, c)];
+        while (e + 1 < tab.count && tab.t[e + 1].first <= c) ++e;
+        const ClipEntry& E = tab.t[e];
         auto go = [&](auto* g) {
             using S = std::remove_const_t<std::remove_pointer_t<decltype(g)>>;
             walk<S>(
@@ -222,8 +224,10 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(
     }
     const float coef = r.y;
     // from the last chunk back: the norm's pass left the end of the gradients in L2
+    int e = tensor_of(tab, tab.chunks - 1 - blockIdx.x);
     for (int c = tab.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-        const ClipEntry& E = tab.t[tensor_of(tab, c)];
+        while (tab.t[e].first > c) --e;
+        const ClipEntry& E = tab.t[e];
         if (coef == 1.f && E.out == E.g) continue;  // nothing to do in place
         auto go = [&](auto* g) {
             using S = std::remove_const_t<std::remove_pointer_t<decltype(g)>>;
