@@ -493,7 +493,7 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
             if (in && at < 32) scratch[at] = lane + 32 * j;
             n += __popc(m);
         }
-        if (n > 32) return false;
+        if (n > 32 || n < k) return false;
         __syncwarp();
         int e = INT_MAX;
         double x = 0.0;
@@ -945,20 +945,22 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
             e = -1;
             s = dg = 0.f;
         }
-        float ds = P.scale * dg;
+        // v = s ds: with renormalised gates from s / S, since 1 / S may leave fp32's range
+        float v = P.scale * dg * s;
         if (P.renorm) {
-            const float S = seg_sum<L>(s);
-            const float m = seg_sum<L>(s / S * dg);
-            ds = S == 0.f ? 0.f : P.scale / S * (dg - m);
+            const float S = seg_sum<L>(s), share = S == 0.f ? 0.f : s / S;
+            const float m = seg_sum<L>(share * dg);
+            v = P.scale * (dg - m) * share;
         }
         if (DENSE) {
-            const float c = P.renorm ? 0.f : seg_sum<L>(s * ds);
+            const float c = P.renorm ? 0.f : seg_sum<L>(v);
             if (sub == 0) {
                 token_c[warp][lane / L] = c;
                 token_lse[warp][lane / L] = lse;
             }
+            if (!P.renorm) v = P.scale * dg;  // p takes the place of s
         }
-        float v = DENSE ? ds : softmax ? ds * s : ds * s * (1.f - s);
+        if (!softmax) v *= 1.f - s;
         // an expert named twice in a token gets its slots' terms summed in slot order, by the first
         const uint32_t same = __match_any_sync(kFull, e < 0 ? -1 - lane : lane / L * E + e);
         if (__any_sync(kFull, (same & (same - 1)) != 0)) {
@@ -983,12 +985,13 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const Select
             for (int h = 1; h < NT; ++h) q += i >= h * E;
             return q;
         };
-        // the gradient of a logit x in a token with (lse, sum of s ds) = (lq, cq)
+        // the gradient of a logit x in a token with (lse, sum of s ds) = (lq, cq); `up` = s ds with
+        // renormalised gates, else ds
         auto grad = [&](float x, float up, float lq, float cq) {
             if (!DENSE) return up;
             if (lq == -INFINITY) return 0.f;  // no expert has a score
             const float p = fast_exp2(kLog2e * (x - lq));
-            return p * (up - cq) + P.z_scale * lq * p;
+            return (P.renorm ? up : p * (up - cq)) + P.z_scale * lq * p;
         };
         auto grad_at = [&](int i, float x) {
             const int q = DENSE ? token_of(i) : 0;

@@ -358,6 +358,38 @@ def test_choice_bwd_of_rows_without_scores():
                 assert (d[2] == 0).all()
 
 
+@pytest.mark.parametrize("mode,z", [("sigmoid", 0.0), ("softmax", 0.0), ("softmax", 1e-2)])
+def test_choice_bwd_of_scores_below_the_normal_range(mode, z):
+    """Renormalised gates of chosen scores around e^-95: 1 / S is no fp32 number, but the gates'
+    gradient is of their ordinary size. A slot's share of S is off by 9 u (eight terms' sum, a
+    division), the mean over the slots by as much again and their products' roundings: 64 u of
+    scale * share * 2 max|dg| covers them. The z-loss's part is that of test_choice_bwd_matches_64_bits."""
+    T, E, k = 37, 64, 8
+    g = torch.Generator().manual_seed(77)
+    l = torch.randn(T, E, generator=g) - 95
+    if mode == "softmax":
+        l[:, -1] = 0.0  # takes all the probability, and a bias keeps it out of the choice
+    l = l.cuda()
+    b = torch.zeros(E, device="cuda")
+    b[-1] = -4.0
+    o = _select(l, b, k, mode, scale=2.5)
+    dg = torch.randn(T, k, generator=g).cuda()
+    got = _bwd(dg, o["idx"], o["score"], l, o["lse"], mode, True, 2.5, E, z_coef=z)
+    torch.cuda.synchronize()
+    idx = o["idx"].cpu().numpy()
+    s, dg64 = o["score"].double().cpu().numpy(), dg.double().cpu().numpy()
+    assert (s > 0).all() and (s < 1e-38).all() and (idx != E - 1).all()
+    share = s / s.sum(1, keepdims=True)
+    want, tol = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(want, idx, 2.5 * share * (dg64 - (share * dg64).sum(1, keepdims=True)), 1)
+    np.put_along_axis(tol, idx, 64 * U * 2.5 * share * 2 * np.abs(dg64).max(1, keepdims=True), 1)
+    if z:
+        p, lse = _scores(l.double().cpu().numpy(), mode)
+        zl = 2 * z / T * lse[:, None] * p
+        want, tol = want + zl, tol + (64 + 100 + 40) * U * np.abs(zl) + U * np.abs(want)
+    assert (np.abs(got.double().cpu().numpy() - want) <= tol + 1e-37).all()
+
+
 def test_choice_bwd_drops_bad_indices_and_adds_repeated_ones():
     T, E, k = 5, 40, 4
     g = torch.Generator().manual_seed(5)
