@@ -700,7 +700,7 @@ extern "C" int moe_router_logits(const moe_bf16* x, const float* W_r, int64_t T,
     if (T <= 0 || d <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || d % 128 != 0) return MOE_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(W_r)) return MOE_ERR_INVALID_ARG;
-    if (!ws) return MOE_ERR_WORKSPACE;
+    if (!ws || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     WsCarver wc(ws, ws_bytes);
     const int epad = route_tc_epad(E);
     int64_t nzp = route_blocks(T);
@@ -732,7 +732,7 @@ extern "C" int moe_router_dw(const float* dlogits, const moe_bf16* x, int64_t T,
     if (T <= 0 || d <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || d % 128 != 0) return MOE_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(dW_r)) return MOE_ERR_INVALID_ARG;
-    if (!ws) return MOE_ERR_WORKSPACE;
+    if (!ws || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     WsCarver wc(ws, ws_bytes);
     const int np = route_tc_np(E);
     int64_t nsplit = route_bwd_splits(T);

@@ -434,8 +434,9 @@ def moe_rms_norm_bwd(dy, dres, z, rstd, w, dz, dx, dw, ws, stream=None):
     T, d = shape = _rows("dy", dy)
     dev = _device(dy)
     rt, zt, bf16, f32 = _res_type("z", z), z.dtype, torch.bfloat16, torch.float32
+    dyp = _ptr("dy", dy, bf16, shape, dev)
     wp, wn = _ws(ws, dev)
-    _check(_lib.load().moe_rms_norm_bwd(_ptr("dy", dy, bf16, shape, dev),
+    _check(_lib.load().moe_rms_norm_bwd(dyp,
                                         _opt("dres", dres, zt, shape, dev),
                                         _ptr("z", z, zt, shape, dev), rt,
                                         _ptr("rstd", rstd, f32, (T,), dev),
@@ -451,8 +452,9 @@ def moe_router_logits(x, W_r, logits, ws, lse=None, z_loss=None, z_coef=0.0, str
     T, d = shape = _rows("x", x)
     E = _rows("W_r", W_r)[0]
     dev, f32 = _device(x), torch.float32
+    xp = _ptr("x", x, torch.bfloat16, shape, dev)
     wp, wn = _ws(ws, dev)
-    _check(_lib.load().moe_router_logits(_ptr("x", x, torch.bfloat16, shape, dev),
+    _check(_lib.load().moe_router_logits(xp,
                                          _ptr("W_r", W_r, f32, (E, d), dev), T, d, E, z_coef,
                                          _ptr("logits", logits, f32, (T, E), dev),
                                          _opt("lse", lse, f32, (T,), dev),
@@ -465,8 +467,9 @@ def moe_router_dw(dlogits, x, dW_r, ws, stream=None):
     T, E = _rows("dlogits", dlogits)
     d = _rows("x", x)[1]
     dev, f32 = _device(dlogits), torch.float32
+    dlp = _ptr("dlogits", dlogits, f32, (T, E), dev)
     wp, wn = _ws(ws, dev)
-    _check(_lib.load().moe_router_dw(_ptr("dlogits", dlogits, f32, (T, E), dev),
+    _check(_lib.load().moe_router_dw(dlp,
                                      _ptr("x", x, torch.bfloat16, (T, d), dev), T, d, E,
                                      _ptr("dW_r", dW_r, f32, (E, d), dev), wp, wn,
                                      _stream_of(stream, dev)), "moe_router_dw")
@@ -522,18 +525,20 @@ def _grad_list(name, ts, dev):
     return ptr, numel, types
 
 
-def _clip_args(grads, dev):
-    """_grad_list as host arrays for the library, and the lists."""
+def _clip_args(grads, norm):
+    """_grad_list as host arrays for the library, the lists, and the device that norm lies on."""
+    if norm is None:
+        raise MoEError("norm is missing")
+    dev = _device(norm)
     ptr, numel, types = lists = _grad_list("grads", grads, dev)
     n = len(ptr)
-    return (ctypes.c_void_p * n)(*ptr), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), lists
+    return (ctypes.c_void_p * n)(*ptr), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), lists, dev
 
 
 def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
     """norm[0] = the global 2-norm of a list of bf16 or fp32 gradients, norm[1] = the factor that
     clips it to max_norm."""
-    dev = _device(norm)
-    ptr, numel, types, _ = _clip_args(grads, dev)
+    ptr, numel, types, _, dev = _clip_args(grads, norm)
     wp, wn = _ws(ws, dev)
     _check(_lib.load().moe_grad_norm(ptr, numel, types, len(grads), max_norm,
                                      _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
@@ -542,8 +547,7 @@ def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
 
 def moe_clip_grads(grads, max_norm, out, norm, ws, stream=None):
     """moe_grad_norm, and out[i] = norm[1] * grads[i]; out None clips in place."""
-    dev = _device(norm)
-    ptr, numel, types, lists = _clip_args(grads, dev)
+    ptr, numel, types, lists, dev = _clip_args(grads, norm)
     optr = ptr
     if out is not None:
         if len(out) != len(grads):

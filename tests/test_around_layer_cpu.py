@@ -170,3 +170,25 @@ def test_binding_refuses_wrong_tensors():
         ops.moe_router_dw(torch.zeros(4, 2), x, torch.zeros(2, 16), ws)
     with pytest.raises(ops.MoEError, match="CUDA tensor"):
         ops.moe_rms_norm_bwd(x, None, x, torch.zeros(4), w, y, None, torch.zeros(16), ws)
+
+
+@needs_nvcc
+def test_router_entries_refuse_a_misaligned_workspace(lib):
+    """Their sums and pieces are read as whole vectors."""
+    assert lib.moe_router_logits(P, P, 16, 256, 8, 0.0, P, None, None, BAD, 1 << 20, None) == WORKSPACE
+    assert lib.moe_router_dw(P, P, 16, 256, 8, P, BAD, 1 << 20, None) == WORKSPACE
+
+
+def test_binding_names_the_missing_tensor():
+    """The first wrong argument is the one that is named, whatever the workspace is."""
+    with pytest.raises(ops.MoEError, match="norm is missing"):
+        ops.moe_clip_grads([torch.zeros(4)], 1.0, None, None, torch.zeros(16384, dtype=torch.uint8))
+    with pytest.raises(ops.MoEError, match="norm is missing"):
+        ops.moe_grad_norm([torch.zeros(4)], 1.0, None, torch.zeros(16384, dtype=torch.uint8))
+    x, ws = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(16384, dtype=torch.uint8)
+    with pytest.raises(ops.MoEError, match="dy must be a CUDA tensor"):
+        ops.moe_rms_norm_bwd(x, None, x, torch.zeros(4), torch.ones(16), x, None, torch.zeros(16), ws)
+    with pytest.raises(ops.MoEError, match="x must be a CUDA tensor"):
+        ops.moe_router_logits(x, torch.zeros(2, 16), torch.zeros(4, 2), ws)
+    with pytest.raises(ops.MoEError, match="dlogits must be a CUDA tensor"):
+        ops.moe_router_dw(torch.zeros(4, 2), x, torch.zeros(2, 16), ws)
