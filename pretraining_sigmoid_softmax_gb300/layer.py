@@ -13,6 +13,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -520,6 +521,7 @@ class _RMSNormFunction(torch.autograd.Function):
         return y if z is None else (y, z)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dres=None):
         z, rstd, w = ctx.saved_tensors
         if dy is None:  # only z was used: its gradient is the residual's and x's

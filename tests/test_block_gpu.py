@@ -192,6 +192,15 @@ def test_norm_module_alone():
         norm(x, r[:5])
 
 
+def test_norm_refuses_a_second_derivative():
+    """Its backward is a kernel: autograd cannot go through it again, and says so."""
+    norm = RMSNorm(256)
+    x = torch.randn(4, 256, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    g, = torch.autograd.grad(norm(x)[0].float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.float().sum().backward()
+
+
 def test_layer_refuses_what_it_cannot_do():
     for kw in (dict(n_group=3), dict(n_group=4, topk_group=5), dict(n_group=4, topk_group=1, k=5),
                dict(group_rule="sum"), dict(gate_scale=0.0), dict(gate_scale=-1.0)):
