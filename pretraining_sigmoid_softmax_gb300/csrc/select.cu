@@ -115,9 +115,9 @@ __device__ __forceinline__ void row_softmax(const float* row, int E, int lane, f
 constexpr float kSmallSum = 9.5367432e-7f;  // 2^-20
 
 // Scores and gates of the chosen experts, stored with the indices: lane `sub` < k of the L lanes
-// of a token holds slot `sub`'s expert and that expert's logit. `live` masks tokens that are not there, or whose choice
-// is made elsewhere. A token whose chosen scores are all zero (in 64 bits) has gates of zero.
-// Executed by the whole warp.
+// of a token holds slot `sub`'s expert and that expert's logit. `live` masks tokens that are not
+// there, or whose choice is made elsewhere. A token whose chosen scores are all zero (in 64 bits)
+// has gates of zero. Executed by the whole warp.
 template <int L>
 __device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int sub, bool live, int my_e,
                                        float l, float mx, float sum) {
@@ -143,6 +143,12 @@ __device__ __forceinline__ void finish(const SelectParams& P, int64_t t, int sub
         P.score[t * P.k + sub] = s;
     }
     if (live && sub == 0 && !sigmoid && P.lse) P.lse[t] = mx + logf(sum);
+}
+
+// The same for one token by a whole warp, in the paths that are taken seldom.
+__device__ __noinline__ void finish_token(const SelectParams& P, int64_t t, int lane, int my_e, float l, float mx,
+                                          float sum) {
+    finish<32>(P, t, lane, true, my_e, l, mx, sum);
 }
 
 // Total order of the choice: larger value, then lower index. An index of INT_MAX marks "none".
@@ -179,6 +185,21 @@ __device__ __forceinline__ void warp_top2(double& a, double& b) {
 }
 
 __device__ __forceinline__ double no_nan(double v) { return v == v ? v : -INFINITY; }
+
+// A score in 64 bits; total: the softmax's sum. One copy of the code, which runs seldom and cold.
+__device__ __noinline__ double score64(bool sigmoid, float l, float mx, double total) {
+    const double e = exp(sigmoid ? -(double)l : (double)l - (double)mx);
+    return (sigmoid ? 1.0 : e) / (sigmoid ? 1.0 + e : total);
+}
+
+// Integers in the order of 64-bit values (of which none is NaN); -0 and 0 are one.
+__device__ __forceinline__ long long order_of(double v) {
+    const long long b = __double_as_longlong(v + 0.0);
+    return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+__device__ __forceinline__ bool ahead_of(long long v1, int i1, long long v2, int i2) {
+    return v1 > v2 || (v1 == v2 && i1 < i2);
+}
 
 // One token's choice in 64 bits by one warp; lane i < k returns slot i's expert. Any expert
 // count up to 256 and any grouping. Lane `lane` holds the experts lane, lane + 32, ...
@@ -278,7 +299,7 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
     float mx = 0.f, sum = 1.f;
     if (P.mode == MOE_MODE_SOFTMAX) row_softmax(P.logits + t * P.E, P.E, lane, mx, sum);
     const int my_e = select_exact(P, t, lane, mx);
-    finish<32>(P, t, lane, true, my_e, lane < P.k ? P.logits[t * P.E + my_e] : 0.f, mx, sum);
+    finish_token(P, t, lane, my_e, lane < P.k ? P.logits[t * P.E + my_e] : 0.f, mx, sum);
 }
 
 // ------------------------------------------------------------------- the choice from 32 bits
@@ -291,10 +312,18 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
 // that halves what a lane holds at each step (or, for more lanes, from k rounds that take the
 // largest of the lanes' first keys).
 //
-// The keys are rounded values. Where two of them that the choice has to tell apart lie within
-// the rounding's bound, the token is chosen again by select_close: groups and experts near the
-// border are evaluated in 64 bits and ranked. Rows that are not for this arithmetic (NaN,
-// infinities, more than 32 experts near the border) are chosen in 64 bits throughout.
+// The keys are rounded values. Where two that the choice has to tell apart lie within the
+// rounding's bound, exact ones decide: of chosen experts whose order alone is open, each slot's
+// lane evaluates its own; where it is open which groups or experts are chosen, the warp chooses that
+// token again by select_close, which evaluates those near the border in 64 bits. Rows that are
+// not for this arithmetic (NaN, infinities, more than 32 experts near the border) are chosen in
+// 64 bits throughout.
+//
+// Bound by instruction issue: 65,536 tokens of 256 experts in 8 groups take 36 us (4.8 us per step
+// of four tokens and warp, 1200 instructions; 16 warps per SM at 128 registers), 29 us where no
+// token comes near a border and 10.8 us for their bytes. A token chosen again takes 2 to 5 us of
+// latency, a 64-bit instruction 64 cycles per warp: so those are few, and their code is kept
+// small, since it runs cold.
 //
 // With a bias the value is s + (b - base), base the smallest bias within 16 of the largest, s by
 // the fast exponential and reciprocal, scaled so that it lies below 1 and clamped at 0. Without
@@ -365,14 +394,14 @@ __device__ __forceinline__ float bias_base(const float (&b)[kMaxExperts / 32], f
     return lo;
 }
 
-// One token whose keys left its choice open, by a whole warp, from its logits in shared memory.
-// Groups (unless they are settled: bit g of `open`, group g stays): lane g finds group g's
-// largest values, evaluates in 64 bits those that may be its two largest, and the groups are
-// ranked. Experts: without a bias the logits' own order; else those that may be among the k
-// largest of the open groups are gathered, one per lane, evaluated in 64 bits and ranked. False
-// where that does not settle it (more than three candidates for a group's two, or more than 32
-// for the k): the token is then left to select_token. `kth`: a value that the k-th largest of the
-// open groups reaches, where the groups are settled.
+// One token whose keys left open which groups or experts are chosen, by a whole warp, from its
+// logits in shared memory. Groups (unless they are settled: bit g of `open`, group g stays): lane
+// g finds group g's largest values, those that may be its two largest are evaluated in 64 bits,
+// and the groups are ranked. Experts: without a bias the logits' own order; else those that may
+// be among the k largest of the open groups are gathered, one per lane, evaluated in 64 bits and
+// ranked. False where that does not settle it (more than three candidates for a group's two, or
+// more than 32 for the k): the token is then left to select_token. `kth`: a value that the k-th
+// largest of the open groups reaches, where the groups are settled.
 template <bool LOGIT>
 __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, float base,
                                           const float* row, bool settled, uint32_t open, float kth,
@@ -397,72 +426,78 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
         inv = fast_rcp(sum);
         if (!LOGIT) {
             total = 0.0;
-            for (int j = 0; j < VJ; ++j)
-                if (lane + 32 * j < E) total += exp((double)l[j] - (double)mx);
+#pragma unroll 1
+            for (int e = lane; e < E; e += 32) total += exp((double)row[e] - (double)mx);
             total = seg_sum<32>(total);
         }
     }
     const float es = score_err(sigmoid, inv);
-    auto value_of = [&](float x, int e) { return fmaxf(fast_score(sigmoid, x, mx, inv) + (P.b[e] - base), 0.f); };
-    auto value = [&](int e) { return value_of(row[e], e); };
-    auto score64 = [&](int e) {
-        const double x = row[e];
-        return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx) / total;
-    };
-    auto value64 = [&](int e) { return no_nan(score64(e) + (double)P.b[e]); };
-
-    if (!settled) {
-        double gs = -INFINITY;
-        bool unsettled = false;
-        if (lane < G) {
-            float a = -INFINITY, b = -INFINITY, c = -INFINITY, d = -INFINITY;  // the four largest
-            int ia = -1, ib = -1, ic = -1;
-            for (int e = lane * per; e < (lane + 1) * per; ++e) {
-                const float v = LOGIT ? (row[e] == row[e] ? row[e] : -INFINITY) : value(e);
-                if (v > a || ia < 0) {
-                    d = c, c = b, b = a, a = v;
-                    ic = ib, ib = ia, ia = e;
-                } else if (v > b || ib < 0) {
-                    d = c, c = b, b = v;
-                    ic = ib, ib = e;
-                } else if (v > c || ic < 0) {
-                    d = c, c = v;
-                    ic = e;
-                } else {
-                    d = fmaxf(d, v);
-                }
-            }
-            if (LOGIT) {
-                gs = top2 ? score64(ia) + score64(ib) : (double)a;
-            } else {
-                // the two largest (or the largest) are among the first three unless the fourth
-                // may reach them
-                const float least = top2 ? b : a;
-                unsettled = per > 3 && !(least - d > value_gap(least, es));
-                double x = value64(ia);
-                double y = per > 1 ? value64(ib) : -INFINITY, z = per > 2 ? value64(ic) : -INFINITY;
-                if (y > x) { const double q = x; x = y; y = q; }
-                y = fmax(y, fmin(x, z));
-                x = fmax(x, z);
-                gs = top2 ? no_nan(x + y) : x;
-            }
-        }
-        if (__any_sync(kFull, unsettled)) return false;
-        int rank = 0;
-        for (int h = 0; h < G; ++h) {
-            const double o = __shfl_sync(kFull, gs, h);
-            rank += before(o, h, gs, lane) ? 1 : 0;
-        }
-        open = __ballot_sync(kFull, lane < G && rank < P.topk_group);
-    }
-
-    int key[VJ];  // closed groups and places past the last expert: INT_MIN, below every value
+    auto value64 = [&](int e) { return no_nan(score64(sigmoid, row[e], mx, total) + (double)P.b[e]); };
+    int key[VJ];  // INT_MIN, below every value, past the last expert
 #pragma unroll
     for (int j = 0; j < VJ; ++j) {
         const int e = lane + 32 * j;
         key[j] = INT_MIN;
-        if (e < E && ((open >> (e / per)) & 1u)) key[j] = LOGIT ? logit_key(l[j]) : __float_as_int(value_of(l[j], e));
+        if (e >= E) continue;
+        key[j] = LOGIT ? logit_key(l[j])
+                       : __float_as_int(fmaxf(fast_score(sigmoid, l[j], mx, inv) + (P.b[e] - base), 0.f));
+        if (!settled) scratch[e] = key[j];
     }
+    if (!settled) {
+        __syncwarp();
+        int a = INT_MIN, b = INT_MIN, c = INT_MIN, d = INT_MIN;  // lane g: group g's four largest
+        int ia = -1, ib = -1, ic = -1;
+        if (lane < G) {
+#pragma unroll 4
+            for (int e = lane * per; e < (lane + 1) * per; ++e) {
+                const int v = scratch[e];
+                const bool A = v > a, B = v > b, C = v > c;
+                d = C ? c : max(d, v);
+                c = B ? b : C ? v : c;
+                ic = B ? ib : C ? e : ic;
+                b = A ? a : B ? v : b;
+                ib = A ? ia : B ? e : ib;
+                a = A ? v : a;
+                ia = A ? e : ia;
+            }
+        }
+        double gs = -INFINITY;
+        if (LOGIT) {
+            if (lane < G)
+                gs = top2 ? score64(sigmoid, row[ia], mx, total) + score64(sigmoid, row[ib], mx, total)
+                          : no_nan((double)row[ia]);
+        } else {
+            // the two largest (or the largest) are among the first three unless the fourth may
+            // reach them
+            const float least = __int_as_float(top2 ? b : a);
+            const bool unsettled = lane < G && per > 3 && !(least - __int_as_float(d) > value_gap(least, es));
+            if (__any_sync(kFull, unsettled)) return false;
+            // three candidates a group, all of them at once where there are lanes for that
+            double v[3];
+            if (3 * G <= 32) {
+                const int h = lane % G, q = lane / G;
+                const int ea = __shfl_sync(kFull, ia, h), eb = __shfl_sync(kFull, ib, h), ec = __shfl_sync(kFull, ic, h);
+                const int e = q == 0 ? ea : q == 1 ? eb : q == 2 ? ec : -1;
+                const double x = e < 0 ? -INFINITY : value64(e);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(kFull, x, h + i * G);
+            } else {
+                v[0] = ia < 0 ? -INFINITY : value64(ia);
+                v[1] = ib < 0 ? -INFINITY : value64(ib);
+                v[2] = ic < 0 ? -INFINITY : value64(ic);
+            }
+            const double x = fmax(v[0], v[1]), y = fmin(v[0], v[1]);
+            if (lane < G) gs = top2 ? no_nan(fmax(x, v[2]) + fmax(y, fmin(x, v[2]))) : fmax(x, v[2]);
+        }
+        int rank = 0;
+        const long long mine = order_of(gs);
+        for (int h = 0; h < G; ++h) rank += ahead_of(__shfl_sync(kFull, mine, h), h, mine, lane);
+        open = __ballot_sync(kFull, lane < G && rank < P.topk_group);
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < VJ; ++j)  // closed groups
+        if (lane + 32 * j < E && !((open >> ((lane + 32 * j) / per)) & 1u)) key[j] = INT_MIN;
     int my_e = 0;
     if (LOGIT || !settled) {  // (where the groups were settled, kth is known)
         uint32_t taken = 0;
@@ -496,24 +531,20 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
         if (n > 32 || n < k) return false;
         __syncwarp();
         int e = INT_MAX;
-        double x = 0.0;
+        long long x = 0;
         if (lane < n) {
             e = scratch[lane];
-            x = value64(e);
+            x = order_of(value64(e));
         }
         int rank = 0;
-        for (int i = 0; i < n; ++i) {
-            const double ox = __shfl_sync(kFull, x, i);
-            const int oe = __shfl_sync(kFull, e, i);
-            rank += before(ox, oe, x, e) ? 1 : 0;
-        }
+        for (int i = 0; i < n; ++i) rank += ahead_of(__shfl_sync(kFull, x, i), __shfl_sync(kFull, e, i), x, e);
         __syncwarp();
         if (lane < n && rank < k) scratch[rank] = e;
         __syncwarp();
         my_e = lane < k ? scratch[lane] : 0;
         __syncwarp();
     }
-    finish<32>(P, t, lane, true, my_e, lane < k ? row[my_e] : 0.f, mx, sum);
+    finish_token(P, t, lane, my_e, lane < k ? row[my_e] : 0.f, mx, sum);
     return true;
 }
 
@@ -610,7 +641,7 @@ template <int L, int NB, bool LOGIT, bool VEC>
 __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectParams P, const SelectLayout Y) {
     constexpr int NT = 32 / L;
     extern __shared__ __align__(16) float smem[];  // biases, then two buffers of rows per warp
-    __shared__ int scratch[kSelWarps][32];
+    __shared__ int scratch[kSelWarps][kMaxExperts];
     __shared__ int taken;  // steps of the CTA's run that its warps have taken
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
@@ -623,8 +654,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     float* const bias = smem;  // (b - base) times the values' scale
     float* const rows = smem + (LOGIT ? 0 : pitch) + warp * 2 * NT * pitch;
 
-    // The CTA's tokens are a run of steps of NT tokens, which its warps take one by one (a token
-    // chosen again delays its warp alone).
+    // The CTA's tokens are a run of steps of NT tokens, which its warps take one by one: a token
+    // chosen again delays its warp alone.
     const int64_t steps = (P.T + NT - 1) / NT;
     const int64_t s0 = blockIdx.x * steps / gridDim.x;
     const int n = (int)((blockIdx.x + 1) * steps / gridDim.x - s0);
@@ -668,7 +699,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     const int turn = VEC ? (sub * Y.vr / 32) % nvec : 0;
     const uint32_t mask = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (lane / L * L);
     const int my_slot = L == 8 ? (int)(kSlotOfLane >> (4 * sub)) & 7 : sub;
-    const int next_lane = L == 8 ? (int)(kLaneOfSlot >> (4 * ((my_slot + 1) & 7))) & 7 : sub + 1;
+    auto slot_lane = [](int slot) { return L == 8 ? (int)(kLaneOfSlot >> (4 * (slot & 7))) & 7 : slot; };
+    const int next_lane = slot_lane(my_slot + 1);
 
     for (int buf = 0; step < n; buf ^= 1) {
         const int ahead = take();
@@ -854,16 +886,35 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 }
             }
         }
-        const int my_e = min(mine & 255, E - 1);  // (of a key that is none: not used)
-        const bool slot_on = my_slot < k;
+        int my_e = min(mine & 255, E - 1);  // (of a key that is none: not used)
         // each slot's key against the next one's (the last slot's against the best one left)
         int next = __shfl_sync(kFull, mine, lane / L * L + (next_lane < L ? next_lane : 0));
         if (my_slot == L - 1 || (L > 8 && my_slot == k - 1)) next = last;
-        bool close = slot_on && units_of(mine) - units_of(next) <= tol;
+        const bool close = units_of(mine) - units_of(next) <= tol;
+        const bool inside = close && my_slot < k - 1;
+        bool border = close && my_slot == k - 1;
         // a lane whose eight are all chosen may hold the ninth of them
-        const int kth = __shfl_sync(kFull, mine, lane / L * L + (L == 8 ? (int)(kLaneOfSlot >> (4 * (k - 1))) & 7 : k - 1));
-        close |= NB > 1 && count > 8 && eighth >= kth;
-        const uint32_t again = __ballot_sync(kFull, live && (odd || groups || close || infinite));
+        const int kth = __shfl_sync(kFull, mine, lane / L * L + slot_lane(k - 1));
+        border |= NB > 1 && count > 8 && eighth >= kth;
+        const bool lost = odd || groups || border || infinite || (!LOGIT && !sigmoid && inside);
+        const uint32_t again = __ballot_sync(kFull, live && lost);
+        if ((LOGIT || sigmoid) && __any_sync(kFull, live && inside)) {
+            // the chosen ones are settled, their order is not: by their own values
+            long long x;
+            if (LOGIT) x = logit_key(held[my_e]);
+            else x = order_of(no_nan(score64(true, held[my_e], 0.f, 1.0) + (double)P.b[my_e]));
+            int rank = 0, e = my_e;
+            for (int i = 0; i < k; ++i) {
+                const int from = lane / L * L + slot_lane(i);
+                rank += ahead_of(__shfl_sync(kFull, x, from), __shfl_sync(kFull, my_e, from), x, my_e);
+            }
+            for (int i = 0; i < k; ++i) {
+                const int from = lane / L * L + slot_lane(i);
+                const int r = __shfl_sync(kFull, rank, from), o = __shfl_sync(kFull, my_e, from);
+                if (r == my_slot) e = o;
+            }
+            my_e = e;
+        }
         finish<L>(P, t, my_slot, live && !(again & mask), my_e, held[my_e], mx, sum);
         if (again) {
             const uint32_t strange = __ballot_sync(kFull, live && (odd || infinite));
@@ -1045,7 +1096,7 @@ int launch_lanes(const SelectParams& P, const SelectLayout& Y, bool vec, cudaStr
     if (blocks > cap) blocks = cap;
     auto kern = vec ? (P.b ? select_kernel<L, NB, false, true> : select_kernel<L, NB, true, true>)
                     : (P.b ? select_kernel<L, NBMAX, false, false> : select_kernel<L, NBMAX, true, false>);
-    if (smem > 40 * 1024 &&
+    if (smem > 36 * 1024 &&  // (beside the kernel's own 8 KB)
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MOE_ERR_LAUNCH;
     kern<<<(unsigned)blocks, kSelWarps * 32, smem, st>>>(P, Y);
