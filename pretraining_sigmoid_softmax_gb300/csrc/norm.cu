@@ -6,8 +6,10 @@
 // Backward, with xhat = z rstd and g = dy w: dz = rstd (g - xhat mean(g xhat)) + dres,
 // dw = sum over tokens of dy xhat.
 //
-// Both are bound by HBM: every tensor is read or written once. A row stays in registers
-// between its loads and its stores.
+// Both are bound by HBM: every tensor is read or written once. A row stays in registers (forward)
+// or shared memory (backward) between its loads and its stores, and the sum of squares and the
+// row's largest value come from one pass. Times below are of launches in a graph, fractions of
+// the rate at which a plain copy moves the same bytes (6.78 TB/s).
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -119,6 +121,10 @@ __device__ __forceinline__ uint2 codes8_of(const float (&q)[8]) {
 // y = (z w) rstd, so the largest |y| is rstd times the largest |z w|, which is known together with
 // the sum of squares: one reduction, one barrier. In the quotient of the codes rstd cancels:
 // y / sy = z w (448 / max |z w|), a product with one factor per row.
+//
+// 65,536 x 4096 with an fp32 stream and codes (3.49 GB): 496 us, 1.04 of a copy; with a bf16 stream
+// and codes 368 us, 0.97; 8191 x 1024 bf16 (67 MB): 13.6 us, 0.73, of which 2.4 us are those of
+// a launch with one row.
 template <typename R, int VPT, bool CODES>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(
     const __nv_bfloat16* x, const R* res, const float* __restrict__ w, float eps, int64_t T, int d,
@@ -198,6 +204,9 @@ __device__ __forceinline__ void cp_wait() {
 // only what its own warp copied), so loads stay in flight across the row's reduction. It keeps the
 // partial sums of dw for its own columns over all rows, so dw costs no traffic per row: the CTA's
 // sums are written once, and norm_dw_kernel adds them in the CTAs' order.
+//
+// 65,536 x 4096 with norm_dw_kernel: bf16 stream (2.15 GB) 323 us, 0.98 of a copy; fp32 stream with
+// the bf16 dx 632 us, 1.00.
 template <typename R, int VPT, int STAGES>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const R* dres, const R* __restrict__ z,
@@ -305,6 +314,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(
 // next rows ahead and reads a row from shared memory twice, for the dot product and for the
 // gradient, instead of holding 64 values a thread across the reduction. The CTA's warps add their
 // sums of dw in their order at the end.
+//
+// 8192 x 1024 bf16 with norm_dw_kernel (67 MB): 15.8 us, 0.63 of a copy (a CTA per row with the ring
+// above: 26.5); 16,384 x 1024 fp32 46 us, 0.86; 65,536 x 256 bf16 28 us, 0.71. What is short of
+// the copy is the launch, the first rows' latency and the sums of dw, 4.5 us in all.
 constexpr int kRowWarps = 4;
 
 template <typename R, int VPT, int STAGES>
@@ -419,7 +432,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) norm_bwd_rows_kernel(
     }
 }
 
-// Rows too wide for the ring: the same sums, with plain loads and up to 1024 threads.
+// Rows too wide for the ring: the same sums, with plain loads and up to 1024 threads. A row's second
+// reading comes from L2, and its dw sums are read and written there too: 8192 x 16,384 bf16 takes
+// 265 us, 0.60 of a copy.
 template <typename R, int VPT>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
     const __nv_bfloat16* __restrict__ dy, const R* dres, const R* __restrict__ z,
@@ -475,7 +490,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
 
 // dw[j] = sum of part[r][j] over r < rows: blocks of 32 columns (eight 16-byte vectors) x 128 row
 // strands, each strand summed in order, then the strands by a tree. The few rows of a strand
-// are loaded together: the launch is all latency.
+// are loaded together: the launch is all latency (4.5 us alone, about half of it behind the kernel
+// before, whose last CTAs it waits for).
 constexpr int kDwStrands = 128;
 
 __global__ void __launch_bounds__(8 * kDwStrands) norm_dw_kernel(const float* __restrict__ part, int rows,

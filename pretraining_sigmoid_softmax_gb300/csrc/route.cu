@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(256) route_bwd_dwr_kernel(
 }
 
 // The three bf16 pieces of a logit gradient [T, E] for the tensor-core dW_r: piece p at
-// dl3 + p * pstride as a [T, np] matrix (zero past E), as route_bwd_dlogits_kernel writes them.
+// dl3 + p * pstride as a [T, np] matrix (zero past E), as route_bwd_dlogits_kernel writes them. A few
+// bytes per element beside the contraction that reads x: simple loads and stores do.
 __global__ void __launch_bounds__(256) split3_cols_kernel(const float* __restrict__ dlogits,
                                                           int64_t T, int E, int np, int64_t pstride,
                                                           __nv_bfloat16* __restrict__ dl3) {

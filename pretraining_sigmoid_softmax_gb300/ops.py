@@ -4,6 +4,7 @@ the layer is computed here."""
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 
@@ -531,8 +532,12 @@ def _clip_args(grads, norm):
         raise MoEError("norm is missing")
     dev = _device(norm)
     ptr, numel, types = lists = _grad_list("grads", grads, dev)
-    n = len(ptr)
-    return (ctypes.c_void_p * n)(*ptr), (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), lists, dev
+    return array("Q", ptr), array("q", numel), array("i", types), lists, dev
+
+
+def _at(a):
+    """The address of a host array's elements (the caller keeps the array)."""
+    return a.buffer_info()[0]
 
 
 def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
@@ -540,7 +545,7 @@ def moe_grad_norm(grads, max_norm, norm, ws, stream=None):
     clips it to max_norm."""
     ptr, numel, types, _, dev = _clip_args(grads, norm)
     wp, wn = _ws(ws, dev)
-    _check(_lib.load().moe_grad_norm(ptr, numel, types, len(grads), max_norm,
+    _check(_lib.load().moe_grad_norm(_at(ptr), _at(numel), _at(types), len(grads), max_norm,
                                      _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
                                      _stream_of(stream, dev)), "moe_grad_norm")
 
@@ -555,8 +560,8 @@ def moe_clip_grads(grads, max_norm, out, norm, ws, stream=None):
         o = _grad_list("out", out, dev)
         if o[1:] != lists[1:]:
             raise MoEError("every output must have its gradient's type and number of elements")
-        optr = (ctypes.c_void_p * len(out))(*o[0])
+        optr = array("Q", o[0])
     wp, wn = _ws(ws, dev)
-    _check(_lib.load().moe_clip_grads(ptr, optr, numel, types, len(grads), max_norm,
+    _check(_lib.load().moe_clip_grads(_at(ptr), _at(optr), _at(numel), _at(types), len(grads), max_norm,
                                       _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
                                       _stream_of(stream, dev)), "moe_clip_grads")
