@@ -947,9 +947,10 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
 //
 // Bound by writing dlogits. L lanes hold a token's slots (L >= k), so a warp forms the gradients of
 // 32 / L tokens at once; it scatters them into zeroed rows in shared memory and stores the rows
-// whole, since the tokens' rows are one piece of memory. 65,536 x 256 sigmoid (73 MB): 13.9 us, 0.78
-// of a copy of its bytes; 32,768 x 128 softmax without renormalised gates, where the logits are
-// read too (37 MB): 10.2 us, 0.54, the rest being launch and first loads.
+// whole, since the tokens' rows are one piece of memory. 65,536 x 256 sigmoid (73 MB): 13.5 us, 0.80
+// of a copy of its bytes; softmax without renormalised gates, where the logits are read too, 26.6
+// us, 0.78; 32,768 x 128 of that (37 MB) 9.0 us, 0.60, the rest being launch and first loads. Four
+// CTAs per SM and no more, 64 registers: at three 27.4 and 10.0 us, at five with spills 37.8 and 14.5.
 struct SelectBwdParams {
     const float* dg;
     const int32_t* idx;
@@ -964,8 +965,10 @@ struct SelectBwdParams {
     int* status;
 };
 
+constexpr int kBwdCtas = 4;  // per SM
+
 template <int L, bool DENSE>
-__global__ void __launch_bounds__(kSelWarps * 32) select_bwd_kernel(const SelectBwdParams P) {
+__global__ void __launch_bounds__(kSelWarps * 32, kBwdCtas) select_bwd_kernel(const SelectBwdParams P) {
     constexpr int NT = 32 / L;
     extern __shared__ __align__(16) float rows[];
     __shared__ float token_c[kSelWarps][NT], token_lse[kSelWarps][NT];
@@ -1136,7 +1139,7 @@ int launch_bwd_lanes(const SelectBwdParams& P, bool dense, cudaStream_t st) {
     constexpr int NT = 32 / L;
     const size_t smem = sizeof(float) * kSelWarps * ((NT * P.E + 3) / 4 * 4);  // 32 KB at most
     int64_t blocks = cdiv(P.T, (int64_t)kSelWarps * NT);
-    const int64_t cap = (int64_t)sm_count() * 6;  // resident CTAs
+    const int64_t cap = (int64_t)sm_count() * kBwdCtas;
     if (blocks > cap) blocks = cap;
     auto kern = dense ? select_bwd_kernel<L, true> : select_bwd_kernel<L, false>;
     kern<<<(unsigned)blocks, kSelWarps * 32, smem, st>>>(P);
