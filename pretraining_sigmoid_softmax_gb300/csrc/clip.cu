@@ -154,7 +154,8 @@ __device__ __forceinline__ int tensor_of(const ClipTable<N>& tab, int c) {
 
 // One partial sum of squares per CTA (added to the CTA's own from earlier launches of the call).
 // Four 16-byte loads a thread in flight: 2.4 GB in 360 us, 6.7 TB/s, the rate of a copy; 101 MB in
-// 28 us. (A ring of asynchronous copies to shared memory: 424 and 25 us.)
+// 24 us (28 with twice the CTAs, in two waves). Loads ahead of the sums, by a ring in shared memory
+// or in registers, take 424 to 428 us for 2.4 GB.
 template <int N>
 __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(
     const __grid_constant__ ClipTable<N> tab, int add, double* __restrict__ part) {
@@ -325,8 +326,10 @@ int fill(ClipTable<N>& tab, const void* const* g, void* const* out, const int64_
     return i;
 }
 
-int grid_for(int64_t chunks) {
-    int64_t cap = (int64_t)sm_count() * 4;  // CTAs of kClipThreads threads that an SM holds
+// CTAs for a table's chunks, `per_sm` at most: those that an SM holds at once by their registers.
+constexpr int kNormCtas = 2, kScaleCtas = 4;
+int grid_for(int64_t chunks, int per_sm) {
+    int64_t cap = (int64_t)sm_count() * per_sm;
     if (cap > kClipParts) cap = kClipParts;
     return (int)(chunks < 1 ? 1 : chunks < cap ? chunks : cap);
 }
@@ -338,7 +341,7 @@ int run_clip(const void* const* g, void* const* out, const int64_t* n, const int
     int nparts = 0, add = 0, launches = 0;
     for (int i = 0; i < count || launches == 0; ++launches) {
         i = fill(tab, g, nullptr, n, type, count, i);
-        int grid = grid_for(tab.chunks);
+        int grid = grid_for(tab.chunks, kNormCtas);
         if (add && grid > nparts) grid = nparts;  // a later launch adds to the sums of the first
         if (!add) nparts = grid;
         clip_norm_kernel<N><<<grid, kClipThreads, 0, st>>>(tab, add, part);
@@ -350,8 +353,8 @@ int run_clip(const void* const* g, void* const* out, const int64_t* n, const int
                                 nparts, max_norm, norm);
     for (int i = 0, l = 0; i < count || l == 0; ++l) {
         i = fill(tab, g, out, n, type, count, i);
-        const int rc = launch_dependent(clip_scale_kernel<N>, dim3(grid_for(tab.chunks)), dim3(kClipThreads),
-                                        0, st, tab, (const double*)part, nparts, max_norm, norm);
+        const int rc = launch_dependent(clip_scale_kernel<N>, dim3(grid_for(tab.chunks, kScaleCtas)),
+                                        dim3(kClipThreads), 0, st, tab, (const double*)part, nparts, max_norm, norm);
         if (rc != MOE_OK) return rc;
     }
     return MOE_OK;
