@@ -615,7 +615,8 @@ int moe_router_dw(const float* dlogits, const moe_bf16* x, int64_t T, int d, int
  * largest selection value are chosen; equal values: the lower index first. topk_score = s of
  * the chosen expert; topk_gate = scale * s, with renorm scale * s / sum of the chosen s (0
  * where that sum is 0 in 64 bits).
- * The choice is the one the values have in 64 bits, whatever the kernel's own rounding.
+ * The choice is the one the values have in 64 bits, whatever the kernel's own rounding. (Values
+ * or sums that differ by no more than their 64-bit rounding may come in either order.)
  * In : logits [T,E] fp32 (moe_route or moe_router_logits); b [E] fp32 or NULL. A logit of -inf
  *      has score 0; a bias of -inf keeps an expert out while there are others. Values that are
  *      NaN come last; every choice is of k distinct experts of [0,E) even so. In softmax mode a
