@@ -313,18 +313,18 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
 // largest of the lanes' first keys).
 //
 // The keys are rounded values. Where two that the choice has to tell apart lie within the
-// rounding's bound, exact ones decide: of chosen experts whose order alone is open, each slot's
-// lane evaluates its own; where it is open which groups or experts are chosen, the warp chooses that
-// token again by select_close, which evaluates those near the border in 64 bits. Rows that are
-// not for this arithmetic (NaN, infinities, more than 32 experts near the border) are chosen in
-// 64 bits throughout.
+// rounding's bound, the warp evaluates those near the border in 64 bits, one token at a time, and
+// ranks them: groups in settle_groups, the slots' experts in settle_slots. Rows that are not for
+// this arithmetic (NaN, infinities, more than 32 experts near the border) are chosen in 64 bits
+// throughout.
 //
-// Bound by instruction issue: 65,536 tokens of 256 experts in 8 groups take 36 us (4.8 us per step
-// of four tokens and warp, 1180 instructions; 16 warps per SM at 128 registers), 29 us where no
-// token comes near a border and 10.8 us for their bytes. 16,383 tokens of 160, softmax: 13.8 us, 9.5
-// without near ties. A token chosen again takes 2 to 5 us of
-// latency, a 64-bit instruction 64 cycles per warp: so those are few, and their code is kept
-// small, since it runs cold.
+// Bound by instruction issue: 65,536 tokens of 256 experts in 8 groups take 32 us (4.4 us per step
+// of four tokens and warp, 1190 instructions at 54% of the issue slots; 16 warps per SM at 128
+// registers), 29 us where no token comes near a border, 10.8 us for their bytes. 16,383 tokens of 160,
+// softmax: 13.0 us, 9.5 without near ties. A token near one took 6 to 11 us of latency when its
+// choice was made anew, nearly all of it instructions that the SM has not met before (a 64-bit one
+// also takes 64 cycles a warp): so what the keys have settled is kept, loops over its few
+// candidates stay rolled, and the 64-bit score is one piece of code.
 //
 // With a bias the value is s + (b - base), base the smallest bias within 16 of the largest, s by
 // the fast exponential and reciprocal, scaled so that it lies below 1 and clamped at 0. Without
@@ -350,10 +350,6 @@ __device__ __forceinline__ float fast_score(bool sigmoid, float l, float mx, flo
 __device__ __forceinline__ float score_err(bool sigmoid, float inv) {
     return sigmoid ? kSigmoidErr : kSoftmaxErr * inv + 0.6f * kU;
 }
-// How far below v another value has to lie to come after it for certain, where both are rounded
-// sums s + (b - base): twice the score's error and both sums' roundings (u each, twice).
-__device__ __forceinline__ float value_gap(float v, float es) { return 2.f * es + 4.2f * kU * v; }
-
 __device__ __forceinline__ int logit_key(float l) {
     const int b = __float_as_int((l == l ? l : -INFINITY) + 0.0f);
     return b ^ ((b >> 31) & 0x7fffffff);
@@ -361,7 +357,8 @@ __device__ __forceinline__ int logit_key(float l) {
 
 // The key of a value v = a x + b clamped to [0, 1) (a NaN to 0): v + 1 has v's 23 fixed-point
 // bits as its mantissa (rounded to half a unit); times 512 they are the key's upper bits, the
-// sign turned so that signed integers order the keys. `id` = expert + INT_MIN.
+// sign turned so that signed integers order the keys. `id` = expert + 1 + INT_MIN, so that INT_MIN is
+// no expert's key.
 constexpr int kKeyBits = 9;
 constexpr float kUnits = 8388608.f;  // per 1
 __device__ __forceinline__ int fixed_key(float x, float a, float b, int id) {
@@ -369,6 +366,7 @@ __device__ __forceinline__ int fixed_key(float x, float a, float b, int id) {
     asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(x), "f"(a), "f"(b));
     return __float_as_int(v + 1.0f) * (1 << kKeyBits) + id;
 }
+__device__ __forceinline__ int expert_of(int key) { return (key & ((1 << kKeyBits) - 1)) - 1; }
 __device__ __forceinline__ int units_of(int key) { return (int)((uint32_t)(key ^ INT_MIN) >> kKeyBits); }
 constexpr float kLogitRange = 16.f;
 constexpr float kBelowOne = 0.9990234f;  // 1 - 2^-10
@@ -395,26 +393,118 @@ __device__ __forceinline__ float bias_base(const float (&b)[kMaxExperts / 32], f
     return lo;
 }
 
-// One token whose keys left open which groups or experts are chosen, by a whole warp, from its
-// logits in shared memory. Groups (unless they are settled: bit g of `open`, group g stays): lane
-// g finds group g's largest values, those that may be its two largest are evaluated in 64 bits,
-// and the groups are ranked. Experts: without a bias the logits' own order; else those that may
-// be among the k largest of the open groups are gathered, one per lane, evaluated in 64 bits and
-// ranked. False where that does not settle it (more than three candidates for a group's two, or
-// more than 32 for the k): the token is then left to select_token. `kth`: a value that the k-th
-// largest of the open groups reaches, where the groups are settled.
+// The sum of e^(l - max) over a row in shared memory, in 64 bits.
+__device__ __noinline__ double softmax_total(const float* row, int E, int lane, float mx) {
+    double total = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) total += exp((double)row[e] - (double)mx);
+    return seg_sum<32>(total);
+}
+
+// Which groups of a token stay, where its keys leave that open, by a whole warp: lane g finds group
+// g's largest keys among the first four of the lanes that hold it (`keys`: eight per lane), those
+// that may be its two largest are evaluated in 64 bits, and the groups are ranked. False where
+// three candidates a group are not enough.
+__device__ __noinline__ bool settle_groups(const SelectParams& P, int lane, const float* row, const int* keys,
+                                           int lpg, int tol, float mx, uint32_t& open) {
+    const int G = P.n_group, per = P.E / G;
+    const bool sigmoid = P.mode == MOE_MODE_SIGMOID, top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
+    int a = INT_MIN, b = INT_MIN, c = INT_MIN, d = INT_MIN;
+    if (lane < G) {
+#pragma unroll 1
+        for (int h = 0; h < lpg; ++h) {
+            const int4 u = *reinterpret_cast<const int4*>(keys + (lane * lpg + h) * 8);
+            const int v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int x = min(a, v[q]), y = min(b, x), z = min(c, y);
+                a = max(a, v[q]);
+                b = max(b, x);
+                c = max(c, y);
+                d = max(d, z);
+            }
+        }
+    }
+    // the two largest (or the largest) are among the first three unless the fourth may reach them
+    if (__any_sync(kFull, lane < G && per > 3 && units_of(top2 ? b : a) - units_of(d) <= tol)) return false;
+    const double total = sigmoid ? 1.0 : softmax_total(row, P.E, lane, mx);
+    // three candidates a group, all of them at once where there are lanes for that
+    double v[3] = {-INFINITY, -INFINITY, -INFINITY};
+    const int step = 3 * G <= 32 ? 3 : 1, h = lane % G, q = lane / G;
+#pragma unroll 1
+    for (int i = 0; i < 3; i += step) {
+        const int ka = __shfl_sync(kFull, a, h), kb = __shfl_sync(kFull, b, h), kc = __shfl_sync(kFull, c, h);
+        const int which = step == 3 ? q : i, k = which == 0 ? ka : which == 1 ? kb : which == 2 ? kc : INT_MIN;
+        double x = -INFINITY;
+        if (k != INT_MIN) x = no_nan(score64(sigmoid, row[expert_of(k)], mx, total) + (double)P.b[expert_of(k)]);
+        if (step == 3) {
+#pragma unroll
+            for (int r = 0; r < 3; ++r) v[r] = __shfl_sync(kFull, x, h + r * G);
+        } else {
+            v[0] = i == 0 ? x : v[0];
+            v[1] = i == 1 ? x : v[1];
+            v[2] = i == 2 ? x : v[2];
+        }
+    }
+    double gs = -INFINITY;
+    if (lane < G) {
+        const double x = fmax(v[0], v[1]), y = fmin(v[0], v[1]);
+        gs = top2 ? no_nan(fmax(x, v[2]) + fmax(y, fmin(x, v[2]))) : fmax(x, v[2]);
+    }
+    int rank = 0;
+    const long long mine = order_of(gs);
+    for (int g = 0; g < G; ++g) rank += ahead_of(__shfl_sync(kFull, mine, g), g, mine, lane);
+    open = __ballot_sync(kFull, lane < G && rank < P.topk_group);
+    return true;
+}
+
+// Which experts a token's slots hold, where the keys leave their order or the last one open, by a
+// whole warp: those of its lanes' keys that may be among the k largest are gathered, one per lane,
+// evaluated (without a bias: the logits themselves) and ranked; list[i] = slot i's expert. False where
+// they are more than 32.
 template <bool LOGIT>
-__device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int lane, float base,
-                                          const float* row, bool settled, uint32_t open, float kth,
-                                          int* scratch) {
+__device__ __noinline__ bool settle_slots(const SelectParams& P, int lane, const float* row, const int* keys,
+                                          int nkeys, int least, float mx, int* list) {
+    const bool sigmoid = P.mode == MOE_MODE_SIGMOID;
+    int n = 0;
+#pragma unroll 1
+    for (int c = lane; c < nkeys; c += 32) {
+        const int key = keys[c];
+        const bool in = key != INT_MIN && units_of(key) >= least;
+        const uint32_t m = __ballot_sync(kFull, in);
+        const int at = n + __popc(m & ((1u << lane) - 1u));
+        if (in && at < 32) list[at] = expert_of(key);
+        n += __popc(m);
+    }
+    if (n > 32 || n < P.k) return false;
+    const double total = LOGIT || sigmoid ? 1.0 : softmax_total(row, P.E, lane, mx);
+    __syncwarp();
+    int e = INT_MAX;
+    long long x = 0;
+    if (lane < n) {
+        e = list[lane];
+        if (LOGIT) x = logit_key(row[e]);
+        else x = order_of(no_nan(score64(sigmoid, row[e], mx, total) + (double)P.b[e]));
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += ahead_of(__shfl_sync(kFull, x, i), __shfl_sync(kFull, e, i), x, e);
+    __syncwarp();
+    if (lane < n && rank < P.k) list[rank] = e;
+    __syncwarp();
+    return true;
+}
+
+// One token without a bias whose groups, or more logits than its lanes list, the keys leave open, by
+// a whole warp, from its logits in shared memory: groups by their largest logits or (in 64 bits)
+// the scores of the two largest, then k times the largest logit left.
+__device__ __noinline__ void select_logits(const SelectParams& P, int64_t t, int lane, const float* row) {
     constexpr int VJ = kMaxExperts / 32;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
     const bool sigmoid = P.mode == MOE_MODE_SIGMOID, top2 = P.rule == MOE_GROUP_TOP2 && per > 1;
     float l[VJ];  // of the experts lane, lane + 32, ...
 #pragma unroll
     for (int j = 0; j < VJ; ++j) l[j] = lane + 32 * j < E ? row[lane + 32 * j] : -INFINITY;
-    float mx = 0.f, sum = 1.f, inv = 1.f;
-    double total = 1.0;
+    float mx = 0.f, sum = 1.f;
     if (!sigmoid) {
         mx = -INFINITY;
 #pragma unroll
@@ -424,129 +514,51 @@ __device__ __noinline__ bool select_close(const SelectParams& P, int64_t t, int 
 #pragma unroll
         for (int j = 0; j < VJ; ++j) sum += fast_exp2(kLog2e * (l[j] - mx));
         sum = seg_sum<32>(sum);
-        inv = fast_rcp(sum);
-        if (!LOGIT) {
-            total = 0.0;
-#pragma unroll 1
-            for (int e = lane; e < E; e += 32) total += exp((double)row[e] - (double)mx);
-            total = seg_sum<32>(total);
-        }
     }
-    const float es = score_err(sigmoid, inv);
-    auto value64 = [&](int e) { return no_nan(score64(sigmoid, row[e], mx, total) + (double)P.b[e]); };
-    int key[VJ];  // INT_MIN, below every value, past the last expert
-#pragma unroll
-    for (int j = 0; j < VJ; ++j) {
-        const int e = lane + 32 * j;
-        key[j] = INT_MIN;
-        if (e >= E) continue;
-        key[j] = LOGIT ? logit_key(l[j])
-                       : __float_as_int(fmaxf(fast_score(sigmoid, l[j], mx, inv) + (P.b[e] - base), 0.f));
-        if (!settled) scratch[e] = key[j];
-    }
-    if (!settled) {
-        __syncwarp();
-        int a = INT_MIN, b = INT_MIN, c = INT_MIN, d = INT_MIN;  // lane g: group g's four largest
-        int ia = -1, ib = -1, ic = -1;
+    uint32_t open = 1u;
+    if (G > 1) {
+        int a = INT_MIN, b = INT_MIN, ia = 0, ib = 0;  // lane g: group g's two largest
         if (lane < G) {
 #pragma unroll 4
             for (int e = lane * per; e < (lane + 1) * per; ++e) {
-                const int v = scratch[e];
-                const bool A = v > a, B = v > b, C = v > c;
-                d = C ? c : max(d, v);
-                c = B ? b : C ? v : c;
-                ic = B ? ib : C ? e : ic;
+                const int v = logit_key(row[e]);
+                const bool A = v > a, B = v > b;
                 b = A ? a : B ? v : b;
                 ib = A ? ia : B ? e : ib;
                 a = A ? v : a;
                 ia = A ? e : ia;
             }
         }
-        double gs = -INFINITY;
-        if (LOGIT) {
-            if (lane < G)
-                gs = top2 ? score64(sigmoid, row[ia], mx, total) + score64(sigmoid, row[ib], mx, total)
-                          : no_nan((double)row[ia]);
-        } else {
-            // the two largest (or the largest) are among the first three unless the fourth may
-            // reach them
-            const float least = __int_as_float(top2 ? b : a);
-            const bool unsettled = lane < G && per > 3 && !(least - __int_as_float(d) > value_gap(least, es));
-            if (__any_sync(kFull, unsettled)) return false;
-            // three candidates a group, all of them at once where there are lanes for that
-            double v[3];
-            if (3 * G <= 32) {
-                const int h = lane % G, q = lane / G;
-                const int ea = __shfl_sync(kFull, ia, h), eb = __shfl_sync(kFull, ib, h), ec = __shfl_sync(kFull, ic, h);
-                const int e = q == 0 ? ea : q == 1 ? eb : q == 2 ? ec : -1;
-                const double x = e < 0 ? -INFINITY : value64(e);
-#pragma unroll
-                for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(kFull, x, h + i * G);
-            } else {
-                v[0] = ia < 0 ? -INFINITY : value64(ia);
-                v[1] = ib < 0 ? -INFINITY : value64(ib);
-                v[2] = ic < 0 ? -INFINITY : value64(ic);
-            }
-            const double x = fmax(v[0], v[1]), y = fmin(v[0], v[1]);
-            if (lane < G) gs = top2 ? no_nan(fmax(x, v[2]) + fmax(y, fmin(x, v[2]))) : fmax(x, v[2]);
-        }
+        double gs = -INFINITY;  // (a common factor, the softmax's sum, leaves the order)
+        if (lane < G)
+            gs = top2 ? score64(sigmoid, row[ia], mx, 1.0) + score64(sigmoid, row[ib], mx, 1.0) : no_nan((double)row[ia]);
         int rank = 0;
         const long long mine = order_of(gs);
         for (int h = 0; h < G; ++h) rank += ahead_of(__shfl_sync(kFull, mine, h), h, mine, lane);
         open = __ballot_sync(kFull, lane < G && rank < P.topk_group);
-        __syncwarp();
     }
+    int key[VJ];  // INT_MIN, below every value, past the last expert and in closed groups
 #pragma unroll
-    for (int j = 0; j < VJ; ++j)  // closed groups
-        if (lane + 32 * j < E && !((open >> ((lane + 32 * j) / per)) & 1u)) key[j] = INT_MIN;
+    for (int j = 0; j < VJ; ++j) {
+        const int e = lane + 32 * j;
+        key[j] = e < E && ((open >> (e / per)) & 1u) ? logit_key(l[j]) : INT_MIN;
+    }
     int my_e = 0;
-    if (LOGIT || !settled) {  // (where the groups were settled, kth is known)
-        uint32_t taken = 0;
-        int top = INT_MIN;
-        for (int i = 0; i < k; ++i) {  // the largest key left, of the lowest index
-            int best = INT_MIN, e = INT_MAX;
+    uint32_t taken = 0;
+    for (int i = 0; i < k; ++i) {  // the largest key left, of the lowest index
+        int best = INT_MIN, e = INT_MAX;
 #pragma unroll
-            for (int j = 0; j < VJ; ++j)
-                if (!((taken >> j) & 1u) && key[j] > best) {
-                    best = key[j];
-                    e = lane + 32 * j;
-                }
-            top = __reduce_max_sync(kFull, best);
-            const int w = __reduce_min_sync(kFull, best == top ? e : INT_MAX);
-            if ((w & 31) == lane) taken |= 1u << (w >> 5);
-            if (lane == i) my_e = w;
-        }
-        kth = __int_as_float(top);
-    }
-    if (!LOGIT) {
-        const float gap = value_gap(kth, es);
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < VJ; ++j) {
-            const bool in = key[j] != INT_MIN && !(kth - __int_as_float(key[j]) > gap);
-            const uint32_t m = __ballot_sync(kFull, in);
-            const int at = n + __popc(m & ((1u << lane) - 1u));
-            if (in && at < 32) scratch[at] = lane + 32 * j;
-            n += __popc(m);
-        }
-        if (n > 32 || n < k) return false;
-        __syncwarp();
-        int e = INT_MAX;
-        long long x = 0;
-        if (lane < n) {
-            e = scratch[lane];
-            x = order_of(value64(e));
-        }
-        int rank = 0;
-        for (int i = 0; i < n; ++i) rank += ahead_of(__shfl_sync(kFull, x, i), __shfl_sync(kFull, e, i), x, e);
-        __syncwarp();
-        if (lane < n && rank < k) scratch[rank] = e;
-        __syncwarp();
-        my_e = lane < k ? scratch[lane] : 0;
-        __syncwarp();
+        for (int j = 0; j < VJ; ++j)
+            if (!((taken >> j) & 1u) && key[j] > best) {
+                best = key[j];
+                e = lane + 32 * j;
+            }
+        const int top = __reduce_max_sync(kFull, best);
+        const int w = __reduce_min_sync(kFull, best == top ? e : INT_MAX);
+        if ((w & 31) == lane) taken |= 1u << (w >> 5);
+        if (lane == i) my_e = w;
     }
     finish_token(P, t, lane, my_e, lane < k ? row[my_e] : 0.f, mx, sum);
-    return true;
 }
 
 // Sorting network for eight keys, largest first, and the eight largest of two sorted eights.
@@ -642,7 +654,7 @@ template <int L, int NB, bool LOGIT, bool VEC>
 __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectParams P, const SelectLayout Y) {
     constexpr int NT = 32 / L;
     extern __shared__ __align__(16) float smem[];  // biases, then two buffers of rows per warp
-    __shared__ int scratch[kSelWarps][kMaxExperts];
+    __shared__ __align__(16) int lists[kSelWarps][kMaxExperts + 32];  // the lanes' keys, eight each; a token's slots
     __shared__ int taken;  // steps of the CTA's run that its warps have taken
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % L;
     const int E = P.E, G = P.n_group, per = E / G, k = P.k;
@@ -654,9 +666,11 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
     const int pitch = (E + 3) / 4 * 4;
     float* const bias = smem;  // (b - base) times the values' scale
     float* const rows = smem + (LOGIT ? 0 : pitch) + warp * 2 * NT * pitch;
+    int* const keys = lists[warp];
+    int* const slots = lists[warp] + kMaxExperts;
 
-    // The CTA's tokens are a run of steps of NT tokens, which its warps take one by one: a token
-    // chosen again delays its warp alone.
+    // The CTA's tokens are a run of steps of NT tokens, which its warps take one by one: a token near
+    // a tie delays its warp alone.
     const int64_t steps = (P.T + NT - 1) / NT;
     const int64_t s0 = blockIdx.x * steps / gridDim.x;
     const int n = (int)((blockIdx.x + 1) * steps / gridDim.x - s0);
@@ -772,7 +786,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 for (int j = 0; j < 4; ++j) kb[4 * h + j] = INT_MIN;
                 if (8 * blk + 4 * h >= Y.vr) continue;
                 load4(2 * blk + h, at, v);
-                const int id = INT_MIN + first + at;
+                const int id = INT_MIN + 1 + first + at;
                 float bv[4] = {kc, kc, kc, kc};
                 if (!LOGIT) {
                     if (VEC) {
@@ -809,16 +823,22 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
 #pragma unroll
             for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
         }
+        auto publish = [&]() {
+            int4* to = reinterpret_cast<int4*>(keys + 8 * lane);
+            to[0] = make_int4(key[0], key[1], key[2], key[3]);
+            to[1] = make_int4(key[4], key[5], key[6], key[7]);
+        };
+        bool open = true;  // the lane's group stays
+        auto lanes_of = [&](int i) { return L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (i * L); };
         bool groups = false;  // unsettled
-        uint32_t heads = 0u;  // lanes that begin a group that stays
         if (G > 1) {
             // a group's score in units; sums of scores without a bias as floats
             int a = key[0], b = key[1];
             float fa = -INFINITY, fb = -INFINITY;
             bool rough = false;
             if (LOGIT && top2) {  // from the logits themselves
-                if (count > 0) fa = held[a & 255];
-                if (count > 1) fb = held[b & 255];
+                if (count > 0) fa = held[expert_of(a)];
+                if (count > 1) fb = held[expert_of(b)];
                 if (fb > fa) {
                     const float x = fa;
                     fa = fb;
@@ -840,14 +860,14 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
             int gs = top2 ? units_of(a) + units_of(b) : units_of(a);
             if (LOGIT && top2)
                 gs = __float_as_int(fast_score(sigmoid, fa, mx, inv) + fast_score(sigmoid, fb, mx, inv));
-            if (top2 && g < G) groups |= units_of(b) == 0;  // a sum that counts a value clamped at 0
             int rank = 0;
             for (int h = 0; h < G; ++h) {
                 const int x = __shfl_sync(kFull, gs, h * Y.lpg, L);
                 rank += x > gs || (x == gs && h < g);
             }
-            const bool kept = g < G && rank < P.topk_group;
+            bool kept = g < G && rank < P.topk_group;
             if (P.topk_group < G) {
+                if (top2 && g < G) groups |= units_of(b) == 0;  // a sum that counts a value clamped at 0
                 const int lo = seg_min<L>(kept ? gs : INT_MAX);
                 const int hi = seg_max<L>(!kept && g < G ? gs : INT_MIN);
                 if (LOGIT && top2) {
@@ -862,7 +882,23 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                     groups |= lo - hi <= (top2 ? 2 * tol : tol);
                 }
             }
-            heads = __ballot_sync(kFull, kept && r == 0);
+            const uint32_t unsettled = LOGIT ? 0u : __ballot_sync(kFull, live && groups && !infinite);
+            if (unsettled) {
+                publish();
+                __syncwarp();
+                for (int i = 0; i < NT; ++i) {  // the warp together, one token at a time
+                    if (!(unsettled & lanes_of(i))) continue;
+                    uint32_t o = 0;
+                    const bool ok = settle_groups(P, lane, rows + buf * NT * pitch + i * E, keys + 8 * i * L, Y.lpg,
+                                                  __shfl_sync(kFull, tol, i * L), __shfl_sync(kFull, mx, i * L), o);
+                    if (ok && lane / L == i) {
+                        kept = g < G && ((o >> g) & 1u);
+                        groups = false;
+                    }
+                }
+                __syncwarp();
+            }
+            open = kept;
             if (!kept) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) key[j] = INT_MIN;
@@ -875,6 +911,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
             mine = merge_lanes8(key, sub, last);
             last = seg_max<L>(last);  // the ninth: what follows slot 7
         } else {  // rounds: the lane that holds the largest key moves its list up
+            publish();
             mine = INT_MIN;
             for (int i = 0;; ++i) {
                 last = seg_max<L>(key[0]);
@@ -887,51 +924,60 @@ __global__ void __launch_bounds__(kSelWarps * 32, 2) select_kernel(const SelectP
                 }
             }
         }
-        int my_e = min(mine & 255, E - 1);  // (of a key that is none: not used)
+        int my_e = max(expert_of(mine), 0);  // (of a key that is none: not used)
         // each slot's key against the next one's (the last slot's against the best one left)
         int next = __shfl_sync(kFull, mine, lane / L * L + (next_lane < L ? next_lane : 0));
         if (my_slot == L - 1 || (L > 8 && my_slot == k - 1)) next = last;
-        const bool close = units_of(mine) - units_of(next) <= tol;
-        const bool inside = close && my_slot < k - 1;
-        bool border = close && my_slot == k - 1;
-        // a lane whose eight are all chosen may hold the ninth of them
         const int kth = __shfl_sync(kFull, mine, lane / L * L + slot_lane(k - 1));
-        border |= NB > 1 && count > 8 && eighth >= kth;
-        const bool lost = odd || groups || border || infinite || (!LOGIT && !sigmoid && inside);
-        const uint32_t again = __ballot_sync(kFull, live && lost);
-        if ((LOGIT || sigmoid) && __any_sync(kFull, live && inside)) {
-            // the chosen ones are settled, their order is not: by their own values
-            long long x;
-            if (LOGIT) x = logit_key(held[my_e]);
-            else x = order_of(no_nan(score64(true, held[my_e], 0.f, 1.0) + (double)P.b[my_e]));
-            int rank = 0, e = my_e;
-            for (int i = 0; i < k; ++i) {
-                const int from = lane / L * L + slot_lane(i);
-                rank += ahead_of(__shfl_sync(kFull, x, from), __shfl_sync(kFull, my_e, from), x, my_e);
+        const bool close = my_slot < k && units_of(mine) - units_of(next) <= tol;
+        // a lane whose eight are all chosen, or may be, can hold a ninth
+        const bool ninth = NB > 1 && count > 8 && units_of(eighth) >= units_of(kth) - tol;
+        const uint32_t near = __ballot_sync(kFull, live && (close || ninth));
+        uint32_t again = __ballot_sync(kFull, live && (odd || groups || infinite));
+        if (near & ~again) {
+            const uint32_t deep = __ballot_sync(kFull, ninth);
+            if (L == 8) publish();
+            __syncwarp();
+            const uint32_t stay = __ballot_sync(kFull, open && r == 0);
+            auto settle = [&](int i, int nkeys, const int* from) {
+                const bool ok = settle_slots<LOGIT>(P, lane, rows + buf * NT * pitch + i * E, from, nkeys,
+                                                    __shfl_sync(kFull, units_of(kth) - tol, i * L),
+                                                    __shfl_sync(kFull, mx, i * L), slots);
+                if (!ok) again |= lanes_of(i);
+                else if (lane / L == i && my_slot < k) my_e = slots[my_slot];
+                __syncwarp();
+            };
+            for (int i = 0; i < NT; ++i) {
+                if (!(near & lanes_of(i)) || (again & lanes_of(i)) || (deep & lanes_of(i))) continue;
+                settle(i, 8 * L, keys + 8 * i * L);
             }
-            for (int i = 0; i < k; ++i) {
-                const int from = lane / L * L + slot_lane(i);
-                const int r = __shfl_sync(kFull, rank, from), o = __shfl_sync(kFull, my_e, from);
-                if (r == my_slot) e = o;
+            for (int i = 0; NB > 1 && i < NT; ++i) {  // by all of the token's keys, not eight a lane
+                if (!(near & deep & lanes_of(i)) || (again & lanes_of(i))) continue;
+                const float kvi = __shfl_sync(kFull, kv, i * L), kci = __shfl_sync(kFull, kc, i * L);
+                const float mxi = __shfl_sync(kFull, mx, i * L);
+                const int nkeys = (E + 31) / 32 * 32;
+#pragma unroll 1
+                for (int e = lane; e < nkeys; e += 32) {
+                    int x = INT_MIN;
+                    if (e < E && (G == 1 || ((stay >> (i * L + e / per * Y.lpg)) & 1u))) {
+                        const float v = rows[buf * NT * pitch + i * E + e];
+                        x = LOGIT ? fixed_key(v, kvi, kci, INT_MIN + 1 + e)
+                                  : fixed_key(fast_score(sigmoid, v, mxi, 1.f), kvi, bias[e], INT_MIN + 1 + e);
+                    }
+                    keys[e] = x;
+                }
+                __syncwarp();
+                settle(i, nkeys, keys);
             }
-            my_e = e;
         }
         finish<L>(P, t, my_slot, live && !(again & mask), my_e, held[my_e], mx, sum);
         if (again) {
             const uint32_t strange = __ballot_sync(kFull, live && (odd || infinite));
-            const uint32_t unsettled = __ballot_sync(kFull, live && groups);
-            for (int i = 0; i < NT; ++i) {  // the warp together, one token at a time
-                const uint32_t m = L == 32 ? kFull : ((1u << (L % 32)) - 1u) << (i * L);
-                if (!(again & m)) continue;
-                uint32_t o = G > 1 ? 0u : 1u;
-                for (int h = 0; h < G; ++h) o |= ((heads >> (i * L + h * Y.lpg)) & 1u) << h;
-                const int ku = units_of(__shfl_sync(kFull, kth, i * L));
-                // the k-th key's value, less what its roundings may have added
-                const float least = (float)(ku - 4) / (scale * kUnits);
-                if ((strange & m) ||
-                    !select_close<LOGIT>(P, t0 + i, lane, base, rows + buf * NT * pitch + i * E, !(unsettled & m),
-                                         o, least, scratch[warp]))
-                    select_token(P, t0 + i, lane);
+            for (int i = 0; i < NT; ++i) {
+                const uint32_t m = lanes_of(i);
+                if (!(again & m) || t0 + i >= P.T) continue;
+                if (LOGIT && !(strange & m)) select_logits(P, t0 + i, lane, rows + buf * NT * pitch + i * E);
+                else select_token(P, t0 + i, lane);
             }
         }
         step = ahead;

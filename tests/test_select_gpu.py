@@ -211,6 +211,25 @@ def test_choice_with_large_biases():
         _check(l, b, 8, "softmax", 8, 4)
 
 
+@pytest.mark.parametrize("mode", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,G,tg", [(256, 8, 8, 1), (256, 8, 4, 1), (128, 6, 8, 1), (256, 32, 8, 1),
+                                      (200, 20, 5, 1), (24, 24, 1, 1), (96, 12, 24, 3), (40, 6, 20, 3),
+                                      (256, 16, 1, 1)])
+def test_choice_of_many_tokens_from_few_lanes(E, k, G, tg, mode):
+    """All of a token's experts in one group (so that few lanes hold them), or all experts chosen,
+    with biases so far apart that some values are clamped in the fast keys, expert 0's among them."""
+    T = 2600
+    g = torch.Generator().manual_seed(E + 3 * k)
+    l = torch.randn(T, E, generator=g)
+    l[::4] = l[::4] * 1e-6
+    l[1::64] = 0.0
+    far = torch.randn(E, generator=g) * 12
+    far[0] = -50.0
+    for bias in (None, torch.rand(E, generator=g) * 0.1, far):
+        for rule in ("max", "top2"):
+            _check(l.cuda(), None if bias is None else bias.cuda(), k, mode, G, tg, rule)
+
+
 def test_choice_agrees_with_the_router_without_groups():
     """One group and renormalised sigmoid gates is moe_route's own choice."""
     T, d, E, k = 1000, 256, 64, 8
