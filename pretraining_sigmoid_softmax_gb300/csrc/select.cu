@@ -531,7 +531,8 @@ __device__ __noinline__ void select_logits(const SelectParams& P, int64_t t, int
         }
         double gs = -INFINITY;  // (a common factor, the softmax's sum, leaves the order)
         if (lane < G)
-            gs = top2 ? score64(sigmoid, row[ia], mx, 1.0) + score64(sigmoid, row[ib], mx, 1.0) : no_nan((double)row[ia]);
+            gs = top2 ? score64(sigmoid, row[ia], mx, 1.0) + score64(sigmoid, row[ib], mx, 1.0)
+                      : no_nan((double)row[ia]);
         int rank = 0;
         const long long mine = order_of(gs);
         for (int h = 0; h < G; ++h) rank += ahead_of(__shfl_sync(kFull, mine, h), h, mine, lane);
@@ -1168,7 +1169,10 @@ int launch_select(const SelectParams& P, cudaStream_t st) {
         if (L < 32 && (L < P.k || L < P.n_group)) continue;
         for (Y.lpg = 1; P.n_group * Y.lpg * 2 <= L;) Y.lpg *= 2;
         Y.vr = (int)cdiv(per, Y.lpg);
-        if (L == 32 || Y.vr <= (L == 8 ? 32 : 16)) break;
+        // the open lanes list twice the slots: one that lists all of a token's experts may hide
+        // others (65,536 x 256, top-8 of one group of 32: 53 us with 16 lanes, 171 with 8)
+        const bool listed = Y.vr <= 8 || 8 * P.topk_group * Y.lpg >= 2 * P.k;
+        if (L == 32 || (Y.vr <= (L == 8 ? 32 : 16) && listed)) break;
     }
     const bool vec = P.E % 4 == 0 && Y.vr % 4 == 0 && per % Y.vr == 0 && aligned16(P.logits);
     const int nb = Y.vr <= 8 ? 1 : Y.vr <= 16 ? 2 : 4;
