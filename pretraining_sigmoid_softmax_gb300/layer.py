@@ -554,11 +554,27 @@ class RMSNorm(torch.nn.Module):
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
             raise ValueError(f"x must be [T, {self.d}] bf16, got {tuple(x.shape)} {x.dtype}")
         if residual is None:
-            return _RMSNormFunction.apply(x, None, self.w, self.eps, yq, sy), x
-        if residual.shape != x.shape or residual.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"residual must be [T, {self.d}] bf16 or fp32 as x has it, got "
-                             f"{tuple(residual.shape)} {residual.dtype}")
-        return _RMSNormFunction.apply(x, residual, self.w, self.eps, yq, sy)
+            y, z = _RMSNormFunction.apply(x, None, self.w, self.eps, yq, sy), x
+        else:
+            if residual.shape != x.shape or residual.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"residual must be [T, {self.d}] bf16 or fp32 as x has it, got "
+                                 f"{tuple(residual.shape)} {residual.dtype}")
+            y, z = _RMSNormFunction.apply(x, residual, self.w, self.eps, yq, sy)
+        if yq is not None:
+            y.codes = yq, sy, None if y.is_inference() else y._version
+        return y, z
+
+
+def _has_codes(norm, y, yq, sy):
+    """The buffers hold the codes of this y, which `norm` returned, as it is now. A hook on the norm, or
+    a module in its place, may have returned another, written into it or left the buffers alone."""
+    codes = getattr(y, "codes", None)
+    if codes is None or codes[0] is not yq or codes[1] is not sy:
+        return False
+    if codes[2] is None:  # an inference tensor counts no writes: nothing else may have had it
+        return (type(norm) is RMSNorm and not norm._forward_hooks
+                and not torch.nn.modules.module._global_forward_hooks)
+    return codes[2] == y._version
 
 
 @torch.no_grad()
@@ -595,7 +611,8 @@ class MoELayer(torch.nn.Module):
     ``norm_eps`` puts the RMS norm in front of the layer (``norm``, an ``RMSNorm``):
     ``forward(x, residual)`` then adds x to the residual stream, runs the layer on the norm of
     the sum and returns (out, stream). With FP8 experts the norm writes their input's codes in
-    the same pass. ``n_group`` > 1 limits each token's experts to the ``topk_group`` best groups
+    the same pass; a y that a hook or another module in ``norm``'s place made is quantised by
+    the layer. ``n_group`` > 1 limits each token's experts to the ``topk_group`` best groups
     (``group_rule`` "max" or "top2": a group's score is its largest selection value or the sum
     of its two largest); ``renorm`` and ``gate_scale`` set how gates follow from scores."""
 
@@ -659,12 +676,13 @@ class MoELayer(torch.nn.Module):
             raise ValueError("a residual is taken by a layer with a norm (norm_eps)")
         plan = self._plan(x.shape[0])
         self._last_plan = plan
-        z = None
+        z, codes = None, False
         if self.norm is not None:
             x, z = self.norm(x, residual, plan.x8 if self.fp8 else None,
                              plan.sx if self.fp8 else None)
+            codes = self.fp8 and _has_codes(self.norm, x, plan.x8, plan.sx)
         out = _MoEFunction.apply(x, self.W_r, self.b, self.W_g, self.W_u, self.W_d, self.Ws_g,
-                                 self.Ws_u, self.Ws_d, plan, self.fp8 and z is not None)
+                                 self.Ws_u, self.Ws_d, plan, codes)
         return out if z is None else (out, z)
 
     def clip_grads_(self, max_norm):

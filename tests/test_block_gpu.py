@@ -266,3 +266,86 @@ def test_plan_step_in_a_graph_and_launch_count(E, mode, T):
         assert _off(out[n], t.double() * (1e-3 / total)) <= 2.0 ** -8
     with pytest.raises(ValueError):
         plan.clip_grads(1.0, {"dW_r": out["dW_r"]})
+
+
+class _OtherNorm(torch.nn.Module):
+    """A norm of the user's own, which knows nothing of codes."""
+
+    def __init__(self, norm):
+        super().__init__()
+        self.norm = norm
+
+    def forward(self, x, residual=None, yq=None, sy=None):
+        y, z = self.norm(x, residual)
+        return y * 4, z
+
+
+class _Scaled(RMSNorm):
+    """Writes the codes, and returns another y than theirs."""
+
+    def forward(self, x, residual=None, yq=None, sy=None):
+        y, z = super().forward(x, residual, yq, sy)
+        return y * 4, z
+
+
+def _in_place(module, args, out):
+    with torch.no_grad():
+        out[0].mul_(4)
+
+
+CHANGES = {
+    "a hook that returns another y": lambda l: l.norm.register_forward_hook(lambda m, a, o: (o[0] * 4, o[1])),
+    "a hook that writes into y": lambda l: l.norm.register_forward_hook(_in_place),
+    "a hook that leaves the code buffers out": lambda l: l.norm.register_forward_pre_hook(lambda m, a: a[:2]),
+    "another module": lambda l: setattr(l, "norm", _OtherNorm(l.norm)),
+    "a subclass": lambda l: setattr(l.norm, "__class__", _Scaled),
+    "a hook that only looks": lambda l: l.norm.register_forward_hook(lambda m, a, o: None),
+}
+
+
+@pytest.mark.parametrize("precision", ["fp8", "fp8_dgrad"])
+@pytest.mark.parametrize("change", CHANGES)
+def test_fp8_block_computes_from_the_y_that_its_norm_returns(change, precision):
+    """Whatever a hook or a module in the norm's place makes of y, the experts run on that y: the same
+    bits as a layer without a norm that is given it (where the norm's own y comes back, its codes
+    are one rounding nearer to the unrounded y than that layer's, two steps of E4M3 at most)."""
+    torch.manual_seed(5)
+    kw = dict(d=256, E=8, k=2, f=128, f_shared=128, precision=precision)
+    layer, plain = MoELayer(norm_eps=1e-6, **kw), MoELayer(**kw)
+    plain.load_state_dict({n: t for n, t in layer.state_dict().items() if not n.startswith("norm.")})
+    x = torch.randn(200, 256, device="cuda").to(torch.bfloat16)
+    layer(x.flip(0))  # the code buffers hold an earlier step's
+    CHANGES[change](layer)
+    out, z = layer(x)
+    y = layer._last_plan.x
+    want = plain(y)
+    torch.cuda.synchronize()
+    assert z is x
+    if change == "a hook that only looks":
+        yq, sy = torch.empty_like(layer._last_plan.x8), torch.empty_like(layer._last_plan.sx)
+        layer.norm(x, None, yq, sy)
+        torch.cuda.synchronize()
+        assert torch.equal(layer._last_plan.x8, yq) and torch.equal(layer._last_plan.sx, sy)
+        assert _off(out, want) <= REL_FP8
+    else:
+        assert torch.equal(layer._last_plan.x8, plain._last_plan.x8)
+        assert torch.equal(layer._last_plan.sx, plain._last_plan.sx)
+        assert torch.equal(out, want)
+
+
+def test_fp8_block_in_inference_mode_computes_from_the_y_of_its_norm():
+    torch.manual_seed(6)
+    layer = MoELayer(256, 8, 2, 128, precision="fp8", norm_eps=1e-6)
+    plain = MoELayer(256, 8, 2, 128, precision="fp8")
+    plain.load_state_dict({n: t for n, t in layer.state_dict().items() if not n.startswith("norm.")})
+    x = torch.randn(64, 256, device="cuda").to(torch.bfloat16)
+    own, _ = layer(x)
+    plain(x)  # (the plans have their buffers)
+    with torch.inference_mode():  # the norm's codes, as in training
+        assert torch.equal(layer(x)[0], own)
+    layer.norm.register_forward_hook(_in_place)
+    with torch.inference_mode():
+        out, _ = layer(x)
+        want = plain(layer._last_plan.x)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
