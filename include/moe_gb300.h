@@ -385,8 +385,9 @@ int moe_combine_bwd(const moe_bf16* dY, const moe_bf16* Y_perm, const float* top
  * moe_combine_bwd_fp8 - moe_combine_bwd (with gates and the gate gradient) that also writes
  * the E4M3 codes of every dY_perm row it stores, for moe_expert_bwd_fp8: dYq and sdY equal
  * moe_quantize_rows_fp8 of dY_perm bit for bit (padding rows: zero codes, scale 1), without
- * a second pass over dY_perm. A row is bf16(g * dY[t]) with g >= 0, a monotone function of
- * dY[t], so its amax is bf16(g * amax|dY[t]|) and its scale is known before it is written.
+ * a second pass over dY_perm. The magnitudes of a row bf16(g * dY[t]) are a monotone function
+ * of those of dY[t], for gates of either sign, so its amax is bf16(|g| * amax|dY[t]|) and its
+ * scale is known before it is written.
  * In / Out as moe_combine_bwd (Y_perm, topk_gate and dg required), plus dYq [padded rows, d]
  * codes and sdY [padded rows] fp32.
  */

@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16* __res
 // dY_perm[row(t,i)] = bf16(g[t,i] * dY[t]); dg[t,i] = <dY[t], Y_perm[row(t,i)]>. Without
 // gates the rows are plain copies of dY[t]; without Y_perm no dg is formed.
 // CODES: also the E4M3 codes and scale of every written row, equal to what
-// moe_quantize_rows_fp8 of dY_perm gives: each row is bf16(g dY[t]), a monotone function of
-// dY[t] for g >= 0, so its amax is bf16(g amax|dY[t]|), known before the row is written.
+// moe_quantize_rows_fp8 of dY_perm gives: the magnitudes of a row bf16(g dY[t]) are a monotone
+// function of those of dY[t], so its amax is bf16(|g| amax|dY[t]|), known before the row is written.
 template <int KMAX, bool CODES = false>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(
     const __nv_bfloat16* __restrict__ dY, const __nv_bfloat16* __restrict__ Y_perm,
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(
         for (int c = lane; c < d / 8; c += 32) m = amax8(reinterpret_cast<const uint4*>(dY + t * d)[c], m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const Fp8Scale sc(__bfloat162float(__float2bfloat16_rn(my_g * m)));
+        const Fp8Scale sc(__bfloat162float(__float2bfloat16_rn(fabsf(my_g) * m)));
         if (lane < k && my_row >= 0) sdY[my_row] = sc.s;
 #pragma unroll
         for (int i = 0; i < KMAX; ++i) {

@@ -624,7 +624,7 @@ class MoELayer(torch.nn.Module):
         if group_rule not in ("max", "top2"):
             raise ValueError("group_rule is max or top2")
         if not 0.0 < gate_scale < float("inf"):
-            raise ValueError("gate_scale is positive (the experts' backward counts on gates >= 0)")
+            raise ValueError("gate_scale is positive")
         if n_group < 1 or E % n_group or not 1 <= topk_group <= n_group \
                 or k > topk_group * (E // n_group):
             raise ValueError(f"{E} experts in {n_group} groups, {topk_group} of them kept, cannot "

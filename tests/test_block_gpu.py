@@ -349,3 +349,25 @@ def test_fp8_block_in_inference_mode_computes_from_the_y_of_its_norm():
         want = plain(layer._last_plan.x)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("scale", [2.5, -2.5])
+def test_plan_with_fp8_data_gradients_and_gates_of_either_sign(scale):
+    """The codes that the expert backward reads are those of the rows, for small gradients too."""
+    torch.manual_seed(7)
+    T, d, E, k, f = 300, 256, 16, 4, 128
+    plan = MoEPlan(MoEShape(T, d, E, k, f, seq_len=T, fp8=True, fp8_dgrad=True, n_group=4, topk_group=2,
+                            gate_scale=scale))
+    dev = dict(device="cuda")
+    bf = dict(dtype=torch.bfloat16)
+    W = (torch.randn(E, d, **dev) / 16, torch.rand(E, **dev) * 0.1, torch.randn(E, f, d, **dev).to(**bf) / 16,
+         torch.randn(E, f, d, **dev).to(**bf) / 16, torch.randn(E, d, f, **dev).to(**bf) / 16)
+    x, dY = torch.randn(T, d, **dev).to(**bf), (torch.randn(T, d, **dev) * 2.0 ** -12).to(**bf)
+    plan.forward(x, *W)
+    plan.backward(dY)
+    n = int(plan.row_offsets[-1])
+    q, s = torch.empty_like(plan.dYq), torch.empty_like(plan.sdY)
+    ops.moe_quantize_rows_fp8(plan.dY_perm, plan.row_offsets[E:], q, s)
+    torch.cuda.synchronize()
+    assert (plan.topk_gate * scale > 0).all()
+    assert torch.equal(plan.sdY[:n], s[:n]) and torch.equal(plan.dYq[:n], q[:n])

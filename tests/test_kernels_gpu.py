@@ -987,3 +987,29 @@ def test_combine_backward_with_fp8_codes():
     assert torch.equal(a_dYp[:n], b_dYp[:n]) and torch.equal(a_dg, b_dg)
     assert torch.equal(q[:n], q_ref[:n])
     assert torch.equal(sq[:n], s_ref[:n])
+
+
+def test_combine_backward_with_fp8_codes_of_negative_gates():
+    """Gates of either sign: the codes and scales are moe_quantize_rows_fp8's of the stored rows bit
+    for bit, for gradients so small that a scale of 1 would leave no code of them."""
+    g = torch.Generator().manual_seed(76)
+    T, d, E, k = 500, 256, 8, 4
+    P = _permute(_random_choice(T, E, k, g), randn_bf16((T, d), g), E)
+    R = P["X_perm"].shape[0]
+    Y_perm = randn_bf16((R, d), g)
+    gate = torch.randn(T, k, generator=g)
+    gate[7] = -gate[7].abs()
+    dY = randn_bf16((T, d), g) * 2.0 ** -12
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    dYp, dg = torch.full((R, d), float("nan"), **bf), torch.empty(T, k, device="cuda")
+    q = torch.full((R, d), 0x7F, dtype=torch.uint8, device="cuda")
+    sq = torch.full((R,), float("nan"), device="cuda")
+    ops.moe_combine_bwd_fp8(dev(dY), dev(Y_perm), dev(gate), P["slot_to_row"], P["row_offsets"],
+                            P["perm_token"], dYp, dg, q, sq)
+    n = int(P["row_offsets"][-1])
+    q_ref = torch.empty(R, d, dtype=torch.uint8, device="cuda")
+    s_ref = torch.empty(R, device="cuda")
+    ops.moe_quantize_rows_fp8(dYp, P["row_offsets"][E:], q_ref, s_ref)
+    torch.cuda.synchronize()
+    assert torch.equal(sq[:n], s_ref[:n])
+    assert torch.equal(q[:n], q_ref[:n])
