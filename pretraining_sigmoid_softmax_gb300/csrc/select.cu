@@ -13,6 +13,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "select_key.h"
 #include "sizes.h"
 
 namespace moe {
@@ -355,19 +356,12 @@ __device__ __forceinline__ int logit_key(float l) {
     return b ^ ((b >> 31) & 0x7fffffff);
 }
 
-// The key of a value v = a x + b clamped to [0, 1) (a NaN to 0): v + 1 has v's 23 fixed-point
-// bits as its mantissa (rounded to half a unit); times 512 they are the key's upper bits, the
-// sign turned so that signed integers order the keys. `id` = expert + 1 + INT_MIN, so that INT_MIN is
-// no expert's key.
-constexpr int kKeyBits = 9;
-constexpr float kUnits = 8388608.f;  // per 1
+// The key of a value v = a x + b clamped to [0, 1) (a NaN to 0), rounded to half a unit.
 __device__ __forceinline__ int fixed_key(float x, float a, float b, int id) {
     float v;
     asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(x), "f"(a), "f"(b));
-    return __float_as_int(v + 1.0f) * (1 << kKeyBits) + id;
+    return key_of(__float_as_uint(v + 1.0f), id);
 }
-__device__ __forceinline__ int expert_of(int key) { return (key & ((1 << kKeyBits) - 1)) - 1; }
-__device__ __forceinline__ int units_of(int key) { return (int)((uint32_t)(key ^ INT_MIN) >> kKeyBits); }
 constexpr float kLogitRange = 16.f;
 constexpr float kBelowOne = 0.9990234f;  // 1 - 2^-10
 

@@ -4,6 +4,7 @@ so the checks hold without a GPU."""
 import ctypes
 import os
 import shutil
+import subprocess
 
 import pytest
 import torch
@@ -192,3 +193,37 @@ def test_binding_names_the_missing_tensor():
         ops.moe_router_logits(x, torch.zeros(2, 16), torch.zeros(4, 2), ws)
     with pytest.raises(ops.MoEError, match="dlogits must be a CUDA tensor"):
         ops.moe_router_dw(torch.zeros(4, 2), x, torch.zeros(2, 16), ws)
+
+
+KEYS_CPP = r"""
+#include <stdio.h>
+#include <string.h>
+#include "select_key.h"
+using namespace moe;
+int main() {
+    int last = INT_MIN;
+    for (long u = 0; u < 8388608; u += u < 64 || u > 8388544 ? 1 : 4093) {
+        const float v = (float)(1.0 + (double)u / kUnits);
+        uint32_t bits;
+        memcpy(&bits, &v, 4);
+        for (int e = 0; e < 256; e += 51) {
+            const int key = key_of(bits, INT_MIN + 1 + e);
+            if (key <= last || units_of(key) != u || expert_of(key) != e) return printf("%ld %d %d\n", u, e, key), 1;
+            last = key;
+        }
+    }
+    return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not installed")
+def test_choice_keys_are_defined_arithmetic(tmp_path):
+    """The keys order values and hold value and expert, in arithmetic that C++ defines throughout."""
+    src, exe = tmp_path / "keys.cpp", tmp_path / "keys"
+    src.write_text(KEYS_CPP)
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", csrc,
+                    str(src), "-o", str(exe)], check=True)
+    res = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout + res.stderr
