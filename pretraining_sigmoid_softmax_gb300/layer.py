@@ -577,17 +577,32 @@ def _has_codes(norm, y, yq, sy):
     return codes[2] == y._version
 
 
+def _run_of(i, g):
+    """A gradient's elements as one run of memory, in whatever order its dimensions lie."""
+    if g.is_contiguous():
+        return g
+    n = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(g.stride(), g.shape) if sz != 1):
+        if stride != n:
+            raise ops.MoEError(f"gradient {i} must lie side by side in memory, got shape "
+                               f"{tuple(g.shape)} with strides {g.stride()}")
+        n *= size
+    return g.as_strided((n,), (1,))
+
+
 @torch.no_grad()
 def clip_grad_norm_(parameters, max_norm):
     """Clips the gradients of ``parameters`` (bf16 or fp32, on one device; those without one are
     passed over) to a global 2-norm of at most ``max_norm``, in place, and returns that norm as
     it was ([] fp32 device tensor, no synchronisation). A norm that is not finite leaves the
-    gradients as they are."""
+    gradients as they are. A gradient's dimensions may lie in any order (a transposed parameter's
+    do), but without gaps between its elements."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in dict.fromkeys(parameters) if p.grad is not None]  # each once
     if not grads:
         return torch.zeros(())
+    grads = [_run_of(i, g) for i, g in enumerate(grads)]
     dev = grads[0].device
     norm = torch.empty(2, dtype=torch.float32, device=dev)
     ws = torch.empty(ops.moe_workspace_bytes(1, 128, 1, 1), dtype=torch.uint8, device=dev)

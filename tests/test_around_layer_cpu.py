@@ -9,7 +9,7 @@ import subprocess
 import pytest
 import torch
 
-from pretraining_sigmoid_softmax_gb300 import _lib, build, ops
+from pretraining_sigmoid_softmax_gb300 import _lib, build, layer, ops
 
 needs_nvcc = pytest.mark.skipif(shutil.which("nvcc") is None and not os.path.exists("/usr/local/cuda/bin/nvcc"),
                                 reason="nvcc not installed")
@@ -227,3 +227,30 @@ def test_choice_keys_are_defined_arithmetic(tmp_path):
                     str(src), "-o", str(exe)], check=True)
     res = subprocess.run([str(exe)], capture_output=True, text=True)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+@needs_nvcc
+def test_clip_grad_norm_hands_over_runs_of_memory(lib, monkeypatch):
+    """Gradients whose dimensions lie in another order are handed over as the memory they are; ones
+    with gaps, or with one element many times, are refused before anything is launched."""
+    seen = []
+    monkeypatch.setattr(layer.ops, "moe_clip_grads", lambda grads, *a: seen.append(grads))
+
+    def clip(*grads):
+        ps = [torch.nn.Parameter(torch.zeros(g.shape)) for g in grads]
+        for p, g in zip(ps, grads):
+            p.grad = g
+        layer.clip_grad_norm_(ps, 1.0)
+    base = torch.arange(210.0)
+    orders = [base.view(14, 15).t(), base.view(5, 6, 7).permute(2, 0, 1), base.view(2, 3, 5, 7).permute(0, 3, 1, 2),
+              base.view(14, 1, 15).permute(2, 1, 0), base[3:203].view(10, 20).t(), base.view(210, 1)]
+    clip(*orders)
+    for got, g in zip(seen[0], orders):
+        assert got.is_contiguous() and got.data_ptr() == g.data_ptr() and got.numel() == g.numel()
+        assert sorted(got.flatten().tolist()) == sorted(g.flatten().tolist())
+    seen.clear()
+    for g in (base.view(14, 15)[:, ::2], base.view(14, 15)[:, :5], base[:8].expand(4, 8),
+              base.as_strided((4, 5), (3, 1)), base.as_strided((4, 5), (1, 6))):
+        with pytest.raises(ops.MoEError, match=r"gradient 1 .*side by side"):
+            clip(base, g)
+    assert not seen

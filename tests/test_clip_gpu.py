@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from pretraining_sigmoid_softmax_gb300 import ops
+from pretraining_sigmoid_softmax_gb300.layer import clip_grad_norm_
 
 from gpu_common import require_gpu
 
@@ -185,3 +186,42 @@ def test_clip_refuses_mismatched_tensors():
         ops.moe_clip_grads([torch.zeros(4, 4, device="cuda").t()], 1.0, None, norm, _ws())
     with pytest.raises(ops.MoEError, match="workspace"):
         ops.moe_clip_grads(g, 1.0, None, norm, _ws()[:64])
+
+
+def _params(shapes, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    ps = [torch.nn.Parameter(torch.zeros(s, device="cuda", dtype=dtype)) for s in shapes]
+    for p in ps:
+        p.grad = torch.randn(p.shape, generator=g).to(dtype).cuda()
+    return ps
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_clip_grad_norm_takes_gradients_in_any_order_of_dimensions(dtype):
+    """A transposed parameter's gradient is transposed too; its elements still lie side by side."""
+    ps = _params([(33, 70), (5, 6, 7), (64,), (1, 40), (4, 3, 5, 2), (0, 3)], dtype, 11)
+    ps[0].grad = ps[0].grad.t().contiguous().t()
+    ps[1].grad = ps[1].grad.permute(2, 0, 1).contiguous().permute(1, 2, 0)
+    ps[4].grad = ps[4].grad.contiguous(memory_format=torch.channels_last)
+    assert sum(not p.grad.is_contiguous() for p in ps) == 3
+    before, at = [p.grad.clone() for p in ps], [(p.grad.data_ptr(), p.grad.stride()) for p in ps]
+    want = _norm64(before)
+    norm = clip_grad_norm_(ps, 0.5)
+    torch.cuda.synchronize()
+    assert abs(float(norm) - want) <= 18 * U * want
+    for p, b, a in zip(ps, before, at):
+        assert (p.grad.data_ptr(), p.grad.stride()) == a
+        w = b.double() * (0.5 / want)
+        assert ((p.grad.double() - w).abs() <= (20 * U + HALF[dtype] * (1 + 20 * U)) * w.abs() + TINY[dtype]).all()
+
+
+def test_clip_grad_norm_refuses_gradients_with_gaps():
+    """Elements of a larger tensor, or one element many times: named, and nothing is clipped."""
+    for grad in (torch.randn(8, 16, device="cuda")[:, ::2], torch.randn(8, 1, device="cuda").expand(8, 8)):
+        ps = _params([(8, 8), (8, 8)], F32, 12)
+        before = ps[0].grad.clone()
+        ps[1].grad = grad
+        with pytest.raises(ops.MoEError, match=r"gradient 1 .*side by side"):
+            clip_grad_norm_(ps, 1e-3)
+        torch.cuda.synchronize()
+        assert torch.equal(ps[0].grad, before)
