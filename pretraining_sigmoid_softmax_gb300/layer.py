@@ -606,7 +606,8 @@ def clip_grad_norm_(parameters, max_norm):
     dev = grads[0].device
     norm = torch.empty(2, dtype=torch.float32, device=dev)
     ws = torch.empty(ops.moe_workspace_bytes(1, 128, 1, 1), dtype=torch.uint8, device=dev)
-    ops.moe_clip_grads(grads, max_norm, None, norm, ws)
+    with torch.cuda.device_of(norm):  # which need not be the current device
+        ops.moe_clip_grads(grads, max_norm, None, norm, ws)
     return norm[0]
 
 

@@ -254,3 +254,27 @@ def test_clip_grad_norm_hands_over_runs_of_memory(lib, monkeypatch):
         with pytest.raises(ops.MoEError, match=r"gradient 1 .*side by side"):
             clip(base, g)
     assert not seen
+
+
+@needs_nvcc
+def test_clip_grad_norm_runs_on_the_gradients_device(lib, monkeypatch):
+    """The library's call is made with the gradients' device as the current one, whichever was."""
+    current = [0]
+
+    class DeviceOf:
+        def __init__(self, t):
+            self.to = 1  # where these stand-ins for gradients are said to lie
+            assert t.shape == (2,)
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.to
+
+        def __exit__(self, *a):
+            current[0] = self.was
+    calls = []
+    monkeypatch.setattr(torch.cuda, "device_of", DeviceOf)
+    monkeypatch.setattr(layer.ops, "moe_clip_grads", lambda g, m, out, norm, ws: (calls.append(current[0]), norm.fill_(3)))
+    p = torch.nn.Parameter(torch.zeros(4))
+    p.grad = torch.ones(4)
+    assert float(layer.clip_grad_norm_(p, 1.0)) == 3.0
+    assert calls == [1] and current == [0]
