@@ -597,11 +597,10 @@ def clip_grad_norm_(parameters, max_norm):
     it was ([] fp32 device tensor, no synchronisation). A norm that is not finite leaves the
     gradients as they are. A gradient's dimensions may lie in any order (a transposed parameter's
     do), but without gaps between its elements."""
-    if isinstance(parameters, torch.Tensor):
-        parameters = [parameters]
-    grads = [p.grad for p in dict.fromkeys(parameters) if p.grad is not None]  # each once
+    ps = dict.fromkeys([parameters] if isinstance(parameters, torch.Tensor) else parameters)  # each once
+    grads = [p.grad for p in ps if p.grad is not None]
     if not grads:
-        return torch.zeros(())
+        return torch.zeros((), dtype=torch.float32, device=next(iter(ps)).device if ps else None)
     grads = [_run_of(i, g) for i, g in enumerate(grads)]
     dev = grads[0].device
     norm = torch.empty(2, dtype=torch.float32, device=dev)

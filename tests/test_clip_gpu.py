@@ -225,3 +225,9 @@ def test_clip_grad_norm_refuses_gradients_with_gaps():
             clip_grad_norm_(ps, 1e-3)
         torch.cuda.synchronize()
         assert torch.equal(ps[0].grad, before)
+
+
+def test_clip_grad_norm_without_gradients_is_a_device_zero():
+    ps = [torch.nn.Parameter(torch.zeros(4, device="cuda"))]
+    norm = clip_grad_norm_(iter(ps), 1.0)
+    assert norm.shape == () and norm.is_cuda and norm.dtype == F32 and float(norm) == 0.0
