@@ -502,17 +502,24 @@ class _MoEFunction(torch.autograd.Function):
                 None, None)
 
 
+def _whole(t):
+    """Contiguous and on a 32-byte boundary, as the norm's vector accesses need it: the tensor itself
+    or, where it is a view that starts anywhere in a larger buffer, a copy."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 32 == 0 else t.clone()
+
+
 class _RMSNormFunction(torch.autograd.Function):
     """y = rms_norm(z) w with z = residual + x; returns (y, z), or y alone without a residual."""
 
     @staticmethod
     def forward(ctx, x, residual, w, eps, yq, sy):
-        x = x.contiguous()
+        x, w = _whole(x), _whole(w)
         y = torch.empty_like(x)
         rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
         z = None
         if residual is not None:
-            residual = residual.contiguous()
+            residual = _whole(residual)
             z = torch.empty_like(residual)
         ops.moe_rms_norm(x, residual, w, eps, z, y, yq, sy, rstd)
         ctx.save_for_backward(x if z is None else z, rstd, w)
@@ -529,8 +536,8 @@ class _RMSNormFunction(torch.autograd.Function):
                 return None, None, None, None, None, None
             return dres.to(torch.bfloat16), dres, None, None, None, None
         T, d = z.shape
-        dy = dy.to(torch.bfloat16).contiguous()
-        dres = None if dres is None else dres.to(z.dtype).contiguous()
+        dy = _whole(dy.to(torch.bfloat16))
+        dres = None if dres is None else _whole(dres.to(z.dtype))
         dz, dw = torch.empty_like(z), torch.empty_like(w)
         dx = torch.empty_like(dy) if z.dtype is not torch.bfloat16 else None
         ws = torch.empty(ops.moe_workspace_bytes(T, d, 1, 1), dtype=torch.uint8, device=z.device)

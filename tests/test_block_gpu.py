@@ -371,3 +371,41 @@ def test_plan_with_fp8_data_gradients_and_gates_of_either_sign(scale):
     torch.cuda.synchronize()
     assert (plan.topk_gate * scale > 0).all()
     assert torch.equal(plan.sdY[:n], s[:n]) and torch.equal(plan.dYq[:n], q[:n])
+
+
+def _view(t, byte):
+    """The same values in a contiguous view that starts `byte` bytes past an allocation's start."""
+    flat = torch.empty(t.numel() + 64, dtype=t.dtype, device=t.device)
+    at = byte // t.element_size()
+    v = flat[at:at + t.numel()].view(t.shape)
+    v.copy_(t.detach())
+    assert v.is_contiguous() and v.data_ptr() % 512 == byte
+    return v
+
+
+@pytest.mark.parametrize("rdtype", [torch.bfloat16, torch.float32, None])
+@pytest.mark.parametrize("byte", [4, 16, 48])
+def test_norm_module_takes_views_that_start_anywhere(byte, rdtype):
+    """Inputs, gradients and the weight as slices of larger buffers: the same bits as from their own."""
+    torch.manual_seed(8)
+    T, d = 21, 264
+    norm, other = RMSNorm(d), RMSNorm(d)
+    w = 1 + 0.1 * torch.randn(d, device="cuda")
+    norm.w.data = w
+    other.w.data = _view(w, byte)
+    x, dy = (torch.randn(T, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    r, dz = ((None, None) if rdtype is None else
+             (torch.randn(T, d, device="cuda").to(rdtype) for _ in range(2)))
+    got = []
+    for n, put in ((norm, lambda t: t.clone()), (other, lambda t: _view(t, byte))):
+        xi = put(x).requires_grad_(True)
+        ri = None if r is None else put(r).requires_grad_(True)
+        y, z = n(xi, ri)
+        if r is None:
+            y.backward(put(dy))
+        else:
+            torch.autograd.backward([y, z], [put(dy), put(dz)])
+        got.append([y.detach(), z.detach(), xi.grad, n.w.grad] + ([] if r is None else [ri.grad]))
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
