@@ -458,7 +458,9 @@ class MoEPlan:
         g = {n: t for n, t in self.grads().items() if n != "dx"}
         if out is not None and set(out) != set(g):
             raise ValueError(f"out must hold {sorted(g)}, got {sorted(out)}")
-        norm = torch.empty(2, dtype=torch.float32, device=self.dW_r.device) if norm is None else norm
+        if norm is None:
+            with torch.cuda.stream(stream):  # memory that no other stream's kernels still use
+                norm = torch.empty(2, dtype=torch.float32, device=self.dW_r.device)
         ops.moe_clip_grads(list(g.values()), max_norm, None if out is None else [out[n] for n in g],
                            norm, self.ws, stream)
         return norm

@@ -409,3 +409,23 @@ def test_norm_module_takes_views_that_start_anywhere(byte, rdtype):
     torch.cuda.synchronize()
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_plan_clips_on_a_stream_with_a_norm_of_that_stream():
+    """The norm's buffer comes from the stream that writes it, not from the current one, whose
+    allocator may hand out memory that the current stream's kernels still use."""
+    torch.manual_seed(9)
+    T, d, E, f = 128, 128, 4, 128
+    plan = MoEPlan(MoEShape(T, d, E, 2, f, seq_len=T))
+    g = [t for n, t in plan.grads().items() if n != "dx"]
+    for t in g:
+        t.copy_(torch.randn(t.shape, device="cuda"))
+    total = float(torch.sqrt(sum((t.double() ** 2).sum() for t in g)))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    norm = plan.clip_grads(1.0, stream=s)
+    s.synchronize()
+    assert abs(float(norm[0]) - total) <= 1e-5 * total
+    at = [seg["stream"] for seg in torch.cuda.memory_snapshot()
+          if seg["address"] <= norm.data_ptr() < seg["address"] + seg["total_size"]]
+    assert at == [s.cuda_stream]
