@@ -702,8 +702,12 @@ class MoELayer(torch.nn.Module):
         self._last_plan = plan
         z, codes = None, False
         if self.norm is not None:
-            x, z = self.norm(x, residual, plan.x8 if self.fp8 else None,
+            y, z = self.norm(x, residual, plan.x8 if self.fp8 else None,
                              plan.sx if self.fp8 else None)
+            if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+                raise ValueError(f"the norm must return y as {list(x.shape)} bf16 on {x.device}, got "
+                                 f"{list(y.shape)} {y.dtype} on {y.device}")
+            x = y
             codes = self.fp8 and _has_codes(self.norm, x, plan.x8, plan.sx)
         out = _MoEFunction.apply(x, self.W_r, self.b, self.W_g, self.W_u, self.W_d, self.Ws_g,
                                  self.Ws_u, self.Ws_d, plan, codes)

@@ -278,3 +278,24 @@ def test_clip_grad_norm_runs_on_the_gradients_device(lib, monkeypatch):
     p.grad = torch.ones(4)
     assert float(layer.clip_grad_norm_(p, 1.0)) == 3.0
     assert calls == [1] and current == [0]
+
+
+class _Returns(torch.nn.Module):
+    def __init__(self, change):
+        super().__init__()
+        self.change = change
+
+    def forward(self, x, residual=None, yq=None, sy=None):
+        return self.change(x), x
+
+
+@needs_nvcc
+@pytest.mark.parametrize("precision", ["bf16", "fp8"])
+@pytest.mark.parametrize("change", [lambda x: x.float(), lambda x: x[:4], lambda x: x[:, :128], lambda x: x[0],
+                                    lambda x: x.half(), lambda x: x.to("meta")])
+def test_layer_refuses_another_kind_of_y_from_its_norm(lib, change, precision):
+    """The kernels read [T, d] bf16 at the address they are given, whatever lies there."""
+    block = layer.MoELayer(256, 4, 2, 128, norm_eps=1e-6, device="cpu", precision=precision)
+    block.norm = _Returns(change)
+    with pytest.raises(ValueError, match="the norm must return"):
+        block(torch.zeros(8, 256, dtype=torch.bfloat16))
