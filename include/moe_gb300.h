@@ -556,7 +556,8 @@ int moe_permute_bwd(const moe_bf16* dX_perm, const int32_t* slot_to_row,
  * rstd = 1 / sqrt(mean_j(z_j^2) + eps), from the stored z; y_j = z_j rstd w_j in fp32, stored
  * as bf16. Codes: sy = fp32(amax_j |y_j| / 448) (1 for a zero row), yq = E4M3(y / sy), round
  * to nearest even, saturating at +-448, both from the fp32 y: one rounding fewer than
- * quantising the bf16 y (moe_quantize_rows_fp8) has. Sums are fp32, in a fixed order.
+ * quantising the bf16 y (moe_quantize_rows_fp8) has. Sums are fp32, in a fixed order: a row whose
+ * squares pass fp32's range (values around 1e19 and above) has rstd 0, and so y 0.
  * In : x [T,d] bf16; residual [T,d] of res_type (MOE_TYPE_BF16 or MOE_TYPE_F32), or NULL: then
  *      z is x itself; w [d] fp32; eps >= 0.
  * Out: z [T,d] of res_type (both or neither of residual and z; z may be the residual's own
@@ -618,6 +619,10 @@ int moe_router_dw(const float* dlogits, const moe_bf16* x, int64_t T, int d, int
  * where that sum is 0 in 64 bits).
  * The choice is the one the values have in 64 bits, whatever the kernel's own rounding. (Values
  * or sums that differ by no more than their 64-bit rounding may come in either order.)
+ * Time: a token is slow (chosen in 64 bits throughout; 65,536 x 256 of them: 2.2 ms instead of 0.03)
+ * where a bias is +inf, where all the biases of a group lie 16 or more below the largest (-inf, say;
+ * single experts masked so cost nothing), and where its logits are all equal and many biases are
+ * too. Without biases, a group with logits that all lie 16 or more below the row's largest: 0.43 ms.
  * In : logits [T,E] fp32 (moe_route or moe_router_logits); b [E] fp32 or NULL. A logit of -inf
  *      has score 0; a bias of -inf keeps an expert out while there are others. Values that are
  *      NaN come last; every choice is of k distinct experts of [0,E) even so. In softmax mode a

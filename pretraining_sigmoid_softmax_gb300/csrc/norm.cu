@@ -316,8 +316,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(
 // sums of dw in their order at the end.
 //
 // 8192 x 1024 bf16 with norm_dw_kernel (67 MB): 15.8 us, 0.63 of a copy (a CTA per row with the ring
-// above: 26.5); 16,384 x 1024 fp32 46 us, 0.86; 65,536 x 256 bf16 28 us, 0.71. What is short of
-// the copy is the launch, the first rows' latency and the sums of dw, 4.5 us in all.
+// above: 26.5); 16,384 x 1024 fp32 46 us, 0.86; 65,536 x 256 bf16 28 us, 0.71. The launch, the first
+// rows' latency and the sums of dw are 4.5 us of each; the rest that short rows lack (3.5 us at 256
+// columns) goes by a row's fixed work, with 16 warps per SM to hide it (four CTAs, also where
+// registers would let more in).
 constexpr int kRowWarps = 4;
 
 template <typename R, int VPT, int STAGES>
@@ -432,9 +434,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) norm_bwd_rows_kernel(
     }
 }
 
-// Rows too wide for the ring: the same sums, with plain loads and up to 1024 threads. A row's second
-// reading comes from L2, and its dw sums are read and written there too: 8192 x 16,384 bf16 takes
-// 265 us, 0.60 of a copy.
+// Rows of more than 8192 columns, which no layer here has: the same sums, with plain loads and up to
+// 1024 threads. A row's second reading comes from L2, and its dw sums are read and written there
+// too, 8 bytes an element for every row: 8192 x 16,384 bf16 takes 265 us, 0.60 of a copy. (A ring of two
+// bf16 rows would fit up to 16,384 columns, with the sums in registers; it is not built.)
 template <typename R, int VPT>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(
     const __nv_bfloat16* __restrict__ dy, const R* dres, const R* __restrict__ z,

@@ -319,13 +319,22 @@ __device__ __noinline__ void select_token(const SelectParams& P, int64_t t, int 
 // this arithmetic (NaN, infinities, more than 32 experts near the border) are chosen in 64 bits
 // throughout.
 //
-// Bound by instruction issue: 65,536 tokens of 256 experts in 8 groups take 32 us (4.4 us per step
-// of four tokens and warp, 1190 instructions at 54% of the issue slots; 16 warps per SM at 128
-// registers), 29 us where no token comes near a border, 10.8 us for their bytes. 16,383 tokens of 160,
-// softmax: 11.1 us, 9.5 without near ties. A token near one took 6 to 11 us of latency when its
-// choice was made anew, nearly all of it instructions that the SM has not met before (a 64-bit one
-// also takes 64 cycles a warp): so what the keys have settled is kept, loops over its few
-// candidates stay rolled, and the 64-bit score is one piece of code.
+// Bound by latency and occupancy: 65,536 tokens of 256 experts in 8 groups take 31 to 32 us (1190
+// instructions and 4.4 us per step of four tokens and warp, 54% of the issue slots with the 16 warps
+// per SM that 128 registers leave; several of the kernels spill 32 to 108 bytes at that), 29 us where
+// no token comes near a border, 10.8 us for their bytes. 16,383 tokens of 160, softmax: 11.1 us, 9.5 without
+// near ties. Rows that are no whole vectors a lane cost little more: 65,536 tokens of 40 experts in one
+// group 16.3 us, 72 19.5, 100 21.5 (64 and 128, in vectors: 15.7 and 20.4). A token near a border took 6 to
+// 11 us of latency when its choice was made anew, nearly all of it instructions that the SM has not met
+// before (a 64-bit one also takes 64 cycles a warp): so what the keys have settled is kept, loops
+// over its few candidates stay rolled, and the 64-bit score is one piece of code.
+//
+// What is slow: tokens that are chosen in 64 bits throughout. With biases that are all equal a token
+// of equal logits (padding) is one; one such token in 64 makes the large case 98 us, 53 with biases of 41
+// levels. A bias of +inf, or a whole group's biases 16 or more below the largest, sends every token
+// there: 2.1 to 2.2 ms. Without a bias a whole group's logits 16 or more below the largest has every
+// token's groups settled from its logits: 0.43 ms. (Single experts masked by -inf, in logits or biases,
+// and with a bias a whole group's logits, cost nothing.)
 //
 // With a bias the value is s + (b - base), base the smallest bias within 16 of the largest, s by
 // the fast exponential and reciprocal, scaled so that it lies below 1 and clamped at 0. Without
@@ -337,9 +346,12 @@ struct SelectLayout {
 constexpr float kU = 5.9604645e-8f;  // 2^-24
 // Bounds of the fast scores' errors. Sigmoid: 1 / (1 + e^-l): the reciprocal is within 1 ulp (2 u
 // relative), the sum within u, and the exponential's relative error (1.5 |l| u + 4 u) enters
-// times s (1 - s): below 5 u in all; 6.4 u leaves room. Softmax: e^(l - max) / sum:
-// (1.5 |l - max| + 4) u, at most 20 u for the sum, its reciprocal and the product; p |l - max| <=
-// 0.37: 25 u p + 0.6 u.
+// times s (1 - s): below 5 u in all; 6.4 u leaves room. Softmax: p = e^(l - max) / sum, where 1 / sum
+// is the row's largest p, P. A term is off by (2.3 |l - max| + 4) u of itself (the roundings of the
+// difference, of log2 e and of their product), and p |l - max| <= 0.37 P: 10 u P for two values. The sum
+// is off by 4 u, 2.3 u times the mean of |l - max| over p (at most ln 256, as the entropy is) and 13
+// roundings, its reciprocal and their products by 4 u: 34 u, a factor that the row's values have in
+// common, so it moves the difference of two by 34 u P at most. Twice the bound, 50 u P + 1.2 u, covers both.
 constexpr float kSigmoidErr = 6.4f * kU;
 constexpr float kSoftmaxErr = 25.f * kU;
 constexpr float kLog2e = 1.44269504f;
