@@ -79,6 +79,11 @@ enum moe_group_rule {    /* score of a group of experts */
     MOE_GROUP_TOP2 = 1  /* the sum of its two largest (its only one, in groups of one) */
 };
 
+enum moe_fp4_format {   /* microscaled 4-bit floating point (E2M1 codes) */
+    MOE_FP4_MX = 0,    /* a power of two (E8M0) for each 32 elements along the contraction */
+    MOE_FP4_NV = 1     /* an E4M3 scale for each 16, under one power of two per row */
+};
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* moe_status_string(int status);
 
@@ -327,6 +332,116 @@ int moe_expert_bwd_fp8(const uint8_t* dYq, const float* sdY, const moe_bf16* dY,
                        float* sAU, moe_bf16* dW_g, moe_bf16* dW_u, moe_bf16* dW_d,
                        const float* dl_rows, const float* W_r, void* ws, size_t ws_bytes,
                        moe_stream_t stream);
+
+/*
+ * Operands in microscaled 4-bit floating point: codes Q [rows, cols / 2] bytes (E2M1: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives; element 2j in the low half of byte j), block scales S and,
+ * in MOE_FP4_NV, a power of two g [rows] fp32 for each row (NULL in MOE_FP4_MX). Element (r, c)
+ * stands for code * scale (* g[r]). The scale of row r and block j (32 or 16 elements along the
+ * row) is the byte
+ *   ((r / 128) * (cols / span) + j / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4
+ * of S, span = 128 (MX) or 64 (NV): tiles of 128 rows x 4 blocks, as the tensor cores take them.
+ * S has moe_fp4_scale_bytes(rows, cols, fmt) bytes. cols % 128 == 0; Q, S and g 16-byte aligned.
+ * Source: the pages name FP8 operands only ("fp8_rowwise", Apex-3 stack); these are the block-scaled
+ * 4-bit operands of the same GEMMs, after the OCP Microscaling Formats specification (MX) and with
+ * blocks of 16 (NV).
+ */
+/* Bytes of the scales of a [rows, cols] operand (0 for sizes or a format that are not allowed). */
+int64_t moe_fp4_scale_bytes(int64_t rows, int cols, int fmt);
+
+/*
+ * moe_quantize_rows_fp4 - rows of a bf16 matrix, or of the concatenation [X | X1], as an operand.
+ * Definition, per block with largest magnitude amax:
+ *   MX: scale = 2^(floor(log2 amax) - 2) (2^-127 at least; also for a zero block), code = E2M1(x / scale);
+ *   NV: g = the smallest power of two (2^-126 at least) with rowmax <= 2688 g (1 for a zero row), scale =
+ *       E4M3(fp32(fp32(amax / g) / 6)), code = E2M1(x / g / scale), 0 where scale is 0.
+ * E2M1 and E4M3 round to nearest even and saturate; the codes are those of the exact quotients.
+ * Infinities and NaN: the block's scale (MX) or the row's g (NV) becomes NaN, and with it what a
+ * product makes of them.
+ * In : X, X1 [rows, cols] bf16 (X1 or NULL); rows_limit: device int64 or NULL, only rows below
+ *      min(rows, *rows_limit) are written. cols (2 cols with X1) <= 32768.
+ * Out: Q, S, g of a [rows, cols] ([rows, 2 cols]) operand. Scales of rows that are not written
+ *      stay as they were.
+ */
+int moe_quantize_rows_fp4(const moe_bf16* X, const moe_bf16* X1, const int64_t* rows_limit,
+                          int64_t rows, int cols, int fmt, uint8_t* Q, uint8_t* S, float* g,
+                          moe_stream_t stream);
+
+/*
+ * moe_quantize_cols_fp4 - the columns of E matrices (X0, or the stacks [X0[e]; X1[e]]) as an operand
+ * whose row e N + n is column n of matrix e, blocks along K: what a GEMM that contracts over the
+ * matrices' rows reads (moe_expert_bwd_fp4). Definition as moe_quantize_rows_fp4 of the transposes.
+ * In : X0, X1 [E, K0, N] bf16 (X1 or NULL; K = K0 or 2 K0).  Out: Qt, S, g of a [E N, K] operand.
+ * K0, N % 128 == 0, each at most 32768; E <= 65535.
+ */
+int moe_quantize_cols_fp4(const moe_bf16* X0, const moe_bf16* X1, int E, int K0, int N, int fmt,
+                          uint8_t* Qt, uint8_t* S, float* g, moe_stream_t stream);
+
+/*
+ * moe_dequantize_fp4 - the numbers an operand stands for, in bf16 (exact within bf16's range).
+ * In : Q, S, g of a [rows, cols] operand; rows_limit as in moe_quantize_rows_fp4.
+ * Out: out [rows, cols] bf16.
+ */
+int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const float* g, const int64_t* rows_limit,
+                       int64_t rows, int cols, int fmt, moe_bf16* out, moe_stream_t stream);
+
+/*
+ * moe_permute_fp4 - an operand's token rows copied to the rows of their experts (as moe_permute_fp8):
+ * what moe_quantize_rows_fp4 gives of the expert-major rows, from a k-fold smaller quantisation.
+ * In : xq, sx, gx of a [T, d] operand; slot_to_row, perm_token, row_offsets from moe_permute.
+ * Out: Xq, sX, gX of a [rows, d] operand (rows = row_offsets[E]); padding rows as zero rows give.
+ */
+int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float* gx, const int32_t* slot_to_row,
+                    const int32_t* perm_token, const int64_t* row_offsets, int64_t T, int d, int E,
+                    int k, int fmt, uint8_t* Xq, uint8_t* sX, float* gX, moe_stream_t stream);
+
+/*
+ * moe_grouped_gemm_fp4 - products grouped by expert: Y[p] = X[p] W[e]^T for the rows p of expert e,
+ * on the tensor cores' block-scaled E2M1 path (fp32 accumulation, one bf16 rounding).
+ * In : X, a [rows, K] operand in the padded expert-major layout; row_offsets [E+1] as in
+ *      moe_expert_fwd (NULL: one matrix over all rows, E = 1); W, an [E N, K] operand.
+ * Out: Y [rows, N] bf16. K, N % 128 == 0. Rows from row_offsets[E] on are left as they were.
+ */
+int moe_grouped_gemm_fp4(const uint8_t* Xq, const uint8_t* sX, const float* gX,
+                         const int64_t* row_offsets, int E, int64_t rows, int K, int N,
+                         const uint8_t* Wq, const uint8_t* sW, const float* gW, int fmt, moe_bf16* Y,
+                         moe_stream_t stream);
+
+/*
+ * moe_expert_fwd_fp4 - moe_expert_fwd on 4-bit operands. a and u as there; h = silu(a) u (times
+ * row_gate) is rounded to bf16 and quantised (moe_quantize_rows_fp4 of H) before the down projection.
+ * In : X, a [rows, d] operand; W_g, W_u [E f, d] and W_d [E d, f] operands; row_offsets, row_gate as in
+ *      moe_expert_fwd. f <= 32768.
+ * Out: A, U [rows, f] bf16, or both NULL where no backward follows; H [rows, f] bf16; the [rows, f]
+ *      operand of H; Y [rows, d] bf16.
+ */
+int moe_expert_fwd_fp4(const uint8_t* Xq, const uint8_t* sX, const float* gX,
+                       const int64_t* row_offsets, int E, int64_t rows, int d, int f,
+                       const uint8_t* Wgq, const uint8_t* sWg, const float* gWg, const uint8_t* Wuq,
+                       const uint8_t* sWu, const float* gWu, const uint8_t* Wdq, const uint8_t* sWd,
+                       const float* gWd, int fmt, moe_bf16* A, moe_bf16* U, moe_bf16* H, uint8_t* Hq,
+                       uint8_t* sH, float* gH, moe_bf16* Y, const float* row_gate,
+                       moe_stream_t stream);
+
+/*
+ * moe_expert_bwd_fp4 - moe_expert_bwd with the two data-gradient GEMMs on 4-bit operands (as
+ * moe_expert_bwd_fp8 on E4M3); the weight gradients are bf16 GEMMs of the bf16 tensors, the gradient
+ * passing the quantisation of the forward unchanged.
+ * In : dY as a [rows, d] operand and (MOE_BWD_W) in bf16; X, H (MOE_BWD_W), A, U (MOE_BWD_DH) bf16;
+ *      W_d's columns as an [E f, d] operand and those of [W_g; W_u] as an [E d, 2f] operand
+ *      (moe_quantize_cols_fp4). parts: as in moe_expert_bwd; what a part does not name may be NULL.
+ * Out: dA, dU [rows, f] bf16 (in, without MOE_BWD_DH); the [rows, 2f] operand of [dA | dU] and dX
+ *      [rows, d] bf16 (MOE_BWD_DX); dW_g, dW_u [E,f,d], dW_d [E,d,f] bf16 (MOE_BWD_W).
+ * dl_rows, W_r: as in moe_expert_bwd. 2f <= 32768.
+ */
+int moe_expert_bwd_fp4(const uint8_t* dYq, const uint8_t* sdY, const float* gdY, const moe_bf16* dY,
+                       const moe_bf16* X, const moe_bf16* A, const moe_bf16* U, const moe_bf16* H,
+                       const int64_t* row_offsets, int E, int64_t rows, int d, int f,
+                       const uint8_t* Wdq, const uint8_t* sWd, const float* gWd, const uint8_t* Wguq,
+                       const uint8_t* sWgu, const float* gWgu, int fmt, moe_bf16* dX, moe_bf16* dA,
+                       moe_bf16* dU, uint8_t* AUq, uint8_t* sAU, float* gAU, moe_bf16* dW_g,
+                       moe_bf16* dW_u, moe_bf16* dW_d, int parts, const float* dl_rows,
+                       const float* W_r, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * moe_combine - gate-weighted sum of the expert outputs (C1).

@@ -129,6 +129,65 @@ def fp8_dequant_cols(W: np.ndarray) -> np.ndarray:
     return fp8_dequant_rows(np.asarray(W).T).T
 
 
+# E2M1's values by code (without the sign bit), and the midpoints between neighbours
+FP4_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+FP4_MIDS = (FP4_VALUES[1:] + FP4_VALUES[:-1]) / 2
+
+
+def fp4_codes(X: np.ndarray, S: np.ndarray) -> np.ndarray:
+    """E2M1 codes of X / S, decided without the division: |x| against each midpoint times the scale
+    (exact in fp64 for bf16 x and these scales), a tie to the even code, above 5 saturating."""
+    a = np.abs(X)
+    code = np.zeros(X.shape, dtype=np.uint8)
+    for i, m in enumerate(FP4_MIDS):  # between codes i and i + 1: the even one takes the tie
+        code += (a > m * S) | ((a == m * S) & (i % 2 == 1))
+    return np.where(S > 0, code + 8 * np.signbit(X).astype(np.uint8), 0).astype(np.uint8)
+
+
+def _e4m3_nearest(v: np.ndarray) -> np.ndarray:
+    """Nonnegative v to the nearest E4M3 number (ties to even, saturating at 448)."""
+    _, e = np.frexp(v)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.minimum(np.round(v / step) * step, 448.0)
+
+
+def quantize_rows_fp4(X: np.ndarray, nv: bool):
+    """Rows in microscaled 4-bit floating point. Returns the codes [rows, cols] (0..15), the block
+    scales [rows, cols / block] as numbers and the rows' powers of two [rows] (1 for MX).
+
+    MX (OCP Microscaling Formats: MXFP4): blocks of 32 under 2^(floor(log2 amax) - 2), at least
+    2^-127. ``nv``: blocks of 16 under E4M3(amax / g / 6), g the smallest power of two (at least
+    2^-126) for which rowmax / g is at most 6 * 448."""
+    X = np.asarray(X, dtype=np.float64)
+    rows, cols = X.shape
+    b = 16 if nv else 32
+    amax = np.abs(X).reshape(rows, cols // b, b).max(-1)
+    g = np.ones(rows)
+    if nv:
+        top = amax.max(-1)
+        _, e = np.frexp(top / 2688.0)
+        e = np.where(np.ldexp(1.0, e - 1) * 2688.0 >= top, e - 1, e)
+        g = np.where(top > 0, np.ldexp(1.0, np.maximum(e, -126)), 1.0)
+        S = _e4m3_nearest(amax / g[:, None] / 6.0)
+    else:
+        _, e = np.frexp(amax)
+        S = np.ldexp(1.0, np.where(amax > 0, np.maximum(e - 3, -127), -127))
+    full = np.repeat(S * g[:, None], b, axis=1)
+    return fp4_codes(X, full), S, g
+
+
+def fp4_dequant_rows(X: np.ndarray, nv: bool) -> np.ndarray:
+    """The numbers that the 4-bit codes and scales of X's rows stand for."""
+    q, S, g = quantize_rows_fp4(X, nv)
+    v = FP4_VALUES[q & 7] * np.where(q >= 8, -1.0, 1.0)
+    return v * np.repeat(S * g[:, None], X.shape[1] // S.shape[1], axis=1)
+
+
+def fp4_dequant_cols(W: np.ndarray, nv: bool) -> np.ndarray:
+    """The same with blocks along W's rows (its columns quantised)."""
+    return fp4_dequant_rows(np.asarray(W).T, nv).T
+
+
 def fp8_dgrad_dh(dy: np.ndarray, W_d: np.ndarray) -> np.ndarray:
     """The down projection's data gradient r = dy W_d with FP8 operands (reading of the
     Apex-3 stack's fp8_rowwise precision for the backward): the rows of dy are scaled along

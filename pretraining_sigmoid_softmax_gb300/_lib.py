@@ -39,6 +39,17 @@ PROTOTYPES = {
     "moe_quantize_cols_fp8": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "moe_expert_bwd_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P,
                                 _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_fp4_scale_bytes": (_I64, [_I64, _I, _I]),
+    "moe_quantize_rows_fp4": (_I, [_P, _P, _P, _I64, _I, _I, _P, _P, _P, _P]),
+    "moe_quantize_cols_fp4": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_dequantize_fp4": (_I, [_P, _P, _P, _P, _I64, _I, _I, _P, _P]),
+    "moe_permute_fp4": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_grouped_gemm_fp4": (_I, [_P, _P, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _I, _P, _P]),
+    "moe_expert_fwd_fp4": (_I, [_P, _P, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_expert_bwd_fp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P,
+                                _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _SZ,
+                                _P]),
     "moe_combine": (_I, [_P, _P, _P, _P, _I64, _I, _I, _P, _P]),
     "moe_bias_update": (_I, [_P, _I, _I64, _I, _F, _P, _P]),
     "moe_bias_update_proportional": (_I, [_P, _I, _I64, _I, _F, _P, _P]),

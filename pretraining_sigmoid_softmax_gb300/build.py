@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 BUILD_DIR = os.path.join(HERE, "_build")
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 SOURCES = ["status.cu", "route.cu", "route_tc.cu", "permute.cu", "grouped_gemm.cu", "fp8.cu",
-           "norm.cu", "select.cu", "clip.cu"]
+           "norm.cu", "select.cu", "clip.cu", "fp4.cu", "fp4_gemm.cu"]
 
 
 def nvcc_path() -> str:

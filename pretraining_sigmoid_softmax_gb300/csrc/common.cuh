@@ -30,6 +30,13 @@ int launch_quantize_rows_fp8(const __nv_bfloat16* X, const int64_t* limit, int64
 int launch_pad_rows_fp8(const int64_t* row_offsets, const int32_t* perm_token, int d, int E,
                         uint8_t* Xq, float* sX, cudaStream_t st);
 
+// Weight gradients of the SwiGLU experts from bf16 tensors (dW_d = dY^T H, dW_g = dA^T X, dW_u =
+// dU^T X for each expert's rows); see grouped_gemm.cu.
+int launch_weight_grads(const moe_bf16* dY, const moe_bf16* X, const moe_bf16* H, const moe_bf16* dA,
+                        const moe_bf16* dU, const int64_t* row_offsets, int E, int64_t rows, int d,
+                        int f, moe_bf16* dW_g, moe_bf16* dW_u, moe_bf16* dW_d, void* ws,
+                        size_t ws_bytes, cudaStream_t st);
+
 inline int launch_status() {
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
@@ -344,6 +351,55 @@ __host__ __device__ constexpr uint32_t idesc_mma(uint32_t n, uint32_t m, bool a_
            | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
            ((n >> 3) << 17)                // N / 8
            | ((m >> 4) << 24);             // M / 16
+}
+
+// Instruction descriptor of the E2M1 products with block scales (kind::mxf4, mxf4nvf4; K = 64).
+// The accumulator is fp32 always; A and B format 1 is E2M1. Bit 23: power-of-two (E8M0) scales,
+// else E4M3. Bits 29-30 and 4-5: which of the four scale bytes of a row A's and B's begin at.
+__host__ __device__ constexpr uint32_t idesc_fp4(uint32_t n, uint32_t m, bool e8m0) {
+    return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) | ((m >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor of an unswizzled tile of 16-byte rows (8-row groups of 128
+// bytes, back to back): a 512-byte scale tile as tcgen05.cp reads it.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr) {
+    uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    desc |= static_cast<uint64_t>(128 >> 4) << 32;
+    desc |= static_cast<uint64_t>(1) << 46;
+    return desc;
+}
+
+// One scale tile (32 lanes x 16 bytes) into four tensor-memory columns, the same in each of the
+// four lane quadrants; for a pair, each CTA's tile into its own tensor memory. Instructions
+// issued after it by this thread read what it wrote.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+}
+
+// D[tmem] (+)= (A sA)[smem] (B sB)[smem]^T for one K = 64 step of E2M1 codes, each block times its
+// scale from tensor memory; NV: E4M3 scales per 16 elements, else powers of two per 32.
+template <bool PAIR, bool NV>
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+#define MOE_UMMA_FP4(group, kind)                                                              \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                      \
+                 "setp.ne.b32 p, %4, 0;\n\t"                                                   \
+                 "tcgen05.mma.cta_group::" group "." kind " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" \
+                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa),  \
+                 "r"(sfb)                                                                      \
+                 : "memory")
+    if constexpr (PAIR && NV) MOE_UMMA_FP4("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (PAIR) MOE_UMMA_FP4("2", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (NV) MOE_UMMA_FP4("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else MOE_UMMA_FP4("1", "kind::mxf4.block_scale.scale_vec::2X");
+#undef MOE_UMMA_FP4
 }
 
 // ------------------------------------------------------- CTA pairs (clusters of two)

@@ -413,3 +413,13 @@ extern "C" int moe_expert_fwd_fp8(const uint8_t* Xq, const float* sX, const int6
         rc = launch<CfgStoreK8>(mh, mh, mwd, mwd, Q, token_tiles_max(rows, d, 128), st, moy);
     return rc;
 }
+
+int moe::launch_weight_grads(const moe_bf16* dY, const moe_bf16* X, const moe_bf16* H,
+                             const moe_bf16* dA, const moe_bf16* dU, const int64_t* row_offsets,
+                             int E, int64_t rows, int d, int f, moe_bf16* dW_g, moe_bf16* dW_u,
+                             moe_bf16* dW_d, void* ws, size_t ws_bytes, cudaStream_t st) {
+    WsCarver wc(ws, ws_bytes);
+    int32_t* order = wc.take<int32_t>(E + 1);
+    if (row_offsets && (!ws || !wc.ok())) return MOE_ERR_WORKSPACE;
+    return weight_grads(dY, X, H, dA, dU, row_offsets, E, rows, d, f, order, dW_g, dW_u, dW_d, st);
+}

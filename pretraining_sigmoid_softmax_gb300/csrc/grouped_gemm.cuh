@@ -32,6 +32,12 @@
 // bytes per FLOP drop by a third compared with a 128 x 256 tile on one SM. Both CTAs' TMA
 // loads complete on the leader's "full" barriers, the leader's commits arrive on both
 // CTAs' barriers (multicast), and both epilogues release the accumulator to the leader.
+// E2M1 operands (two codes a byte, 256 K elements per 128-byte row) bring the scales of their
+// blocks as 512-byte tiles of 128 rows x 4 blocks: TMA copies them beside the operands,
+// tcgen05.cp puts them into tensor memory in front of the instructions that read them, and
+// the tensor cores multiply them in (kind::mxf4 with a power of two per 32, kind::mxf4nvf4
+// with an E4M3 scale per 16). The scales leave less than two whole accumulators of 256
+// columns, so the two share a few columns (Cfg::OV).
 // Operand tiles use the 128-byte swizzle. K-major tiles are TMA boxes of 64 K-elements x
 // rows; MN-major tiles are boxes of 64 MN-elements x 64 k-rows. Every wait on an mbarrier
 // is bounded in time; a wait that runs out records MOE_ERR_TIMEOUT, stops every role of
@@ -54,6 +60,8 @@ namespace {
 constexpr int BM = 128;
 constexpr int BK = 64;        // bf16 K elements per stage (128 bytes per row)
 constexpr int BK_FP8 = 128;   // E4M3 K elements per stage (also 128 bytes per row)
+constexpr int BK_FP4 = 256;   // E2M1 K elements per stage (also 128 bytes per row)
+constexpr int kSfTile = 512;  // bytes of a scale tile: 128 rows x 4 blocks
 constexpr int kEpiWarps = 8;  // default: two per TMEM lane quadrant, each half the columns
 constexpr int kSmemBudget = 200 * 1024;
 
@@ -69,16 +77,22 @@ constexpr int kSmemBudgetAu = 220 * 1024;
 // backward, whose operand ring then keeps a fifth stage (what bounds it at K = 4096).
 constexpr int kOutCols = 16;
 
+// Operand types (Cfg's QT_; 0 and 1 also as false and true).
+enum Operands : int { kBf16 = 0, kE4m3 = 1, kMxFp4 = 2, kNvFp4 = 3 };
+
 template <int BN_, bool A_MN_, bool B_MN_, bool DUAL_, int EPI_, bool TWO_K_, bool WGRAD_,
-          bool PAIR_ = false, bool FP8_ = false, int OC_ = kOutCols, int EW_ = kEpiWarps>
+          bool PAIR_ = false, int QT_ = kBf16, int OC_ = kOutCols, int EW_ = kEpiWarps>
 struct Cfg {
     // epilogue warps: 8 (two per TMEM lane quadrant), or 16 for GEMMs whose reduction is so
     // short that the epilogue, not the tensor cores, sets the pace (at most 96 registers)
     static constexpr int EW = EW_;
     static constexpr int THREADS = 128 + 32 * EW;
     static_assert(EW == 8 || EW == 16, "epilogue warps");
-    static constexpr bool FP8 = FP8_;        // E4M3 operands with row / column scales
-    static constexpr int KB = FP8 ? BK_FP8 : BK;  // K elements per stage
+    static constexpr bool FP8 = QT_ == kE4m3;  // E4M3 operands with row / column scales
+    static constexpr bool NV = QT_ == kNvFp4;  // E2M1, E4M3 scale per 16, power of two per row
+    static constexpr bool FP4 = QT_ == kMxFp4 || NV;
+    static constexpr bool SCALED = FP8 || NV;  // row and column scales applied in the epilogue
+    static constexpr int KB = FP4 ? BK_FP4 : FP8 ? BK_FP8 : BK;  // K elements per stage
     static constexpr int BN = BN_;           // output columns per tile (per B matrix if DUAL)
     static constexpr bool A_MN = A_MN_;
     static constexpr bool B_MN = B_MN_;
@@ -92,7 +106,14 @@ struct Cfg {
     static constexpr int TILE_M = PAIR ? 2 * BM : BM;        // rows of one (pair) tile
     static constexpr int A_BYTES = BM * 128;     // 128-byte rows in either type
     static constexpr int B_BYTES = BROWS * 128;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;   // this CTA's bytes per K block
+    // E2M1: tiles of scales per operand row block and stage (a tile spans 128 K elements with
+    // blocks of 32, 64 with blocks of 16). Each CTA of a pair takes its own A rows' scales and
+    // those of all the tile's B columns.
+    static constexpr int SFK = FP4 ? (NV ? 4 : 2) : 0;
+    static constexpr int SFB_TILES = (MMA_N + 127) / 128;
+    static constexpr int SFA_BYTES = SFK * kSfTile;
+    static constexpr int SF_BYTES = SFA_BYTES * (1 + SFB_TILES);
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;  // this CTA's bytes per K block
     static constexpr bool AU = EPI == kEpiSwigluBwd;
     static constexpr int AU_BUF_BYTES = 2 * 32 * kAuCols * 2;  // a and u: 32 rows x kAuCols
     static constexpr int AU_BYTES = AU ? EW * kAuBufs * AU_BUF_BYTES : 0;
@@ -109,12 +130,23 @@ struct Cfg {
     static constexpr int BUDGET = (AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
     static constexpr int STAGES = (BUDGET / STAGE_BYTES) > 6 ? 6 : (BUDGET / STAGE_BYTES);
     static constexpr int ACC_COLS = MMA_N;
-    static constexpr int TMEM_COLS = 2 * ACC_COLS;  // two accumulator buffers
+    // E2M1: the scales of a stage take SFK * 4 * (1 + SFB_TILES) columns of tensor memory at
+    // its start. With 256-column accumulators the two buffers then share OV columns: the last
+    // of buffer 0 are the first of buffer 1. The epilogue takes the shared columns first and
+    // reports them read, and a tile's first instruction waits for that report of the tile
+    // before it (and for the whole of the one before that, as without sharing).
+    static constexpr int OV = FP4 && ACC_COLS == 256 ? (NV ? 48 : 32) : 0;
+    static constexpr int ACC0 = FP4 ? (OV ? OV : 128) : 0;
+    static constexpr int ACC1 = FP4 ? 256 : ACC_COLS;
+    static constexpr int TMEM_COLS = FP4 ? 512 : 2 * ACC_COLS;  // two accumulator buffers
+    static_assert(!FP4 || SFK * 4 * (1 + SFB_TILES) <= ACC0, "columns of the scales");
     // DUAL: the W_g and W_u boxes form one 2*BN-row B tile (on one CTA, back to back; in a
     // pair, W_g on the leader and W_u on the peer), so one instruction fills gate columns
     // [0, BN) and up columns [BN, 2BN).
-    static constexpr uint32_t IDESC = idesc_mma(MMA_N, TILE_M, A_MN, B_MN, FP8);
-    static_assert(!FP8 || (!A_MN && !B_MN && !WGRAD && !TWO_K), "FP8: forward K-major GEMMs");
+    static constexpr uint32_t IDESC =
+        FP4 ? idesc_fp4(MMA_N, TILE_M, !NV) : idesc_mma(MMA_N, TILE_M, A_MN, B_MN, FP8);
+    static_assert(!(FP8 || FP4) || (!A_MN && !B_MN && !WGRAD && !TWO_K),
+                  "E4M3 and E2M1: K-major GEMMs");
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory columns");
     static_assert(BN % 64 == 0 && MMA_N <= 256 && BROWS % 64 == 0, "tile width");
     static constexpr size_t MISC_BYTES = 512 + sizeof(int64_t) * (kMaxExperts + 1) +
@@ -122,7 +154,9 @@ struct Cfg {
                                          sizeof(int32_t) * (kMaxExperts + 1);
     static constexpr size_t SMEM_BYTES =
         1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + MISC_BYTES;
-    static_assert((2 * STAGES + 4 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
+    static_assert((2 * STAGES + 5 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
+    static_assert(OV == 0 || (OCOLS == kOutCols && OV <= BN / (EW / 4)), "shared columns of one warp");
+    static_assert(STAGES * SF_BYTES % 1024 == 0, "alignment of what follows the stages");
 
 };
 
@@ -151,6 +185,7 @@ struct Params {
     // (the slot's logit gradient times its expert's router row, both fp32)
     const float* r1_row;
     const float* r1_col;
+    bool only_h;               // E2M1 G1: h alone is written (nothing is kept for a backward)
     int* status;
     uint64_t wait_limit_ns;
 };
@@ -168,10 +203,12 @@ struct TileInfo {
 struct SmemLayout {
     uint8_t* a;        // STAGES x A tile
     uint8_t* b;        // STAGES x B tile(s)
+    uint8_t* sf;       // STAGES x scale tiles (E2M1): A's, then B's
     uint64_t* full;    // STAGES
     uint64_t* empty;   // STAGES
     uint64_t* tfull;   // 2
     uint64_t* tempty;  // 2
+    uint64_t* tshared; // the accumulators' shared columns are read (E2M1)
     uint32_t* tmem_slot;
     int* abort_flag;
     int64_t* offs;     // E + 1
@@ -188,14 +225,16 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.a = base;
     s.b = base + (size_t)C::STAGES * C::A_BYTES;
-    s.au = base + (size_t)C::STAGES * C::STAGE_BYTES;  // 1024-aligned: stage sizes are
+    s.sf = base + (size_t)C::STAGES * (C::A_BYTES + C::B_BYTES);
+    s.au = base + (size_t)C::STAGES * C::STAGE_BYTES;  // 1024-aligned: the stages are together
     s.ob = s.au + C::AU_BYTES;  // 1024-aligned: the a/u buffers are whole KB
     uint8_t* misc = s.ob + C::OUT_BYTES;
     s.full = reinterpret_cast<uint64_t*>(misc);
     s.empty = s.full + C::STAGES;
     s.tfull = s.empty + C::STAGES;
     s.tempty = s.tfull + 2;
-    s.au_full = s.tempty + 2;
+    s.tshared = s.tempty + 2;
+    s.au_full = s.tshared + 1;
     s.tmem_slot = reinterpret_cast<uint32_t*>(s.au_full + (C::AU ? C::EW * kAuBufs : 0));
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
     s.offs = reinterpret_cast<int64_t*>(misc + 512);
@@ -278,7 +317,8 @@ __device__ __forceinline__ TileInfo decode(int64_t tile, const Params& P, const 
             ti.e = last_le(S.offs, P.E, ti.m0);
             ti.row_end = S.offs[ti.e + 1];
         }
-        ti.k_iters = (P.K0 + (C::TWO_K ? P.K1 : 0)) / C::KB;
+        if constexpr (C::FP4) ti.k_iters = (P.K0 + C::KB - 1) / C::KB;  // the last may be half a block
+        else ti.k_iters = (P.K0 + (C::TWO_K ? P.K1 : 0)) / C::KB;
     }
     return ti;
 }
@@ -288,6 +328,67 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
                                          int32_t c0, int32_t c1) {
     if constexpr (C::PAIR) tma_load_2d_pair(dst, map, bar, c0, c1);
     else tma_load_2d(dst, map, bar, c0, c1);
+}
+
+// Loads of K block `kb` of an E2M1 tile. Where K ends inside the block (K is a multiple of 128)
+// the codes past it read as zero and the scales past it are whatever lies there; no
+// instruction uses either.
+template <class C>
+__device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint32_t a_dst,
+                                                uint32_t b_dst, uint32_t sf_dst, uint32_t bar,
+                                                const Params& P, const CUtensorMap* ma0,
+                                                const CUtensorMap* mb0, const CUtensorMap* mb1,
+                                                const CUtensorMap* msa, const CUtensorMap* msb0,
+                                                const CUtensorMap* msb1, uint32_t rank) {
+    const int32_t kbyte = kb * (C::KB / 2);
+    const int32_t ktiles = P.K0 / (C::KB / C::SFK);  // scale tiles along K
+    const int32_t kt = kb * C::SFK;
+    const int32_t brow = ti.e * P.N + ti.n0;  // a multiple of 128, as N and the tile's columns are
+    tma_load<C>(a_dst, ma0, bar, kbyte, (int32_t)ti.m0);
+    if constexpr (C::DUAL) {
+        if constexpr (C::PAIR) {
+            tma_load<C>(b_dst, rank == 0 ? mb0 : mb1, bar, kbyte, brow);
+        } else {
+            tma_load<C>(b_dst, mb0, bar, kbyte, brow);
+            tma_load<C>(b_dst + C::BN * 128, mb1, bar, kbyte, brow);
+        }
+    } else {
+        tma_load<C>(b_dst, mb0, bar, kbyte, brow + (C::PAIR ? (int32_t)rank * C::BROWS : 0));
+    }
+    tma_load<C>(sf_dst, msa, bar, 0, (int32_t)(ti.m0 / BM) * ktiles + kt);
+#pragma unroll
+    for (int h = 0; h < C::SFB_TILES; ++h)
+        tma_load<C>(sf_dst + (1 + h) * C::SFA_BYTES, C::DUAL && h == 1 ? msb1 : msb0, bar, 0,
+                    (brow / BM + (C::DUAL ? 0 : h)) * ktiles + kt);
+}
+
+// Instructions of one E2M1 K block: its scales into tensor memory (column tmem_sf on; in issue
+// order in front of the instructions that read them), then a step per 64 K elements.
+template <class C>
+__device__ __forceinline__ void issue_mma_fp4(uint32_t d_tmem, uint32_t tmem_sf, uint32_t a_s,
+                                              uint32_t b_s, uint32_t sf_s, int steps, bool first) {
+    constexpr int kPerTile = C::NV ? 1 : 2;  // steps that one scale tile covers
+    const uint32_t sfb = tmem_sf + C::SFK * 4;
+    const int tiles = steps / kPerTile;
+#pragma unroll
+    for (int t = 0; t < C::SFK; ++t) {
+        if (t >= tiles) break;
+        tmem_cp_scales<C::PAIR>(tmem_sf + 4 * t, sdesc_plain(sf_s + t * kSfTile));
+#pragma unroll
+        for (int h = 0; h < C::SFB_TILES; ++h)
+            tmem_cp_scales<C::PAIR>(sfb + 4 * (C::SFB_TILES * t + h),
+                                    sdesc_plain(sf_s + (1 + h) * C::SFA_BYTES + t * kSfTile));
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+        if (kk >= steps) break;
+        const int t = kk / kPerTile;
+        const uint32_t id = C::NV ? 0u : 2u * (kk & 1);  // which half of the tile's four blocks
+        umma_fp4<C::PAIR, C::NV>(d_tmem, sdesc_sw128(a_s + kk * 32, 16, 1024),
+                                 sdesc_sw128(b_s + kk * 32, 16, 1024),
+                                 C::IDESC | (id << 29) | (id << 4), tmem_sf + 4 * t,
+                                 sfb + 4 * C::SFB_TILES * t, !first || kk > 0);
+    }
 }
 
 // Loads of K block `kb` of a tile into this CTA's stage buffers; `bar` is the barrier the
@@ -341,6 +442,29 @@ __device__ __forceinline__ void issue_loads(const TileInfo& ti, int kb, uint32_t
 __device__ __forceinline__ uint4 pack_chunk8(const float* v) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                       pack_bf16x2(v[6], v[7]));
+}
+
+// E2M1 accumulators that share columns: which chunks of a tile a warp takes first, and the report
+// that the shared ones are read. Buffer 0 shares its last columns, so its chunks run backwards;
+// the warps that hold the shared columns (the last or the first group) report, once a tile.
+struct Shared {
+    bool reversed;  // chunks in descending order of their columns
+    bool reports;   // this warp holds shared columns
+    uint32_t bar;   // shared::cluster address in a pair, else this CTA's barrier
+};
+
+template <class C>
+__device__ __forceinline__ void report_shared(Shared& sh, int lane) {
+    if constexpr (C::OV > 0) {
+        if (!sh.reports) return;
+        sh.reports = false;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (C::PAIR) mbar_arrive_cluster(sh.bar);
+            else mbar_arrive(sh.bar);
+        }
+    }
 }
 
 // FP8 dequantisation of a 32-column accumulator chunk: value * scale(A row) * scale(B row
@@ -427,7 +551,8 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
                                                    uint32_t t_acc, int q, int lane, int slot,
                                                    int c_lo, int ncols, const Params& P,
                                                    const CUtensorMap* mo0, const CUtensorMap* mo1,
-                                                   const CUtensorMap* mo2, uint32_t& n) {
+                                                   const CUtensorMap* mo2, uint32_t& n,
+                                                   Shared& sh) {
     constexpr int W = C::OCOLS;
     if (ti.m0 >= ti.row_end) return;  // warp-uniform: the whole half is past the segment
     const int64_t row0 = ti.m0 + 32 * q;
@@ -435,19 +560,20 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
     // row scale is read from the last row instead
     const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
     for (int i = 0; i < ncols / W; ++i, ++n) {
-        const int c = c_lo + i * W;
+        const int c = c_lo + (C::OV && sh.reversed ? ncols / W - 1 - i : i) * W;
         float v[C::NOUT][W];
         if constexpr (C::EPI == kEpiSwigluFwd) {
             uint32_t g[W], u[W];
             tmem_ld_cols<W>(t_acc + c, g);
             tmem_ld_cols<W>(t_acc + C::BN + c, u);
             tmem_ld_wait();
+            if (C::OV && i == C::OV / W - 1) report_shared<C>(sh, lane);
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 v[0][j] = __uint_as_float(g[j]);
                 v[1][j] = __uint_as_float(u[j]);
             }
-            if constexpr (C::FP8) fp8_scale<W>(v[0], v[1], P, row, ti, c);
+            if constexpr (C::SCALED) fp8_scale<W>(v[0], v[1], P, row, ti, c);
             const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
 #pragma unroll
             for (int j = 0; j < W; ++j)
@@ -456,9 +582,10 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
             uint32_t r[W];
             tmem_ld_cols<W>(t_acc + c, r);
             tmem_ld_wait();
+            if (C::OV && i == C::OV / W - 1) report_shared<C>(sh, lane);
 #pragma unroll
             for (int j = 0; j < W; ++j) v[0][j] = __uint_as_float(r[j]);
-            if constexpr (C::FP8) fp8_scale<W>(v[0], v[0], P, row, ti, c, /*dual=*/false);
+            if constexpr (C::SCALED) fp8_scale<W>(v[0], v[0], P, row, ti, c, /*dual=*/false);
             if constexpr (C::EPI == kEpiStore && !C::WGRAD) {
                 if (P.r1_row) {  // the slot's router term, one fp32 FMA per element
                     const float g = __ldg(P.r1_row + row);
@@ -478,10 +605,12 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
         uint8_t* buf = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
         if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
         __syncwarp();
+        const int o_lo = C::FP4 && C::EPI == kEpiSwigluFwd && P.only_h ? 2 : 0;
 #pragma unroll
         for (int o = 0; o < C::NOUT; ++o)
 #pragma unroll
             for (int j = 0; j < W / 8; ++j)
+                if (o >= o_lo)
                 *reinterpret_cast<uint4*>(buf + o * C::OUT_BOX_BYTES +
                                           (W == 32 ? sw64_offset(lane, j) : sw32_offset(lane, j))) =
                     pack_chunk8(v[o] + 8 * j);
@@ -491,7 +620,7 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
             const CUtensorMap* mo[3] = {mo0, mo1, mo2};
 #pragma unroll
             for (int o = 0; o < C::NOUT; ++o)
-                tma_store_2d(mo[o], smem_u32(buf + o * C::OUT_BOX_BYTES), ti.n0 + c, (int32_t)row0);
+                if (o >= o_lo) tma_store_2d(mo[o], smem_u32(buf + o * C::OUT_BOX_BYTES), ti.n0 + c, (int32_t)row0);
             bulk_commit();
         }
     }
@@ -526,6 +655,12 @@ __device__ __forceinline__ void au_issue(const SmemLayout& S, const CUtensorMap*
     tma_load_2d(dst + C::AU_BUF_BYTES / 2, mu, bar, col, (int32_t)row0);
 }
 
+// Which chunk of columns a warp takes i-th.
+template <class C>
+__device__ __forceinline__ int au_chunk(int i, int nch, const Shared& sh) {
+    return C::OV && sh.reversed ? nch - 1 - i : i;
+}
+
 // One tile of this warp's columns [c_lo, c_lo + ncols). `n` counts the warp's chunks over the
 // kernel's life (it picks buffer and phase). Returns false when a wait failed (uniform
 // across the warp).
@@ -535,7 +670,8 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
                                                   int c_lo, int ncols, const Params& P,
                                                   const CUtensorMap* ma, const CUtensorMap* mu,
                                                   const CUtensorMap* mda, const CUtensorMap* mdu,
-                                                  uint32_t& n, volatile int* abort_flag) {
+                                                  uint32_t& n, volatile int* abort_flag,
+                                                  Shared& sh) {
     static_assert(kAuCols == kOutCols, "one staged output chunk per a/u chunk");
     const int nch = ncols / kAuCols;
     const int64_t row0 = ti.m0 + 32 * q;
@@ -549,7 +685,7 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
     const float g = (P.row_scale && ok_row) ? __ldg(P.row_scale + row) : 1.0f;
     float gpart = 0.f;
     for (int i = 0; i < nch; ++i, ++n) {
-        const int c = c_lo + i * kAuCols;
+        const int c = c_lo + au_chunk<C>(i, nch, sh) * kAuCols;
         const int b = (int)(n % kAuBufs);
         uint32_t acc[kAuCols];
         tmem_ld_cols<kAuCols>(t_acc + c, acc);
@@ -558,6 +694,7 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
         tmem_ld_wait();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
+        if (C::OV && i == C::OV / kAuCols - 1) report_shared<C>(sh, lane);
         float dav[kAuCols], duv[kAuCols];
         if (store) {  // lanes past an unpadded layout's end see zero-filled a, u and acc
             const uint8_t* abuf = S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES;
@@ -566,7 +703,7 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
 #pragma unroll
             for (int j = 0; j < kAuCols; ++j) accf[j] = __uint_as_float(acc[j]);
             // FP8 operands: the dequantised r = (dy codes) (W_d codes) * scale(row) * scale(col)
-            if constexpr (C::FP8)
+            if constexpr (C::SCALED)
                 fp8_scale<kAuCols>(accf, accf, P, ok_row ? row : ti.row_end - 1, ti, c, false);
 #pragma unroll
             for (int j = 0; j < kAuCols / 8; ++j) {
@@ -587,14 +724,15 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
                 }
             }
             const int col = ti.n0 + c;
-            if (P.gate_part && (col + kAuCols) % 64 == 0) {  // last chunk of a 64-column group
+            if (!C::OV && P.gate_part && (col + kAuCols) % 64 == 0) {  // last chunk of a 64-column group
                 if (ok_row) P.gate_part[row * (int64_t)(P.ld_out / 64) + col / 64] = gpart;
                 gpart = 0.f;
             }
         }
         __syncwarp();  // every lane is done with a/u buffer b
         if (lane == 0 && i + kAuBufs < nch)
-            au_issue<C>(S, ma, mu, slot, n + kAuBufs, row0, ti.n0 + c + kAuBufs * kAuCols);
+            au_issue<C>(S, ma, mu, slot, n + kAuBufs, row0,
+                        ti.n0 + c_lo + au_chunk<C>(i + kAuBufs, nch, sh) * kAuCols);
         if (store) {
             uint8_t* ob = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
             if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
@@ -616,15 +754,12 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
     return true;
 }
 
+// msa, msb0, msb1: scale tiles of A, the first and the second B operand (E2M1 only).
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1)
-    grouped_gemm_kernel(const __grid_constant__ CUtensorMap ma0,
-                        const __grid_constant__ CUtensorMap ma1,
-                        const __grid_constant__ CUtensorMap mb0,
-                        const __grid_constant__ CUtensorMap mb1,
-                        const __grid_constant__ CUtensorMap mo0,
-                        const __grid_constant__ CUtensorMap mo1,
-                        const __grid_constant__ CUtensorMap mo2, const Params P) {
+__device__ __forceinline__ void grouped_gemm_body(
+    const CUtensorMap& ma0, const CUtensorMap& ma1, const CUtensorMap& mb0, const CUtensorMap& mb1,
+    const CUtensorMap& mo0, const CUtensorMap& mo1, const CUtensorMap& mo2, const CUtensorMap* msa,
+    const CUtensorMap* msb0, const CUtensorMap* msb1, const Params& P) {
     extern __shared__ uint8_t gg_smem_raw[];
     const SmemLayout S = carve<C>(gg_smem_raw);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -643,6 +778,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(smem_u32(&S.tfull[b]), 1);
             mbar_init(smem_u32(&S.tempty[b]), C::PAIR ? 2 * C::EW : C::EW);
         }
+        if constexpr (C::OV > 0) mbar_init(smem_u32(S.tshared), C::PAIR ? 8 : 4);
         if constexpr (C::AU)
             for (int b = 0; b < C::EW * kAuBufs; ++b) mbar_init(smem_u32(&S.au_full[b]), 1);
         *S.abort_flag = 0;
@@ -705,6 +841,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tma_prefetch_desc(&mb0);
         if (C::TWO_K || C::WGRAD) tma_prefetch_desc(&ma1);
         if (C::TWO_K || C::DUAL) tma_prefetch_desc(&mb1);
+        if constexpr (C::FP4) {
+            tma_prefetch_desc(msa);
+            tma_prefetch_desc(msb0);
+            if (C::DUAL) tma_prefetch_desc(msb1);
+        }
         int stage = 0;
         uint32_t phase = 0;
         for (int64_t tile = first_tile; tile < ntiles; tile += tile_step) {
@@ -724,9 +865,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 } else {
                     mbar_arrive_expect_tx(full, C::STAGE_BYTES);
                 }
-                issue_loads<C>(ti, kb, smem_u32(S.a + (size_t)stage * C::A_BYTES),
-                               smem_u32(S.b + (size_t)stage * C::B_BYTES), bar, P, &ma0, &ma1,
-                               &mb0, &mb1, rank);
+                const uint32_t a_dst = smem_u32(S.a + (size_t)stage * C::A_BYTES);
+                const uint32_t b_dst = smem_u32(S.b + (size_t)stage * C::B_BYTES);
+                if constexpr (C::FP4)
+                    issue_loads_fp4<C>(ti, kb, a_dst, b_dst,
+                                       smem_u32(S.sf + (size_t)stage * C::SF_BYTES), bar, P, &ma0,
+                                       &mb0, &mb1, msa, msb0, msb1, rank);
+                else
+                    issue_loads<C>(ti, kb, a_dst, b_dst, bar, P, &ma0, &ma1, &mb0, &mb1, rank);
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1u;
@@ -746,8 +892,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (!mbar_wait_bounded(smem_u32(&S.tempty[buf]), use ^ 1u, abort_flag, P.status,
                                    P.wait_limit_ns, 31))
                 break;
+            if constexpr (C::OV > 0)  // the columns shared with the previous tile's accumulator
+                if (local > 0 && !mbar_wait_bounded(smem_u32(S.tshared), (local - 1) & 1, abort_flag,
+                                                    P.status, P.wait_limit_ns, 35))
+                    break;
             tc_fence_after();
-            const uint32_t d_tmem = tmem_base + buf * C::ACC_COLS;
+            const uint32_t d_tmem = tmem_base + (buf ? C::ACC1 : C::ACC0);
             bool ok = true;
             for (int kb = 0; kb < ti.k_iters; ++kb) {
                 if (!mbar_wait_bounded(smem_u32(&S.full[stage]), phase, abort_flag, P.status,
@@ -758,6 +908,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_fence_after();
                 const uint32_t a_s = smem_u32(S.a + (size_t)stage * C::A_BYTES);
                 const uint32_t b_s = smem_u32(S.b + (size_t)stage * C::B_BYTES);
+                if constexpr (C::FP4) {
+                    const int left = (P.K0 - kb * C::KB) / 64;
+                    issue_mma_fp4<C>(d_tmem, tmem_base, a_s, b_s,
+                                     smem_u32(S.sf + (size_t)stage * C::SF_BYTES),
+                                     left < 4 ? left : 4, kb == 0);
+                } else {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {  // 4 instructions of 32 bytes of K
                     const uint64_t adesc = C::A_MN ? sdesc_sw128(a_s + kk * 2048, 8192, 1024)
@@ -769,6 +925,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     else if constexpr (C::PAIR) umma_bf16_pair(d_tmem, adesc, bdesc, C::IDESC, acc);
                     else if constexpr (C::FP8) umma_fp8(d_tmem, adesc, bdesc, C::IDESC, acc);
                     else umma_bf16(d_tmem, adesc, bdesc, C::IDESC, acc);
+                }
                 }
                 if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.empty[stage]), 0x3);
                 else umma_commit(smem_u32(&S.empty[stage]));
@@ -795,28 +952,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const TileInfo ti = decode<C>(tile, P, S, rank);
             const int buf = local & 1;
             const uint32_t ph = (local >> 1) & 1;
+            const int group = (warp - 4) / 4;
+            Shared sh{buf == 0, C::OV && (buf == 0 ? group == C::EW / 4 - 1 : group == 0),
+                      C::OV && C::PAIR ? mapa_shared(smem_u32(S.tshared), 0) : smem_u32(S.tshared)};
             if constexpr (C::AU) {  // this tile's first a/u chunks while the MMA runs
                 if (lane == 0)
                     for (int i = 0; i < kAuBufs && i < kCols / kAuCols; ++i)
                         au_issue<C>(S, &ma1, &mb1, slot, n_au + i, ti.m0 + 32 * q,
-                                    ti.n0 + c_lo + i * kAuCols);
+                                    ti.n0 + c_lo + au_chunk<C>(i, kCols / kAuCols, sh) * kAuCols);
             }
             bool ok = mbar_wait_bounded(smem_u32(&S.tfull[buf]), ph, abort_flag, P.status,
                                         P.wait_limit_ns, 33);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t t_acc = tmem_base + buf * C::ACC_COLS + ((uint32_t)(32 * q) << 16);
+            const uint32_t t_acc =
+                tmem_base + (buf ? C::ACC1 : C::ACC0) + ((uint32_t)(32 * q) << 16);
             if constexpr (C::AU) {
                 if (!swiglu_bwd_staged<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &ma1, &mb1,
-                                          &mo0, &mo1, n_au, abort_flag))
+                                          &mo0, &mo1, n_au, abort_flag, sh))
                     break;
             } else if constexpr (C::TS) {
                 epilogue_tma_store<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &mo0, &mo1, &mo2,
-                                      n_au);
+                                      n_au, sh);
             } else {
                 epilogue_wgrad<C>(ti, t_acc, row_in_tile, P, c_lo, c_lo + kCols);
             }
+            report_shared<C>(sh, lane);  // a half past its segment read nothing
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -841,6 +1003,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (C::PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
         else tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap ma0,
+                        const __grid_constant__ CUtensorMap ma1,
+                        const __grid_constant__ CUtensorMap mb0,
+                        const __grid_constant__ CUtensorMap mb1,
+                        const __grid_constant__ CUtensorMap mo0,
+                        const __grid_constant__ CUtensorMap mo1,
+                        const __grid_constant__ CUtensorMap mo2, const Params P) {
+    grouped_gemm_body<C>(ma0, ma1, mb0, mb1, mo0, mo1, mo2, nullptr, nullptr, nullptr, P);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap ma0,
+                            const __grid_constant__ CUtensorMap ma1,
+                            const __grid_constant__ CUtensorMap mb0,
+                            const __grid_constant__ CUtensorMap mb1,
+                            const __grid_constant__ CUtensorMap mo0,
+                            const __grid_constant__ CUtensorMap mo1,
+                            const __grid_constant__ CUtensorMap mo2,
+                            const __grid_constant__ CUtensorMap msa,
+                            const __grid_constant__ CUtensorMap msb0,
+                            const __grid_constant__ CUtensorMap msb1, const Params P) {
+    grouped_gemm_body<C>(ma0, ma1, mb0, mb1, mo0, mo1, mo2, &msa, &msb0, &msb1, P);
 }
 
 // ---------------------------------------------------------------------- host side
@@ -887,17 +1076,21 @@ bool out_maps(CUtensorMap (&mo)[3], const void* o0, const void* o1, const void* 
     return true;
 }
 
-// `mo` (TMA-store configurations only): the output maps from out_maps.
+// `mo` (TMA-store configurations only): the output maps from out_maps. `sf` (E2M1 only): the maps
+// of A's, the first and the second B operand's scale tiles.
 template <class C>
 int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
            const CUtensorMap& b1, const Params& P, int64_t max_tiles, cudaStream_t st,
-           const CUtensorMap* mo = nullptr) {
+           const CUtensorMap* mo = nullptr, const CUtensorMap* sf = nullptr) {
     static_assert(C::SMEM_BYTES <= 227 * 1024, "shared memory");
-    if (C::TS && !mo) return MOE_ERR_LAUNCH;
+    if ((C::TS && !mo) || (C::FP4 && !sf)) return MOE_ERR_LAUNCH;
     const CUtensorMap& o0 = mo ? mo[0] : a0;
     const CUtensorMap& o1 = mo ? mo[1] : a0;
     const CUtensorMap& o2 = mo ? mo[2] : a0;
-    auto kern = grouped_gemm_kernel<C>;
+    auto kern = [] {
+        if constexpr (C::FP4) return grouped_gemm_fp4_kernel<C>;
+        else return grouped_gemm_kernel<C>;
+    }();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)C::SMEM_BYTES) != cudaSuccess)
         return MOE_ERR_LAUNCH;
@@ -921,14 +1114,22 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
         if (max_tiles < pairs) pairs = max_tiles;
         if (pairs < 1) pairs = 1;
         cfg.gridDim = dim3(2 * (unsigned)pairs);
-        if (cudaLaunchKernelEx(&cfg, kern, a0, a1, b0, b1, o0, o1, o2, P) != cudaSuccess)
-            return MOE_ERR_LAUNCH;
+        cudaError_t rc;
+        if constexpr (C::FP4)
+            rc = cudaLaunchKernelEx(&cfg, kern, a0, a1, b0, b1, o0, o1, o2, sf[0], sf[1], sf[2], P);
+        else
+            rc = cudaLaunchKernelEx(&cfg, kern, a0, a1, b0, b1, o0, o1, o2, P);
+        if (rc != cudaSuccess) return MOE_ERR_LAUNCH;
         return launch_status();
     } else {
         int64_t grid = sm_count();
         if (max_tiles < grid) grid = max_tiles;
         if (grid < 1) grid = 1;
-        kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, st>>>(a0, a1, b0, b1, o0, o1, o2, P);
+        if constexpr (C::FP4)
+            kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, st>>>(a0, a1, b0, b1, o0, o1, o2, sf[0],
+                                                                    sf[1], sf[2], P);
+        else
+            kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, st>>>(a0, a1, b0, b1, o0, o1, o2, P);
         return launch_status();
     }
 }

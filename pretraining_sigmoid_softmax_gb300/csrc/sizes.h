@@ -14,6 +14,7 @@ constexpr int kNormMaxD = 32768;           // norm: widest row
 constexpr int kNormBwdParts = 608;         // norm backward: CTAs, a dw partial row each
 constexpr int kClipParts = 1216;           // gradient norm: CTAs, a partial sum each
 constexpr int kMaxGroups = 32;             // choice of experts: groups
+constexpr int kFp4MaxCols = 32768;          // 4-bit quantisation: widest row
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

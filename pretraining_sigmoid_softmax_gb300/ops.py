@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
+from typing import NamedTuple
 
 import torch
 
@@ -565,3 +566,209 @@ def moe_clip_grads(grads, max_norm, out, norm, ws, stream=None):
     _check(_lib.load().moe_clip_grads(_at(ptr), _at(optr), _at(numel), _at(types), len(grads), max_norm,
                                       _ptr("norm", norm, torch.float32, (2,), dev), wp, wn,
                                       _stream_of(stream, dev)), "moe_clip_grads")
+
+
+# ------------------------------------------------- microscaled 4-bit operands
+
+FP4_MX = 0  # a power of two for each 32 elements
+FP4_NV = 1  # an E4M3 scale for each 16 under a power of two for each row
+
+
+class Fp4(NamedTuple):
+    """A matrix (or a stack of E of them) in microscaled 4-bit floating point: codes q
+    [..., rows, cols / 2] uint8, tiled block scales s (uint8, ``moe_fp4_scale_bytes`` of all rows),
+    the rows' powers of two g fp32 (FP4_NV; None in FP4_MX), and the format."""
+    q: torch.Tensor
+    s: torch.Tensor
+    g: torch.Tensor | None
+    fmt: int
+
+
+def moe_fp4_scale_bytes(rows: int, cols: int, fmt: int) -> int:
+    return _lib.load().moe_fp4_scale_bytes(rows, cols, fmt)
+
+
+def fp4_empty(shape, fmt, device="cuda") -> Fp4:
+    """Buffers of an operand with this shape of elements ([..., rows, cols], cols % 128 == 0)."""
+    *lead, cols = shape
+    rows = 1
+    for n in lead:
+        rows *= n
+    nbytes = moe_fp4_scale_bytes(rows, cols, fmt)
+    if nbytes == 0:
+        raise MoEError(f"no 4-bit operand of shape {tuple(shape)} in format {fmt}: at least one row, "
+                       "columns in whole blocks of 128, FP4_MX or FP4_NV")
+    return Fp4(torch.empty((*lead, cols // 2), dtype=torch.uint8, device=device),
+               torch.empty((nbytes,), dtype=torch.uint8, device=device),
+               torch.empty((rows,), dtype=torch.float32, device=device) if fmt == FP4_NV else None, fmt)
+
+
+def _fp4(name, m, shape, fmt, dev):
+    """The addresses of an operand of this shape of elements and this format."""
+    if m is None:
+        raise MoEError(f"{name} is missing")
+    if m.fmt != fmt:
+        raise MoEError(f"{name} has format {m.fmt}, the call's is {fmt}")
+    *lead, cols = shape
+    rows = 1
+    for n in lead:
+        rows *= n
+    g = None
+    if fmt == FP4_NV:
+        g = _ptr(f"{name}.g", m.g, torch.float32, (rows,), dev)
+    elif m.g is not None:
+        raise MoEError(f"{name}.g: FP4_MX operands have no powers of two for their rows")
+    return (_ptr(f"{name}.q", m.q, torch.uint8, (*lead, cols // 2), dev),
+            _ptr(f"{name}.s", m.s, torch.uint8, (moe_fp4_scale_bytes(rows, cols, fmt),), dev), g)
+
+
+def _fp4_rows(name, m):
+    """The element shape of a 2-D operand, its format and the device of the call."""
+    if m is None:
+        raise MoEError(f"{name} is missing")
+    rows, half = _rows(f"{name}.q", m.q)
+    return rows, 2 * half, m.fmt, _device(m.q)
+
+
+def _fp4_stack(name, m):
+    """The number of matrices and the rows of a 3-D operand."""
+    if m is None:
+        raise MoEError(f"{name} is missing")
+    if m.q.dim() != 3:
+        raise MoEError(f"{name}.q must be [E, rows, cols / 2], got shape {tuple(m.q.shape)}")
+    return m.q.shape[0], m.q.shape[1]
+
+
+def _offsets(row_offsets, E, dev):
+    if row_offsets is None and E != 1:
+        raise MoEError(f"row_offsets is missing, with {E} experts")
+    return _opt("row_offsets", row_offsets, torch.int64, (E + 1,), dev)
+
+
+def _limit(rows_limit, dev):
+    return _opt("rows_limit", rows_limit, torch.int64, (1,), dev)
+
+
+def moe_quantize_rows_fp4(X, out, X1=None, rows_limit=None, stream=None):
+    """Rows of X [rows, cols] bf16, or of [X | X1], to the operand ``out`` (an Fp4)."""
+    rows, cols = shape = _rows("X", X)
+    dev, bf16 = _device(X), torch.bfloat16
+    fmt = out.fmt
+    q, s, g = _fp4("out", out, (rows, cols if X1 is None else 2 * cols), fmt, dev)
+    _check(_lib.load().moe_quantize_rows_fp4(_ptr("X", X, bf16, shape, dev),
+                                             _opt("X1", X1, bf16, shape, dev), _limit(rows_limit, dev),
+                                             rows, cols, fmt, q, s, g, _stream_of(stream, dev)),
+           "moe_quantize_rows_fp4")
+
+
+def moe_quantize_cols_fp4(X0, X1, out, stream=None):
+    """Columns of E matrices [E, K0, N] bf16 (of the stacks of X0 over X1 where X1 is given) to the
+    operand ``out`` [E, N, K], blocks along K = K0 or 2 K0."""
+    if X0 is None or X0.dim() != 3:
+        raise MoEError("X0 must be [E, K0, N]" + ("" if X0 is None else f", got shape {tuple(X0.shape)}"))
+    E, K0, N = shape = X0.shape
+    dev, bf16 = _device(X0), torch.bfloat16
+    q, s, g = _fp4("out", out, (E, N, K0 if X1 is None else 2 * K0), out.fmt, dev)
+    _check(_lib.load().moe_quantize_cols_fp4(_ptr("X0", X0, bf16, shape, dev),
+                                             _opt("X1", X1, bf16, shape, dev), E, K0, N, out.fmt, q, s,
+                                             g, _stream_of(stream, dev)), "moe_quantize_cols_fp4")
+
+
+def moe_dequantize_fp4(m, out, rows_limit=None, stream=None):
+    """The numbers an operand stands for, as bf16 in ``out`` (of its rows and columns)."""
+    half = m.q.shape[-1]
+    rows = m.q.numel() // max(half, 1)
+    dev = _device(m.q)
+    q, s, g = _fp4("m", m, (*m.q.shape[:-1], 2 * half), m.fmt, dev)
+    if out is not None and out.dim() >= 2 and out.is_contiguous():
+        out = out.view(-1, out.shape[-1])
+    _check(_lib.load().moe_dequantize_fp4(q, s, g, _limit(rows_limit, dev), rows, 2 * half, m.fmt,
+                                          _ptr("out", out, torch.bfloat16, (rows, 2 * half), dev),
+                                          _stream_of(stream, dev)), "moe_dequantize_fp4")
+
+
+def moe_permute_fp4(x, slot_to_row, perm_token, row_offsets, X, stream=None):
+    """The token rows of the operand x copied to their experts' rows of the operand X."""
+    T, d, fmt, dev = _fp4_rows("x", x)
+    R = _fp4_rows("X", X)[0]
+    k, E, i32 = _rows("slot_to_row", slot_to_row)[1], row_offsets.numel() - 1, torch.int32
+    if R < moe_padded_rows(T, k, E):
+        raise MoEError(f"X has {R} rows, the layout takes up to {moe_padded_rows(T, k, E)}")
+    _check(_lib.load().moe_permute_fp4(*_fp4("x", x, (T, d), fmt, dev),
+                                       _ptr("slot_to_row", slot_to_row, i32, (T, k), dev),
+                                       _ptr("perm_token", perm_token, i32, (R,), dev),
+                                       _ptr("row_offsets", row_offsets, torch.int64, (E + 1,), dev), T, d,
+                                       E, k, fmt, *_fp4("X", X, (R, d), fmt, dev),
+                                       _stream_of(stream, dev)), "moe_permute_fp4")
+
+
+def moe_grouped_gemm_fp4(X, row_offsets, W, Y, stream=None):
+    """Y[p] = X[p] W[e]^T for the rows p of each expert e: X [rows, K] and W [E, N, K] operands,
+    Y [rows, N] bf16; row_offsets None: one matrix over all rows."""
+    rows, K, fmt, dev = _fp4_rows("X", X)
+    E, N = _fp4_stack("W", W)
+    _check(_lib.load().moe_grouped_gemm_fp4(*_fp4("X", X, (rows, K), fmt, dev),
+                                            _offsets(row_offsets, E, dev), E, rows, K, N,
+                                            *_fp4("W", W, (E, N, K), fmt, dev), fmt,
+                                            _ptr("Y", Y, torch.bfloat16, (rows, N), dev),
+                                            _stream_of(stream, dev)), "moe_grouped_gemm_fp4")
+
+
+def moe_expert_fwd_fp4(X, row_offsets, W_g, W_u, W_d, A, U, H, Hc, Y, stream=None, row_gate=None):
+    """moe_expert_fwd on 4-bit operands: X [rows, d], W_g and W_u [E, f, d], W_d [E, d, f]; Hc takes
+    the operand made of H. A and U None: nothing is kept for a backward."""
+    rows, d, fmt, dev = _fp4_rows("X", X)
+    E, f = _fp4_stack("W_g", W_g)
+    bf16 = torch.bfloat16
+    _check(_lib.load().moe_expert_fwd_fp4(*_fp4("X", X, (rows, d), fmt, dev),
+                                          _offsets(row_offsets, E, dev), E, rows, d, f,
+                                          *_fp4("W_g", W_g, (E, f, d), fmt, dev),
+                                          *_fp4("W_u", W_u, (E, f, d), fmt, dev),
+                                          *_fp4("W_d", W_d, (E, d, f), fmt, dev), fmt,
+                                          _opt("A", A, bf16, (rows, f), dev),
+                                          _opt("U", U, bf16, (rows, f), dev),
+                                          _ptr("H", H, bf16, (rows, f), dev),
+                                          *_fp4("Hc", Hc, (rows, f), fmt, dev),
+                                          _ptr("Y", Y, bf16, (rows, d), dev),
+                                          _opt("row_gate", row_gate, torch.float32, (rows,), dev),
+                                          _stream_of(stream, dev)), "moe_expert_fwd_fp4")
+
+
+def moe_expert_bwd_fp4(dYc, dY, X, A, U, H, row_offsets, W_d, W_gu, dX, dA, dU, AUc, dW_g, dW_u, dW_d,
+                       ws, stream=None, parts=BWD_ALL, dl_rows=None, W_r=None):
+    """moe_expert_bwd with its data gradients on 4-bit operands: dYc, the rows of dY; W_d [E, f, d] and
+    W_gu [E, d, 2f], the columns of W_d and of W_g over W_u (moe_quantize_cols_fp4); AUc takes the
+    operand made of [dA | dU]. What ``parts`` leaves out may be None."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    rows, f = _rows("dA", dA)
+    dev = _device(dA)
+    dh, dx, w = parts & BWD_DH, parts & BWD_DX, parts & BWD_W
+    if dh:
+        _, d, fmt, _ = _fp4_rows("dYc", dYc)
+        E = _fp4_stack("W_d", W_d)[0]
+    elif dx:
+        E, d = _fp4_stack("W_gu", W_gu)
+        fmt = W_gu.fmt
+    else:
+        d, fmt = _rows("dY", dY)[1], FP4_MX
+        E = 1 if row_offsets is None else row_offsets.numel() - 1
+    no = (None, None, None)
+    wp, wn = _ws(ws, dev) if w and row_offsets is not None else (None, 0)
+
+    def rows_of(name, t, cols, need):
+        return (_ptr if need else _opt)(name, t, bf16, (rows, cols), dev)
+
+    def weight(name, t, shape):
+        return (_ptr if w else _opt)(name, t, bf16, shape, dev)
+
+    _check(_lib.load().moe_expert_bwd_fp4(
+        *(_fp4("dYc", dYc, (rows, d), fmt, dev) if dh else no), rows_of("dY", dY, d, w),
+        rows_of("X", X, d, w), rows_of("A", A, f, dh), rows_of("U", U, f, dh), rows_of("H", H, f, w),
+        _offsets(row_offsets, E, dev), E, rows, d, f,
+        *(_fp4("W_d", W_d, (E, f, d), fmt, dev) if dh else no),
+        *(_fp4("W_gu", W_gu, (E, d, 2 * f), fmt, dev) if dx else no), fmt, rows_of("dX", dX, d, dx),
+        rows_of("dA", dA, f, True), rows_of("dU", dU, f, True),
+        *(_fp4("AUc", AUc, (rows, 2 * f), fmt, dev) if dx else no), weight("dW_g", dW_g, (E, f, d)),
+        weight("dW_u", dW_u, (E, f, d)), weight("dW_d", dW_d, (E, d, f)), int(parts),
+        _opt("dl_rows", dl_rows, f32, (rows,), dev), _opt("W_r", W_r, f32, (E, d), dev), wp, wn,
+        _stream_of(stream, dev)), "moe_expert_bwd_fp4")

@@ -1,0 +1,259 @@
+"""Microscaled 4-bit operands (codes, scales, dispatch), the grouped product and the SwiGLU experts on
+them, against the oracle's definition in 64 bits.
+
+Codes and scales are compared bit for bit: every quotient is decided as the exact one is. A product
+of the operands is compared with the exact product of the numbers that they stand for: half a bf16
+step of it, and (K + 2) 2^-24 of the sum of magnitudes for the fp32 accumulation
+(``assert_gemm_exact``)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe_oracle as O
+from pretraining_sigmoid_softmax_gb300 import ops
+
+from gpu_common import assert_close, assert_gemm_exact, dev, h64, padded_offsets, randn_bf16, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [ops.FP4_MX, ops.FP4_NV]
+FILL = 0xEE
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    require_gpu()
+
+
+def operand(shape, fmt, fill=FILL):
+    m = ops.fp4_empty(shape, fmt)
+    m.q.fill_(fill)
+    m.s.fill_(fill)
+    if m.g is not None:
+        m.g.fill_(-7.0)
+    return m
+
+
+def codes_of(m):
+    """Codes one a byte, [rows, cols]."""
+    q = m.q.reshape(-1, m.q.shape[-1]).cpu().numpy()
+    return np.stack([q & 15, q >> 4], -1).reshape(q.shape[0], -1)
+
+
+def scale_bytes_of(m):
+    """[rows, blocks] scale bytes, each found at its documented place."""
+    rows, cols = m.q.numel() // m.q.shape[-1], 2 * m.q.shape[-1]
+    b = 16 if m.fmt == ops.FP4_NV else 32
+    span = 4 * b
+    r, j = np.arange(rows)[:, None], np.arange(cols // b)[None, :]
+    at = ((r // 128) * (cols // span) + j // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + j % 4
+    return m.s.cpu().numpy()[at], at
+
+
+def numbers(byte, fmt):
+    if fmt == ops.FP4_NV:
+        return torch.from_numpy(byte).view(torch.float8_e4m3fn).double().numpy()
+    return np.ldexp(1.0, byte.astype(np.int64) - 127)
+
+
+def check_operand(m, X64, n=None):
+    """Rows below n hold the oracle's codes and scales of X64; the others are untouched."""
+    nv = m.fmt == ops.FP4_NV
+    n = X64.shape[0] if n is None else n
+    code, S, g = O.quantize_rows_fp4(X64[:n], nv)
+    got = codes_of(m)
+    assert np.array_equal(got[:n], code)
+    byte, at = scale_bytes_of(m)
+    assert np.array_equal(numbers(byte[:n], m.fmt), S)
+    raw = m.s.cpu().numpy()
+    rest = np.ones(raw.shape, bool)
+    rest[at[:n]] = False
+    assert (raw[rest] == FILL).all(), "scales of rows that were not given"
+    if nv:
+        assert np.array_equal(m.g.cpu().numpy()[:n], g)
+        assert (m.g[n:] == -7.0).all()
+    assert (m.q.reshape(got.shape[0], -1)[n:] == FILL).all()
+
+
+def rows_in(rows, cols, seed, scale=1.0):
+    """Rows of different magnitudes with outliers, ties, zero blocks and a zero row."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * scale
+    x *= torch.pow(2.0, torch.randint(-12, 12, (rows, 1), generator=g).float())
+    x[:, ::97] *= 64
+    x = x.to(torch.bfloat16)
+    x[:, 32:64] = 0                                                    # a zero block
+    grid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, -0.25, -0.75, -1.25, -1.75, -2.5,
+                         -3.5, -5.0, 7.5]).to(torch.bfloat16)
+    x[0, 64:80], x[0, 80:96] = grid, grid * 0.5                        # exact midpoints
+    if rows > 2:
+        x[2] = 0
+    return x
+
+
+SIZES = [(1, 128), (3, 256), (7, 4096), (129, 384), (130, 1024), (1300, 2048), (2500, 128),
+         (1230, 4096), (5, 8192), (2, 32768), (3, 8320)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_row_codes_are_bit_exact(rows, cols, fmt):
+    x = rows_in(rows, cols, rows + cols)
+    m = operand((rows, cols), fmt)
+    ops.moe_quantize_rows_fp4(dev(x), m)
+    torch.cuda.synchronize()
+    check_operand(m, h64(x))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,cols,n", [(300, 256, 140), (1400, 384, 1290), (9, 4224, 4), (4, 128, 0)])
+def test_row_codes_of_two_halves_and_a_limit(rows, cols, n, fmt):
+    x0, x1 = rows_in(rows, cols, 1), rows_in(rows, cols, 2, 8.0)
+    m = operand((rows, 2 * cols), fmt)
+    limit = torch.tensor([n], device="cuda")
+    ops.moe_quantize_rows_fp4(dev(x0), m, X1=dev(x1), rows_limit=limit)
+    torch.cuda.synchronize()
+    check_operand(m, h64(torch.cat([x0, x1], 1)), n)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_codes_at_the_ends_of_the_range(fmt):
+    """Rows of one magnitude each, from bf16's subnormals to its largest numbers, and the magnitudes
+    around the border where a row's power of two changes (2688 times a power of two)."""
+    g = torch.Generator().manual_seed(5)
+    base = torch.randn(40, 256, generator=g).to(torch.bfloat16)
+    x = torch.cat([(base[:20].double() * 2.0 ** e).to(torch.bfloat16)[:2] for e in
+                   (-130, -126, -120, -110, -60, 0, 60, 110, 120)])
+    edge = base[:12].float().clamp(-1, 1).to(torch.bfloat16)
+    for i, v in enumerate([2672, 2688, 2704, 1344, 1352, 1336, 448, 6, 5.25, 5.28125, 5.21875, 2 ** 20 * 1.3125]):
+        edge[i, 0] = v
+    x = torch.cat([x, edge])
+    m = operand(tuple(x.shape), fmt)
+    ops.moe_quantize_rows_fp4(dev(x), m)
+    torch.cuda.synchronize()
+    check_operand(m, h64(x))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("E,K0,N,stack", [(1, 128, 128, False), (3, 256, 384, True), (5, 384, 256, False),
+                                          (2, 1024, 128, True)])
+def test_column_codes_are_bit_exact(E, K0, N, stack, fmt):
+    mats = [torch.stack([rows_in(K0, N, 7 * e + i) for e in range(E)]) for i in range(2 if stack else 1)]
+    if E > 1:
+        mats[0][1] = 0
+    m = operand((E, N, K0 * len(mats)), fmt)
+    ops.moe_quantize_cols_fp4(dev(mats[0]), dev(mats[1]) if stack else None, m)
+    torch.cuda.synchronize()
+    both = torch.cat(mats, 1).transpose(1, 2).reshape(E * N, -1)
+    check_operand(m, h64(both))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,cols", [(1, 128), (333, 640), (4000, 256)])
+def test_dequantised_numbers_are_exact(rows, cols, fmt):
+    x = rows_in(rows, cols, 3)
+    m = operand((rows, cols), fmt)
+    ops.moe_quantize_rows_fp4(dev(x), m)
+    out = torch.full((rows, cols), -3.0, dtype=torch.bfloat16, device="cuda")
+    n = rows - rows // 3
+    ops.moe_dequantize_fp4(m, out, rows_limit=torch.tensor([n], device="cuda"))
+    torch.cuda.synchronize()
+    assert np.array_equal(h64(out)[:n], O.fp4_dequant_rows(h64(x), fmt == ops.FP4_NV)[:n])
+    assert (out[n:] == -3.0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_infinities_and_nan_stay_in_their_block_or_row(fmt):
+    x = rows_in(6, 256, 9)
+    x[0, 70], x[3, 5], x[5, 200] = float("inf"), float("nan"), -float("inf")
+    m = operand((6, 256), fmt)
+    ops.moe_quantize_rows_fp4(dev(x), m)
+    out = torch.empty(6, 256, dtype=torch.bfloat16, device="cuda")
+    ops.moe_dequantize_fp4(m, out)
+    torch.cuda.synchronize()
+    bad = torch.zeros(6, 256, dtype=torch.bool)
+    if fmt == ops.FP4_NV:
+        bad[[0, 3, 5]] = True
+    else:
+        bad[0, 64:96], bad[3, 0:32], bad[5, 192:224] = True, True, True
+    assert torch.equal(out.cpu().isnan(), bad)
+    clean = x.clone()
+    clean[bad] = 0
+    want = O.fp4_dequant_rows(h64(clean), fmt == ops.FP4_NV)
+    assert np.array_equal(h64(out)[~bad.numpy()], want[~bad.numpy()])
+
+
+def _routing(T, E, k, g, skew):
+    w = torch.tensor([1.0 / (1 + i) ** (1.5 if skew else 0.0) for i in range(E)])
+    return torch.stack([torch.multinomial(w, k, generator=g) for _ in range(T)]).to(torch.int32)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,d,E,k,skew", [(1000, 256, 8, 2, False), (777, 512, 16, 4, True),
+                                          (5, 128, 16, 4, True), (1, 1152, 4, 1, False)])
+def test_permuted_codes_equal_quantised_permuted_rows(T, d, E, k, skew, fmt):
+    g = torch.Generator().manual_seed(T)
+    x = rows_in(T, d, T)
+    idx = dev(_routing(T, E, k, g, skew))
+    R = ops.moe_padded_rows(T, k, E)
+    i32, i64 = dict(dtype=torch.int32, device="cuda"), dict(dtype=torch.int64, device="cuda")
+    counts, off, ro = torch.empty(E, **i32), torch.empty(E + 1, **i64), torch.empty(E + 1, **i64)
+    tok, s2r = torch.empty(R, **i32), torch.empty(T, k, **i32)
+    Xp = torch.empty(R, d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ops.moe_workspace_bytes(T, d, E, k), dtype=torch.uint8, device="cuda")
+    ops.moe_permute(idx, dev(x), E, counts, off, ro, tok, s2r, Xp, ws)
+    xc, X = operand((T, d), fmt), operand((R, d), fmt)
+    ops.moe_quantize_rows_fp4(dev(x), xc)
+    ops.moe_permute_fp4(xc, s2r, tok, ro, X)
+    torch.cuda.synchronize()
+    n = int(ro[-1])
+    check_operand(X, h64(torch.cat([Xp[:n].cpu(), torch.zeros(R - n, d, dtype=torch.bfloat16)])), n)
+
+
+def layout(counts, extra=128):
+    """Offsets (or None), capacity, and the rows of each expert."""
+    if isinstance(counts, int):
+        return None, counts, [(0, counts)]
+    ro = padded_offsets(counts)
+    return ro, int(ro[-1]) + extra, [(int(ro[e]), int(ro[e]) + c) for e, c in enumerate(counts)]
+
+
+def made(t, fmt, limit=None):
+    m = ops.fp4_empty(tuple(t.shape), fmt)
+    ops.moe_quantize_rows_fp4(dev(t.reshape(-1, t.shape[-1])),
+                              ops.Fp4(m.q.view(-1, m.q.shape[-1]), m.s, m.g, fmt), rows_limit=limit)
+    return m
+
+
+COUNTS = [1, 600, [300, 0, 129, 1, 513], [0, 0, 128], [1, 1, 1, 127, 256]]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K,N", [(128, 128), (256, 256), (384, 640), (1152, 512), (2048, 256)])
+@pytest.mark.parametrize("counts", COUNTS)
+def test_product_matches_the_exact_one(counts, K, N, fmt):
+    g = torch.Generator().manual_seed(K + N)
+    ro, rows, segs = layout(counts)
+    E = len(segs)
+    X = torch.zeros(rows, K, dtype=torch.bfloat16)
+    for lo, hi in segs:
+        X[lo:hi] = rows_in(hi - lo, K, lo) if hi - lo > 2 else randn_bf16((hi - lo, K), g)
+    W = randn_bf16((E, N, K), g, K ** -0.5)
+    ro_d = None if ro is None else dev(torch.from_numpy(ro))
+    Xm, Wm = made(X, fmt, None if ro is None else ro_d[E:]), made(W, fmt)
+    if ro is not None:  # codes and scales past the layout are garbage, and stay out of the sums
+        n = int(ro[-1])
+        Xm.q[n:], Xm.s[n * K // (16 if fmt == ops.FP4_NV else 32):] = 0x77, 0x7F
+    Y = torch.full((rows, N), -3.0, dtype=torch.bfloat16, device="cuda")
+    ops.moe_grouped_gemm_fp4(Xm, ro_d, Wm, Y)
+    torch.cuda.synchronize()
+    assert ops.moe_device_status() == (0, 0)
+    nv = fmt == ops.FP4_NV
+    for e, (lo, hi) in enumerate(segs):
+        if hi > lo:
+            assert_gemm_exact(Y[lo:hi], O.fp4_dequant_rows(h64(X[lo:hi]), nv),
+                              O.fp4_dequant_rows(h64(W[e]), nv).T, f"e{e}")
+        if ro is not None:
+            assert (Y[hi:int(ro[e + 1])] == 0).all()
+    if ro is not None:
+        assert (Y[int(ro[-1]):] == -3.0).all()
