@@ -34,8 +34,10 @@ class MoEConfig:
     aux_seq: float = 0.0     # sequence-wise load-balancing loss coefficient (0 = off)
     seq_len: int = 0         # tokens per sequence for the sequence-wise loss
     # expert GEMM operands: "bf16"; "fp8" (E4M3 rowwise forward GEMMs); "fp8_dgrad" (also the
-    # backward's data-gradient GEMMs on E4M3; weight gradients stay bf16)
+    # backward's data-gradient GEMMs on E4M3; weight gradients stay bf16); "fp4", "fp4_dgrad":
+    # the same on microscaled 4-bit operands (fp4_format "nv" or "mx")
     precision: str = "bf16"
+    fp4_format: str = "nv"
 
     @property
     def fp8(self) -> bool:

@@ -18,6 +18,9 @@ from torch.autograd.function import once_differentiable
 from . import ops
 
 
+FP4_FORMATS = {"mx": ops.FP4_MX, "nv": ops.FP4_NV}
+
+
 @dataclass
 class MoEShape:
     T: int
@@ -40,6 +43,10 @@ class MoEShape:
     group_rule: int = ops.GROUP_TOP2
     renorm: bool | None = None
     gate_scale: float = 1.0
+    # expert forward GEMMs (and the backward's data-gradient GEMMs) on microscaled 4-bit operands
+    fp4: bool = False
+    fp4_dgrad: bool = False
+    fp4_format: int = ops.FP4_NV
 
     @property
     def renormalised(self) -> bool:
@@ -59,7 +66,9 @@ class MoEShape:
     def from_config(cls, cfg) -> "MoEShape":
         return cls(cfg.T, cfg.d, cfg.E, cfg.k, cfg.f, cfg.f_shared, cfg.mode_id, cfg.z_coef,
                    cfg.aux_switch, cfg.aux_seq, cfg.seq_len or cfg.T,
-                   cfg.precision in ("fp8", "fp8_dgrad"), cfg.precision == "fp8_dgrad")
+                   cfg.precision in ("fp8", "fp8_dgrad"), cfg.precision == "fp8_dgrad",
+                   fp4=cfg.precision in ("fp4", "fp4_dgrad"), fp4_dgrad=cfg.precision == "fp4_dgrad",
+                   fp4_format=FP4_FORMATS[cfg.fp4_format])
 
 
 def _empty(shape, dtype, dev):
@@ -80,6 +89,8 @@ class MoEPlan:
     def __init__(self, shape: MoEShape, device="cuda", backward: bool = True,
                  overlap_shared: bool | None = None):
         s = self.s = shape
+        if s.fp4 and s.fp8:
+            raise ValueError("the experts' operands are fp8 or fp4, not both")
         dev = torch.device(device)
         bf, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
         T, d, E, k, f, fs = s.T, s.d, s.E, s.k, s.f, s.f_shared
@@ -107,18 +118,20 @@ class MoEPlan:
         self.perm_token = _empty((R,), i32, dev)
         self.slot_to_row = _empty((T, k), i32, dev)
         self.X_perm = _empty((R, d), bf, dev)
-        self.A = _empty((R, f), bf, dev)
-        self.U = _empty((R, f), bf, dev)
+        # a and u are kept for a backward (the 4-bit experts can leave them out)
+        self.keeps = backward or not s.fp4
+        self.A = _empty((R, f), bf, dev) if self.keeps else None
+        self.U = _empty((R, f), bf, dev) if self.keeps else None
         self.H = _empty((R, f), bf, dev)
         self.Y_perm = _empty((R, d), bf, dev)
         # bf16 experts take each row's gate inside (g * h before the linear down projection);
-        # the FP8 experts quantise the ungated h, so there the combine applies the gates
-        self.fold_gate = not s.fp8
+        # the FP8 and 4-bit experts quantise the ungated h, so there the combine applies the gates
+        self.fold_gate = not (s.fp8 or s.fp4)
         self.row_gate = _empty((R,), f32, dev) if self.fold_gate else None
         self.out = _empty((T, d), bf, dev)
         if fs:
-            self.As = _empty((T, fs), bf, dev)
-            self.Us = _empty((T, fs), bf, dev)
+            self.As = _empty((T, fs), bf, dev) if self.keeps else None
+            self.Us = _empty((T, fs), bf, dev) if self.keeps else None
             self.Hs = _empty((T, fs), bf, dev)
             self.Ys = _empty((T, d), bf, dev)
         if s.fp8:  # E4M3 codes and fp32 scales of every forward GEMM operand
@@ -136,6 +149,19 @@ class MoEPlan:
                 self.Wsg8, self.sWsg = _empty((1, fs, d), u8, dev), _empty((fs,), f32, dev)
                 self.Wsu8, self.sWsu = _empty((1, fs, d), u8, dev), _empty((fs,), f32, dev)
                 self.Wsd8, self.sWsd = _empty((1, d, fs), u8, dev), _empty((d,), f32, dev)
+        if s.fp4:  # 4-bit operands: the tokens' rows, the experts' rows and the rows of h
+            def op4(*shape):
+                return ops.fp4_empty(shape, s.fp4_format, dev)
+
+            self.x4, self.X4, self.H4 = op4(T, d), op4(R, d), op4(R, f)
+            self.Hs4 = op4(T, fs) if fs else None
+            self.W4 = None  # of the weights: made by the first forward that is not given them
+            if backward and s.fp4_dgrad:
+                self.dY4, self.AU4 = op4(R, d), op4(R, 2 * f)
+                self.Wd4_t, self.Wgu4_t = op4(E, f, d), op4(E, d, 2 * f)
+                if fs:
+                    self.dYs4, self.AUs4 = op4(T, d), op4(T, 2 * fs)
+                    self.Wsd4_t, self.Wsgu4_t = op4(1, fs, d), op4(1, d, 2 * fs)
         if s.has_aux:
             self.aux_loss = torch.zeros((2,), dtype=f32, device=dev)
             self.aux_f = _empty((E + (T // s.seq_len) * E,), f32, dev)
@@ -220,15 +246,18 @@ class MoEPlan:
             n += 2 + (1 if backward else 0)                 # balancing losses (+ gradient)
         n += 4                                              # permute (the padding rows and
                                                             # folded row gates in the scatter)
-        if s.fp8:  # quantise x, W_g, W_u, W_d; expert-major codes (2); G1, quantise H, G2
+        if s.fp8 or s.fp4:  # quantise x, W_g, W_u, W_d; expert-major codes (2); G1, quantise H, G2
             n += 9 + (6 if s.f_shared else 0)               # (shared: its weights, G1, H, G2)
         else:
             n += 2 + (2 if s.f_shared else 0)               # expert forward (G1, G2)
         n += 1                                              # combine
         if backward:
             n += 1                                          # combine backward (+ padding rows)
-            n += 1 if not s.fp8 else 0                      # gate gradient from its partials
-            if s.fp8_dgrad:  # pad the dY codes, W_d and W_g/W_u columns (3 each), B2,
+            n += 1 if self.fold_gate else 0                 # gate gradient from its partials
+            if s.fp4_dgrad:  # dY rows, W_d and W_g/W_u columns (3 each, or 1 in blocks of 32), B2,
+                cols = 2 if s.fp4_format == ops.FP4_MX else 6  # [dA|dU] rows, B4, order, B3, B5
+                n += 7 + cols + (6 + cols if s.f_shared else 0)
+            elif s.fp8_dgrad:  # pad the dY codes, W_d and W_g/W_u columns (3 each), B2,
                 n += 13 + (12 if s.f_shared else 0)         # [dA|dU] rows, B4, order, B3, B5
                                                             # (shared: quantise dY rows)
             else:
@@ -244,8 +273,10 @@ class MoEPlan:
 
     # ------------------------------------------------------------------ forward
     def forward(self, x, W_r, b, W_g, W_u, W_d, Ws_g=None, Ws_u=None, Ws_d=None, stream=None,
-                codes=False):
-        """codes: x's E4M3 codes and scales are in x8 and sx already (moe_rms_norm wrote them)."""
+                codes=False, weights4=None):
+        """codes: x's E4M3 codes and scales are in x8 and sx already (moe_rms_norm wrote them).
+        weights4 (4-bit experts): the operands of the weights, in ``weights4``'s order, where they are
+        made already; else every forward makes them."""
         s = self.s
         self.x = x
         self.W = (W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d)
@@ -253,9 +284,13 @@ class MoEPlan:
         main = stream if stream is not None else torch.cuda.current_stream()
         if s.fp8 and not codes:  # before the fork: the routed rows and the shared expert both
             ops.moe_quantize_rows_fp8(x, None, self.x8, self.sx, stream)  # use them
+        W4 = None
+        if s.fp4:
+            ops.moe_quantize_rows_fp4(x, self.x4, stream=stream)
+            W4 = self._weights4(weights4, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, stream)
         if s.f_shared and self.overlap:  # fork: the shared expert on the side stream
             self.side.wait_stream(main)
-            self._shared_forward(x, Ws_g, Ws_u, Ws_d, self.side)
+            self._shared_forward(x, Ws_g, Ws_u, Ws_d, self.side, W4)
         if s.selects:
             ops.moe_router_logits(x, W_r, self.logits, self.ws, self.lse if softmax else None,
                                   self.z_loss if softmax else None, s.z_coef, stream)
@@ -288,6 +323,11 @@ class MoEPlan:
             self._gemm(ops.moe_expert_fwd_fp8, self.X8, self.sX, self.row_offsets, self.Wg8,
                        self.sWg, self.Wu8, self.sWu, self.Wd8, self.sWd, self.A, self.U, self.H,
                        self.H8, self.sH, self.Y_perm, self.ws, stream=stream)
+        elif s.fp4:
+            ops.moe_permute_fp4(self.x4, self.slot_to_row, self.perm_token, self.row_offsets, self.X4,
+                                stream)
+            self._gemm(ops.moe_expert_fwd_fp4, self.X4, self.row_offsets, *W4[:3], self.A, self.U,
+                       self.H, self.H4, self.Y_perm, stream=stream)
         else:
             self._gemm(ops.moe_expert_fwd, self.X_perm, self.row_offsets, W_g, W_u, W_d, self.A,
                        self.U, self.H, self.Y_perm, self.ws, stream=stream, row_gate=self.row_gate)
@@ -295,15 +335,28 @@ class MoEPlan:
             if self.overlap:  # join
                 main.wait_stream(self.side)
             else:
-                self._shared_forward(x, Ws_g, Ws_u, Ws_d, stream)
+                self._shared_forward(x, Ws_g, Ws_u, Ws_d, stream, W4)
             ys = self.Ys
         ops.moe_combine(self.Y_perm, None if self.fold_gate else self.topk_gate, self.slot_to_row,
                         ys, self.out, stream)
         return self.out
 
-    def _shared_forward(self, x, Ws_g, Ws_u, Ws_d, side):
+    def _weights4(self, given, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, stream):
+        """The 4-bit operands of the weights: those given, or this plan's, made anew."""
+        if given is not None:
+            return given
+        if self.W4 is None:
+            self.W4 = weights4(self.s.fp4_format, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, stream)
+        else:
+            _quantize_weights4(self.W4, (W_g, W_u, W_d, Ws_g, Ws_u, Ws_d), stream)
+        return self.W4
+
+    def _shared_forward(self, x, Ws_g, Ws_u, Ws_d, side, W4=None):
         """The shared expert's forward on stream `side` (every token, weight 1)."""
-        if self.s.fp8:
+        if self.s.fp4:
+            self._gemm(ops.moe_expert_fwd_fp4, self.x4, None, *W4[3:], self.As, self.Us, self.Hs,
+                       self.Hs4, self.Ys, stream=side)
+        elif self.s.fp8:
             q = ops.moe_quantize_rows_fp8
             q(Ws_g, None, self.Wsg8, self.sWsg, side)
             q(Ws_u, None, self.Wsu8, self.sWsu, side)
@@ -350,6 +403,19 @@ class MoEPlan:
                        self.Wguq_t, self.sWgu_t, self.dX_perm, self.dA, self.dU, self.AUq,
                        self.sAU, self.dW_g, self.dW_u, self.dW_d, self.ws, stream=stream,
                        dl_rows=self.dl_rows, W_r=W_r if self.router_rows else None)
+        elif s.fp4_dgrad:
+            ops.moe_combine_bwd(dY, self.Y_perm, self.topk_gate, self.slot_to_row, self.row_offsets,
+                                self.perm_token, self.dY_perm, self.dg, stream)
+            ops.moe_quantize_rows_fp4(self.dY_perm, self.dY4, rows_limit=self.row_offsets[s.E:],
+                                      stream=stream)
+            ops.moe_quantize_cols_fp4(W_d, None, self.Wd4_t, stream)
+            ops.moe_quantize_cols_fp4(W_g, W_u, self.Wgu4_t, stream)
+            if self.router_rows:
+                self._route_bwd(x, None, stream)
+            self._gemm(ops.moe_expert_bwd_fp4, self.dY4, self.dY_perm, self.X_perm, self.A, self.U,
+                       self.H, self.row_offsets, self.Wd4_t, self.Wgu4_t, self.dX_perm, self.dA,
+                       self.dU, self.AU4, self.dW_g, self.dW_u, self.dW_d, self.ws, stream=stream,
+                       dl_rows=self.dl_rows, W_r=W_r if self.router_rows else None)
         else:
             ops.moe_combine_bwd(dY, self.Y_perm, self.topk_gate, self.slot_to_row,
                                 self.row_offsets, self.perm_token, self.dY_perm, self.dg, stream)
@@ -364,9 +430,10 @@ class MoEPlan:
                                  s.aux_seq, self.dlogits_aux, stream)
             extra = self.dlogits_aux
         rows = self.router_rows
-        if not (rows and s.fp8_dgrad):  # (the FP8 path formed the logit gradient above)
+        formed = s.fp8_dgrad or s.fp4_dgrad  # (those paths formed the logit gradient above)
+        if not (rows and formed):
             self._route_bwd(x, extra, stream)
-        if rows and not s.fp8_dgrad:
+        if rows and not formed:
             self._gemm(ops.moe_expert_bwd, self.dY_perm, self.X_perm, self.A, self.U, self.H,
                        self.row_offsets, W_g, W_u, W_d, self.dX_perm, self.dA, self.dU,
                        self.dW_g, self.dW_u, self.dW_d, self.ws, stream=stream,
@@ -407,6 +474,14 @@ class MoEPlan:
                           dl_rows=self.dl_rows)
 
     def _shared_backward(self, dY, x, Ws_g, Ws_u, Ws_d, st):
+        if self.s.fp4_dgrad:
+            ops.moe_quantize_rows_fp4(dY, self.dYs4, stream=st)
+            ops.moe_quantize_cols_fp4(Ws_d[None], None, self.Wsd4_t, st)
+            ops.moe_quantize_cols_fp4(Ws_g[None], Ws_u[None], self.Wsgu4_t, st)
+            self._gemm(ops.moe_expert_bwd_fp4, self.dYs4, dY, x, self.As, self.Us, self.Hs, None,
+                       self.Wsd4_t, self.Wsgu4_t, self.dxs, self.dAs, self.dUs, self.AUs4,
+                       self.dWs_g[None], self.dWs_u[None], self.dWs_d[None], self.ws_side, stream=st)
+            return
         if self.s.fp8_dgrad:
             ops.moe_quantize_rows_fp8(dY, None, self.dYsq, self.sdYs, st)
             ops.moe_quantize_cols_fp8(Ws_d[None], None, self.Wsdq_t, self.sWsd_t, st)
@@ -475,6 +550,22 @@ class MoEPlan:
         return g
 
 
+def _quantize_weights4(out, W, stream=None):
+    for m, w in zip(out, (w for w in W if w is not None)):
+        ops.moe_quantize_rows_fp4(w.reshape(-1, w.shape[-1]),
+                                  ops.Fp4(m.q.view(-1, m.q.shape[-1]), m.s, m.g, m.fmt), stream=stream)
+
+
+def weights4(fmt, W_g, W_u, W_d, Ws_g=None, Ws_u=None, Ws_d=None, stream=None):
+    """The 4-bit operands of a layer's expert weights (and of its shared expert's, as stacks of one),
+    for ``MoEPlan.forward(weights4=...)``."""
+    W = (W_g, W_u, W_d) + ((Ws_g[None], Ws_u[None], Ws_d[None]) if Ws_g is not None else ())
+    with torch.cuda.stream(stream):
+        out = tuple(ops.fp4_empty(tuple(w.shape), fmt, w.device) for w in W)
+    _quantize_weights4(out, W, stream)
+    return out
+
+
 class _MoEFunction(torch.autograd.Function):
     """One layer step as an autograd node over a plan's fixed buffers.
 
@@ -483,11 +574,12 @@ class _MoEFunction(torch.autograd.Function):
     forwards and the backward refuses a stale one."""
 
     @staticmethod
-    def forward(ctx, x, W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, plan, codes=False):
+    def forward(ctx, x, W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, plan, codes=False, weights4=None):
         ctx.plan = plan
         plan.generation += 1
         ctx.generation = plan.generation
-        out = plan.forward(x.contiguous(), W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, codes=codes)
+        out = plan.forward(x.contiguous(), W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, codes=codes,
+                           weights4=weights4)
         return out.clone()
 
     @staticmethod
@@ -503,7 +595,7 @@ class _MoEFunction(torch.autograd.Function):
         return (g["dx"].clone(), g["dW_r"].clone(), None, g["dW_g"].clone(), g["dW_u"].clone(),
                 g["dW_d"].clone(), g["dWs_g"].clone() if shared else None,
                 g["dWs_u"].clone() if shared else None, g["dWs_d"].clone() if shared else None,
-                None, None)
+                None, None, None)
 
 
 def _whole(t):
@@ -641,12 +733,18 @@ class MoELayer(torch.nn.Module):
     the same pass; a y that a hook or another module in ``norm``'s place made is quantised by
     the layer. ``n_group`` > 1 limits each token's experts to the ``topk_group`` best groups
     (``group_rule`` "max" or "top2": a group's score is its largest selection value or the sum
-    of its two largest); ``renorm`` and ``gate_scale`` set how gates follow from scores."""
+    of its two largest); ``renorm`` and ``gate_scale`` set how gates follow from scores.
+
+    ``precision`` "fp8" or "fp4" runs the experts' forward GEMMs on E4M3 or microscaled 4-bit operands
+    (``fp4_format`` "nv" or "mx"), "fp8_dgrad" and "fp4_dgrad" the backward's data gradients too. For
+    serving on 4-bit weights, ``hold_weights()`` quantises them once: forwards then take these codes,
+    keep nothing for a backward and are refused where a gradient is asked for, until
+    ``hold_weights(False)``. Call it again after the weights have changed."""
 
     def __init__(self, d, E, k, f, f_shared=0, mode="sigmoid", z_coef=0.0, gamma=1e-3,
                  device="cuda", bias_rule="sign", aux_switch=0.0, aux_seq=0.0, seq_len=0,
                  precision="bf16", norm_eps=None, n_group=1, topk_group=1, group_rule="top2",
-                 renorm=None, gate_scale=1.0):
+                 renorm=None, gate_scale=1.0, fp4_format="nv"):
         super().__init__()
         if group_rule not in ("max", "top2"):
             raise ValueError("group_rule is max or top2")
@@ -657,15 +755,20 @@ class MoELayer(torch.nn.Module):
             raise ValueError(f"{E} experts in {n_group} groups, {topk_group} of them kept, cannot "
                              f"give {k} experts")
         if mode not in ("sigmoid", "softmax") or bias_rule not in ("sign", "proportional") \
-                or precision not in ("bf16", "fp8", "fp8_dgrad"):
+                or precision not in ("bf16", "fp8", "fp8_dgrad", "fp4", "fp4_dgrad"):
             raise ValueError("mode is sigmoid or softmax, bias_rule sign or proportional, "
-                             "precision bf16, fp8 or fp8_dgrad")
+                             "precision bf16, fp8, fp8_dgrad, fp4 or fp4_dgrad")
+        if fp4_format not in FP4_FORMATS:
+            raise ValueError("fp4_format is nv or mx")
         self.d, self.E, self.k, self.f, self.f_shared = d, E, k, f, f_shared
         self.mode = ops.MODE_SIGMOID if mode == "sigmoid" else ops.MODE_SOFTMAX
         self.z_coef, self.gamma, self.bias_rule = z_coef, gamma, bias_rule
         self.aux_switch, self.aux_seq, self.seq_len = aux_switch, aux_seq, seq_len
         self.fp8 = precision in ("fp8", "fp8_dgrad")
         self.fp8_dgrad = precision == "fp8_dgrad"
+        self.fp4 = precision in ("fp4", "fp4_dgrad")
+        self.fp4_dgrad = precision == "fp4_dgrad"
+        self.fp4_format = FP4_FORMATS[fp4_format]
         self.n_group, self.topk_group = n_group, topk_group
         self.group_rule = ops.GROUP_MAX if group_rule == "max" else ops.GROUP_TOP2
         self.renorm, self.gate_scale = renorm, gate_scale
@@ -684,23 +787,41 @@ class MoELayer(torch.nn.Module):
             self.Ws_g = self.Ws_u = self.Ws_d = None
         self._plans = {}
         self._last_plan = None
+        self._held = None  # 4-bit operands of the weights, while they are held
+
+    @torch.no_grad()
+    def hold_weights(self, hold=True):
+        """Quantises the weights to 4 bits now and lets forwards use them until ``hold_weights(False)``."""
+        if not self.fp4:
+            raise ValueError("weights are held by a layer of precision fp4 or fp4_dgrad")
+        self._held = (weights4(self.fp4_format, self.W_g, self.W_u, self.W_d, self.Ws_g, self.Ws_u,
+                               self.Ws_d) if hold else None)
 
     def _plan(self, T):
-        if T not in self._plans:
+        """The plan of a token count; one without a backward while the weights are held."""
+        serving = self._held is not None
+        key = (T, "held") if serving else T
+        if key not in self._plans:
             shape = MoEShape(T, self.d, self.E, self.k, self.f, self.f_shared, self.mode,
                              self.z_coef, self.aux_switch, self.aux_seq, self.seq_len or T,
                              self.fp8, self.fp8_dgrad, self.n_group, self.topk_group,
-                             self.group_rule, self.renorm, self.gate_scale)
-            plan = MoEPlan(shape, self.W_g.device)
+                             self.group_rule, self.renorm, self.gate_scale, self.fp4, self.fp4_dgrad,
+                             self.fp4_format)
+            plan = MoEPlan(shape, self.W_g.device, backward=not serving)
             plan.generation = 0
-            self._plans[T] = plan
-        return self._plans[T]
+            self._plans[key] = plan
+        return self._plans[key]
 
     def forward(self, x, residual=None):
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
             raise ValueError(f"x must be [T, {self.d}] bf16, got {tuple(x.shape)} {x.dtype}")
         if residual is not None and self.norm is None:
             raise ValueError("a residual is taken by a layer with a norm (norm_eps)")
+        if self._held is not None and torch.is_grad_enabled() and (
+                x.requires_grad or (residual is not None and residual.requires_grad)
+                or any(p.requires_grad for p in self.parameters())):
+            raise ValueError("the layer's weights are held for serving: run it under torch.no_grad(), or "
+                             "call hold_weights(False) to train")
         plan = self._plan(x.shape[0])
         self._last_plan = plan
         z, codes = None, False
@@ -713,7 +834,7 @@ class MoELayer(torch.nn.Module):
             x = y
             codes = self.fp8 and _has_codes(self.norm, x, plan.x8, plan.sx)
         out = _MoEFunction.apply(x, self.W_r, self.b, self.W_g, self.W_u, self.W_d, self.Ws_g,
-                                 self.Ws_u, self.Ws_d, plan, codes)
+                                 self.Ws_u, self.Ws_d, plan, codes, self._held)
         return out if z is None else (out, z)
 
     def clip_grads_(self, max_norm):

@@ -257,3 +257,116 @@ def test_product_matches_the_exact_one(counts, K, N, fmt):
             assert (Y[hi:int(ro[e + 1])] == 0).all()
     if ro is not None:
         assert (Y[int(ro[-1]):] == -3.0).all()
+
+
+def _expert_inputs(counts, d, f, seed):
+    g = torch.Generator().manual_seed(seed)
+    ro, rows, segs = layout(counts)
+    E = len(segs)
+    t = {n: torch.zeros(rows, c, dtype=torch.bfloat16) for n, c in
+         (("X", d), ("dY", d), ("A", f), ("U", f), ("H", f))}
+    for lo, hi in segs:
+        for n, std in (("X", 1.0), ("dY", 0.3), ("A", 1.0), ("U", 1.0), ("H", 0.5)):
+            t[n][lo:hi] = randn_bf16((hi - lo, t[n].shape[1]), g, std)
+    W = dict(W_g=randn_bf16((E, f, d), g, d ** -0.5), W_u=randn_bf16((E, f, d), g, d ** -0.5),
+             W_d=randn_bf16((E, d, f), g, f ** -0.5))
+    return t, W, ro, rows, segs
+
+
+EXPERTS = [(1, 256, 128), (600, 512, 256), ([300, 0, 129, 1, 513], 512, 256), ([130, 5, 0], 384, 128),
+           ([1, 0, 1], 256, 384)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("keep,gates", [(True, False), (False, False), (True, True)])
+@pytest.mark.parametrize("counts,d,f", EXPERTS)
+def test_expert_forward_matches_the_definition(counts, d, f, keep, gates, fmt):
+    """a and u as exact products of the operands; h against silu(a) u of the exact a and u; the operand
+    of H as the oracle's of the stored H; y as the exact product of that operand."""
+    t, W, ro, rows, segs = _expert_inputs(counts, d, f, d + f)
+    nv = fmt == ops.FP4_NV
+    ro_d = None if ro is None else dev(torch.from_numpy(ro))
+    n = rows if ro is None else int(ro[-1])
+    X = made(t["X"], fmt, None if ro is None else ro_d[len(segs):])
+    new = lambda c: torch.full((rows, c), -3.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    A, U = (new(f), new(f)) if keep else (None, None)
+    H, Y, Hc = new(f), new(d), operand((rows, f), fmt)
+    rg = None
+    if gates:
+        rg = torch.rand(rows, generator=torch.Generator().manual_seed(1)) + 0.5
+    ops.moe_expert_fwd_fp4(X, ro_d, made(W["W_g"], fmt), made(W["W_u"], fmt), made(W["W_d"], fmt), A, U, H,
+                           Hc, Y, row_gate=None if rg is None else dev(rg))
+    torch.cuda.synchronize()
+    assert ops.moe_device_status() == (0, 0)
+    check_operand(Hc, h64(H), n)
+    for e, (lo, hi) in enumerate(segs):
+        if hi == lo:
+            continue
+        x = O.fp4_dequant_rows(h64(t["X"][lo:hi]), nv)
+        wg, wu, wd = (O.fp4_dequant_rows(h64(W[k][e]), nv) for k in ("W_g", "W_u", "W_d"))
+        if keep:
+            assert_gemm_exact(A[lo:hi], x, wg.T, f"A e{e}")
+            assert_gemm_exact(U[lo:hi], x, wu.T, f"U e{e}")
+        a, u = x @ wg.T, x @ wu.T
+        h = a / (1 + np.exp(-a)) * u * (1.0 if rg is None else h64(rg)[lo:hi, None])
+        assert_close(H[lo:hi], h, f"H e{e}", atol=1e-5, rtol=2.0 ** -8 + 1e-5)
+        assert_gemm_exact(Y[lo:hi], O.fp4_dequant_rows(h64(H[lo:hi]), nv), wd.T, f"Y e{e}")
+    for o in (A, U, H, Y):
+        assert o is None or (o[n:] == -3.0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,d,f", EXPERTS)
+@pytest.mark.parametrize("router", [False, True])
+def test_expert_backward_matches_the_definition(counts, d, f, router, fmt):
+    """da and du against the SwiGLU backward of the exact product; the operand of [dA | dU] as the
+    oracle's of the stored ones; dX as the exact product of that operand (plus the router's term);
+    the weight gradients as exact products of the bf16 tensors."""
+    if router and isinstance(counts, int):
+        pytest.skip("the router term needs the routed layout")
+    t, W, ro, rows, segs = _expert_inputs(counts, d, f, d + f + 1)
+    nv, E = fmt == ops.FP4_NV, len(segs)
+    ro_d = None if ro is None else dev(torch.from_numpy(ro))
+    n = rows if ro is None else int(ro[-1])
+    Wd, Wgu = ops.fp4_empty((E, f, d), fmt), ops.fp4_empty((E, d, 2 * f), fmt)
+    ops.moe_quantize_cols_fp4(dev(W["W_d"]), None, Wd)
+    ops.moe_quantize_cols_fp4(dev(W["W_g"]), dev(W["W_u"]), Wgu)
+    new = lambda *c: torch.full(c, -3.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    dA, dU, dX = new(rows, f), new(rows, f), new(rows, d)
+    dWg, dWu, dWd = new(E, f, d), new(E, f, d), new(E, d, f)
+    AUc = operand((rows, 2 * f), fmt)
+    dl = torch.randn(rows, generator=torch.Generator().manual_seed(2))
+    W_r = torch.randn(E, d, generator=torch.Generator().manual_seed(3))
+    ws = torch.empty(ops.moe_workspace_bytes(rows, d, E, 1), dtype=torch.uint8, device="cuda")
+    dYc = made(t["dY"], fmt, None if ro is None else ro_d[E:])
+    args = (dYc, dev(t["dY"]), dev(t["X"]), dev(t["A"]), dev(t["U"]), dev(t["H"]), ro_d, Wd, Wgu, dX, dA, dU,
+            AUc, dWg, dWu, dWd, ws)
+    kw = dict(dl_rows=dev(dl), W_r=dev(W_r)) if router else {}
+    if router:  # in two calls, as the layer needs the gates' gradient between them
+        ops.moe_expert_bwd_fp4(*args, parts=ops.BWD_DH)
+        ops.moe_expert_bwd_fp4(*args, parts=ops.BWD_DX | ops.BWD_W, **kw)
+    else:
+        ops.moe_expert_bwd_fp4(*args)
+    torch.cuda.synchronize()
+    assert ops.moe_device_status() == (0, 0)
+    check_operand(AUc, np.concatenate([h64(dA), h64(dU)], 1), n)
+    for e, (lo, hi) in enumerate(segs):
+        if hi == lo:
+            assert not any(w[e].any() for w in (dWg, dWu, dWd))
+            continue
+        x, dy, a, u, h = (h64(t[k][lo:hi]) for k in ("X", "dY", "A", "U", "H"))
+        wg, wu, wd = (h64(W[k][e]) for k in ("W_g", "W_u", "W_d"))
+        r = O.fp4_dequant_rows(dy, nv) @ O.fp4_dequant_cols(wd, nv)
+        da, du = O.swiglu_backward(r, a, u)
+        assert_close(dA[lo:hi], da, f"dA e{e}", atol=1e-5, rtol=2.0 ** -8 + 1e-5)
+        assert_close(dU[lo:hi], du, f"dU e{e}", atol=1e-5, rtol=2.0 ** -8 + 1e-5)
+        AU = O.fp4_dequant_rows(np.concatenate([h64(dA[lo:hi]), h64(dU[lo:hi])], 1), nv)
+        Wb = O.fp4_dequant_cols(np.concatenate([wg, wu]), nv)
+        if router:  # one more exact column: the slot's logit gradient times the router row
+            AU, Wb = np.concatenate([AU, h64(dl)[lo:hi, None]], 1), np.concatenate([Wb, h64(W_r)[e][None]])
+        assert_gemm_exact(dX[lo:hi], AU, Wb, f"dX e{e}")
+        assert_gemm_exact(dWd[e], dy.T, h, f"dW_d e{e}")
+        assert_gemm_exact(dWg[e], h64(dA[lo:hi]).T, x, f"dW_g e{e}")
+        assert_gemm_exact(dWu[e], h64(dU[lo:hi]).T, x, f"dW_u e{e}")
+    for o in (dA, dU, dX):
+        assert (o[n:] == -3.0).all()
