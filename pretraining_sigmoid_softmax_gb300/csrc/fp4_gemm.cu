@@ -55,7 +55,7 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
     CUtensorMap mx, mw, sf[3], mo[3];
     if (!code_map(&mx, X.q, K, rows) || !code_map(&mw, W.q, K, (uint64_t)E * N) ||
         !scale_map<NV>(&sf[0], X.s, K, rows) || !scale_map<NV>(&sf[1], W.s, K, (int64_t)E * N) ||
-        !out_maps(mo, Y, nullptr, nullptr, N, rows))
+        !out_maps(mo, Y, nullptr, nullptr, N, rows, G::StoreP::OCOLS))
         return MOE_ERR_LAUNCH;
     sf[2] = sf[1];
     Params P = base_params(row_offsets, rows, E);
@@ -80,7 +80,7 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
     if (!code_map(&mx, X.q, d, rows) || !code_map(&mg, Wg.q, d, (uint64_t)E * f) ||
         !code_map(&mu, Wu.q, d, (uint64_t)E * f) || !scale_map<NV>(&sf[0], X.s, d, rows) ||
         !scale_map<NV>(&sf[1], Wg.s, d, (int64_t)E * f) || !scale_map<NV>(&sf[2], Wu.s, d, (int64_t)E * f) ||
-        !out_maps(mo, A ? A : H, U ? U : H, H, f, rows))
+        !out_maps(mo, A ? A : H, U ? U : H, H, f, rows, G::G1P::OCOLS))
         return MOE_ERR_LAUNCH;
     Params P = base_params(row_offsets, rows, E);
     P.N = f;
@@ -102,11 +102,11 @@ int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const in
     CUtensorMap my, mw, ma, mu, sf[3], mo[3];
     if (!code_map(&my, dY.q, d, rows) || !code_map(&mw, Wd.q, d, (uint64_t)E * f) ||
         !scale_map<NV>(&sf[0], dY.s, d, rows) || !scale_map<NV>(&sf[1], Wd.s, d, (int64_t)E * f) ||
-        !make_map(&ma, A, f, rows, kAuCols, 32, false, CU_TENSOR_MAP_SWIZZLE_32B) ||
-        !make_map(&mu, U, f, rows, kAuCols, 32, false, CU_TENSOR_MAP_SWIZZLE_32B) ||
-        !out_maps(mo, dA, dU, nullptr, f, rows))
+        !make_map(&ma, A, f, rows, G::BwdP::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&mu, U, f, rows, G::BwdP::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !out_maps(mo, dA, dU, nullptr, f, rows, G::BwdP::OCOLS))
         return MOE_ERR_LAUNCH;
-    static_assert(kAuCols == 16, "32-byte rows of the staged a and u");
+    static_assert(G::BwdP::AUC == 32, "64-byte rows of the staged a and u");
     sf[2] = sf[1];
     Params P = base_params(row_offsets, rows, E);
     P.N = f;

@@ -115,17 +115,22 @@ struct Cfg {
     static constexpr int SF_BYTES = SFA_BYTES * (1 + SFB_TILES);
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;  // this CTA's bytes per K block
     static constexpr bool AU = EPI == kEpiSwigluBwd;
-    static constexpr int AU_BUF_BYTES = 2 * 32 * kAuCols * 2;  // a and u: 32 rows x kAuCols
+    // staged a and u, and the outputs made of them: 32 columns a chunk for E2M1, whose main loops are
+    // so short that the number of TMA rows sets the pace, else 16
+    static constexpr int AUC = FP4 ? 32 : kAuCols;
+    static constexpr int AU_BUF_BYTES = 2 * 32 * AUC * 2;  // a and u: 32 rows x AUC
     static constexpr int AU_BYTES = AU ? EW * kAuBufs * AU_BUF_BYTES : 0;
     static constexpr bool TS = !WGRAD;  // token-major outputs leave by TMA stores
     static constexpr int NOUT = EPI == kEpiSwigluFwd ? 3 : EPI == kEpiSwigluBwd ? 2 : 1;
     // output columns per staged chunk: 16, or 32 (single-output epilogues of short-K GEMMs,
     // where the per-chunk fence and store issue dominate) at the same shared-memory size
-    static constexpr int OCOLS = OC_;
-    static_assert(OCOLS == 16 || (OCOLS == 32 && NOUT == 1 && !AU), "output chunk width");
+    // (E2M1: 64 columns a box, whole 128-byte lines, in two buffers a warp; see epilogue_fp4)
+    static constexpr int OCOLS = FP4 ? (AU ? AUC : 64) : OC_;
+    static_assert(FP4 || OCOLS == 16 || (OCOLS == 32 && NOUT == 1 && !AU), "output chunk width");
     static constexpr int OUT_BOX_BYTES = 32 * OCOLS * 2;             // one output, one chunk
-    static constexpr int OUT_BUF_BYTES = NOUT * OUT_BOX_BYTES;       // one chunk, every output
-    static constexpr int OUT_DEPTH = (AU || OCOLS == 32 || EW == 16) ? 1 : 2;  // chunks per warp
+    static constexpr int OUT_BUF_BYTES = (FP4 && !AU ? 1 : NOUT) * OUT_BOX_BYTES;  // one buffer
+    static constexpr int OUT_DEPTH =
+        FP4 && !AU ? 2 : (AU || OCOLS == 32 || EW == 16) ? 1 : 2;    // buffers per warp
     static constexpr int OUT_BYTES = TS ? EW * OUT_DEPTH * OUT_BUF_BYTES : 0;
     static constexpr int BUDGET = (AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
     static constexpr int STAGES = (BUDGET / STAGE_BYTES) > 6 ? 6 : (BUDGET / STAGE_BYTES);
@@ -155,7 +160,8 @@ struct Cfg {
     static constexpr size_t SMEM_BYTES =
         1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + MISC_BYTES;
     static_assert((2 * STAGES + 5 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
-    static_assert(OV == 0 || (OCOLS == kOutCols && OV <= BN / (EW / 4)), "shared columns of one warp");
+    static_assert(OV <= BN / (EW / 4), "the shared columns are one warp's (in each lane quadrant)");
+    static_assert(!FP4 || EW == 8, "two epilogue warps per lane quadrant");
     static_assert(STAGES * SF_BYTES % 1024 == 0, "alignment of what follows the stages");
 
 };
@@ -497,6 +503,23 @@ __device__ __forceinline__ void fp8_scale(float* a, float* b, const Params& P, i
     }
 }
 
+// The slot's router term in a chunk of a data-gradient row, one fp32 FMA per element.
+template <int W>
+__device__ __forceinline__ void add_router_term(float* v, const Params& P, int64_t row,
+                                                const TileInfo& ti, int c) {
+    const float g = __ldg(P.r1_row + row);
+    const float4* w =
+        reinterpret_cast<const float4*>(P.r1_col + (int64_t)ti.e * P.N + ti.n0 + c);
+#pragma unroll
+    for (int j = 0; j < W / 4; ++j) {
+        const float4 w4 = __ldg(w + j);
+        v[4 * j] = fmaf(g, w4.x, v[4 * j]);
+        v[4 * j + 1] = fmaf(g, w4.y, v[4 * j + 1]);
+        v[4 * j + 2] = fmaf(g, w4.z, v[4 * j + 2]);
+        v[4 * j + 3] = fmaf(g, w4.w, v[4 * j + 3]);
+    }
+}
+
 // Weight-gradient epilogue: columns [c_lo, c_hi) of this thread's output row (a weight row;
 // always inside the output, as M_out and N are whole tiles). An expert with no rows gives
 // zeros.
@@ -551,8 +574,7 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
                                                    uint32_t t_acc, int q, int lane, int slot,
                                                    int c_lo, int ncols, const Params& P,
                                                    const CUtensorMap* mo0, const CUtensorMap* mo1,
-                                                   const CUtensorMap* mo2, uint32_t& n,
-                                                   Shared& sh) {
+                                                   const CUtensorMap* mo2, uint32_t& n) {
     constexpr int W = C::OCOLS;
     if (ti.m0 >= ti.row_end) return;  // warp-uniform: the whole half is past the segment
     const int64_t row0 = ti.m0 + 32 * q;
@@ -560,20 +582,19 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
     // row scale is read from the last row instead
     const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
     for (int i = 0; i < ncols / W; ++i, ++n) {
-        const int c = c_lo + (C::OV && sh.reversed ? ncols / W - 1 - i : i) * W;
+        const int c = c_lo + i * W;
         float v[C::NOUT][W];
         if constexpr (C::EPI == kEpiSwigluFwd) {
             uint32_t g[W], u[W];
             tmem_ld_cols<W>(t_acc + c, g);
             tmem_ld_cols<W>(t_acc + C::BN + c, u);
             tmem_ld_wait();
-            if (C::OV && i == C::OV / W - 1) report_shared<C>(sh, lane);
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 v[0][j] = __uint_as_float(g[j]);
                 v[1][j] = __uint_as_float(u[j]);
             }
-            if constexpr (C::SCALED) fp8_scale<W>(v[0], v[1], P, row, ti, c);
+            if constexpr (C::FP8) fp8_scale<W>(v[0], v[1], P, row, ti, c);
             const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
 #pragma unroll
             for (int j = 0; j < W; ++j)
@@ -582,35 +603,19 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
             uint32_t r[W];
             tmem_ld_cols<W>(t_acc + c, r);
             tmem_ld_wait();
-            if (C::OV && i == C::OV / W - 1) report_shared<C>(sh, lane);
 #pragma unroll
             for (int j = 0; j < W; ++j) v[0][j] = __uint_as_float(r[j]);
-            if constexpr (C::SCALED) fp8_scale<W>(v[0], v[0], P, row, ti, c, /*dual=*/false);
-            if constexpr (C::EPI == kEpiStore && !C::WGRAD) {
-                if (P.r1_row) {  // the slot's router term, one fp32 FMA per element
-                    const float g = __ldg(P.r1_row + row);
-                    const float4* w = reinterpret_cast<const float4*>(
-                        P.r1_col + (int64_t)ti.e * P.N + ti.n0 + c);
-#pragma unroll
-                    for (int j = 0; j < W / 4; ++j) {
-                        const float4 w4 = __ldg(w + j);
-                        v[0][4 * j] = fmaf(g, w4.x, v[0][4 * j]);
-                        v[0][4 * j + 1] = fmaf(g, w4.y, v[0][4 * j + 1]);
-                        v[0][4 * j + 2] = fmaf(g, w4.z, v[0][4 * j + 2]);
-                        v[0][4 * j + 3] = fmaf(g, w4.w, v[0][4 * j + 3]);
-                    }
-                }
-            }
+            if constexpr (C::FP8) fp8_scale<W>(v[0], v[0], P, row, ti, c, /*dual=*/false);
+            if constexpr (C::EPI == kEpiStore && !C::WGRAD)
+                if (P.r1_row) add_router_term<W>(v[0], P, row, ti, c);
         }
         uint8_t* buf = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
         if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
         __syncwarp();
-        const int o_lo = C::FP4 && C::EPI == kEpiSwigluFwd && P.only_h ? 2 : 0;
 #pragma unroll
         for (int o = 0; o < C::NOUT; ++o)
 #pragma unroll
             for (int j = 0; j < W / 8; ++j)
-                if (o >= o_lo)
                 *reinterpret_cast<uint4*>(buf + o * C::OUT_BOX_BYTES +
                                           (W == 32 ? sw64_offset(lane, j) : sw32_offset(lane, j))) =
                     pack_chunk8(v[o] + 8 * j);
@@ -620,24 +625,119 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
             const CUtensorMap* mo[3] = {mo0, mo1, mo2};
 #pragma unroll
             for (int o = 0; o < C::NOUT; ++o)
-                if (o >= o_lo) tma_store_2d(mo[o], smem_u32(buf + o * C::OUT_BOX_BYTES), ti.n0 + c, (int32_t)row0);
+                tma_store_2d(mo[o], smem_u32(buf + o * C::OUT_BOX_BYTES), ti.n0 + c, (int32_t)row0);
             bulk_commit();
+        }
+    }
+}
+
+// ------------------------------------------------- outputs of the E2M1 GEMMs
+// A tile's main loop is a quarter of the bf16 one's, so the number of rows that the TMA stores
+// move sets the pace (16-column boxes: 5 to 8 cycles for each 32-byte row of a box, which made the
+// large down projection 2.29 ms): boxes are 64 columns x 32 rows, whole 128-byte lines, two 4 KB
+// buffers a warp. A warp takes 64 columns out of tensor memory before anything else, so that
+// shared columns are free a few hundred cycles after the tile's last instruction.
+
+// Byte offset of 16-byte piece j of row r in a 128-byte-swizzled box of 128-byte rows.
+__device__ __forceinline__ int sw128_offset(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+
+// 64 packed columns of this thread's row into the warp's next buffer, and out by TMA.
+template <class C>
+__device__ __forceinline__ void store_chunk64(const SmemLayout& S, int slot, int lane,
+                                              const uint32_t (&w)[32], const CUtensorMap* mo, int col,
+                                              int64_t row0, uint32_t& n) {
+    uint8_t* buf = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
+    ++n;
+    if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(buf + sw128_offset(lane, j)) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(mo, smem_u32(buf), col, (int32_t)row0);
+        bulk_commit();
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo& ti, uint32_t t_acc,
+                                             int q, int lane, int slot, int c_lo, const Params& P,
+                                             const CUtensorMap* mo0, const CUtensorMap* mo1,
+                                             const CUtensorMap* mo2, uint32_t& n, Shared& sh) {
+    constexpr int kChunks = C::BN / (C::EW / 4) / 64;
+    static_assert(kChunks >= 1, "64 columns a warp");
+    if (ti.m0 >= ti.row_end) return;  // warp-uniform: the whole half is past the segment
+    const int64_t row0 = ti.m0 + 32 * q;
+    // rows past row_end (the tail of an unpadded layout) are clipped by the store
+    const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
+#pragma unroll 1
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = c_lo + (C::OV && sh.reversed ? kChunks - 1 - i : i) * 64;
+        if constexpr (C::EPI == kEpiSwigluFwd) {
+            static_assert(kChunks == 1, "gate and up columns of a warp in one chunk");
+            uint32_t g[2][32], u[2][32], h[32];
+            tmem_ld32(t_acc + c, g[0]);
+            tmem_ld32(t_acc + c + 32, g[1]);
+            tmem_ld32(t_acc + C::BN + c, u[0]);
+            tmem_ld32(t_acc + C::BN + c + 32, u[1]);
+            tmem_ld_wait();
+            report_shared<C>(sh, lane);
+            const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
+            uint32_t a[32], b[32];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float* gf = reinterpret_cast<float*>(g[k]);
+                float* uf = reinterpret_cast<float*>(u[k]);
+                if constexpr (C::NV) fp8_scale<32>(gf, uf, P, row, ti, c + 32 * k);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float g0 = gf[2 * j], g1 = gf[2 * j + 1];
+                    const float u0 = uf[2 * j], u1 = uf[2 * j + 1];
+                    a[16 * k + j] = pack_bf16x2(g0, g1);
+                    b[16 * k + j] = pack_bf16x2(u0, u1);
+                    h[16 * k + j] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * u0 * rg,
+                                                __fdividef(g1, 1.0f + __expf(-g1)) * u1 * rg);
+                }
+            }
+            if (!P.only_h) {
+                store_chunk64<C>(S, slot, lane, a, mo0, ti.n0 + c, row0, n);
+                store_chunk64<C>(S, slot, lane, b, mo1, ti.n0 + c, row0, n);
+            }
+            store_chunk64<C>(S, slot, lane, h, mo2, ti.n0 + c, row0, n);
+        } else {
+            uint32_t r[2][32], w[32];
+            tmem_ld32(t_acc + c, r[0]);
+            tmem_ld32(t_acc + c + 32, r[1]);
+            tmem_ld_wait();
+            report_shared<C>(sh, lane);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float* v = reinterpret_cast<float*>(r[k]);
+                if constexpr (C::NV) fp8_scale<32>(v, v, P, row, ti, c + 32 * k, /*dual=*/false);
+                if (P.r1_row) add_router_term<32>(v, P, row, ti, c + 32 * k);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[16 * k + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            }
+            store_chunk64<C>(S, slot, lane, w, mo0, ti.n0 + c, row0, n);
         }
     }
 }
 
 // ------------------------------------------------- SwiGLU backward with staged a and u
 // Each epilogue warp owns 32 rows x (BN / 2) columns of the tile and walks them in chunks of
-// kAuCols. The chunk's saved a and u arrive by TMA (boxes of kAuCols x 32 rows, swizzled
+// AUC. The chunk's saved a and u arrive by TMA (boxes of AUC x 32 rows, swizzled
 // so that the row-per-lane reads below hit distinct banks) into one of the warp's kAuBufs
 // buffers; lane 0 issues the copy of chunk n + kAuBufs once the warp is done with chunk n,
 // and a tile's first chunks before its accumulator is ready.
 
 // Byte offset of 16-byte piece j of row r in a staged (a or u) chunk.
+template <int COLS>
 __device__ __forceinline__ int au_offset(int r, int j) {
-    if constexpr (kAuCols == 32) return r * 64 + ((j ^ ((r >> 1) & 3)) << 4);  // 64-byte swizzle
-    else if constexpr (kAuCols == 16) return r * 32 + ((j ^ ((r >> 2) & 1)) << 4);  // 32-byte
-    else return r * 16;                                                            // unswizzled
+    if constexpr (COLS == 32) return sw64_offset(r, j);
+    else return sw32_offset(r, j);
 }
 
 template <class C>
@@ -672,8 +772,10 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
                                                   const CUtensorMap* mda, const CUtensorMap* mdu,
                                                   uint32_t& n, volatile int* abort_flag,
                                                   Shared& sh) {
-    static_assert(kAuCols == kOutCols, "one staged output chunk per a/u chunk");
-    const int nch = ncols / kAuCols;
+    constexpr int W = C::AUC;
+    constexpr int kBox = C::OUT_BOX_BYTES;
+    static_assert(W == C::OCOLS, "one staged output chunk per a/u chunk");
+    const int nch = ncols / W;
     const int64_t row0 = ti.m0 + 32 * q;
     const int64_t row = row0 + lane;
     const bool ok_row = row < ti.row_end;
@@ -685,30 +787,30 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
     const float g = (P.row_scale && ok_row) ? __ldg(P.row_scale + row) : 1.0f;
     float gpart = 0.f;
     for (int i = 0; i < nch; ++i, ++n) {
-        const int c = c_lo + au_chunk<C>(i, nch, sh) * kAuCols;
+        const int c = c_lo + au_chunk<C>(i, nch, sh) * W;
         const int b = (int)(n % kAuBufs);
-        uint32_t acc[kAuCols];
-        tmem_ld_cols<kAuCols>(t_acc + c, acc);
+        uint32_t acc[W];
+        tmem_ld_cols<W>(t_acc + c, acc);
         bool ok = mbar_wait_bounded(smem_u32(&S.au_full[slot * kAuBufs + b]), (n / kAuBufs) & 1u,
                                     abort_flag, P.status, P.wait_limit_ns, 34);
         tmem_ld_wait();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
-        if (C::OV && i == C::OV / kAuCols - 1) report_shared<C>(sh, lane);
-        float dav[kAuCols], duv[kAuCols];
+        if (C::OV && i == (C::OV + W - 1) / W - 1) report_shared<C>(sh, lane);
+        float dav[W], duv[W];
         if (store) {  // lanes past an unpadded layout's end see zero-filled a, u and acc
             const uint8_t* abuf = S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES;
             const uint8_t* ubuf = abuf + C::AU_BUF_BYTES / 2;
-            float accf[kAuCols];
+            float accf[W];
 #pragma unroll
-            for (int j = 0; j < kAuCols; ++j) accf[j] = __uint_as_float(acc[j]);
+            for (int j = 0; j < W; ++j) accf[j] = __uint_as_float(acc[j]);
             // FP8 operands: the dequantised r = (dy codes) (W_d codes) * scale(row) * scale(col)
             if constexpr (C::SCALED)
-                fp8_scale<kAuCols>(accf, accf, P, ok_row ? row : ti.row_end - 1, ti, c, false);
+                fp8_scale<W>(accf, accf, P, ok_row ? row : ti.row_end - 1, ti, c, false);
 #pragma unroll
-            for (int j = 0; j < kAuCols / 8; ++j) {
-                const uint4 a4 = *reinterpret_cast<const uint4*>(abuf + au_offset(lane, j));
-                const uint4 u4 = *reinterpret_cast<const uint4*>(ubuf + au_offset(lane, j));
+            for (int j = 0; j < W / 8; ++j) {
+                const uint4 a4 = *reinterpret_cast<const uint4*>(abuf + au_offset<W>(lane, j));
+                const uint4 u4 = *reinterpret_cast<const uint4*>(ubuf + au_offset<W>(lane, j));
                 const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w};
                 const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
@@ -724,7 +826,7 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
                 }
             }
             const int col = ti.n0 + c;
-            if (!C::OV && P.gate_part && (col + kAuCols) % 64 == 0) {  // last chunk of a 64-column group
+            if (!C::OV && P.gate_part && (col + W) % 64 == 0) {  // last chunk of a 64-column group
                 if (ok_row) P.gate_part[row * (int64_t)(P.ld_out / 64) + col / 64] = gpart;
                 gpart = 0.f;
             }
@@ -732,21 +834,21 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
         __syncwarp();  // every lane is done with a/u buffer b
         if (lane == 0 && i + kAuBufs < nch)
             au_issue<C>(S, ma, mu, slot, n + kAuBufs, row0,
-                        ti.n0 + c_lo + au_chunk<C>(i + kAuBufs, nch, sh) * kAuCols);
+                        ti.n0 + c_lo + au_chunk<C>(i + kAuBufs, nch, sh) * W);
         if (store) {
             uint8_t* ob = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
             if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < kAuCols / 8; ++j) {
-                *reinterpret_cast<uint4*>(ob + sw32_offset(lane, j)) = pack_chunk8(dav + 8 * j);
-                *reinterpret_cast<uint4*>(ob + 1024 + sw32_offset(lane, j)) = pack_chunk8(duv + 8 * j);
+            for (int j = 0; j < W / 8; ++j) {
+                *reinterpret_cast<uint4*>(ob + au_offset<W>(lane, j)) = pack_chunk8(dav + 8 * j);
+                *reinterpret_cast<uint4*>(ob + kBox + au_offset<W>(lane, j)) = pack_chunk8(duv + 8 * j);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
                 tma_store_2d(mda, smem_u32(ob), ti.n0 + c, (int32_t)row0);
-                tma_store_2d(mdu, smem_u32(ob + 1024), ti.n0 + c, (int32_t)row0);
+                tma_store_2d(mdu, smem_u32(ob + kBox), ti.n0 + c, (int32_t)row0);
                 bulk_commit();
             }
         }
@@ -957,9 +1059,9 @@ __device__ __forceinline__ void grouped_gemm_body(
                       C::OV && C::PAIR ? mapa_shared(smem_u32(S.tshared), 0) : smem_u32(S.tshared)};
             if constexpr (C::AU) {  // this tile's first a/u chunks while the MMA runs
                 if (lane == 0)
-                    for (int i = 0; i < kAuBufs && i < kCols / kAuCols; ++i)
+                    for (int i = 0; i < kAuBufs && i < kCols / C::AUC; ++i)
                         au_issue<C>(S, &ma1, &mb1, slot, n_au + i, ti.m0 + 32 * q,
-                                    ti.n0 + c_lo + au_chunk<C>(i, kCols / kAuCols, sh) * kAuCols);
+                                    ti.n0 + c_lo + au_chunk<C>(i, kCols / C::AUC, sh) * C::AUC);
             }
             bool ok = mbar_wait_bounded(smem_u32(&S.tfull[buf]), ph, abort_flag, P.status,
                                         P.wait_limit_ns, 33);
@@ -972,9 +1074,11 @@ __device__ __forceinline__ void grouped_gemm_body(
                 if (!swiglu_bwd_staged<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &ma1, &mb1,
                                           &mo0, &mo1, n_au, abort_flag, sh))
                     break;
+            } else if constexpr (C::FP4) {
+                epilogue_fp4<C>(S, ti, t_acc, q, lane, slot, c_lo, P, &mo0, &mo1, &mo2, n_au, sh);
             } else if constexpr (C::TS) {
                 epilogue_tma_store<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &mo0, &mo1, &mo2,
-                                      n_au, sh);
+                                      n_au);
             } else {
                 epilogue_wgrad<C>(ti, t_acc, row_in_tile, P, c_lo, c_lo + kCols);
             }
@@ -1065,12 +1169,14 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor maps for the TMA-store epilogue: boxes of `cols` (16 or 32) x 32 rows over [rows, ld]
-// bf16, swizzled as the epilogue lays them out (32- or 64-byte rows).
+// Tensor maps for the TMA-store epilogue: boxes of `cols` (16, 32 or 64) x 32 rows over [rows, ld]
+// bf16, swizzled as the epilogue lays them out (32-, 64- or 128-byte rows).
 bool out_maps(CUtensorMap (&mo)[3], const void* o0, const void* o1, const void* o2, uint64_t ld,
               uint64_t rows, int cols = kOutCols) {
     const void* o[3] = {o0, o1 ? o1 : o0, o2 ? o2 : o0};
-    const CUtensorMapSwizzle swz = cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+    const CUtensorMapSwizzle swz = cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                   : cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                : CU_TENSOR_MAP_SWIZZLE_32B;
     for (int i = 0; i < 3; ++i)
         if (!make_map(&mo[i], o[i], ld, rows, (uint32_t)cols, 32, false, swz)) return false;
     return true;
