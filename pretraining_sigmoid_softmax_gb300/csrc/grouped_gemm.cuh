@@ -33,10 +33,12 @@
 // loads complete on the leader's "full" barriers, the leader's commits arrive on both
 // CTAs' barriers (multicast), and both epilogues release the accumulator to the leader.
 // E2M1 operands (two codes a byte, 256 K elements per 128-byte row) bring the scales of their
-// blocks as 512-byte tiles of 128 rows x 4 blocks: TMA copies them beside the operands,
-// tcgen05.cp puts them into tensor memory in front of the instructions that read them, and
-// the tensor cores multiply them in (kind::mxf4 with a power of two per 32, kind::mxf4nvf4
-// with an E4M3 scale per 16). The scales leave less than two whole accumulators of 256
+// blocks as 512-byte tiles of 128 rows x 4 blocks: TMA copies them beside the operands, two
+// threads of their own (warps 2 and 3) put them into tensor memory with tcgen05.cp, a stage
+// ahead, and the tensor cores multiply them in (kind::mxf4 with a power of two per 32,
+// kind::mxf4nvf4 with an E4M3 scale per 16). Issued by the MMA thread itself the copies and
+// the products take turns: a stage of 256 K elements took 0.55 us (MX, 6 copies) and 0.74
+// (NV, 12), and takes 0.41 and 0.47 with the two copying threads. The scales leave less than two whole accumulators of 256
 // columns, so the two share a few columns (Cfg::OV).
 // Operand tiles use the 128-byte swizzle. K-major tiles are TMA boxes of 64 K-elements x
 // rows; MN-major tiles are boxes of 64 MN-elements x 64 k-rows. Every wait on an mbarrier
@@ -135,16 +137,19 @@ struct Cfg {
     static constexpr int BUDGET = (AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
     static constexpr int STAGES = (BUDGET / STAGE_BYTES) > 6 ? 6 : (BUDGET / STAGE_BYTES);
     static constexpr int ACC_COLS = MMA_N;
-    // E2M1: the scales of a stage take SFK * 4 * (1 + SFB_TILES) columns of tensor memory at
-    // its start. With 256-column accumulators the two buffers then share OV columns: the last
+    // E2M1: the scales of a stage take SFC columns of tensor memory, and two stages' lie at its
+    // start. With 256-column accumulators the two buffers then share OV columns: the last
     // of buffer 0 are the first of buffer 1. The epilogue takes the shared columns first and
     // reports them read, and a tile's first instruction waits for that report of the tile
     // before it (and for the whole of the one before that, as without sharing).
-    static constexpr int OV = FP4 && ACC_COLS == 256 ? (NV ? 48 : 32) : 0;
+    static constexpr int SFC = SFK * 4 * (1 + SFB_TILES);
+    static constexpr int OV = FP4 && ACC_COLS == 256 ? 2 * SFC : 0;
+    // groups of epilogue warps (of one column range, four lane quadrants) that hold shared columns
+    static constexpr int OV_GROUPS = OV <= BN / (EW / 4) ? 1 : 2;
     static constexpr int ACC0 = FP4 ? (OV ? OV : 128) : 0;
     static constexpr int ACC1 = FP4 ? 256 : ACC_COLS;
     static constexpr int TMEM_COLS = FP4 ? 512 : 2 * ACC_COLS;  // two accumulator buffers
-    static_assert(!FP4 || SFK * 4 * (1 + SFB_TILES) <= ACC0, "columns of the scales");
+    static_assert(!FP4 || 2 * SFC <= ACC0, "columns of the scales");
     // DUAL: the W_g and W_u boxes form one 2*BN-row B tile (on one CTA, back to back; in a
     // pair, W_g on the leader and W_u on the peer), so one instruction fills gate columns
     // [0, BN) and up columns [BN, 2BN).
@@ -159,9 +164,9 @@ struct Cfg {
                                          sizeof(int32_t) * (kMaxExperts + 1);
     static constexpr size_t SMEM_BYTES =
         1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + MISC_BYTES;
-    static_assert((2 * STAGES + 5 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
-    static_assert(OV <= BN / (EW / 4), "the shared columns are one warp's (in each lane quadrant)");
+    static_assert((2 * STAGES + 9 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
     static_assert(!FP4 || EW == 8, "two epilogue warps per lane quadrant");
+    static_assert(OV_GROUPS == 1 || DUAL, "which warps report shared columns");
     static_assert(STAGES * SF_BYTES % 1024 == 0, "alignment of what follows the stages");
 
 };
@@ -214,6 +219,8 @@ struct SmemLayout {
     uint64_t* empty;   // STAGES
     uint64_t* tfull;   // 2
     uint64_t* tempty;  // 2
+    uint64_t* sfready; // 2: a stage's scales are in tensor memory (E2M1)
+    uint64_t* sfempty; // 2: the instructions that read them are done
     uint64_t* tshared; // the accumulators' shared columns are read (E2M1)
     uint32_t* tmem_slot;
     int* abort_flag;
@@ -240,7 +247,9 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
     s.tfull = s.empty + C::STAGES;
     s.tempty = s.tfull + 2;
     s.tshared = s.tempty + 2;
-    s.au_full = s.tshared + 1;
+    s.sfready = s.tshared + 1;
+    s.sfempty = s.sfready + 2;
+    s.au_full = s.sfempty + 2;
     s.tmem_slot = reinterpret_cast<uint32_t*>(s.au_full + (C::AU ? C::EW * kAuBufs : 0));
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
     s.offs = reinterpret_cast<int64_t*>(misc + 512);
@@ -368,16 +377,15 @@ __device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint
                     (brow / BM + (C::DUAL ? 0 : h)) * ktiles + kt);
 }
 
-// Instructions of one E2M1 K block: its scales into tensor memory (column tmem_sf on; in issue
-// order in front of the instructions that read them), then a step per 64 K elements.
+// The scales of one E2M1 K block of `steps` steps of 64 into tensor memory (column tmem_sf on): tiles
+// `half` * SFK / 2 on, half of them; the other copying thread takes the rest.
 template <class C>
-__device__ __forceinline__ void issue_mma_fp4(uint32_t d_tmem, uint32_t tmem_sf, uint32_t a_s,
-                                              uint32_t b_s, uint32_t sf_s, int steps, bool first) {
-    constexpr int kPerTile = C::NV ? 1 : 2;  // steps that one scale tile covers
+__device__ __forceinline__ void issue_scales_fp4(uint32_t tmem_sf, uint32_t sf_s, int steps, int half) {
     const uint32_t sfb = tmem_sf + C::SFK * 4;
-    const int tiles = steps / kPerTile;
+    const int tiles = C::NV ? steps : steps / 2;
 #pragma unroll
-    for (int t = 0; t < C::SFK; ++t) {
+    for (int i = 0; i < C::SFK / 2; ++i) {
+        const int t = half * (C::SFK / 2) + i;
         if (t >= tiles) break;
         tmem_cp_scales<C::PAIR>(tmem_sf + 4 * t, sdesc_plain(sf_s + t * kSfTile));
 #pragma unroll
@@ -385,10 +393,17 @@ __device__ __forceinline__ void issue_mma_fp4(uint32_t d_tmem, uint32_t tmem_sf,
             tmem_cp_scales<C::PAIR>(sfb + 4 * (C::SFB_TILES * t + h),
                                     sdesc_plain(sf_s + (1 + h) * C::SFA_BYTES + t * kSfTile));
     }
+}
+
+// The products of one E2M1 K block: a step per 64 K elements.
+template <class C>
+__device__ __forceinline__ void issue_mma_fp4(uint32_t d_tmem, uint32_t tmem_sf, uint32_t a_s,
+                                              uint32_t b_s, int steps, bool first) {
+    const uint32_t sfb = tmem_sf + C::SFK * 4;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
         if (kk >= steps) break;
-        const int t = kk / kPerTile;
+        const int t = C::NV ? kk : kk / 2;
         const uint32_t id = C::NV ? 0u : 2u * (kk & 1);  // which half of the tile's four blocks
         umma_fp4<C::PAIR, C::NV>(d_tmem, sdesc_sw128(a_s + kk * 32, 16, 1024),
                                  sdesc_sw128(b_s + kk * 32, 16, 1024),
@@ -641,19 +656,24 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
 // Byte offset of 16-byte piece j of row r in a 128-byte-swizzled box of 128-byte rows.
 __device__ __forceinline__ int sw128_offset(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-// 64 packed columns of this thread's row into the warp's next buffer, and out by TMA.
+// A warp's boxes: open one (its buffer's last store has read it), put a half of 32 packed columns of
+// this thread's row into it, send it off.
 template <class C>
-__device__ __forceinline__ void store_chunk64(const SmemLayout& S, int slot, int lane,
-                                              const uint32_t (&w)[32], const CUtensorMap* mo, int col,
-                                              int64_t row0, uint32_t& n) {
+__device__ __forceinline__ uint8_t* open_box(const SmemLayout& S, int slot, int lane, uint32_t& n) {
     uint8_t* buf = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
     ++n;
-    if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
+    if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();
     __syncwarp();
+    return buf;
+}
+__device__ __forceinline__ void put_half(uint8_t* buf, int lane, int half, const uint32_t* w) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(buf + sw128_offset(lane, j)) =
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(buf + sw128_offset(lane, 4 * half + j)) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+__device__ __forceinline__ void send_box(const uint8_t* buf, int lane, const CUtensorMap* mo, int col,
+                                         int64_t row0) {
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -667,61 +687,75 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
                                              int q, int lane, int slot, int c_lo, const Params& P,
                                              const CUtensorMap* mo0, const CUtensorMap* mo1,
                                              const CUtensorMap* mo2, uint32_t& n, Shared& sh) {
-    constexpr int kChunks = C::BN / (C::EW / 4) / 64;
-    static_assert(kChunks >= 1, "64 columns a warp");
+    constexpr int kHalves = C::BN / (C::EW / 4) / 32;  // of this warp's columns (of gate and of up)
+    static_assert(kHalves % 2 == 0, "whole boxes");
     if (ti.m0 >= ti.row_end) return;  // warp-uniform: the whole half is past the segment
     const int64_t row0 = ti.m0 + 32 * q;
     // rows past row_end (the tail of an unpadded layout) are clipped by the store
     const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
-#pragma unroll 1
-    for (int i = 0; i < kChunks; ++i) {
-        const int c = c_lo + (C::OV && sh.reversed ? kChunks - 1 - i : i) * 64;
-        if constexpr (C::EPI == kEpiSwigluFwd) {
-            static_assert(kChunks == 1, "gate and up columns of a warp in one chunk");
-            uint32_t g[2][32], u[2][32], h[32];
-            tmem_ld32(t_acc + c, g[0]);
-            tmem_ld32(t_acc + c + 32, g[1]);
-            tmem_ld32(t_acc + C::BN + c, u[0]);
-            tmem_ld32(t_acc + C::BN + c + 32, u[1]);
-            tmem_ld_wait();
-            report_shared<C>(sh, lane);
-            const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
-            uint32_t a[32], b[32];
+    if constexpr (C::EPI == kEpiSwigluFwd) {
+        static_assert(kHalves == 2, "gate and up columns of a warp in one box each");
+        uint32_t g[2][32], u[2][32], h[32];
+        tmem_ld32(t_acc + c_lo, g[0]);
+        tmem_ld32(t_acc + c_lo + 32, g[1]);
+        tmem_ld32(t_acc + C::BN + c_lo, u[0]);
+        tmem_ld32(t_acc + C::BN + c_lo + 32, u[1]);
+        tmem_ld_wait();
+        report_shared<C>(sh, lane);
+        const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
+        uint32_t a[32], b[32];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float* gf = reinterpret_cast<float*>(g[k]);
-                float* uf = reinterpret_cast<float*>(u[k]);
-                if constexpr (C::NV) fp8_scale<32>(gf, uf, P, row, ti, c + 32 * k);
+        for (int k = 0; k < 2; ++k) {
+            float* gf = reinterpret_cast<float*>(g[k]);
+            float* uf = reinterpret_cast<float*>(u[k]);
+            if constexpr (C::NV) fp8_scale<32>(gf, uf, P, row, ti, c_lo + 32 * k);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float g0 = gf[2 * j], g1 = gf[2 * j + 1];
-                    const float u0 = uf[2 * j], u1 = uf[2 * j + 1];
-                    a[16 * k + j] = pack_bf16x2(g0, g1);
-                    b[16 * k + j] = pack_bf16x2(u0, u1);
-                    h[16 * k + j] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * u0 * rg,
-                                                __fdividef(g1, 1.0f + __expf(-g1)) * u1 * rg);
-                }
+            for (int j = 0; j < 16; ++j) {
+                const float g0 = gf[2 * j], g1 = gf[2 * j + 1];
+                const float u0 = uf[2 * j], u1 = uf[2 * j + 1];
+                a[16 * k + j] = pack_bf16x2(g0, g1);
+                b[16 * k + j] = pack_bf16x2(u0, u1);
+                h[16 * k + j] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * u0 * rg,
+                                            __fdividef(g1, 1.0f + __expf(-g1)) * u1 * rg);
             }
-            if (!P.only_h) {
-                store_chunk64<C>(S, slot, lane, a, mo0, ti.n0 + c, row0, n);
-                store_chunk64<C>(S, slot, lane, b, mo1, ti.n0 + c, row0, n);
-            }
-            store_chunk64<C>(S, slot, lane, h, mo2, ti.n0 + c, row0, n);
-        } else {
-            uint32_t r[2][32], w[32];
-            tmem_ld32(t_acc + c, r[0]);
-            tmem_ld32(t_acc + c + 32, r[1]);
-            tmem_ld_wait();
-            report_shared<C>(sh, lane);
+        }
+        const CUtensorMap* mo[3] = {mo0, mo1, mo2};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float* v = reinterpret_cast<float*>(r[k]);
-                if constexpr (C::NV) fp8_scale<32>(v, v, P, row, ti, c + 32 * k, /*dual=*/false);
-                if (P.r1_row) add_router_term<32>(v, P, row, ti, c + 32 * k);
+        for (int o = 0; o < 3; ++o) {
+            if (o < 2 && P.only_h) continue;
+            const uint32_t* w = o == 0 ? a : o == 1 ? b : h;
+            uint8_t* buf = open_box<C>(S, slot, lane, n);
+            put_half(buf, lane, 0, w);
+            put_half(buf, lane, 1, w + 16);
+            send_box(buf, lane, mo[o], ti.n0 + c_lo, row0);
+        }
+    } else {
+        // halves in order, or (buffer 0 of accumulators that share columns) the last first; those with
+        // shared columns are taken out of tensor memory at once
+        constexpr int kAhead = C::OV ? (C::OV + 31) / 32 : 2;
+        uint32_t r[kHalves][32];
+        auto half = [&](int i) { return C::OV && sh.reversed ? kHalves - 1 - i : i; };
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[16 * k + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        for (int i = 0; i < kAhead; ++i) tmem_ld32(t_acc + c_lo + 32 * half(i), r[i]);
+        tmem_ld_wait();
+        report_shared<C>(sh, lane);
+        uint8_t* buf = nullptr;
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+            const int c = c_lo + 32 * half(i);
+            if (i >= kAhead) {
+                tmem_ld32(t_acc + c, r[i]);
+                tmem_ld_wait();
             }
-            store_chunk64<C>(S, slot, lane, w, mo0, ti.n0 + c, row0, n);
+            float* v = reinterpret_cast<float*>(r[i]);
+            if constexpr (C::NV) fp8_scale<32>(v, v, P, row, ti, c, /*dual=*/false);
+            if (P.r1_row) add_router_term<32>(v, P, row, ti, c);
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            if (i % 2 == 0) buf = open_box<C>(S, slot, lane, n);
+            put_half(buf, lane, half(i) & 1, w);
+            if (i % 2 == 1) send_box(buf, lane, mo0, ti.n0 + (c & ~63), row0);
         }
     }
 }
@@ -880,7 +914,13 @@ __device__ __forceinline__ void grouped_gemm_body(
             mbar_init(smem_u32(&S.tfull[b]), 1);
             mbar_init(smem_u32(&S.tempty[b]), C::PAIR ? 2 * C::EW : C::EW);
         }
-        if constexpr (C::OV > 0) mbar_init(smem_u32(S.tshared), C::PAIR ? 8 : 4);
+        if constexpr (C::OV > 0)
+            mbar_init(smem_u32(S.tshared), 4 * C::OV_GROUPS * (C::PAIR ? 2 : 1));
+        if constexpr (C::FP4)
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&S.sfready[b]), 2);  // both copying threads
+                mbar_init(smem_u32(&S.sfempty[b]), 1);
+            }
         if constexpr (C::AU)
             for (int b = 0; b < C::EW * kAuBufs; ++b) mbar_init(smem_u32(&S.au_full[b]), 1);
         *S.abort_flag = 0;
@@ -987,6 +1027,7 @@ __device__ __forceinline__ void grouped_gemm_body(
         int stage = 0;
         uint32_t phase = 0;
         int local = 0;
+        uint32_t blocks = 0;  // K blocks so far (E2M1: buffer and phase of the scales)
         for (int64_t tile = first_tile; tile < ntiles; tile += tile_step, ++local) {
             const TileInfo ti = decode<C>(tile, P, S, rank);
             const int buf = local & 1;
@@ -1011,23 +1052,32 @@ __device__ __forceinline__ void grouped_gemm_body(
                 const uint32_t a_s = smem_u32(S.a + (size_t)stage * C::A_BYTES);
                 const uint32_t b_s = smem_u32(S.b + (size_t)stage * C::B_BYTES);
                 if constexpr (C::FP4) {
+                    const int sb = blocks & 1;
+                    if (!mbar_wait_bounded(smem_u32(&S.sfready[sb]), (blocks >> 1) & 1, abort_flag,
+                                           P.status, P.wait_limit_ns, 36)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                     const int left = (P.K0 - kb * C::KB) / 64;
-                    issue_mma_fp4<C>(d_tmem, tmem_base, a_s, b_s,
-                                     smem_u32(S.sf + (size_t)stage * C::SF_BYTES),
-                                     left < 4 ? left : 4, kb == 0);
+                    issue_mma_fp4<C>(d_tmem, tmem_base + sb * C::SFC, a_s, b_s, left < 4 ? left : 4,
+                                     kb == 0);
+                    if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.sfempty[sb]), 0x1);
+                    else umma_commit(smem_u32(&S.sfempty[sb]));
+                    ++blocks;
                 } else {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {  // 4 instructions of 32 bytes of K
-                    const uint64_t adesc = C::A_MN ? sdesc_sw128(a_s + kk * 2048, 8192, 1024)
-                                                   : sdesc_sw128(a_s + kk * 32, 16, 1024);
-                    const uint64_t bdesc = C::B_MN ? sdesc_sw128(b_s + kk * 2048, 8192, 1024)
-                                                   : sdesc_sw128(b_s + kk * 32, 16, 1024);
-                    const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
-                    if constexpr (C::PAIR && C::FP8) umma_fp8_pair(d_tmem, adesc, bdesc, C::IDESC, acc);
-                    else if constexpr (C::PAIR) umma_bf16_pair(d_tmem, adesc, bdesc, C::IDESC, acc);
-                    else if constexpr (C::FP8) umma_fp8(d_tmem, adesc, bdesc, C::IDESC, acc);
-                    else umma_bf16(d_tmem, adesc, bdesc, C::IDESC, acc);
-                }
+                    for (int kk = 0; kk < 4; ++kk) {  // 4 instructions of 32 bytes of K
+                        const uint64_t adesc = C::A_MN ? sdesc_sw128(a_s + kk * 2048, 8192, 1024)
+                                                       : sdesc_sw128(a_s + kk * 32, 16, 1024);
+                        const uint64_t bdesc = C::B_MN ? sdesc_sw128(b_s + kk * 2048, 8192, 1024)
+                                                       : sdesc_sw128(b_s + kk * 32, 16, 1024);
+                        const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
+                        if constexpr (C::PAIR && C::FP8) umma_fp8_pair(d_tmem, adesc, bdesc, C::IDESC, acc);
+                        else if constexpr (C::PAIR) umma_bf16_pair(d_tmem, adesc, bdesc, C::IDESC, acc);
+                        else if constexpr (C::FP8) umma_fp8(d_tmem, adesc, bdesc, C::IDESC, acc);
+                        else umma_bf16(d_tmem, adesc, bdesc, C::IDESC, acc);
+                    }
                 }
                 if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.empty[stage]), 0x3);
                 else umma_commit(smem_u32(&S.empty[stage]));
@@ -1039,6 +1089,35 @@ __device__ __forceinline__ void grouped_gemm_body(
             if (!ok) break;
             if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.tfull[buf]), 0x3);
             else umma_commit(smem_u32(&S.tfull[buf]));
+        }
+    } else if (C::FP4 && (warp == 2 || warp == 3) && lane == 0 && leader) {
+        // ------------------------------------------------------------ scales to tensor memory
+        if constexpr (C::FP4) {
+            int stage = 0;
+            uint32_t phase = 0, blocks = 0;
+            bool ok = true;
+            for (int64_t tile = first_tile; ok && tile < ntiles; tile += tile_step) {
+                const TileInfo ti = decode<C>(tile, P, S, rank);
+                for (int kb = 0; kb < ti.k_iters; ++kb, ++blocks) {
+                    const int sb = blocks & 1;
+                    ok = mbar_wait_bounded(smem_u32(&S.full[stage]), phase, abort_flag, P.status,
+                                           P.wait_limit_ns, 37) &&
+                         mbar_wait_bounded(smem_u32(&S.sfempty[sb]), ((blocks >> 1) & 1) ^ 1u,
+                                           abort_flag, P.status, P.wait_limit_ns, 38);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int left = (P.K0 - kb * C::KB) / 64;
+                    issue_scales_fp4<C>(tmem_base + sb * C::SFC,
+                                        smem_u32(S.sf + (size_t)stage * C::SF_BYTES),
+                                        left < 4 ? left : 4, warp - 2);
+                    if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.sfready[sb]), 0x1);
+                    else umma_commit(smem_u32(&S.sfready[sb]));
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
@@ -1055,7 +1134,8 @@ __device__ __forceinline__ void grouped_gemm_body(
             const int buf = local & 1;
             const uint32_t ph = (local >> 1) & 1;
             const int group = (warp - 4) / 4;
-            Shared sh{buf == 0, C::OV && (buf == 0 ? group == C::EW / 4 - 1 : group == 0),
+            Shared sh{buf == 0,
+                      C::OV && (C::OV_GROUPS == 2 || (buf == 0 ? group == C::EW / 4 - 1 : group == 0)),
                       C::OV && C::PAIR ? mapa_shared(smem_u32(S.tshared), 0) : smem_u32(S.tshared)};
             if constexpr (C::AU) {  // this tile's first a/u chunks while the MMA runs
                 if (lane == 0)
