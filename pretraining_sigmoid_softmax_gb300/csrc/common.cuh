@@ -360,40 +360,46 @@ __host__ __device__ constexpr uint32_t idesc_fp4(uint32_t n, uint32_t m, bool e8
     return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) | ((m >> 4) << 24);
 }
 
-// Shared-memory matrix descriptor of an unswizzled tile of 16-byte rows (8-row groups of 128
-// bytes, back to back): a 512-byte scale tile as tcgen05.cp reads it.
-__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr) {
-    uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    desc |= static_cast<uint64_t>(128 >> 4) << 32;
-    desc |= static_cast<uint64_t>(1) << 46;
-    return desc;
-}
+// Shared-memory matrix descriptors as two words: the low one is the address (tiles of one kind differ
+// in it alone), the high one is the same for every tile of a kind.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+// 128-byte-swizzled K-major operand (as sdesc_sw128 with groups of 8 rows 1024 bytes apart); low word.
+__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t saddr) { return desc_lo(saddr) | (1u << 16); }
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Unswizzled tile of 16-byte rows (groups of 8 rows, 128 bytes each, back to back): a 512-byte scale
+// tile as tcgen05.cp reads it.
+constexpr uint32_t kDescHiPlain = (128u >> 4) | (1u << 14);
 
 // One scale tile (32 lanes x 16 bytes) into four tensor-memory columns, the same in each of the
-// four lane quadrants; for a pair, each CTA's tile into its own tensor memory. Instructions
-// issued after it by this thread read what it wrote.
+// four lane quadrants; for a pair, each CTA's tile into its own tensor memory.
 template <bool PAIR>
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t desc) {
     if constexpr (PAIR)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                     : "memory");
+        asm volatile(
+            "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+            "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(desc),
+            "n"(kDescHiPlain)
+            : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                     : "memory");
+        asm volatile(
+            "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+            "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(desc),
+            "n"(kDescHiPlain)
+            : "memory");
 }
 
 // D[tmem] (+)= (A sA)[smem] (B sB)[smem]^T for one K = 64 step of E2M1 codes, each block times its
-// scale from tensor memory; NV: E4M3 scales per 16 elements, else powers of two per 32.
+// scale from tensor memory; NV: E4M3 scales per 16 elements, else powers of two per 32. a and b: low
+// words of the operands' descriptors.
 template <bool PAIR, bool NV>
-__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t accumulate) {
-#define MOE_UMMA_FP4(group, kind)                                                              \
-    asm volatile("{\n\t.reg .pred p;\n\t"                                                      \
-                 "setp.ne.b32 p, %4, 0;\n\t"                                                   \
-                 "tcgen05.mma.cta_group::" group "." kind " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" \
-                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa),  \
-                 "r"(sfb)                                                                      \
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+#define MOE_UMMA_FP4(group, kind)                                                                \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"                                    \
+                 "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %7};\n\tmov.b64 y, {%2, %7};\n\t"     \
+                 "tcgen05.mma.cta_group::" group "." kind " [%0], x, y, %3, [%5], [%6], p;\n\t}"   \
+                 ::"r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb),  \
+                 "n"(kDescHiSw128)                                                               \
                  : "memory")
     if constexpr (PAIR && NV) MOE_UMMA_FP4("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
     else if constexpr (PAIR) MOE_UMMA_FP4("2", "kind::mxf4.block_scale.scale_vec::2X");
@@ -420,6 +426,14 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // Arrive on an mbarrier given by a shared::cluster address (own or peer CTA).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
+// The same without release semantics, for a thread that publishes no memory: it only says that its
+// tensor-memory reads are over (tcgen05.wait::ld and the fence before it see to that). A releasing
+// arrive waits for the thread's earlier stores, those of the TMA among them, to drain.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
 }
 

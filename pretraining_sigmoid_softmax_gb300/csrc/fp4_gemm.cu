@@ -1,5 +1,6 @@
 // The grouped GEMMs on microscaled 4-bit operands (formats: fp4.cuh; kernel template:
 // grouped_gemm.cuh): the plain grouped product, and the experts' forward and backward.
+#include <stdlib.h>
 #include "fp4.cuh"
 #include "grouped_gemm.cuh"
 
@@ -10,11 +11,16 @@ namespace {
 template <bool NV>
 struct Fp4Gemm {
     static constexpr int QT = NV ? kNvFp4 : kMxFp4;
-    using G1P = Cfg<128, false, false, true, kEpiSwigluFwd, false, false, true, QT>;
-    using StoreP = Cfg<256, false, false, false, kEpiStore, false, false, true, QT>;
-    using Store = Cfg<128, false, false, false, kEpiStore, false, false, false, QT>;
-    using BwdP = Cfg<256, false, false, false, kEpiSwigluBwd, false, false, true, QT>;
-    using Bwd = Cfg<128, false, false, false, kEpiSwigluBwd, false, false, false, QT>;
+#ifndef EWS
+#define EWS 8
+#endif
+#ifndef EWG
+#define EWG 8
+#endif
+    using G1P = Cfg<128, false, false, true, kEpiSwigluFwd, false, false, true, QT, 16, EWG>;
+    using StoreP = Cfg<256, false, false, false, kEpiStore, false, false, true, QT, 16, EWS>;
+    using StoreP192 = Cfg<192, false, false, false, kEpiStore, false, false, true, QT, 16, 12>;
+    using BwdP = Cfg<192, false, false, false, kEpiSwigluBwd, false, false, true, QT, 16, 12>;
 };
 
 // An operand: codes [rows, K / 2], tiled scales and, in NV, the rows' powers of two.
@@ -29,8 +35,8 @@ bool operand_ok(const Operand& o, int fmt) {
            aligned16(o.g);
 }
 
-bool code_map(CUtensorMap* m, const uint8_t* q, int K, uint64_t rows) {
-    return make_map(m, q, (uint64_t)K / 2, rows, 128, 128, true);
+bool code_map(CUtensorMap* m, const uint8_t* q, int K, uint64_t rows, int box_rows = 128) {
+    return make_map(m, q, (uint64_t)K / 2, rows, 128, (uint32_t)box_rows, true);
 }
 
 // Scale tiles as rows of 128 32-bit words, SFK of them a box.
@@ -53,7 +59,9 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
             const Operand& W, moe_bf16* Y, const float* r1_row, const float* r1_col, cudaStream_t st) {
     using G = Fp4Gemm<NV>;
     CUtensorMap mx, mw, sf[3], mo[3];
-    if (!code_map(&mx, X.q, K, rows) || !code_map(&mw, W.q, K, (uint64_t)E * N) ||
+    const bool wide = getenv("W256") ? atoi(getenv("W256")) : true;
+    if (!code_map(&mx, X.q, K, rows) ||
+        !code_map(&mw, W.q, K, (uint64_t)E * N, N % 256 == 0 && wide ? 128 : 96) ||
         !scale_map<NV>(&sf[0], X.s, K, rows) || !scale_map<NV>(&sf[1], W.s, K, (int64_t)E * N) ||
         !out_maps(mo, Y, nullptr, nullptr, N, rows, G::StoreP::OCOLS))
         return MOE_ERR_LAUNCH;
@@ -65,9 +73,9 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
     P.sb0 = W.g;
     P.r1_row = r1_row;
     P.r1_col = r1_col;
-    if (N % 256 == 0)
+    if (N % 256 == 0 && wide)
         return launch<typename G::StoreP>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 256), st, mo, sf);
-    return launch<typename G::Store>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 128), st, mo, sf);
+    return launch<typename G::StoreP192>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 192), st, mo, sf);
 }
 
 // a, u = X W_g^T, X W_u^T; h = silu(a) u.
@@ -100,7 +108,7 @@ int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const in
                cudaStream_t st) {
     using G = Fp4Gemm<NV>;
     CUtensorMap my, mw, ma, mu, sf[3], mo[3];
-    if (!code_map(&my, dY.q, d, rows) || !code_map(&mw, Wd.q, d, (uint64_t)E * f) ||
+    if (!code_map(&my, dY.q, d, rows) || !code_map(&mw, Wd.q, d, (uint64_t)E * f, 96) ||
         !scale_map<NV>(&sf[0], dY.s, d, rows) || !scale_map<NV>(&sf[1], Wd.s, d, (int64_t)E * f) ||
         !make_map(&ma, A, f, rows, G::BwdP::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !make_map(&mu, U, f, rows, G::BwdP::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
@@ -114,9 +122,7 @@ int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const in
     P.ld_out = f;
     P.sa = dY.g;
     P.sb0 = Wd.g;
-    if (f % 256 == 0)
-        return launch<typename G::BwdP>(my, ma, mw, mu, P, token_tiles_max(rows, f, 256), st, mo, sf);
-    return launch<typename G::Bwd>(my, ma, mw, mu, P, token_tiles_max(rows, f, 128), st, mo, sf);
+    return launch<typename G::BwdP>(my, ma, mw, mu, P, token_tiles_max(rows, f, 192), st, mo, sf);
 }
 
 int quantize(const moe_bf16* X, const moe_bf16* X1, const int64_t* row_offsets, int E, int64_t rows,

@@ -86,10 +86,11 @@ template <int BN_, bool A_MN_, bool B_MN_, bool DUAL_, int EPI_, bool TWO_K_, bo
           bool PAIR_ = false, int QT_ = kBf16, int OC_ = kOutCols, int EW_ = kEpiWarps>
 struct Cfg {
     // epilogue warps: 8 (two per TMEM lane quadrant), or 16 for GEMMs whose reduction is so
-    // short that the epilogue, not the tensor cores, sets the pace (at most 96 registers)
+    // short that the epilogue, not the tensor cores, sets the pace (at most 96 registers); 12
+    // for the 192-column tiles of E2M1
     static constexpr int EW = EW_;
     static constexpr int THREADS = 128 + 32 * EW;
-    static_assert(EW == 8 || EW == 16, "epilogue warps");
+    static_assert(EW == 8 || EW == 16 || EW == 12, "epilogue warps");
     static constexpr bool FP8 = QT_ == kE4m3;  // E4M3 operands with row / column scales
     static constexpr bool NV = QT_ == kNvFp4;  // E2M1, E4M3 scale per 16, power of two per row
     static constexpr bool FP4 = QT_ == kMxFp4 || NV;
@@ -121,19 +122,22 @@ struct Cfg {
     // so short that the number of TMA rows sets the pace, else 16
     static constexpr int AUC = FP4 ? 32 : kAuCols;
     static constexpr int AU_BUF_BYTES = 2 * 32 * AUC * 2;  // a and u: 32 rows x AUC
+    static_assert(!(FP4 && AU) || BN / (EW / 4) == kAuBufs * AUC, "E2M1: a tile's a and u staged whole");
     static constexpr int AU_BYTES = AU ? EW * kAuBufs * AU_BUF_BYTES : 0;
     static constexpr bool TS = !WGRAD;  // token-major outputs leave by TMA stores
     static constexpr int NOUT = EPI == kEpiSwigluFwd ? 3 : EPI == kEpiSwigluBwd ? 2 : 1;
     // output columns per staged chunk: 16, or 32 (single-output epilogues of short-K GEMMs,
     // where the per-chunk fence and store issue dominate) at the same shared-memory size
     // (E2M1: 64 columns a box, whole 128-byte lines, in two buffers a warp; see epilogue_fp4)
-    static constexpr int OCOLS = FP4 ? (AU ? AUC : 64) : OC_;
+    static constexpr int OCOLS =  // (E2M1 with AU: from a's and u's own buffers)
+        FP4 ? (AU ? AUC : BN / (EW / 4) < 64 ? BN / (EW / 4) : 64) : OC_;
     static_assert(FP4 || OCOLS == 16 || (OCOLS == 32 && NOUT == 1 && !AU), "output chunk width");
     static constexpr int OUT_BOX_BYTES = 32 * OCOLS * 2;             // one output, one chunk
     static constexpr int OUT_BUF_BYTES = (FP4 && !AU ? 1 : NOUT) * OUT_BOX_BYTES;  // one buffer
     static constexpr int OUT_DEPTH =
-        FP4 && !AU ? 2 : (AU || OCOLS == 32 || EW == 16) ? 1 : 2;    // buffers per warp
-    static constexpr int OUT_BYTES = TS ? EW * OUT_DEPTH * OUT_BUF_BYTES : 0;
+        FP4 ? (EPI == kEpiSwigluFwd ? 3 : AU ? 1 : BN / (EW / 4) / 64)
+            : (AU || OCOLS == 32 || EW == 16) ? 1 : 2;  // buffers per warp
+    static constexpr int OUT_BYTES = TS && !(FP4 && AU) ? EW * OUT_DEPTH * OUT_BUF_BYTES : 0;
     static constexpr int BUDGET = (AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
     static constexpr int STAGES = (BUDGET / STAGE_BYTES) > 6 ? 6 : (BUDGET / STAGE_BYTES);
     static constexpr int ACC_COLS = MMA_N;
@@ -145,11 +149,11 @@ struct Cfg {
     static constexpr int SFC = SFK * 4 * (1 + SFB_TILES);
     static constexpr int OV = FP4 && ACC_COLS == 256 ? 2 * SFC : 0;
     // groups of epilogue warps (of one column range, four lane quadrants) that hold shared columns
-    static constexpr int OV_GROUPS = OV <= BN / (EW / 4) ? 1 : 2;
+    static constexpr int OV_GROUPS = (OV + BN / (EW / 4) - 1) / (BN / (EW / 4));
     static constexpr int ACC0 = FP4 ? (OV ? OV : 128) : 0;
-    static constexpr int ACC1 = FP4 ? 256 : ACC_COLS;
+    static constexpr int ACC1 = FP4 ? (OV ? 256 : ACC0 + ACC_COLS) : ACC_COLS;
     static constexpr int TMEM_COLS = FP4 ? 512 : 2 * ACC_COLS;  // two accumulator buffers
-    static_assert(!FP4 || 2 * SFC <= ACC0, "columns of the scales");
+    static_assert(!FP4 || (2 * SFC <= ACC0 && ACC1 + ACC_COLS <= 512), "columns of the scales");
     // DUAL: the W_g and W_u boxes form one 2*BN-row B tile (on one CTA, back to back; in a
     // pair, W_g on the leader and W_u on the peer), so one instruction fills gate columns
     // [0, BN) and up columns [BN, 2BN).
@@ -158,15 +162,14 @@ struct Cfg {
     static_assert(!(FP8 || FP4) || (!A_MN && !B_MN && !WGRAD && !TWO_K),
                   "E4M3 and E2M1: K-major GEMMs");
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory columns");
-    static_assert(BN % 64 == 0 && MMA_N <= 256 && BROWS % 64 == 0, "tile width");
+    static_assert(BN % 64 == 0 && MMA_N <= 256 && BROWS % (FP4 ? 32 : 64) == 0, "tile width");
     static constexpr size_t MISC_BYTES = 512 + sizeof(int64_t) * (kMaxExperts + 1) +
                                          sizeof(int32_t) * kMaxExperts +
                                          sizeof(int32_t) * (kMaxExperts + 1);
     static constexpr size_t SMEM_BYTES =
         1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + MISC_BYTES;
-    static_assert((2 * STAGES + 9 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
-    static_assert(!FP4 || EW == 8, "two epilogue warps per lane quadrant");
-    static_assert(OV_GROUPS == 1 || DUAL, "which warps report shared columns");
+    static_assert((2 * STAGES + 7 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
+    static_assert(!(OV && AU), "the SwiGLU backward reports no shared columns");
     static_assert(STAGES * SF_BYTES % 1024 == 0, "alignment of what follows the stages");
 
 };
@@ -220,7 +223,6 @@ struct SmemLayout {
     uint64_t* tfull;   // 2
     uint64_t* tempty;  // 2
     uint64_t* sfready; // 2: a stage's scales are in tensor memory (E2M1)
-    uint64_t* sfempty; // 2: the instructions that read them are done
     uint64_t* tshared; // the accumulators' shared columns are read (E2M1)
     uint32_t* tmem_slot;
     int* abort_flag;
@@ -248,8 +250,7 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
     s.tempty = s.tfull + 2;
     s.tshared = s.tempty + 2;
     s.sfready = s.tshared + 1;
-    s.sfempty = s.sfready + 2;
-    s.au_full = s.sfempty + 2;
+    s.au_full = s.sfready + 2;
     s.tmem_slot = reinterpret_cast<uint32_t*>(s.au_full + (C::AU ? C::EW * kAuBufs : 0));
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
     s.offs = reinterpret_cast<int64_t*>(misc + 512);
@@ -260,9 +261,16 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
 
 __device__ __forceinline__ int64_t cdiv_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Tiles along N; E2M1's last one may reach past it (its operands there are other rows or zeros, its
+// outputs are clipped by the stores).
+template <class C>
+__device__ __forceinline__ int col_tiles(const Params& P) {
+    return C::FP4 ? (P.N + C::BN - 1) / C::BN : P.N / C::BN;
+}
+
 template <class C>
 __device__ __forceinline__ int64_t total_tiles(const Params& P, const SmemLayout& S) {
-    const int n_tiles = P.N / C::BN;
+    const int n_tiles = col_tiles<C>(P);
     if constexpr (C::WGRAD) {
         return (int64_t)P.E * P.nprob * (P.M_out / C::TILE_M) * n_tiles;
     } else {
@@ -292,7 +300,7 @@ template <class C>
 __device__ __forceinline__ TileInfo decode(int64_t tile, const Params& P, const SmemLayout& S,
                                            uint32_t rank) {
     TileInfo ti;
-    const int n_tiles = P.N / C::BN;
+    const int n_tiles = col_tiles<C>(P);
     const int64_t half = C::PAIR ? (int64_t)rank * BM : 0;
     if constexpr (C::WGRAD) {
         const int m_tiles = P.M_out / C::TILE_M;
@@ -332,10 +340,48 @@ __device__ __forceinline__ TileInfo decode(int64_t tile, const Params& P, const 
             ti.e = last_le(S.offs, P.E, ti.m0);
             ti.row_end = S.offs[ti.e + 1];
         }
-        if constexpr (C::FP4) ti.k_iters = (P.K0 + C::KB - 1) / C::KB;  // the last may be half a block
-        else ti.k_iters = (P.K0 + (C::TWO_K ? P.K1 : 0)) / C::KB;
+        ti.k_iters = (P.K0 + (C::TWO_K ? P.K1 : 0)) / C::KB;
     }
     return ti;
+}
+
+// The same for E2M1, whose tiles take as long as decode's 64-bit divisions and search: 32-bit
+// arithmetic (the launch has fewer than 2^31 tiles), and the expert found from the last tile's, as
+// the tiles a CTA takes ascend. The MMA and copying threads need no more of a tile than its columns.
+template <class C>
+__device__ __forceinline__ TileInfo decode_fp4(uint32_t tile, int& e, const Params& P,
+                                               const SmemLayout& S, uint32_t rank) {
+    TileInfo ti;
+    const uint32_t n_tiles = col_tiles<C>(P);
+    const uint32_t mt = tile / n_tiles;
+    ti.n0 = (int)(tile - mt * n_tiles) * C::BN;
+    ti.p = 0;
+    ti.k_lo = 0;
+    ti.k_iters = (P.K0 + C::KB - 1) / C::KB;  // the last may be half a block
+    const int64_t half = C::PAIR ? (int64_t)rank * BM : 0;
+    if (!P.row_offsets) {
+        ti.e = 0;
+        ti.m0 = (int64_t)mt * C::TILE_M + half;
+        ti.row_end = P.rows;
+    } else if constexpr (C::PAIR) {
+        while (e + 1 < P.E && (uint32_t)S.ptp[e + 1] <= mt) ++e;
+        ti.e = e;
+        ti.m0 = S.offs[e] + (int64_t)(mt - S.ptp[e]) * C::TILE_M + half;
+        ti.row_end = S.offs[e + 1];
+    } else {
+        ti.m0 = (int64_t)mt * BM;
+        while (e + 1 < P.E && S.offs[e + 1] <= ti.m0) ++e;
+        ti.e = e;
+        ti.row_end = S.offs[e + 1];
+    }
+    return ti;
+}
+
+template <class C>
+__device__ __forceinline__ TileInfo next_tile(int64_t tile, int& e, const Params& P,
+                                              const SmemLayout& S, uint32_t rank) {
+    if constexpr (C::FP4) return decode_fp4<C>((uint32_t)tile, e, P, S, rank);
+    else return decode<C>(tile, P, S, rank);
 }
 
 template <class C>
@@ -358,7 +404,7 @@ __device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint
     const int32_t kbyte = kb * (C::KB / 2);
     const int32_t ktiles = P.K0 / (C::KB / C::SFK);  // scale tiles along K
     const int32_t kt = kb * C::SFK;
-    const int32_t brow = ti.e * P.N + ti.n0;  // a multiple of 128, as N and the tile's columns are
+    const int32_t brow = ti.e * P.N + ti.n0;  // N is a multiple of 128, n0 at least of 64
     tma_load<C>(a_dst, ma0, bar, kbyte, (int32_t)ti.m0);
     if constexpr (C::DUAL) {
         if constexpr (C::PAIR) {
@@ -378,38 +424,33 @@ __device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint
 }
 
 // The scales of one E2M1 K block of `steps` steps of 64 into tensor memory (column tmem_sf on): tiles
-// `half` * SFK / 2 on, half of them; the other copying thread takes the rest.
+// `half` * SFK / 2 on, half of them; the other copying thread takes the rest. sf_lo: low word of the
+// descriptor of the stage's first scale tile.
 template <class C>
-__device__ __forceinline__ void issue_scales_fp4(uint32_t tmem_sf, uint32_t sf_s, int steps, int half) {
+__device__ __forceinline__ void issue_scales_fp4(uint32_t tmem_sf, uint32_t sf_lo, int steps, int half) {
     const uint32_t sfb = tmem_sf + C::SFK * 4;
     const int tiles = C::NV ? steps : steps / 2;
 #pragma unroll
     for (int i = 0; i < C::SFK / 2; ++i) {
         const int t = half * (C::SFK / 2) + i;
         if (t >= tiles) break;
-        tmem_cp_scales<C::PAIR>(tmem_sf + 4 * t, sdesc_plain(sf_s + t * kSfTile));
+        tmem_cp_scales<C::PAIR>(tmem_sf + 4 * t, sf_lo + t * (kSfTile / 16));
 #pragma unroll
         for (int h = 0; h < C::SFB_TILES; ++h)
             tmem_cp_scales<C::PAIR>(sfb + 4 * (C::SFB_TILES * t + h),
-                                    sdesc_plain(sf_s + (1 + h) * C::SFA_BYTES + t * kSfTile));
+                                    sf_lo + ((1 + h) * C::SFA_BYTES + t * kSfTile) / 16);
     }
 }
 
-// The products of one E2M1 K block: a step per 64 K elements.
-template <class C>
-__device__ __forceinline__ void issue_mma_fp4(uint32_t d_tmem, uint32_t tmem_sf, uint32_t a_s,
-                                              uint32_t b_s, int steps, bool first) {
-    const uint32_t sfb = tmem_sf + C::SFK * 4;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-        if (kk >= steps) break;
-        const int t = C::NV ? kk : kk / 2;
-        const uint32_t id = C::NV ? 0u : 2u * (kk & 1);  // which half of the tile's four blocks
-        umma_fp4<C::PAIR, C::NV>(d_tmem, sdesc_sw128(a_s + kk * 32, 16, 1024),
-                                 sdesc_sw128(b_s + kk * 32, 16, 1024),
-                                 C::IDESC | (id << 29) | (id << 4), tmem_sf + 4 * t,
-                                 sfb + 4 * C::SFB_TILES * t, !first || kk > 0);
-    }
+// One step of 64 K elements of an E2M1 K block; a_lo and b_lo: low words of the descriptors of the
+// stage's operands, sfb: column of the B scales.
+template <class C, int KK>
+__device__ __forceinline__ void issue_step_fp4(uint32_t d_tmem, uint32_t sfa, uint32_t sfb,
+                                               uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+    constexpr int t = C::NV ? KK : KK / 2;
+    constexpr uint32_t id = C::NV ? 0u : 2u * (KK & 1);  // which half of the tile's four blocks
+    umma_fp4<C::PAIR, C::NV>(d_tmem, a_lo + 2 * KK, b_lo + 2 * KK, C::IDESC | (id << 29) | (id << 4),
+                             sfa + 4 * t, sfb + 4 * C::SFB_TILES * t, accumulate);
 }
 
 // Loads of K block `kb` of a tile into this CTA's stage buffers; `bar` is the barrier the
@@ -463,29 +504,6 @@ __device__ __forceinline__ void issue_loads(const TileInfo& ti, int kb, uint32_t
 __device__ __forceinline__ uint4 pack_chunk8(const float* v) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                       pack_bf16x2(v[6], v[7]));
-}
-
-// E2M1 accumulators that share columns: which chunks of a tile a warp takes first, and the report
-// that the shared ones are read. Buffer 0 shares its last columns, so its chunks run backwards;
-// the warps that hold the shared columns (the last or the first group) report, once a tile.
-struct Shared {
-    bool reversed;  // chunks in descending order of their columns
-    bool reports;   // this warp holds shared columns
-    uint32_t bar;   // shared::cluster address in a pair, else this CTA's barrier
-};
-
-template <class C>
-__device__ __forceinline__ void report_shared(Shared& sh, int lane) {
-    if constexpr (C::OV > 0) {
-        if (!sh.reports) return;
-        sh.reports = false;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            if constexpr (C::PAIR) mbar_arrive_cluster(sh.bar);
-            else mbar_arrive(sh.bar);
-        }
-    }
 }
 
 // FP8 dequantisation of a 32-column accumulator chunk: value * scale(A row) * scale(B row
@@ -648,104 +666,127 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
 
 // ------------------------------------------------- outputs of the E2M1 GEMMs
 // A tile's main loop is a quarter of the bf16 one's, so the number of rows that the TMA stores
-// move sets the pace (16-column boxes: 5 to 8 cycles for each 32-byte row of a box, which made the
-// large down projection 2.29 ms): boxes are 64 columns x 32 rows, whole 128-byte lines, two 4 KB
-// buffers a warp. A warp takes 64 columns out of tensor memory before anything else, so that
-// shared columns are free a few hundred cycles after the tile's last instruction.
+// move and the time from a tile's last instruction until its columns are free set the pace. Boxes are
+// up to 64 columns x 32 rows, whole 128-byte lines (with 16-column boxes the gate and up projections
+// of experts of 768 took 1144 us, with 64-column ones 540), and sixteen warps (twelve for 192
+// columns) take one box's columns each.
 
 // Byte offset of 16-byte piece j of row r in a 128-byte-swizzled box of 128-byte rows.
 __device__ __forceinline__ int sw128_offset(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-// A warp's boxes: open one (its buffer's last store has read it), put a half of 32 packed columns of
-// this thread's row into it, send it off.
+// 32 packed columns of this thread's row into its place in a box of C::OCOLS columns.
 template <class C>
-__device__ __forceinline__ uint8_t* open_box(const SmemLayout& S, int slot, int lane, uint32_t& n) {
-    uint8_t* buf = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
-    ++n;
-    if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();
-    __syncwarp();
-    return buf;
-}
 __device__ __forceinline__ void put_half(uint8_t* buf, int lane, int half, const uint32_t* w) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(buf + sw128_offset(lane, 4 * half + j)) =
+        *reinterpret_cast<uint4*>(buf + (C::OCOLS == 64 ? sw128_offset(lane, 4 * half + j)
+                                                        : sw64_offset(lane, j))) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
-__device__ __forceinline__ void send_box(const uint8_t* buf, int lane, const CUtensorMap* mo, int col,
-                                         int64_t row0) {
-    fence_async_smem();
+
+// Arrivals at the leading CTA's barriers (this CTA's, outside pairs) that a warp's reads are over: of
+// the columns shared with the next tile's accumulator, and of the whole one.
+struct Readers {
+    bool shared;            // this warp holds shared columns
+    uint32_t shared_bar, whole_bar;
+};
+template <class C>
+__device__ __forceinline__ void arrive_read(uint32_t bar, int lane) {
+    tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
-        tma_store_2d(mo, smem_u32(buf), col, (int32_t)row0);
-        bulk_commit();
-    }
+    if (lane != 0) return;
+    if constexpr (C::PAIR) mbar_arrive_cluster_relaxed(bar);
+    else mbar_arrive(bar);
 }
 
 template <class C>
 __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo& ti, uint32_t t_acc,
-                                             int q, int lane, int slot, int c_lo, const Params& P,
+                                             int lane, int slot, int c_lo, int64_t row0, const Params& P,
                                              const CUtensorMap* mo0, const CUtensorMap* mo1,
-                                             const CUtensorMap* mo2, uint32_t& n, Shared& sh) {
-    constexpr int kHalves = C::BN / (C::EW / 4) / 32;  // of this warp's columns (of gate and of up)
-    static_assert(kHalves % 2 == 0, "whole boxes");
-    if (ti.m0 >= ti.row_end) return;  // warp-uniform: the whole half is past the segment
-    const int64_t row0 = ti.m0 + 32 * q;
+                                             const CUtensorMap* mo2, bool reversed, const Readers& rd) {
+    constexpr int kCols = C::BN / (C::EW / 4);    // of this warp (in each accumulator)
+    // nothing to write: the half of a pair's tile past its segment, columns past the outputs
+    if (ti.m0 >= ti.row_end || (C::BN % 128 && ti.n0 + c_lo >= P.N)) {
+        if (C::OV && rd.shared) arrive_read<C>(rd.shared_bar, lane);
+        arrive_read<C>(rd.whole_bar, lane);
+        return;
+    }
     // rows past row_end (the tail of an unpadded layout) are clipped by the store
     const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
+    uint8_t* buf = S.ob + (size_t)slot * C::OUT_DEPTH * C::OUT_BUF_BYTES;
     if constexpr (C::EPI == kEpiSwigluFwd) {
-        static_assert(kHalves == 2, "gate and up columns of a warp in one box each");
-        uint32_t g[2][32], u[2][32], h[32];
-        tmem_ld32(t_acc + c_lo, g[0]);
-        tmem_ld32(t_acc + c_lo + 32, g[1]);
-        tmem_ld32(t_acc + C::BN + c_lo, u[0]);
-        tmem_ld32(t_acc + C::BN + c_lo + 32, u[1]);
-        tmem_ld_wait();
-        report_shared<C>(sh, lane);
-        const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
-        uint32_t a[32], b[32];
+        constexpr int kHalves = C::OCOLS / 32;
+        static_assert(kCols == C::OCOLS, "one box a warp and output");
+        uint32_t g[kHalves][32], u[kHalves][32];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kHalves; ++k) {
+            tmem_ld32(t_acc + c_lo + 32 * k, g[k]);
+            tmem_ld32(t_acc + C::BN + c_lo + 32 * k, u[k]);
+        }
+        tmem_ld_wait();
+        if (C::OV && rd.shared) arrive_read<C>(rd.shared_bar, lane);
+        arrive_read<C>(rd.whole_bar, lane);
+        if (lane == 0) bulk_wait_read<0>();  // the previous tile's boxes have left
+        __syncwarp();
+        const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
+#pragma unroll
+        for (int k = 0; k < kHalves; ++k) {
             float* gf = reinterpret_cast<float*>(g[k]);
             float* uf = reinterpret_cast<float*>(u[k]);
             if constexpr (C::NV) fp8_scale<32>(gf, uf, P, row, ti, c_lo + 32 * k);
+            uint32_t w[16];
+            if (!P.only_h) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(gf[2 * j], gf[2 * j + 1]);
+                put_half<C>(buf, lane, k, w);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(uf[2 * j], uf[2 * j + 1]);
+                put_half<C>(buf + C::OUT_BUF_BYTES, lane, k, w);
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float g0 = gf[2 * j], g1 = gf[2 * j + 1];
-                const float u0 = uf[2 * j], u1 = uf[2 * j + 1];
-                a[16 * k + j] = pack_bf16x2(g0, g1);
-                b[16 * k + j] = pack_bf16x2(u0, u1);
-                h[16 * k + j] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * u0 * rg,
-                                            __fdividef(g1, 1.0f + __expf(-g1)) * u1 * rg);
+                w[j] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * uf[2 * j] * rg,
+                                   __fdividef(g1, 1.0f + __expf(-g1)) * uf[2 * j + 1] * rg);
             }
+            put_half<C>(buf + 2 * C::OUT_BUF_BYTES, lane, k, w);
         }
-        const CUtensorMap* mo[3] = {mo0, mo1, mo2};
-#pragma unroll
-        for (int o = 0; o < 3; ++o) {
-            if (o < 2 && P.only_h) continue;
-            const uint32_t* w = o == 0 ? a : o == 1 ? b : h;
-            uint8_t* buf = open_box<C>(S, slot, lane, n);
-            put_half(buf, lane, 0, w);
-            put_half(buf, lane, 1, w + 16);
-            send_box(buf, lane, mo[o], ti.n0 + c_lo, row0);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (!P.only_h) {
+                tma_store_2d(mo0, smem_u32(buf), ti.n0 + c_lo, (int32_t)row0);
+                tma_store_2d(mo1, smem_u32(buf + C::OUT_BUF_BYTES), ti.n0 + c_lo, (int32_t)row0);
+            }
+            tma_store_2d(mo2, smem_u32(buf + 2 * C::OUT_BUF_BYTES), ti.n0 + c_lo, (int32_t)row0);
+            bulk_commit();
         }
     } else {
-        // halves in order, or (buffer 0 of accumulators that share columns) the last first; those with
-        // shared columns are taken out of tensor memory at once
-        constexpr int kAhead = C::OV ? (C::OV + 31) / 32 : 2;
+        // halves of 32 columns in order, or (buffer 0 of accumulators that share columns) the last
+        // first; those with shared columns are taken out of tensor memory at once
+        constexpr int kHalves = kCols / 32;
+        constexpr int kAhead = !C::OV || kHalves < (C::OV + 31) / 32 ? kHalves : (C::OV + 31) / 32;
+        auto half = [&](int i) { return C::OV && reversed ? kHalves - 1 - i : i; };
         uint32_t r[kHalves][32];
-        auto half = [&](int i) { return C::OV && sh.reversed ? kHalves - 1 - i : i; };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) tmem_ld32(t_acc + c_lo + 32 * half(i), r[i]);
         tmem_ld_wait();
-        report_shared<C>(sh, lane);
-        uint8_t* buf = nullptr;
+        if (C::OV && rd.shared) arrive_read<C>(rd.shared_bar, lane);
+        if (kAhead == kHalves) arrive_read<C>(rd.whole_bar, lane);
 #pragma unroll
         for (int i = 0; i < kHalves; ++i) {
             const int c = c_lo + 32 * half(i);
-            if (i >= kAhead) {
-                tmem_ld32(t_acc + c, r[i]);
-                tmem_ld_wait();
+            if (i % 2 == 0) {
+                if (i + 1 >= kAhead) {  // the rest of this box
+#pragma unroll
+                    for (int k = i < kAhead ? kAhead : i; k < i + 2; ++k)
+                        tmem_ld32(t_acc + c_lo + 32 * half(k), r[k]);
+                    tmem_ld_wait();
+                    if (kAhead < kHalves && i + 2 == kHalves) arrive_read<C>(rd.whole_bar, lane);
+                }
+                // the store that last read this buffer is done
+                if (lane == 0) bulk_wait_read<kHalves / 2 - 1>();
+                __syncwarp();
             }
             float* v = reinterpret_cast<float*>(r[i]);
             if constexpr (C::NV) fp8_scale<32>(v, v, P, row, ti, c, /*dual=*/false);
@@ -753,25 +794,32 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            if (i % 2 == 0) buf = open_box<C>(S, slot, lane, n);
-            put_half(buf, lane, half(i) & 1, w);
-            if (i % 2 == 1) send_box(buf, lane, mo0, ti.n0 + (c & ~63), row0);
+            uint8_t* box = buf + i / 2 * C::OUT_BUF_BYTES;
+            put_half<C>(box, lane, half(i) & 1, w);
+            if (i % 2 == 1) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(mo0, smem_u32(box), ti.n0 + (c & ~63), (int32_t)row0);
+                    bulk_commit();
+                }
+            }
         }
     }
 }
 
 // ------------------------------------------------- SwiGLU backward with staged a and u
 // Each epilogue warp owns 32 rows x (BN / 2) columns of the tile and walks them in chunks of
-// AUC. The chunk's saved a and u arrive by TMA (boxes of AUC x 32 rows, swizzled
+// kAuCols. The chunk's saved a and u arrive by TMA (boxes of kAuCols x 32 rows, swizzled
 // so that the row-per-lane reads below hit distinct banks) into one of the warp's kAuBufs
 // buffers; lane 0 issues the copy of chunk n + kAuBufs once the warp is done with chunk n,
 // and a tile's first chunks before its accumulator is ready.
 
 // Byte offset of 16-byte piece j of row r in a staged (a or u) chunk.
-template <int COLS>
 __device__ __forceinline__ int au_offset(int r, int j) {
-    if constexpr (COLS == 32) return sw64_offset(r, j);
-    else return sw32_offset(r, j);
+    if constexpr (kAuCols == 32) return r * 64 + ((j ^ ((r >> 1) & 3)) << 4);  // 64-byte swizzle
+    else if constexpr (kAuCols == 16) return r * 32 + ((j ^ ((r >> 2) & 1)) << 4);  // 32-byte
+    else return r * 16;                                                            // unswizzled
 }
 
 template <class C>
@@ -789,12 +837,6 @@ __device__ __forceinline__ void au_issue(const SmemLayout& S, const CUtensorMap*
     tma_load_2d(dst + C::AU_BUF_BYTES / 2, mu, bar, col, (int32_t)row0);
 }
 
-// Which chunk of columns a warp takes i-th.
-template <class C>
-__device__ __forceinline__ int au_chunk(int i, int nch, const Shared& sh) {
-    return C::OV && sh.reversed ? nch - 1 - i : i;
-}
-
 // One tile of this warp's columns [c_lo, c_lo + ncols). `n` counts the warp's chunks over the
 // kernel's life (it picks buffer and phase). Returns false when a wait failed (uniform
 // across the warp).
@@ -804,12 +846,9 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
                                                   int c_lo, int ncols, const Params& P,
                                                   const CUtensorMap* ma, const CUtensorMap* mu,
                                                   const CUtensorMap* mda, const CUtensorMap* mdu,
-                                                  uint32_t& n, volatile int* abort_flag,
-                                                  Shared& sh) {
-    constexpr int W = C::AUC;
-    constexpr int kBox = C::OUT_BOX_BYTES;
-    static_assert(W == C::OCOLS, "one staged output chunk per a/u chunk");
-    const int nch = ncols / W;
+                                                  uint32_t& n, volatile int* abort_flag) {
+    static_assert(kAuCols == kOutCols, "one staged output chunk per a/u chunk");
+    const int nch = ncols / kAuCols;
     const int64_t row0 = ti.m0 + 32 * q;
     const int64_t row = row0 + lane;
     const bool ok_row = row < ti.row_end;
@@ -821,30 +860,29 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
     const float g = (P.row_scale && ok_row) ? __ldg(P.row_scale + row) : 1.0f;
     float gpart = 0.f;
     for (int i = 0; i < nch; ++i, ++n) {
-        const int c = c_lo + au_chunk<C>(i, nch, sh) * W;
+        const int c = c_lo + i * kAuCols;
         const int b = (int)(n % kAuBufs);
-        uint32_t acc[W];
-        tmem_ld_cols<W>(t_acc + c, acc);
+        uint32_t acc[kAuCols];
+        tmem_ld_cols<kAuCols>(t_acc + c, acc);
         bool ok = mbar_wait_bounded(smem_u32(&S.au_full[slot * kAuBufs + b]), (n / kAuBufs) & 1u,
                                     abort_flag, P.status, P.wait_limit_ns, 34);
         tmem_ld_wait();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
-        if (C::OV && i == (C::OV + W - 1) / W - 1) report_shared<C>(sh, lane);
-        float dav[W], duv[W];
+        float dav[kAuCols], duv[kAuCols];
         if (store) {  // lanes past an unpadded layout's end see zero-filled a, u and acc
             const uint8_t* abuf = S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES;
             const uint8_t* ubuf = abuf + C::AU_BUF_BYTES / 2;
-            float accf[W];
+            float accf[kAuCols];
 #pragma unroll
-            for (int j = 0; j < W; ++j) accf[j] = __uint_as_float(acc[j]);
+            for (int j = 0; j < kAuCols; ++j) accf[j] = __uint_as_float(acc[j]);
             // FP8 operands: the dequantised r = (dy codes) (W_d codes) * scale(row) * scale(col)
-            if constexpr (C::SCALED)
-                fp8_scale<W>(accf, accf, P, ok_row ? row : ti.row_end - 1, ti, c, false);
+            if constexpr (C::FP8)
+                fp8_scale<kAuCols>(accf, accf, P, ok_row ? row : ti.row_end - 1, ti, c, false);
 #pragma unroll
-            for (int j = 0; j < W / 8; ++j) {
-                const uint4 a4 = *reinterpret_cast<const uint4*>(abuf + au_offset<W>(lane, j));
-                const uint4 u4 = *reinterpret_cast<const uint4*>(ubuf + au_offset<W>(lane, j));
+            for (int j = 0; j < kAuCols / 8; ++j) {
+                const uint4 a4 = *reinterpret_cast<const uint4*>(abuf + au_offset(lane, j));
+                const uint4 u4 = *reinterpret_cast<const uint4*>(ubuf + au_offset(lane, j));
                 const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w};
                 const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
@@ -852,42 +890,112 @@ __device__ __forceinline__ bool swiglu_bwd_staged(const SmemLayout& S, const Til
                     const float a = (h & 1) ? bf16_hi(aw[h >> 1]) : bf16_lo(aw[h >> 1]);
                     const float u = (h & 1) ? bf16_hi(uw[h >> 1]) : bf16_lo(uw[h >> 1]);
                     const float acc_h = accf[8 * j + h];
-                    // (E2M1: an approximate quotient, 2 ulp; the correctly rounded one made this epilogue
-                    // the pace of the whole kernel, 632 instead of 400 us with experts of 768)
-                    const float sa = C::FP4 ? __fdividef(1.0f, 1.0f + __expf(-a))
-                                            : 1.0f / (1.0f + __expf(-a));
-                    if (!C::FP4 && P.gate_part) gpart = fmaf(acc_h, a * sa * u, gpart);
+                    const float sa = 1.0f / (1.0f + __expf(-a));
+                    if (P.gate_part) gpart = fmaf(acc_h, a * sa * u, gpart);
                     const float dh = acc_h * g;
                     dav[8 * j + h] = dh * u * sa * (1.0f + a * (1.0f - sa));
                     duv[8 * j + h] = dh * a * sa;
                 }
             }
             const int col = ti.n0 + c;
-            if (!C::FP4 && P.gate_part && (col + W) % 64 == 0) {  // last chunk of a 64-column group
+            if (P.gate_part && (col + kAuCols) % 64 == 0) {  // last chunk of a 64-column group
                 if (ok_row) P.gate_part[row * (int64_t)(P.ld_out / 64) + col / 64] = gpart;
                 gpart = 0.f;
             }
         }
         __syncwarp();  // every lane is done with a/u buffer b
         if (lane == 0 && i + kAuBufs < nch)
-            au_issue<C>(S, ma, mu, slot, n + kAuBufs, row0,
-                        ti.n0 + c_lo + au_chunk<C>(i + kAuBufs, nch, sh) * W);
+            au_issue<C>(S, ma, mu, slot, n + kAuBufs, row0, ti.n0 + c + kAuBufs * kAuCols);
         if (store) {
             uint8_t* ob = S.ob + ((size_t)slot * C::OUT_DEPTH + n % C::OUT_DEPTH) * C::OUT_BUF_BYTES;
             if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // the store that last read it is done
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < W / 8; ++j) {
-                *reinterpret_cast<uint4*>(ob + au_offset<W>(lane, j)) = pack_chunk8(dav + 8 * j);
-                *reinterpret_cast<uint4*>(ob + kBox + au_offset<W>(lane, j)) = pack_chunk8(duv + 8 * j);
+            for (int j = 0; j < kAuCols / 8; ++j) {
+                *reinterpret_cast<uint4*>(ob + sw32_offset(lane, j)) = pack_chunk8(dav + 8 * j);
+                *reinterpret_cast<uint4*>(ob + 1024 + sw32_offset(lane, j)) = pack_chunk8(duv + 8 * j);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
                 tma_store_2d(mda, smem_u32(ob), ti.n0 + c, (int32_t)row0);
-                tma_store_2d(mdu, smem_u32(ob + kBox), ti.n0 + c, (int32_t)row0);
+                tma_store_2d(mdu, smem_u32(ob + 1024), ti.n0 + c, (int32_t)row0);
                 bulk_commit();
             }
+        }
+    }
+    return true;
+}
+
+// The same for E2M1, in 32-column chunks: a warp has 64 columns of a tile, so a tile's two chunks are
+// staged whole while its main loop runs; dA and dU take the places of a and u in shared memory and
+// leave from there. (In 16-column chunks with an output buffer beside them, and the correctly rounded
+// quotient, the epilogue set the pace: 632 us with experts of 768, against 703 before that.)
+template <class C>
+__device__ __forceinline__ void au_issue_fp4(const SmemLayout& S, const CUtensorMap* ma,
+                                             const CUtensorMap* mu, int slot, int64_t row0, int col) {
+    bulk_wait_read<0>();  // the previous tile's dA and dU have left
+#pragma unroll
+    for (int b = 0; b < kAuBufs; ++b) {
+        const uint32_t dst = smem_u32(S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES);
+        const uint32_t bar = smem_u32(&S.au_full[slot * kAuBufs + b]);
+        mbar_arrive_expect_tx_relaxed(bar, C::AU_BUF_BYTES);
+        tma_load_2d(dst, ma, bar, col + b * C::AUC, (int32_t)row0);
+        tma_load_2d(dst + C::AU_BUF_BYTES / 2, mu, bar, col + b * C::AUC, (int32_t)row0);
+    }
+}
+
+template <class C>
+__device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileInfo& ti,
+                                               uint32_t t_acc, int q, int lane, int slot, int c_lo,
+                                               const Params& P, const CUtensorMap* mda,
+                                               const CUtensorMap* mdu, uint32_t local,
+                                               volatile int* abort_flag) {
+    const int64_t row0 = ti.m0 + 32 * q;
+    const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
+    const bool store = row0 < ti.row_end;  // as in swiglu_bwd_staged
+    bool ok = true;
+#pragma unroll
+    for (int b = 0; b < kAuBufs; ++b) {
+        const int c = c_lo + b * C::AUC;
+        uint32_t acc[32];
+        tmem_ld32(t_acc + c, acc);
+        ok = mbar_wait_bounded(smem_u32(&S.au_full[slot * kAuBufs + b]), local & 1u, abort_flag,
+                               P.status, P.wait_limit_ns, 34) && ok;
+        tmem_ld_wait();
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (!store || ti.n0 + c >= P.N) continue;  // warp-uniform; N may end inside the last tile
+        uint8_t* abuf = S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES;
+        uint8_t* ubuf = abuf + C::AU_BUF_BYTES / 2;
+        float* r = reinterpret_cast<float*>(acc);
+        if constexpr (C::NV) fp8_scale<32>(r, r, P, row, ti, c, /*dual=*/false);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4* ap = reinterpret_cast<uint4*>(abuf + sw64_offset(lane, j));
+            uint4* up = reinterpret_cast<uint4*>(ubuf + sw64_offset(lane, j));
+            const uint4 a4 = *ap, u4 = *up;
+            const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w};
+            const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
+            float da[8], du[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const float av = (h & 1) ? bf16_hi(aw[h >> 1]) : bf16_lo(aw[h >> 1]);
+                const float uv = (h & 1) ? bf16_hi(uw[h >> 1]) : bf16_lo(uw[h >> 1]);
+                // an approximate quotient (2 ulp); the correctly rounded one: 632 instead of 401 us
+                const float sa = __fdividef(1.0f, 1.0f + __expf(-av));
+                const float dh = r[8 * j + h];
+                da[h] = dh * uv * sa * (1.0f + av * (1.0f - sa));
+                du[h] = dh * av * sa;
+            }
+            *ap = pack_chunk8(da);
+            *up = pack_chunk8(du);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(mda, smem_u32(abuf), ti.n0 + c, (int32_t)row0);
+            tma_store_2d(mdu, smem_u32(ubuf), ti.n0 + c, (int32_t)row0);
+            bulk_commit();
         }
     }
     return true;
@@ -920,10 +1028,7 @@ __device__ __forceinline__ void grouped_gemm_body(
         if constexpr (C::OV > 0)
             mbar_init(smem_u32(S.tshared), 4 * C::OV_GROUPS * (C::PAIR ? 2 : 1));
         if constexpr (C::FP4)
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&S.sfready[b]), 2);  // both copying threads
-                mbar_init(smem_u32(&S.sfempty[b]), 1);
-            }
+            for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&S.sfready[b]), 2);  // both copying threads
         if constexpr (C::AU)
             for (int b = 0; b < C::EW * kAuBufs; ++b) mbar_init(smem_u32(&S.au_full[b]), 1);
         *S.abort_flag = 0;
@@ -991,10 +1096,10 @@ __device__ __forceinline__ void grouped_gemm_body(
             tma_prefetch_desc(msb0);
             if (C::DUAL) tma_prefetch_desc(msb1);
         }
-        int stage = 0;
+        int stage = 0, expert = 0;
         uint32_t phase = 0;
         for (int64_t tile = first_tile; tile < ntiles; tile += tile_step) {
-            const TileInfo ti = decode<C>(tile, P, S, rank);
+            const TileInfo ti = next_tile<C>(tile, expert, P, S, rank);
             bool ok = true;
             for (int kb = 0; kb < ti.k_iters; ++kb) {
                 if (!mbar_wait_bounded(smem_u32(&S.empty[stage]), phase ^ 1u, abort_flag, P.status,
@@ -1031,8 +1136,15 @@ __device__ __forceinline__ void grouped_gemm_body(
         uint32_t phase = 0;
         int local = 0;
         uint32_t blocks = 0;  // K blocks so far (E2M1: buffer and phase of the scales)
+        const uint32_t a_lo0 = desc_lo_sw128(smem_u32(S.a)), b_lo0 = desc_lo_sw128(smem_u32(S.b));
         for (int64_t tile = first_tile; tile < ntiles; tile += tile_step, ++local) {
-            const TileInfo ti = decode<C>(tile, P, S, rank);
+            int k_iters, n0 = 0;
+            if constexpr (C::FP4) {
+                k_iters = (P.K0 + C::KB - 1) / C::KB;
+                if (C::BN % 128) n0 = (int)((uint32_t)tile % (uint32_t)col_tiles<C>(P)) * C::BN;
+            } else {
+                k_iters = decode<C>(tile, P, S, rank).k_iters;
+            }
             const int buf = local & 1;
             const uint32_t use = (local >> 1) & 1;
             if (!mbar_wait_bounded(smem_u32(&S.tempty[buf]), use ^ 1u, abort_flag, P.status,
@@ -1045,30 +1157,38 @@ __device__ __forceinline__ void grouped_gemm_body(
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (buf ? C::ACC1 : C::ACC0);
             bool ok = true;
-            for (int kb = 0; kb < ti.k_iters; ++kb) {
+            for (int kb = 0; kb < k_iters; ++kb) {
                 if (!mbar_wait_bounded(smem_u32(&S.full[stage]), phase, abort_flag, P.status,
                                        P.wait_limit_ns, 32)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t a_s = smem_u32(S.a + (size_t)stage * C::A_BYTES);
-                const uint32_t b_s = smem_u32(S.b + (size_t)stage * C::B_BYTES);
                 if constexpr (C::FP4) {
-                    const int sb = blocks & 1;
-                    if (!mbar_wait_bounded(smem_u32(&S.sfready[sb]), (blocks >> 1) & 1, abort_flag,
-                                           P.status, P.wait_limit_ns, 36)) {
+                    // One thread issues everything, and what it takes to issue a block (two waits,
+                    // four steps, a commit) is near what the block's products take: descriptors
+                    // are one addition each, and a whole block has no branches.
+                    const uint32_t sf = tmem_base + (blocks & 1) * C::SFC;
+                    // 192 columns may begin in the middle of a scale tile: two words (of 32 rows) on
+                    const uint32_t sfb = sf + C::SFK * 4 + (C::BN % 128 ? n0 % 128 / 32 : 0);
+                    const uint32_t a_lo = a_lo0 + stage * (C::A_BYTES / 16);
+                    const uint32_t b_lo = b_lo0 + stage * (C::B_BYTES / 16);
+                    if (!mbar_wait_bounded(smem_u32(&S.sfready[blocks & 1]), (blocks >> 1) & 1,
+                                           abort_flag, P.status, P.wait_limit_ns, 36)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int left = (P.K0 - kb * C::KB) / 64;
-                    issue_mma_fp4<C>(d_tmem, tmem_base + sb * C::SFC, a_s, b_s, left < 4 ? left : 4,
-                                     kb == 0);
-                    if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.sfempty[sb]), 0x1);
-                    else umma_commit(smem_u32(&S.sfempty[sb]));
+                    issue_step_fp4<C, 0>(d_tmem, sf, sfb, a_lo, b_lo, kb > 0);
+                    issue_step_fp4<C, 1>(d_tmem, sf, sfb, a_lo, b_lo, 1);
+                    if (P.K0 - kb * C::KB > 128) {  // K is a multiple of 128
+                        issue_step_fp4<C, 2>(d_tmem, sf, sfb, a_lo, b_lo, 1);
+                        issue_step_fp4<C, 3>(d_tmem, sf, sfb, a_lo, b_lo, 1);
+                    }
                     ++blocks;
                 } else {
+                    const uint32_t a_s = smem_u32(S.a + (size_t)stage * C::A_BYTES);
+                    const uint32_t b_s = smem_u32(S.b + (size_t)stage * C::B_BYTES);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {  // 4 instructions of 32 bytes of K
                         const uint64_t adesc = C::A_MN ? sdesc_sw128(a_s + kk * 2048, 8192, 1024)
@@ -1096,25 +1216,34 @@ __device__ __forceinline__ void grouped_gemm_body(
     } else if (C::FP4 && (warp == 2 || warp == 3) && lane == 0 && leader) {
         // ------------------------------------------------------------ scales to tensor memory
         if constexpr (C::FP4) {
-            int stage = 0;
-            uint32_t phase = 0, blocks = 0;
+            static_assert(C::STAGES >= 3, "a stage's phase while its scales' buffer is awaited");
+            int stage = 0, old_stage = 0;
+            uint32_t phase = 0, old_phase = 0, blocks = 0;
+            const uint32_t sf_lo0 = desc_lo(smem_u32(S.sf));
             bool ok = true;
+            const int k_iters = (P.K0 + C::KB - 1) / C::KB;
             for (int64_t tile = first_tile; ok && tile < ntiles; tile += tile_step) {
-                const TileInfo ti = decode<C>(tile, P, S, rank);
-                for (int kb = 0; kb < ti.k_iters; ++kb, ++blocks) {
-                    const int sb = blocks & 1;
+                for (int kb = 0; kb < k_iters; ++kb, ++blocks) {
+                    // the products that read this buffer's last scales are those of two blocks
+                    // ago, whose end frees their stage: no barrier of its own. (That stage's next
+                    // use ends only after this thread has come past it, so the phase is unique.)
                     ok = mbar_wait_bounded(smem_u32(&S.full[stage]), phase, abort_flag, P.status,
                                            P.wait_limit_ns, 37) &&
-                         mbar_wait_bounded(smem_u32(&S.sfempty[sb]), ((blocks >> 1) & 1) ^ 1u,
-                                           abort_flag, P.status, P.wait_limit_ns, 38);
+                         (blocks < 2 ||
+                          mbar_wait_bounded(smem_u32(&S.empty[old_stage]), old_phase, abort_flag,
+                                            P.status, P.wait_limit_ns, 38));
                     if (!ok) break;
                     tc_fence_after();
                     const int left = (P.K0 - kb * C::KB) / 64;
-                    issue_scales_fp4<C>(tmem_base + sb * C::SFC,
-                                        smem_u32(S.sf + (size_t)stage * C::SF_BYTES),
-                                        left < 4 ? left : 4, warp - 2);
-                    if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.sfready[sb]), 0x1);
-                    else umma_commit(smem_u32(&S.sfready[sb]));
+                    issue_scales_fp4<C>(tmem_base + (blocks & 1) * C::SFC,
+                                        sf_lo0 + stage * (C::SF_BYTES / 16), left < 4 ? left : 4,
+                                        warp - 2);
+                    if constexpr (C::PAIR) umma_commit_pair(smem_u32(&S.sfready[blocks & 1]), 0x1);
+                    else umma_commit(smem_u32(&S.sfready[blocks & 1]));
+                    if (blocks >= 2 && ++old_stage == C::STAGES) {
+                        old_stage = 0;
+                        old_phase ^= 1u;
+                    }
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -1131,20 +1260,30 @@ __device__ __forceinline__ void grouped_gemm_body(
         const int c_lo = ((warp - 4) / 4) * kCols;
         const int slot = warp - 4;
         uint32_t n_au = 0;  // staged a/u chunks consumed by this warp
-        int local = 0;
+        int local = 0, expert = 0;
         for (int64_t tile = first_tile; tile < ntiles; tile += tile_step, ++local) {
-            const TileInfo ti = decode<C>(tile, P, S, rank);
+            const TileInfo ti = next_tile<C>(tile, expert, P, S, rank);
             const int buf = local & 1;
             const uint32_t ph = (local >> 1) & 1;
-            const int group = (warp - 4) / 4;
-            Shared sh{buf == 0,
-                      C::OV && (C::OV_GROUPS == 2 || (buf == 0 ? group == C::EW / 4 - 1 : group == 0)),
-                      C::OV && C::PAIR ? mapa_shared(smem_u32(S.tshared), 0) : smem_u32(S.tshared)};
-            if constexpr (C::AU) {  // this tile's first a/u chunks while the MMA runs
+            Readers rd{};
+            if constexpr (C::FP4) {  // buffer 0 shares its last columns, buffer 1 its first
+                const int group = (warp - 4) / 4;
+                rd.shared = buf == 0 ? group >= C::EW / 4 - C::OV_GROUPS : group < C::OV_GROUPS;
+                rd.shared_bar = smem_u32(S.tshared);
+                rd.whole_bar = smem_u32(&S.tempty[buf]);
+                if constexpr (C::PAIR) {
+                    rd.shared_bar = mapa_shared(rd.shared_bar, 0);
+                    rd.whole_bar = mapa_shared(rd.whole_bar, 0);
+                }
+            }
+            if constexpr (C::AU && C::FP4) {
                 if (lane == 0)
-                    for (int i = 0; i < kAuBufs && i < kCols / C::AUC; ++i)
+                    au_issue_fp4<C>(S, &ma1, &mb1, slot, ti.m0 + 32 * q, ti.n0 + c_lo);
+            } else if constexpr (C::AU) {  // this tile's first a/u chunks while the MMA runs
+                if (lane == 0)
+                    for (int i = 0; i < kAuBufs && i < kCols / kAuCols; ++i)
                         au_issue<C>(S, &ma1, &mb1, slot, n_au + i, ti.m0 + 32 * q,
-                                    ti.n0 + c_lo + au_chunk<C>(i, kCols / C::AUC, sh) * C::AUC);
+                                    ti.n0 + c_lo + i * kAuCols);
             }
             bool ok = mbar_wait_bounded(smem_u32(&S.tfull[buf]), ph, abort_flag, P.status,
                                         P.wait_limit_ns, 33);
@@ -1153,19 +1292,28 @@ __device__ __forceinline__ void grouped_gemm_body(
             tc_fence_after();
             const uint32_t t_acc =
                 tmem_base + (buf ? C::ACC1 : C::ACC0) + ((uint32_t)(32 * q) << 16);
-            if constexpr (C::AU) {
+            if constexpr (C::AU && C::FP4) {
+                if (!swiglu_bwd_fp4<C>(S, ti, t_acc, q, lane, slot, c_lo, P, &mo0, &mo1,
+                                       (uint32_t)local, abort_flag))
+                    break;
+            } else if constexpr (C::AU) {
                 if (!swiglu_bwd_staged<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &ma1, &mb1,
-                                          &mo0, &mo1, n_au, abort_flag, sh))
+                                          &mo0, &mo1, n_au, abort_flag))
                     break;
             } else if constexpr (C::FP4) {
-                epilogue_fp4<C>(S, ti, t_acc, q, lane, slot, c_lo, P, &mo0, &mo1, &mo2, n_au, sh);
+                epilogue_fp4<C>(S, ti, t_acc, lane, slot, c_lo, ti.m0 + 32 * q, P, &mo0, &mo1, &mo2,
+                                buf == 0, rd);
+                continue;
             } else if constexpr (C::TS) {
                 epilogue_tma_store<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &mo0, &mo1, &mo2,
                                       n_au);
             } else {
                 epilogue_wgrad<C>(ti, t_acc, row_in_tile, P, c_lo, c_lo + kCols);
             }
-            report_shared<C>(sh, lane);  // a half past its segment read nothing
+            if constexpr (C::FP4) {
+                arrive_read<C>(rd.whole_bar, lane);
+                continue;
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -1333,7 +1481,7 @@ Params base_params(const int64_t* row_offsets, int64_t rows, int E) {
     return P;
 }
 
-int64_t token_tiles_max(int64_t rows, int N, int BN) { return cdiv(rows, BM) * (N / BN); }
+int64_t token_tiles_max(int64_t rows, int N, int BN) { return cdiv(rows, BM) * cdiv(N, BN); }
 
 bool gemm_shape_ok(int d, int f) { return d % 128 == 0 && f % 128 == 0 && d > 0 && f > 0; }
 
