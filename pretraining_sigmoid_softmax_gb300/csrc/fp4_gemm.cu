@@ -1,26 +1,23 @@
 // The grouped GEMMs on microscaled 4-bit operands (formats: fp4.cuh; kernel template:
 // grouped_gemm.cuh): the plain grouped product, and the experts' forward and backward.
-#include <stdlib.h>
 #include "fp4.cuh"
 #include "grouped_gemm.cuh"
 
 namespace moe {
 namespace {
 
-// Configurations (P: CTA pairs).
+// Configurations, all on CTA pairs. MX stages are smaller, so with one output buffer a warp five of
+// them fit instead of four, which the loads' latency (1.5 us a round of the stages) is worth: down
+// projections of 1536 1544 -> 1270 us, gate and up of 2048 422 -> 371. NV copies twice the scales and
+// is bound by that: two output buffers and four stages (sums of 768: 300 us against 330).
 template <bool NV>
 struct Fp4Gemm {
     static constexpr int QT = NV ? kNvFp4 : kMxFp4;
-#ifndef EWS
-#define EWS 8
-#endif
-#ifndef EWG
-#define EWG 8
-#endif
-    using G1P = Cfg<128, false, false, true, kEpiSwigluFwd, false, false, true, QT, 16, EWG>;
-    using StoreP = Cfg<256, false, false, false, kEpiStore, false, false, true, QT, 16, EWS>;
-    using StoreP192 = Cfg<192, false, false, false, kEpiStore, false, false, true, QT, 16, 12>;
-    using BwdP = Cfg<192, false, false, false, kEpiSwigluBwd, false, false, true, QT, 16, 12>;
+    using G1 = Cfg<128, false, false, true, kEpiSwigluFwd, false, false, true, QT, 16, 8, !NV>;
+    using Store = Cfg<256, false, false, false, kEpiStore, false, false, true, QT, 16, 8, !NV>;
+    // outputs that are no multiple of 256 wide: 192 columns (the last tile clipped)
+    using Store192 = Cfg<192, false, false, false, kEpiStore, false, false, true, QT, 16, 12>;
+    using Bwd = Cfg<192, false, false, false, kEpiSwigluBwd, false, false, true, QT, 16, 12>;
 };
 
 // An operand: codes [rows, K / 2], tiled scales and, in NV, the rows' powers of two.
@@ -46,7 +43,7 @@ bool scale_map(CUtensorMap* m, const uint8_t* s, int K, int64_t rows) {
     if (!enc) return false;
     cuuint64_t dims[2] = {kSfTile / 4, (cuuint64_t)(cdiv(rows, 128) * (K / Fp4<NV>::TILE_K))};
     cuuint64_t strides[1] = {kSfTile};
-    cuuint32_t box[2] = {kSfTile / 4, (cuuint32_t)Fp4Gemm<NV>::StoreP::SFK};
+    cuuint32_t box[2] = {kSfTile / 4, (cuuint32_t)Fp4Gemm<NV>::Store::SFK};
     cuuint32_t es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(s), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -59,11 +56,11 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
             const Operand& W, moe_bf16* Y, const float* r1_row, const float* r1_col, cudaStream_t st) {
     using G = Fp4Gemm<NV>;
     CUtensorMap mx, mw, sf[3], mo[3];
-    const bool wide = getenv("W256") ? atoi(getenv("W256")) : true;
+    const bool wide = N % 256 == 0;
     if (!code_map(&mx, X.q, K, rows) ||
-        !code_map(&mw, W.q, K, (uint64_t)E * N, N % 256 == 0 && wide ? 128 : 96) ||
+        !code_map(&mw, W.q, K, (uint64_t)E * N, wide ? 128 : 96) ||
         !scale_map<NV>(&sf[0], X.s, K, rows) || !scale_map<NV>(&sf[1], W.s, K, (int64_t)E * N) ||
-        !out_maps(mo, Y, nullptr, nullptr, N, rows, G::StoreP::OCOLS))
+        !out_maps(mo, Y, nullptr, nullptr, N, rows, G::Store::OCOLS))
         return MOE_ERR_LAUNCH;
     sf[2] = sf[1];
     Params P = base_params(row_offsets, rows, E);
@@ -73,9 +70,9 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
     P.sb0 = W.g;
     P.r1_row = r1_row;
     P.r1_col = r1_col;
-    if (N % 256 == 0 && wide)
-        return launch<typename G::StoreP>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 256), st, mo, sf);
-    return launch<typename G::StoreP192>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 192), st, mo, sf);
+    if (wide)
+        return launch<typename G::Store>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 256), st, mo, sf);
+    return launch<typename G::Store192>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 192), st, mo, sf);
 }
 
 // a, u = X W_g^T, X W_u^T; h = silu(a) u.
@@ -88,7 +85,7 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
     if (!code_map(&mx, X.q, d, rows) || !code_map(&mg, Wg.q, d, (uint64_t)E * f) ||
         !code_map(&mu, Wu.q, d, (uint64_t)E * f) || !scale_map<NV>(&sf[0], X.s, d, rows) ||
         !scale_map<NV>(&sf[1], Wg.s, d, (int64_t)E * f) || !scale_map<NV>(&sf[2], Wu.s, d, (int64_t)E * f) ||
-        !out_maps(mo, A ? A : H, U ? U : H, H, f, rows, G::G1P::OCOLS))
+        !out_maps(mo, A ? A : H, U ? U : H, H, f, rows, G::G1::OCOLS))
         return MOE_ERR_LAUNCH;
     Params P = base_params(row_offsets, rows, E);
     P.N = f;
@@ -98,7 +95,7 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
     P.sb1 = Wu.g;
     P.row_scale = row_gate;
     P.only_h = A == nullptr;
-    return launch<typename G::G1P>(mx, mx, mg, mu, P, token_tiles_max(rows, f, 128), st, mo, sf);
+    return launch<typename G::G1>(mx, mx, mg, mu, P, token_tiles_max(rows, f, 128), st, mo, sf);
 }
 
 // r = dY W_d; da, du from the saved a and u.
@@ -110,11 +107,11 @@ int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const in
     CUtensorMap my, mw, ma, mu, sf[3], mo[3];
     if (!code_map(&my, dY.q, d, rows) || !code_map(&mw, Wd.q, d, (uint64_t)E * f, 96) ||
         !scale_map<NV>(&sf[0], dY.s, d, rows) || !scale_map<NV>(&sf[1], Wd.s, d, (int64_t)E * f) ||
-        !make_map(&ma, A, f, rows, G::BwdP::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !make_map(&mu, U, f, rows, G::BwdP::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !out_maps(mo, dA, dU, nullptr, f, rows, G::BwdP::OCOLS))
+        !make_map(&ma, A, f, rows, G::Bwd::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&mu, U, f, rows, G::Bwd::AUC, 32, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !out_maps(mo, dA, dU, nullptr, f, rows, G::Bwd::OCOLS))
         return MOE_ERR_LAUNCH;
-    static_assert(G::BwdP::AUC == 32, "64-byte rows of the staged a and u");
+    static_assert(G::Bwd::AUC == 32, "64-byte rows of the staged a and u");
     sf[2] = sf[1];
     Params P = base_params(row_offsets, rows, E);
     P.N = f;
@@ -122,7 +119,7 @@ int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const in
     P.ld_out = f;
     P.sa = dY.g;
     P.sb0 = Wd.g;
-    return launch<typename G::BwdP>(my, ma, mw, mu, P, token_tiles_max(rows, f, 192), st, mo, sf);
+    return launch<typename G::Bwd>(my, ma, mw, mu, P, token_tiles_max(rows, f, 192), st, mo, sf);
 }
 
 int quantize(const moe_bf16* X, const moe_bf16* X1, const int64_t* row_offsets, int E, int64_t rows,

@@ -74,6 +74,7 @@ enum Epi : int { kEpiSwigluFwd = 0, kEpiStore = 1, kEpiSwigluBwd = 2 };
 constexpr int kAuCols = 16;
 constexpr int kAuBufs = 2;
 constexpr int kSmemBudgetAu = 220 * 1024;
+constexpr int kSmemBudgetDeep = 222 * 1024;
 // Token-major epilogues stage their outputs in shared memory, 16 columns x 32 rows per warp
 // and output, and write them with TMA stores: two buffers deep, or one for the SwiGLU
 // backward, whose operand ring then keeps a fifth stage (what bounds it at K = 4096).
@@ -83,7 +84,8 @@ constexpr int kOutCols = 16;
 enum Operands : int { kBf16 = 0, kE4m3 = 1, kMxFp4 = 2, kNvFp4 = 3 };
 
 template <int BN_, bool A_MN_, bool B_MN_, bool DUAL_, int EPI_, bool TWO_K_, bool WGRAD_,
-          bool PAIR_ = false, int QT_ = kBf16, int OC_ = kOutCols, int EW_ = kEpiWarps>
+          bool PAIR_ = false, int QT_ = kBf16, int OC_ = kOutCols, int EW_ = kEpiWarps,
+          bool DEEP_ = false>
 struct Cfg {
     // epilogue warps: 8 (two per TMEM lane quadrant), or 16 for GEMMs whose reduction is so
     // short that the epilogue, not the tensor cores, sets the pace (at most 96 registers); 12
@@ -94,6 +96,7 @@ struct Cfg {
     static constexpr bool FP8 = QT_ == kE4m3;  // E4M3 operands with row / column scales
     static constexpr bool NV = QT_ == kNvFp4;  // E2M1, E4M3 scale per 16, power of two per row
     static constexpr bool FP4 = QT_ == kMxFp4 || NV;
+    static constexpr bool DEEP = DEEP_;  // E2M1: one output buffer a warp, one operand stage more
     static constexpr bool SCALED = FP8 || NV;  // row and column scales applied in the epilogue
     static constexpr int KB = FP4 ? BK_FP4 : FP8 ? BK_FP8 : BK;  // K elements per stage
     static constexpr int BN = BN_;           // output columns per tile (per B matrix if DUAL)
@@ -135,10 +138,11 @@ struct Cfg {
     static constexpr int OUT_BOX_BYTES = 32 * OCOLS * 2;             // one output, one chunk
     static constexpr int OUT_BUF_BYTES = (FP4 && !AU ? 1 : NOUT) * OUT_BOX_BYTES;  // one buffer
     static constexpr int OUT_DEPTH =
-        FP4 ? (EPI == kEpiSwigluFwd ? 3 : AU ? 1 : BN / (EW / 4) / 64)
+        FP4 ? (AU || DEEP || EW != 8 ? 1 : 2)
             : (AU || OCOLS == 32 || EW == 16) ? 1 : 2;  // buffers per warp
     static constexpr int OUT_BYTES = TS && !(FP4 && AU) ? EW * OUT_DEPTH * OUT_BUF_BYTES : 0;
-    static constexpr int BUDGET = (AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
+    static constexpr int BUDGET =
+        (DEEP ? kSmemBudgetDeep : AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
     static constexpr int STAGES = (BUDGET / STAGE_BYTES) > 6 ? 6 : (BUDGET / STAGE_BYTES);
     static constexpr int ACC_COLS = MMA_N;
     // E2M1: the scales of a stage take SFC columns of tensor memory, and two stages' lie at its
@@ -164,11 +168,11 @@ struct Cfg {
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory columns");
     static_assert(BN % 64 == 0 && MMA_N <= 256 && BROWS % (FP4 ? 32 : 64) == 0, "tile width");
     static constexpr size_t MISC_BYTES = 512 + sizeof(int64_t) * (kMaxExperts + 1) +
-                                         sizeof(int32_t) * kMaxExperts +
+                                         (WGRAD || !DEEP ? sizeof(int32_t) * kMaxExperts : 0) +
                                          sizeof(int32_t) * (kMaxExperts + 1);
     static constexpr size_t SMEM_BYTES =
         1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + MISC_BYTES;
-    static_assert((2 * STAGES + 7 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
+    static_assert((3 * STAGES + 7 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
     static_assert(!(OV && AU), "the SwiGLU backward reports no shared columns");
     static_assert(STAGES * SF_BYTES % 1024 == 0, "alignment of what follows the stages");
 
@@ -222,7 +226,8 @@ struct SmemLayout {
     uint64_t* empty;   // STAGES
     uint64_t* tfull;   // 2
     uint64_t* tempty;  // 2
-    uint64_t* sfready; // 2: a stage's scales are in tensor memory (E2M1)
+    uint64_t* sffull;  // STAGES: a stage's scales are in shared memory (E2M1)
+    uint64_t* sfready; // 2: they are in tensor memory
     uint64_t* tshared; // the accumulators' shared columns are read (E2M1)
     uint32_t* tmem_slot;
     int* abort_flag;
@@ -249,13 +254,14 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
     s.tfull = s.empty + C::STAGES;
     s.tempty = s.tfull + 2;
     s.tshared = s.tempty + 2;
-    s.sfready = s.tshared + 1;
+    s.sffull = s.tshared + 1;
+    s.sfready = s.sffull + C::STAGES;
     s.au_full = s.sfready + 2;
     s.tmem_slot = reinterpret_cast<uint32_t*>(s.au_full + (C::AU ? C::EW * kAuBufs : 0));
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
     s.offs = reinterpret_cast<int64_t*>(misc + 512);
     s.order = reinterpret_cast<int32_t*>(s.offs + kMaxExperts + 1);
-    s.ptp = s.order + kMaxExperts;
+    s.ptp = s.order + (C::WGRAD || !C::DEEP ? kMaxExperts : 0);
     return s;
 }
 
@@ -397,7 +403,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
 template <class C>
 __device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint32_t a_dst,
                                                 uint32_t b_dst, uint32_t sf_dst, uint32_t bar,
-                                                const Params& P, const CUtensorMap* ma0,
+                                                uint32_t sf_bar, const Params& P, const CUtensorMap* ma0,
                                                 const CUtensorMap* mb0, const CUtensorMap* mb1,
                                                 const CUtensorMap* msa, const CUtensorMap* msb0,
                                                 const CUtensorMap* msb1, uint32_t rank) {
@@ -405,6 +411,12 @@ __device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint
     const int32_t ktiles = P.K0 / (C::KB / C::SFK);  // scale tiles along K
     const int32_t kt = kb * C::SFK;
     const int32_t brow = ti.e * P.N + ti.n0;  // N is a multiple of 128, n0 at least of 64
+    // the scales first: they are copied on while the operands still arrive
+    tma_load<C>(sf_dst, msa, sf_bar, 0, (int32_t)(ti.m0 / BM) * ktiles + kt);
+#pragma unroll
+    for (int h = 0; h < C::SFB_TILES; ++h)
+        tma_load<C>(sf_dst + (1 + h) * C::SFA_BYTES, C::DUAL && h == 1 ? msb1 : msb0, sf_bar, 0,
+                    (brow / BM + (C::DUAL ? 0 : h)) * ktiles + kt);
     tma_load<C>(a_dst, ma0, bar, kbyte, (int32_t)ti.m0);
     if constexpr (C::DUAL) {
         if constexpr (C::PAIR) {
@@ -416,11 +428,6 @@ __device__ __forceinline__ void issue_loads_fp4(const TileInfo& ti, int kb, uint
     } else {
         tma_load<C>(b_dst, mb0, bar, kbyte, brow + (C::PAIR ? (int32_t)rank * C::BROWS : 0));
     }
-    tma_load<C>(sf_dst, msa, bar, 0, (int32_t)(ti.m0 / BM) * ktiles + kt);
-#pragma unroll
-    for (int h = 0; h < C::SFB_TILES; ++h)
-        tma_load<C>(sf_dst + (1 + h) * C::SFA_BYTES, C::DUAL && h == 1 ? msb1 : msb0, bar, 0,
-                    (brow / BM + (C::DUAL ? 0 : h)) * ktiles + kt);
 }
 
 // The scales of one E2M1 K block of `steps` steps of 64 into tensor memory (column tmem_sf on): tiles
@@ -726,40 +733,40 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
         tmem_ld_wait();
         if (C::OV && rd.shared) arrive_read<C>(rd.shared_bar, lane);
         arrive_read<C>(rd.whole_bar, lane);
-        if (lane == 0) bulk_wait_read<0>();  // the previous tile's boxes have left
-        __syncwarp();
         const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
+        if constexpr (C::NV)
 #pragma unroll
-        for (int k = 0; k < kHalves; ++k) {
-            float* gf = reinterpret_cast<float*>(g[k]);
-            float* uf = reinterpret_cast<float*>(u[k]);
-            if constexpr (C::NV) fp8_scale<32>(gf, uf, P, row, ti, c_lo + 32 * k);
-            uint32_t w[16];
-            if (!P.only_h) {
+            for (int k = 0; k < kHalves; ++k)
+                fp8_scale<32>(reinterpret_cast<float*>(g[k]), reinterpret_cast<float*>(u[k]), P, row, ti,
+                              c_lo + 32 * k);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(gf[2 * j], gf[2 * j + 1]);
-                put_half<C>(buf, lane, k, w);
+        for (int o = 0; o < 3; ++o) {  // a, u, h
+            if (o < 2 && P.only_h) continue;
+            uint8_t* box = buf + o % C::OUT_DEPTH * C::OUT_BUF_BYTES;
+            if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();  // its last store has read it
+            __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(uf[2 * j], uf[2 * j + 1]);
-                put_half<C>(buf + C::OUT_BUF_BYTES, lane, k, w);
+            for (int k = 0; k < kHalves; ++k) {
+                const float* gf = reinterpret_cast<const float*>(g[k]);
+                const float* uf = reinterpret_cast<const float*>(u[k]);
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float g0 = gf[2 * j], g1 = gf[2 * j + 1];
+                    const float u0 = uf[2 * j], u1 = uf[2 * j + 1];
+                    w[j] = o == 0   ? pack_bf16x2(g0, g1)
+                           : o == 1 ? pack_bf16x2(u0, u1)
+                                    : pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * u0 * rg,
+                                                  __fdividef(g1, 1.0f + __expf(-g1)) * u1 * rg);
+                }
+                put_half<C>(box, lane, k, w);
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float g0 = gf[2 * j], g1 = gf[2 * j + 1];
-                w[j] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * uf[2 * j] * rg,
-                                   __fdividef(g1, 1.0f + __expf(-g1)) * uf[2 * j + 1] * rg);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(o == 0 ? mo0 : o == 1 ? mo1 : mo2, smem_u32(box), ti.n0 + c_lo, (int32_t)row0);
+                bulk_commit();
             }
-            put_half<C>(buf + 2 * C::OUT_BUF_BYTES, lane, k, w);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (!P.only_h) {
-                tma_store_2d(mo0, smem_u32(buf), ti.n0 + c_lo, (int32_t)row0);
-                tma_store_2d(mo1, smem_u32(buf + C::OUT_BUF_BYTES), ti.n0 + c_lo, (int32_t)row0);
-            }
-            tma_store_2d(mo2, smem_u32(buf + 2 * C::OUT_BUF_BYTES), ti.n0 + c_lo, (int32_t)row0);
-            bulk_commit();
         }
     } else {
         // halves of 32 columns in order, or (buffer 0 of accumulators that share columns) the last
@@ -785,7 +792,7 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
                     if (kAhead < kHalves && i + 2 == kHalves) arrive_read<C>(rd.whole_bar, lane);
                 }
                 // the store that last read this buffer is done
-                if (lane == 0) bulk_wait_read<kHalves / 2 - 1>();
+                if (lane == 0) bulk_wait_read<C::OUT_DEPTH - 1>();
                 __syncwarp();
             }
             float* v = reinterpret_cast<float*>(r[i]);
@@ -794,7 +801,7 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            uint8_t* box = buf + i / 2 * C::OUT_BUF_BYTES;
+            uint8_t* box = buf + i / 2 % C::OUT_DEPTH * C::OUT_BUF_BYTES;
             put_half<C>(box, lane, half(i) & 1, w);
             if (i % 2 == 1) {
                 fence_async_smem();
@@ -1027,8 +1034,10 @@ __device__ __forceinline__ void grouped_gemm_body(
         }
         if constexpr (C::OV > 0)
             mbar_init(smem_u32(S.tshared), 4 * C::OV_GROUPS * (C::PAIR ? 2 : 1));
-        if constexpr (C::FP4)
+        if constexpr (C::FP4) {
+            for (int s = 0; s < C::STAGES; ++s) mbar_init(smem_u32(&S.sffull[s]), 1);
             for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&S.sfready[b]), 2);  // both copying threads
+        }
         if constexpr (C::AU)
             for (int b = 0; b < C::EW * kAuBufs; ++b) mbar_init(smem_u32(&S.au_full[b]), 1);
         *S.abort_flag = 0;
@@ -1111,17 +1120,20 @@ __device__ __forceinline__ void grouped_gemm_body(
                 uint32_t bar = full;
                 if constexpr (C::PAIR) {
                     bar = mapa_shared(full, 0);  // both CTAs' copies complete on the leader's
-                    if (leader) mbar_arrive_expect_tx(full, 2 * C::STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(full, 2 * (C::STAGE_BYTES - C::SF_BYTES));
                 } else {
-                    mbar_arrive_expect_tx(full, C::STAGE_BYTES);
+                    mbar_arrive_expect_tx(full, C::STAGE_BYTES - C::SF_BYTES);
                 }
                 const uint32_t a_dst = smem_u32(S.a + (size_t)stage * C::A_BYTES);
                 const uint32_t b_dst = smem_u32(S.b + (size_t)stage * C::B_BYTES);
-                if constexpr (C::FP4)
+                if constexpr (C::FP4) {
+                    uint32_t sf_bar = smem_u32(&S.sffull[stage]);
+                    if (leader) mbar_arrive_expect_tx(sf_bar, (C::PAIR ? 2 : 1) * C::SF_BYTES);
+                    if constexpr (C::PAIR) sf_bar = mapa_shared(sf_bar, 0);
                     issue_loads_fp4<C>(ti, kb, a_dst, b_dst,
-                                       smem_u32(S.sf + (size_t)stage * C::SF_BYTES), bar, P, &ma0,
-                                       &mb0, &mb1, msa, msb0, msb1, rank);
-                else
+                                       smem_u32(S.sf + (size_t)stage * C::SF_BYTES), bar, sf_bar, P,
+                                       &ma0, &mb0, &mb1, msa, msb0, msb1, rank);
+                } else
                     issue_loads<C>(ti, kb, a_dst, b_dst, bar, P, &ma0, &ma1, &mb0, &mb1, rank);
                 if (++stage == C::STAGES) {
                     stage = 0;
@@ -1227,7 +1239,7 @@ __device__ __forceinline__ void grouped_gemm_body(
                     // the products that read this buffer's last scales are those of two blocks
                     // ago, whose end frees their stage: no barrier of its own. (That stage's next
                     // use ends only after this thread has come past it, so the phase is unique.)
-                    ok = mbar_wait_bounded(smem_u32(&S.full[stage]), phase, abort_flag, P.status,
+                    ok = mbar_wait_bounded(smem_u32(&S.sffull[stage]), phase, abort_flag, P.status,
                                            P.wait_limit_ns, 37) &&
                          (blocks < 2 ||
                           mbar_wait_bounded(smem_u32(&S.empty[old_stage]), old_phase, abort_flag,
