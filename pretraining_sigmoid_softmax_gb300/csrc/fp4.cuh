@@ -76,6 +76,19 @@ struct MxScale {
     }
 };
 
+// The code bytes and the scale byte of an MX block given as 16 packed bf16 pairs.
+__device__ __forceinline__ uint32_t mx_block(const uint32_t (&w)[16], uint4& codes) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = absmax2(m, w[j]);
+    const MxScale sc(halves_max(m));
+    codes = make_uint4(sc.codes(make_uint4(w[0], w[1], w[2], w[3])),
+                       sc.codes(make_uint4(w[4], w[5], w[6], w[7])),
+                       sc.codes(make_uint4(w[8], w[9], w[10], w[11])),
+                       sc.codes(make_uint4(w[12], w[13], w[14], w[15])));
+    return sc.byte;
+}
+
 // The power of two of an NV row whose largest magnitude has the bf16 bits `top`: 2688 is
 // 1.3125 * 2^11, and bf16's seven fraction bits of 1.3125 are 40.
 struct NvRow {

@@ -78,8 +78,8 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
 // a, u = X W_g^T, X W_u^T; h = silu(a) u.
 template <bool NV>
 int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, int d, int f,
-           const Operand& Wg, const Operand& Wu, moe_bf16* A, moe_bf16* U, moe_bf16* H,
-           const float* row_gate, cudaStream_t st) {
+           const Operand& Wg, const Operand& Wu, moe_bf16* A, moe_bf16* U, moe_bf16* H, uint8_t* Hq,
+           uint8_t* sH, const float* row_gate, cudaStream_t st) {
     using G = Fp4Gemm<NV>;
     CUtensorMap mx, mg, mu, sf[3], mo[3];
     if (!code_map(&mx, X.q, d, rows) || !code_map(&mg, Wg.q, d, (uint64_t)E * f) ||
@@ -95,6 +95,8 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
     P.sb1 = Wu.g;
     P.row_scale = row_gate;
     P.only_h = A == nullptr;
+    P.oq = Hq;
+    P.os = sH;
     return launch<typename G::G1>(mx, mx, mg, mu, P, token_tiles_max(rows, f, 128), st, mo, sf);
 }
 
@@ -102,7 +104,7 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
 template <bool NV>
 int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const int64_t* row_offsets,
                int E, int64_t rows, int d, int f, const Operand& Wd, moe_bf16* dA, moe_bf16* dU,
-               cudaStream_t st) {
+               uint8_t* AUq, uint8_t* sAU, cudaStream_t st) {
     using G = Fp4Gemm<NV>;
     CUtensorMap my, mw, ma, mu, sf[3], mo[3];
     if (!code_map(&my, dY.q, d, rows) || !code_map(&mw, Wd.q, d, (uint64_t)E * f, 96) ||
@@ -119,6 +121,8 @@ int swiglu_bwd(const Operand& dY, const moe_bf16* A, const moe_bf16* U, const in
     P.ld_out = f;
     P.sa = dY.g;
     P.sb0 = Wd.g;
+    P.oq = AUq;
+    P.os = sAU;
     return launch<typename G::Bwd>(my, ma, mw, mu, P, token_tiles_max(rows, f, 192), st, mo, sf);
 }
 
@@ -170,10 +174,10 @@ extern "C" int moe_expert_fwd_fp4(const uint8_t* Xq, const uint8_t* sX, const fl
     if (!device_status_word()) return MOE_ERR_LAUNCH;
     cudaStream_t st = (cudaStream_t)stream;
     const bool nv = fmt == MOE_FP4_NV;
-    int rc = nv ? swiglu<true>(X, row_offsets, E, rows, d, f, Wg, Wu, A, U, H, row_gate, st)
-                : swiglu<false>(X, row_offsets, E, rows, d, f, Wg, Wu, A, U, H, row_gate, st);
-    if (rc != MOE_OK) return rc;
-    rc = quantize(H, nullptr, row_offsets, E, rows, f, fmt, Hq, sH, gH, st);
+    // MX: the epilogue has whole blocks of h and forms their codes; NV needs the whole row first
+    int rc = nv ? swiglu<true>(X, row_offsets, E, rows, d, f, Wg, Wu, A, U, H, nullptr, nullptr, row_gate, st)
+                : swiglu<false>(X, row_offsets, E, rows, d, f, Wg, Wu, A, U, H, Hq, sH, row_gate, st);
+    if (rc == MOE_OK && nv) rc = quantize(H, nullptr, row_offsets, E, rows, f, fmt, Hq, sH, gH, st);
     if (rc != MOE_OK) return rc;
     return nv ? product<true>(Hc, row_offsets, E, rows, f, d, Wd, Y, nullptr, nullptr, st)
               : product<false>(Hc, row_offsets, E, rows, f, d, Wd, Y, nullptr, nullptr, st);
@@ -212,13 +216,16 @@ extern "C" int moe_expert_bwd_fp4(const uint8_t* dYq, const uint8_t* sdY, const 
     cudaStream_t st = (cudaStream_t)stream;
     const bool nv = fmt == MOE_FP4_NV;
     int rc = MOE_OK;
+    // MX: dA's and dU's codes are formed where they are written, if this call goes on to use them
+    const bool formed = !nv && (parts & MOE_BWD_DH) && (parts & MOE_BWD_DX);
     if (parts & MOE_BWD_DH) {
-        rc = nv ? swiglu_bwd<true>(dYc, A, U, row_offsets, E, rows, d, f, Wd, dA, dU, st)
-                : swiglu_bwd<false>(dYc, A, U, row_offsets, E, rows, d, f, Wd, dA, dU, st);
+        rc = nv ? swiglu_bwd<true>(dYc, A, U, row_offsets, E, rows, d, f, Wd, dA, dU, nullptr, nullptr, st)
+                : swiglu_bwd<false>(dYc, A, U, row_offsets, E, rows, d, f, Wd, dA, dU,
+                                    formed ? AUq : nullptr, formed ? sAU : nullptr, st);
         if (rc != MOE_OK) return rc;
     }
     if (parts & MOE_BWD_DX) {
-        rc = quantize(dA, dU, row_offsets, E, rows, f, fmt, AUq, sAU, gAU, st);
+        if (!formed) rc = quantize(dA, dU, row_offsets, E, rows, f, fmt, AUq, sAU, gAU, st);
         if (rc != MOE_OK) return rc;
         rc = nv ? product<true>(AU, row_offsets, E, rows, 2 * f, d, Wgu, dX, dl_rows, W_r, st)
                 : product<false>(AU, row_offsets, E, rows, 2 * f, d, Wgu, dX, dl_rows, W_r, st);

@@ -53,6 +53,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "sizes.h"
 #include "tmap.h"
 
@@ -204,6 +205,10 @@ struct Params {
     const float* r1_row;
     const float* r1_col;
     bool only_h;               // E2M1 G1: h alone is written (nothing is kept for a backward)
+    // MX: the operand of the bf16 outputs, formed from them in the epilogue (G1: of h; B2: of
+    // [dA | dU]): codes and scale tiles, or null
+    uint8_t* oq;
+    uint8_t* os;
     int* status;
     uint64_t wait_limit_ns;
 };
@@ -691,6 +696,17 @@ __device__ __forceinline__ void put_half(uint8_t* buf, int lane, int half, const
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
+// An MX block (32 packed columns from `col` on, of this thread's row) to its codes and its scale in an
+// operand of `cols` columns, as quantising the stored bf16 row does. A warp writes half a sector of
+// codes and a byte of a scale word a row; the second block of the two that a warp has fills both.
+__device__ __forceinline__ void store_mx_block(const uint32_t (&w)[16], uint8_t* q, uint8_t* s, int cols,
+                                               int64_t row, int col) {
+    uint4 codes;
+    const uint32_t byte = mx_block(w, codes);
+    *reinterpret_cast<uint4*>(q + row * (cols / 2) + col / 2) = codes;
+    s[fp4_scale_word(row, col / 128, cols / 128) + col % 128 / 32] = (uint8_t)byte;
+}
+
 // Arrivals at the leading CTA's barriers (this CTA's, outside pairs) that a warp's reads are over: of
 // the columns shared with the next tile's accumulator, and of the whole one.
 struct Readers {
@@ -760,6 +776,8 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
                                                   __fdividef(g1, 1.0f + __expf(-g1)) * u1 * rg);
                 }
                 put_half<C>(box, lane, k, w);
+                if (!C::NV && o == 2 && P.oq && row0 + lane < ti.row_end)
+                    store_mx_block(w, P.oq, P.os, P.N, row, ti.n0 + c_lo + 32 * k);
             }
             fence_async_smem();
             __syncwarp();
@@ -976,6 +994,7 @@ __device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileIn
         uint8_t* ubuf = abuf + C::AU_BUF_BYTES / 2;
         float* r = reinterpret_cast<float*>(acc);
         if constexpr (C::NV) fp8_scale<32>(r, r, P, row, ti, c, /*dual=*/false);
+        uint32_t wa[16], wu[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4* ap = reinterpret_cast<uint4*>(abuf + sw64_offset(lane, j));
@@ -994,8 +1013,15 @@ __device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileIn
                 da[h] = dh * uv * sa * (1.0f + av * (1.0f - sa));
                 du[h] = dh * av * sa;
             }
-            *ap = pack_chunk8(da);
-            *up = pack_chunk8(du);
+            const uint4 pa = pack_chunk8(da), pu = pack_chunk8(du);
+            *ap = pa;
+            *up = pu;
+            wa[4 * j] = pa.x, wa[4 * j + 1] = pa.y, wa[4 * j + 2] = pa.z, wa[4 * j + 3] = pa.w;
+            wu[4 * j] = pu.x, wu[4 * j + 1] = pu.y, wu[4 * j + 2] = pu.z, wu[4 * j + 3] = pu.w;
+        }
+        if (!C::NV && P.oq && row0 + lane < ti.row_end) {  // the halves of [dA | dU]
+            store_mx_block(wa, P.oq, P.os, 2 * P.N, row, ti.n0 + c);
+            store_mx_block(wu, P.oq, P.os, 2 * P.N, row, P.N + ti.n0 + c);
         }
         fence_async_smem();
         __syncwarp();
