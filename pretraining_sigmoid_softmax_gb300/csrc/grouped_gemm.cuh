@@ -50,6 +50,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -60,6 +61,7 @@
 namespace moe {
 namespace {
 
+constexpr int kMaxDevices = 64;  // as the status words
 constexpr int BM = 128;
 constexpr int BK = 64;        // bf16 K elements per stage (128 bytes per row)
 constexpr int BK_FP8 = 128;   // E4M3 K elements per stage (also 128 bytes per row)
@@ -1466,8 +1468,15 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
         if constexpr (C::FP4) return grouped_gemm_fp4_kernel<C>;
         else return grouped_gemm_kernel<C>;
     }();
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)C::SMEM_BYTES) != cudaSuccess)
+    // What the runtime says of a kernel on a device does not change: asked once for each. (E2M1; a call
+    // for one token is mostly the host's work.)
+    static std::atomic<int> resident[C::FP4 ? kMaxDevices : 1];
+    int dev = 0;
+    if (C::FP4 && (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices))
+        return MOE_ERR_LAUNCH;
+    int clusters = C::FP4 ? resident[dev].load(std::memory_order_acquire) : 0;
+    if (clusters == 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (int)C::SMEM_BYTES) != cudaSuccess)
         return MOE_ERR_LAUNCH;
     if constexpr (C::PAIR) {
         cudaLaunchConfig_t cfg = {};
@@ -1482,9 +1491,11 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
-        int clusters = 0;  // pairs that fit on the GPU at once (one CTA per SM)
-        if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1)
-            clusters = sm_count() / 2;
+        if (clusters == 0) {  // pairs that fit on the GPU at once (one CTA per SM)
+            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1)
+                clusters = sm_count() / 2;
+            if (C::FP4) resident[dev].store(clusters, std::memory_order_release);
+        }
         int64_t pairs = clusters;
         if (max_tiles < pairs) pairs = max_tiles;
         if (pairs < 1) pairs = 1;

@@ -609,10 +609,23 @@ def _fp4(name, m, shape, fmt, dev):
         raise MoEError(f"{name} is missing")
     if m.fmt != fmt:
         raise MoEError(f"{name} has format {m.fmt}, the call's is {fmt}")
-    *lead, cols = shape
-    rows = 1
-    for n in lead:
-        rows *= n
+    if len(shape) == 2:
+        lead, rows, cols = shape[:1], shape[0], shape[1]
+    else:
+        lead, rows, cols = shape[:2], shape[0] * shape[1], shape[2]
+    # one check for all that is as it should be; what follows says what is not
+    q, s, g = m.q, m.s, m.g
+    u8 = torch.uint8
+    if (cols % 128 == 0 and rows > 0 and q.dtype is u8 and q.shape == (*lead, cols // 2)
+            and q.is_contiguous() and q.get_device() == dev and s.dtype is u8 and s.dim() == 1
+            and s.numel() == (rows + 127) // 128 * cols * (8 if fmt == FP4_NV else 4)
+            and s.is_contiguous() and s.get_device() == dev):
+        if g is None:
+            if fmt == FP4_MX:
+                return q.data_ptr(), s.data_ptr(), None
+        elif (fmt == FP4_NV and g.dtype is torch.float32 and g.shape == (rows,)
+              and g.is_contiguous() and g.get_device() == dev):
+            return q.data_ptr(), s.data_ptr(), g.data_ptr()
     g = None
     if fmt == FP4_NV:
         g = _ptr(f"{name}.g", m.g, torch.float32, (rows,), dev)
@@ -634,9 +647,10 @@ def _fp4_stack(name, m):
     """The number of matrices and the rows of a 3-D operand."""
     if m is None:
         raise MoEError(f"{name} is missing")
-    if m.q.dim() != 3:
-        raise MoEError(f"{name}.q must be [E, rows, cols / 2], got shape {tuple(m.q.shape)}")
-    return m.q.shape[0], m.q.shape[1]
+    shape = m.q.shape
+    if len(shape) != 3:
+        raise MoEError(f"{name}.q must be [E, rows, cols / 2], got shape {tuple(shape)}")
+    return shape[0], shape[1]
 
 
 def _offsets(row_offsets, E, dev):
@@ -676,11 +690,14 @@ def moe_quantize_cols_fp4(X0, X1, out, stream=None):
 
 def moe_dequantize_fp4(m, out, rows_limit=None, stream=None):
     """The numbers an operand stands for, as bf16 in ``out`` (of its rows and columns)."""
-    half = m.q.shape[-1]
-    rows = m.q.numel() // max(half, 1)
+    shape = m.q.shape
+    if len(shape) not in (2, 3):
+        raise MoEError(f"m.q must be [rows, cols / 2] or [E, rows, cols / 2], got shape {tuple(shape)}")
+    half = shape[-1]
+    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     dev = _device(m.q)
-    q, s, g = _fp4("m", m, (*m.q.shape[:-1], 2 * half), m.fmt, dev)
-    if out is not None and out.dim() >= 2 and out.is_contiguous():
+    q, s, g = _fp4("m", m, (*shape[:-1], 2 * half), m.fmt, dev)
+    if out is not None and out.dim() == 3 and out.is_contiguous():
         out = out.view(-1, out.shape[-1])
     _check(_lib.load().moe_dequantize_fp4(q, s, g, _limit(rows_limit, dev), rows, 2 * half, m.fmt,
                                           _ptr("out", out, torch.bfloat16, (rows, 2 * half), dev),
