@@ -13,29 +13,31 @@ constexpr int kThreads = 256;
 
 // Rows. A thread takes 16 consecutive elements (32 bytes) at a time and keeps up to NIT such
 // pieces in registers, so that a row is read once although its largest value (NV) is needed
-// first. WPR warps share a row. Blocks of 16 lie in one thread, blocks of 32 in two; the four
+// first. TPR threads share a row. Blocks of 16 lie in one thread, blocks of 32 in two; the four
 // scales of a tile's row are put together by shuffles and stored as one word.
-template <bool NV, int WPR, int NIT>
+// 65,535 x 4096 (MX): 107 us, 0.94 of the copy rate over 0.68 GB.
+template <bool NV, int TPR, int NIT>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
     const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ X1,
     const int64_t* __restrict__ limit, int64_t rows, int cols, uint8_t* __restrict__ Q,
     uint8_t* __restrict__ S, float* __restrict__ G) {
-    constexpr int ROWS = kThreads / 32 / WPR;  // rows a CTA takes at a time
-    __shared__ uint32_t part[NV && WPR > 1 ? kThreads / 32 : 1];
+    constexpr int ROWS = kThreads / TPR;  // rows a CTA takes at a time
+    static_assert(TPR <= 32 || TPR == kThreads, "a row in one warp or in the whole CTA");
+    __shared__ uint32_t part[NV && TPR > 32 ? kThreads / 32 : 1];
     const int lane = threadIdx.x % 32;
-    const int t = threadIdx.x % (32 * WPR);
+    const int t = threadIdx.x % TPR;
     const int np0 = cols / 16;                 // pieces of X's row
     const int np = X1 ? 2 * np0 : np0;
     const int64_t ktiles = np * 16 / Fp4<NV>::TILE_K;
     int64_t n = rows;
     if (limit) n = min(n, *limit);
     for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < n; r0 += (int64_t)gridDim.x * ROWS) {
-        const int64_t r = r0 + threadIdx.x / (32 * WPR);
+        const int64_t r = r0 + threadIdx.x / TPR;
         const bool in_row = r < n;
         uint4 v[NIT][2];
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int p = t + i * 32 * WPR;
+            const int p = t + i * TPR;
             v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
             if (in_row && p < np) {
                 const __nv_bfloat16* src = p < np0 ? X + r * cols + 16 * p
@@ -51,12 +53,18 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
         if constexpr (NV) {
 #pragma unroll
             for (int i = 0; i < NIT; ++i) top = max(top, am[i]);
-            top = __reduce_max_sync(0xffffffffu, top);
-            if constexpr (WPR > 1) {
+            if constexpr (TPR >= 32) {
+                top = __reduce_max_sync(0xffffffffu, top);
+            } else {
+#pragma unroll
+                for (int o = TPR / 2; o > 0; o >>= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            if constexpr (TPR > 32) {
                 if (lane == 0) part[threadIdx.x / 32] = top;
                 __syncthreads();
 #pragma unroll
-                for (int w = 0; w < WPR; ++w) top = max(top, part[threadIdx.x / (32 * WPR) * WPR + w]);
+                for (int w = 0; w < kThreads / 32; ++w) top = max(top, part[w]);
                 __syncthreads();
             }
         }
@@ -64,8 +72,8 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
         if (NV && in_row && t == 0) G[r] = row.g;
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int p = t + i * 32 * WPR;
-            if (i * 32 * WPR >= np) break;  // the same for the whole CTA
+            const int p = t + i * TPR;
+            if (i * TPR >= np) break;  // the same for the whole CTA
             uint2 code;
             uint32_t word;
             if constexpr (NV) {
@@ -92,40 +100,55 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
 }
 
 // The numbers that codes stand for: E2M1 * scale (* g), one rounding to bf16, which is exact (the
-// product has at most 6 significant bits) unless it leaves bf16's range.
-template <bool NV>
+// product has at most 6 significant bits) unless it leaves bf16's range. A thread makes 8 numbers,
+// 16 bytes, so that a warp's store is one run of 512 (with 32 bytes a thread the two stores of a
+// sector's halves made 65,535 x 4096 134 us). `Index` counts pieces of 8; 32 bits where they do.
+template <bool NV, class Index>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(
     const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S, const float* __restrict__ G,
     const int64_t* __restrict__ limit, int64_t rows, int cols, __nv_bfloat16* __restrict__ out) {
-    const int np = cols / 16;
+    const Index np = cols / 8;
     const int64_t ktiles = cols / Fp4<NV>::TILE_K;
-    constexpr int PT = Fp4<NV>::TILE_K / 16;
+    constexpr int PB = Fp4<NV>::BLOCK / 8;  // pieces of a block
+    constexpr int U = 4;                    // pieces a thread has in flight
     int64_t n = rows;
     if (limit) n = min(n, *limit);
     const int64_t total = n * np;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = i / np;
-        const int p = (int)(i - r * np);
-        const uint2 code = reinterpret_cast<const uint2*>(Q)[i];
-        const uint32_t byte = S[fp4_scale_word(r, p / PT, ktiles) + p % PT / (PT / 4)];
-        float s;
-        if constexpr (NV)
-            s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3))) * G[r];
-        else
-            s = byte == 255 ? __uint_as_float(0x7fffffffu)
-                            : byte ? __uint_as_float(byte << 23) : __uint_as_float(1u << 22);
-        uint32_t w[8];
+    for (int64_t i0 = (int64_t)blockIdx.x * kThreads * U + threadIdx.x; i0 < total;
+         i0 += (int64_t)gridDim.x * kThreads * U) {
+        uint32_t code[U], byte[U];
+        float g[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = ((j < 4 ? code.x : code.y) >> (8 * (j & 3))) & 0xffu;
-            const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)b, __NV_E2M1));
-            const float2 f = __half22float2(h);
-            w[j] = pack_bf16x2(f.x * s, f.y * s);
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kThreads;
+            code[u] = byte[u] = 0;
+            g[u] = 1.0f;
+            if (i >= total) continue;
+            const Index r = (Index)i / np, p = (Index)i - r * np;
+            code[u] = reinterpret_cast<const uint32_t*>(Q)[i];
+            byte[u] = S[fp4_scale_word(r, p / (4 * PB), ktiles) + p / PB % 4];
+            if (NV) g[u] = G[r];
         }
-        uint4* dst = reinterpret_cast<uint4*>(out) + 2 * i;
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kThreads;
+            if (i >= total) break;
+            float s;
+            if constexpr (NV)
+                s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte[u], __NV_E4M3))) * g[u];
+            else
+                s = byte[u] == 255 ? __uint_as_float(0x7fffffffu)
+                                   : byte[u] ? __uint_as_float(byte[u] << 23) : __uint_as_float(1u << 22);
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t b = (code[u] >> (8 * j)) & 0xffu;
+                const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)b, __NV_E2M1));
+                const float2 f = __half22float2(h);
+                w[j] = pack_bf16x2(f.x * s, f.y * s);
+            }
+            reinterpret_cast<uint4*>(out)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
@@ -133,35 +156,159 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(
 // X is E matrices of K x N bf16, or, with X1, the K = 2 K0 stack of X0 over X1. Column n's codes
 // are written as row e N + n of the operand, K-major, its blocks along K.
 
-// NV: largest magnitude of each column (as bits, which order as the magnitudes do; `top` starts at
-// zero): a thread takes 8 columns and kTopRows rows.
-constexpr int kTopThreads = 128;
-constexpr int kTopRows = 128;
+// A CTA takes a strip of NC columns and KT rows through shared memory: all K rows in NV, whose columns'
+// largest values are needed first, so that X is read once; 256 rows in MX. A thread then makes the
+// codes of 32 K elements of one column (16 bytes: one block of 32 or two of 16), which go back
+// through shared memory to leave as whole lines. NV operands whose strips are too long for that
+// (K over kStripMaxK) get the columns' largest values from a pass of its own.
+constexpr int kStripRowsMx = 256;
+constexpr int kStripMaxK = 3328;
 
-__global__ void __launch_bounds__(kTopThreads) column_top_kernel(const __nv_bfloat16* __restrict__ X0,
-                                                                 const __nv_bfloat16* __restrict__ X1,
-                                                                 int K0, int N,
-                                                                 uint32_t* __restrict__ top) {
+// One row of a strip in shared memory: NC columns, padded so that consecutive rows start in other banks.
+template <int NC>
+struct Strip {
+    static constexpr int PITCH = NC + 2;  // 16-bit elements
+};
+
+template <bool NV, int NC>
+__global__ void __launch_bounds__(kThreads) quantize_cols_kernel(
+    const __nv_bfloat16* __restrict__ X0, const __nv_bfloat16* __restrict__ X1, int K0, int N, int KT,
+    uint8_t* __restrict__ Qt, uint8_t* __restrict__ S, float* __restrict__ G, bool have_top) {
+    extern __shared__ __align__(16) uint8_t strip_smem[];
+    constexpr int P = Strip<NC>::PITCH;
+    constexpr int WORD_K = Fp4<NV>::TILE_K;
+    uint16_t* tile = reinterpret_cast<uint16_t*>(strip_smem);  // [KT][P]
+    __shared__ uint32_t top[NC];
+    const int K = X1 ? 2 * K0 : K0;
+    const int e = blockIdx.z, n0 = blockIdx.x * NC, k0 = blockIdx.y * KT;
+    const int kn = min(KT, K - k0);  // a multiple of 128
+    if (NV && threadIdx.x < NC) top[threadIdx.x] = have_top ? __float_as_uint(G[(int64_t)e * N + n0 + threadIdx.x]) : 0u;
+    if (NV) __syncthreads();
+    // in: 16 bytes (8 columns) a thread and row
+    constexpr int V = NC / 8;
+    const int c8 = threadIdx.x % V;
+    uint4 m = make_uint4(0, 0, 0, 0);
+    constexpr int U = 8;  // rows a thread has in flight
+    for (int r0 = threadIdx.x / V; r0 < kn; r0 += U * (kThreads / V)) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * (kThreads / V), k = k0 + r;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (r < kn)
+                v[u] = *reinterpret_cast<const uint4*>(
+                    (k < K0 ? X0 + ((int64_t)e * K0 + k) * N : X1 + ((int64_t)e * K0 + (k - K0)) * N) + n0 + 8 * c8);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * (kThreads / V);
+            if (r >= kn) break;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(tile + r * P + 8 * c8);
+            dst[0] = v[u].x;
+            dst[1] = v[u].y;
+            dst[2] = v[u].z;
+            dst[3] = v[u].w;
+            if (NV)
+                m = make_uint4(absmax2(m.x, v[u].x), absmax2(m.y, v[u].y), absmax2(m.z, v[u].z),
+                               absmax2(m.w, v[u].w));
+        }
+    }
+    if (NV && !have_top) {
+        const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            atomicMax(&top[8 * c8 + 2 * q], w[q] & 0xffffu);
+            atomicMax(&top[8 * c8 + 2 * q + 1], w[q] >> 16);
+        }
+    }
+    __syncthreads();
+    // codes: column n, 32 rows from 32 q on. NC columns x kThreads / NC pieces at a time; the codes of
+    // a round replace the rows they were made of (a column's piece of 16 bytes in the round's rows)
+    constexpr int QN = kThreads / NC;  // pieces of 32 rows a round
+    const int n = threadIdx.x % NC;
+    const int64_t r = (int64_t)e * N + n0 + n;
+    NvRow row(0);
+    if (NV) {
+        if (have_top) {  // G holds the rows' powers of two already
+            row.g = __uint_as_float(top[n]);
+            row.inv = 1.0f / row.g;  // of a power of two: exact
+        } else {
+            row = NvRow(top[n]);
+            if (threadIdx.x < NC) G[r] = row.g;
+        }
+    }
+    for (int q0 = 0; q0 < kn / 32; q0 += QN) {
+        const int q = q0 + threadIdx.x / NC;
+        const bool in = q < kn / 32;
+        uint4 code = make_uint4(0, 0, 0, 0);
+        if (in) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint16_t* src = tile + (32 * q + 8 * j + 2 * h) * P + n;
+                    w[h] = src[0] | ((uint32_t)src[P] << 16);
+                }
+                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            const uint32_t a = halves_max(absmax8(absmax8(0u, v[0]), v[1]));
+            const uint32_t b = halves_max(absmax8(absmax8(0u, v[2]), v[3]));
+            const int64_t kk = k0 + 32 * q;
+            uint8_t* word = S + fp4_scale_word(r, kk / WORD_K, K / WORD_K);
+            if constexpr (NV) {
+                const NvScale sa(a, row), sb(b, row);
+                code = make_uint4(sa.codes(v[0]), sa.codes(v[1]), sb.codes(v[2]), sb.codes(v[3]));
+                *reinterpret_cast<uint16_t*>(word + kk % WORD_K / 16) = (uint16_t)(sa.byte | (sb.byte << 8));
+            } else {
+                const MxScale sc(max(a, b));
+                code = make_uint4(sc.codes(v[0]), sc.codes(v[1]), sc.codes(v[2]), sc.codes(v[3]));
+                word[kk % WORD_K / 32] = (uint8_t)sc.byte;
+            }
+        }
+        __syncthreads();  // every row of this round has been read
+        // the round's codes, QN pieces of 16 bytes a column, in the place of its rows
+        uint4* out = reinterpret_cast<uint4*>(tile + 32 * q0 * P);  // 4 P bytes a row pair: 16-aligned
+        out[n * (QN + 1) + threadIdx.x / NC] = code;
+        __syncthreads();
+        const int piece = threadIdx.x % QN, col = threadIdx.x / QN;
+        if (q0 + piece < kn / 32)
+            *reinterpret_cast<uint4*>(Qt + ((int64_t)e * N + n0 + col) * (K / 2) + (k0 + 32 * (q0 + piece)) / 2) =
+                out[col * (QN + 1) + piece];
+    }
+}
+
+// NV, long strips: largest magnitude of each column (as bits, which order as the magnitudes do; `top`
+// starts at zero). A thread takes 8 columns of every sixteenth row.
+constexpr int kTopRows = 256;
+
+__global__ void __launch_bounds__(kThreads) column_top_kernel(const __nv_bfloat16* __restrict__ X0,
+                                                              const __nv_bfloat16* __restrict__ X1,
+                                                              int K0, int N, uint32_t* __restrict__ top) {
     const int e = blockIdx.y;
     const int K = X1 ? 2 * K0 : K0;
-    const int c = (blockIdx.x * kTopThreads + threadIdx.x) * 8;
-    if (c >= N) return;
-    const int r0 = blockIdx.z * kTopRows, r1 = min(K, r0 + kTopRows);
+    const int c = blockIdx.x * 128 + threadIdx.x % 16 * 8;  // N is a multiple of 128
+    const int r1 = min(K, (int)(blockIdx.z + 1) * kTopRows);
     uint4 m = make_uint4(0, 0, 0, 0);
 #pragma unroll 8
-    for (int r = r0; r < r1; ++r) {
+    for (int r = blockIdx.z * kTopRows + threadIdx.x / 16; r < r1; r += kThreads / 16) {
         const __nv_bfloat16* src = r < K0 ? X0 + ((int64_t)e * K0 + r) * N
                                           : X1 + ((int64_t)e * K0 + (r - K0)) * N;
         const uint4 v = *reinterpret_cast<const uint4*>(src + c);
         m = make_uint4(absmax2(m.x, v.x), absmax2(m.y, v.y), absmax2(m.z, v.z), absmax2(m.w, v.w));
     }
-    uint32_t* dst = top + (int64_t)e * N + c;
+    __shared__ uint32_t part[128];
+    if (threadIdx.x < 128) part[threadIdx.x] = 0;
+    __syncthreads();
     const uint32_t w[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        atomicMax(dst + 2 * q, w[q] & 0xffffu);
-        atomicMax(dst + 2 * q + 1, w[q] >> 16);
+        atomicMax(&part[threadIdx.x % 16 * 8 + 2 * q], w[q] & 0xffffu);
+        atomicMax(&part[threadIdx.x % 16 * 8 + 2 * q + 1], w[q] >> 16);
     }
+    __syncthreads();
+    if (threadIdx.x < 128) atomicMax(top + (int64_t)e * N + blockIdx.x * 128 + threadIdx.x, part[threadIdx.x]);
 }
 
 // Column maxima (bits) to the rows' powers of two, in place.
@@ -170,84 +317,37 @@ __global__ void column_g_kernel(float* __restrict__ G, int64_t n) {
     if (i < n) G[i] = NvRow(__float_as_uint(G[i])).g;
 }
 
-// Tiles of 128 K-rows x 64 columns through shared memory. A thread makes the codes of 32 K
-// elements of one column: 16 bytes, one block of 32 or two of 16.
-constexpr int kColK = 128;
-constexpr int kColN = 64;
-
-template <bool NV>
-__global__ void __launch_bounds__(kThreads) quantize_cols_kernel(
-    const __nv_bfloat16* __restrict__ X0, const __nv_bfloat16* __restrict__ X1, int K0, int N,
-    uint8_t* __restrict__ Qt, uint8_t* __restrict__ S, const float* __restrict__ G) {
-    __shared__ __align__(16) uint16_t tile[kColK][kColN + 2];
-    __shared__ __align__(16) uint8_t scale[kColN][8];
-    const int e = blockIdx.z, n0 = blockIdx.x * kColN, k0 = blockIdx.y * kColK;
-    const int K = X1 ? 2 * K0 : K0;  // K0 % 128 == 0: a tile lies in one of the two
-    const __nv_bfloat16* src = (k0 < K0 ? X0 + ((int64_t)e * K0 + k0) * N
-                                        : X1 + ((int64_t)e * K0 + (k0 - K0)) * N) + n0;
-    for (int i = threadIdx.x; i < kColK * (kColN / 8); i += kThreads) {
-        const int r = i / (kColN / 8), c8 = i % (kColN / 8);
-        const uint4 v = *reinterpret_cast<const uint4*>(src + (int64_t)r * N + 8 * c8);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(&tile[r][8 * c8]);
-        dst[0] = v.x;
-        dst[1] = v.y;
-        dst[2] = v.z;
-        dst[3] = v.w;
-    }
-    __syncthreads();
-    {
-        const int n = threadIdx.x % kColN, q = threadIdx.x / kColN;
-        uint4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int k = 32 * q + 8 * j + 2 * h;
-                w[h] = tile[k][n] | ((uint32_t)tile[k + 1][n] << 16);
-            }
-            v[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        const uint32_t a = halves_max(absmax8(absmax8(0u, v[0]), v[1]));
-        const uint32_t b = halves_max(absmax8(absmax8(0u, v[2]), v[3]));
-        const int64_t r = (int64_t)e * N + n0 + n;
-        uint4 code;
-        if constexpr (NV) {
-            NvRow row(0);
-            row.g = G[r];
-            row.inv = 1.0f / row.g;  // of a power of two: exact
-            const NvScale sa(a, row), sb(b, row);
-            code = make_uint4(sa.codes(v[0]), sa.codes(v[1]), sb.codes(v[2]), sb.codes(v[3]));
-            scale[n][2 * q] = (uint8_t)sa.byte;
-            scale[n][2 * q + 1] = (uint8_t)sb.byte;
-        } else {
-            const MxScale sc(max(a, b));
-            code = make_uint4(sc.codes(v[0]), sc.codes(v[1]), sc.codes(v[2]), sc.codes(v[3]));
-            scale[n][q] = (uint8_t)sc.byte;
-        }
-        *reinterpret_cast<uint4*>(Qt + r * (K / 2) + k0 / 2 + 16 * q) = code;
-    }
-    __syncthreads();
-    constexpr int WORDS = kColK / Fp4<NV>::TILE_K;  // scale tiles that a tile's columns pass
-    if (threadIdx.x < kColN * WORDS) {
-        const int n = threadIdx.x % kColN, w = threadIdx.x / kColN;
-        *reinterpret_cast<uint32_t*>(
-            S + fp4_scale_word((int64_t)e * N + n0 + n, k0 / Fp4<NV>::TILE_K + w, K / Fp4<NV>::TILE_K)) =
-            *reinterpret_cast<const uint32_t*>(&scale[n][4 * w]);
-    }
-}
-
 // ---------------------------------------------------------- dispatch of quantised rows
 // Codes and scales of a row depend on that row alone, so those of an expert-major row are its
 // token's: a warp copies a token's codes and scale words to its k rows.
-constexpr int kGatherWarps = 8;
+// The CTAs behind those take the padding rows of each segment (the trailing rows with perm_token < 0;
+// at most MOE_ROW_ALIGN - 1 per expert): zero codes, scales of zero bits and g = 1, as quantising a
+// zero row gives.
+constexpr int kPadSplit = 8;
 
-__global__ void __launch_bounds__(kGatherWarps * 32) permute_kernel(
+__global__ void __launch_bounds__(kThreads) permute_kernel(
     const uint8_t* __restrict__ xq, const uint8_t* __restrict__ sx, const float* __restrict__ gx,
-    const int32_t* __restrict__ slot_to_row, int64_t T, int d, int k, int ktiles,
+    const int32_t* __restrict__ slot_to_row, const int32_t* __restrict__ perm_token,
+    const int64_t* __restrict__ row_offsets, int64_t T, int d, int k, int ktiles, int64_t token_ctas,
     uint8_t* __restrict__ Xq, uint8_t* __restrict__ sX, float* __restrict__ gX) {
+    if (blockIdx.x >= token_ctas) {
+        const int e = (int)(blockIdx.x - token_ctas) / kPadSplit, part = (int)(blockIdx.x - token_ctas) % kPadSplit;
+        const int64_t hi = row_offsets[e + 1];
+        int64_t lo = row_offsets[e];
+        if (hi - lo > MOE_ROW_ALIGN - 1) lo = hi - (MOE_ROW_ALIGN - 1);
+        for (int64_t r = lo + part * (kThreads / 32) + threadIdx.x / 32; r < hi;
+             r += kPadSplit * (kThreads / 32)) {  // a warp a row
+            if (perm_token[r] >= 0) continue;
+            for (int c = threadIdx.x % 32; c < d / 32; c += 32)
+                reinterpret_cast<uint4*>(Xq + r * (d / 2))[c] = make_uint4(0, 0, 0, 0);
+            for (int c = threadIdx.x % 32; c < ktiles; c += 32)
+                *reinterpret_cast<uint32_t*>(sX + fp4_scale_word(r, c, ktiles)) = 0;
+            if (gX && threadIdx.x % 32 == 0) gX[r] = 1.0f;
+        }
+        return;
+    }
     const int lane = threadIdx.x % 32;
-    const int64_t t = (int64_t)blockIdx.x * kGatherWarps + threadIdx.x / 32;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     if (t >= T) return;
     int32_t my_row = -1;
     if (lane < k) my_row = slot_to_row[t * k + lane];
@@ -277,39 +377,13 @@ __global__ void __launch_bounds__(kGatherWarps * 32) permute_kernel(
     }
 }
 
-// Padding rows of each segment (the trailing rows with perm_token < 0; at most MOE_ROW_ALIGN - 1
-// per expert): zero codes, scales of zero bits and g = 1, as quantising a zero row gives.
-constexpr int kPadSplit = 16;
-
-__global__ void __launch_bounds__(kThreads) pad_rows_kernel(const int64_t* __restrict__ row_offsets,
-                                                            const int32_t* __restrict__ perm_token,
-                                                            int d, int ktiles,
-                                                            uint8_t* __restrict__ Xq,
-                                                            uint8_t* __restrict__ sX,
-                                                            float* __restrict__ gX) {
-    const int e = blockIdx.x;
-    const int64_t hi = row_offsets[e + 1];
-    int64_t lo = row_offsets[e];
-    if (hi - lo > MOE_ROW_ALIGN - 1) lo = hi - (MOE_ROW_ALIGN - 1);
-    const int per_row = d / 32;
-    for (int64_t i = (int64_t)blockIdx.y * kThreads + threadIdx.x; i < (hi - lo) * per_row;
-         i += (int64_t)gridDim.y * kThreads) {
-        const int64_t r = lo + i / per_row;
-        const int c = (int)(i % per_row);
-        if (perm_token[r] >= 0) continue;
-        reinterpret_cast<uint4*>(Xq + r * (d / 2))[c] = make_uint4(0, 0, 0, 0);
-        if (c < ktiles) *reinterpret_cast<uint32_t*>(sX + fp4_scale_word(r, c, ktiles)) = 0;
-        if (gX && c == 0) gX[r] = 1.0f;
-    }
-}
-
-template <bool NV, int WPR, int NIT>
+template <bool NV, int TPR, int NIT>
 int launch_rows(const __nv_bfloat16* X, const __nv_bfloat16* X1, const int64_t* limit, int64_t rows,
                 int cols, uint8_t* Q, uint8_t* S, float* g, cudaStream_t st) {
-    int64_t blocks = cdiv(rows, kThreads / 32 / WPR);
+    int64_t blocks = cdiv(rows, kThreads / TPR);
     const int64_t cap = (int64_t)sm_count() * 16;
     if (blocks > cap) blocks = cap;
-    quantize_rows_kernel<NV, WPR, NIT><<<(unsigned)blocks, kThreads, 0, st>>>(X, X1, limit, rows, cols,
+    quantize_rows_kernel<NV, TPR, NIT><<<(unsigned)blocks, kThreads, 0, st>>>(X, X1, limit, rows, cols,
                                                                              Q, S, g);
     return launch_status();
 }
@@ -321,13 +395,45 @@ int rows_by_width(const __nv_bfloat16* X, const __nv_bfloat16* X1, const int64_t
     // A warp holds rows of up to 4096 elements; wider ones, and rows too few to fill the GPU with
     // a warp each, take a CTA of eight.
     if (width > 4096 || rows < 8 * (int64_t)sm_count()) {
-        if (width <= 4096) return launch_rows<NV, 8, 1>(X, X1, limit, rows, cols, Q, S, g, st);
-        if (width <= 8192) return launch_rows<NV, 8, 2>(X, X1, limit, rows, cols, Q, S, g, st);
+        if (width <= 4096) return launch_rows<NV, 256, 1>(X, X1, limit, rows, cols, Q, S, g, st);
+        if (width <= 8192) return launch_rows<NV, 256, 2>(X, X1, limit, rows, cols, Q, S, g, st);
+        return launch_rows<NV, 256, 8>(X, X1, limit, rows, cols, Q, S, g, st);
+    }
+    // many narrow rows: eight threads each, so that none idles and several pieces are in flight
+    if (width <= 1024 && rows >= 256 * (int64_t)sm_count()) {
+        if (width <= 256) return launch_rows<NV, 8, 2>(X, X1, limit, rows, cols, Q, S, g, st);
+        if (width <= 512) return launch_rows<NV, 8, 4>(X, X1, limit, rows, cols, Q, S, g, st);
         return launch_rows<NV, 8, 8>(X, X1, limit, rows, cols, Q, S, g, st);
     }
-    if (width <= 1024) return launch_rows<NV, 1, 2>(X, X1, limit, rows, cols, Q, S, g, st);
-    if (width <= 2048) return launch_rows<NV, 1, 4>(X, X1, limit, rows, cols, Q, S, g, st);
-    return launch_rows<NV, 1, 8>(X, X1, limit, rows, cols, Q, S, g, st);
+    if (width <= 1024) return launch_rows<NV, 32, 2>(X, X1, limit, rows, cols, Q, S, g, st);
+    if (width <= 2048) return launch_rows<NV, 32, 4>(X, X1, limit, rows, cols, Q, S, g, st);
+    return launch_rows<NV, 32, 8>(X, X1, limit, rows, cols, Q, S, g, st);
+}
+
+template <bool NV, int NC>
+int launch_cols(const __nv_bfloat16* X0, const __nv_bfloat16* X1, int E, int K0, int N, int K, int KT,
+                uint8_t* Qt, uint8_t* S, float* g, bool have_top, cudaStream_t st) {
+    const size_t smem = (size_t)KT * Strip<NC>::PITCH * 2;
+    auto kern = quantize_cols_kernel<NV, NC>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MOE_ERR_LAUNCH;
+    kern<<<dim3((unsigned)(N / NC), (unsigned)cdiv(K, KT), (unsigned)E), kThreads, smem, st>>>(
+        X0, X1, K0, N, KT, Qt, S, g, have_top);
+    return launch_status();
+}
+
+template <bool NV>
+void launch_dequantize(const uint8_t* Q, const uint8_t* S, const float* g, const int64_t* limit,
+                       int64_t rows, int cols, __nv_bfloat16* out, cudaStream_t st) {
+    const int64_t pieces = rows * (cols / 8);
+    int64_t blocks = cdiv(pieces, 4 * kThreads);
+    const int64_t cap = (int64_t)sm_count() * 32;
+    if (blocks > cap) blocks = cap;
+    if (pieces < (int64_t(1) << 32))
+        dequantize_kernel<NV, uint32_t><<<(unsigned)blocks, kThreads, 0, st>>>(Q, S, g, limit, rows, cols, out);
+    else
+        dequantize_kernel<NV, int64_t><<<(unsigned)blocks, kThreads, 0, st>>>(Q, S, g, limit, rows, cols, out);
 }
 
 bool fmt_ok(int fmt) { return fmt == MOE_FP4_MX || fmt == MOE_FP4_NV; }
@@ -380,18 +486,17 @@ extern "C" int moe_quantize_cols_fp4(const moe_bf16* X0, const moe_bf16* X1, int
     const auto* x0 = reinterpret_cast<const __nv_bfloat16*>(X0);
     const auto* x1 = reinterpret_cast<const __nv_bfloat16*>(X1);
     const int K = X1 ? 2 * K0 : K0;
-    const dim3 grid((unsigned)(N / kColN), (unsigned)(K / kColK), (unsigned)E);
-    if (fmt == MOE_FP4_MX) {
-        quantize_cols_kernel<false><<<grid, kThreads, 0, st>>>(x0, x1, K0, N, Qt, S, nullptr);
-        return launch_status();
-    }
+    if (fmt == MOE_FP4_MX)
+        return launch_cols<false, 64>(x0, x1, E, K0, N, K, K < kStripRowsMx ? K : kStripRowsMx, Qt, S, nullptr,
+                                      false, st);
+    if (K <= kStripMaxK) return launch_cols<true, 32>(x0, x1, E, K0, N, K, K, Qt, S, g, false, st);
     const int64_t n = (int64_t)E * N;
     if (cudaMemsetAsync(g, 0, sizeof(float) * n, st) != cudaSuccess) return MOE_ERR_LAUNCH;
-    column_top_kernel<<<dim3((unsigned)cdiv(N, 8 * kTopThreads), (unsigned)E, (unsigned)cdiv(K, kTopRows)),
-                        kTopThreads, 0, st>>>(x0, x1, K0, N, reinterpret_cast<uint32_t*>(g));
+    column_top_kernel<<<dim3((unsigned)(N / 128), (unsigned)E, (unsigned)cdiv(K, kTopRows)), kThreads, 0, st>>>(
+        x0, x1, K0, N, reinterpret_cast<uint32_t*>(g));
     column_g_kernel<<<(unsigned)cdiv(n, 256), 256, 0, st>>>(g, n);
-    quantize_cols_kernel<true><<<grid, kThreads, 0, st>>>(x0, x1, K0, N, Qt, S, g);
-    return launch_status();
+    if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
+    return launch_cols<true, 32>(x0, x1, E, K0, N, K, 512, Qt, S, g, true, st);
 }
 
 extern "C" int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const float* g,
@@ -402,16 +507,9 @@ extern "C" int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const floa
     if (cols % 128 != 0) return MOE_ERR_UNSUPPORTED;
     if (!aligned16(Q) || !aligned16(S) || !aligned16(out) || !aligned4(g)) return MOE_ERR_INVALID_ARG;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
-    int64_t blocks = cdiv(rows * (cols / 16), kThreads);
-    const int64_t cap = (int64_t)sm_count() * 32;
-    if (blocks > cap) blocks = cap;
     auto* o = reinterpret_cast<__nv_bfloat16*>(out);
-    if (fmt == MOE_FP4_NV)
-        dequantize_kernel<true><<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(
-            Q, S, g, rows_limit, rows, cols, o);
-    else
-        dequantize_kernel<false><<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(
-            Q, S, g, rows_limit, rows, cols, o);
+    if (fmt == MOE_FP4_NV) launch_dequantize<true>(Q, S, g, rows_limit, rows, cols, o, (cudaStream_t)stream);
+    else launch_dequantize<false>(Q, S, g, rows_limit, rows, cols, o, (cudaStream_t)stream);
     return launch_status();
 }
 
@@ -430,9 +528,8 @@ extern "C" int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
     const int ktiles = d / (fmt == MOE_FP4_NV ? Fp4<true>::TILE_K : Fp4<false>::TILE_K);
-    permute_kernel<<<(unsigned)cdiv(T, kGatherWarps), kGatherWarps * 32, 0, st>>>(
-        xq, sx, gx, slot_to_row, T, d, k, ktiles, Xq, sX, gX);
-    pad_rows_kernel<<<dim3(E, kPadSplit), kThreads, 0, st>>>(row_offsets, perm_token, d, ktiles, Xq, sX,
-                                                            gX);
+    const int64_t token_ctas = cdiv(T, kThreads / 32);
+    permute_kernel<<<(unsigned)(token_ctas + (int64_t)E * kPadSplit), kThreads, 0, st>>>(
+        xq, sx, gx, slot_to_row, perm_token, row_offsets, T, d, k, ktiles, token_ctas, Xq, sX, gX);
     return launch_status();
 }

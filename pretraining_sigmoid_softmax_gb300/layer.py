@@ -236,6 +236,12 @@ class MoEPlan:
         b.record(st)
         self.gemm_events.append((a, b))
 
+    def _dgrad_launches4(self, d, f):
+        """Kernels of a routed expert's 4-bit data and weight gradients, with their operands."""
+        if self.s.fp4_format == ops.FP4_MX:
+            return 8
+        return 7 + sum(1 if K <= 3328 else 3 for K in (d, 2 * f))
+
     def launches_per_step(self, backward=True, bias_update=False) -> int:
         """Kernel launches of one step through this plan (what the entry points enqueue)."""
         s = self.s
@@ -248,18 +254,18 @@ class MoEPlan:
                                                             # folded row gates in the scatter)
         if s.fp8 or s.fp4:  # quantise x, W_g, W_u, W_d; expert-major codes (2); G1, quantise H, G2
             n += 9 + (6 if s.f_shared else 0)               # (shared: its weights, G1, H, G2)
-            if s.fp4 and s.fp4_format == ops.FP4_MX:        # H's codes are formed in G1
-                n -= 2 if s.f_shared else 1
+            if s.fp4:  # the expert-major codes take one; in blocks of 32, H's are formed in G1
+                n -= 1 + (s.fp4_format == ops.FP4_MX) * (2 if s.f_shared else 1)
         else:
             n += 2 + (2 if s.f_shared else 0)               # expert forward (G1, G2)
         n += 1                                              # combine
         if backward:
             n += 1                                          # combine backward (+ padding rows)
             n += 1 if self.fold_gate else 0                 # gate gradient from its partials
-            if s.fp4_dgrad:  # dY rows, W_d and W_g/W_u columns (3 each, or 1 in blocks of 32), B2,
-                mx = s.fp4_format == ops.FP4_MX              # [dA|dU] rows (formed in B2 in blocks of
-                cols = 1 if mx else 6                        # 32), B4, order, B3, B5
-                n += 7 + cols + (6 + cols if s.f_shared else 0)
+            if s.fp4_dgrad:  # dY rows, W_d and W_g/W_u columns (1 each, 3 for long NV ones), B2,
+                # [dA|dU] rows (formed in B2 in blocks of 32), B4, order, B3, B5
+                n += self._dgrad_launches4(s.d, s.f) + (self._dgrad_launches4(s.d, s.f_shared) - 1
+                                                        if s.f_shared else 0)
             elif s.fp8_dgrad:  # pad the dY codes, W_d and W_g/W_u columns (3 each), B2,
                 n += 13 + (12 if s.f_shared else 0)         # [dA|dU] rows, B4, order, B3, B5
                                                             # (shared: quantise dY rows)

@@ -92,7 +92,7 @@ def rows_in(rows, cols, seed, scale=1.0):
 
 
 SIZES = [(1, 128), (3, 256), (7, 4096), (129, 384), (130, 1024), (1300, 2048), (2500, 128),
-         (1230, 4096), (5, 8192), (2, 32768), (3, 8320)]
+         (1230, 4096), (5, 8192), (2, 32768), (3, 8320), (39001, 128), (38999, 384), (39000, 896)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -136,7 +136,8 @@ def test_codes_at_the_ends_of_the_range(fmt):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("E,K0,N,stack", [(1, 128, 128, False), (3, 256, 384, True), (5, 384, 256, False),
-                                          (2, 1024, 128, True)])
+                                          (2, 1024, 128, True), (2, 3456, 128, False),
+                                          (1, 1792, 256, True), (1, 1664, 128, True)])
 def test_column_codes_are_bit_exact(E, K0, N, stack, fmt):
     mats = [torch.stack([rows_in(K0, N, 7 * e + i) for e in range(E)]) for i in range(2 if stack else 1)]
     if E > 1:
