@@ -171,7 +171,7 @@ struct Strip {
 };
 
 template <bool NV, int NC>
-__global__ void __launch_bounds__(kThreads) quantize_cols_kernel(
+__global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
     const __nv_bfloat16* __restrict__ X0, const __nv_bfloat16* __restrict__ X1, int K0, int N, int KT,
     uint8_t* __restrict__ Qt, uint8_t* __restrict__ S, float* __restrict__ G, bool have_top) {
     extern __shared__ __align__(16) uint8_t strip_smem[];
@@ -399,11 +399,10 @@ int rows_by_width(const __nv_bfloat16* X, const __nv_bfloat16* X1, const int64_t
         if (width <= 8192) return launch_rows<NV, 256, 2>(X, X1, limit, rows, cols, Q, S, g, st);
         return launch_rows<NV, 256, 8>(X, X1, limit, rows, cols, Q, S, g, st);
     }
-    // many narrow rows: eight threads each, so that none idles and several pieces are in flight
-    if (width <= 1024 && rows >= 256 * (int64_t)sm_count()) {
+    // many narrow rows: few threads each, so that none idles
+    if (width <= 512 && rows >= 256 * (int64_t)sm_count()) {
         if (width <= 256) return launch_rows<NV, 8, 2>(X, X1, limit, rows, cols, Q, S, g, st);
-        if (width <= 512) return launch_rows<NV, 8, 4>(X, X1, limit, rows, cols, Q, S, g, st);
-        return launch_rows<NV, 8, 8>(X, X1, limit, rows, cols, Q, S, g, st);
+        if (width <= 512) return launch_rows<NV, 16, 2>(X, X1, limit, rows, cols, Q, S, g, st);
     }
     if (width <= 1024) return launch_rows<NV, 32, 2>(X, X1, limit, rows, cols, Q, S, g, st);
     if (width <= 2048) return launch_rows<NV, 32, 4>(X, X1, limit, rows, cols, Q, S, g, st);
@@ -489,14 +488,14 @@ extern "C" int moe_quantize_cols_fp4(const moe_bf16* X0, const moe_bf16* X1, int
     if (fmt == MOE_FP4_MX)
         return launch_cols<false, 64>(x0, x1, E, K0, N, K, K < kStripRowsMx ? K : kStripRowsMx, Qt, S, nullptr,
                                       false, st);
-    if (K <= kStripMaxK) return launch_cols<true, 32>(x0, x1, E, K0, N, K, K, Qt, S, g, false, st);
+    if (K <= kStripMaxK) return launch_cols<true, 16>(x0, x1, E, K0, N, K, K, Qt, S, g, false, st);
     const int64_t n = (int64_t)E * N;
     if (cudaMemsetAsync(g, 0, sizeof(float) * n, st) != cudaSuccess) return MOE_ERR_LAUNCH;
     column_top_kernel<<<dim3((unsigned)(N / 128), (unsigned)E, (unsigned)cdiv(K, kTopRows)), kThreads, 0, st>>>(
         x0, x1, K0, N, reinterpret_cast<uint32_t*>(g));
     column_g_kernel<<<(unsigned)cdiv(n, 256), 256, 0, st>>>(g, n);
     if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
-    return launch_cols<true, 32>(x0, x1, E, K0, N, K, 512, Qt, S, g, true, st);
+    return launch_cols<true, 16>(x0, x1, E, K0, N, K, 512, Qt, S, g, true, st);
 }
 
 extern "C" int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const float* g,

@@ -17,8 +17,19 @@ struct Fp4Gemm {
     using Store = Cfg<256, false, false, false, kEpiStore, false, false, true, QT, 16, 8, !NV>;
     // outputs that are no multiple of 256 wide: 192 columns (the last tile clipped)
     using Store192 = Cfg<192, false, false, false, kEpiStore, false, false, true, QT, 16, 12>;
+    // few rows an expert: one CTA a tile (few_rows below)
+    using G1One = Cfg<128, false, false, true, kEpiSwigluFwd, false, false, false, QT, 16, 8, true>;
+    using StoreOne = Cfg<128, false, false, false, kEpiStore, false, false, false, QT, 16, 8, true>;
     using Bwd = Cfg<192, false, false, false, kEpiSwigluBwd, false, false, true, QT, 16, 12>;
 };
+
+// Whether most experts have one 128-row tile at most: the capacity of T k rows on E experts is T k + 127
+// E, so 192 E stands for about 64 rows an expert. A pair's second half would then load and multiply
+// rows of other experts, and half as many tiles would share the weights' loads: one token through
+// experts of 4096 x 1536 takes EXPERTS_TOKEN.
+bool few_rows(const int64_t* row_offsets, int E, int64_t rows) {
+    return row_offsets ? rows <= 192 * (int64_t)E : rows <= BM;
+}
 
 // An operand: codes [rows, K / 2], tiled scales and, in NV, the rows' powers of two.
 struct Operand {
@@ -56,9 +67,9 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
             const Operand& W, moe_bf16* Y, const float* r1_row, const float* r1_col, cudaStream_t st) {
     using G = Fp4Gemm<NV>;
     CUtensorMap mx, mw, sf[3], mo[3];
-    const bool wide = N % 256 == 0;
+    const bool one = few_rows(row_offsets, E, rows), wide = N % 256 == 0;
     if (!code_map(&mx, X.q, K, rows) ||
-        !code_map(&mw, W.q, K, (uint64_t)E * N, wide ? 128 : 96) ||
+        !code_map(&mw, W.q, K, (uint64_t)E * N, one || wide ? 128 : 96) ||
         !scale_map<NV>(&sf[0], X.s, K, rows) || !scale_map<NV>(&sf[1], W.s, K, (int64_t)E * N) ||
         !out_maps(mo, Y, nullptr, nullptr, N, rows, G::Store::OCOLS))
         return MOE_ERR_LAUNCH;
@@ -70,6 +81,8 @@ int product(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, i
     P.sb0 = W.g;
     P.r1_row = r1_row;
     P.r1_col = r1_col;
+    if (one)
+        return launch<typename G::StoreOne>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 128), st, mo, sf);
     if (wide)
         return launch<typename G::Store>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 256), st, mo, sf);
     return launch<typename G::Store192>(mx, mx, mw, mw, P, token_tiles_max(rows, N, 192), st, mo, sf);
@@ -97,6 +110,8 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
     P.only_h = A == nullptr;
     P.oq = Hq;
     P.os = sH;
+    if (few_rows(row_offsets, E, rows))
+        return launch<typename G::G1One>(mx, mx, mg, mu, P, token_tiles_max(rows, f, 128), st, mo, sf);
     return launch<typename G::G1>(mx, mx, mg, mu, P, token_tiles_max(rows, f, 128), st, mo, sf);
 }
 
