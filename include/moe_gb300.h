@@ -388,12 +388,16 @@ int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const float* g, const
 /*
  * moe_permute_fp4 - an operand's token rows copied to the rows of their experts (as moe_permute_fp8):
  * what moe_quantize_rows_fp4 gives of the expert-major rows, from a k-fold smaller quantisation.
- * In : xq, sx, gx of a [T, d] operand; slot_to_row, perm_token, row_offsets from moe_permute.
- * Out: Xq, sX, gX of a [rows, d] operand (rows = row_offsets[E]); padding rows as zero rows give.
+ * In : xq, sx, gx of a [T, d] operand; slot_to_row, perm_token, row_offsets from moe_permute; rows:
+ *      the row capacity. Slots with slot_to_row < 0 are skipped; a row of slot_to_row or an offset
+ *      past the capacity records MOE_ERR_BAD_INDEX (site 21) and is skipped.
+ * Out: Xq, sX, gX of a [rows, d] operand; padding rows as zero rows give, rows from row_offsets[E] on
+ *      as they were.
  */
 int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float* gx, const int32_t* slot_to_row,
-                    const int32_t* perm_token, const int64_t* row_offsets, int64_t T, int d, int E,
-                    int k, int fmt, uint8_t* Xq, uint8_t* sX, float* gX, moe_stream_t stream);
+                    const int32_t* perm_token, const int64_t* row_offsets, int64_t T, int64_t rows,
+                    int d, int E, int k, int fmt, uint8_t* Xq, uint8_t* sX, float* gX,
+                    moe_stream_t stream);
 
 /*
  * moe_grouped_gemm_fp4 - products grouped by expert: Y[p] = X[p] W[e]^T for the rows p of expert e,
@@ -401,6 +405,7 @@ int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float* gx, const
  * In : X, a [rows, K] operand in the padded expert-major layout; row_offsets [E+1] as in
  *      moe_expert_fwd (NULL: one matrix over all rows, E = 1); W, an [E N, K] operand.
  * Out: Y [rows, N] bf16. K, N % 128 == 0. Rows from row_offsets[E] on are left as they were.
+ * rows and E N are at most 2^31 - 512 here and in the two calls below (MOE_ERR_UNSUPPORTED).
  */
 int moe_grouped_gemm_fp4(const uint8_t* Xq, const uint8_t* sX, const float* gX,
                          const int64_t* row_offsets, int E, int64_t rows, int K, int N,

@@ -43,7 +43,7 @@ PROTOTYPES = {
     "moe_quantize_rows_fp4": (_I, [_P, _P, _P, _I64, _I, _I, _P, _P, _P, _P]),
     "moe_quantize_cols_fp4": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
     "moe_dequantize_fp4": (_I, [_P, _P, _P, _P, _I64, _I, _I, _P, _P]),
-    "moe_permute_fp4": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_permute_fp4": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _P, _P, _P, _P]),
     "moe_grouped_gemm_fp4": (_I, [_P, _P, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _I, _P, _P]),
     "moe_expert_fwd_fp4": (_I, [_P, _P, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                 _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),

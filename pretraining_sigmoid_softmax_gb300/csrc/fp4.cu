@@ -324,16 +324,22 @@ __global__ void column_g_kernel(float* __restrict__ G, int64_t n) {
 // at most MOE_ROW_ALIGN - 1 per expert): zero codes, scales of zero bits and g = 1, as quantising a
 // zero row gives.
 constexpr int kPadSplit = 8;
+constexpr int kSitePermuteFp4 = 21;
 
 __global__ void __launch_bounds__(kThreads) permute_kernel(
     const uint8_t* __restrict__ xq, const uint8_t* __restrict__ sx, const float* __restrict__ gx,
     const int32_t* __restrict__ slot_to_row, const int32_t* __restrict__ perm_token,
-    const int64_t* __restrict__ row_offsets, int64_t T, int d, int k, int ktiles, int64_t token_ctas,
-    uint8_t* __restrict__ Xq, uint8_t* __restrict__ sX, float* __restrict__ gX) {
+    const int64_t* __restrict__ row_offsets, int64_t T, int64_t rows, int d, int k, int ktiles,
+    int64_t token_ctas, uint8_t* __restrict__ Xq, uint8_t* __restrict__ sX, float* __restrict__ gX,
+    int* __restrict__ status) {
     if (blockIdx.x >= token_ctas) {
         const int e = (int)(blockIdx.x - token_ctas) / kPadSplit, part = (int)(blockIdx.x - token_ctas) % kPadSplit;
         const int64_t hi = row_offsets[e + 1];
         int64_t lo = row_offsets[e];
+        if (lo < 0 || hi < lo || hi > rows) {  // not a layout of these rows
+            if (threadIdx.x == 0) record_error(status, MOE_ERR_BAD_INDEX, kSitePermuteFp4);
+            return;
+        }
         if (hi - lo > MOE_ROW_ALIGN - 1) lo = hi - (MOE_ROW_ALIGN - 1);
         for (int64_t r = lo + part * (kThreads / 32) + threadIdx.x / 32; r < hi;
              r += kPadSplit * (kThreads / 32)) {  // a warp a row
@@ -351,6 +357,10 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(
     if (t >= T) return;
     int32_t my_row = -1;
     if (lane < k) my_row = slot_to_row[t * k + lane];
+    if (my_row >= rows) {
+        record_error(status, MOE_ERR_BAD_INDEX, kSitePermuteFp4);
+        my_row = -1;
+    }
     if (gx && my_row >= 0) gX[my_row] = gx[t];
     const uint4* src = reinterpret_cast<const uint4*>(xq + t * (d / 2));
     const int nvec = d / 32;
@@ -514,21 +524,24 @@ extern "C" int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const floa
 
 extern "C" int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float* gx,
                                const int32_t* slot_to_row, const int32_t* perm_token,
-                               const int64_t* row_offsets, int64_t T, int d, int E, int k, int fmt,
-                               uint8_t* Xq, uint8_t* sX, float* gX, moe_stream_t stream) {
+                               const int64_t* row_offsets, int64_t T, int64_t rows, int d, int E,
+                               int k, int fmt, uint8_t* Xq, uint8_t* sX, float* gX, moe_stream_t stream) {
     if (!xq || !sx || !slot_to_row || !perm_token || !row_offsets || !Xq || !sX || !fmt_ok(fmt) ||
         !g_ok(fmt, gx) || !g_ok(fmt, gX))
         return MOE_ERR_INVALID_ARG;
-    if (T <= 0 || d <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || k > E || k > 32 || d % 128 != 0) return MOE_ERR_UNSUPPORTED;
+    if (T <= 0 || rows <= 0 || d <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts || k > E || k > 32 || d % 128 != 0 || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     if (!aligned16(xq) || !aligned16(sx) || !aligned16(Xq) || !aligned16(sX) || !aligned4(gx) ||
         !aligned4(gX))
         return MOE_ERR_INVALID_ARG;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
+    int* status = device_status_word();
+    if (!status) return MOE_ERR_LAUNCH;
     cudaStream_t st = (cudaStream_t)stream;
     const int ktiles = d / (fmt == MOE_FP4_NV ? Fp4<true>::TILE_K : Fp4<false>::TILE_K);
     const int64_t token_ctas = cdiv(T, kThreads / 32);
     permute_kernel<<<(unsigned)(token_ctas + (int64_t)E * kPadSplit), kThreads, 0, st>>>(
-        xq, sx, gx, slot_to_row, perm_token, row_offsets, T, d, k, ktiles, token_ctas, Xq, sX, gX);
+        xq, sx, gx, slot_to_row, perm_token, row_offsets, T, rows, d, k, ktiles, token_ctas, Xq, sX, gX,
+        status);
     return launch_status();
 }

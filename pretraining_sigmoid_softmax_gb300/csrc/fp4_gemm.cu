@@ -38,6 +38,15 @@ struct Operand {
     const float* g;
 };
 
+// Rows and tiles are counted in 32 bits on the device: of the token rows, the weights' rows and the
+// scale tiles (a tensor map's coordinates), and of the output tiles.
+bool sizes_ok(int64_t rows, int E, int K, int N) {
+    const int64_t most = INT32_MAX - 511;
+    const int64_t wide = rows > (int64_t)E * N ? rows : (int64_t)E * N;
+    return wide <= most && cdiv(wide, 128) * (K / 64) <= most &&
+           (cdiv(rows, BM) + E) * cdiv(N, 128) <= most;
+}
+
 bool operand_ok(const Operand& o, int fmt) {
     return o.q && o.s && (fmt == MOE_FP4_NV) == (o.g != nullptr) && aligned16(o.q) && aligned16(o.s) &&
            aligned16(o.g);
@@ -161,7 +170,7 @@ extern "C" int moe_grouped_gemm_fp4(const uint8_t* Xq, const uint8_t* sX, const 
     const Operand X{Xq, sX, gX}, W{Wq, sW, gW};
     if (!operand_ok(X, fmt) || !operand_ok(W, fmt) || !Y || !aligned16(Y)) return MOE_ERR_INVALID_ARG;
     if (E <= 0 || rows <= 0 || (!row_offsets && E != 1)) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || !gemm_shape_ok(K, N)) return MOE_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || !gemm_shape_ok(K, N) || !sizes_ok(rows, E, K, N)) return MOE_ERR_UNSUPPORTED;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     if (!device_status_word()) return MOE_ERR_LAUNCH;
     cudaStream_t st = (cudaStream_t)stream;
@@ -184,7 +193,9 @@ extern "C" int moe_expert_fwd_fp4(const uint8_t* Xq, const uint8_t* sX, const fl
     for (const moe_bf16* p : {A, U, H, Y})
         if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
     if (E <= 0 || rows <= 0 || (!row_offsets && E != 1)) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || !gemm_shape_ok(d, f) || f > kFp4MaxCols) return MOE_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || !gemm_shape_ok(d, f) || f > kFp4MaxCols || !sizes_ok(rows, E, d, f) ||
+        !sizes_ok(rows, E, f, d))
+        return MOE_ERR_UNSUPPORTED;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     if (!device_status_word()) return MOE_ERR_LAUNCH;
     cudaStream_t st = (cudaStream_t)stream;
@@ -224,7 +235,8 @@ extern "C" int moe_expert_bwd_fp4(const uint8_t* dYq, const uint8_t* sdY, const 
     if ((dl_rows == nullptr) != (W_r == nullptr)) return MOE_ERR_INVALID_ARG;
     if (W_r && (!row_offsets || !aligned16(W_r))) return MOE_ERR_INVALID_ARG;
     if (E <= 0 || rows <= 0 || (!row_offsets && E != 1)) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || !gemm_shape_ok(d, f) || 2 * (int64_t)f > kFp4MaxCols)
+    if (E > kMaxExperts || !gemm_shape_ok(d, f) || 2 * (int64_t)f > kFp4MaxCols ||
+        !sizes_ok(rows, E, d, f) || !sizes_ok(rows, E, 2 * f, d))
         return MOE_ERR_UNSUPPORTED;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     if (!device_status_word()) return MOE_ERR_LAUNCH;

@@ -626,13 +626,16 @@ def _fp4(name, m, shape, fmt, dev):
         elif (fmt == FP4_NV and g.dtype is torch.float32 and g.shape == (rows,)
               and g.is_contiguous() and g.get_device() == dev):
             return q.data_ptr(), s.data_ptr(), g.data_ptr()
-    g = None
-    if fmt == FP4_NV:
-        g = _ptr(f"{name}.g", m.g, torch.float32, (rows,), dev)
-    elif m.g is not None:
+    if fmt == FP4_MX and g is not None:
         raise MoEError(f"{name}.g: FP4_MX operands have no powers of two for their rows")
-    return (_ptr(f"{name}.q", m.q, torch.uint8, (*lead, cols // 2), dev),
-            _ptr(f"{name}.s", m.s, torch.uint8, (moe_fp4_scale_bytes(rows, cols, fmt),), dev), g)
+    parts = [("q", q, u8, (*lead, cols // 2)), ("s", s, u8, (moe_fp4_scale_bytes(rows, cols, fmt),))]
+    if fmt == FP4_NV:
+        parts.append(("g", g, torch.float32, (rows,)))
+    for part, t, dtype, want in parts:  # kinds and sizes first, then where they lie
+        if t is None or t.dtype is not dtype or t.shape != want:
+            _ptr(f"{name}.{part}", t, dtype, want, dev)
+    return tuple(_ptr(f"{name}.{part}", t, dtype, want, dev) for part, t, dtype, want in parts) + (
+        () if fmt == FP4_NV else (None,))
 
 
 def _fp4_rows(name, m):
@@ -667,6 +670,8 @@ def moe_quantize_rows_fp4(X, out, X1=None, rows_limit=None, stream=None):
     """Rows of X [rows, cols] bf16, or of [X | X1], to the operand ``out`` (an Fp4)."""
     rows, cols = shape = _rows("X", X)
     dev, bf16 = _device(X), torch.bfloat16
+    if out is None:
+        raise MoEError("out is missing")
     fmt = out.fmt
     q, s, g = _fp4("out", out, (rows, cols if X1 is None else 2 * cols), fmt, dev)
     _check(_lib.load().moe_quantize_rows_fp4(_ptr("X", X, bf16, shape, dev),
@@ -682,6 +687,8 @@ def moe_quantize_cols_fp4(X0, X1, out, stream=None):
         raise MoEError("X0 must be [E, K0, N]" + ("" if X0 is None else f", got shape {tuple(X0.shape)}"))
     E, K0, N = shape = X0.shape
     dev, bf16 = _device(X0), torch.bfloat16
+    if out is None:
+        raise MoEError("out is missing")
     q, s, g = _fp4("out", out, (E, N, K0 if X1 is None else 2 * K0), out.fmt, dev)
     _check(_lib.load().moe_quantize_cols_fp4(_ptr("X0", X0, bf16, shape, dev),
                                              _opt("X1", X1, bf16, shape, dev), E, K0, N, out.fmt, q, s,
@@ -690,6 +697,8 @@ def moe_quantize_cols_fp4(X0, X1, out, stream=None):
 
 def moe_dequantize_fp4(m, out, rows_limit=None, stream=None):
     """The numbers an operand stands for, as bf16 in ``out`` (of its rows and columns)."""
+    if m is None:
+        raise MoEError("m is missing")
     shape = m.q.shape
     if len(shape) not in (2, 3):
         raise MoEError(f"m.q must be [rows, cols / 2] or [E, rows, cols / 2], got shape {tuple(shape)}")
@@ -708,14 +717,16 @@ def moe_permute_fp4(x, slot_to_row, perm_token, row_offsets, X, stream=None):
     """The token rows of the operand x copied to their experts' rows of the operand X."""
     T, d, fmt, dev = _fp4_rows("x", x)
     R = _fp4_rows("X", X)[0]
+    if row_offsets is None or row_offsets.numel() < 2:
+        raise MoEError("row_offsets must be [E + 1]")
     k, E, i32 = _rows("slot_to_row", slot_to_row)[1], row_offsets.numel() - 1, torch.int32
     if R < moe_padded_rows(T, k, E):
         raise MoEError(f"X has {R} rows, the layout takes up to {moe_padded_rows(T, k, E)}")
     _check(_lib.load().moe_permute_fp4(*_fp4("x", x, (T, d), fmt, dev),
                                        _ptr("slot_to_row", slot_to_row, i32, (T, k), dev),
                                        _ptr("perm_token", perm_token, i32, (R,), dev),
-                                       _ptr("row_offsets", row_offsets, torch.int64, (E + 1,), dev), T, d,
-                                       E, k, fmt, *_fp4("X", X, (R, d), fmt, dev),
+                                       _ptr("row_offsets", row_offsets, torch.int64, (E + 1,), dev), T, R,
+                                       d, E, k, fmt, *_fp4("X", X, (R, d), fmt, dev),
                                        _stream_of(stream, dev)), "moe_permute_fp4")
 
 
@@ -724,8 +735,8 @@ def moe_grouped_gemm_fp4(X, row_offsets, W, Y, stream=None):
     Y [rows, N] bf16; row_offsets None: one matrix over all rows."""
     rows, K, fmt, dev = _fp4_rows("X", X)
     E, N = _fp4_stack("W", W)
-    _check(_lib.load().moe_grouped_gemm_fp4(*_fp4("X", X, (rows, K), fmt, dev),
-                                            _offsets(row_offsets, E, dev), E, rows, K, N,
+    ro = _offsets(row_offsets, E, dev)
+    _check(_lib.load().moe_grouped_gemm_fp4(*_fp4("X", X, (rows, K), fmt, dev), ro, E, rows, K, N,
                                             *_fp4("W", W, (E, N, K), fmt, dev), fmt,
                                             _ptr("Y", Y, torch.bfloat16, (rows, N), dev),
                                             _stream_of(stream, dev)), "moe_grouped_gemm_fp4")
@@ -736,9 +747,8 @@ def moe_expert_fwd_fp4(X, row_offsets, W_g, W_u, W_d, A, U, H, Hc, Y, stream=Non
     the operand made of H. A and U None: nothing is kept for a backward."""
     rows, d, fmt, dev = _fp4_rows("X", X)
     E, f = _fp4_stack("W_g", W_g)
-    bf16 = torch.bfloat16
-    _check(_lib.load().moe_expert_fwd_fp4(*_fp4("X", X, (rows, d), fmt, dev),
-                                          _offsets(row_offsets, E, dev), E, rows, d, f,
+    bf16, ro = torch.bfloat16, _offsets(row_offsets, E, dev)
+    _check(_lib.load().moe_expert_fwd_fp4(*_fp4("X", X, (rows, d), fmt, dev), ro, E, rows, d, f,
                                           *_fp4("W_g", W_g, (E, f, d), fmt, dev),
                                           *_fp4("W_u", W_u, (E, f, d), fmt, dev),
                                           *_fp4("W_d", W_d, (E, d, f), fmt, dev), fmt,

@@ -371,3 +371,240 @@ def test_expert_backward_matches_the_definition(counts, d, f, router, fmt):
         assert_gemm_exact(dWu[e], h64(dU[lo:hi]).T, x, f"dW_u e{e}")
     for o in (dA, dU, dX):
         assert (o[n:] == -3.0).all()
+
+
+# ------------------------------------------------------------------ at the edges of the calls
+
+def _random_operand(shape, fmt, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+    return made(t, fmt)
+
+
+def numbers_of(m):
+    """[..., rows, cols] in fp64 on the GPU."""
+    out = torch.empty((*m.q.shape[:-1], 2 * m.q.shape[-1]), dtype=torch.bfloat16, device="cuda")
+    ops.moe_dequantize_fp4(m, out)
+    return out.double()
+
+
+def check_product(Y, X, W, segs):
+    """assert_gemm_exact's bound, on the GPU."""
+    for e, (lo, hi) in enumerate(segs):
+        a, w = numbers_of(X)[lo:hi], numbers_of(W)[e]
+        ex, mag = a @ w.t(), a.abs() @ w.abs().t()
+        _, p = torch.frexp(ex.abs())
+        ulp = torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), p.double() - 8)
+        off = (Y[lo:hi].double() - ex).abs() - 0.5001 * ulp - (a.shape[1] + 2) * 2.0 ** -24 * mag
+        assert (off <= 0).all(), (e, float(off.max()))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,K,N", [([9000, 3, 0, 4100, 128, 7777], 2048, 1024), (20000, 1536, 2048),
+                                        ([130] * 40, 640, 384), ([64] * 64, 4096, 512)])
+def test_products_that_use_every_stage_and_buffer_again(counts, K, N, fmt):
+    """More tiles than the GPU takes at once, long and short sums, whole and clipped tiles; two runs give
+    the same bits."""
+    ro, rows, segs = layout(counts)
+    ro_d = None if ro is None else dev(torch.from_numpy(ro))
+    X, W = _random_operand((rows, K), fmt, 1), _random_operand((len(segs), N, K), fmt, 2)
+    Y = torch.full((rows, N), -3.0, dtype=torch.bfloat16, device="cuda")
+    ops.moe_grouped_gemm_fp4(X, ro_d, W, Y)
+    again = torch.empty_like(Y)
+    ops.moe_grouped_gemm_fp4(X, ro_d, W, again)
+    torch.cuda.synchronize()
+    assert ops.moe_device_status() == (0, 0)
+    n = rows if ro is None else int(ro[-1])
+    assert torch.equal(Y[:n], again[:n])
+    check_product(Y, X, W, segs)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_no_rows_at_all(fmt):
+    """Experts that are all empty: nothing is written."""
+    ro, rows, _ = layout([0, 0, 0])
+    X, W = _random_operand((rows, 256), fmt, 1), _random_operand((3, 128, 256), fmt, 2)
+    Y = torch.full((rows, 128), -3.0, dtype=torch.bfloat16, device="cuda")
+    ops.moe_grouped_gemm_fp4(X, dev(torch.from_numpy(ro)), W, Y)
+    torch.cuda.synchronize()
+    assert (Y == -3.0).all() and ops.moe_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [100, 700])
+def test_infinities_and_nan_stay_in_their_rows_and_columns(rows, fmt):
+    """A row of X that holds one makes its row of Y NaN (its block's or its row's scale is NaN), a row of W
+    its column; nothing else."""
+    g = torch.Generator().manual_seed(4)
+    x, w = randn_bf16((rows, 512), g), randn_bf16((1, 384, 512), g)
+    x[3, 40], x[rows - 1, 511], w[0, 7, 0], w[0, 300, 130] = float("inf"), float("nan"), float("nan"), -float("inf")
+    Y = torch.empty(rows, 384, dtype=torch.bfloat16, device="cuda")
+    ops.moe_grouped_gemm_fp4(made(x, fmt), None, made(w, fmt), Y)
+    torch.cuda.synchronize()
+    want = torch.zeros(rows, 384, dtype=torch.bool)
+    want[[3, rows - 1]] = True
+    want[:, [7, 300]] = True
+    assert torch.equal(Y.isnan().cpu(), want)
+    x[[3, rows - 1]] = 0
+    w[0, [7, 300]] = 0
+    nv, ok = fmt == ops.FP4_NV, ~want.numpy()
+    ex = O.fp4_dequant_rows(h64(x), nv) @ O.fp4_dequant_rows(h64(w[0]), nv).T
+    assert (np.abs(h64(Y) - ex)[ok] <= (2.0 ** -8 * np.abs(ex) + 1e-3)[ok]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bad", [[0, 128, 100, 384], [0, 100, 256, 384], [128, 256, 384, 384],
+                                 [0, 128, 256, 4096]])
+def test_layouts_that_are_none_are_reported(bad, fmt):
+    """A decrease, a segment that is no whole number of tiles, a start other than 0, an end past the
+    capacity: the kernels record it and write nothing."""
+    X, W = _random_operand((512, 256), fmt, 1), _random_operand((3, 256, 256), fmt, 2)
+    ro = torch.tensor(bad, device="cuda")
+    Y = torch.full((512, 256), -3.0, dtype=torch.bfloat16, device="cuda")
+    ops.moe_clear_device_status()
+    ops.moe_grouped_gemm_fp4(X, ro, W, Y)
+    torch.cuda.synchronize()
+    assert ops.moe_device_status() == (5, 20) and (Y == -3.0).all()
+    ops.moe_clear_device_status()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_dispatch_reports_rows_past_the_capacity(fmt):
+    R = ops.moe_padded_rows(4, 2, 2)
+    x, X = operand((4, 128), fmt, 0x11), operand((R, 128), fmt)
+    s2r = torch.tensor([[0, 128], [1, R], [2, -1], [3, 129]], dtype=torch.int32, device="cuda")
+    tok = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    tok[[0, 1, 2, 3, 128, 129]] = torch.tensor([0, 1, 2, 3, 0, 3], dtype=torch.int32, device="cuda")
+    for ro, rest in (([0, 128, 256], 0), ([0, 128, R + 128], FILL)):
+        ops.moe_clear_device_status()
+        for t in (X.q, X.s):
+            t.fill_(FILL)
+        ops.moe_permute_fp4(x, s2r, tok, torch.tensor(ro, device="cuda"), X)
+        torch.cuda.synchronize()
+        assert ops.moe_device_status() == (5, 21)
+        q = X.q.cpu()
+        for r in (0, 1, 2, 3, 128, 129):
+            assert (q[r] == 0x11).all(), r
+        assert (q[4:128] == 0).all() and (q[130:256] == rest).all() and (q[256:] == FILL).all()
+    ops.moe_clear_device_status()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_captured_calls_replay_on_new_inputs_and_streams(fmt):
+    """Quantisation, dispatch and experts recorded once and replayed with other tokens, beside the same on
+    another stream."""
+    T, d, f, E, k = 70, 256, 256, 8, 2
+    g = torch.Generator().manual_seed(1)
+    idx = dev(_routing(T, E, k, g, False))
+    R = ops.moe_padded_rows(T, k, E)
+    i32, i64 = dict(dtype=torch.int32, device="cuda"), dict(dtype=torch.int64, device="cuda")
+    counts, off, ro = torch.empty(E, **i32), torch.empty(E + 1, **i64), torch.empty(E + 1, **i64)
+    tok, s2r = torch.empty(R, **i32), torch.empty(T, k, **i32)
+    ws = torch.empty(ops.moe_workspace_bytes(T, d, E, k), dtype=torch.uint8, device="cuda")
+    x = dev(randn_bf16((T, d), g))
+    ops.moe_permute(idx, x, E, counts, off, ro, tok, s2r, torch.empty(R, d, dtype=torch.bfloat16, device="cuda"),
+                    ws)
+    W = [_random_operand(s, fmt, i) for i, s in enumerate([(E, f, d), (E, f, d), (E, d, f)])]
+
+    class Buffers:
+        def __init__(self):
+            z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+            self.x, self.A, self.U, self.H, self.Y = z(T, d), z(R, f), z(R, f), z(R, f), z(R, d)
+            self.xc, self.X, self.Hc = (ops.fp4_empty(s, fmt) for s in ((T, d), (R, d), (R, f)))
+
+        def run(self, stream=None):
+            ops.moe_quantize_rows_fp4(self.x, self.xc, stream=stream)
+            ops.moe_permute_fp4(self.xc, s2r, tok, ro, self.X, stream=stream)
+            ops.moe_expert_fwd_fp4(self.X, ro, *W, self.A, self.U, self.H, self.Hc, self.Y, stream=stream)
+
+    a, b, want = Buffers(), Buffers(), Buffers()
+    a.x.copy_(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run()
+    for seed in (5, 6):
+        new = dev(randn_bf16((T, d), torch.Generator().manual_seed(seed)))
+        a.x.copy_(new)
+        b.x.copy_(new.flip(0))
+        torch.cuda.synchronize()
+        graph.replay()
+        b.run(side)
+        torch.cuda.synchronize()
+        for got in (a, b):
+            want.x.copy_(got.x)
+            want.run()
+            torch.cuda.synchronize()
+            n = int(ro[-1])
+            for t in ("A", "U", "H", "Y"):
+                assert torch.equal(getattr(got, t)[:n], getattr(want, t)[:n]), t
+    assert ops.moe_device_status() == (0, 0)
+
+
+def test_swiglu_gradients_against_differences():
+    """dA and dU against central differences of <r, silu(a) u> in 64 bits: the differences are off by
+    eps^2 / 6 of the third derivative (below 1 for silu), the kernel's values by half a bf16 step."""
+    for fmt in FMTS:
+        t, W, ro, rows, segs = _expert_inputs(300, 256, 128, 7)
+        Wd, new = ops.fp4_empty((1, 128, 256), fmt), lambda c: torch.empty(rows, c, dtype=torch.bfloat16,
+                                                                           device="cuda")
+        ops.moe_quantize_cols_fp4(dev(W["W_d"]), None, Wd)
+        dA, dU = new(128), new(128)
+        ops.moe_expert_bwd_fp4(made(t["dY"], fmt), None, None, dev(t["A"]), dev(t["U"]), None, None, Wd, None, None,
+                               dA, dU, None, None, None, None, None, parts=ops.BWD_DH)
+        torch.cuda.synchronize()
+        nv = fmt == ops.FP4_NV
+        r = O.fp4_dequant_rows(h64(t["dY"]), nv) @ O.fp4_dequant_cols(h64(W["W_d"][0]), nv)
+        a, u, eps = h64(t["A"]), h64(t["U"]), 1e-4
+        f = lambda a, u: r * O.silu(a) * u  # noqa: E731
+        for got, dif, third in ((dA, (f(a + eps, u) - f(a - eps, u)) / (2 * eps), np.abs(r * u)),
+                                (dU, (f(a, u + eps) - f(a, u - eps)) / (2 * eps), 0.0)):
+            bound = 2.0 ** -8 * np.abs(dif) + eps * eps * third + 1e-5 * (1 + np.abs(r) * (1 + np.abs(a * u)))
+            assert (np.abs(h64(got) - dif) <= bound).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_more_than_2_to_31_elements(fmt):
+    """Offsets past 32 bits: the last rows of a large matrix have the codes and numbers they have alone."""
+    rows, cols = 530000, 4096
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(
+        generator=torch.Generator(device="cuda").manual_seed(1))
+    m = ops.fp4_empty((rows, cols), fmt)
+    ops.moe_quantize_rows_fp4(x, m)
+    out = torch.empty_like(x)
+    ops.moe_dequantize_fp4(m, out)
+    for lo in (0, 262144, rows - 384):
+        part = x[lo:lo + 384].contiguous()
+        small, alone = ops.fp4_empty((384, cols), fmt), torch.empty(384, cols, dtype=torch.bfloat16, device="cuda")
+        ops.moe_quantize_rows_fp4(part, small)
+        ops.moe_dequantize_fp4(small, alone)
+        torch.cuda.synchronize()
+        assert torch.equal(m.q[lo:lo + 384], small.q) and torch.equal(out[lo:lo + 384], alone)
+
+
+def test_refusals_on_the_gpu():
+    E = ops.MoEError
+    m = ops.fp4_empty((4, 256), ops.FP4_NV)
+    buf = torch.zeros(4 * 256 + 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(E, match="invalid argument"):
+        ops.moe_quantize_rows_fp4(buf[1:1 + 1024].view(4, 256), m)       # off 16 bytes
+    ops.moe_quantize_rows_fp4(buf[8:].view(4, 256), m)                   # a view on them
+    with pytest.raises(E, match="contiguous"):
+        ops.moe_quantize_rows_fp4(torch.zeros(256, 4, dtype=torch.bfloat16, device="cuda").t(), m)
+    with pytest.raises(E, match="must be torch.bfloat16"):
+        ops.moe_quantize_rows_fp4(torch.zeros(4, 256, device="cuda"), m)
+    with pytest.raises(E, match="rows_limit must have shape"):
+        ops.moe_quantize_rows_fp4(buf[8:].view(4, 256), m, rows_limit=torch.zeros(2, dtype=torch.int64,
+                                                                                    device="cuda"))
+    with pytest.raises(E, match="format"):
+        ops.moe_grouped_gemm_fp4(m, None, ops.fp4_empty((1, 128, 256), ops.FP4_MX),
+                                 torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(E, match="unsupported"):
+        ops.moe_quantize_rows_fp4(torch.zeros(1, 32896, dtype=torch.bfloat16, device="cuda"),
+                                  ops.fp4_empty((1, 32896), ops.FP4_MX))
+    torch.cuda.synchronize()
+    assert ops.moe_device_status() == (0, 0)
