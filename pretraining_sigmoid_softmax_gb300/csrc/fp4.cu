@@ -213,12 +213,16 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
                                absmax2(m.w, v[u].w));
         }
     }
-    if (NV && !have_top) {
-        const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+    if (NV && !have_top) {  // a warp's rows first, or its lanes would queue at the same few words
+        uint32_t w[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            atomicMax(&top[8 * c8 + 2 * q], w[q] & 0xffffu);
-            atomicMax(&top[8 * c8 + 2 * q + 1], w[q] >> 16);
+#pragma unroll
+            for (int o = 16; o >= V; o >>= 1) w[q] = __vmaxu2(w[q], __shfl_xor_sync(0xffffffffu, w[q], o));
+            if (threadIdx.x % 32 < V) {
+                atomicMax(&top[8 * c8 + 2 * q], w[q] & 0xffffu);
+                atomicMax(&top[8 * c8 + 2 * q + 1], w[q] >> 16);
+            }
         }
     }
     __syncthreads();
@@ -301,11 +305,14 @@ __global__ void __launch_bounds__(kThreads) column_top_kernel(const __nv_bfloat1
     __shared__ uint32_t part[128];
     if (threadIdx.x < 128) part[threadIdx.x] = 0;
     __syncthreads();
-    const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+    uint32_t w[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        atomicMax(&part[threadIdx.x % 16 * 8 + 2 * q], w[q] & 0xffffu);
-        atomicMax(&part[threadIdx.x % 16 * 8 + 2 * q + 1], w[q] >> 16);
+        w[q] = __vmaxu2(w[q], __shfl_xor_sync(0xffffffffu, w[q], 16));
+        if (threadIdx.x % 32 < 16) {
+            atomicMax(&part[threadIdx.x % 16 * 8 + 2 * q], w[q] & 0xffffu);
+            atomicMax(&part[threadIdx.x % 16 * 8 + 2 * q + 1], w[q] >> 16);
+        }
     }
     __syncthreads();
     if (threadIdx.x < 128) atomicMax(top + (int64_t)e * N + blockIdx.x * 128 + threadIdx.x, part[threadIdx.x]);

@@ -77,7 +77,7 @@ enum Epi : int { kEpiSwigluFwd = 0, kEpiStore = 1, kEpiSwigluBwd = 2 };
 constexpr int kAuCols = 16;
 constexpr int kAuBufs = 2;
 constexpr int kSmemBudgetAu = 220 * 1024;
-constexpr int kSmemBudgetDeep = 222 * 1024;
+constexpr int kSmemBudgetFp4 = 222 * 1024;
 // Token-major epilogues stage their outputs in shared memory, 16 columns x 32 rows per warp
 // and output, and write them with TMA stores: two buffers deep, or one for the SwiGLU
 // backward, whose operand ring then keeps a fifth stage (what bounds it at K = 4096).
@@ -100,7 +100,6 @@ struct Cfg {
     static constexpr bool NV = QT_ == kNvFp4;  // E2M1, E4M3 scale per 16, power of two per row
     static constexpr bool FP4 = QT_ == kMxFp4 || NV;
     static constexpr bool DEEP = DEEP_;  // E2M1: one output buffer a warp, one operand stage more
-    static constexpr bool SCALED = FP8 || NV;  // row and column scales applied in the epilogue
     static constexpr int KB = FP4 ? BK_FP4 : FP8 ? BK_FP8 : BK;  // K elements per stage
     static constexpr int BN = BN_;           // output columns per tile (per B matrix if DUAL)
     static constexpr bool A_MN = A_MN_;
@@ -144,8 +143,11 @@ struct Cfg {
         FP4 ? (AU || DEEP || EW != 8 ? 1 : 2)
             : (AU || OCOLS == 32 || EW == 16) ? 1 : 2;  // buffers per warp
     static constexpr int OUT_BYTES = TS && !(FP4 && AU) ? EW * OUT_DEPTH * OUT_BUF_BYTES : 0;
+    // NV: each epilogue warp's columns' powers of two, fetched while the tile's main loop runs
+    static constexpr int CS_FLOATS = NV ? BN / (EW / 4) * (DUAL ? 2 : 1) : 0;
+    static constexpr int CS_BYTES = EW * CS_FLOATS * 4;
     static constexpr int BUDGET =
-        (DEEP ? kSmemBudgetDeep : AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES;
+        (FP4 ? kSmemBudgetFp4 : AU || TS ? kSmemBudgetAu : kSmemBudget) - AU_BYTES - OUT_BYTES - CS_BYTES;
     static constexpr int STAGES = (BUDGET / STAGE_BYTES) > 6 ? 6 : (BUDGET / STAGE_BYTES);
     static constexpr int ACC_COLS = MMA_N;
     // E2M1: the scales of a stage take SFC columns of tensor memory, and two stages' lie at its
@@ -171,10 +173,10 @@ struct Cfg {
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory columns");
     static_assert(BN % 64 == 0 && MMA_N <= 256 && BROWS % (FP4 ? 32 : 64) == 0, "tile width");
     static constexpr size_t MISC_BYTES = 512 + sizeof(int64_t) * (kMaxExperts + 1) +
-                                         (WGRAD || !DEEP ? sizeof(int32_t) * kMaxExperts : 0) +
+                                         (FP4 ? 0 : sizeof(int32_t) * kMaxExperts) +
                                          sizeof(int32_t) * (kMaxExperts + 1);
     static constexpr size_t SMEM_BYTES =
-        1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + MISC_BYTES;
+        1024 + (size_t)STAGES * STAGE_BYTES + AU_BYTES + OUT_BYTES + CS_BYTES + MISC_BYTES;
     static_assert((3 * STAGES + 7 + EW * kAuBufs) * 8 + 8 <= 512, "barrier block");
     static_assert(!(OV && AU), "the SwiGLU backward reports no shared columns");
     static_assert(STAGES * SF_BYTES % 1024 == 0, "alignment of what follows the stages");
@@ -243,6 +245,7 @@ struct SmemLayout {
     int32_t* ptp;      // E + 1: exclusive prefix of pair tiles per expert (pair, token-major)
     uint8_t* au;       // SwiGLU backward: EW x kAuBufs staged (a | u) chunks
     uint64_t* au_full; // EW x kAuBufs
+    float* cs;         // NV: EW x CS_FLOATS columns' powers of two
     uint8_t* ob;       // TMA-store epilogues: EW x OUT_DEPTH staged output chunks
 };
 
@@ -255,7 +258,8 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
     s.sf = base + (size_t)C::STAGES * (C::A_BYTES + C::B_BYTES);
     s.au = base + (size_t)C::STAGES * C::STAGE_BYTES;  // 1024-aligned: the stages are together
     s.ob = s.au + C::AU_BYTES;  // 1024-aligned: the a/u buffers are whole KB
-    uint8_t* misc = s.ob + C::OUT_BYTES;
+    s.cs = reinterpret_cast<float*>(s.ob + C::OUT_BYTES);
+    uint8_t* misc = s.ob + C::OUT_BYTES + C::CS_BYTES;
     s.full = reinterpret_cast<uint64_t*>(misc);
     s.empty = s.full + C::STAGES;
     s.tfull = s.empty + C::STAGES;
@@ -268,7 +272,7 @@ __device__ __forceinline__ SmemLayout carve(uint8_t* raw) {
     s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
     s.offs = reinterpret_cast<int64_t*>(misc + 512);
     s.order = reinterpret_cast<int32_t*>(s.offs + kMaxExperts + 1);
-    s.ptp = s.order + (C::WGRAD || !C::DEEP ? kMaxExperts : 0);
+    s.ptp = s.order + (C::FP4 ? 0 : kMaxExperts);
     return s;
 }
 
@@ -688,6 +692,36 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
 // Byte offset of 16-byte piece j of row r in a 128-byte-swizzled box of 128-byte rows.
 __device__ __forceinline__ int sw128_offset(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
+// NV: the powers of two of a warp's columns (of each accumulator) into its place in shared memory, and
+// that of this thread's row; then an accumulator chunk of 32 columns times both.
+template <class C>
+__device__ __forceinline__ float fetch_powers(float* cs, const Params& P, const TileInfo& ti, int64_t row,
+                                              int c_lo, int lane) {
+    constexpr int kCols = C::BN / (C::EW / 4);
+    __syncwarp();  // the previous tile's have been used
+#pragma unroll
+    for (int i = 0; i < (C::CS_FLOATS / 4 + 31) / 32; ++i) {
+        const int j = 4 * (lane + 32 * i);  // of gate, then of up
+        const int c = ti.n0 + c_lo + j % kCols;
+        if (j < C::CS_FLOATS && c < P.N)
+            *reinterpret_cast<float4*>(cs + j) = __ldg(reinterpret_cast<const float4*>(
+                (C::DUAL && j >= kCols ? P.sb1 : P.sb0) + (int64_t)ti.e * P.N + c));
+    }
+    const float g = __ldg(P.sa + row);
+    __syncwarp();
+    return g;
+}
+__device__ __forceinline__ void apply_powers(float* v, float g, const float* cs) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 w = reinterpret_cast<const float4*>(cs)[q];
+        v[4 * q] *= g * w.x;
+        v[4 * q + 1] *= g * w.y;
+        v[4 * q + 2] *= g * w.z;
+        v[4 * q + 3] *= g * w.w;
+    }
+}
+
 // 32 packed columns of this thread's row into its place in a box of C::OCOLS columns.
 template <class C>
 __device__ __forceinline__ void put_half(uint8_t* buf, int lane, int half, const uint32_t* w) {
@@ -728,7 +762,8 @@ template <class C>
 __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo& ti, uint32_t t_acc,
                                              int lane, int slot, int c_lo, int64_t row0, const Params& P,
                                              const CUtensorMap* mo0, const CUtensorMap* mo1,
-                                             const CUtensorMap* mo2, bool reversed, const Readers& rd) {
+                                             const CUtensorMap* mo2, bool reversed, const Readers& rd,
+                                             float g_row, const float* cs) {
     constexpr int kCols = C::BN / (C::EW / 4);    // of this warp (in each accumulator)
     // nothing to write: the half of a pair's tile past its segment, columns past the outputs
     if (ti.m0 >= ti.row_end || (C::BN % 128 && ti.n0 + c_lo >= P.N)) {
@@ -752,11 +787,13 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
         if (C::OV && rd.shared) arrive_read<C>(rd.shared_bar, lane);
         arrive_read<C>(rd.whole_bar, lane);
         const float rg = P.row_scale ? __ldg(P.row_scale + row) : 1.0f;
-        if constexpr (C::NV)
+        if constexpr (C::NV) {
 #pragma unroll
-            for (int k = 0; k < kHalves; ++k)
-                fp8_scale<32>(reinterpret_cast<float*>(g[k]), reinterpret_cast<float*>(u[k]), P, row, ti,
-                              c_lo + 32 * k);
+            for (int k = 0; k < kHalves; ++k) {
+                apply_powers(reinterpret_cast<float*>(g[k]), g_row, cs + 32 * k);
+                apply_powers(reinterpret_cast<float*>(u[k]), g_row, cs + kCols + 32 * k);
+            }
+        }
 #pragma unroll
         for (int o = 0; o < 3; ++o) {  // a, u, h
             if (o < 2 && P.only_h) continue;
@@ -816,7 +853,7 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
                 __syncwarp();
             }
             float* v = reinterpret_cast<float*>(r[i]);
-            if constexpr (C::NV) fp8_scale<32>(v, v, P, row, ti, c, /*dual=*/false);
+            if constexpr (C::NV) apply_powers(v, g_row, cs + c - c_lo);
             if (P.r1_row) add_router_term<32>(v, P, row, ti, c);
             uint32_t w[16];
 #pragma unroll
@@ -977,7 +1014,7 @@ __device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileIn
                                                uint32_t t_acc, int q, int lane, int slot, int c_lo,
                                                const Params& P, const CUtensorMap* mda,
                                                const CUtensorMap* mdu, uint32_t local,
-                                               volatile int* abort_flag) {
+                                               volatile int* abort_flag, float g_row, const float* cs) {
     const int64_t row0 = ti.m0 + 32 * q;
     const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
     const bool store = row0 < ti.row_end;  // as in swiglu_bwd_staged
@@ -995,7 +1032,7 @@ __device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileIn
         uint8_t* abuf = S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES;
         uint8_t* ubuf = abuf + C::AU_BUF_BYTES / 2;
         float* r = reinterpret_cast<float*>(acc);
-        if constexpr (C::NV) fp8_scale<32>(r, r, P, row, ti, c, /*dual=*/false);
+        if constexpr (C::NV) apply_powers(r, g_row, cs + c - c_lo);
         uint32_t wa[16], wu[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1325,6 +1362,13 @@ __device__ __forceinline__ void grouped_gemm_body(
                         au_issue<C>(S, &ma1, &mb1, slot, n_au + i, ti.m0 + 32 * q,
                                     ti.n0 + c_lo + i * kAuCols);
             }
+            float* cs = S.cs + slot * C::CS_FLOATS;
+            float g_row = 1.0f;
+            if constexpr (C::NV) {
+                const int64_t r = ti.m0 + row_in_tile;
+                if (ti.m0 < ti.row_end)
+                    g_row = fetch_powers<C>(cs, P, ti, r < ti.row_end ? r : ti.row_end - 1, c_lo, lane);
+            }
             bool ok = mbar_wait_bounded(smem_u32(&S.tfull[buf]), ph, abort_flag, P.status,
                                         P.wait_limit_ns, 33);
             ok = __all_sync(0xffffffffu, ok);
@@ -1334,7 +1378,7 @@ __device__ __forceinline__ void grouped_gemm_body(
                 tmem_base + (buf ? C::ACC1 : C::ACC0) + ((uint32_t)(32 * q) << 16);
             if constexpr (C::AU && C::FP4) {
                 if (!swiglu_bwd_fp4<C>(S, ti, t_acc, q, lane, slot, c_lo, P, &mo0, &mo1,
-                                       (uint32_t)local, abort_flag))
+                                       (uint32_t)local, abort_flag, g_row, cs))
                     break;
             } else if constexpr (C::AU) {
                 if (!swiglu_bwd_staged<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &ma1, &mb1,
@@ -1342,7 +1386,7 @@ __device__ __forceinline__ void grouped_gemm_body(
                     break;
             } else if constexpr (C::FP4) {
                 epilogue_fp4<C>(S, ti, t_acc, lane, slot, c_lo, ti.m0 + 32 * q, P, &mo0, &mo1, &mo2,
-                                buf == 0, rd);
+                                buf == 0, rd, g_row, cs);
                 continue;
             } else if constexpr (C::TS) {
                 epilogue_tma_store<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &mo0, &mo1, &mo2,
