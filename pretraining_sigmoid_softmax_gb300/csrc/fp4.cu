@@ -1,5 +1,7 @@
 // Quantisation to microscaled 4-bit floating point and back, and the dispatch of quantised rows
-// (the formats: fp4.cuh). All four are bound by memory.
+// (the formats: fp4.cuh). All four are bound by memory. They are launched behind one another
+// (launch_dependent), as are the GEMMs that read what they make: a token's chain of short kernels
+// is set up while the one before ends.
 #include <cuda_fp4.h>
 #include <cuda_runtime.h>
 
@@ -21,6 +23,8 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
     const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ X1,
     const int64_t* __restrict__ limit, int64_t rows, int cols, uint8_t* __restrict__ Q,
     uint8_t* __restrict__ S, float* __restrict__ G) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     constexpr int ROWS = kThreads / TPR;  // rows a CTA takes at a time
     static_assert(TPR <= 32 || TPR == kThreads, "a row in one warp or in the whole CTA");
     __shared__ uint32_t part[NV && TPR > 32 ? kThreads / 32 : 1];
@@ -107,6 +111,8 @@ template <bool NV, class Index>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(
     const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S, const float* __restrict__ G,
     const int64_t* __restrict__ limit, int64_t rows, int cols, __nv_bfloat16* __restrict__ out) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     const Index np = cols / 8;
     const int64_t ktiles = cols / Fp4<NV>::TILE_K;
     constexpr int PB = Fp4<NV>::BLOCK / 8;  // pieces of a block
@@ -174,6 +180,8 @@ template <bool NV, int NC>
 __global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
     const __nv_bfloat16* __restrict__ X0, const __nv_bfloat16* __restrict__ X1, int K0, int N, int KT,
     uint8_t* __restrict__ Qt, uint8_t* __restrict__ S, float* __restrict__ G, bool have_top) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     extern __shared__ __align__(16) uint8_t strip_smem[];
     constexpr int P = Strip<NC>::PITCH;
     constexpr int WORD_K = Fp4<NV>::TILE_K;
@@ -339,6 +347,8 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(
     const int64_t* __restrict__ row_offsets, int64_t T, int64_t rows, int d, int k, int ktiles,
     int64_t token_ctas, uint8_t* __restrict__ Xq, uint8_t* __restrict__ sX, float* __restrict__ gX,
     int* __restrict__ status) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     if (blockIdx.x >= token_ctas) {
         const int e = (int)(blockIdx.x - token_ctas) / kPadSplit, part = (int)(blockIdx.x - token_ctas) % kPadSplit;
         const int64_t hi = row_offsets[e + 1];
@@ -400,9 +410,8 @@ int launch_rows(const __nv_bfloat16* X, const __nv_bfloat16* X1, const int64_t* 
     int64_t blocks = cdiv(rows, kThreads / TPR);
     const int64_t cap = (int64_t)sm_count() * 16;
     if (blocks > cap) blocks = cap;
-    quantize_rows_kernel<NV, TPR, NIT><<<(unsigned)blocks, kThreads, 0, st>>>(X, X1, limit, rows, cols,
-                                                                             Q, S, g);
-    return launch_status();
+    return launch_dependent(quantize_rows_kernel<NV, TPR, NIT>, dim3((unsigned)blocks), dim3(kThreads), 0, st,
+                            X, X1, limit, rows, cols, Q, S, g);
 }
 
 template <bool NV>
@@ -434,22 +443,19 @@ int launch_cols(const __nv_bfloat16* X0, const __nv_bfloat16* X1, int E, int K0,
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MOE_ERR_LAUNCH;
-    kern<<<dim3((unsigned)(N / NC), (unsigned)cdiv(K, KT), (unsigned)E), kThreads, smem, st>>>(
-        X0, X1, K0, N, KT, Qt, S, g, have_top);
-    return launch_status();
+    return launch_dependent(kern, dim3((unsigned)(N / NC), (unsigned)cdiv(K, KT), (unsigned)E), dim3(kThreads),
+                            smem, st, X0, X1, K0, N, KT, Qt, S, g, have_top);
 }
 
 template <bool NV>
-void launch_dequantize(const uint8_t* Q, const uint8_t* S, const float* g, const int64_t* limit,
+int launch_dequantize(const uint8_t* Q, const uint8_t* S, const float* g, const int64_t* limit,
                        int64_t rows, int cols, __nv_bfloat16* out, cudaStream_t st) {
     const int64_t pieces = rows * (cols / 8);
     int64_t blocks = cdiv(pieces, 4 * kThreads);
     const int64_t cap = (int64_t)sm_count() * 32;
     if (blocks > cap) blocks = cap;
-    if (pieces < (int64_t(1) << 32))
-        dequantize_kernel<NV, uint32_t><<<(unsigned)blocks, kThreads, 0, st>>>(Q, S, g, limit, rows, cols, out);
-    else
-        dequantize_kernel<NV, int64_t><<<(unsigned)blocks, kThreads, 0, st>>>(Q, S, g, limit, rows, cols, out);
+    auto kern = pieces < (int64_t(1) << 32) ? dequantize_kernel<NV, uint32_t> : dequantize_kernel<NV, int64_t>;
+    return launch_dependent(kern, dim3((unsigned)blocks), dim3(kThreads), 0, st, Q, S, g, limit, rows, cols, out);
 }
 
 bool fmt_ok(int fmt) { return fmt == MOE_FP4_MX || fmt == MOE_FP4_NV; }
@@ -524,9 +530,9 @@ extern "C" int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const floa
     if (!aligned16(Q) || !aligned16(S) || !aligned16(out) || !aligned4(g)) return MOE_ERR_INVALID_ARG;
     if (!device_supported()) return MOE_ERR_UNSUPPORTED;
     auto* o = reinterpret_cast<__nv_bfloat16*>(out);
-    if (fmt == MOE_FP4_NV) launch_dequantize<true>(Q, S, g, rows_limit, rows, cols, o, (cudaStream_t)stream);
-    else launch_dequantize<false>(Q, S, g, rows_limit, rows, cols, o, (cudaStream_t)stream);
-    return launch_status();
+    return fmt == MOE_FP4_NV
+               ? launch_dequantize<true>(Q, S, g, rows_limit, rows, cols, o, (cudaStream_t)stream)
+               : launch_dequantize<false>(Q, S, g, rows_limit, rows, cols, o, (cudaStream_t)stream);
 }
 
 extern "C" int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float* gx,
@@ -547,8 +553,7 @@ extern "C" int moe_permute_fp4(const uint8_t* xq, const uint8_t* sx, const float
     cudaStream_t st = (cudaStream_t)stream;
     const int ktiles = d / (fmt == MOE_FP4_NV ? Fp4<true>::TILE_K : Fp4<false>::TILE_K);
     const int64_t token_ctas = cdiv(T, kThreads / 32);
-    permute_kernel<<<(unsigned)(token_ctas + (int64_t)E * kPadSplit), kThreads, 0, st>>>(
-        xq, sx, gx, slot_to_row, perm_token, row_offsets, T, rows, d, k, ktiles, token_ctas, Xq, sX, gX,
-        status);
-    return launch_status();
+    return launch_dependent(permute_kernel, dim3((unsigned)(token_ctas + (int64_t)E * kPadSplit)), dim3(kThreads),
+                            0, st, xq, sx, gx, slot_to_row, perm_token, row_offsets, T, rows, d, k, ktiles,
+                            token_ctas, Xq, sX, gX, status);
 }

@@ -109,7 +109,10 @@ struct NvScale {
     float s, rs;  // the scale and its rounded reciprocal; rs is 0 for a scale of 0
     __device__ __forceinline__ NvScale(uint32_t amax, const NvRow& row) {
         const float am = __uint_as_float(amax << 16) * row.inv;
-        byte = __nv_cvt_float_to_fp8(__fdiv_rn(am, 6.0f), __NV_SATFINITE, __NV_E4M3);
+        // RN(am / 6) by the rounded reciprocal and one correction (Markstein), as quot below
+        const float sixth = 1.0f / 6.0f, q0 = __fmul_rn(am, sixth);
+        const float q = __fmaf_rn(__fmaf_rn(-q0, 6.0f, am), sixth, q0);
+        byte = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
         s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
         rs = s > 0.f ? __frcp_rn(s) : 0.f;
         rinv = row.inv;

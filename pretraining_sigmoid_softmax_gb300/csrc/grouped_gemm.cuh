@@ -1108,6 +1108,10 @@ __device__ __forceinline__ void grouped_gemm_body(
         *S.abort_flag = 0;
         fence_mbar_init();
     }
+    if constexpr (C::FP4) {  // (launched behind its stream's previous kernel, as that one ends)
+        grid_launch_dependents();
+        grid_dependency_wait();
+    }
     if (P.row_offsets)
         for (int i = tid; i <= P.E; i += C::THREADS) S.offs[i] = P.row_offsets[i];
     if (C::WGRAD)
@@ -1524,7 +1528,7 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
         return MOE_ERR_LAUNCH;
     if constexpr (C::PAIR) {
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = 1;
@@ -1545,6 +1549,11 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
         if (pairs < 1) pairs = 1;
         cfg.gridDim = dim3(2 * (unsigned)pairs);
         cudaError_t rc;
+        if constexpr (C::FP4) {
+            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[1].val.programmaticStreamSerializationAllowed = 1;
+            cfg.numAttrs = 2;
+        }
         if constexpr (C::FP4)
             rc = cudaLaunchKernelEx(&cfg, kern, a0, a1, b0, b1, o0, o1, o2, sf[0], sf[1], sf[2], P);
         else
@@ -1555,12 +1564,14 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
         int64_t grid = sm_count();
         if (max_tiles < grid) grid = max_tiles;
         if (grid < 1) grid = 1;
-        if constexpr (C::FP4)
-            kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, st>>>(a0, a1, b0, b1, o0, o1, o2, sf[0],
-                                                                    sf[1], sf[2], P);
-        else
+        if constexpr (C::FP4) {
+            if (clusters == 0) resident[dev].store(1, std::memory_order_release);  // the attribute is set
+            return launch_dependent(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM_BYTES, st, a0,
+                                    a1, b0, b1, o0, o1, o2, sf[0], sf[1], sf[2], P);
+        } else {
             kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, st>>>(a0, a1, b0, b1, o0, o1, o2, P);
-        return launch_status();
+            return launch_status();
+        }
     }
 }
 
