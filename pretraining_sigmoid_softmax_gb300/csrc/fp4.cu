@@ -164,33 +164,38 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(
 
 // A CTA takes a strip of NC columns and KT rows through shared memory: all K rows in NV, whose columns'
 // largest values are needed first, so that X is read once; 256 rows in MX. A thread then makes the
-// codes of 32 K elements of one column (16 bytes: one block of 32 or two of 16), which go back
-// through shared memory to leave as whole lines. NV operands whose strips are too long for that
-// (K over kStripMaxK) get the columns' largest values from a pass of its own.
+// codes of 32 K elements (a piece) of two neighbouring columns, whose values lie in one word a row;
+// they go back through shared memory to leave as whole lines. NV operands whose strips are too long
+// for that (K over kStripMaxK) get the columns' largest values from a pass of its own.
 constexpr int kStripRowsMx = 256;
+constexpr int kStripRowsNv = 512;  // after that pass
 constexpr int kStripMaxK = 3328;
 
-// One row of a strip in shared memory: NC columns, padded so that consecutive rows start in other banks.
+// A strip in shared memory, in words of two columns: rows padded by one word and pieces of 32 rows by
+// NC / 2, so that the rows a warp's lanes read at once, 32 apart, lie in different banks.
 template <int NC>
 struct Strip {
-    static constexpr int PITCH = NC + 2;  // 16-bit elements
+    static constexpr int W = NC / 2;
+    static constexpr int PIECE = 32 * (W + 1) + W;
+    __device__ __forceinline__ static int word(int r) { return r / 32 * PIECE + r % 32 * (W + 1); }
+    static size_t bytes(int rows) { return (size_t)rows / 32 * PIECE * 4; }
 };
 
 template <bool NV, int NC>
 __global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
     const __nv_bfloat16* __restrict__ X0, const __nv_bfloat16* __restrict__ X1, int K0, int N, int KT,
-    uint8_t* __restrict__ Qt, uint8_t* __restrict__ S, float* __restrict__ G, bool have_top) {
+    uint8_t* __restrict__ Qt, uint8_t* __restrict__ S, float* __restrict__ G, bool have_g) {
     grid_launch_dependents();
     grid_dependency_wait();
     extern __shared__ __align__(16) uint8_t strip_smem[];
-    constexpr int P = Strip<NC>::PITCH;
+    using L = Strip<NC>;
     constexpr int WORD_K = Fp4<NV>::TILE_K;
-    uint16_t* tile = reinterpret_cast<uint16_t*>(strip_smem);  // [KT][P]
+    uint32_t* tile = reinterpret_cast<uint32_t*>(strip_smem);
     __shared__ uint32_t top[NC];
     const int K = X1 ? 2 * K0 : K0;
     const int e = blockIdx.z, n0 = blockIdx.x * NC, k0 = blockIdx.y * KT;
     const int kn = min(KT, K - k0);  // a multiple of 128
-    if (NV && threadIdx.x < NC) top[threadIdx.x] = have_top ? __float_as_uint(G[(int64_t)e * N + n0 + threadIdx.x]) : 0u;
+    if (NV && threadIdx.x < NC) top[threadIdx.x] = 0;
     if (NV) __syncthreads();
     // in: 16 bytes (8 columns) a thread and row
     constexpr int V = NC / 8;
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
         for (int u = 0; u < U; ++u) {
             const int r = r0 + u * (kThreads / V);
             if (r >= kn) break;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(tile + r * P + 8 * c8);
+            uint32_t* dst = tile + L::word(r) + 4 * c8;
             dst[0] = v[u].x;
             dst[1] = v[u].y;
             dst[2] = v[u].z;
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
                                absmax2(m.w, v[u].w));
         }
     }
-    if (NV && !have_top) {  // a warp's rows first, or its lanes would queue at the same few words
+    if (NV && !have_g) {  // a warp's rows first, or its lanes would queue at the same few words
         uint32_t w[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -234,60 +239,78 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_cols_kernel(
         }
     }
     __syncthreads();
-    // codes: column n, 32 rows from 32 q on. NC columns x kThreads / NC pieces at a time; the codes of
-    // a round replace the rows they were made of (a column's piece of 16 bytes in the round's rows)
-    constexpr int QN = kThreads / NC;  // pieces of 32 rows a round
-    const int n = threadIdx.x % NC;
-    const int64_t r = (int64_t)e * N + n0 + n;
-    NvRow row(0);
+    // codes: columns 2 p and 2 p + 1, rows from 32 q on; QN pieces a round, whose codes then take the
+    // place of the rows they were made of
+    constexpr int QN = kThreads / L::W;
+    const int p = threadIdx.x % L::W;
+    const int64_t r = (int64_t)e * N + n0 + 2 * p;
+    NvRow row0(0), row1(0);
     if (NV) {
-        if (have_top) {  // G holds the rows' powers of two already
-            row.g = __uint_as_float(top[n]);
-            row.inv = 1.0f / row.g;  // of a power of two: exact
+        if (have_g) {
+            row0.g = G[r], row1.g = G[r + 1];
+            row0.inv = 1.0f / row0.g, row1.inv = 1.0f / row1.g;  // of powers of two: exact
         } else {
-            row = NvRow(top[n]);
-            if (threadIdx.x < NC) G[r] = row.g;
+            row0 = NvRow(top[2 * p]), row1 = NvRow(top[2 * p + 1]);
+            if (threadIdx.x < L::W) G[r] = row0.g, G[r + 1] = row1.g;
         }
     }
     for (int q0 = 0; q0 < kn / 32; q0 += QN) {
-        const int q = q0 + threadIdx.x / NC;
-        const bool in = q < kn / 32;
-        uint4 code = make_uint4(0, 0, 0, 0);
-        if (in) {
-            uint4 v[4];
+        const int np = min(QN, kn / 32 - q0);  // pieces of this round
+        const int q = threadIdx.x / L::W;
+        uint32_t code[2][4] = {};
+        if (q < np) {
+            const uint32_t* src = tile + L::word(32 * (q0 + q)) + p;
+            const int64_t kk = k0 + 32 * (q0 + q);
+            uint8_t* s0 = S + fp4_scale_word(r, kk / WORD_K, K / WORD_K) + kk % WORD_K / Fp4<NV>::BLOCK;
+            uint8_t* s1 = S + fp4_scale_word(r + 1, kk / WORD_K, K / WORD_K) + kk % WORD_K / Fp4<NV>::BLOCK;
+            constexpr int B = Fp4<NV>::BLOCK;
+            uint32_t bytes0 = 0, bytes1 = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
+            for (int h = 0; h < 32 / B; ++h) {  // blocks of the piece
+                uint32_t v[B], am = 0;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint16_t* src = tile + (32 * q + 8 * j + 2 * h) * P + n;
-                    w[h] = src[0] | ((uint32_t)src[P] << 16);
+                for (int i = 0; i < B; ++i) {
+                    v[i] = src[(h * B + i) * (L::W + 1)];
+                    am = absmax2(am, v[i]);
                 }
-                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                auto make = [&](const auto& sa, const auto& sb) {
+                    bytes0 |= sa.byte << (8 * h);
+                    bytes1 |= sb.byte << (8 * h);
+#pragma unroll
+                    for (int j = 0; j < B / 8; ++j) {
+                        float a[8], b[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            a[i] = sa.quot(bf16_lo(v[8 * j + i]));
+                            b[i] = sb.quot(bf16_hi(v[8 * j + i]));
+                        }
+                        code[0][h * (B / 8) + j] = sa.finish(fp4_codes8(a));
+                        code[1][h * (B / 8) + j] = sb.finish(fp4_codes8(b));
+                    }
+                };
+                if constexpr (NV) make(NvScale(am & 0xffffu, row0), NvScale(am >> 16, row1));
+                else make(MxScale(am & 0xffffu), MxScale(am >> 16));
             }
-            const uint32_t a = halves_max(absmax8(absmax8(0u, v[0]), v[1]));
-            const uint32_t b = halves_max(absmax8(absmax8(0u, v[2]), v[3]));
-            const int64_t kk = k0 + 32 * q;
-            uint8_t* word = S + fp4_scale_word(r, kk / WORD_K, K / WORD_K);
             if constexpr (NV) {
-                const NvScale sa(a, row), sb(b, row);
-                code = make_uint4(sa.codes(v[0]), sa.codes(v[1]), sb.codes(v[2]), sb.codes(v[3]));
-                *reinterpret_cast<uint16_t*>(word + kk % WORD_K / 16) = (uint16_t)(sa.byte | (sb.byte << 8));
+                *reinterpret_cast<uint16_t*>(s0) = (uint16_t)bytes0;
+                *reinterpret_cast<uint16_t*>(s1) = (uint16_t)bytes1;
             } else {
-                const MxScale sc(max(a, b));
-                code = make_uint4(sc.codes(v[0]), sc.codes(v[1]), sc.codes(v[2]), sc.codes(v[3]));
-                word[kk % WORD_K / 32] = (uint8_t)sc.byte;
+                *s0 = (uint8_t)bytes0;
+                *s1 = (uint8_t)bytes1;
             }
         }
         __syncthreads();  // every row of this round has been read
-        // the round's codes, QN pieces of 16 bytes a column, in the place of its rows
-        uint4* out = reinterpret_cast<uint4*>(tile + 32 * q0 * P);  // 4 P bytes a row pair: 16-aligned
-        out[n * (QN + 1) + threadIdx.x / NC] = code;
+        uint4* out = reinterpret_cast<uint4*>(tile + L::word(32 * q0));  // pieces are multiples of 16 bytes
+        if (q < np) {
+            out[2 * p * (np + 1) + q] = make_uint4(code[0][0], code[0][1], code[0][2], code[0][3]);
+            out[(2 * p + 1) * (np + 1) + q] = make_uint4(code[1][0], code[1][1], code[1][2], code[1][3]);
+        }
         __syncthreads();
-        const int piece = threadIdx.x % QN, col = threadIdx.x / QN;
-        if (q0 + piece < kn / 32)
+        for (int i = threadIdx.x; i < NC * np; i += kThreads) {
+            const int col = i / np, piece = i - col * np;
             *reinterpret_cast<uint4*>(Qt + ((int64_t)e * N + n0 + col) * (K / 2) + (k0 + 32 * (q0 + piece)) / 2) =
-                out[col * (QN + 1) + piece];
+                out[col * (np + 1) + piece];
+        }
     }
 }
 
@@ -437,14 +460,14 @@ int rows_by_width(const __nv_bfloat16* X, const __nv_bfloat16* X1, const int64_t
 
 template <bool NV, int NC>
 int launch_cols(const __nv_bfloat16* X0, const __nv_bfloat16* X1, int E, int K0, int N, int K, int KT,
-                uint8_t* Qt, uint8_t* S, float* g, bool have_top, cudaStream_t st) {
-    const size_t smem = (size_t)KT * Strip<NC>::PITCH * 2;
+                uint8_t* Qt, uint8_t* S, float* g, bool have_g, cudaStream_t st) {
+    const size_t smem = Strip<NC>::bytes(KT);
     auto kern = quantize_cols_kernel<NV, NC>;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MOE_ERR_LAUNCH;
     return launch_dependent(kern, dim3((unsigned)(N / NC), (unsigned)cdiv(K, KT), (unsigned)E), dim3(kThreads),
-                            smem, st, X0, X1, K0, N, KT, Qt, S, g, have_top);
+                            smem, st, X0, X1, K0, N, KT, Qt, S, g, have_g);
 }
 
 template <bool NV>
@@ -518,7 +541,7 @@ extern "C" int moe_quantize_cols_fp4(const moe_bf16* X0, const moe_bf16* X1, int
         x0, x1, K0, N, reinterpret_cast<uint32_t*>(g));
     column_g_kernel<<<(unsigned)cdiv(n, 256), 256, 0, st>>>(g, n);
     if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
-    return launch_cols<true, 16>(x0, x1, E, K0, N, K, 512, Qt, S, g, true, st);
+    return launch_cols<true, 16>(x0, x1, E, K0, N, K, kStripRowsNv, Qt, S, g, true, st);
 }
 
 extern "C" int moe_dequantize_fp4(const uint8_t* Q, const uint8_t* S, const float* g,

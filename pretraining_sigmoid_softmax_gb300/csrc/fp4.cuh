@@ -68,6 +68,8 @@ struct MxScale {
         byte = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
         inv = __uint_as_float(e == 255 ? 0x3f800000u : (254u - byte) << 23);
     }
+    __device__ __forceinline__ float quot(float x) const { return x * inv; }
+    __device__ __forceinline__ uint32_t finish(uint32_t codes) const { return codes; }
     __device__ __forceinline__ uint32_t codes(const uint4 w) const {
         const float v[8] = {bf16_lo(w.x) * inv, bf16_hi(w.x) * inv, bf16_lo(w.y) * inv,
                             bf16_hi(w.y) * inv, bf16_lo(w.z) * inv, bf16_hi(w.z) * inv,
@@ -128,7 +130,10 @@ struct NvScale {
         const float v[8] = {quot(bf16_lo(w.x)), quot(bf16_hi(w.x)), quot(bf16_lo(w.y)),
                             quot(bf16_hi(w.y)), quot(bf16_lo(w.z)), quot(bf16_hi(w.z)),
                             quot(bf16_lo(w.w)), quot(bf16_hi(w.w))};
-        return s > 0.f ? fp4_codes8(v) : 0u;  // no sign either under a scale of 0
+        return finish(fp4_codes8(v));
+    }
+    __device__ __forceinline__ uint32_t finish(uint32_t codes) const {
+        return s > 0.f ? codes : 0u;  // no sign either under a scale of 0
     }
 };
 
