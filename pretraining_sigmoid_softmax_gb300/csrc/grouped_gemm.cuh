@@ -23,7 +23,7 @@
 //            fused elementwise step, bf16 outputs. Token-major outputs (G1, G2, B2, B4) are
 //            packed into swizzled shared-memory boxes and written by TMA stores; B2 reads
 //            its saved a and u through TMA-staged boxes; weight gradients store per thread.
-//            Two warps per quadrant double the loads and stores in flight; GEMMs with a
+//            Two warps per quadrant double the loads and stores in flight; bf16 GEMMs with a
 //            reduction of at most 1024 (G1) or 512 (G2) take four per quadrant (warps 4-19), as their main
 //            loop is shorter than eight warps' epilogue of the previous tile.
 // Pair mode (a cluster of two CTAs on two SMs): the leading CTA issues
@@ -133,7 +133,7 @@ struct Cfg {
     static constexpr int NOUT = EPI == kEpiSwigluFwd ? 3 : EPI == kEpiSwigluBwd ? 2 : 1;
     // output columns per staged chunk: 16, or 32 (single-output epilogues of short-K GEMMs,
     // where the per-chunk fence and store issue dominate) at the same shared-memory size
-    // (E2M1: 64 columns a box, whole 128-byte lines, in two buffers a warp; see epilogue_fp4)
+    // (E2M1: 64 columns a box, whole 128-byte lines, in one or two buffers a warp; see epilogue_fp4)
     static constexpr int OCOLS =  // (E2M1 with AU: from a's and u's own buffers)
         FP4 ? (AU ? AUC : BN / (EW / 4) < 64 ? BN / (EW / 4) : 64) : OC_;
     static_assert(FP4 || OCOLS == 16 || (OCOLS == 32 && NOUT == 1 && !AU), "output chunk width");
@@ -686,8 +686,9 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
 // A tile's main loop is a quarter of the bf16 one's, so the number of rows that the TMA stores
 // move and the time from a tile's last instruction until its columns are free set the pace. Boxes are
 // up to 64 columns x 32 rows, whole 128-byte lines (with 16-column boxes the gate and up projections
-// of experts of 768 took 1144 us, with 64-column ones 540), and sixteen warps (twelve for 192
-// columns) take one box's columns each.
+// of experts of 768 took 1144 us, with 64-column ones 540). Eight warps take 64 (gate and up) or 128
+// columns each, twelve 64 of 192 columns; a warp reads its shared columns, or all of them where they
+// fit in registers, before it packs any, so that the next tile's instructions wait for the loads only.
 
 // Byte offset of 16-byte piece j of row r in a 128-byte-swizzled box of 128-byte rows.
 __device__ __forceinline__ int sw128_offset(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }

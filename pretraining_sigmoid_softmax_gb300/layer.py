@@ -291,6 +291,8 @@ class MoEPlan:
         self.W = (W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d)
         softmax = s.mode == ops.MODE_SOFTMAX
         main = stream if stream is not None else torch.cuda.current_stream()
+        if weights4 is not None and not s.fp4:
+            raise ValueError("weights4 is for a layer of 4-bit experts")
         if s.fp8 and not codes:  # before the fork: the routed rows and the shared expert both
             ops.moe_quantize_rows_fp8(x, None, self.x8, self.sx, stream)  # use them
         W4 = None
@@ -353,6 +355,9 @@ class MoEPlan:
     def _weights4(self, given, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, stream):
         """The 4-bit operands of the weights: those given, or this plan's, made anew."""
         if given is not None:
+            if len(given) != (6 if self.s.f_shared else 3):
+                raise ValueError(f"weights4 has {len(given)} operands, the layer "
+                                 f"{6 if self.s.f_shared else 3} weights")
             return given
         if self.W4 is None:
             self.W4 = weights4(self.s.fp4_format, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, stream)
@@ -748,7 +753,8 @@ class MoELayer(torch.nn.Module):
     (``fp4_format`` "nv" or "mx"), "fp8_dgrad" and "fp4_dgrad" the backward's data gradients too. For
     serving on 4-bit weights, ``hold_weights()`` quantises them once: forwards then take these codes,
     keep nothing for a backward and are refused where a gradient is asked for, until
-    ``hold_weights(False)``. Call it again after the weights have changed."""
+    ``hold_weights(False)``. Call it again after the weights have changed: the new codes take the old
+    ones' place, so a graph captured while they were held goes on with the new ones."""
 
     def __init__(self, d, E, k, f, f_shared=0, mode="sigmoid", z_coef=0.0, gamma=1e-3,
                  device="cuda", bias_rule="sign", aux_switch=0.0, aux_seq=0.0, seq_len=0,
@@ -800,11 +806,17 @@ class MoELayer(torch.nn.Module):
 
     @torch.no_grad()
     def hold_weights(self, hold=True):
-        """Quantises the weights to 4 bits now and lets forwards use them until ``hold_weights(False)``."""
+        """Quantises the weights to 4 bits now and lets forwards use them until ``hold_weights(False)``,
+        which frees them: a graph captured while they were held is not replayed after that."""
         if not self.fp4:
             raise ValueError("weights are held by a layer of precision fp4 or fp4_dgrad")
-        self._held = (weights4(self.fp4_format, self.W_g, self.W_u, self.W_d, self.Ws_g, self.Ws_u,
-                               self.Ws_d) if hold else None)
+        W = (self.W_g, self.W_u, self.W_d, self.Ws_g, self.Ws_u, self.Ws_d)
+        if not hold:
+            self._held = None
+        elif self._held is None or self._held[0].q.device != self.W_g.device:
+            self._held = weights4(self.fp4_format, *W)
+        else:
+            _quantize_weights4(self._held, W)
 
     def _plan(self, T):
         """The plan of a token count; one without a backward while the weights are held."""

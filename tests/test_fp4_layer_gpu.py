@@ -185,6 +185,42 @@ def test_held_weights_give_the_same_output(name, fmt):
     assert x.grad is not None
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_a_captured_forward_follows_weights_held_again(fmt):
+    layer, x = _layer("shared", "fp4", fmt)
+    layer.hold_weights()
+    with torch.no_grad():
+        for _ in range(2):
+            layer(x)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = layer(x)
+        for _ in range(3):
+            for w in (layer.W_g, layer.W_d, layer.Ws_u):
+                w.copy_(torch.randn_like(w) * 0.1)
+            layer.hold_weights()
+            graph.replay()
+            got = out.clone()
+            want = layer(x)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
+def test_plans_refuse_other_weights():
+    layer, x = _layer("shared", "fp4", "mx")
+    W = [getattr(layer, n).detach() for n in ("W_g", "W_u", "W_d", "Ws_g", "Ws_u", "Ws_d")]
+    plan = MoEPlan(layer._plan(x.shape[0]).s, backward=False)
+    with pytest.raises(ValueError, match="3 operands"):
+        plan.forward(x, layer.W_r.detach(), layer.b, *W, weights4=weights4(ops.FP4_MX, *W[:3]))
+    with pytest.raises(ops.MoEError, match="format"):
+        plan.forward(x, layer.W_r.detach(), layer.b, *W, weights4=weights4(ops.FP4_NV, *W))
+    bf16, x = _layer("shared", "bf16", "mx")
+    plan = MoEPlan(bf16._plan(x.shape[0]).s, backward=False)
+    with pytest.raises(ValueError, match="4-bit"):
+        plan.forward(x, layer.W_r.detach(), layer.b, *W, weights4=weights4(ops.FP4_MX, *W))
+
+
 def test_serving_tokens_one_by_one_equals_the_batch():
     """Rows do not depend on one another: tokens alone give what they give in a batch."""
     layer, x = _layer("sigmoid", "fp4", "mx")
