@@ -107,7 +107,7 @@ int swiglu(const Operand& X, const int64_t* row_offsets, int E, int64_t rows, in
     if (!code_map(&mx, X.q, d, rows) || !code_map(&mg, Wg.q, d, (uint64_t)E * f) ||
         !code_map(&mu, Wu.q, d, (uint64_t)E * f) || !scale_map<NV>(&sf[0], X.s, d, rows) ||
         !scale_map<NV>(&sf[1], Wg.s, d, (int64_t)E * f) || !scale_map<NV>(&sf[2], Wu.s, d, (int64_t)E * f) ||
-        !out_maps(mo, A ? A : H, U ? U : H, H, f, rows, G::G1::OCOLS))
+        !out_maps(mo, A ? A : H, U, A ? H : nullptr, f, rows, G::G1::OCOLS))
         return MOE_ERR_LAUNCH;
     Params P = base_params(row_offsets, rows, E);
     P.N = f;

@@ -394,7 +394,7 @@ def _ws(ws, dev):
 
 def _rows(name, t):
     """The shape of a 2-D tensor; both sizes at least 1."""
-    if t is None or t.dim() != 2 or 0 in t.shape:
+    if t is None or t.dim() != 2 or t.numel() == 0:
         raise MoEError(f"{name} must be a 2-D tensor with at least one row and column"
                        + ("" if t is None else f", got shape {tuple(t.shape)}"))
     return t.shape
@@ -617,8 +617,8 @@ def _fp4(name, m, shape, fmt, dev):
     q, s, g = m.q, m.s, m.g
     u8 = torch.uint8
     if (cols % 128 == 0 and rows > 0 and q.dtype is u8 and q.shape == (*lead, cols // 2)
-            and q.is_contiguous() and q.get_device() == dev and s.dtype is u8 and s.dim() == 1
-            and s.numel() == (rows + 127) // 128 * cols * (8 if fmt == FP4_NV else 4)
+            and q.is_contiguous() and q.get_device() == dev and s.dtype is u8
+            and s.shape == ((rows + 127) // 128 * cols * (8 if fmt == FP4_NV else 4),)
             and s.is_contiguous() and s.get_device() == dev):
         if g is None:
             if fmt == FP4_MX:
@@ -642,8 +642,11 @@ def _fp4_rows(name, m):
     """The element shape of a 2-D operand, its format and the device of the call."""
     if m is None:
         raise MoEError(f"{name} is missing")
-    rows, half = _rows(f"{name}.q", m.q)
-    return rows, 2 * half, m.fmt, _device(m.q)
+    q = m.q
+    if q is None or q.dim() != 2 or q.numel() == 0:
+        _rows(f"{name}.q", q)
+    rows, half = q.shape
+    return rows, 2 * half, m.fmt, _device(q)
 
 
 def _fp4_stack(name, m):
@@ -716,7 +719,9 @@ def moe_dequantize_fp4(m, out, rows_limit=None, stream=None):
 def moe_permute_fp4(x, slot_to_row, perm_token, row_offsets, X, stream=None):
     """The token rows of the operand x copied to their experts' rows of the operand X."""
     T, d, fmt, dev = _fp4_rows("x", x)
-    R = _fp4_rows("X", X)[0]
+    if X is None:
+        raise MoEError("X is missing")
+    R = _rows("X.q", X.q)[0]
     if row_offsets is None or row_offsets.numel() < 2:
         raise MoEError("row_offsets must be [E + 1]")
     k, E, i32 = _rows("slot_to_row", slot_to_row)[1], row_offsets.numel() - 1, torch.int32
