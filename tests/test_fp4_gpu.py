@@ -137,7 +137,9 @@ def test_codes_at_the_ends_of_the_range(fmt):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("E,K0,N,stack", [(1, 128, 128, False), (3, 256, 384, True), (5, 384, 256, False),
                                           (2, 1024, 128, True), (2, 3456, 128, False),
-                                          (1, 1792, 256, True), (1, 1664, 128, True)])
+                                          (1, 1792, 256, True), (1, 1664, 128, True),
+                                          (3, 256, 128, False), (2, 640, 128, False),
+                                          (1, 768, 384, False)])
 def test_column_codes_are_bit_exact(E, K0, N, stack, fmt):
     mats = [torch.stack([rows_in(K0, N, 7 * e + i) for e in range(E)]) for i in range(2 if stack else 1)]
     if E > 1:
