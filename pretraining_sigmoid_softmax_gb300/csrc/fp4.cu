@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
 // The numbers that codes stand for: E2M1 * scale (* g), one rounding to bf16, which is exact (the
 // product has at most 6 significant bits) unless it leaves bf16's range. A thread makes 8 numbers,
 // 16 bytes, so that a warp's store is one run of 512 (with 32 bytes a thread the two stores of a
-// sector's halves made 65,535 x 4096 134 us). `Index` counts pieces of 8; 32 bits where they do.
+// sector's halves made 65,535 x 4096 134 us; now 114, 0.88 of the copy rate, the issue slots 80% in use).
+// `Index` counts pieces of 8; 32 bits where they do.
 template <bool NV, class Index>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(
     const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S, const float* __restrict__ G,
@@ -167,6 +168,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(
 // codes of 32 K elements (a piece) of two neighbouring columns, whose values lie in one word a row;
 // they go back through shared memory to leave as whole lines. NV operands whose strips are too long
 // for that (K over kStripMaxK) get the columns' largest values from a pass of its own.
+// 128 stacks of 1536 x 2048 (MX): 186 us, 0.80 of the copy rate over 1.0 GB. 64 matrices of 1024 x 256
+// (NV): 19 us over 43 MB; a CTA loads, then computes, and few CTAs are at a time in either.
 constexpr int kStripRowsMx = 256;
 constexpr int kStripRowsNv = 512;  // after that pass
 constexpr int kStripMaxK = 3328;
@@ -357,7 +360,9 @@ __global__ void column_g_kernel(float* __restrict__ G, int64_t n) {
 
 // ---------------------------------------------------------- dispatch of quantised rows
 // Codes and scales of a row depend on that row alone, so those of an expert-major row are its
-// token's: a warp copies a token's codes and scale words to its k rows.
+// token's: a warp copies a token's codes and scale words to its k rows. 32,768 tokens of 2048 to 8 rows each
+// (MX): 68 us for 0.34 GB (0.73 of the copy rate; the scale words, 4 bytes each, are what slows it:
+// gathered into whole tiles by their destination they took longer).
 // The CTAs behind those take the padding rows of each segment (the trailing rows with perm_token < 0;
 // at most MOE_ROW_ALIGN - 1 per expert): zero codes, scales of zero bits and g = 1, as quantising a
 // zero row gives.
