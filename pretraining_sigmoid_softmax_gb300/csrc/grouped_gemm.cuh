@@ -693,25 +693,26 @@ __device__ __forceinline__ void epilogue_tma_store(const SmemLayout& S, const Ti
 // Byte offset of 16-byte piece j of row r in a 128-byte-swizzled box of 128-byte rows.
 __device__ __forceinline__ int sw128_offset(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-// NV: the powers of two of a warp's columns (of each accumulator) into its place in shared memory, and
-// that of this thread's row; then an accumulator chunk of 32 columns times both.
+// NV: the powers of two of a tile's columns (of each accumulator) on their way into this warp's place in
+// shared memory; that of this thread's row is returned. They are asked for as soon as those of the tile
+// before have been used: where a tile has few stages, its main loop would not cover their latency
+// (8191 tokens through 8 of 64 experts of 1024 x 256: 107 us a pass, 109 with them fetched as a tile
+// begins; 115 in its epilogue).
 template <class C>
-__device__ __forceinline__ float fetch_powers(float* cs, const Params& P, const TileInfo& ti, int64_t row,
+__device__ __forceinline__ float start_powers(float* cs, const Params& P, const TileInfo& ti, int row_in_tile,
                                               int c_lo, int lane) {
     constexpr int kCols = C::BN / (C::EW / 4);
+    static_assert(C::CS_FLOATS <= 128, "one copy a lane");
     __syncwarp();  // the previous tile's have been used
-#pragma unroll
-    for (int i = 0; i < (C::CS_FLOATS / 4 + 31) / 32; ++i) {
-        const int j = 4 * (lane + 32 * i);  // of gate, then of up
-        const int c = ti.n0 + c_lo + j % kCols;
-        if (j < C::CS_FLOATS && c < P.N)
-            *reinterpret_cast<float4*>(cs + j) = __ldg(reinterpret_cast<const float4*>(
-                (C::DUAL && j >= kCols ? P.sb1 : P.sb0) + (int64_t)ti.e * P.N + c));
-    }
-    const float g = __ldg(P.sa + row);
-    __syncwarp();
-    return g;
+    if (ti.m0 >= ti.row_end) return 1.0f;
+    const int j = 4 * lane;  // of gate, then of up
+    const int c = ti.n0 + c_lo + j % kCols;
+    if (j < C::CS_FLOATS && c < P.N)
+        cp_async16(cs + j, (C::DUAL && j >= kCols ? P.sb1 : P.sb0) + (int64_t)ti.e * P.N + c);
+    const int64_t r = ti.m0 + row_in_tile;
+    return __ldg(P.sa + (r < ti.row_end ? r : ti.row_end - 1));
 }
+// Then an accumulator chunk of 32 columns times both.
 __device__ __forceinline__ void apply_powers(float* v, float g, const float* cs) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -759,17 +760,19 @@ __device__ __forceinline__ void arrive_read(uint32_t bar, int lane) {
     else mbar_arrive(bar);
 }
 
-template <class C>
+// next_powers(): called once the tile's powers of two have been used (NV).
+template <class C, class Next>
 __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo& ti, uint32_t t_acc,
                                              int lane, int slot, int c_lo, int64_t row0, const Params& P,
                                              const CUtensorMap* mo0, const CUtensorMap* mo1,
                                              const CUtensorMap* mo2, bool reversed, const Readers& rd,
-                                             float g_row, const float* cs) {
+                                             float g_row, const float* cs, const Next& next_powers) {
     constexpr int kCols = C::BN / (C::EW / 4);    // of this warp (in each accumulator)
     // nothing to write: the half of a pair's tile past its segment, columns past the outputs
     if (ti.m0 >= ti.row_end || (C::BN % 128 && ti.n0 + c_lo >= P.N)) {
         if (C::OV && rd.shared) arrive_read<C>(rd.shared_bar, lane);
         arrive_read<C>(rd.whole_bar, lane);
+        next_powers();
         return;
     }
     // rows past row_end (the tail of an unpadded layout) are clipped by the store
@@ -794,6 +797,7 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
                 apply_powers(reinterpret_cast<float*>(g[k]), g_row, cs + 32 * k);
                 apply_powers(reinterpret_cast<float*>(u[k]), g_row, cs + kCols + 32 * k);
             }
+            next_powers();
         }
 #pragma unroll
         for (int o = 0; o < 3; ++o) {  // a, u, h
@@ -854,7 +858,10 @@ __device__ __forceinline__ void epilogue_fp4(const SmemLayout& S, const TileInfo
                 __syncwarp();
             }
             float* v = reinterpret_cast<float*>(r[i]);
-            if constexpr (C::NV) apply_powers(v, g_row, cs + c - c_lo);
+            if constexpr (C::NV) {
+                apply_powers(v, g_row, cs + c - c_lo);
+                if (i == kHalves - 1) next_powers();
+            }
             if (P.r1_row) add_router_term<32>(v, P, row, ti, c);
             uint32_t w[16];
 #pragma unroll
@@ -1010,12 +1017,13 @@ __device__ __forceinline__ void au_issue_fp4(const SmemLayout& S, const CUtensor
     }
 }
 
-template <class C>
+template <class C, class Next>
 __device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileInfo& ti,
                                                uint32_t t_acc, int q, int lane, int slot, int c_lo,
                                                const Params& P, const CUtensorMap* mda,
                                                const CUtensorMap* mdu, uint32_t local,
-                                               volatile int* abort_flag, float g_row, const float* cs) {
+                                               volatile int* abort_flag, float g_row, const float* cs,
+                                               const Next& next_powers) {
     const int64_t row0 = ti.m0 + 32 * q;
     const int64_t row = row0 + lane < ti.row_end ? row0 + lane : ti.row_end - 1;
     const bool store = row0 < ti.row_end;  // as in swiglu_bwd_staged
@@ -1029,11 +1037,13 @@ __device__ __forceinline__ bool swiglu_bwd_fp4(const SmemLayout& S, const TileIn
                                P.status, P.wait_limit_ns, 34) && ok;
         tmem_ld_wait();
         if (!__all_sync(0xffffffffu, ok)) return false;
-        if (!store || ti.n0 + c >= P.N) continue;  // warp-uniform; N may end inside the last tile
+        const bool in = store && ti.n0 + c < P.N;  // warp-uniform; N may end inside the last tile
+        if (C::NV && in) apply_powers(reinterpret_cast<float*>(acc), g_row, cs + c - c_lo);
+        if (C::NV && b == kAuBufs - 1) next_powers();
+        if (!in) continue;
         uint8_t* abuf = S.au + ((size_t)slot * kAuBufs + b) * C::AU_BUF_BYTES;
         uint8_t* ubuf = abuf + C::AU_BUF_BYTES / 2;
         float* r = reinterpret_cast<float*>(acc);
-        if constexpr (C::NV) apply_powers(r, g_row, cs + c - c_lo);
         uint32_t wa[16], wu[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1352,8 +1362,24 @@ __device__ __forceinline__ void grouped_gemm_body(
         const int slot = warp - 4;
         uint32_t n_au = 0;  // staged a/u chunks consumed by this warp
         int local = 0, expert = 0;
+        float* cs = S.cs + slot * C::CS_FLOATS;
+        TileInfo following{};  // NV: the next tile
+        float g_row = 1.0f, g_next = 1.0f;
+        if constexpr (C::NV) {
+            if (first_tile < ntiles) {
+                following = next_tile<C>(first_tile, expert, P, S, rank);
+                g_next = start_powers<C>(cs, P, following, row_in_tile, c_lo, lane);
+            }
+        }
         for (int64_t tile = first_tile; tile < ntiles; tile += tile_step, ++local) {
-            const TileInfo ti = next_tile<C>(tile, expert, P, S, rank);
+            const TileInfo ti = C::NV ? following : next_tile<C>(tile, expert, P, S, rank);
+            const bool more = C::NV && tile + tile_step < ntiles;
+            if (more) following = next_tile<C>(tile + tile_step, expert, P, S, rank);
+            g_row = g_next;
+            auto next_powers = [&] {
+                if constexpr (C::NV)
+                    if (more) g_next = start_powers<C>(cs, P, following, row_in_tile, c_lo, lane);
+            };
             const int buf = local & 1;
             const uint32_t ph = (local >> 1) & 1;
             Readers rd{};
@@ -1376,23 +1402,20 @@ __device__ __forceinline__ void grouped_gemm_body(
                         au_issue<C>(S, &ma1, &mb1, slot, n_au + i, ti.m0 + 32 * q,
                                     ti.n0 + c_lo + i * kAuCols);
             }
-            float* cs = S.cs + slot * C::CS_FLOATS;
-            float g_row = 1.0f;
-            if constexpr (C::NV) {
-                const int64_t r = ti.m0 + row_in_tile;
-                if (ti.m0 < ti.row_end)
-                    g_row = fetch_powers<C>(cs, P, ti, r < ti.row_end ? r : ti.row_end - 1, c_lo, lane);
-            }
             bool ok = mbar_wait_bounded(smem_u32(&S.tfull[buf]), ph, abort_flag, P.status,
                                         P.wait_limit_ns, 33);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
+            if constexpr (C::NV) {
+                cp_async_wait_all();
+                __syncwarp();
+            }
             const uint32_t t_acc =
                 tmem_base + (buf ? C::ACC1 : C::ACC0) + ((uint32_t)(32 * q) << 16);
             if constexpr (C::AU && C::FP4) {
                 if (!swiglu_bwd_fp4<C>(S, ti, t_acc, q, lane, slot, c_lo, P, &mo0, &mo1,
-                                       (uint32_t)local, abort_flag, g_row, cs))
+                                       (uint32_t)local, abort_flag, g_row, cs, next_powers))
                     break;
             } else if constexpr (C::AU) {
                 if (!swiglu_bwd_staged<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &ma1, &mb1,
@@ -1400,7 +1423,7 @@ __device__ __forceinline__ void grouped_gemm_body(
                     break;
             } else if constexpr (C::FP4) {
                 epilogue_fp4<C>(S, ti, t_acc, lane, slot, c_lo, ti.m0 + 32 * q, P, &mo0, &mo1, &mo2,
-                                buf == 0, rd, g_row, cs);
+                                buf == 0, rd, g_row, cs, next_powers);
                 continue;
             } else if constexpr (C::TS) {
                 epilogue_tma_store<C>(S, ti, t_acc, q, lane, slot, c_lo, kCols, P, &mo0, &mo1, &mo2,
@@ -1419,6 +1442,7 @@ __device__ __forceinline__ void grouped_gemm_body(
                 else mbar_arrive(smem_u32(&S.tempty[buf]));
             }
         }
+        if constexpr (C::NV) cp_async_wait_all();  // (a wait that ran out leaves one under way)
         if constexpr (C::TS) {
             if (lane == 0) bulk_wait<0>();  // this warp's stores are complete
         }
