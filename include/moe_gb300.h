@@ -158,6 +158,7 @@ int moe_route(const moe_bf16* x, const float* W_r, const float* b, int64_t T, in
  *      layout, multiples of 128); perm_token [moe_padded_rows] int32 (token of each row,
  *      -1 for padding rows); slot_to_row [T,k] int32 (row of slot (t,i));
  *      X_perm [moe_padded_rows, d] bf16 (x rows in the permuted layout, padding rows 0).
+ * x and X_perm may both be NULL: the layout alone (for rows that are dispatched as codes).
  * Optional (both or neither, else MOE_ERR_INVALID_ARG): topk_gate [T,k] fp32 in, row_gate
  *      [moe_padded_rows] fp32 out: the gate of each row's slot, 0 on padding rows (what
  *      moe_row_gates writes, for the gate folded into the experts), formed in the same pass.

@@ -115,19 +115,19 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(
 constexpr int kPadSplit = 16;
 
 // Padding rows of expert e's segment, share `split` of kPadSplit: perm_token = -1, a zero row
-// of buf and (optionally) a zero row gate.
+// of buf (unless it is null) and (optionally) a zero row gate.
 __device__ __forceinline__ void pad_rows_share(const int64_t* __restrict__ row_offsets,
                                                const int32_t* __restrict__ counts, int d,
                                                int32_t* __restrict__ perm_token,
                                                __nv_bfloat16* __restrict__ buf,
                                                float* __restrict__ row_gate, int e, int split) {
     const int64_t lo = row_offsets[e] + counts[e], hi = row_offsets[e + 1];
-    const int vec_per_row = d / 8;
+    const int vec_per_row = buf ? d / 8 : 1;
     for (int64_t i = (int64_t)split * blockDim.x + threadIdx.x; i < (hi - lo) * vec_per_row;
          i += (int64_t)kPadSplit * blockDim.x) {
         const int64_t r = lo + i / vec_per_row;
         const int c = (int)(i % vec_per_row);
-        reinterpret_cast<uint4*>(buf + r * d)[c] = make_uint4(0, 0, 0, 0);
+        if (buf) reinterpret_cast<uint4*>(buf + r * d)[c] = make_uint4(0, 0, 0, 0);
         if (c == 0) {
             if (perm_token) perm_token[r] = -1;
             if (row_gate) row_gate[r] = 0.f;
@@ -543,8 +543,8 @@ extern "C" int moe_permute(const int32_t* topk_idx, const moe_bf16* x, int64_t T
                            int32_t* perm_token, int32_t* slot_to_row, moe_bf16* X_perm,
                            const float* topk_gate, float* row_gate, void* ws, size_t ws_bytes,
                            moe_stream_t stream) {
-    if (!topk_idx || !x || !counts || !offsets || !row_offsets || !perm_token || !slot_to_row ||
-        !X_perm)
+    if (!topk_idx || !counts || !offsets || !row_offsets || !perm_token || !slot_to_row ||
+        (x == nullptr) != (X_perm == nullptr))
         return MOE_ERR_INVALID_ARG;
     if ((topk_gate == nullptr) != (row_gate == nullptr)) return MOE_ERR_INVALID_ARG;
     if (!shape_ok(T, d, E, k)) return MOE_ERR_INVALID_ARG;
@@ -564,6 +564,7 @@ extern "C" int moe_permute(const int32_t* topk_idx, const moe_bf16* x, int64_t T
     scatter_kernel<<<(unsigned)(nb + (int64_t)E * kPadSplit), kScatterThreads, 0, st>>>(
         topk_idx, T, E, k, nb, bbase, row_offsets, counts, d, perm_token, slot_to_row,
         reinterpret_cast<__nv_bfloat16*>(X_perm), topk_gate, row_gate);
+    if (!X_perm) return launch_status();  // the layout alone
     gather_kernel<<<warp_grid(T), 256, 0, st>>>(reinterpret_cast<const __nv_bfloat16*>(x),
                                                 slot_to_row, T, d, k,
                                                 reinterpret_cast<__nv_bfloat16*>(X_perm));

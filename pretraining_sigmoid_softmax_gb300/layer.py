@@ -117,9 +117,9 @@ class MoEPlan:
         self.row_offsets = _empty((E + 1,), i64, dev)
         self.perm_token = _empty((R,), i32, dev)
         self.slot_to_row = _empty((T, k), i32, dev)
-        self.X_perm = _empty((R, d), bf, dev)
-        # a and u are kept for a backward (the 4-bit experts can leave them out)
+        # the bf16 rows, a and u are kept for a backward (the 4-bit experts can leave them out)
         self.keeps = backward or not s.fp4
+        self.X_perm = _empty((R, d), bf, dev) if self.keeps else None
         self.A = _empty((R, f), bf, dev) if self.keeps else None
         self.U = _empty((R, f), bf, dev) if self.keeps else None
         self.H = _empty((R, f), bf, dev)
@@ -250,7 +250,7 @@ class MoEPlan:
         n += 1 if s.selects else 0                          # choice within groups
         if s.has_aux:
             n += 2 + (1 if backward else 0)                 # balancing losses (+ gradient)
-        n += 4                                              # permute (the padding rows and
+        n += 4 if self.keeps else 3                         # permute (the padding rows and
                                                             # folded row gates in the scatter)
         if s.fp8 or s.fp4:  # quantise x, W_g, W_u, W_d; expert-major codes (2); G1, quantise H, G2
             n += 9 + (6 if s.f_shared else 0)               # (shared: its weights, G1, H, G2)
@@ -319,7 +319,7 @@ class MoEPlan:
         # the combine's gate weights move before the (linear) down projection: the routed
         # experts emit g * y directly, and the combine adds rows without weights; the
         # dispatch copies each slot's gate to its row as it places the row
-        ops.moe_permute(self.topk_idx, x, s.E, self.counts, self.offsets, self.row_offsets,
+        ops.moe_permute(self.topk_idx, x if self.keeps else None, s.E, self.counts, self.offsets, self.row_offsets,
                         self.perm_token, self.slot_to_row, self.X_perm, self.ws, stream,
                         topk_gate=self.topk_gate if self.fold_gate else None,
                         row_gate=self.row_gate)

@@ -90,8 +90,9 @@ def moe_route(x, W_r, b, k, mode, z_coef, logits, topk_idx, topk_gate, topk_scor
 
 def moe_permute(topk_idx, x, E, counts, offsets, row_offsets, perm_token, slot_to_row, X_perm,
                 ws, stream=None, topk_gate=None, row_gate=None):
+    """x and X_perm None: the layout alone."""
     T, k = topk_idx.shape
-    d = x.shape[1]
+    d = ROW_ALIGN if x is None else x.shape[1]
     _contig(topk_idx, x, counts, offsets, row_offsets, perm_token, slot_to_row, X_perm, ws)
     if row_gate is not None:
         _contig(topk_gate, row_gate)

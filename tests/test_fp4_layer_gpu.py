@@ -336,6 +336,52 @@ def test_launch_count_matches_the_plan(name, fmt, precision):
     assert len([n for n in kernels if "moe::" in n]) == plan.launches_per_step()
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_launch_count_without_a_backward(fmt):
+    from torch.autograd import DeviceType
+    from torch.profiler import ProfilerActivity, profile
+    layer, x = _layer("shared", "fp4", fmt)
+    W = [getattr(layer, n).detach() for n in ("W_g", "W_u", "W_d", "Ws_g", "Ws_u", "Ws_d")]
+    plan = MoEPlan(layer._plan(x.shape[0]).s, backward=False)
+    assert plan.X_perm is None
+    plan.forward(x, layer.W_r.detach(), layer.b, *W)
+    torch.cuda.synchronize()
+    kernels = []
+    for _ in range(2):  # the profiler's first session in a process may record no activity
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            plan.forward(x, layer.W_r.detach(), layer.b, *W)
+            torch.cuda.synchronize()
+        kernels = [e.name for e in prof.events() if e.device_type == DeviceType.CUDA]
+        if kernels:
+            break
+    if not kernels:
+        pytest.skip("the profiler recorded no CUDA activity on this machine")
+    assert len([n for n in kernels if "moe::" in n]) == plan.launches_per_step(backward=False)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (700, 16, 4)])
+def test_layout_without_its_rows(T, E, k):
+    torch.manual_seed(T)
+    idx = torch.rand(T, E, device="cuda").topk(k, 1).indices.to(torch.int32)
+    gate, R, i32, i64 = torch.rand(T, k, device="cuda"), ops.moe_padded_rows(T, k, E), torch.int32, torch.int64
+    ws = torch.empty(ops.moe_workspace_bytes(T, 128, E, k), dtype=torch.uint8, device="cuda")
+    x = torch.randn(T, 128, device="cuda").to(torch.bfloat16)
+    outs = []
+    for rows in (True, False):
+        o = [torch.full(n, -7, dtype=t, device="cuda") for n, t in (
+            ((E,), i32), ((E + 1,), i64), ((E + 1,), i64), ((R,), i32), ((T, k), i32))]
+        g = torch.full((R,), -7.0, device="cuda")
+        ops.moe_permute(idx, x if rows else None, E, *o,
+                        torch.empty(R, 128, dtype=torch.bfloat16, device="cuda") if rows else None, ws,
+                        topk_gate=gate, row_gate=g)
+        outs.append(o + [g])
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    with pytest.raises(ops.MoEError, match="invalid"):
+        ops.moe_permute(idx, x, E, *o, None, ws)
+
+
 def test_layer_refuses_unknown_formats_and_weights_to_hold():
     with pytest.raises(ValueError, match="fp4_format"):
         MoELayer(128, 4, 2, 128, precision="fp4", fp4_format="e2m1")
