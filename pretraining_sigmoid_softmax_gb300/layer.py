@@ -91,6 +91,8 @@ class MoEPlan:
         s = self.s = shape
         if s.fp4 and s.fp8:
             raise ValueError("the experts' operands are fp8 or fp4, not both")
+        if s.fp4_dgrad and (s.fp8_dgrad or not s.fp4):
+            raise ValueError("fp4_dgrad is for fp4 experts, without fp8_dgrad")
         dev = torch.device(device)
         bf, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
         T, d, E, k, f, fs = s.T, s.d, s.E, s.k, s.f, s.f_shared
@@ -388,6 +390,7 @@ class MoEPlan:
         x = self.x
         W_r, b, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d = self.W
         main = stream if stream is not None else torch.cuda.current_stream()
+        formed = False  # whether the logit gradient was formed before the rows that take its term
         if s.f_shared and self.overlap:  # fork: the shared expert's backward on the side stream
             self.side.wait_stream(main)
             self._shared_backward(dY, x, Ws_g, Ws_u, Ws_d, self.side)
@@ -412,6 +415,7 @@ class MoEPlan:
             ops.moe_quantize_cols_fp8(W_g, W_u, self.Wguq_t, self.sWgu_t, stream)
             if self.router_rows:  # the gate gradient is known: the logit gradient first
                 self._route_bwd(x, None, stream)
+                formed = True
             self._gemm(ops.moe_expert_bwd_fp8, self.dYq, self.sdY, self.dY_perm, self.X_perm,
                        self.A, self.U, self.H, self.row_offsets, self.Wdq_t, self.sWd_t,
                        self.Wguq_t, self.sWgu_t, self.dX_perm, self.dA, self.dU, self.AUq,
@@ -426,6 +430,7 @@ class MoEPlan:
             ops.moe_quantize_cols_fp4(W_g, W_u, self.Wgu4_t, stream)
             if self.router_rows:
                 self._route_bwd(x, None, stream)
+                formed = True
             self._gemm(ops.moe_expert_bwd_fp4, self.dY4, self.dY_perm, self.X_perm, self.A, self.U,
                        self.H, self.row_offsets, self.Wd4_t, self.Wgu4_t, self.dX_perm, self.dA,
                        self.dU, self.AU4, self.dW_g, self.dW_u, self.dW_d, self.ws, stream=stream,
@@ -444,8 +449,7 @@ class MoEPlan:
                                  s.aux_seq, self.dlogits_aux, stream)
             extra = self.dlogits_aux
         rows = self.router_rows
-        formed = s.fp8_dgrad or s.fp4_dgrad  # (those paths formed the logit gradient above)
-        if not (rows and formed):
+        if not formed:
             self._route_bwd(x, extra, stream)
         if rows and not formed:
             self._gemm(ops.moe_expert_bwd, self.dY_perm, self.X_perm, self.A, self.U, self.H,
