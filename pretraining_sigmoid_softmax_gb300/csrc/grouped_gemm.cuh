@@ -712,7 +712,8 @@ __device__ __forceinline__ float start_powers(float* cs, const Params& P, const 
     const int64_t r = ti.m0 + row_in_tile;
     return __ldg(P.sa + (r < ti.row_end ? r : ti.row_end - 1));
 }
-// Then an accumulator chunk of 32 columns times both.
+// Then an accumulator chunk of 32 columns times both, as one number: exact, or scale_in_place has been there
+// first and both are 1.
 __device__ __forceinline__ void apply_powers(float* v, float g, const float* cs) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -722,6 +723,48 @@ __device__ __forceinline__ void apply_powers(float* v, float g, const float* cs)
         v[4 * q + 2] *= g * w.z;
         v[4 * q + 3] *= g * w.w;
     }
+}
+
+// A power is 2^-126 to 2^118, so that a row's times a column's can leave fp32's range where the scaled sum
+// does not: sums of zeros would be NaN under 2^89 and 2^89, one of 2^30 would be 0 under 2^-102 and
+// 2^-49. Whether this warp's all lie within 2^63 of 1, whose products are exact (the same for all lanes).
+template <class C>
+__device__ __forceinline__ bool powers_multiply(const float* cs, float g, int lane) {
+    const float lo = 0x1p-63f, hi = 0x1p63f;
+    bool ok = g >= lo && g <= hi;
+    if (4 * lane < C::CS_FLOATS) {
+        const float4 w = reinterpret_cast<const float4*>(cs)[lane];
+        ok = ok && w.x >= lo && w.x <= hi && w.y >= lo && w.y <= hi && w.z >= lo && w.z <= hi &&
+             w.w >= lo && w.w <= hi;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+// Where they do not, the tile's part of this warp (t_warp: its columns of the first accumulator) is scaled in
+// tensor memory before its epilogue, 32 columns at a time, and ones take the place of the powers. Powers
+// on different sides of 1 are multiplied first, which is exact; those on the same side one after the
+// other, each taking the sum further the same way. Out of line, for the registers of the epilogues: 8191
+// tokens through 8 of 64 experts of 1024 x 256 take 113 us a pass (111 without the question), 115 with
+// this inlined and 122 with the choice made among the accumulators that an epilogue holds.
+template <class C>
+__device__ __noinline__ void scale_in_place(uint32_t t_warp, float g, float* cs, int lane) {
+    constexpr int kCols = C::BN / (C::EW / 4);
+#pragma unroll 1
+    for (int j = 0; j < C::CS_FLOATS; j += 32) {  // of gate, then of up
+        const uint32_t at = t_warp + (C::DUAL && j >= kCols ? C::BN - kCols : 0) + j;
+        uint32_t r[32];
+        tmem_ld32(at, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float v = __uint_as_float(r[i]), w = cs[j + i];
+            r[i] = __float_as_uint((g < 1.0f) == (w < 1.0f) ? v * g * w : v * (g * w));
+        }
+        tmem_st32(at, r);
+    }
+    tmem_st_wait();
+    __syncwarp();  // every lane has used the powers
+    if (4 * lane < C::CS_FLOATS) reinterpret_cast<float4*>(cs)[lane] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    __syncwarp();
 }
 
 // 32 packed columns of this thread's row into its place in a box of C::OCOLS columns.
@@ -1402,17 +1445,25 @@ __device__ __forceinline__ void grouped_gemm_body(
                         au_issue<C>(S, &ma1, &mb1, slot, n_au + i, ti.m0 + 32 * q,
                                     ti.n0 + c_lo + i * kAuCols);
             }
+            bool apart = false;  // NV: powers that are not multiplied with one another
+            if constexpr (C::NV) {
+                cp_async_wait_all();
+                __syncwarp();
+                if (ti.m0 < ti.row_end && (C::BN % 128 == 0 || ti.n0 + c_lo < P.N))  // (else it has none)
+                    apart = !powers_multiply<C>(cs, g_row, lane);
+            }
             bool ok = mbar_wait_bounded(smem_u32(&S.tfull[buf]), ph, abort_flag, P.status,
                                         P.wait_limit_ns, 33);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            if constexpr (C::NV) {
-                cp_async_wait_all();
-                __syncwarp();
-            }
             const uint32_t t_acc =
                 tmem_base + (buf ? C::ACC1 : C::ACC0) + ((uint32_t)(32 * q) << 16);
+            if constexpr (C::NV)
+                if (apart) {
+                    scale_in_place<C>(t_acc + c_lo, g_row, cs, lane);
+                    g_row = 1.0f;
+                }
             if constexpr (C::AU && C::FP4) {
                 if (!swiglu_bwd_fp4<C>(S, ti, t_acc, q, lane, slot, c_lo, P, &mo0, &mo1,
                                        (uint32_t)local, abort_flag, g_row, cs, next_powers))
