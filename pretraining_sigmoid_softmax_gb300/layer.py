@@ -282,6 +282,11 @@ class MoEPlan:
             n += 1
         return n
 
+    def buffers(self):
+        """This plan's own tensors (not the inputs and weights that it was last given)."""
+        own = _tensors([v for n, v in vars(self).items() if n not in ("x", "W")])
+        return list({id(t): t for t in own}.values())
+
     # ------------------------------------------------------------------ forward
     def forward(self, x, W_r, b, W_g, W_u, W_d, Ws_g=None, Ws_u=None, Ws_d=None, stream=None,
                 codes=False, weights4=None):
@@ -568,6 +573,15 @@ class MoEPlan:
         return g
 
 
+def _tensors(v):
+    """The tensors in nested lists and tuples."""
+    if isinstance(v, torch.Tensor):
+        yield v
+    elif isinstance(v, (list, tuple)):
+        for u in v:
+            yield from _tensors(u)
+
+
 def _quantize_weights4(out, W, stream=None):
     for m, w in zip(out, (w for w in W if w is not None)):
         ops.moe_quantize_rows_fp4(w.reshape(-1, w.shape[-1]),
@@ -758,7 +772,14 @@ class MoELayer(torch.nn.Module):
     serving on 4-bit weights, ``hold_weights()`` quantises them once: forwards then take these codes,
     keep nothing for a backward and are refused where a gradient is asked for, until
     ``hold_weights(False)``. Call it again after the weights have changed: the new codes take the old
-    ones' place, so a graph captured while they were held goes on with the new ones."""
+    ones' place, so a graph captured while they were held goes on with the new ones (on the stream of the
+    forwards, or ordered with it). Plans for serving are dropped too, those used longest ago first, once
+    they take more than ``HELD_PLAN_BYTES``; one that a graph was captured on stays until
+    ``hold_weights(False)``."""
+
+    # Bytes of the plans of held weights that are kept beside the last forward's, captured ones not counted.
+    # A plan of the large layer (d 4096, 64 experts of 1536) takes 0.12 GB for a few tokens, 7.7 for 65,536.
+    HELD_PLAN_BYTES = 16 << 30
 
     def __init__(self, d, E, k, f, f_shared=0, mode="sigmoid", z_coef=0.0, gamma=1e-3,
                  device="cuda", bias_rule="sign", aux_switch=0.0, aux_seq=0.0, seq_len=0,
@@ -807,6 +828,7 @@ class MoELayer(torch.nn.Module):
         self._plans = {}
         self._last_plan = None
         self._held = None  # 4-bit operands of the weights, while they are held
+        self._held_streams = set()  # on which forwards have used them
 
     @torch.no_grad()
     def hold_weights(self, hold=True):
@@ -816,17 +838,61 @@ class MoELayer(torch.nn.Module):
             raise ValueError("weights are held by a layer of precision fp4 or fp4_dgrad")
         W = (self.W_g, self.W_u, self.W_d, self.Ws_g, self.Ws_u, self.Ws_d)
         if not hold:
-            self._held = None
-        elif self._held is None or self._held[0].q.device != self.W_g.device:
+            self._release_held()
+            return
+        if self._held is not None and self._held[0].q.device != self.W_g.device:
+            self._release_held()
+        if self._held is None:
             self._held = weights4(self.fp4_format, *W)
         else:
             _quantize_weights4(self._held, W)
+
+    def _held_plans(self):
+        return [(key, plan) for key, plan in self._plans.items() if isinstance(key, tuple)]
+
+    def _drop(self, key):
+        """Lets go of a plan. Its memory goes to others behind what forwards have put on their streams."""
+        self._after_forwards(self._plans.pop(key).buffers())
+
+    def _after_forwards(self, tensors):
+        for stream_id, index, kind in self._held_streams:
+            st = torch.cuda.Stream(stream_id=stream_id, device_index=index, device_type=kind)
+            for t in tensors:
+                if t.is_cuda and t.device.index == index:
+                    t.record_stream(st)
+
+    def _release_held(self):
+        plans = self._held_plans()
+        if any(plan.captured for _, plan in plans):
+            torch.cuda.synchronize(self._held[0].q.device)  # replays that are under way, on any stream
+        last = self._last_plan
+        if any(plan is last for _, plan in plans):  # what update_bias and the losses read of it remains
+            self._last_plan = object.__new__(MoEPlan)
+            vars(self._last_plan).update({n: v for n, v in vars(last).items()
+                                          if n in ("s", "counts", "z_loss", "aux_loss")})
+        for key, _ in plans:
+            self._drop(key)
+        self._after_forwards(list(_tensors(self._held)))
+        self._held = None
+        self._held_streams.clear()
+
+    def _limit_held_plans(self, newest):
+        """Drops the plans of held weights that were used longest ago, down to HELD_PLAN_BYTES."""
+        old = [(key, sum(t.untyped_storage().nbytes() for t in plan.buffers()))
+               for key, plan in self._held_plans() if plan is not newest and not plan.captured]
+        total = sum(n for _, n in old)
+        for key, n in old:
+            if total <= self.HELD_PLAN_BYTES:
+                break
+            self._drop(key)
+            total -= n
 
     def _plan(self, T):
         """The plan of a token count; one without a backward while the weights are held."""
         serving = self._held is not None
         key = (T, "held") if serving else T
-        if key not in self._plans:
+        plan = self._plans.get(key)
+        if plan is None:
             shape = MoEShape(T, self.d, self.E, self.k, self.f, self.f_shared, self.mode,
                              self.z_coef, self.aux_switch, self.aux_seq, self.seq_len or T,
                              self.fp8, self.fp8_dgrad, self.n_group, self.topk_group,
@@ -834,8 +900,16 @@ class MoELayer(torch.nn.Module):
                              self.fp4_format)
             plan = MoEPlan(shape, self.W_g.device, backward=not serving)
             plan.generation = 0
+            plan.captured = False
             self._plans[key] = plan
-        return self._plans[key]
+            if serving and not torch.cuda.is_current_stream_capturing():
+                self._limit_held_plans(plan)
+        if serving:
+            self._plans[key] = self._plans.pop(key)  # the last one used
+            plan.captured = plan.captured or torch.cuda.is_current_stream_capturing()
+            st = torch.cuda.current_stream(self.W_g.device)
+            self._held_streams.add((st.stream_id, st.device_index, st.device_type))
+        return plan
 
     def forward(self, x, residual=None):
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:

@@ -40,3 +40,142 @@ def test_a_backward_forms_every_gradient_whatever_the_flags():
     for n, g in got[False].items():
         assert torch.isfinite(g).all() and torch.equal(got[True][n], g), n
     assert ops.moe_device_status() == (0, 0)
+
+
+# ----------------------------------------------------------------- plans of held weights
+
+def _serving(f_shared=128, **kw):
+    torch.manual_seed(2)
+    layer = MoELayer(256, 8, 2, 128, f_shared, precision="fp4", **kw)
+    layer.hold_weights()
+    return layer
+
+
+def _x(T, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(100 * seed + T)
+    return torch.randn(T, 256, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def _bytes(plan):
+    return sum(t.untyped_storage().nbytes() for t in plan.buffers())
+
+
+@torch.no_grad()
+def test_a_plan_owns_what_it_allocates():
+    """buffers() are all of a plan's memory, and neither the inputs nor the weights."""
+    layer = _serving()
+    before = torch.cuda.memory_allocated()
+    plan = MoEPlan(layer._plan(40).s, backward=False)
+    del layer._plans[40, "held"]
+    torch.cuda.synchronize()
+    grown = torch.cuda.memory_allocated() - before
+    assert _bytes(plan) <= grown <= _bytes(plan) + 512 * len(plan.buffers())  # allocations are of 512 bytes
+    x, W = _x(40), [getattr(layer, n).detach() for n in ("W_g", "W_u", "W_d", "Ws_g", "Ws_u", "Ws_d")]
+    n = len(plan.buffers())
+    plan.forward(x, layer.W_r.detach(), layer.b, *W, weights4=layer._held)
+    assert len(plan.buffers()) == n
+    assert not any(t is u for t in plan.buffers() for u in [x, *W])
+
+
+@torch.no_grad()
+def test_batches_of_every_size_keep_a_bounded_number_of_plans():
+    layer = _serving()
+    want = {T: layer(_x(T)).clone() for T in (1, 2, 3)}
+    one = _bytes(layer._plans[3, "held"])
+    layer.HELD_PLAN_BYTES = 4 * one + one // 2
+    kept = []
+    for T in list(range(4, 40)) + [1, 2, 3, 2, 1]:
+        out = layer(_x(T))
+        if T in want:
+            assert torch.equal(out, want[T])
+        held = layer._held_plans()
+        kept.append(len(held))
+        assert held[-1][0] == (T, "held") and layer._last_plan is held[-1][1]
+        assert sum(_bytes(p) for _, p in held[:-1]) <= layer.HELD_PLAN_BYTES
+    assert max(kept) <= 5 and kept[-1] >= 4
+    assert [k for k, _ in layer._held_plans()][-3:] == [(3, "held"), (2, "held"), (1, "held")]
+    layer.HELD_PLAN_BYTES = 0
+    layer(_x(50))
+    assert len(layer._held_plans()) == 1
+
+
+@torch.no_grad()
+def test_released_weights_leave_no_plans_and_no_memory():
+    layer = _serving(mode="softmax", z_coef=1e-3)
+    layer.hold_weights(False)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    layer.hold_weights()
+    for T in (3, 300, 5):
+        layer(_x(T))
+    z = layer.z_loss().clone()
+    assert torch.cuda.memory_allocated() > before + _bytes(layer._plans[300, "held"])
+    layer.hold_weights(False)
+    torch.cuda.synchronize()
+    assert layer._held is None and not layer._held_plans()
+    assert torch.cuda.memory_allocated() <= before + 4096     # the losses and counts of the last forward
+    assert torch.equal(layer.z_loss(), z) and layer.aux_loss() is None
+    layer.hold_weights(False)                                 # nothing more to release
+    layer.hold_weights()
+    assert torch.equal(layer(_x(5)), layer(_x(5)))
+
+
+@torch.no_grad()
+def test_the_last_counts_move_the_bias_after_the_release():
+    a, b = _serving(), _serving()
+    a(_x(70)), b(_x(70))
+    a.update_bias()
+    b.hold_weights(False)
+    b.update_bias()
+    assert a.b.any() and torch.equal(a.b, b.b)
+
+
+@torch.no_grad()
+def test_captured_plans_stay():
+    """A graph's buffers are not given to others while the weights are held, however many plans follow."""
+    layer = _serving()
+    layer.HELD_PLAN_BYTES = 0
+    x = _x(9)
+    layer(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x)
+    for T in (1, 2, 3, 200):
+        torch.full((4 << 20,), float("nan"), device="cuda")
+        layer(_x(T))
+    assert [k[0] for k, _ in layer._held_plans()] == [9, 200]
+    for seed in (1, 2):
+        x.copy_(_x(9, seed))
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, layer(_x(9, seed)))
+    layer.hold_weights(False)
+    assert not layer._held_plans()
+
+
+@torch.no_grad()
+def test_dropped_plans_of_another_stream_are_not_given_away_early():
+    """A forward waits on its stream while its plan is dropped and others ask for memory: its output is that
+    of a forward left alone. So with its weights' codes, released meanwhile."""
+    layer = _serving(f_shared=0)
+    want = layer(_x(33)).clone()
+    layer.HELD_PLAN_BYTES = 0
+    side, x = torch.cuda.Stream(), _x(33)
+    layer(_x(34))                                             # the plan of 33 is gone
+    plan = layer._plan(33)                                    # made on this stream, used on another
+    sizes = [t.untyped_storage().nbytes() for t in plan.buffers() + list(layer._held[0][:2])]
+    del plan
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                        # 0.1 s of clock cycles
+        out = layer(x)
+    layer(_x(35))
+    assert [k[0] for k, _ in layer._held_plans()] == [35]
+    layer.hold_weights(False)
+    assert not side.query()                                   # the forward is still under way
+    noise = [torch.full((n,), 0x77, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(noise) == 2 * len(sizes)
+    assert ops.moe_device_status() == (0, 0)
