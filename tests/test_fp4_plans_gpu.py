@@ -2,10 +2,13 @@
 import pytest
 import torch
 
+from oracle import moe_oracle as O
 from pretraining_sigmoid_softmax_gb300 import ops
 from pretraining_sigmoid_softmax_gb300.layer import MoELayer, MoEPlan, MoEShape
 
 from gpu_common import require_gpu
+from test_fp4_layer_gpu import REL, _off
+from test_fp4_layer_gpu import reference as step_in_64_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +182,93 @@ def test_dropped_plans_of_another_stream_are_not_given_away_early():
     torch.cuda.synchronize()
     assert torch.equal(out, want) and len(noise) == 2 * len(sizes)
     assert ops.moe_device_status() == (0, 0)
+
+
+# ------------------------------------------------------- branches of the step in 4 bits
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("precision", ["fp4", "fp4_dgrad"])
+@pytest.mark.parametrize("kw", [dict(mode="softmax", z_coef=10.0, aux_switch=100.0),
+                                dict(aux_switch=100.0, aux_seq=50.0, seq_len=64, f=768),
+                                dict(mode="softmax", z_coef=10.0, aux_seq=100.0, seq_len=128, f_shared=128)])
+def test_router_losses_beside_4_bit_experts(kw, precision, fmt):
+    """The z-loss and the balancing losses enter the router's gradient and x's, as in 64 bits; the bound
+    is that of the step without them (test_fp4_layer_gpu)."""
+    T, kw = 256, {"f": 128, **kw}
+    torch.manual_seed(4)
+    layer = MoELayer(256, 8, 2, precision=precision, fp4_format=fmt, **kw)
+    x = _x(T).requires_grad_(True)
+    dout = 0.02 * torch.randn_like(x)
+    layer(x).backward(dout)
+    torch.cuda.synchronize()
+    idx = layer._last_plan.topk_idx.long()
+    want, dx, grads = step_in_64_bits(layer, x.detach(), idx, dout)
+    x64, W_r = x.detach().double(), layer.W_r.detach().double()
+    l = x64 @ W_r.t()
+    mode = O.SOFTMAX if layer.mode == ops.MODE_SOFTMAX else O.SIGMOID
+    dl = torch.from_numpy(O.aux_losses_backward(l.cpu().numpy(), idx.cpu().numpy(), mode, layer.seq_len or T,
+                                                layer.aux_switch, layer.aux_seq)).cuda()
+    if layer.z_coef:
+        dl = dl + layer.z_coef * 2 / T * torch.logsumexp(l, 1, keepdim=True) * torch.softmax(l, 1)
+    alone = dl.t() @ x64
+    assert alone.norm() > 4 * REL * grads["W_r"].norm()        # left out, it would be seen
+    assert _off(x.grad, dx + dl @ W_r) <= REL
+    grads["W_r"] = grads["W_r"] + alone
+    for n, p in layer.named_parameters():
+        assert _off(p.grad, grads[n]) <= REL, n
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("precision", ["fp4", "fp4_dgrad"])
+def test_shared_expert_on_one_stream_or_two(precision, fmt):
+    """The shared expert beside the routed ones (small layers) or behind them (large ones): the same bits."""
+    torch.manual_seed(5)
+    layer = MoELayer(384, 8, 2, 256, 384, precision=precision, fp4_format=fmt)
+    x, dY, W = _inputs(layer, 515)
+    got = []
+    for overlap in (False, True):
+        plan = MoEPlan(layer._plan(515).s, overlap_shared=overlap)
+        assert (plan.ws_side is plan.ws) is not overlap
+        for g in plan.grads().values():
+            g.fill_(float("nan"))
+        for _ in range(2):
+            plan.forward(x, layer.W_r.detach(), layer.b, *W)
+            plan.backward(dY)
+        torch.cuda.synchronize()
+        got.append({"out": plan.out, **plan.grads()})
+    for n, t in got[0].items():
+        assert torch.isfinite(t).all() and torch.equal(t, got[1][n]), n
+    held = MoEPlan(layer._plan(515).s, backward=False, overlap_shared=False)
+    held.forward(x, layer.W_r.detach(), layer.b, *W)
+    torch.cuda.synchronize()
+    assert torch.equal(held.out, got[0]["out"])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("d,f,f_shared", [(3328, 128, 0), (3456, 128, 128), (128, 1792, 0), (128, 1664, 1792)])
+def test_launch_count_with_long_columns(d, f, f_shared, fmt):
+    """NV columns of more than 3328 elements take three kernels each."""
+    from torch.autograd import DeviceType
+    from torch.profiler import ProfilerActivity, profile
+    torch.manual_seed(6)
+    layer = MoELayer(d, 4, 2, f, f_shared, precision="fp4_dgrad", fp4_format=fmt)
+    x, dY, W = _inputs(layer, 60)
+    plan = MoEPlan(layer._plan(60).s)
+
+    def step():
+        plan.forward(x, layer.W_r.detach(), layer.b, *W)
+        plan.backward(dY)
+
+    step()
+    torch.cuda.synchronize()
+    kernels = []
+    for _ in range(2):  # the profiler's first session in a process may record no activity
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            step()
+            torch.cuda.synchronize()
+        kernels = [e.name for e in prof.events() if e.device_type == DeviceType.CUDA]
+        if kernels:
+            break
+    if not kernels:
+        pytest.skip("the profiler recorded no CUDA activity on this machine")
+    assert len([n for n in kernels if "moe::" in n]) == plan.launches_per_step()
