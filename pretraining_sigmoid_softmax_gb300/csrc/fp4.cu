@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(
 // they go back through shared memory to leave as whole lines. NV operands whose strips are too long
 // for that (K over kStripMaxK) get the columns' largest values from a pass of its own.
 // 128 stacks of 1536 x 2048 (MX): 186 us, 0.80 of the copy rate over 1.0 GB. 64 matrices of 1024 x 256
-// (NV): 19 us over 43 MB; a CTA loads, then computes, and few CTAs are at a time in either.
+// (NV): 23 us over 43 MB; a CTA loads, then computes, and few CTAs are at a time in either.
 constexpr int kStripRowsMx = 256;
 constexpr int kStripRowsNv = 512;  // after that pass
 constexpr int kStripMaxK = 3328;
@@ -456,7 +456,7 @@ int rows_by_width(const __nv_bfloat16* X, const __nv_bfloat16* X1, const int64_t
     // many narrow rows: few threads each, so that none idles
     if (width <= 512 && rows >= 256 * (int64_t)sm_count()) {
         if (width <= 256) return launch_rows<NV, 8, 2>(X, X1, limit, rows, cols, Q, S, g, st);
-        if (width <= 512) return launch_rows<NV, 16, 2>(X, X1, limit, rows, cols, Q, S, g, st);
+        return launch_rows<NV, 16, 2>(X, X1, limit, rows, cols, Q, S, g, st);
     }
     if (width <= 1024) return launch_rows<NV, 32, 2>(X, X1, limit, rows, cols, Q, S, g, st);
     if (width <= 2048) return launch_rows<NV, 32, 4>(X, X1, limit, rows, cols, Q, S, g, st);
@@ -541,7 +541,9 @@ extern "C" int moe_quantize_cols_fp4(const moe_bf16* X0, const moe_bf16* X1, int
                                       false, st);
     // short columns: as many of them as give the threads a piece each (NC / 2 * K / 32 pieces). 16.8 M
     // elements in columns of 256: 33 us in strips of 16, 23 of 32, 21 of 64; of 512: 25, 21 and 23; of
-    // 768: 26, 26, 28; of 1024: 23, 27, 29
+    // 768: 26, 26, 28; of 1024: 23, 27, 29. Longer ones (16 matrices, 1024 columns each): of 1280 31 in
+    // strips of 16 and of 32, of 1536 44 and 40, of 2048 58 and 58, of 2560 58 and 70; there a strip takes 47
+    // KB and more in 16 columns, and twice that leaves two CTAs an SM or one
     if (K <= 256) return launch_cols<true, 64>(x0, x1, E, K0, N, K, K, Qt, S, g, false, st);
     if (K <= 640) return launch_cols<true, 32>(x0, x1, E, K0, N, K, K, Qt, S, g, false, st);
     if (K <= kStripMaxK) return launch_cols<true, 16>(x0, x1, E, K0, N, K, K, Qt, S, g, false, st);

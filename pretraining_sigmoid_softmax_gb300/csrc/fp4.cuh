@@ -9,9 +9,10 @@
 //   NV: blocks of 16; scale s = E4M3(RN(RN(amax / g) / 6)) under a power of two g for each row, the
 //       smallest with rowmax / g <= 6 * 448, so that the row's largest block has a scale of 224
 //       to 448. RN(x / g / s) is decided against E2M1's midpoints as the exact quotient is: a
-//       midpoint times s has at most 6 significant bits and x has 8, so a quotient that is not
-//       a midpoint differs from it by more than 2^-16 of it. A row with an infinity or NaN gets
-//       g = NaN. Blocks whose scale rounds to 0 have codes of 0.
+//       midpoint (at most 3 significant bits: 1.75, 3.5) times s (4) has at most 7 significant bits
+//       and x has 8, so where x / g is not that product it is at least 2^-8 of it away, and fp32
+//       rounds by 2^-24. A row with an infinity or NaN gets g = NaN. Blocks whose scale rounds
+//       to 0 have codes of 0.
 //
 // Scale tiles: the scales of 128 rows x 4 consecutive blocks are 512 bytes together, in the order
 // in which tcgen05.cp puts them into tensor memory (a row's four bytes side by side).

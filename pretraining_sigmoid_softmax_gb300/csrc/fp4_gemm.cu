@@ -6,9 +6,9 @@
 namespace moe {
 namespace {
 
-// Configurations, on CTA pairs where an expert has many rows. 532,000 rows of 1536 by 4096 columns (MX):
-// 1267 us, 5.3 PFLOP/s; gate and up of 2048 by 768 for 278,000 rows 405 us, 4.7 TB/s;
-// SwiGLU backward of the same 445 us, 5.3 TB/s. MX stages are smaller, so with one output buffer a warp five of
+// Configurations, on CTA pairs where an expert has many rows. 524,288 token rows (532,000 with the padding) of
+// 1536 by 4096 columns (MX): 1265 us, 5.2 PFLOP/s; gate and up of 2048 by 768 for 278,000 rows 405 us, 4.7 TB/s;
+// SwiGLU backward of the same, with the codes of [dA | dU], 458 us, 5.1 TB/s. MX stages are smaller, so with one output buffer a warp five of
 // them fit instead of four, which the loads' latency (1.5 us a round of the stages) is worth: down
 // projections of 1536 1544 -> 1270 us, gate and up of 2048 422 -> 371. NV copies twice the scales and
 // is bound by that: two output buffers and four stages (sums of 768: 300 us against 330).
