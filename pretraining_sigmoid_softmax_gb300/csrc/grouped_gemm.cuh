@@ -744,8 +744,8 @@ __device__ __forceinline__ bool powers_multiply(const float* cs, float g, int la
 // tensor memory before its epilogue, 32 columns at a time, and ones take the place of the powers. Powers
 // on different sides of 1 are multiplied first, which is exact; those on the same side one after the
 // other, each taking the sum further the same way. Out of line, for the registers of the epilogues: 8191
-// tokens through 8 of 64 experts of 1024 x 256 take 113 us a pass (111 without the question), 115 with
-// this inlined and 122 with the choice made among the accumulators that an epilogue holds.
+// tokens through 8 of 64 experts of 1024 x 256 take 113 us a pass with the caches flushed (111 without the
+// question), 115 with this inlined and 122 with the choice made among the accumulators that an epilogue holds.
 template <class C>
 __device__ __noinline__ void scale_in_place(uint32_t t_warp, float g, float* cs, int lane) {
     constexpr int kCols = C::BN / (C::EW / 4);

@@ -10,6 +10,7 @@ call order. Around the layer: the residual addition with the RMS norm in front o
 """
 from __future__ import annotations
 
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -19,6 +20,7 @@ from . import ops
 
 
 FP4_FORMATS = {"mx": ops.FP4_MX, "nv": ops.FP4_NV}
+_PLANS = threading.RLock()  # layers' tables of plans (of all layers, so that a layer can be copied)
 
 
 @dataclass
@@ -840,15 +842,15 @@ class MoELayer(torch.nn.Module):
         if not self.fp4:
             raise ValueError("weights are held by a layer of precision fp4 or fp4_dgrad")
         W = (self.W_g, self.W_u, self.W_d, self.Ws_g, self.Ws_u, self.Ws_d)
-        if not hold:
-            self._release_held()
-            return
-        if self._held is not None and self._held[0].q.device != self.W_g.device:
-            self._release_held()
-        if self._held is None:
-            self._held = weights4(self.fp4_format, *W)
-        else:
-            _quantize_weights4(self._held, W)
+        with _PLANS:
+            if not hold or (self._held is not None and self._held[0].q.device != self.W_g.device):
+                self._release_held()
+            if not hold:
+                return
+            if self._held is None:
+                self._held = weights4(self.fp4_format, *W)
+            else:
+                _quantize_weights4(self._held, W)
 
     def _held_plans(self):
         return [(key, plan) for key, plan in self._plans.items() if isinstance(key, tuple)]
@@ -892,27 +894,28 @@ class MoELayer(torch.nn.Module):
 
     def _plan(self, T):
         """The plan of a token count; one without a backward while the weights are held."""
-        serving = self._held is not None
-        key = (T, "held") if serving else T
-        plan = self._plans.get(key)
-        if plan is None:
-            shape = MoEShape(T, self.d, self.E, self.k, self.f, self.f_shared, self.mode,
-                             self.z_coef, self.aux_switch, self.aux_seq, self.seq_len or T,
-                             self.fp8, self.fp8_dgrad, self.n_group, self.topk_group,
-                             self.group_rule, self.renorm, self.gate_scale, self.fp4, self.fp4_dgrad,
-                             self.fp4_format)
-            plan = MoEPlan(shape, self.W_g.device, backward=not serving)
-            plan.generation = 0
-            plan.captured = False
-            self._plans[key] = plan
-            if serving and not torch.cuda.is_current_stream_capturing():
-                self._limit_held_plans(plan)
-        if serving:
-            self._plans[key] = self._plans.pop(key)  # the last one used
-            plan.captured = plan.captured or torch.cuda.is_current_stream_capturing()
-            st = torch.cuda.current_stream(self.W_g.device)
-            self._held_streams.add((st.stream_id, st.device_index, st.device_type))
-        return plan
+        with _PLANS:
+            serving = self._held is not None
+            key = (T, "held") if serving else T
+            plan = self._plans.get(key)
+            if plan is None:
+                shape = MoEShape(T, self.d, self.E, self.k, self.f, self.f_shared, self.mode,
+                                 self.z_coef, self.aux_switch, self.aux_seq, self.seq_len or T,
+                                 self.fp8, self.fp8_dgrad, self.n_group, self.topk_group,
+                                 self.group_rule, self.renorm, self.gate_scale, self.fp4,
+                                 self.fp4_dgrad, self.fp4_format)
+                plan = MoEPlan(shape, self.W_g.device, backward=not serving)
+                plan.generation = 0
+                plan.captured = False
+                self._plans[key] = plan
+                if serving and not torch.cuda.is_current_stream_capturing():
+                    self._limit_held_plans(plan)
+            if serving:
+                self._plans[key] = self._plans.pop(key)  # the last one used
+                plan.captured = plan.captured or torch.cuda.is_current_stream_capturing()
+                st = torch.cuda.current_stream(self.W_g.device)
+                self._held_streams.add((st.stream_id, st.device_index, st.device_type))
+            return plan
 
     def forward(self, x, residual=None):
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:

@@ -1,4 +1,7 @@
 """Plans that a layer of 4-bit experts is made of: their backward's branches, and how long they live."""
+import copy
+import threading
+
 import pytest
 import torch
 
@@ -182,6 +185,48 @@ def test_dropped_plans_of_another_stream_are_not_given_away_early():
     torch.cuda.synchronize()
     assert torch.equal(out, want) and len(noise) == 2 * len(sizes)
     assert ops.moe_device_status() == (0, 0)
+
+
+def test_threads_with_batches_of_their_own_share_a_layer():
+    """Four threads, each on its stream with its token counts, while plans come and go."""
+    layer = _serving(f_shared=0)
+    layer.HELD_PLAN_BYTES = 0
+    with torch.no_grad():
+        want = {T: layer(_x(T)).clone() for T in range(1, 25)}
+    torch.cuda.synchronize()
+    wrong = []
+
+    def serve(first):
+        try:
+            with torch.no_grad(), torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(60):
+                    T = first + 4 * (i % 6)
+                    out = layer(_x(T))
+                    torch.cuda.current_stream().synchronize()
+                    if not torch.equal(out, want[T]):
+                        wrong.append(T)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=serve, args=(n,)) for n in (1, 2, 3, 4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert len(layer._held_plans()) == 1 and ops.moe_device_status() == (0, 0)
+
+
+@torch.no_grad()
+def test_a_copied_layer_has_its_own_held_weights():
+    layer = _serving(f_shared=0)
+    want = layer(_x(6)).clone()
+    other = copy.deepcopy(layer)
+    layer.hold_weights(False)
+    torch.full((1 << 20,), float("nan"), device="cuda")
+    assert other._held is not None and torch.equal(other(_x(6)), want)
+    other.hold_weights(False)
+    assert torch.equal(other(_x(6)), want)
 
 
 # ------------------------------------------------------- branches of the step in 4 bits
