@@ -783,7 +783,8 @@ class MoELayer(torch.nn.Module):
     ``hold_weights(False)``."""
 
     # Bytes of the plans of held weights that are kept beside the last forward's, captured ones not counted.
-    # A plan of the large layer (d 4096, 64 experts of 1536) takes 0.12 GB for a few tokens, 7.7 for 65,536.
+    # A plan of the large layer (d 4096, 64 experts of 1536) takes 0.12 GB for a few tokens, 8.5 for 65,536
+    # (9.5 with the shared expert).
     HELD_PLAN_BYTES = 16 << 30
 
     def __init__(self, d, E, k, f, f_shared=0, mode="sigmoid", z_coef=0.0, gamma=1e-3,
