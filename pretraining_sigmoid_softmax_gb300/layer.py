@@ -772,9 +772,10 @@ class MoELayer(torch.nn.Module):
 
     ``precision`` "fp8" or "fp4" runs the experts' forward GEMMs on E4M3 or microscaled 4-bit operands
     (``fp4_format`` "nv" or "mx"), "fp8_dgrad" and "fp4_dgrad" the backward's data gradients too. That
-    pays where experts are wide (d_ff 1536 and d 4096: a step of 32 to 36 ms instead of 51); with d_ff
-    256 and d 1024 the passes that make the operands cost more than the products gain, and a step takes 0.78
-    (MX) to 1.12 ms (E4M3) instead of 0.70 in bf16. For serving on 4-bit weights, ``hold_weights()`` quantises them once: forwards then take these codes,
+    pays where experts are wide (d_ff 1536 and d 4096: a step of 32 to 46 ms instead of 51); with d_ff
+    256 and d 1024 the passes that make the operands cost more than the products gain, and a step takes
+    0.78 (MX) to 1.12 ms (E4M3) instead of 0.70 in bf16. For serving on 4-bit weights,
+    ``hold_weights()`` quantises them once: forwards then take these codes,
     keep nothing for a backward and are refused where a gradient is asked for, until
     ``hold_weights(False)``. Call it again after the weights have changed: the new codes take the old
     ones' place, so a graph captured while they were held goes on with the new ones (on the stream of the
